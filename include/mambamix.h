@@ -416,6 +416,129 @@ int mamba_mixer_project(const void* x, const float* conv_w, const float* conv_b,
                         int32_t n_events);
 /* Workspace bytes of mamba_mixer_project for T tokens (0 for invalid sizes).  Host only. */
 size_t mamba_mixer_project_workspace_bytes(int64_t T, int32_t d, int32_t N, int32_t R);
+/*
+ * ------------------------------------------------------------------------------------------
+ * The head scan: linear attention with one decay per head, for layers whose decay is a scalar
+ * per head and whose state is a matrix [P, N] per head:
+ *
+ *   delta = softplus(dt[t,h] + dt_bias[h])
+ *   a     = exp(-exp(A_log[h]) * delta)
+ *   h_t   = a h_{t-1} + delta x_t B_t^T                 h [P, N]
+ *   y_t   = h_t C_t + D[h] x_t
+ *
+ * H heads of P channels; G groups of B and C vectors, H a multiple of G: head h reads group
+ * h / (H / G).  dt == NULL means delta = 1: a fixed decay exp(-exp(A_log[h])) for each head, and
+ * dt_bias is not read.  D == NULL means no skip term.  The sequence boundaries, the state's
+ * meaning and the io types are those of mamba_mixer_prefill.
+ *
+ *   x        [T, H, P] io    rows (one token's H P values, contiguous) x_stride elements apart
+ *   dt       [T, H]    io    rows dt_stride apart, or NULL
+ *   B, C     [T, G, N] io    rows b_stride and c_stride apart
+ *   A_log, dt_bias, D [H] f32
+ *   state_in  [S, H, P, N] f32   initial states, or NULL: zeros
+ *   state_out [S, H, P, N] f32   final states; may be state_in itself (in place), else the two may
+ *                                not overlap.  An empty sequence's final state is its initial one.
+ *   y        [T, H, P] io    contiguous
+ * The strides let x, B, C and dt be column ranges of one projection output; each is at least the
+ * row's length (MM_ERR_DIM).  y and state_out may overlap no input but state_out == state_in.
+ * Limits: 1 <= P <= MM_HEADS_MAX_P, 1 <= N <= MM_HEADS_MAX_N (else MM_ERR_UNSUPPORTED).
+ * T == 0 copies the states and is otherwise a no-op; H == 0 is a no-op.
+ */
+#define MM_HEADS_MAX_P 256
+#define MM_HEADS_MAX_N 256
+
+/* The head scan over S packed sequences.  workspace: mamba_mixer_heads_prefill_workspace_bytes
+ * bytes (0 for short calls), 256-byte aligned, contents on entry do not matter. */
+int mamba_mixer_heads_prefill(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
+                              const float* D, const float* dt_bias, const int32_t* cu_seqlens, const float* state_in,
+                              float* state_out, void* y, int32_t S, int64_t T, int32_t H, int32_t P, int32_t G,
+                              int32_t N, int32_t io_dtype, int64_t x_stride, int64_t dt_stride, int64_t b_stride,
+                              int64_t c_stride, void* workspace, size_t workspace_bytes, void* stream);
+size_t mamba_mixer_heads_prefill_workspace_bytes(int32_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N,
+                                                 int32_t io_dtype);
+
+/* One token for each of Bs rows; row r is state slot r.  x [Bs, H, P], dt [Bs, H], B, C [Bs, G, N],
+ * y [Bs, H, P]; the rest as above. */
+int mamba_mixer_heads_decode(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
+                             const float* D, const float* dt_bias, const float* state_in, float* state_out, void* y,
+                             int32_t Bs, int32_t H, int32_t P, int32_t G, int32_t N, int32_t io_dtype,
+                             int64_t x_stride, int64_t dt_stride, int64_t b_stride, int64_t c_stride, void* stream);
+
+/*
+ * The gradients of the head scan, given dy = dL/dy [T, H, P] (io, contiguous) and dstate_out =
+ * dL/d(final states) [S, H, P, N] (f32, or NULL: the loss does not depend on them).  The inputs are
+ * those of the forward call (state_in the initial states, not overwritten since).
+ *   dx [T, H, P], ddt [T, H], dB, dC [T, G, N]   io, rows dx_stride, ddt_stride, db_stride, dc_stride
+ *                                apart (so that they can be column ranges of one gradient); dB and dC are
+ *                                summed over the group's heads; ddt is NULL when dt is
+ *   dA_log, dD, ddt_bias [H]     f32; dD is NULL when D is, ddt_bias when dt is
+ *   dstate_in [S, H, P, N]       f32, or NULL: not wanted
+ * All outputs are overwritten, and summed in a fixed order: the results do not vary from run to run.
+ * workspace: mamba_mixer_heads_backward_workspace_bytes bytes, 256-byte aligned.
+ * No output may overlap an input or another output (column ranges of one array with the same row
+ * stride are taken apart).  With T == 0 the parameters' gradients are zeros and dstate_in is a copy of
+ * dstate_out.
+ */
+int mamba_mixer_heads_backward(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
+                               const float* D, const float* dt_bias, const int32_t* cu_seqlens, const float* state_in,
+                               const void* dy, const float* dstate_out, void* dx, void* ddt, void* dB, void* dC,
+                               float* dA_log, float* dD, float* ddt_bias, float* dstate_in, int32_t S, int64_t T,
+                               int32_t H, int32_t P, int32_t G, int32_t N, int32_t io_dtype, int64_t x_stride,
+                               int64_t dt_stride, int64_t b_stride, int64_t c_stride, int64_t dx_stride,
+                               int64_t ddt_stride, int64_t db_stride, int64_t dc_stride, void* workspace,
+                               size_t workspace_bytes, void* stream);
+size_t mamba_mixer_heads_backward_workspace_bytes(int32_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N,
+                                                  int32_t io_dtype);
+
+/*
+ * The norm after a mixer block, fused with its gate.  With s = z sigmoid(z) and
+ * n(u) = u / sqrt(mean(u^2) + eps) over each of `groups` equal ranges of the d columns:
+ *   gate_first != 0:  out = weight n(y s)          gate_first == 0:  out = weight n(y) s
+ *   y [rows, d], z [rows, d] io, rows y_stride and z_stride apart; weight [d] f32;
+ *   out [rows, d] io, contiguous; may be y itself when y is contiguous (in place), and may overlap
+ *   no other input (MM_ERR_ALIAS)
+ * d is a multiple of groups (MM_ERR_DIM), eps >= 0.  rows == 0 or d == 0 is a no-op.
+ */
+int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, void* out, int64_t rows, int32_t d,
+                          int32_t groups, float eps, int32_t gate_first, int32_t io_dtype, int64_t y_stride,
+                          int64_t z_stride, void* stream);
+/* Its gradients: dy, dz [rows, d] io (rows dy_stride, dz_stride apart), dweight [d] f32, from
+ * dout [rows, d] (contiguous).  Outputs overlap no input and no other output (column ranges of one
+ * array with the same row stride are taken apart).  Sums in a fixed order. */
+int mamba_mixer_gate_norm_backward(const void* dout, const void* y, const void* z, const float* weight, void* dy,
+                                   void* dz, float* dweight, int64_t rows, int32_t d, int32_t groups, float eps,
+                                   int32_t gate_first, int32_t io_dtype, int64_t y_stride, int64_t z_stride,
+                                   int64_t dy_stride, int64_t dz_stride, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+size_t mamba_mixer_gate_norm_backward_workspace_bytes(int64_t rows, int32_t d, int32_t groups);
+
+/*
+ * The boundary between two blocks: the norm after one (optional), its residual scale, the residual
+ * addition and the norm before the next:
+ *   p = h, or post_weight n(h) when post_weight != NULL
+ *   r' = residual + scale scale_vec p              (scale_vec == NULL: ones; residual == NULL: zeros)
+ *   out = weight n(r')                             (from r' before its rounding)
+ *   h, out [rows, d] io; residual, residual_out [rows, d] of type res_dtype (MM_IO_*), float32 or io's;
+ *   weight, post_weight, scale_vec [d] f32.  All contiguous.  residual_out may be residual itself;
+ *   otherwise the outputs overlap no input and not one another.  d <= MM_NORM_MAX_D.
+ */
+#define MM_NORM_MAX_D 32768
+int mamba_mixer_residual_norm(const void* h, const void* residual, const float* weight, const float* post_weight,
+                              const float* scale_vec, float scale, void* residual_out, void* out, int64_t rows,
+                              int32_t d, float eps, int32_t io_dtype, int32_t res_dtype, void* stream);
+/* Its gradients, from dout (io) and dresidual_out (res_dtype, or NULL: zeros), the block's output h and
+ * the NEW residual residual_out that the forward call wrote:
+ *   dresidual [rows, d] res_dtype, dh [rows, d] io, dweight [d], and dpost_weight and dscale_vec [d] when
+ *   post_weight and scale_vec are given (else NULL).  Sums in a fixed order.  dresidual may be
+ *   dresidual_out itself. */
+int mamba_mixer_residual_norm_backward(const void* dout, const void* dresidual_out, const void* h,
+                                       const void* residual_out, const float* weight, const float* post_weight,
+                                       const float* scale_vec, float scale, void* dresidual, void* dh, float* dweight,
+                                       float* dpost_weight, float* dscale_vec, int64_t rows, int32_t d, float eps,
+                                       int32_t io_dtype, int32_t res_dtype, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+size_t mamba_mixer_residual_norm_backward_workspace_bytes(int64_t rows, int32_t d);
+
 /* Static text for a status code (never NULL).  Host only. */
 const char* mamba_mixer_status_string(int status);
 

@@ -86,6 +86,28 @@ def load() -> ctypes.CDLL:
     lib.mamba_mixer_project.restype = ctypes.c_int
     lib.mamba_mixer_project_workspace_bytes.argtypes = [i64, i32, i32, i32]
     lib.mamba_mixer_project_workspace_bytes.restype = sz
+    f32 = ctypes.c_float
+    lib.mamba_mixer_heads_prefill.argtypes = [P] * 11 + [i32, i64, i32, i32, i32, i32, i32] + [i64] * 4 + [P, sz, P]
+    lib.mamba_mixer_heads_prefill.restype = ctypes.c_int
+    lib.mamba_mixer_heads_decode.argtypes = [P] * 10 + [i32] * 6 + [i64] * 4 + [P]
+    lib.mamba_mixer_heads_decode.restype = ctypes.c_int
+    lib.mamba_mixer_heads_backward.argtypes = ([P] * 19 + [i32, i64, i32, i32, i32, i32, i32] + [i64] * 8 + [P, sz, P])
+    lib.mamba_mixer_heads_backward.restype = ctypes.c_int
+    for name in ("mamba_mixer_heads_prefill_workspace_bytes", "mamba_mixer_heads_backward_workspace_bytes"):
+        getattr(lib, name).argtypes = [i32, i64, i32, i32, i32, i32, i32]
+        getattr(lib, name).restype = sz
+    lib.mamba_mixer_gate_norm.argtypes = [P] * 4 + [i64, i32, i32, f32, i32, i32, i64, i64, P]
+    lib.mamba_mixer_gate_norm.restype = ctypes.c_int
+    lib.mamba_mixer_gate_norm_backward.argtypes = [P] * 7 + [i64, i32, i32, f32, i32, i32] + [i64] * 4 + [P, sz, P]
+    lib.mamba_mixer_gate_norm_backward.restype = ctypes.c_int
+    lib.mamba_mixer_gate_norm_backward_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.mamba_mixer_gate_norm_backward_workspace_bytes.restype = sz
+    lib.mamba_mixer_residual_norm.argtypes = [P] * 5 + [f32, P, P, i64, i32, f32, i32, i32, P]
+    lib.mamba_mixer_residual_norm.restype = ctypes.c_int
+    lib.mamba_mixer_residual_norm_backward.argtypes = ([P] * 7 + [f32] + [P] * 5 + [i64, i32, f32, i32, i32, P, sz, P])
+    lib.mamba_mixer_residual_norm_backward.restype = ctypes.c_int
+    lib.mamba_mixer_residual_norm_backward_workspace_bytes.argtypes = [i64, i32]
+    lib.mamba_mixer_residual_norm_backward_workspace_bytes.restype = sz
     lib.mamba_mixer_status_string.argtypes = [ctypes.c_int]
     lib.mamba_mixer_status_string.restype = ctypes.c_char_p
     lib.mamba_mixer_version.argtypes = []
@@ -603,3 +625,8 @@ def decode_replay_multi(x_ring, dt_ring, B_ring, z_ring, C_ring, A_log, D, dt_bi
     if rc != MM_OK:
         raise MambaMixError(rc, "mamba_mixer_decode_replay_multi")
     return y_ring
+
+
+# the head scan and the norms around a mixer block
+from .heads import (gate_norm, gate_norm_backward, heads_backward, heads_decode,  # noqa: E402,F401
+                    heads_prefill, residual_norm, residual_norm_backward)

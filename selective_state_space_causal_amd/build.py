@@ -7,7 +7,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "mambamix.hip")
+SRC = [os.path.join(HERE, "csrc", f) for f in ("mambamix.hip", "heads.hip")]
 LIB = os.path.join(HERE, "libmambamix.so")
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -26,23 +26,43 @@ def hipcc() -> str:
 
 def build(verbose: bool = False) -> str:
     """Compile the HIP library (always recompiles) and return its path."""
+    objs, running = [], []
+    for src in SRC:
+        objs.append(f"{LIB}.{os.path.basename(src)}.o")
+        cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f != "-shared"], "-I", INCLUDE, "-c", "-o", objs[-1], src]
+        running.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+    said = "".join(p.communicate()[0] for p in running)
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-o", tmp, SRC]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
+    if all(p.returncode == 0 for p in running):
+        res = subprocess.run([hipcc(), "-shared", "-fPIC", "--offload-arch=gfx950", "-o", tmp, *objs],
+                             capture_output=True, text=True)
+        said += res.stdout + res.stderr
+        ok = res.returncode == 0
+    else:
+        ok = False
+    for o in objs:
+        if os.path.exists(o):
+            os.remove(o)
+    if not ok:
+        sys.stderr.write(said)
         raise RuntimeError("hipcc failed to build libmambamix")
     if verbose:
-        sys.stderr.write(res.stderr)
+        sys.stderr.write(said)
     os.replace(tmp, LIB)
     return LIB
 
 
 def asm(out: str) -> None:
-    """Write the gfx950 device assembly of the library to ``out`` (for inspection)."""
-    cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")], "-I", INCLUDE,
-           "--cuda-device-only", "-S", "-o", out, SRC]
-    subprocess.run(cmd, check=True, capture_output=True)
+    """Write the gfx950 device assembly of the library to ``out`` (for inspection), one source after another."""
+    text = ""
+    for src in SRC:
+        cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")], "-I", INCLUDE,
+               "--cuda-device-only", "-S", "-o", out, src]
+        subprocess.run(cmd, check=True, capture_output=True)
+        with open(out) as f:
+            text += f.read()
+    with open(out, "w") as f:
+        f.write(text)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,599 @@
+// The head scan and the norms around a mixer block: argument checks, plans and launches of the
+// entry points declared in include/mambamix.h.  The kernels are in mm_heads.h and mm_norm.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include <stdint.h>
+
+#include <cmath>
+
+#include "mambamix.h"
+#include "mm_device.h"
+#include "mm_heads.h"
+#include "mm_host.h"
+#include "mm_norm.h"
+
+namespace mm {
+namespace {
+
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;  // of one launch
+
+int launched() { return hipGetLastError() == hipSuccess ? MM_OK : MM_ERR_HIP; }
+
+// ---------------------------------------------------------------- the head scan: plans
+
+struct HeadsPlan {
+  int64_t Ls;      // tokens per segment
+  bool whole;      // every sequence is one segment
+  int64_t rows;    // segments at most
+  int64_t rows64;  // 64-token blocks at most (backward)
+  int nrp, nrn;    // 16-row blocks of P and N
+  size_t off_carry, off_decay, off_carry2, off_decay2, off_hb, off_dots, off_dB, off_dC, off_q, off_r, off_delta,
+      off_sums, total;
+};
+
+// A workgroup of the sequential kernels walks one segment, about 0.1 us a token, so few long
+// sequences are cut until some four workgroups are on every CU; segments shorter than 256 tokens
+// are not worth their states.
+constexpr int64_t kSeqWorkgroups = 1024;
+
+int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int N, bool backward) {
+  p = HeadsPlan{};
+  p.nrp = static_cast<int>(cdiv(P, kSeqRows));
+  p.nrn = static_cast<int>(cdiv(N, kSeqRows));
+  const int64_t per = static_cast<int64_t>(H) * (backward ? std::min(p.nrp, p.nrn) : p.nrp);
+  const int64_t want = cdiv(kSeqWorkgroups, std::max<int64_t>(per, 1));
+  p.Ls = std::max<int64_t>(256, cdiv(cdiv(T, std::max<int64_t>(want, 1)), kHeadsBlock) * kHeadsBlock);
+  if (want <= S || p.Ls >= T) p.Ls = (T / kHeadsBlock + 1) * kHeadsBlock;
+  p.whole = p.Ls > T;
+  p.rows = segment_rows(S, T, p.Ls);
+  p.rows64 = segment_rows(S, T, kHeadsBlock);
+  const size_t set = static_cast<size_t>(H) * P * N * 4;
+  const size_t th = static_cast<size_t>(T) * H;
+  size_t off = 0;
+  const auto take = [&off](size_t& at, size_t n) { at = off; off += align256(n); };
+  if (!p.whole) {
+    take(p.off_carry, p.rows * set);
+    take(p.off_decay, static_cast<size_t>(p.rows) * H * 4);
+  }
+  if (backward) {
+    if (!p.whole) {
+      take(p.off_carry2, p.rows * set);
+      take(p.off_decay2, static_cast<size_t>(p.rows) * H * 4);
+    }
+    take(p.off_hb, p.rows64 * set);
+    take(p.off_dots, static_cast<size_t>(p.rows64) * H * p.nrp * 4);
+    take(p.off_dB, th * N * 4);
+    take(p.off_dC, th * N * 4);
+    take(p.off_q, th * 4);
+    take(p.off_r, th * 4);
+    take(p.off_delta, th * 4);
+    take(p.off_sums, static_cast<size_t>(p.rows64) * H * 3 * 4);
+  }
+  p.total = off;
+  const int64_t most = std::max<int64_t>(p.rows * H * std::max(p.nrp, p.nrn), p.rows64 * H);
+  if (most * kSeqThreads > kMaxThreads || static_cast<int64_t>(th) * 16 > kMaxThreads) return MM_ERR_DIM;
+  return MM_OK;
+}
+
+int check_heads_sizes(int64_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N, int32_t io) {
+  if (S < 0 || T < 0 || H < 0 || P < 0 || G < 0 || N < 0 || T > INT32_MAX || S > INT32_MAX) return MM_ERR_DIM;
+  if (io != MM_IO_F32 && io != MM_IO_BF16) return MM_ERR_UNSUPPORTED;
+  if (P < 1 || P > MM_HEADS_MAX_P || N < 1 || N > MM_HEADS_MAX_N) return MM_ERR_UNSUPPORTED;
+  if (S == 0 && T > 0) return MM_ERR_DIM;
+  if (H > 0 && (G < 1 || H % G != 0)) return MM_ERR_DIM;
+  const uint64_t d = static_cast<uint64_t>(H) * P;
+  if (d > 0 && (static_cast<uint64_t>(T) > MM_MAX_ROWS_X_D / d || static_cast<uint64_t>(S) > MM_MAX_ROWS_X_D / d))
+    return MM_ERR_DIM;
+  return MM_OK;
+}
+
+template <typename IO>
+Tok<IO> tok(const void* p, int64_t ts, int W, int div) {
+  return Tok<IO>{static_cast<const IO*>(p), ts, W, div};
+}
+
+template <typename IO, bool REV, bool LOCAL>
+void launch_seq(const SeqRun<IO>& q, const HeadPar& hp, int64_t rows, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(rows * hp.H * cdiv(q.R, kSeqRows))), block(kSeqThreads);
+  if (grid.x == 0) return;
+  if (q.K <= 16) hipLaunchKernelGGL((k_heads_seq<IO, 1, REV, LOCAL>), grid, block, 0, st, q, hp);
+  else if (q.K <= 32) hipLaunchKernelGGL((k_heads_seq<IO, 2, REV, LOCAL>), grid, block, 0, st, q, hp);
+  else if (q.K <= 64) hipLaunchKernelGGL((k_heads_seq<IO, 4, REV, LOCAL>), grid, block, 0, st, q, hp);
+  else if (q.K <= 128) hipLaunchKernelGGL((k_heads_seq<IO, 8, REV, LOCAL>), grid, block, 0, st, q, hp);
+  else hipLaunchKernelGGL((k_heads_seq<IO, 16, REV, LOCAL>), grid, block, 0, st, q, hp);
+}
+
+void launch_carry(float* carry, const float* decay, const float* init, const HeadPar& hp, int64_t PN, int64_t Ls,
+                  bool reverse, hipStream_t st) {
+  for (int s0 = 0; s0 < hp.S; s0 += 65535)
+    hipLaunchKernelGGL(k_heads_carry, dim3(static_cast<unsigned>(cdiv(hp.H * PN, 256)),
+                                           static_cast<unsigned>(std::min(hp.S - s0, 65535))),
+                       dim3(256), 0, st, carry, decay, init, hp.cu, hp.H, PN, Ls, reverse ? 1 : 0, s0);
+}
+
+struct HeadsArgs {
+  const void *x, *B, *C;
+  int64_t x_ts, b_ts, c_ts;
+  int P, G, N;
+  HeadPar hp;
+};
+
+template <typename IO>
+int launch_prefill(const HeadsPlan& p, const HeadsArgs& a, const float* state_in, float* state_out, void* y, char* ws,
+                   hipStream_t st) {
+  const int div = a.hp.H / a.G;
+  SeqRun<IO> q{};
+  q.u = tok<IO>(a.x, a.x_ts, a.P, 1);
+  q.v = tok<IO>(a.B, a.b_ts, a.N, div);
+  q.s = tok<IO>(a.C, a.c_ts, a.N, div);
+  q.R = a.P;
+  q.K = a.N;
+  q.sr = a.N;
+  q.sk = 1;
+  q.sh = static_cast<int64_t>(a.P) * a.N;
+  q.init = state_in;
+  q.fin = state_out;
+  q.Ls = p.Ls;
+  q.out = static_cast<IO*>(y);
+  q.out_ts = static_cast<int64_t>(a.hp.H) * a.P;
+  q.add_D = 1;
+  if (!p.whole) {
+    q.carry = reinterpret_cast<float*>(ws + p.off_carry);
+    q.decay = reinterpret_cast<float*>(ws + p.off_decay);
+    launch_seq<IO, false, true>(q, a.hp, p.rows, st);
+    launch_carry(q.carry, q.decay, state_in, a.hp, q.sh, p.Ls, false, st);
+  }
+  launch_seq<IO, false, false>(q, a.hp, p.rows, st);
+  return launched();
+}
+
+struct HeadsGrads {
+  const void* dy;
+  const float *state_in, *dstate_out;
+  void *dx, *ddt, *dB, *dC;
+  int64_t dx_ts, ddt_ts, db_ts, dc_ts;
+  float *dA_log, *dD, *ddt_bias, *dstate_in;
+};
+
+template <typename IO>
+int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o, char* ws, hipStream_t st) {
+  const int H = a.hp.H, div = H / a.G;
+  const int64_t T = a.hp.T, set = static_cast<int64_t>(a.P) * a.N;
+  const Tok<IO> x = tok<IO>(a.x, a.x_ts, a.P, 1), dy = tok<IO>(o.dy, static_cast<int64_t>(H) * a.P, a.P, 1);
+  const Tok<IO> B = tok<IO>(a.B, a.b_ts, a.N, div), C = tok<IO>(a.C, a.c_ts, a.N, div);
+  float* f[] = {reinterpret_cast<float*>(ws + p.off_hb), reinterpret_cast<float*>(ws + p.off_dots),
+                reinterpret_cast<float*>(ws + p.off_dB), reinterpret_cast<float*>(ws + p.off_dC),
+                reinterpret_cast<float*>(ws + p.off_q), reinterpret_cast<float*>(ws + p.off_r),
+                reinterpret_cast<float*>(ws + p.off_delta), reinterpret_cast<float*>(ws + p.off_sums)};
+  // dC (and the states at the blocks' ends): forward, the state transposed (rows N)
+  SeqRun<IO> c{};
+  c.u = B;
+  c.v = x;
+  c.s = dy;
+  c.R = a.N;
+  c.K = a.P;
+  c.sr = 1;
+  c.sk = a.N;
+  c.sh = set;
+  c.init = o.state_in;
+  c.Ls = p.Ls;
+  c.out32 = f[3];
+  c.store = f[0];
+  // dB: reverse, the state transposed
+  SeqRun<IO> b = c;
+  b.u = C;
+  b.v = dy;
+  b.s = x;
+  b.init = o.dstate_out;
+  b.out32 = f[2];
+  b.store = nullptr;
+  // dx, dstate_in and the inner products at the blocks' ends: reverse (rows P)
+  SeqRun<IO> d = b;
+  d.u = dy;
+  d.v = C;
+  d.s = B;
+  d.R = a.P;
+  d.K = a.N;
+  d.sr = a.N;
+  d.sk = 1;
+  d.fin = o.dstate_in;
+  d.out32 = nullptr;
+  d.out = static_cast<IO*>(o.dx);
+  d.out_ts = o.dx_ts;
+  d.out_delta = 1;
+  d.add_D = 1;
+  d.dots_with = f[0];
+  d.dots = f[1];
+  if (!p.whole) {
+    c.carry = reinterpret_cast<float*>(ws + p.off_carry);
+    c.decay = reinterpret_cast<float*>(ws + p.off_decay);
+    b.carry = d.carry = reinterpret_cast<float*>(ws + p.off_carry2);
+    b.decay = d.decay = reinterpret_cast<float*>(ws + p.off_decay2);
+    launch_seq<IO, false, true>(c, a.hp, p.rows, st);
+    launch_carry(c.carry, c.decay, o.state_in, a.hp, set, p.Ls, false, st);
+    launch_seq<IO, true, true>(d, a.hp, p.rows, st);
+    launch_carry(d.carry, d.decay, o.dstate_out, a.hp, set, p.Ls, true, st);
+  }
+  launch_seq<IO, false, false>(c, a.hp, p.rows, st);
+  launch_seq<IO, true, false>(d, a.hp, p.rows, st);
+  if (T > 0) {
+    launch_seq<IO, true, false>(b, a.hp, p.rows, st);
+    const unsigned nqr = static_cast<unsigned>(cdiv(T * H * 16, 256));
+    hipLaunchKernelGGL((k_heads_qr<IO>), dim3(nqr), dim3(256), 0, st, B, C, f[2], f[3], f[4], f[5], T, H, a.N);
+    hipLaunchKernelGGL((k_heads_ddt<IO>), dim3(static_cast<unsigned>(p.rows64 * H)), dim3(64), 0, st, a.hp, x, dy, f[4],
+                       f[5], f[1], p.nrp, f[6], static_cast<IO*>(o.ddt), o.ddt_ts, f[7], a.P);
+    hipLaunchKernelGGL((k_heads_group<IO>), dim3(static_cast<unsigned>(cdiv(T * a.G * a.N, 256))), dim3(256), 0, st,
+                       f[2], f[3], f[6], static_cast<IO*>(o.dB), static_cast<IO*>(o.dC), o.db_ts, o.dc_ts, T, H, a.G,
+                       a.N);
+  }
+  hipLaunchKernelGGL(k_heads_params, dim3(static_cast<unsigned>(H)), dim3(256), 0, st, f[7], T > 0 ? p.rows64 : 0, H,
+                     o.dA_log, o.ddt_bias, o.dD);
+  return launched();
+}
+
+// ---------------------------------------------------------------- the head scan: checks
+
+Rows rows(const void* p, int64_t n, int64_t width, int64_t stride, size_t es) {
+  return Rows{p, n, static_cast<size_t>(width) * es, static_cast<size_t>(stride) * es};
+}
+Rows flat(const void* p, size_t bytes) { return Rows{p, 1, bytes, bytes}; }
+
+// arrays of zero bytes may be NULL; `es`: the element size they are aligned to
+struct Array {
+  Rows r;
+  size_t es;
+  bool optional;  // NULL allowed
+};
+int check_arrays(const Array* a, int n) {
+  for (int i = 0; i < n; ++i)
+    if (a[i].r.p == nullptr && !a[i].optional && a[i].r.extent() > 0) return MM_ERR_NULL;
+  for (int i = 0; i < n; ++i)
+    if (!aligned(a[i].r.p, a[i].es)) return MM_ERR_ALIGN;
+  return MM_OK;
+}
+// no output on an input or another output; same: an output may be this input itself
+int check_overlap(const Array* in, int ni, const Array* out, int no, const void* same = nullptr) {
+  for (int i = 0; i < no; ++i) {
+    if (out[i].r.p == nullptr) continue;
+    for (int k = 0; k < ni; ++k) {
+      if (in[k].r.p == nullptr || (same != nullptr && out[i].r.p == same && in[k].r.p == same)) continue;
+      if (overlap(out[i].r, in[k].r)) return MM_ERR_ALIAS;
+    }
+    for (int k = i + 1; k < no; ++k)
+      if (out[k].r.p != nullptr && overlap(out[i].r, out[k].r)) return MM_ERR_ALIAS;
+  }
+  return MM_OK;
+}
+
+size_t esize(int32_t io) { return io == MM_IO_BF16 ? 2 : 4; }
+
+// ---------------------------------------------------------------- norms: checks
+
+int check_norm_sizes(int64_t rows, int32_t d, float eps, int32_t io) {
+  if (rows < 0 || d < 0 || !(eps >= 0.0f)) return MM_ERR_DIM;
+  if (io != MM_IO_F32 && io != MM_IO_BF16) return MM_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX || (d > 0 && static_cast<uint64_t>(rows) > MM_MAX_ROWS_X_D / static_cast<uint64_t>(d))) return MM_ERR_DIM;
+  return MM_OK;
+}
+int check_gate_sizes(int64_t rows, int32_t d, int32_t groups, float eps, int32_t io) {
+  const int rc = check_norm_sizes(rows, d, eps, io);
+  if (rc != MM_OK) return rc;
+  if (groups < 1 || d % groups != 0 || rows * groups * kNormThreads > kMaxThreads) return MM_ERR_DIM;
+  return MM_OK;
+}
+int check_residual_sizes(int64_t rows, int32_t d, float eps, int32_t io, int32_t res) {
+  const int rc = check_norm_sizes(rows, d, eps, io);
+  if (rc != MM_OK) return rc;
+  if (rows * kNormThreads > kMaxThreads) return MM_ERR_DIM;
+  if (d > MM_NORM_MAX_D || (res != MM_IO_F32 && res != io)) return MM_ERR_UNSUPPORTED;
+  return MM_OK;
+}
+
+// the io and residual types of a call, as template arguments of f
+template <typename F>
+int by_types(int32_t io, int32_t res, F f) {
+  if (io == MM_IO_F32) return f(float{}, float{});
+  if (res == MM_IO_F32) return f(uint16_t{}, float{});
+  return f(uint16_t{}, uint16_t{});
+}
+template <typename K>
+int allow_lds(K kernel, size_t bytes) {
+  if (bytes > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes)) != hipSuccess)
+    return MM_ERR_HIP;
+  return MM_OK;
+}
+
+}  // namespace
+}  // namespace mm
+
+using namespace mm;
+
+extern "C" {
+
+size_t mamba_mixer_heads_prefill_workspace_bytes(int32_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N,
+                                                 int32_t io_dtype) {
+  HeadsPlan p;
+  if (check_heads_sizes(S, T, H, P, G, N, io_dtype) != MM_OK || plan_heads(p, S, T, H, P, N, false) != MM_OK) return 0;
+  return p.total;
+}
+
+int mamba_mixer_heads_prefill(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
+                              const float* D, const float* dt_bias, const int32_t* cu_seqlens, const float* state_in,
+                              float* state_out, void* y, int32_t S, int64_t T, int32_t H, int32_t P, int32_t G,
+                              int32_t N, int32_t io_dtype, int64_t x_stride, int64_t dt_stride, int64_t b_stride,
+                              int64_t c_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_heads_sizes(S, T, H, P, G, N, io_dtype);
+  if (rc != MM_OK) return rc;
+  if (H == 0 || S == 0) return MM_OK;
+  const int64_t d = static_cast<int64_t>(H) * P, gn = static_cast<int64_t>(G) * N;
+  if (x_stride < d || b_stride < gn || c_stride < gn || (dt != nullptr && dt_stride < H)) return MM_ERR_DIM;
+  const size_t es = esize(io_dtype), nh = static_cast<size_t>(H) * 4, ns = static_cast<size_t>(S) * d * N * 4;
+  const Array in[] = {{rows(x, T, d, x_stride, es), es, false}, {rows(dt, T, H, dt_stride, es), es, true},
+                      {rows(B, T, gn, b_stride, es), es, false}, {rows(C, T, gn, c_stride, es), es, false},
+                      {flat(A_log, nh), 4, false}, {flat(D, nh), 4, true},
+                      {flat(dt_bias, dt != nullptr ? nh : 0), 4, false},
+                      {flat(cu_seqlens, (static_cast<size_t>(S) + 1) * 4), 4, false}, {flat(state_in, ns), 4, true}};
+  const Array out[] = {{flat(y, static_cast<size_t>(T) * d * es), es, false}, {flat(state_out, ns), 4, false}};
+  if ((rc = check_arrays(in, 9)) != MM_OK || (rc = check_arrays(out, 2)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 9, out, 2, state_in)) != MM_OK) return rc;
+  HeadsPlan p;
+  if ((rc = plan_heads(p, S, T, H, P, N, false)) != MM_OK) return rc;
+  if (p.total > 0 && (workspace == nullptr || workspace_bytes < p.total)) return MM_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
+  const HeadsArgs a{x, B, C, x_stride, b_stride, c_stride, P, G, N,
+                    {dt, dt_stride, A_log, dt_bias, D, cu_seqlens, S, H, T}};
+  char* ws = static_cast<char*>(workspace);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (io_dtype == MM_IO_BF16) return launch_prefill<uint16_t>(p, a, state_in, state_out, y, ws, st);
+  return launch_prefill<float>(p, a, state_in, state_out, y, ws, st);
+}
+
+int mamba_mixer_heads_decode(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
+                             const float* D, const float* dt_bias, const float* state_in, float* state_out, void* y,
+                             int32_t Bs, int32_t H, int32_t P, int32_t G, int32_t N, int32_t io_dtype,
+                             int64_t x_stride, int64_t dt_stride, int64_t b_stride, int64_t c_stride, void* stream) {
+  int rc = check_heads_sizes(Bs, Bs, H, P, G, N, io_dtype);
+  if (rc != MM_OK) return rc;
+  if (H == 0 || Bs == 0) return MM_OK;
+  const int64_t d = static_cast<int64_t>(H) * P, gn = static_cast<int64_t>(G) * N;
+  if (x_stride < d || b_stride < gn || c_stride < gn || (dt != nullptr && dt_stride < H)) return MM_ERR_DIM;
+  const size_t es = esize(io_dtype), nh = static_cast<size_t>(H) * 4, ns = static_cast<size_t>(Bs) * d * N * 4;
+  const Array in[] = {{rows(x, Bs, d, x_stride, es), es, false}, {rows(dt, Bs, H, dt_stride, es), es, true},
+                      {rows(B, Bs, gn, b_stride, es), es, false}, {rows(C, Bs, gn, c_stride, es), es, false},
+                      {flat(A_log, nh), 4, false}, {flat(D, nh), 4, true},
+                      {flat(dt_bias, dt != nullptr ? nh : 0), 4, false}, {flat(state_in, ns), 4, true}};
+  const Array out[] = {{flat(y, static_cast<size_t>(Bs) * d * es), es, false}, {flat(state_out, ns), 4, false}};
+  if ((rc = check_arrays(in, 8)) != MM_OK || (rc = check_arrays(out, 2)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 8, out, 2, state_in)) != MM_OK) return rc;
+  const HeadPar hp{dt, dt_stride, A_log, dt_bias, D, nullptr, Bs, H, Bs};
+  const int64_t blocks = static_cast<int64_t>(Bs) * H * cdiv(P, kSeqRows);
+  if (blocks * kSeqThreads > kMaxThreads) return MM_ERR_DIM;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const auto go = [&](auto io) {
+    using IO = decltype(io);
+    const Tok<IO> xt = tok<IO>(x, x_stride, P, 1), bt = tok<IO>(B, b_stride, N, H / G), ct = tok<IO>(C, c_stride, N, H / G);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kSeqThreads);
+    IO* yo = static_cast<IO*>(y);
+    if (N <= 64)
+      hipLaunchKernelGGL((k_heads_decode_any<IO, 4>), grid, block, 0, st, xt, bt, ct, hp, state_in, state_out, yo, P, N);
+    else
+      hipLaunchKernelGGL((k_heads_decode_any<IO, 16>), grid, block, 0, st, xt, bt, ct, hp, state_in, state_out, yo, P, N);
+  };
+  if (io_dtype == MM_IO_BF16) go(uint16_t{}); else go(float{});
+  return launched();
+}
+
+size_t mamba_mixer_heads_backward_workspace_bytes(int32_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N,
+                                                  int32_t io_dtype) {
+  HeadsPlan p;
+  if (check_heads_sizes(S, T, H, P, G, N, io_dtype) != MM_OK || plan_heads(p, S, T, H, P, N, true) != MM_OK) return 0;
+  return p.total;
+}
+
+int mamba_mixer_heads_backward(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
+                               const float* D, const float* dt_bias, const int32_t* cu_seqlens, const float* state_in,
+                               const void* dy, const float* dstate_out, void* dx, void* ddt, void* dB, void* dC,
+                               float* dA_log, float* dD, float* ddt_bias, float* dstate_in, int32_t S, int64_t T,
+                               int32_t H, int32_t P, int32_t G, int32_t N, int32_t io_dtype, int64_t x_stride,
+                               int64_t dt_stride, int64_t b_stride, int64_t c_stride, int64_t dx_stride,
+                               int64_t ddt_stride, int64_t db_stride, int64_t dc_stride, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  int rc = check_heads_sizes(S, T, H, P, G, N, io_dtype);
+  if (rc != MM_OK) return rc;
+  if (H == 0) return MM_OK;
+  const int64_t d = static_cast<int64_t>(H) * P, gn = static_cast<int64_t>(G) * N;
+  if (x_stride < d || b_stride < gn || c_stride < gn || dx_stride < d || db_stride < gn || dc_stride < gn ||
+      (dt != nullptr && (dt_stride < H || ddt_stride < H)))
+    return MM_ERR_DIM;
+  const size_t es = esize(io_dtype), nh = static_cast<size_t>(H) * 4, ns = static_cast<size_t>(S) * d * N * 4;
+  const size_t ndt = dt != nullptr ? nh : 0;
+  const Array in[] = {{rows(x, T, d, x_stride, es), es, false}, {rows(dt, T, H, dt_stride, es), es, true},
+                      {rows(B, T, gn, b_stride, es), es, false}, {rows(C, T, gn, c_stride, es), es, false},
+                      {flat(dy, static_cast<size_t>(T) * d * es), es, false}, {flat(A_log, nh), 4, false},
+                      {flat(D, nh), 4, true}, {flat(dt_bias, ndt), 4, false},
+                      {flat(cu_seqlens, S > 0 ? (static_cast<size_t>(S) + 1) * 4 : 0), 4, false},
+                      {flat(state_in, ns), 4, true}, {flat(dstate_out, ns), 4, true}};
+  const Array out[] = {{rows(dx, T, d, dx_stride, es), es, false}, {rows(ddt, dt != nullptr ? T : 0, H, ddt_stride, es), es, false},
+                       {rows(dB, T, gn, db_stride, es), es, false}, {rows(dC, T, gn, dc_stride, es), es, false},
+                       {flat(dA_log, nh), 4, false}, {flat(dD, D != nullptr ? nh : 0), 4, false},
+                       {flat(ddt_bias, ndt), 4, false}, {flat(dstate_in, ns), 4, true}};
+  if ((rc = check_arrays(in, 11)) != MM_OK || (rc = check_arrays(out, 8)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 11, out, 8)) != MM_OK) return rc;
+  HeadsPlan p;
+  if ((rc = plan_heads(p, S, T, H, P, N, true)) != MM_OK) return rc;
+  if (p.total > 0 && (workspace == nullptr || workspace_bytes < p.total)) return MM_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
+  const HeadsArgs a{x, B, C, x_stride, b_stride, c_stride, P, G, N,
+                    {dt, dt_stride, A_log, dt_bias, D, cu_seqlens, S, H, T}};
+  const HeadsGrads o{dy, state_in, dstate_out, dx, ddt, dB, dC, dx_stride, ddt_stride, db_stride, dc_stride,
+                     dA_log, D != nullptr ? dD : nullptr, dt != nullptr ? ddt_bias : nullptr, dstate_in};
+  char* ws = static_cast<char*>(workspace);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (io_dtype == MM_IO_BF16) return launch_backward<uint16_t>(p, a, o, ws, st);
+  return launch_backward<float>(p, a, o, ws, st);
+}
+
+// ---------------------------------------------------------------- norms
+
+int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, void* out, int64_t nrows, int32_t d,
+                          int32_t groups, float eps, int32_t gate_first, int32_t io_dtype, int64_t y_stride,
+                          int64_t z_stride, void* stream) {
+  int rc = check_gate_sizes(nrows, d, groups, eps, io_dtype);
+  if (rc != MM_OK) return rc;
+  if (nrows == 0 || d == 0) return MM_OK;
+  if (y_stride < d || z_stride < d) return MM_ERR_DIM;
+  const size_t es = esize(io_dtype);
+  const Array in[] = {{rows(y, nrows, d, y_stride, es), es, false}, {rows(z, nrows, d, z_stride, es), es, false},
+                      {flat(weight, static_cast<size_t>(d) * 4), 4, false}};
+  const Array o[] = {{flat(out, static_cast<size_t>(nrows) * d * es), es, false}};
+  if ((rc = check_arrays(in, 3)) != MM_OK || (rc = check_arrays(o, 1)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 3, o, 1, y_stride == d ? y : nullptr)) != MM_OK) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const auto go = [&](auto io) {
+    using IO = decltype(io);
+    const GateArgs<IO> a{static_cast<const IO*>(y), static_cast<const IO*>(z), nullptr, y_stride, z_stride, weight,
+                         nrows, d, groups, eps, gate_first != 0 ? 1 : 0};
+    hipLaunchKernelGGL((k_gate_norm<IO>), dim3(static_cast<unsigned>(nrows * groups)), dim3(kNormThreads), 0, st, a,
+                       static_cast<IO*>(out));
+  };
+  if (io_dtype == MM_IO_BF16) go(uint16_t{}); else go(float{});
+  return launched();
+}
+
+size_t mamba_mixer_gate_norm_backward_workspace_bytes(int64_t nrows, int32_t d, int32_t groups) {
+  if (check_gate_sizes(nrows, d, groups, 0.0f, MM_IO_F32) != MM_OK) return 0;
+  return align256(static_cast<size_t>(nrows) * groups * 4) + align256(static_cast<size_t>(kNormParts) * d * 4);
+}
+
+int mamba_mixer_gate_norm_backward(const void* dout, const void* y, const void* z, const float* weight, void* dy,
+                                   void* dz, float* dweight, int64_t nrows, int32_t d, int32_t groups, float eps,
+                                   int32_t gate_first, int32_t io_dtype, int64_t y_stride, int64_t z_stride,
+                                   int64_t dy_stride, int64_t dz_stride, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  int rc = check_gate_sizes(nrows, d, groups, eps, io_dtype);
+  if (rc != MM_OK) return rc;
+  if (d == 0) return MM_OK;
+  if (y_stride < d || z_stride < d || dy_stride < d || dz_stride < d) return MM_ERR_DIM;
+  const size_t es = esize(io_dtype), nd = static_cast<size_t>(d) * 4;
+  const Array in[] = {{flat(dout, static_cast<size_t>(nrows) * d * es), es, false},
+                      {rows(y, nrows, d, y_stride, es), es, false}, {rows(z, nrows, d, z_stride, es), es, false},
+                      {flat(weight, nd), 4, false}};
+  const Array o[] = {{rows(dy, nrows, d, dy_stride, es), es, false}, {rows(dz, nrows, d, dz_stride, es), es, false},
+                     {flat(dweight, nd), 4, false}};
+  if ((rc = check_arrays(in, 4)) != MM_OK || (rc = check_arrays(o, 3)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 4, o, 3)) != MM_OK) return rc;
+  const size_t need = mamba_mixer_gate_norm_backward_workspace_bytes(nrows, d, groups);
+  if (workspace == nullptr || workspace_bytes < need) return MM_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  float* stats = static_cast<float*>(workspace);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(static_cast<size_t>(nrows) * groups * 4));
+  const int64_t parts = std::min<int64_t>(kNormParts, nrows);
+  const unsigned cols = static_cast<unsigned>(cdiv(d, kNormThreads));
+  const auto go = [&](auto io) {
+    using IO = decltype(io);
+    const GateArgs<IO> a{static_cast<const IO*>(y), static_cast<const IO*>(z), static_cast<const IO*>(dout), y_stride,
+                         z_stride, weight, nrows, d, groups, eps, gate_first != 0 ? 1 : 0};
+    hipLaunchKernelGGL((k_gate_norm_bwd<IO>), dim3(static_cast<unsigned>(nrows * groups)), dim3(kNormThreads), 0, st, a,
+                       static_cast<IO*>(dy), static_cast<IO*>(dz), dy_stride, dz_stride, stats);
+    hipLaunchKernelGGL((k_gate_norm_dw<IO>), dim3(cols, static_cast<unsigned>(parts)), dim3(kNormThreads), 0, st, a, stats,
+                       part, cdiv(nrows, parts));
+  };
+  if (nrows > 0) { if (io_dtype == MM_IO_BF16) go(uint16_t{}); else go(float{}); }
+  hipLaunchKernelGGL(k_norm_parts, dim3(cols), dim3(kNormThreads), 0, st, part, dweight, static_cast<int>(parts),
+                     static_cast<int64_t>(d), d);
+  return launched();
+}
+
+int mamba_mixer_residual_norm(const void* h, const void* residual, const float* weight, const float* post_weight,
+                              const float* scale_vec, float scale, void* residual_out, void* out, int64_t nrows,
+                              int32_t d, float eps, int32_t io_dtype, int32_t res_dtype, void* stream) {
+  int rc = check_residual_sizes(nrows, d, eps, io_dtype, res_dtype);
+  if (rc != MM_OK) return rc;
+  if (nrows == 0 || d == 0) return MM_OK;
+  const size_t es = esize(io_dtype), rs = esize(res_dtype), n = static_cast<size_t>(nrows) * d, nd = static_cast<size_t>(d) * 4;
+  const Array in[] = {{flat(h, n * es), es, false}, {flat(residual, n * rs), rs, true}, {flat(weight, nd), 4, false},
+                      {flat(post_weight, nd), 4, true}, {flat(scale_vec, nd), 4, true}};
+  const Array o[] = {{flat(residual_out, n * rs), rs, false}, {flat(out, n * es), es, false}};
+  if ((rc = check_arrays(in, 5)) != MM_OK || (rc = check_arrays(o, 2)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 5, o, 2, residual != out ? residual : nullptr)) != MM_OK) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return by_types(io_dtype, res_dtype, [&](auto io, auto rt) {
+    using IO = decltype(io);
+    using RES = decltype(rt);
+    const ResArgs<IO, RES> a{static_cast<const IO*>(h), static_cast<const RES*>(residual), weight, post_weight,
+                             scale_vec, scale, eps, nrows, d};
+    const int r = allow_lds(&k_residual_norm<IO, RES>, nd);
+    if (r != MM_OK) return r;
+    hipLaunchKernelGGL((k_residual_norm<IO, RES>), dim3(static_cast<unsigned>(nrows)), dim3(kNormThreads), nd, st, a,
+                       static_cast<RES*>(residual_out), static_cast<IO*>(out));
+    return launched();
+  });
+}
+
+size_t mamba_mixer_residual_norm_backward_workspace_bytes(int64_t nrows, int32_t d) {
+  if (check_residual_sizes(nrows, d, 0.0f, MM_IO_F32, MM_IO_F32) != MM_OK) return 0;
+  return align256(static_cast<size_t>(nrows) * 3 * 4) + align256(static_cast<size_t>(kNormParts) * 3 * d * 4);
+}
+
+int mamba_mixer_residual_norm_backward(const void* dout, const void* dresidual_out, const void* h,
+                                       const void* residual_out, const float* weight, const float* post_weight,
+                                       const float* scale_vec, float scale, void* dresidual, void* dh, float* dweight,
+                                       float* dpost_weight, float* dscale_vec, int64_t nrows, int32_t d, float eps,
+                                       int32_t io_dtype, int32_t res_dtype, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  int rc = check_residual_sizes(nrows, d, eps, io_dtype, res_dtype);
+  if (rc != MM_OK) return rc;
+  if (d == 0) return MM_OK;
+  const size_t es = esize(io_dtype), rs = esize(res_dtype), n = static_cast<size_t>(nrows) * d, nd = static_cast<size_t>(d) * 4;
+  const Array in[] = {{flat(dout, n * es), es, false}, {flat(dresidual_out, n * rs), rs, true}, {flat(h, n * es), es, false},
+                      {flat(residual_out, n * rs), rs, false}, {flat(weight, nd), 4, false},
+                      {flat(post_weight, nd), 4, true}, {flat(scale_vec, nd), 4, true}};
+  const Array o[] = {{flat(dresidual, n * rs), rs, false}, {flat(dh, n * es), es, false}, {flat(dweight, nd), 4, false},
+                     {flat(dpost_weight, post_weight != nullptr ? nd : 0), 4, false},
+                     {flat(dscale_vec, scale_vec != nullptr ? nd : 0), 4, false}};
+  if ((rc = check_arrays(in, 7)) != MM_OK || (rc = check_arrays(o, 5)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 7, o, 5, dresidual == dresidual_out ? dresidual_out : nullptr)) != MM_OK) return rc;
+  const size_t need = mamba_mixer_residual_norm_backward_workspace_bytes(nrows, d);
+  if (workspace == nullptr || workspace_bytes < need) return MM_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  float* stats = static_cast<float*>(workspace);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(static_cast<size_t>(nrows) * 3 * 4));
+  const int64_t parts = std::min<int64_t>(kNormParts, nrows);
+  const unsigned cols = static_cast<unsigned>(cdiv(d, kNormThreads));
+  if (nrows > 0) {
+    rc = by_types(io_dtype, res_dtype, [&](auto io, auto rt) {
+      using IO = decltype(io);
+      using RES = decltype(rt);
+      const ResArgs<IO, RES> a{static_cast<const IO*>(h), static_cast<const RES*>(residual_out), weight, post_weight,
+                               scale_vec, scale, eps, nrows, d};
+      const IO* go = static_cast<const IO*>(dout);
+      const RES* gr = static_cast<const RES*>(dresidual_out);
+      const int r = allow_lds(&k_residual_norm_bwd<IO, RES>, nd);
+      if (r != MM_OK) return r;
+      // the rows' factors and the weights' sums before the gradients: dresidual may be written over dresidual_out
+      const dim3 grid(static_cast<unsigned>(nrows)), block(kNormThreads);
+      hipLaunchKernelGGL((k_residual_norm_bwd<IO, RES>), grid, block, nd, st, a, go, gr, static_cast<RES*>(nullptr),
+                         static_cast<IO*>(nullptr), stats);
+      hipLaunchKernelGGL((k_residual_norm_dw<IO, RES>), dim3(cols, static_cast<unsigned>(parts)), block, 0, st, a, go, gr,
+                         stats, part, cdiv(nrows, parts));
+      hipLaunchKernelGGL((k_residual_norm_bwd<IO, RES>), grid, block, nd, st, a, go, gr, static_cast<RES*>(dresidual),
+                         static_cast<IO*>(dh), stats);
+      return launched();
+    });
+    if (rc != MM_OK) return rc;
+  }
+  float* outs[] = {dweight, dpost_weight, dscale_vec};
+  for (int i = 0; i < 3; ++i)
+    if (i == 0 || (i == 1 ? post_weight : scale_vec) != nullptr)
+      hipLaunchKernelGGL(k_norm_parts, dim3(cols), dim3(kNormThreads), 0, st, part + static_cast<int64_t>(i) * d, outs[i],
+                         static_cast<int>(parts), static_cast<int64_t>(3) * d, d);
+  return launched();
+}
+
+}  // extern "C"

@@ -29,6 +29,7 @@
 #include "mm_backward.h"
 #include "mm_decode.h"
 #include "mm_device.h"
+#include "mm_host.h"
 #include "mm_prefill.h"
 #include "mm_project.h"
 #include "mm_row.h"
@@ -49,9 +50,7 @@ constexpr int64_t kCUs = 256;
 constexpr int kReplayN = 16;
 constexpr int kReplayMaxW = 4;
 
-inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline int nmax_for(int N) { return N <= 4 ? 4 : (N <= 8 ? 8 : 16); }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Plan {
   int engine;  // MM_ENGINE_LANE or MM_ENGINE_ROW
@@ -196,13 +195,6 @@ const char* kernel_name(const Plan& p, int i) {
     return fin;
   }
   return "";
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && a0 < b0 + nb && b0 < a0 + na;
 }
 
 // Records events[k] (if given) on the stream before the k-th kernel and events[n]
@@ -375,11 +367,6 @@ int check_prefill_sizes(int32_t S, int64_t T, int32_t d, int32_t N, int32_t K, i
   if (d > 0 && static_cast<uint64_t>(S) > MM_MAX_ROWS_X_D / static_cast<uint64_t>(d)) return MM_ERR_DIM;
   return MM_OK;
 }
-
-struct Span {
-  const void* p;
-  size_t n;
-};
 
 // Validation and launch shared by the replay entry points.  multi: z, C and y are rings
 // [W][Bs][...] indexed by window step; otherwise they are this step's [Bs][...].  dual: the

@@ -1,0 +1,428 @@
+// The head scan: linear attention with one decay per head, over packed sequences.
+//
+//   delta = softplus(dt + dt_bias)          (1 when no dt is given: a fixed decay for each head)
+//   h_t   = a_t h_{t-1} + delta_t x_t B_t^T,   a_t = exp(-exp(A_log) delta_t)     [P, N] per head
+//   y_t   = h_t C_t + D x_t                    head h reads group h / (H / G) of B and C
+//
+// Segments.  A sequence is cut where the packed token index is a multiple of Ls (the segment
+// length), so the segment with tokens [b Ls, (b + 1) Ls) of sequence s has the row s + b in every
+// per-segment array: the rows of the sequences follow one another without overlap, no plan has to
+// be computed, and there are at most T / Ls + S of them.  With Ls > T every sequence is one segment.
+// With shorter segments three launches replace one: the state each segment adds from zero
+// (LOCAL), the states the segments start from (k_heads_carry), and the outputs.
+//
+// The kernels here take the recurrence token by token in float32 and serve every type, size and
+// stride.
+#pragma once
+
+#include "mm_device.h"
+
+namespace mm {
+
+constexpr int kHeadsMaxN = 256;  // columns of the state (N, and P in the backward's transposed runs)
+constexpr int kHeadsMaxP = 256;
+constexpr int kSeqThreads = 256;
+constexpr int kSeqRows = 16;     // state rows per workgroup: one per 16-lane row
+constexpr int kSeqTok = 16;      // tokens staged at a time
+constexpr int kHeadsBlock = 64;  // tokens per block of the backward's inner products
+
+// row rho of a per-segment array: its sequence, and its tokens [t0, t1) (none: t0 >= t1)
+struct Segment {
+  int s;
+  int64_t t0, t1;
+  int64_t seq0, seq1;  // the sequence's tokens
+  __device__ bool first() const { return t0 <= seq0; }
+  __device__ bool last() const { return t1 >= seq1; }
+};
+// the largest s with s + cu[s] / L <= rho
+__device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ cu, int S, int64_t rho, int64_t L) {
+  int lo = 0, hi = S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (mid + cu[mid] / L <= rho) lo = mid; else hi = mid - 1;
+  }
+  Segment g;
+  g.s = lo;
+  g.seq0 = cu[lo];
+  g.seq1 = cu[lo + 1];
+  const int64_t b = rho - lo;
+  g.t0 = b * L > g.seq0 ? b * L : g.seq0;
+  g.t1 = (b + 1) * L < g.seq1 ? (b + 1) * L : g.seq1;
+  return g;
+}
+// rows of a per-segment array for S sequences and T tokens
+inline int64_t segment_rows(int64_t S, int64_t T, int64_t L) { return S + T / L; }
+
+// a token tensor [T, ., W]: element (t, h, i) at t * ts + (h / div) * W + i
+template <typename IO>
+struct Tok {
+  const IO* p;
+  int64_t ts;
+  int W, div;
+  __device__ const IO* at(int64_t t, int h) const { return p + t * ts + static_cast<int64_t>(h / div) * W; }
+};
+
+struct HeadPar {
+  const void* dt;        // [T, H] io, or NULL
+  int64_t dt_ts;
+  const float* A_log;    // [H]
+  const float* dt_bias;  // [H] (NULL without dt)
+  const float* D;        // [H] or NULL
+  const int32_t* cu;
+  int S, H;
+  int64_t T;
+};
+template <typename IO>
+__device__ __forceinline__ float head_delta(const HeadPar& hp, int64_t t, int h) {
+  if (hp.dt == nullptr) return 1.0f;
+  return softplus(ld_io(static_cast<const IO*>(hp.dt) + t * hp.dt_ts, h) + hp.dt_bias[h]);
+}
+__device__ __forceinline__ float head_A2(const HeadPar& hp, int h) {  // A log2(e)
+  return -exp2_hw(hp.A_log[h] * kLog2e) * kLog2e;
+}
+
+// sum over the 16 lanes of a row, in every lane of it
+__device__ __forceinline__ float row_sum16(float v) {
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x128, 0xF, 0xF, true);  // row_ror:8
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x124, 0xF, 0xF, true);  // row_ror:4
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x122, 0xF, 0xF, true);  // row_ror:2
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x121, 0xF, 0xF, true);  // row_ror:1
+  return v;
+}
+
+// One run of the recurrence on a state of R rows and K columns (element (r, k) of a stored state at
+// r sr + k sk):
+//   forward   h = a_t h + w_t u_t[r] v_t[k],   out_t[r] = sum_k h s_t[k]          w = delta
+//   reverse   h = h + u_t[r] v_t[k],           out_t[r] = sum_k h s_t[k],  then h = a_t h
+// (the reverse run is the adjoint's recurrence from the last token to the first).  The four
+// products of the scan and its gradients are such runs:
+//   y   forward, u = x (R = P), v = B, s = C          dx   reverse, u = dy (R = P), v = C, s = B
+//   dC  forward, u = B (R = N), v = x, s = dy         dB   reverse, u = C (R = N), v = dy, s = x
+template <typename IO>
+struct SeqRun {
+  Tok<IO> u, v, s;
+  int R, K;
+  int64_t sr, sk, sh;         // strides of a stored state: rows, columns, heads
+  const float* init;          // [S] states, or NULL for zeros
+  float* fin;                 // [S] states out, or NULL
+  float* carry;               // [rows] states: written by LOCAL runs, else read where a sequence has several segments
+  float* decay;               // [rows, H] log2 of a segment's decay, written by LOCAL runs
+  int64_t Ls;
+  IO* out;                    // [T, H, R], rows out_ts apart, or NULL
+  int64_t out_ts;
+  float* out32;               // [T, H, R] contiguous in float32, or NULL
+  int out_delta;              // multiply the output by delta
+  int add_D;                  // add D u
+  const float* dots_with;     // reverse: the forward states at the ends of 64-token blocks, [rows64] states, or NULL
+  float* dots;                // and the inner products with them, [rows64, H, row blocks]
+  float* store;               // forward: those states, or NULL
+};
+
+template <typename IO, int KV, bool REV, bool LOCAL>
+__global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar hp) {
+  constexpr int KP = 16 * KV;
+  __shared__ float sv[kSeqTok][KP], ss[kSeqTok][KP];
+  __shared__ float su[kSeqTok][kSeqRows], so[kSeqTok][kSeqRows + 1];
+  __shared__ float sdel[kSeqTok], sdec[kSeqTok];
+  __shared__ float sdot[kSeqThreads / kWave];
+  const int tid = threadIdx.x, lane = tid & 15, row = tid >> 4;
+  const int nrb = (q.R + kSeqRows - 1) / kSeqRows;
+  const int rb = blockIdx.x % nrb;
+  const int h = (blockIdx.x / nrb) % hp.H;
+  const int64_t rho = blockIdx.x / nrb / hp.H;
+  const Segment g = segment_of(hp.cu, hp.S, rho, q.Ls);
+  const int r = rb * kSeqRows + row;
+  const bool many = g.seq1 > g.seq0 && (g.seq1 - 1) / q.Ls > g.seq0 / q.Ls;  // several segments
+  if (g.t0 >= g.t1 && !(g.seq0 == g.seq1 && rho == g.s + g.seq0 / q.Ls)) return;
+  if (LOCAL && (!many || (REV ? g.first() : g.last()))) return;
+  const int64_t soff = h * q.sh + static_cast<int64_t>(r) * q.sr;
+  const int64_t sset = static_cast<int64_t>(hp.H) * q.sh;
+  const float A2 = head_A2(hp, h);
+  const float Dh = (q.add_D && hp.D != nullptr) ? hp.D[h] : 0.0f;
+  float st[KV];
+#pragma unroll
+  for (int i = 0; i < KV; ++i) st[i] = 0.0f;
+  if (!LOCAL) {
+    const float* from = many ? q.carry + rho * sset : (q.init ? q.init + g.s * sset : nullptr);
+    if (from != nullptr && r < q.R)
+#pragma unroll
+      for (int i = 0; i < KV; ++i) {
+        const int k = lane * KV + i;
+        if (k < q.K) st[i] = from[soff + k * q.sk];
+      }
+  }
+  float dsum = 0.0f;
+  const int64_t n = g.t1 - g.t0;
+  // blocks of kSeqTok tokens from the segment's first token on, taken in reverse by a reverse run
+  const int64_t nb = n > 0 ? (n + kSeqTok - 1) / kSeqTok : 0;
+  for (int64_t ib = 0; ib < nb; ++ib) {
+    const int64_t tb = g.t0 + (REV ? nb - 1 - ib : ib) * kSeqTok;
+    const int cnt = static_cast<int>(g.t1 - tb < kSeqTok ? g.t1 - tb : kSeqTok);
+    __syncthreads();
+    for (int i = tid; i < kSeqTok * KP; i += kSeqThreads) {
+      const int t = i / KP, k = i % KP;
+      const bool in = t < cnt && k < q.K;
+      sv[t][k] = in ? ld_io(q.v.at(tb + t, h), k) : 0.0f;
+      if (!LOCAL) ss[t][k] = in ? ld_io(q.s.at(tb + t, h), k) : 0.0f;
+    }
+    {
+      const int t = tid >> 4, rr = rb * kSeqRows + (tid & 15);
+      su[t][tid & 15] = (t < cnt && rr < q.R) ? ld_io(q.u.at(tb + t, h), rr) : 0.0f;
+    }
+    if (tid < kSeqTok) {
+      const float d = tid < cnt ? head_delta<IO>(hp, tb + tid, h) : 0.0f;
+      sdel[tid] = d;
+      sdec[tid] = d * A2;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int j = 0; j < kSeqTok; ++j) {
+      const int t = REV ? kSeqTok - 1 - j : j;
+      if (t >= cnt) continue;
+      const int64_t tok = tb + t;
+      if (REV && !LOCAL && q.dots_with != nullptr && ((tok + 1) % kHeadsBlock == 0 || tok + 1 == g.seq1)) {
+        // before token tok enters: h is the adjoint of the state after it
+        const float* with = q.dots_with + (g.s + tok / kHeadsBlock) * sset + soff;
+        float d = 0.0f;
+        if (r < q.R)
+#pragma unroll
+          for (int i = 0; i < KV; ++i) {
+            const int k = lane * KV + i;
+            if (k < q.K) d = __builtin_fmaf(st[i], with[k * q.sk], d);
+          }
+        d = row_sum16(d);
+        d += __shfl_xor(d, 16);
+        d += __shfl_xor(d, 32);
+        if ((tid & 63) == 0) sdot[tid >> 6] = d;
+        __syncthreads();
+        if (tid == 0)
+          q.dots[((g.s + tok / kHeadsBlock) * hp.H + h) * nrb + rb] = (sdot[0] + sdot[1]) + (sdot[2] + sdot[3]);
+        __syncthreads();
+      }
+      const float a = exp2_hw(sdec[t]);
+      dsum += sdec[t];
+      const float uu = su[t][row] * (REV ? 1.0f : sdel[t]);
+      float o = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KV; ++i) {
+        const int k = lane * KV + i;
+        st[i] = REV ? __builtin_fmaf(uu, sv[t][k], st[i]) : __builtin_fmaf(a, st[i], uu * sv[t][k]);
+        if (!LOCAL) o = __builtin_fmaf(st[i], ss[t][k], o);
+        if (REV) st[i] *= a;
+      }
+      if (!LOCAL) {
+        o = row_sum16(o);
+        if (lane == 0) so[t][row] = (q.out_delta ? sdel[t] * o : o) + Dh * su[t][row];
+      }
+      if (!REV && !LOCAL && q.store != nullptr && ((tok + 1) % kHeadsBlock == 0 || tok + 1 == g.seq1) && r < q.R)
+#pragma unroll
+        for (int i = 0; i < KV; ++i) {
+          const int k = lane * KV + i;
+          if (k < q.K) q.store[(g.s + tok / kHeadsBlock) * sset + soff + k * q.sk] = st[i];
+        }
+    }
+    if (!LOCAL && (q.out != nullptr || q.out32 != nullptr)) {
+      __syncthreads();
+      const int t = tid >> 4, rr = rb * kSeqRows + (tid & 15);
+      if (t < cnt && rr < q.R) {
+        const int64_t at = static_cast<int64_t>(h) * q.R + rr;
+        if (q.out != nullptr) st_io(q.out, (tb + t) * q.out_ts + at, so[t][tid & 15]);
+        if (q.out32 != nullptr) q.out32[(tb + t) * hp.H * q.R + at] = so[t][tid & 15];
+      }
+    }
+  }
+  float* to = LOCAL ? q.carry + rho * sset : ((REV ? g.first() : g.last()) && q.fin ? q.fin + g.s * sset : nullptr);
+  if (to != nullptr && r < q.R)
+#pragma unroll
+    for (int i = 0; i < KV; ++i) {
+      const int k = lane * KV + i;
+      if (k < q.K) to[soff + k * q.sk] = st[i];
+    }
+  if (LOCAL && rb == 0 && tid == 0) q.decay[rho * hp.H + h] = dsum;
+}
+
+// The states that the segments of a sequence start from, in place of what they add: one thread per
+// state element of a sequence with several segments, segment after segment.  reverse: from the last.
+__global__ __launch_bounds__(256) void k_heads_carry(float* __restrict__ carry, const float* __restrict__ decay,
+                                                     const float* __restrict__ init, const int32_t* __restrict__ cu,
+                                                     int H, int64_t PN, int64_t Ls, int reverse, int s0) {
+  const int s = s0 + blockIdx.y;
+  const int64_t seq0 = cu[s], seq1 = cu[s + 1];
+  if (seq1 <= seq0 || (seq1 - 1) / Ls <= seq0 / Ls) return;
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t set = H * PN;
+  if (e >= set) return;
+  const int h = static_cast<int>(e / PN);
+  const int64_t r0 = s + seq0 / Ls, r1 = s + (seq1 - 1) / Ls;
+  float cur = init != nullptr ? init[s * set + e] : 0.0f;
+  for (int64_t i = 0; i <= r1 - r0; ++i) {
+    const int64_t rho = reverse ? r1 - i : r0 + i;
+    float* slot = carry + rho * set + e;
+    float local = 0.0f;
+    if (i < r1 - r0) local = *slot;
+    *slot = cur;
+    if (i < r1 - r0) cur = __builtin_fmaf(exp2_hw(decay[rho * H + h]), cur, local);
+  }
+}
+
+// ------------------------------------------------------------------------------------ decode
+// One token for each row of a batch: state rows p over 16-lane rows as in the sequential kernel.
+template <typename IO, int KV>
+__global__ __launch_bounds__(kSeqThreads) void k_heads_decode_any(Tok<IO> x, Tok<IO> B, Tok<IO> C, HeadPar hp,
+                                                                  const float* state_in, float* state_out,
+                                                                  IO* __restrict__ y, int P, int N) {
+  const int tid = threadIdx.x, lane = tid & 15, row = tid >> 4;
+  const int nrb = (P + kSeqRows - 1) / kSeqRows;
+  const int rb = blockIdx.x % nrb;
+  const int h = (blockIdx.x / nrb) % hp.H;
+  const int64_t b = blockIdx.x / nrb / hp.H;
+  const int p = rb * kSeqRows + row;
+  if (p >= P) return;
+  const float delta = head_delta<IO>(hp, b, h);
+  const float a = exp2_hw(delta * head_A2(hp, h));
+  const float xv = ld_io(x.at(b, h), p);
+  const float dx = delta * xv;
+  const int64_t off = ((b * hp.H + h) * P + p) * static_cast<int64_t>(N);
+  const IO *Bp = B.at(b, h), *Cp = C.at(b, h);
+  float o = 0.0f;
+#pragma unroll
+  for (int i = 0; i < KV; ++i) {
+    const int n = i * 16 + lane;
+    if (n < N) {
+      const float v = __builtin_fmaf(a, state_in ? state_in[off + n] : 0.0f, dx * ld_io(Bp, n));
+      state_out[off + n] = v;
+      o = __builtin_fmaf(v, ld_io(Cp, n), o);
+    }
+  }
+  o = row_sum16(o);
+  if (lane == 0) st_io(y, (b * hp.H + h) * P + p, o + (hp.D ? hp.D[h] * xv : 0.0f));
+}
+
+// ------------------------------------------------------------------------------------ backward
+// q_t = C_t . dC_t and r_t = B_t . dB_t (head by head, dB before its factor delta): a 16-lane row per (t, h)
+template <typename IO>
+__global__ __launch_bounds__(256) void k_heads_qr(Tok<IO> B, Tok<IO> C, const float* __restrict__ dB,
+                                                  const float* __restrict__ dC, float* __restrict__ q,
+                                                  float* __restrict__ r, int64_t T, int H, int N) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
+  const int lane = threadIdx.x & 15;
+  if (i >= T * H) return;
+  const int64_t t = i / H;
+  const int h = static_cast<int>(i % H);
+  const IO *Bp = B.at(t, h), *Cp = C.at(t, h);
+  float sq = 0.0f, sr = 0.0f;
+  for (int n = lane; n < N; n += 16) {
+    sq = __builtin_fmaf(ld_io(Cp, n), dC[i * N + n], sq);
+    sr = __builtin_fmaf(ld_io(Bp, n), dB[i * N + n], sr);
+  }
+  sq = row_sum16(sq);
+  sr = row_sum16(sr);
+  if (lane == 0) {
+    q[i] = sq;
+    r[i] = sr;
+  }
+}
+
+// The gradients of delta.  With l = log a, dl_t = <G_t, a_t h_{t-1}> satisfies dl_t = dl_{t+1} + q_t - p_t
+// (p = delta r), so inside a 64-token block it is a sum from the block's end, where it is the inner product
+// of the adjoint and the state (dots): the sum restarts there and its rounding does not build up along the
+// sequence.  One wave per (block, head), one token per lane.
+template <typename IO>
+__global__ __launch_bounds__(64) void k_heads_ddt(HeadPar hp, Tok<IO> x, Tok<IO> dy, const float* __restrict__ q,
+                                                  const float* __restrict__ r, const float* __restrict__ dots, int ndots,
+                                                  float* __restrict__ delta, IO* __restrict__ ddt, int64_t ddt_ts,
+                                                  float* __restrict__ sums, int P) {
+  const int lane = threadIdx.x;
+  const int h = blockIdx.x % hp.H;
+  const int64_t rho = blockIdx.x / hp.H;
+  const Segment g = segment_of(hp.cu, hp.S, rho, kHeadsBlock);
+  float* part = sums + (rho * hp.H + h) * 3;
+  if (g.t0 >= g.t1) {
+    if (lane < 3) part[lane] = 0.0f;
+    return;
+  }
+  const int64_t t = g.t0 + lane;
+  const bool in = t < g.t1;
+  float del = 0.0f, rr = 0.0f, diff = 0.0f;
+  if (in) {
+    del = head_delta<IO>(hp, t, h);
+    delta[t * hp.H + h] = del;
+    rr = r[t * hp.H + h];
+    diff = q[t * hp.H + h] - del * rr;
+  }
+  float e = 0.0f;
+  for (int i = 0; i < ndots; ++i) e += dots[(rho * hp.H + h) * ndots + i];
+  for (int k = 1; k < 64; k *= 2) {  // sums over the lanes from this one on
+    const float o = __shfl_down(diff, k);
+    if (lane + k < 64) diff += o;
+  }
+  const float dl = e + diff;
+  const float A = -exp2_hw(hp.A_log[h] * kLog2e);
+  float dA = 0.0f, db = 0.0f, dD = 0.0f;
+  if (in) {
+    dA = del * dl * A;
+    if (hp.dt != nullptr) {
+      const float v = ld_io(static_cast<const IO*>(hp.dt) + t * hp.dt_ts, h) + hp.dt_bias[h];
+      db = __builtin_fmaf(A, dl, rr) * rcp_hw(1.0f + exp2_hw(-v * kLog2e));
+      st_io(ddt, t * ddt_ts + h, db);
+    }
+    const IO *xp = x.at(t, h), *gp = dy.at(t, h);
+    for (int p = 0; p < P; ++p) dD = __builtin_fmaf(ld_io(xp, p), ld_io(gp, p), dD);
+  }
+  for (int k = 32; k > 0; k /= 2) {
+    dA += __shfl_xor(dA, k);
+    db += __shfl_xor(db, k);
+    dD += __shfl_xor(dD, k);
+  }
+  if (lane == 0) {
+    part[0] = dA;
+    part[1] = db;
+    part[2] = dD;
+  }
+}
+
+// dB and dC of a group: the sums of its heads' shares (dB's times delta)
+template <typename IO>
+__global__ __launch_bounds__(256) void k_heads_group(const float* __restrict__ dBh, const float* __restrict__ dCh,
+                                                     const float* __restrict__ delta, IO* __restrict__ dB,
+                                                     IO* __restrict__ dC, int64_t db_ts, int64_t dc_ts, int64_t T, int H,
+                                                     int G, int N) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= T * G * N) return;
+  const int n = static_cast<int>(i % N);
+  const int g = static_cast<int>(i / N % G);
+  const int64_t t = i / N / G;
+  const int hg = H / G;
+  float b = 0.0f, c = 0.0f;
+  for (int h = g * hg; h < (g + 1) * hg; ++h) {
+    const int64_t o = (t * H + h) * N + n;
+    b = __builtin_fmaf(delta[t * H + h], dBh[o], b);
+    c += dCh[o];
+  }
+  st_io(dB, t * db_ts + static_cast<int64_t>(g) * N + n, b);
+  st_io(dC, t * dc_ts + static_cast<int64_t>(g) * N + n, c);
+}
+
+// dA_log, ddt_bias and dD: the sums of the blocks' parts, one workgroup per head, in a fixed order
+__global__ __launch_bounds__(256) void k_heads_params(const float* __restrict__ sums, int64_t rows, int H,
+                                                      float* __restrict__ dA_log, float* __restrict__ ddt_bias,
+                                                      float* __restrict__ dD) {
+  __shared__ float s[3][256];
+  const int h = blockIdx.x, tid = threadIdx.x;
+  float v[3] = {0.0f, 0.0f, 0.0f};
+  for (int64_t i = tid; i < rows; i += 256)
+    for (int k = 0; k < 3; ++k) v[k] += sums[(i * H + h) * 3 + k];
+  for (int k = 0; k < 3; ++k) s[k][tid] = v[k];
+  for (int w = 128; w > 0; w /= 2) {
+    __syncthreads();
+    if (tid < w)
+      for (int k = 0; k < 3; ++k) s[k][tid] += s[k][tid + w];
+  }
+  if (tid == 0) {
+    dA_log[h] = s[0][0];
+    if (ddt_bias != nullptr) ddt_bias[h] = s[1][0];
+    if (dD != nullptr) dD[h] = s[2][0];
+  }
+}
+
+}  // namespace mm

@@ -1,0 +1,303 @@
+"""The head scan (linear attention with one decay per head) and the norms around a mixer block: the
+binding of the ``mamba_mixer_heads_*``, ``mamba_mixer_gate_norm*`` and ``mamba_mixer_residual_norm*``
+calls.  Like the rest of the binding it checks shapes and types, allocates outputs and workspace and
+passes pointers; the computation is in the library's kernels.
+
+Token tensors may be column ranges of a wider one (a projection's output): their rows may be strided,
+the elements of a row are contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import MM_OK, MambaMixError, _check, _io_code, _ptr, _stream, check_cu_seqlens, load
+
+
+def _opt(t):
+    return _ptr(t) if t is not None else ctypes.c_void_p(0)
+
+
+def _rows(t, shape, dtype, name) -> int:
+    """Check a token tensor [T, ...] whose rows may be strided; returns the row stride in elements."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    width = 1
+    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != width and t.numel() > 0:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        width *= n
+    if t.shape[0] <= 1 or t.numel() == 0:
+        return max(width, 1)
+    if t.stride(0) < width:
+        raise ValueError(f"{name}: rows must not overlap (stride {t.stride(0)}, row length {width})")
+    return t.stride(0)
+
+
+def _head_inputs(x, dt, B, C, A_log, D, dt_bias):
+    """Checks of the inputs all three head-scan calls share; returns (T, H, P, G, N, strides)."""
+    import torch
+
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be [T, H, P] and B [T, G, N]")
+    T, H, P = x.shape
+    G, N = B.shape[1], B.shape[2]
+    io = x.dtype
+    _io_code(x)
+    strides = [_rows(x, (T, H, P), io, "x"), 0, _rows(B, (T, G, N), io, "B"), _rows(C, (T, G, N), io, "C")]
+    _check(A_log, (H,), torch.float32, "A_log")
+    if dt is not None:
+        strides[1] = _rows(dt, (T, H), io, "dt")
+        if dt_bias is None:
+            raise ValueError("dt_bias: required with dt")
+        _check(dt_bias, (H,), torch.float32, "dt_bias")
+    if D is not None:
+        _check(D, (H,), torch.float32, "D")
+    return T, H, P, G, N, strides
+
+
+def _workspace(given, need, device):
+    import torch
+
+    if given is None:
+        given = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    return given, _opt(given), 0 if given is None else given.numel() * given.element_size()
+
+
+def _out(t, shape, dtype, device, name):
+    """An output tensor: the caller's (rows may be strided) or a new one; returns it and its row stride."""
+    import torch
+
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    return t, _rows(t, shape, dtype, name)
+
+
+def _raise(rc, where):
+    if rc != MM_OK:
+        raise MambaMixError(rc, where)
+
+
+def heads_prefill(x, dt, B, C, A_log, D, dt_bias, cu_seqlens, state_in=None, state_out=None, y=None, workspace=None,
+                  stream=None):
+    """The head scan over packed sequences (see ``mamba_mixer_heads_prefill``).
+
+    x [T, H, P], dt [T, H] (None: a fixed decay for each head), B, C [T, G, N] share one io dtype
+    (float32 or bfloat16); A_log, D, dt_bias [H] float32 (D may be None); cu_seqlens [S+1] int32;
+    state_in [S, H, P, N] float32 (None: zeros).  Returns (y [T, H, P], state_out [S, H, P, N]);
+    pass state_out=state_in to update a state in place.
+    """
+    import torch
+
+    from . import CHECK_CU
+
+    T, H, P, G, N, strides = _head_inputs(x, dt, B, C, A_log, D, dt_bias)
+    S = cu_seqlens.shape[0] - 1
+    _check(cu_seqlens, (S + 1,), torch.int32, "cu_seqlens")
+    if CHECK_CU:
+        check_cu_seqlens(cu_seqlens, T)
+    if state_in is not None:
+        _check(state_in, (S, H, P, N), torch.float32, "state_in")
+    if state_out is None:
+        state_out = torch.empty((S, H, P, N), dtype=torch.float32, device=x.device)
+    _check(state_out, (S, H, P, N), torch.float32, "state_out")
+    if y is None:
+        y = torch.empty((T, H, P), dtype=x.dtype, device=x.device)
+    _check(y, (T, H, P), x.dtype, "y")
+    io = _io_code(x)
+    need = load().mamba_mixer_heads_prefill_workspace_bytes(S, T, H, P, G, N, io) if workspace is None else 0
+    workspace, wptr, wbytes = _workspace(workspace, need, x.device)
+    rc = load().mamba_mixer_heads_prefill(
+        _ptr(x), _opt(dt), _ptr(B), _ptr(C), _ptr(A_log), _opt(D), _opt(dt_bias), _ptr(cu_seqlens), _opt(state_in),
+        _ptr(state_out), _ptr(y), S, T, H, P, G, N, io, *strides, wptr, wbytes, _stream(stream))
+    _raise(rc, "mamba_mixer_heads_prefill")
+    return y, state_out
+
+
+def heads_decode(x, dt, B, C, A_log, D, dt_bias, state_in=None, state_out=None, y=None, stream=None):
+    """One token of the head scan for each of Bs rows (see ``mamba_mixer_heads_decode``): x [Bs, H, P],
+    dt [Bs, H] or None, B, C [Bs, G, N], state_in [Bs, H, P, N] float32 (None: zeros).  Returns
+    (y [Bs, H, P], state_out); pass state_out=state_in to update the states in place."""
+    import torch
+
+    Bs, H, P, G, N, strides = _head_inputs(x, dt, B, C, A_log, D, dt_bias)
+    if state_in is not None:
+        _check(state_in, (Bs, H, P, N), torch.float32, "state_in")
+    if state_out is None:
+        state_out = torch.empty((Bs, H, P, N), dtype=torch.float32, device=x.device)
+    _check(state_out, (Bs, H, P, N), torch.float32, "state_out")
+    if y is None:
+        y = torch.empty((Bs, H, P), dtype=x.dtype, device=x.device)
+    _check(y, (Bs, H, P), x.dtype, "y")
+    rc = load().mamba_mixer_heads_decode(
+        _ptr(x), _opt(dt), _ptr(B), _ptr(C), _ptr(A_log), _opt(D), _opt(dt_bias), _opt(state_in), _ptr(state_out),
+        _ptr(y), Bs, H, P, G, N, _io_code(x), *strides, _stream(stream))
+    _raise(rc, "mamba_mixer_heads_decode")
+    return y, state_out
+
+
+def heads_backward(x, dt, B, C, A_log, D, dt_bias, cu_seqlens, state_in, dy, dstate_out=None, dx=None, ddt=None,
+                   dB=None, dC=None, need_dstate=True, workspace=None, stream=None) -> dict:
+    """The gradients of ``heads_prefill`` (see ``mamba_mixer_heads_backward``) from dy [T, H, P] and
+    dstate_out [S, H, P, N] (None: the loss does not depend on the final states).  dx, ddt, dB and dC may be
+    given (column ranges of one gradient, for instance).  Returns a dict of dx, ddt, dB, dC (io), dA_log, dD,
+    ddt_bias and dstate_in (float32); ddt and ddt_bias are None without dt, dD without D, dstate_in with
+    need_dstate=False."""
+    import torch
+
+    from . import CHECK_CU
+
+    T, H, P, G, N, strides = _head_inputs(x, dt, B, C, A_log, D, dt_bias)
+    S = cu_seqlens.shape[0] - 1
+    io, dev = x.dtype, x.device
+    _check(cu_seqlens, (S + 1,), torch.int32, "cu_seqlens")
+    if CHECK_CU:
+        check_cu_seqlens(cu_seqlens, T)
+    for t, n in ((state_in, "state_in"), (dstate_out, "dstate_out")):
+        if t is not None:
+            _check(t, (S, H, P, N), torch.float32, n)
+    _check(dy, (T, H, P), io, "dy")
+    dx, sx = _out(dx, (T, H, P), io, dev, "dx")
+    ddt, sd = _out(ddt, (T, H), io, dev, "ddt") if dt is not None else (None, 0)
+    dB, sb = _out(dB, (T, G, N), io, dev, "dB")
+    dC, sc = _out(dC, (T, G, N), io, dev, "dC")
+    new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+    dA_log, dD, dbias = new(H), new(H) if D is not None else None, new(H) if dt is not None else None
+    dstate_in = new(S, H, P, N) if need_dstate else None
+    code = _io_code(x)
+    need = load().mamba_mixer_heads_backward_workspace_bytes(S, T, H, P, G, N, code) if workspace is None else 0
+    workspace, wptr, wbytes = _workspace(workspace, need, dev)
+    rc = load().mamba_mixer_heads_backward(
+        _ptr(x), _opt(dt), _ptr(B), _ptr(C), _ptr(A_log), _opt(D), _opt(dt_bias), _ptr(cu_seqlens), _opt(state_in),
+        _ptr(dy), _opt(dstate_out), _ptr(dx), _opt(ddt), _ptr(dB), _ptr(dC), _ptr(dA_log), _opt(dD), _opt(dbias),
+        _opt(dstate_in), S, T, H, P, G, N, code, *strides, sx, sd, sb, sc, wptr, wbytes, _stream(stream))
+    _raise(rc, "mamba_mixer_heads_backward")
+    return dict(dx=dx, ddt=ddt, dB=dB, dC=dC, dA_log=dA_log, dD=dD, ddt_bias=dbias, dstate_in=dstate_in)
+
+
+def _gate_inputs(y, z, weight, groups):
+    import torch
+
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, d]")
+    rows, d = y.shape
+    _io_code(y)
+    _check(weight, (d,), torch.float32, "weight")
+    return rows, d, _rows(y, (rows, d), y.dtype, "y"), _rows(z, (rows, d), y.dtype, "z")
+
+
+def gate_norm(y, z, weight, groups: int = 1, eps: float = 1e-5, gate_first: bool = True, out=None, stream=None):
+    """The norm after a mixer block, fused with its gate (see ``mamba_mixer_gate_norm``): with s = SiLU(z),
+    weight n(y s) (gate_first) or weight n(y) s, n the root-mean-square norm of each of `groups` column
+    ranges.  y, z [rows, d] io, weight [d] float32.  Returns out [rows, d]."""
+    import torch
+
+    rows, d, ys, zs = _gate_inputs(y, z, weight, groups)
+    if out is None:
+        out = torch.empty((rows, d), dtype=y.dtype, device=y.device)
+    _check(out, (rows, d), y.dtype, "out")
+    rc = load().mamba_mixer_gate_norm(_ptr(y), _ptr(z), _ptr(weight), _ptr(out), rows, d, int(groups), float(eps),
+                                      1 if gate_first else 0, _io_code(y), ys, zs, _stream(stream))
+    _raise(rc, "mamba_mixer_gate_norm")
+    return out
+
+
+def gate_norm_backward(dout, y, z, weight, groups: int = 1, eps: float = 1e-5, gate_first: bool = True, dy=None,
+                       dz=None, workspace=None, stream=None):
+    """The gradients of ``gate_norm`` from dout [rows, d]: (dy, dz, dweight); dy and dz may be given (with
+    strided rows)."""
+    import torch
+
+    rows, d, ys, zs = _gate_inputs(y, z, weight, groups)
+    _check(dout, (rows, d), y.dtype, "dout")
+    dy, dys = _out(dy, (rows, d), y.dtype, y.device, "dy")
+    dz, dzs = _out(dz, (rows, d), y.dtype, y.device, "dz")
+    dweight = torch.empty(d, dtype=torch.float32, device=y.device)
+    need = load().mamba_mixer_gate_norm_backward_workspace_bytes(rows, d, int(groups)) if workspace is None else 0
+    workspace, wptr, wbytes = _workspace(workspace, need, y.device)
+    rc = load().mamba_mixer_gate_norm_backward(
+        _ptr(dout), _ptr(y), _ptr(z), _ptr(weight), _ptr(dy), _ptr(dz), _ptr(dweight), rows, d, int(groups), float(eps),
+        1 if gate_first else 0, _io_code(y), ys, zs, dys, dzs, wptr, wbytes, _stream(stream))
+    _raise(rc, "mamba_mixer_gate_norm_backward")
+    return dy, dz, dweight
+
+
+def _residual_inputs(h, residual, weight, post_weight, scale_vec):
+    import torch
+
+    if h.dim() != 2:
+        raise ValueError("h must be [rows, d]")
+    rows, d = h.shape
+    _check(h, (rows, d), h.dtype, "h")
+    _io_code(h)
+    for t, n in ((weight, "weight"), (post_weight, "post_weight"), (scale_vec, "scale_vec")):
+        if t is not None:
+            _check(t, (d,), torch.float32, n)
+    res = residual.dtype if residual is not None else h.dtype
+    if residual is not None:
+        if res not in (torch.float32, h.dtype):
+            raise TypeError(f"residual: expected float32 or {h.dtype}, got {res}")
+        _check(residual, (rows, d), res, "residual")
+    return rows, d, res
+
+
+def residual_norm(h, residual, weight, post_weight=None, scale: float = 1.0, scale_vec=None, eps: float = 1e-5,
+                  residual_out=None, out=None, stream=None):
+    """The boundary between two blocks (see ``mamba_mixer_residual_norm``): p = h, or post_weight n(h);
+    r' = residual + scale scale_vec p; out = weight n(r').  h [rows, d] io; residual [rows, d] float32 or h's
+    type (None: zeros, of h's type); weight, post_weight, scale_vec [d] float32.  Returns (out, residual_out);
+    pass residual_out=residual to update the residual in place."""
+    import torch
+
+    rows, d, res = _residual_inputs(h, residual, weight, post_weight, scale_vec)
+    if residual_out is None:
+        residual_out = torch.empty((rows, d), dtype=res, device=h.device)
+    elif residual is None:
+        res = residual_out.dtype
+    if out is None:
+        out = torch.empty((rows, d), dtype=h.dtype, device=h.device)
+    _check(residual_out, (rows, d), res, "residual_out")
+    _check(out, (rows, d), h.dtype, "out")
+    rc = load().mamba_mixer_residual_norm(
+        _ptr(h), _opt(residual), _ptr(weight), _opt(post_weight), _opt(scale_vec), float(scale), _ptr(residual_out),
+        _ptr(out), rows, d, float(eps), _io_code(h), _io_code(residual_out), _stream(stream))
+    _raise(rc, "mamba_mixer_residual_norm")
+    return out, residual_out
+
+
+def residual_norm_backward(dout, dresidual_out, h, residual_out, weight, post_weight=None, scale: float = 1.0,
+                           scale_vec=None, eps: float = 1e-5, dresidual=None, dh=None, workspace=None,
+                           stream=None) -> dict:
+    """The gradients of ``residual_norm`` from dout [rows, d] and dresidual_out [rows, d] (None: zeros);
+    residual_out is the new residual that the forward call returned.  Returns a dict of dresidual, dh, dweight
+    and, with post_weight and scale_vec, dpost_weight and dscale_vec."""
+    import torch
+
+    rows, d, res = _residual_inputs(h, residual_out, weight, post_weight, scale_vec)
+    _check(dout, (rows, d), h.dtype, "dout")
+    if dresidual_out is not None:
+        _check(dresidual_out, (rows, d), res, "dresidual_out")
+    if dresidual is None:
+        dresidual = torch.empty((rows, d), dtype=res, device=h.device)
+    if dh is None:
+        dh = torch.empty((rows, d), dtype=h.dtype, device=h.device)
+    _check(dresidual, (rows, d), res, "dresidual")
+    _check(dh, (rows, d), h.dtype, "dh")
+    new = lambda: torch.empty(d, dtype=torch.float32, device=h.device)  # noqa: E731
+    got = dict(dresidual=dresidual, dh=dh, dweight=new())
+    if post_weight is not None:
+        got["dpost_weight"] = new()
+    if scale_vec is not None:
+        got["dscale_vec"] = new()
+    need = load().mamba_mixer_residual_norm_backward_workspace_bytes(rows, d) if workspace is None else 0
+    workspace, wptr, wbytes = _workspace(workspace, need, h.device)
+    rc = load().mamba_mixer_residual_norm_backward(
+        _ptr(dout), _opt(dresidual_out), _ptr(h), _ptr(residual_out), _ptr(weight), _opt(post_weight), _opt(scale_vec),
+        float(scale), _ptr(dresidual), _ptr(dh), _ptr(got["dweight"]), _opt(got.get("dpost_weight")),
+        _opt(got.get("dscale_vec")), rows, d, float(eps), _io_code(h), _io_code(residual_out), wptr, wbytes,
+        _stream(stream))
+    _raise(rc, "mamba_mixer_residual_norm_backward")
+    return got
