@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
+#include <type_traits>
 
 #include <stdint.h>
 
@@ -11,6 +13,7 @@
 #include "mambamix.h"
 #include "mm_device.h"
 #include "mm_heads.h"
+#include "mm_heads_mma.h"
 #include "mm_host.h"
 #include "mm_norm.h"
 
@@ -25,6 +28,7 @@ int launched() { return hipGetLastError() == hipSuccess ? MM_OK : MM_ERR_HIP; }
 
 struct HeadsPlan {
   int64_t Ls;      // tokens per segment
+  bool mma;        // the matrix-core kernels
   bool whole;      // every sequence is one segment
   int64_t rows;    // segments at most
   int64_t rows64;  // 64-token blocks at most (backward)
@@ -38,14 +42,30 @@ struct HeadsPlan {
 // are not worth their states.
 constexpr int64_t kSeqWorkgroups = 1024;
 
-int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int N, bool backward) {
+// The matrix-core kernels take bfloat16 io and N <= 128.  Their workgroups take two 64-channel blocks of
+// a group; two workgroups fit on a CU.
+constexpr int kMmaMaxN = 128;
+constexpr int64_t kMmaWorkgroups = 1024;
+
+int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, int io, bool backward, int64_t max_stride) {
   p = HeadsPlan{};
+  p.mma = io == MM_IO_BF16 && N <= kMmaMaxN && !backward && max_stride <= kMmaMaxStride &&
+          static_cast<int64_t>(H) * P <= kMmaMaxStride;
   p.nrp = static_cast<int>(cdiv(P, kSeqRows));
   p.nrn = static_cast<int>(cdiv(N, kSeqRows));
   const int64_t per = static_cast<int64_t>(H) * (backward ? std::min(p.nrp, p.nrn) : p.nrp);
   const int64_t want = cdiv(kSeqWorkgroups, std::max<int64_t>(per, 1));
   p.Ls = std::max<int64_t>(256, cdiv(cdiv(T, std::max<int64_t>(want, 1)), kHeadsBlock) * kHeadsBlock);
   if (want <= S || p.Ls >= T) p.Ls = (T / kHeadsBlock + 1) * kHeadsBlock;
+  if (p.mma) {
+    // Few long sequences are cut until about kMmaWorkgroups workgroups walk at once; a segment's state
+    // costs as much traffic as 128 tokens of it, so none is shorter than 1024 tokens.  Measured at 16384
+    // packed tokens, d 4096: segments of 512 tokens 274 us, 1024 261, 2048 310, whole sequences 342.
+    const int64_t pairs = H > 0 ? G * cdiv(H / G * cdiv(P, 64), 2) : 1;
+    const int64_t want_m = cdiv(kMmaWorkgroups, pairs);
+    p.Ls = std::max<int64_t>(1024, cdiv(cdiv(T, want_m), kMmaTok) * kMmaTok);
+    if (want_m <= S || p.Ls >= T) p.Ls = (T / kMmaTok + 1) * kMmaTok;
+  }
   p.whole = p.Ls > T;
   p.rows = segment_rows(S, T, p.Ls);
   p.rows64 = segment_rows(S, T, kHeadsBlock);
@@ -119,6 +139,75 @@ struct HeadsArgs {
   int P, G, N;
   HeadPar hp;
 };
+
+// 16-byte pieces of rows and states: every row starts on one
+bool heads_vec(const HeadsArgs& a, std::initializer_list<const void*> more) {
+  if (a.P % 8 != 0 || a.N % 8 != 0 || a.x_ts % 8 != 0 || a.b_ts % 8 != 0 || a.c_ts % 8 != 0) return false;
+  for (const void* p : {a.x, a.B, a.C})
+    if (!aligned(p, 16)) return false;
+  for (const void* p : more)
+    if (!aligned(p, 16)) return false;
+  return true;
+}
+
+template <typename K>
+int allow_lds(K kernel, size_t bytes) {
+  if (bytes > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes)) != hipSuccess)
+    return MM_ERR_HIP;
+  return MM_OK;
+}
+
+template <int NK, bool LOCAL, bool VEC>
+int launch_mma_t(const MmaArgs& q, const HeadPar& hp, hipStream_t st) {
+  const int rc = allow_lds(&k_heads_mma<NK, LOCAL, VEC>, MmaGeo<NK>::bytes);
+  if (rc != MM_OK) return rc;
+  const dim3 grid(static_cast<unsigned>(q.rows * q.pairs));
+  if (grid.x > 0)
+    hipLaunchKernelGGL((k_heads_mma<NK, LOCAL, VEC>), grid, dim3(kMmaThreads), MmaGeo<NK>::bytes, st, q, hp);
+  return MM_OK;
+}
+template <bool LOCAL>
+int launch_mma(const MmaArgs& q, const HeadPar& hp, bool vec, hipStream_t st) {
+  const auto go = [&](auto nk) {
+    constexpr int NK = decltype(nk)::value;
+    return vec ? launch_mma_t<NK, LOCAL, true>(q, hp, st) : launch_mma_t<NK, LOCAL, false>(q, hp, st);
+  };
+  if (q.N <= 32) return go(std::integral_constant<int, 1>{});
+  if (q.N <= 64) return go(std::integral_constant<int, 2>{});
+  return go(std::integral_constant<int, 4>{});
+}
+
+int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* state_in, float* state_out, void* y,
+                       char* ws, hipStream_t st) {
+  const int div = a.hp.H / a.G;
+  MmaArgs q{};
+  q.x = tok<uint16_t>(a.x, a.x_ts, a.P, 1);
+  q.B = tok<uint16_t>(a.B, a.b_ts, a.N, div);
+  q.C = tok<uint16_t>(a.C, a.c_ts, a.N, div);
+  q.P = a.P;
+  q.N = a.N;
+  q.npb = static_cast<int>(cdiv(a.P, 64));
+  q.vper = div * q.npb;
+  q.ppg = static_cast<int>(cdiv(q.vper, 2));
+  q.pairs = q.ppg * a.G;
+  q.rows = p.rows;
+  q.Ls = p.Ls;
+  q.state_in = state_in;
+  q.state_out = state_out;
+  q.y = static_cast<uint16_t*>(y);
+  const bool vec = heads_vec(a, {state_in, state_out, y});
+  if (!p.whole) {
+    q.carry = reinterpret_cast<float*>(ws + p.off_carry);
+    q.decay = reinterpret_cast<float*>(ws + p.off_decay);
+    const int rc = launch_mma<true>(q, a.hp, vec, st);
+    if (rc != MM_OK) return rc;
+    launch_carry(q.carry, q.decay, state_in, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, false, st);
+  }
+  const int rc = launch_mma<false>(q, a.hp, vec, st);
+  return rc != MM_OK ? rc : launched();
+}
 
 template <typename IO>
 int launch_prefill(const HeadsPlan& p, const HeadsArgs& a, const float* state_in, float* state_out, void* y, char* ws,
@@ -267,6 +356,18 @@ int check_overlap(const Array* in, int ni, const Array* out, int no, const void*
   return MM_OK;
 }
 
+// the largest workspace of a call of these sizes, whatever its strides are
+size_t heads_workspace(int64_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N, int32_t io, bool backward) {
+  if (check_heads_sizes(S, T, H, P, G, N, io) != MM_OK) return 0;
+  size_t most = 0;
+  for (int64_t stride : {int64_t{0}, int64_t{INT32_MAX}}) {
+    HeadsPlan p;
+    if (H == 0 || plan_heads(p, S, T, H, P, G, N, io, backward, stride) != MM_OK) return 0;
+    most = std::max(most, p.total);
+  }
+  return most;
+}
+
 size_t esize(int32_t io) { return io == MM_IO_BF16 ? 2 : 4; }
 
 // ---------------------------------------------------------------- norms: checks
@@ -298,14 +399,6 @@ int by_types(int32_t io, int32_t res, F f) {
   if (res == MM_IO_F32) return f(uint16_t{}, float{});
   return f(uint16_t{}, uint16_t{});
 }
-template <typename K>
-int allow_lds(K kernel, size_t bytes) {
-  if (bytes > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(bytes)) != hipSuccess)
-    return MM_ERR_HIP;
-  return MM_OK;
-}
 
 }  // namespace
 }  // namespace mm
@@ -316,9 +409,7 @@ extern "C" {
 
 size_t mamba_mixer_heads_prefill_workspace_bytes(int32_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N,
                                                  int32_t io_dtype) {
-  HeadsPlan p;
-  if (check_heads_sizes(S, T, H, P, G, N, io_dtype) != MM_OK || plan_heads(p, S, T, H, P, N, false) != MM_OK) return 0;
-  return p.total;
+  return heads_workspace(S, T, H, P, G, N, io_dtype, false);
 }
 
 int mamba_mixer_heads_prefill(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
@@ -341,13 +432,14 @@ int mamba_mixer_heads_prefill(const void* x, const void* dt, const void* B, cons
   if ((rc = check_arrays(in, 9)) != MM_OK || (rc = check_arrays(out, 2)) != MM_OK) return rc;
   if ((rc = check_overlap(in, 9, out, 2, state_in)) != MM_OK) return rc;
   HeadsPlan p;
-  if ((rc = plan_heads(p, S, T, H, P, N, false)) != MM_OK) return rc;
+  if ((rc = plan_heads(p, S, T, H, P, G, N, io_dtype, false, std::max({x_stride, b_stride, c_stride}))) != MM_OK) return rc;
   if (p.total > 0 && (workspace == nullptr || workspace_bytes < p.total)) return MM_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
   const HeadsArgs a{x, B, C, x_stride, b_stride, c_stride, P, G, N,
                     {dt, dt_stride, A_log, dt_bias, D, cu_seqlens, S, H, T}};
   char* ws = static_cast<char*>(workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (p.mma) return launch_prefill_mma(p, a, state_in, state_out, y, ws, st);
   if (io_dtype == MM_IO_BF16) return launch_prefill<uint16_t>(p, a, state_in, state_out, y, ws, st);
   return launch_prefill<float>(p, a, state_in, state_out, y, ws, st);
 }
@@ -389,9 +481,7 @@ int mamba_mixer_heads_decode(const void* x, const void* dt, const void* B, const
 
 size_t mamba_mixer_heads_backward_workspace_bytes(int32_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N,
                                                   int32_t io_dtype) {
-  HeadsPlan p;
-  if (check_heads_sizes(S, T, H, P, G, N, io_dtype) != MM_OK || plan_heads(p, S, T, H, P, N, true) != MM_OK) return 0;
-  return p.total;
+  return heads_workspace(S, T, H, P, G, N, io_dtype, true);
 }
 
 int mamba_mixer_heads_backward(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
@@ -424,7 +514,7 @@ int mamba_mixer_heads_backward(const void* x, const void* dt, const void* B, con
   if ((rc = check_arrays(in, 11)) != MM_OK || (rc = check_arrays(out, 8)) != MM_OK) return rc;
   if ((rc = check_overlap(in, 11, out, 8)) != MM_OK) return rc;
   HeadsPlan p;
-  if ((rc = plan_heads(p, S, T, H, P, N, true)) != MM_OK) return rc;
+  if ((rc = plan_heads(p, S, T, H, P, G, N, io_dtype, true, std::max({x_stride, b_stride, c_stride, dx_stride}))) != MM_OK) return rc;
   if (p.total > 0 && (workspace == nullptr || workspace_bytes < p.total)) return MM_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
   const HeadsArgs a{x, B, C, x_stride, b_stride, c_stride, P, G, N,

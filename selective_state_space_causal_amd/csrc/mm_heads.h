@@ -33,13 +33,22 @@ struct Segment {
   int64_t seq0, seq1;  // the sequence's tokens
   __device__ bool first() const { return t0 <= seq0; }
   __device__ bool last() const { return t1 >= seq1; }
+  // whether the sequence has several segments, and whether this row is one (or an empty sequence's only one)
+  __device__ bool many(int64_t L) const {
+    return seq1 > seq0 && static_cast<uint32_t>(seq1 - 1) / static_cast<uint32_t>(L) >
+                              static_cast<uint32_t>(seq0) / static_cast<uint32_t>(L);
+  }
+  __device__ bool none(int64_t rho, int64_t L) const {
+    return t0 >= t1 && !(seq0 == seq1 && rho == s + static_cast<uint32_t>(seq0) / static_cast<uint32_t>(L));
+  }
 };
 // the largest s with s + cu[s] / L <= rho
 __device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ cu, int S, int64_t rho, int64_t L) {
   int lo = 0, hi = S - 1;
+  const uint32_t L32 = static_cast<uint32_t>(L);
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (mid + cu[mid] / L <= rho) lo = mid; else hi = mid - 1;
+    if (mid + static_cast<int64_t>(static_cast<uint32_t>(cu[mid]) / L32) <= rho) lo = mid; else hi = mid - 1;
   }
   Segment g;
   g.s = lo;
@@ -132,8 +141,8 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar
   const int64_t rho = blockIdx.x / nrb / hp.H;
   const Segment g = segment_of(hp.cu, hp.S, rho, q.Ls);
   const int r = rb * kSeqRows + row;
-  const bool many = g.seq1 > g.seq0 && (g.seq1 - 1) / q.Ls > g.seq0 / q.Ls;  // several segments
-  if (g.t0 >= g.t1 && !(g.seq0 == g.seq1 && rho == g.s + g.seq0 / q.Ls)) return;
+  const bool many = g.many(q.Ls);
+  if (g.none(rho, q.Ls)) return;
   if (LOCAL && (!many || (REV ? g.first() : g.last()))) return;
   const int64_t soff = h * q.sh + static_cast<int64_t>(r) * q.sr;
   const int64_t sset = static_cast<int64_t>(hp.H) * q.sh;
