@@ -490,6 +490,7 @@ int mamba_mixer_heads_backward(const void* x, const void* dt, const void* B, con
 size_t mamba_mixer_heads_backward_workspace_bytes(int32_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N,
                                                   int32_t io_dtype);
 
+#define MM_NORM_MAX_D 32768
 /*
  * The norm after a mixer block, fused with its gate.  With s = z sigmoid(z) and
  * n(u) = u / sqrt(mean(u^2) + eps) over each of `groups` equal ranges of the d columns:
@@ -522,7 +523,6 @@ size_t mamba_mixer_gate_norm_backward_workspace_bytes(int64_t rows, int32_t d, i
  *   weight, post_weight, scale_vec [d] f32.  All contiguous.  residual_out may be residual itself;
  *   otherwise the outputs overlap no input and not one another.  d <= MM_NORM_MAX_D.
  */
-#define MM_NORM_MAX_D 32768
 int mamba_mixer_residual_norm(const void* h, const void* residual, const float* weight, const float* post_weight,
                               const float* scale_vec, float scale, void* residual_out, void* out, int64_t rows,
                               int32_t d, float eps, int32_t io_dtype, int32_t res_dtype, void* stream);

@@ -21,6 +21,7 @@ namespace mm {
 namespace {
 
 constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;  // of one launch
+constexpr int64_t kCUs = 256;
 
 int launched() { return hipGetLastError() == hipSuccess ? MM_OK : MM_ERR_HIP; }
 
@@ -381,13 +382,14 @@ int check_norm_sizes(int64_t rows, int32_t d, float eps, int32_t io) {
 int check_gate_sizes(int64_t rows, int32_t d, int32_t groups, float eps, int32_t io) {
   const int rc = check_norm_sizes(rows, d, eps, io);
   if (rc != MM_OK) return rc;
-  if (groups < 1 || d % groups != 0 || rows * groups * kNormThreads > kMaxThreads) return MM_ERR_DIM;
+  if (groups < 1 || d % groups != 0) return MM_ERR_DIM;
+  if (d / groups > kNormUnit && rows * groups * kWideThreads > kMaxThreads) return MM_ERR_DIM;
   return MM_OK;
 }
 int check_residual_sizes(int64_t rows, int32_t d, float eps, int32_t io, int32_t res) {
   const int rc = check_norm_sizes(rows, d, eps, io);
   if (rc != MM_OK) return rc;
-  if (rows * kNormThreads > kMaxThreads) return MM_ERR_DIM;
+  if (d > kNormUnit && rows * kWideThreads > kMaxThreads) return MM_ERR_DIM;
   if (d > MM_NORM_MAX_D || (res != MM_IO_F32 && res != io)) return MM_ERR_UNSUPPORTED;
   return MM_OK;
 }
@@ -398,6 +400,37 @@ int by_types(int32_t io, int32_t res, F f) {
   if (io == MM_IO_F32) return f(float{}, float{});
   if (res == MM_IO_F32) return f(uint16_t{}, float{});
   return f(uint16_t{}, uint16_t{});
+}
+
+// How a row (or its group) of n columns is spread: pieces of 8 columns, at most 512 threads and as few pieces per
+// thread as that allows.
+struct NormShape {
+  int threads, nv;
+};
+NormShape norm_shape(int n) {
+  const int pieces = static_cast<int>(cdiv(n, 8));
+  int nv = 1;
+  while (cdiv(pieces, nv) > kNormMaxThreads) nv *= 2;
+  return {static_cast<int>(cdiv(cdiv(pieces, nv), kWave) * kWave), nv};
+}
+// Workgroups of a backward call, for every group: rows beyond this many wait their turn.  Two workgroups (or 16
+// waves) per CU keep enough rows in flight; more would only add partial sums of the weights.
+int64_t norm_slots(int64_t rows, int n, int groups, bool backward) {
+  const int t = norm_shape(n).threads;
+  const int64_t wgs = kCUs * (backward ? std::max(2, 1024 / t) : std::max(4, 2048 / t));
+  return std::max<int64_t>(1, std::min<int64_t>(rows, cdiv(wgs, groups)));
+}
+template <typename F>
+void by_pieces(int nv, F f) {
+  if (nv == 1) f(std::integral_constant<int, 1>{});
+  else f(std::integral_constant<int, 2>{});
+}
+// workspace of a backward call: partial sums of K weights, for wide rows behind the rows' factors
+size_t norm_workspace(int64_t rows, int d, int groups, int K) {
+  if (d == 0) return 0;
+  if (d / groups > kNormUnit)
+    return align256(static_cast<size_t>(rows) * groups * K * 4) + align256(static_cast<size_t>(kWideParts) * K * d * 4);
+  return align256(static_cast<size_t>(norm_slots(rows, d / groups, groups, true)) * K * d * 4);
 }
 
 }  // namespace
@@ -547,8 +580,16 @@ int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, voi
     using IO = decltype(io);
     const GateArgs<IO> a{static_cast<const IO*>(y), static_cast<const IO*>(z), nullptr, y_stride, z_stride, weight,
                          nrows, d, groups, eps, gate_first != 0 ? 1 : 0};
-    hipLaunchKernelGGL((k_gate_norm<IO>), dim3(static_cast<unsigned>(nrows * groups)), dim3(kNormThreads), 0, st, a,
-                       static_cast<IO*>(out));
+    if (d / groups > kNormUnit) {
+      hipLaunchKernelGGL((k_wide_gate_norm<IO>), dim3(static_cast<unsigned>(nrows * groups)), dim3(kWideThreads), 0, st, a,
+                         static_cast<IO*>(out));
+      return;
+    }
+    const NormShape sh = norm_shape(d / groups);
+    const dim3 grid(static_cast<unsigned>(norm_slots(nrows, d / groups, groups, false) * groups));
+    by_pieces(sh.nv, [&](auto nv) {
+      hipLaunchKernelGGL((k_gate_norm<IO, decltype(nv)::value>), grid, dim3(sh.threads), 0, st, a, static_cast<IO*>(out));
+    });
   };
   if (io_dtype == MM_IO_BF16) go(uint16_t{}); else go(float{});
   return launched();
@@ -556,7 +597,7 @@ int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, voi
 
 size_t mamba_mixer_gate_norm_backward_workspace_bytes(int64_t nrows, int32_t d, int32_t groups) {
   if (check_gate_sizes(nrows, d, groups, 0.0f, MM_IO_F32) != MM_OK) return 0;
-  return align256(static_cast<size_t>(nrows) * groups * 4) + align256(static_cast<size_t>(kNormParts) * d * 4);
+  return norm_workspace(nrows, d, groups, 1);
 }
 
 int mamba_mixer_gate_norm_backward(const void* dout, const void* y, const void* z, const float* weight, void* dy,
@@ -580,22 +621,33 @@ int mamba_mixer_gate_norm_backward(const void* dout, const void* y, const void* 
   if (workspace == nullptr || workspace_bytes < need) return MM_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  float* stats = static_cast<float*>(workspace);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(static_cast<size_t>(nrows) * groups * 4));
-  const int64_t parts = std::min<int64_t>(kNormParts, nrows);
-  const unsigned cols = static_cast<unsigned>(cdiv(d, kNormThreads));
+  float* part = static_cast<float*>(workspace);
+  const int n = d / groups;
+  const bool wide = n > kNormUnit;
+  const int64_t slots = wide ? std::min<int64_t>(kWideParts, nrows) : norm_slots(nrows, n, groups, true);
+  float* const stats = part;
+  if (wide) part += align256(static_cast<size_t>(nrows) * groups * 4) / 4;
   const auto go = [&](auto io) {
     using IO = decltype(io);
     const GateArgs<IO> a{static_cast<const IO*>(y), static_cast<const IO*>(z), static_cast<const IO*>(dout), y_stride,
                          z_stride, weight, nrows, d, groups, eps, gate_first != 0 ? 1 : 0};
-    hipLaunchKernelGGL((k_gate_norm_bwd<IO>), dim3(static_cast<unsigned>(nrows * groups)), dim3(kNormThreads), 0, st, a,
-                       static_cast<IO*>(dy), static_cast<IO*>(dz), dy_stride, dz_stride, stats);
-    hipLaunchKernelGGL((k_gate_norm_dw<IO>), dim3(cols, static_cast<unsigned>(parts)), dim3(kNormThreads), 0, st, a, stats,
-                       part, cdiv(nrows, parts));
+    if (wide) {
+      const dim3 block(kWideThreads), cols(static_cast<unsigned>(cdiv(d, kWideThreads)), static_cast<unsigned>(slots));
+      hipLaunchKernelGGL((k_wide_gate_norm_bwd<IO>), dim3(static_cast<unsigned>(nrows * groups)), block, 0, st, a,
+                         static_cast<IO*>(dy), static_cast<IO*>(dz), dy_stride, dz_stride, stats);
+      hipLaunchKernelGGL((k_wide_gate_norm_dw<IO>), cols, block, 0, st, a, stats, part, cdiv(nrows, slots));
+      return;
+    }
+    const NormShape sh = norm_shape(n);
+    by_pieces(sh.nv, [&](auto nv) {
+      hipLaunchKernelGGL((k_gate_norm_bwd<IO, decltype(nv)::value>), dim3(static_cast<unsigned>(slots * groups)),
+                         dim3(sh.threads), 0, st, a, static_cast<IO*>(dy), static_cast<IO*>(dz), dy_stride, dz_stride, part);
+    });
   };
   if (nrows > 0) { if (io_dtype == MM_IO_BF16) go(uint16_t{}); else go(float{}); }
-  hipLaunchKernelGGL(k_norm_parts, dim3(cols), dim3(kNormThreads), 0, st, part, dweight, static_cast<int>(parts),
-                     static_cast<int64_t>(d), d);
+  const NormParts np{{part, nullptr, nullptr}, {dweight, nullptr, nullptr}};
+  hipLaunchKernelGGL(k_norm_parts, dim3(static_cast<unsigned>(cdiv(d, 16))), dim3(256), 0, st, np,
+                     static_cast<int>(nrows > 0 ? slots : 0), static_cast<int64_t>(d), d);
   return launched();
 }
 
@@ -617,17 +669,26 @@ int mamba_mixer_residual_norm(const void* h, const void* residual, const float* 
     using RES = decltype(rt);
     const ResArgs<IO, RES> a{static_cast<const IO*>(h), static_cast<const RES*>(residual), weight, post_weight,
                              scale_vec, scale, eps, nrows, d};
-    const int r = allow_lds(&k_residual_norm<IO, RES>, nd);
-    if (r != MM_OK) return r;
-    hipLaunchKernelGGL((k_residual_norm<IO, RES>), dim3(static_cast<unsigned>(nrows)), dim3(kNormThreads), nd, st, a,
-                       static_cast<RES*>(residual_out), static_cast<IO*>(out));
+    if (d > kNormUnit) {
+      const int r = allow_lds(&k_wide_residual_norm<IO, RES>, nd);
+      if (r != MM_OK) return r;
+      hipLaunchKernelGGL((k_wide_residual_norm<IO, RES>), dim3(static_cast<unsigned>(nrows)), dim3(kWideThreads), nd, st, a,
+                         static_cast<RES*>(residual_out), static_cast<IO*>(out));
+      return launched();
+    }
+    const NormShape sh = norm_shape(d);
+    by_pieces(sh.nv, [&](auto nv) {
+      hipLaunchKernelGGL((k_residual_norm<IO, RES, decltype(nv)::value>),
+                         dim3(static_cast<unsigned>(norm_slots(nrows, d, 1, false))), dim3(sh.threads), 0, st, a,
+                         static_cast<RES*>(residual_out), static_cast<IO*>(out));
+    });
     return launched();
   });
 }
 
 size_t mamba_mixer_residual_norm_backward_workspace_bytes(int64_t nrows, int32_t d) {
   if (check_residual_sizes(nrows, d, 0.0f, MM_IO_F32, MM_IO_F32) != MM_OK) return 0;
-  return align256(static_cast<size_t>(nrows) * 3 * 4) + align256(static_cast<size_t>(kNormParts) * 3 * d * 4);
+  return norm_workspace(nrows, d, 1, 3);
 }
 
 int mamba_mixer_residual_norm_backward(const void* dout, const void* dresidual_out, const void* h,
@@ -652,37 +713,53 @@ int mamba_mixer_residual_norm_backward(const void* dout, const void* dresidual_o
   if (workspace == nullptr || workspace_bytes < need) return MM_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  float* stats = static_cast<float*>(workspace);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(static_cast<size_t>(nrows) * 3 * 4));
-  const int64_t parts = std::min<int64_t>(kNormParts, nrows);
-  const unsigned cols = static_cast<unsigned>(cdiv(d, kNormThreads));
+  float* part = static_cast<float*>(workspace);
+  const bool wide = d > kNormUnit;
+  const int64_t slots = wide ? std::min<int64_t>(kWideParts, nrows) : norm_slots(nrows, d, 1, true);
+  float* const stats = part;
+  if (wide) part += align256(static_cast<size_t>(nrows) * 3 * 4) / 4;
   if (nrows > 0) {
     rc = by_types(io_dtype, res_dtype, [&](auto io, auto rt) {
       using IO = decltype(io);
       using RES = decltype(rt);
       const ResArgs<IO, RES> a{static_cast<const IO*>(h), static_cast<const RES*>(residual_out), weight, post_weight,
                                scale_vec, scale, eps, nrows, d};
-      const IO* go = static_cast<const IO*>(dout);
-      const RES* gr = static_cast<const RES*>(dresidual_out);
-      const int r = allow_lds(&k_residual_norm_bwd<IO, RES>, nd);
-      if (r != MM_OK) return r;
-      // the rows' factors and the weights' sums before the gradients: dresidual may be written over dresidual_out
-      const dim3 grid(static_cast<unsigned>(nrows)), block(kNormThreads);
-      hipLaunchKernelGGL((k_residual_norm_bwd<IO, RES>), grid, block, nd, st, a, go, gr, static_cast<RES*>(nullptr),
-                         static_cast<IO*>(nullptr), stats);
-      hipLaunchKernelGGL((k_residual_norm_dw<IO, RES>), dim3(cols, static_cast<unsigned>(parts)), block, 0, st, a, go, gr,
-                         stats, part, cdiv(nrows, parts));
-      hipLaunchKernelGGL((k_residual_norm_bwd<IO, RES>), grid, block, nd, st, a, go, gr, static_cast<RES*>(dresidual),
-                         static_cast<IO*>(dh), stats);
+      if (wide) {
+        const int r = allow_lds(&k_wide_residual_norm_bwd<IO, RES>, nd);
+        if (r != MM_OK) return r;
+        const IO* go = static_cast<const IO*>(dout);
+        const RES* gr = static_cast<const RES*>(dresidual_out);
+        const dim3 grid(static_cast<unsigned>(nrows)), block(kWideThreads);
+        const dim3 cols(static_cast<unsigned>(cdiv(d, kWideThreads)), static_cast<unsigned>(slots));
+        // the rows' factors and the weights' sums before the gradients: dresidual may be written over dresidual_out
+        hipLaunchKernelGGL((k_wide_residual_norm_bwd<IO, RES>), grid, block, nd, st, a, go, gr, static_cast<RES*>(nullptr),
+                           static_cast<IO*>(nullptr), stats);
+        hipLaunchKernelGGL((k_wide_residual_norm_dw<IO, RES>), cols, block, 0, st, a, go, gr, stats, part,
+                           cdiv(nrows, slots));
+        hipLaunchKernelGGL((k_wide_residual_norm_bwd<IO, RES>), grid, block, nd, st, a, go, gr,
+                           static_cast<RES*>(dresidual), static_cast<IO*>(dh), stats);
+        return launched();
+      }
+      const NormShape sh = norm_shape(d);
+      by_pieces(sh.nv, [&](auto nv) {
+        hipLaunchKernelGGL((k_residual_norm_bwd<IO, RES, decltype(nv)::value>), dim3(static_cast<unsigned>(slots)),
+                           dim3(sh.threads), 0, st, a, static_cast<const IO*>(dout), static_cast<const RES*>(dresidual_out),
+                           static_cast<RES*>(dresidual), static_cast<IO*>(dh), part);
+      });
       return launched();
     });
     if (rc != MM_OK) return rc;
   }
-  float* outs[] = {dweight, dpost_weight, dscale_vec};
+  NormParts np{};
+  int k = 0;
+  float* const outs[] = {dweight, post_weight != nullptr ? dpost_weight : nullptr, scale_vec != nullptr ? dscale_vec : nullptr};
   for (int i = 0; i < 3; ++i)
-    if (i == 0 || (i == 1 ? post_weight : scale_vec) != nullptr)
-      hipLaunchKernelGGL(k_norm_parts, dim3(cols), dim3(kNormThreads), 0, st, part + static_cast<int64_t>(i) * d, outs[i],
-                         static_cast<int>(parts), static_cast<int64_t>(3) * d, d);
+    if (outs[i] != nullptr) {
+      np.part[k] = part + static_cast<int64_t>(i) * d;
+      np.out[k++] = outs[i];
+    }
+  hipLaunchKernelGGL(k_norm_parts, dim3(static_cast<unsigned>(cdiv(d, 16)), static_cast<unsigned>(k)), dim3(256), 0, st, np,
+                     static_cast<int>(nrows > 0 ? slots : 0), static_cast<int64_t>(3) * d, d);
   return launched();
 }
 

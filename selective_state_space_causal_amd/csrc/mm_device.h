@@ -214,6 +214,14 @@ __device__ __forceinline__ void scan_range(const Chan<NMAX>& ch, int64_t g, int6
   }
 }
 
+// sum over the 16 lanes of a row, in every lane of it
+__device__ __forceinline__ float row_sum16(float v) {
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x128, 0xF, 0xF, true);  // row_ror:8
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x124, 0xF, 0xF, true);  // row_ror:4
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x122, 0xF, 0xF, true);  // row_ror:2
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x121, 0xF, 0xF, true);  // row_ror:1
+  return v;
+}
 
 template <typename T>
 __device__ __forceinline__ T nt_load(const T* p) { return __builtin_nontemporal_load(p); }

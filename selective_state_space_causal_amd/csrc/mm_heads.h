@@ -90,15 +90,6 @@ __device__ __forceinline__ float head_A2(const HeadPar& hp, int h) {  // A log2(
   return -exp2_hw(hp.A_log[h] * kLog2e) * kLog2e;
 }
 
-// sum over the 16 lanes of a row, in every lane of it
-__device__ __forceinline__ float row_sum16(float v) {
-  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x128, 0xF, 0xF, true);  // row_ror:8
-  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x124, 0xF, 0xF, true);  // row_ror:4
-  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x122, 0xF, 0xF, true);  // row_ror:2
-  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x121, 0xF, 0xF, true);  // row_ror:1
-  return v;
-}
-
 // One run of the recurrence on a state of R rows and K columns (element (r, k) of a stored state at
 // r sr + k sk):
 //   forward   h = a_t h + w_t u_t[r] v_t[k],   out_t[r] = sum_k h s_t[k]          w = delta

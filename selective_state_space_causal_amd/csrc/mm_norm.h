@@ -1,28 +1,126 @@
-// The norms around a mixer block, one pass each over their rows:
+// The norms around a mixer block, one pass over their rows:
 //   gate_norm       s = z sigmoid(z);  gate first: out = w n(y s),  gate last: out = w n(y) s,
 //                   n(u) = u rsqrt(mean(u^2) + eps) over each of `groups` equal column ranges
 //   residual_norm   p = h or w_post n(h);  r' = r + scale scale_vec p;  out = w n(r')
 // and their gradients.  All arithmetic is float32; the outputs are rounded once.
+//
+// Bound by memory.  A workgroup takes a (row, group) at a time, eight neighbouring columns per thread
+// and NV such pieces, in registers from the load to the store: every array is read and written once.
+// The next row is loaded before this one's sums are taken.  In the backward a workgroup keeps to one
+// column range over all its rows, so the weights' gradients gather in registers too and leave as one
+// partial sum per workgroup, added in a fixed order by k_norm_parts.
+// Rows may start anywhere: 16-byte accesses need no alignment here, and a row's last piece is taken
+// element by element.
 #pragma once
 
 #include "mm_device.h"
 
 namespace mm {
 
-constexpr int kNormThreads = 256;
-constexpr int kNormParts = 256;  // row ranges of the weight gradients' sums
+constexpr int kNormMaxThreads = 512;
+constexpr int kNormMaxPieces = 2;  // per thread
+constexpr int kNormUnit = kNormMaxThreads * kNormMaxPieces * 8;  // columns that fit: 8192
 
-__device__ __forceinline__ float wave_sum(float v) {
-  for (int k = 32; k > 0; k /= 2) v += __shfl_xor(v, k);
-  return v;
+typedef uint32_t nu4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float nf4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// eight elements as loaded
+template <typename IO>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  nu4 v;
+};
+template <>
+struct Raw8<float> {
+  nf4 a, b;
+};
+// n: how many exist (the others read as zeros)
+__device__ __forceinline__ Raw8<uint16_t> load_raw(const uint16_t* p, int n) {
+  Raw8<uint16_t> r;
+  r.v = nu4{0, 0, 0, 0};
+  if (n >= 8) {
+    r.v = *reinterpret_cast<const nu4*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) r.v[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
+  }
+  return r;
 }
-// sum over the workgroup, in every thread; `s` is 4 floats of LDS
-__device__ __forceinline__ float group_sum(float v, float* s) {
-  v = wave_sum(v);
+__device__ __forceinline__ Raw8<float> load_raw(const float* p, int n) {
+  Raw8<float> r;
+  r.a = r.b = nf4{0, 0, 0, 0};
+  if (n >= 8) {
+    r.a = *reinterpret_cast<const nf4*>(p);
+    r.b = *reinterpret_cast<const nf4*>(p + 4);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) r.a[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (4 + i < n) r.b[i] = p[4 + i];
+  }
+  return r;
+}
+__device__ __forceinline__ float get(const Raw8<uint16_t>& r, int i) {
+  return __uint_as_float(i % 2 ? r.v[i / 2] & 0xFFFF0000u : r.v[i / 2] << 16);
+}
+__device__ __forceinline__ float get(const Raw8<float>& r, int i) { return i < 4 ? r.a[i & 3] : r.b[i & 3]; }
+__device__ __forceinline__ void store_8(uint16_t* p, int n, const float (&v)[8]) {
+  typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+  typedef float f8 __attribute__((ext_vector_type(8)));
+  f8 f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = v[i];
+  const b8 b = __builtin_convertvector(f, b8);  // round to nearest even
+  if (n >= 8) {
+    *reinterpret_cast<nu4*>(p) = __builtin_bit_cast(nu4, b);
+  } else {
+    const nu4 u = __builtin_bit_cast(nu4, b);
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i % 2)));
+  }
+}
+__device__ __forceinline__ void store_8(float* p, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    *reinterpret_cast<nf4*>(p) = nf4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<nf4*>(p + 4) = nf4{v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+// Sums of K values over the workgroup, in every thread; LDS for two calls in turn, so that one barrier
+// serves each.
+struct NormRed {
+  float s[2][3][kNormMaxThreads / kWave];
+};
+template <int K>
+__device__ __forceinline__ void group_sums(float (&v)[K], NormRed& red, int& turn) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    v[k] = row_sum16(v[k]);
+    v[k] += __shfl_xor(v[k], 16);
+    v[k] += __shfl_xor(v[k], 32);
+  }
+  const int waves = blockDim.x / kWave;
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) red.s[turn][k][threadIdx.x >> 6] = v[k];
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float t = 0.0f;
+    for (int w = 0; w < waves; ++w) t += red.s[turn][k][w];
+    v[k] = t;
+  }
+  turn ^= 1;
 }
 __device__ __forceinline__ float sigmoid(float z) { return rcp_hw(1.0f + exp2_hw(-z * kLog2e)); }
 
@@ -37,46 +135,403 @@ struct GateArgs {
   int gate_first;
 };
 
+// Workgroups b, b + groups, ...: the rows b / groups, b / groups + slots, ... of group b % groups.
+template <typename IO, int NV>
+__global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm(GateArgs<IO> a, IO* __restrict__ out) {
+  __shared__ NormRed red;
+  int turn = 0;
+  const int n = a.d / a.groups, g = blockIdx.x % a.groups, T = blockDim.x;
+  const int64_t slots = gridDim.x / a.groups;
+  const bool first = a.gate_first != 0;
+  Raw8<float> w[NV];
+  Raw8<IO> y[NV], z[NV];
+  const auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * T + threadIdx.x) * 8;
+      y[i] = load_raw(a.y + row * a.y_ts + g * n + c, n - c);
+      z[i] = load_raw(a.z + row * a.z_ts + g * n + c, n - c);
+    }
+  };
+  int64_t row = blockIdx.x / a.groups;
+  load(row);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * T + threadIdx.x) * 8;
+    w[i] = load_raw(a.w + g * n + c, n - c);
+  }
+  for (; row < a.rows; row += slots) {
+    float v[NV][8], sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float yv = get(y[i], e), zv = get(z[i], e);
+        v[i][e] = yv * (zv * sigmoid(zv));
+        const float u = first ? v[i][e] : yv;
+        sum[0] = __builtin_fmaf(u, u, sum[0]);
+      }
+    if (row + slots < a.rows) load(row + slots);
+    group_sums(sum, red, turn);
+    const float k = rsqrtf(sum[0] / n + a.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * T + threadIdx.x) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] *= k * get(w[i], e);
+      if (c < n) store_8(out + row * a.d + g * n + c, n - c, v[i]);
+    }
+  }
+}
+
+// With u = y s (gate first) or y, n = u k, k = rsqrt(mean(u^2) + eps) and dn = dout w (times s, gate last):
+//   du = k (dn - n mean(dn n));  first: dy = du s, dz = du y s';  last: dy = du, dz = dout w n s'
+// part: [slots, d] partial sums of dw.
+template <typename IO, int NV>
+__global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm_bwd(GateArgs<IO> a, IO* __restrict__ dy, IO* __restrict__ dz,
+                                                                   int64_t dy_ts, int64_t dz_ts,
+                                                                   float* __restrict__ part) {
+  __shared__ NormRed red;
+  int turn = 0;
+  const int n = a.d / a.groups, g = blockIdx.x % a.groups, T = blockDim.x;
+  const int64_t slots = gridDim.x / a.groups;
+  const bool first = a.gate_first != 0;
+  Raw8<float> w[NV];
+  Raw8<IO> y[NV], z[NV], go[NV];
+  float dw[NV][8];
+  const auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * T + threadIdx.x) * 8;
+      y[i] = load_raw(a.y + row * a.y_ts + g * n + c, n - c);
+      z[i] = load_raw(a.z + row * a.z_ts + g * n + c, n - c);
+      go[i] = load_raw(a.dout + row * a.d + g * n + c, n - c);
+    }
+  };
+  int64_t row = blockIdx.x / a.groups;
+  load(row);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * T + threadIdx.x) * 8;
+    w[i] = load_raw(a.w + g * n + c, n - c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  }
+  for (; row < a.rows; row += slots) {
+    Raw8<IO> yr[NV], zr[NV], gr[NV];
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      yr[i] = y[i];
+      zr[i] = z[i];
+      gr[i] = go[i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float zv = get(zr[i], e), s = zv * sigmoid(zv), yv = get(yr[i], e);
+        const float u = first ? yv * s : yv, gw = get(gr[i], e) * get(w[i], e);
+        sum[0] = __builtin_fmaf(u, u, sum[0]);
+        sum[1] = __builtin_fmaf(gw * s, yv, sum[1]);  // dn u, either way
+      }
+    }
+    if (row + slots < a.rows) load(row + slots);
+    group_sums(sum, red, turn);
+    const float k = rsqrtf(sum[0] / n + a.eps);
+    const float km = k * k * (sum[1] / n);  // k mean(dn n): n mean(dn n) = u km
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * T + threadIdx.x) * 8;
+      float oy[8], oz[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float zv = get(zr[i], e), sg = sigmoid(zv), s = zv * sg, ds = sg * (1.0f + zv * (1.0f - sg));
+        const float yv = get(yr[i], e), gv = get(gr[i], e), gw = gv * get(w[i], e);
+        if (first) {
+          const float du = k * (gw - yv * s * km);
+          oy[e] = du * s;
+          oz[e] = du * yv * ds;
+        } else {
+          oy[e] = k * (gw * s - yv * km);
+          oz[e] = gw * yv * k * ds;
+        }
+        dw[i][e] = __builtin_fmaf(gv * k, yv * s, dw[i][e]);
+      }
+      if (c < n) {
+        store_8(dy + row * dy_ts + g * n + c, n - c, oy);
+        store_8(dz + row * dz_ts + g * n + c, n - c, oz);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * T + threadIdx.x) * 8;
+    if (c < n) store_8(part + static_cast<int64_t>(blockIdx.x / a.groups) * a.d + g * n + c, n - c, dw[i]);
+  }
+}
+
+// out[c] = the sum of part[i][c] over i: 16 columns per workgroup, 16 threads for each, in a fixed order
+struct NormParts {
+  const float* part[3];
+  float* out[3];
+};
+__global__ __launch_bounds__(256) void k_norm_parts(NormParts p, int parts, int64_t stride, int d) {
+  __shared__ float s[16][17];
+  const int c = blockIdx.x * 16 + (threadIdx.x & 15), r = threadIdx.x >> 4;
+  const float* part = p.part[blockIdx.y];
+  float v = 0.0f;
+  if (c < d) {
+    int i = r;
+    for (; i + 112 < parts; i += 128) {
+      float t[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[k] = part[(i + 16 * k) * stride + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += t[k];
+    }
+    for (; i < parts; i += 16) v += part[i * stride + c];
+  }
+  s[r][threadIdx.x & 15] = v;
+  __syncthreads();
+  if (r == 0 && c < d) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t += s[k][threadIdx.x & 15];
+    p.out[blockIdx.y][c] = t;
+  }
+}
+
+template <typename IO, typename RES>
+struct ResArgs {
+  const IO* h;
+  const RES* res;  // the residual before (forward) or after (backward) the addition; forward: may be NULL
+  const float *w, *wp, *vec;
+  float scale, eps;
+  int64_t rows;
+  int d;
+};
+// eight of a per-column parameter; ones where there is none
+__device__ __forceinline__ Raw8<float> load_or_one(const float* p, int c, int n) {
+  if (p != nullptr) return load_raw(p + c, n);
+  Raw8<float> r;
+  r.a = r.b = nf4{1, 1, 1, 1};
+  return r;
+}
+
+template <typename IO, typename RES, int NV>
+__global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm(ResArgs<IO, RES> a, RES* __restrict__ res_out,
+                                                                   IO* __restrict__ out) {
+  __shared__ NormRed red;
+  int turn = 0;
+  const int n = a.d, T = blockDim.x;
+  Raw8<float> w[NV], f[NV];  // f: everything that multiplies h's norm
+  Raw8<IO> h[NV];
+  Raw8<RES> res[NV];
+  const auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * T + threadIdx.x) * 8;
+      h[i] = load_raw(a.h + row * n + c, n - c);
+      res[i] = load_raw(a.res + (a.res != nullptr ? row * n + c : 0), a.res != nullptr ? n - c : 0);
+    }
+  };
+  int64_t row = blockIdx.x;
+  load(row);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * T + threadIdx.x) * 8;
+    w[i] = load_raw(a.w + c, n - c);
+    f[i] = load_or_one(a.wp, c, n - c);
+    const Raw8<float> v = load_or_one(a.vec, c, n - c);
+    f[i].a *= a.scale * v.a;
+    f[i].b *= a.scale * v.b;
+  }
+  for (; row < a.rows; row += gridDim.x) {
+    float kp = 1.0f;
+    if (a.wp != nullptr) {
+      float sum[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[0] = __builtin_fmaf(get(h[i], e), get(h[i], e), sum[0]);
+      group_sums(sum, red, turn);
+      kp = rsqrtf(sum[0] / n + a.eps);
+    }
+    float r[NV][8], sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        r[i][e] = __builtin_fmaf(get(h[i], e) * kp, get(f[i], e), get(res[i], e));
+        sum[0] = __builtin_fmaf(r[i][e], r[i][e], sum[0]);
+      }
+    if (row + gridDim.x < a.rows) load(row + gridDim.x);
+    group_sums(sum, red, turn);
+    const float k = rsqrtf(sum[0] / n + a.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * T + threadIdx.x) * 8;
+      if (c < n) store_8(res_out + row * n + c, n - c, r[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[i][e] *= k * get(w[i], e);
+      if (c < n) store_8(out + row * n + c, n - c, r[i]);
+    }
+  }
+}
+
+// With r the new residual, k = rsqrt(mean(r^2) + eps), n = r k and dn = dout w:
+//   dr = dr' + k (dn - n mean(dn n)),  dp = scale vec dr,  and through the norm of h, kp = rsqrt(mean(h^2) + eps):
+//   dh = kp (dp wp - h kp^2 mean(dp wp h))          (without wp: dh = dp)
+// part: per slot the partial sums of dw = dout n, dwp = dp h kp and dvec = scale dr p.
+template <typename IO, typename RES, int NV>
+__global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm_bwd(ResArgs<IO, RES> a, const IO* __restrict__ dout,
+                                                                       const RES* dres_out, RES* dres,
+                                                                       IO* __restrict__ dh, float* __restrict__ part) {
+  __shared__ NormRed red;
+  int turn = 0;
+  const int n = a.d, T = blockDim.x;
+  const bool post = a.wp != nullptr;
+  Raw8<float> w[NV], wp[NV], vec[NV];
+  Raw8<IO> h[NV], go[NV];
+  Raw8<RES> res[NV], up[NV];
+  float acc[3][NV][8];
+  const auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * T + threadIdx.x) * 8;
+      h[i] = load_raw(a.h + row * n + c, n - c);
+      go[i] = load_raw(dout + row * n + c, n - c);
+      res[i] = load_raw(a.res + row * n + c, n - c);
+      up[i] = load_raw(dres_out + (dres_out != nullptr ? row * n + c : 0), dres_out != nullptr ? n - c : 0);
+    }
+  };
+  int64_t row = blockIdx.x;
+  load(row);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * T + threadIdx.x) * 8;
+    w[i] = load_raw(a.w + c, n - c);
+    wp[i] = load_or_one(a.wp, c, n - c);
+    vec[i] = load_or_one(a.vec, c, n - c);
+    vec[i].a *= a.scale;
+    vec[i].b *= a.scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[0][i][e] = acc[1][i][e] = acc[2][i][e] = 0.0f;
+  }
+  for (; row < a.rows; row += gridDim.x) {
+    float sum[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float rv = get(res[i], e), hv = get(h[i], e);
+        sum[0] = __builtin_fmaf(rv, rv, sum[0]);
+        sum[1] = __builtin_fmaf(get(go[i], e) * get(w[i], e), rv, sum[1]);
+        sum[2] = __builtin_fmaf(hv, hv, sum[2]);
+      }
+    group_sums(sum, red, turn);
+    const float k = rsqrtf(sum[0] / n + a.eps), km = k * k * (sum[1] / n);
+    const float kp = post ? rsqrtf(sum[2] / n + a.eps) : 1.0f;
+    float dr[NV][8], sh[1] = {0.0f};
+    Raw8<IO> hr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      hr[i] = h[i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float rv = get(res[i], e), gv = get(go[i], e), hv = get(h[i], e);
+        dr[i][e] = get(up[i], e) + k * (gv * get(w[i], e) - rv * km);
+        const float dp = dr[i][e] * get(vec[i], e);
+        sh[0] = __builtin_fmaf(dp * get(wp[i], e), hv, sh[0]);
+        acc[0][i][e] = __builtin_fmaf(gv, rv * k, acc[0][i][e]);
+        acc[1][i][e] = __builtin_fmaf(dp, hv * kp, acc[1][i][e]);
+        // scale dr p; the parameter may be zero, so not dp p / vec
+        acc[2][i][e] = __builtin_fmaf(a.scale * dr[i][e], hv * kp * get(wp[i], e), acc[2][i][e]);
+      }
+    }
+    if (row + gridDim.x < a.rows) load(row + gridDim.x);
+    float m = 0.0f;
+    if (post) {
+      group_sums(sh, red, turn);
+      m = kp * kp * (sh[0] / n);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * T + threadIdx.x) * 8;
+      if (c < n) store_8(dres + row * n + c, n - c, dr[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float dp = dr[i][e] * get(vec[i], e);
+        dr[i][e] = post ? kp * (dp * get(wp[i], e) - get(hr[i], e) * m) : dp;
+      }
+      if (c < n) store_8(dh + row * n + c, n - c, dr[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * T + threadIdx.x) * 8;
+    if (c < n)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) store_8(part + (static_cast<int64_t>(blockIdx.x) * 3 + k) * n + c, n - c, acc[k][i]);
+  }
+}
+
+// ------------------------------------------------------------------------------------ wide rows
+// Units of more than 8192 columns do not fit the registers: 256 threads walk the row once for its sums and
+// again for its outputs (from the caches), and the weights' gradients are sums down the columns, in a kernel
+// of their own, from the rows' saved factors.
+constexpr int kWideThreads = 256;
+constexpr int kWideParts = 256;  // row ranges of the weight gradients' sums
+struct WideRed {
+  float s[4];
+};
+__device__ __forceinline__ float wide_sum(float v, WideRed& red) {
+  v = row_sum16(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red.s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (red.s[0] + red.s[1]) + (red.s[2] + red.s[3]);
+}
+
 template <typename IO>
-__global__ __launch_bounds__(kNormThreads) void k_gate_norm(GateArgs<IO> a, IO* __restrict__ out) {
-  __shared__ float red[4];
+__global__ __launch_bounds__(kWideThreads) void k_wide_gate_norm(GateArgs<IO> a, IO* __restrict__ out) {
+  __shared__ WideRed red;
   const int n = a.d / a.groups, g = blockIdx.x % a.groups;
   const int64_t row = blockIdx.x / a.groups;
   const IO *y = a.y + row * a.y_ts + g * n, *z = a.z + row * a.z_ts + g * n;
   float ss = 0.0f;
-  for (int i = threadIdx.x; i < n; i += kNormThreads) {
+  for (int i = threadIdx.x; i < n; i += kWideThreads) {
     const float zv = ld_io(z, i);
     const float u = a.gate_first ? ld_io(y, i) * (zv * sigmoid(zv)) : ld_io(y, i);
     ss = __builtin_fmaf(u, u, ss);
   }
-  const float k = rsqrtf(group_sum(ss, red) / n + a.eps);
-  for (int i = threadIdx.x; i < n; i += kNormThreads) {
+  const float k = rsqrtf(wide_sum(ss, red) / n + a.eps);
+  for (int i = threadIdx.x; i < n; i += kWideThreads) {
     const float zv = ld_io(z, i);
     st_io(out, row * a.d + g * n + i, ld_io(y, i) * (zv * sigmoid(zv)) * k * a.w[g * n + i]);
   }
 }
 
-// dy, dz and, for the weight gradient's sums, each unit's factor k = rsqrt(mean + eps)
 template <typename IO>
-__global__ __launch_bounds__(kNormThreads) void k_gate_norm_bwd(GateArgs<IO> a, IO* __restrict__ dy, IO* __restrict__ dz,
+__global__ __launch_bounds__(kWideThreads) void k_wide_gate_norm_bwd(GateArgs<IO> a, IO* __restrict__ dy, IO* __restrict__ dz,
                                                                 int64_t dy_ts, int64_t dz_ts, float* __restrict__ stats) {
-  __shared__ float red[4];
+  __shared__ WideRed red;
   const int n = a.d / a.groups, g = blockIdx.x % a.groups;
   const int64_t row = blockIdx.x / a.groups;
   const IO *y = a.y + row * a.y_ts + g * n, *z = a.z + row * a.z_ts + g * n, *go = a.dout + row * a.d + g * n;
   const float* w = a.w + g * n;
   float ss = 0.0f, sd = 0.0f;
-  for (int i = threadIdx.x; i < n; i += kNormThreads) {
+  for (int i = threadIdx.x; i < n; i += kWideThreads) {
     const float zv = ld_io(z, i), s = zv * sigmoid(zv), yv = ld_io(y, i);
     const float u = a.gate_first ? yv * s : yv;
     ss = __builtin_fmaf(u, u, ss);
     sd = __builtin_fmaf(ld_io(go, i) * w[i] * (a.gate_first ? 1.0f : s), u, sd);
   }
-  ss = group_sum(ss, red);
-  sd = group_sum(sd, red);
+  ss = wide_sum(ss, red);
+  sd = wide_sum(sd, red);
   const float k = rsqrtf(ss / n + a.eps);
   const float m = sd * k / n;  // mean(dn n)
-  for (int i = threadIdx.x; i < n; i += kNormThreads) {
+  for (int i = threadIdx.x; i < n; i += kWideThreads) {
     const float zv = ld_io(z, i), sg = sigmoid(zv), s = zv * sg, ds = sg * (1.0f + zv * (1.0f - sg));
     const float yv = ld_io(y, i), go_w = ld_io(go, i) * w[i];
     const float u = a.gate_first ? yv * s : yv;
@@ -88,11 +543,10 @@ __global__ __launch_bounds__(kNormThreads) void k_gate_norm_bwd(GateArgs<IO> a, 
   if (threadIdx.x == 0) stats[row * a.groups + g] = k;
 }
 
-// partial sums of dw over the rows of one of kNormParts ranges
 template <typename IO>
-__global__ __launch_bounds__(kNormThreads) void k_gate_norm_dw(GateArgs<IO> a, const float* __restrict__ stats,
+__global__ __launch_bounds__(kWideThreads) void k_wide_gate_norm_dw(GateArgs<IO> a, const float* __restrict__ stats,
                                                                float* __restrict__ part, int64_t per) {
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
+  const int c = blockIdx.x * kWideThreads + threadIdx.x;
   if (c >= a.d) return;
   const int g = c / (a.d / a.groups);
   const int64_t r0 = blockIdx.y * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
@@ -105,43 +559,23 @@ __global__ __launch_bounds__(kNormThreads) void k_gate_norm_dw(GateArgs<IO> a, c
   part[static_cast<int64_t>(blockIdx.y) * a.d + c] = sum;
 }
 
-// out[c] = sum of the parts' c, in order
-__global__ __launch_bounds__(kNormThreads) void k_norm_parts(const float* __restrict__ part, float* __restrict__ out,
-                                                             int parts, int64_t stride, int d) {
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
-  if (c >= d) return;
-  float s = 0.0f;
-  for (int i = 0; i < parts; ++i) s += part[i * stride + c];
-  out[c] = s;
-}
-
 template <typename IO, typename RES>
-struct ResArgs {
-  const IO* h;
-  const RES* res;  // the residual before (forward) or after (backward) the addition; forward: may be NULL
-  const float *w, *wp, *vec;
-  float scale, eps;
-  int64_t rows;
-  int d;
-};
-
-template <typename IO, typename RES>
-__global__ __launch_bounds__(kNormThreads) void k_residual_norm(ResArgs<IO, RES> a, RES* __restrict__ res_out,
+__global__ __launch_bounds__(kWideThreads) void k_wide_residual_norm(ResArgs<IO, RES> a, RES* __restrict__ res_out,
                                                                 IO* __restrict__ out) {
-  __shared__ float red[4];
+  __shared__ WideRed red;
   extern __shared__ float r[];  // the row's new residual
   const int64_t base = static_cast<int64_t>(blockIdx.x) * a.d;
   float kp = 1.0f;
   if (a.wp != nullptr) {
     float ss = 0.0f;
-    for (int i = threadIdx.x; i < a.d; i += kNormThreads) {
+    for (int i = threadIdx.x; i < a.d; i += kWideThreads) {
       const float v = ld_io(a.h, base + i);
       ss = __builtin_fmaf(v, v, ss);
     }
-    kp = rsqrtf(group_sum(ss, red) / a.d + a.eps);
+    kp = rsqrtf(wide_sum(ss, red) / a.d + a.eps);
   }
   float ss = 0.0f;
-  for (int i = threadIdx.x; i < a.d; i += kNormThreads) {
+  for (int i = threadIdx.x; i < a.d; i += kWideThreads) {
     float p = ld_io(a.h, base + i);
     if (a.wp != nullptr) p *= kp * a.wp[i];
     const float v = __builtin_fmaf(a.vec != nullptr ? a.scale * a.vec[i] : a.scale, p,
@@ -150,28 +584,28 @@ __global__ __launch_bounds__(kNormThreads) void k_residual_norm(ResArgs<IO, RES>
     ss = __builtin_fmaf(v, v, ss);
     st_io(res_out, base + i, v);
   }
-  const float k = rsqrtf(group_sum(ss, red) / a.d + a.eps);
-  for (int i = threadIdx.x; i < a.d; i += kNormThreads) st_io(out, base + i, r[i] * k * a.w[i]);
+  const float k = rsqrtf(wide_sum(ss, red) / a.d + a.eps);
+  for (int i = threadIdx.x; i < a.d; i += kWideThreads) st_io(out, base + i, r[i] * k * a.w[i]);
 }
 
 template <typename IO, typename RES>
-__global__ __launch_bounds__(kNormThreads) void k_residual_norm_bwd(ResArgs<IO, RES> a, const IO* __restrict__ dout,
-                                                                    const RES* __restrict__ dres_out,
-                                                                    RES* __restrict__ dres, IO* __restrict__ dh,
+__global__ __launch_bounds__(kWideThreads) void k_wide_residual_norm_bwd(ResArgs<IO, RES> a, const IO* __restrict__ dout,
+                                                                    const RES* dres_out,
+                                                                    RES* dres, IO* __restrict__ dh,
                                                                     float* __restrict__ stats) {
-  __shared__ float red[4];
+  __shared__ WideRed red;
   extern __shared__ float dr[];  // the row's gradient of the residual
   const int64_t base = static_cast<int64_t>(blockIdx.x) * a.d;
   float ss = 0.0f, sd = 0.0f, sp = 0.0f;
-  for (int i = threadIdx.x; i < a.d; i += kNormThreads) {
+  for (int i = threadIdx.x; i < a.d; i += kWideThreads) {
     const float v = ld_io(a.res, base + i), hv = ld_io(a.h, base + i);
     ss = __builtin_fmaf(v, v, ss);
     sd = __builtin_fmaf(ld_io(dout, base + i) * a.w[i], v, sd);
     sp = __builtin_fmaf(hv, hv, sp);
   }
-  ss = group_sum(ss, red);
-  sd = group_sum(sd, red);
-  sp = group_sum(sp, red);
+  ss = wide_sum(ss, red);
+  sd = wide_sum(sd, red);
+  sp = wide_sum(sp, red);
   const float k = rsqrtf(ss / a.d + a.eps), m = sd * k / a.d;
   const float kp = a.wp != nullptr ? rsqrtf(sp / a.d + a.eps) : 1.0f;
   if (dres == nullptr) {  // the rows' factors alone
@@ -183,7 +617,7 @@ __global__ __launch_bounds__(kNormThreads) void k_residual_norm_bwd(ResArgs<IO, 
     return;
   }
   float sh = 0.0f;
-  for (int i = threadIdx.x; i < a.d; i += kNormThreads) {
+  for (int i = threadIdx.x; i < a.d; i += kWideThreads) {
     const float v = ld_io(a.res, base + i);
     const float g = (dres_out != nullptr ? ld_io(dres_out, base + i) : 0.0f) +
                     k * (ld_io(dout, base + i) * a.w[i] - v * k * m);
@@ -192,20 +626,19 @@ __global__ __launch_bounds__(kNormThreads) void k_residual_norm_bwd(ResArgs<IO, 
     if (a.wp != nullptr)
       sh = __builtin_fmaf(g * (a.vec != nullptr ? a.scale * a.vec[i] : a.scale) * a.wp[i], ld_io(a.h, base + i), sh);
   }
-  const float mp = a.wp != nullptr ? group_sum(sh, red) * kp / a.d : 0.0f;
-  for (int i = threadIdx.x; i < a.d; i += kNormThreads) {
+  const float mp = a.wp != nullptr ? wide_sum(sh, red) * kp / a.d : 0.0f;
+  for (int i = threadIdx.x; i < a.d; i += kWideThreads) {
     const float dp = dr[i] * (a.vec != nullptr ? a.scale * a.vec[i] : a.scale);
     st_io(dh, base + i, a.wp != nullptr ? kp * (dp * a.wp[i] - ld_io(a.h, base + i) * kp * mp) : dp);
   }
 }
 
-// partial sums of dw, dw_post and dscale_vec over the rows of one range
 template <typename IO, typename RES>
-__global__ __launch_bounds__(kNormThreads) void k_residual_norm_dw(ResArgs<IO, RES> a, const IO* __restrict__ dout,
-                                                                   const RES* __restrict__ dres_out,
+__global__ __launch_bounds__(kWideThreads) void k_wide_residual_norm_dw(ResArgs<IO, RES> a, const IO* __restrict__ dout,
+                                                                   const RES* dres_out,
                                                                    const float* __restrict__ stats,
                                                                    float* __restrict__ part, int64_t per) {
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
+  const int c = blockIdx.x * kWideThreads + threadIdx.x;
   if (c >= a.d) return;
   const int64_t r0 = blockIdx.y * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
   const float w = a.w[c], wp = a.wp != nullptr ? a.wp[c] : 1.0f;
