@@ -495,21 +495,38 @@ int mamba_mixer_heads_decode(const void* x, const void* dt, const void* B, const
   if ((rc = check_arrays(in, 8)) != MM_OK || (rc = check_arrays(out, 2)) != MM_OK) return rc;
   if ((rc = check_overlap(in, 8, out, 2, state_in)) != MM_OK) return rc;
   const HeadPar hp{dt, dt_stride, A_log, dt_bias, D, nullptr, Bs, H, Bs};
-  const int64_t blocks = static_cast<int64_t>(Bs) * H * cdiv(P, kSeqRows);
-  if (blocks * kSeqThreads > kMaxThreads) return MM_ERR_DIM;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const auto go = [&](auto io) {
+  const bool vec = N % 4 == 0 && aligned(state_in, 16) && aligned(state_out, 16);
+  const auto go = [&](auto io) -> int {
     using IO = decltype(io);
     const Tok<IO> xt = tok<IO>(x, x_stride, P, 1), bt = tok<IO>(B, b_stride, N, H / G), ct = tok<IO>(C, c_stride, N, H / G);
-    const dim3 grid(static_cast<unsigned>(blocks)), block(kSeqThreads);
     IO* yo = static_cast<IO*>(y);
-    if (N <= 64)
-      hipLaunchKernelGGL((k_heads_decode_any<IO, 4>), grid, block, 0, st, xt, bt, ct, hp, state_in, state_out, yo, P, N);
-    else
-      hipLaunchKernelGGL((k_heads_decode_any<IO, 16>), grid, block, 0, st, xt, bt, ct, hp, state_in, state_out, yo, P, N);
+    const int64_t heads = static_cast<int64_t>(Bs) * H;
+    if (!vec) {
+      const int64_t blocks = heads * cdiv(P, kSeqRows);
+      if (blocks * kSeqThreads > kMaxThreads) return MM_ERR_DIM;
+      const dim3 grid(static_cast<unsigned>(blocks)), block(kSeqThreads);
+      if (N <= 64)
+        hipLaunchKernelGGL((k_heads_decode_any<IO, 4>), grid, block, 0, st, xt, bt, ct, hp, state_in, state_out, yo, P, N);
+      else
+        hipLaunchKernelGGL((k_heads_decode_any<IO, 16>), grid, block, 0, st, xt, bt, ct, hp, state_in, state_out, yo, P, N);
+      return launched();
+    }
+    const auto run = [&](auto rl) -> int {
+      constexpr int RL = decltype(rl)::value;
+      const int64_t per = cdiv(P, kSeqThreads / RL * kDecodeRows);
+      if (heads * per * kSeqThreads > kMaxThreads) return MM_ERR_DIM;
+      hipLaunchKernelGGL((k_heads_decode<IO, RL>), dim3(static_cast<unsigned>(heads * per)), dim3(kSeqThreads), 0, st, xt, bt,
+                         ct, hp, state_in, state_out, yo, P, N, static_cast<int>(per));
+      return launched();
+    };
+    if (N <= 16) return run(std::integral_constant<int, 4>{});
+    if (N <= 32) return run(std::integral_constant<int, 8>{});
+    if (N <= 64) return run(std::integral_constant<int, 16>{});
+    if (N <= 128) return run(std::integral_constant<int, 32>{});
+    return run(std::integral_constant<int, 64>{});
   };
-  if (io_dtype == MM_IO_BF16) go(uint16_t{}); else go(float{});
-  return launched();
+  return io_dtype == MM_IO_BF16 ? go(uint16_t{}) : go(float{});
 }
 
 size_t mamba_mixer_heads_backward_workspace_bytes(int32_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N,
