@@ -13,6 +13,7 @@
 #include "mambamix.h"
 #include "mm_device.h"
 #include "mm_heads.h"
+#include "mm_heads_grad.h"
 #include "mm_heads_mma.h"
 #include "mm_host.h"
 #include "mm_norm.h"
@@ -35,7 +36,8 @@ struct HeadsPlan {
   int64_t rows64;  // 64-token blocks at most (backward)
   int nrp, nrn;    // 16-row blocks of P and N
   size_t off_carry, off_decay, off_carry2, off_decay2, off_hb, off_dots, off_dB, off_dC, off_q, off_r, off_delta,
-      off_sums, total;
+      off_sums, off_gs, total;
+  int npb, nk, splits;  // matrix-core backward: 64-channel blocks per head, 32-column steps of N, shares of a group's heads
 };
 
 // A workgroup of the sequential kernels walks one segment, about 0.1 us a token, so few long
@@ -50,7 +52,7 @@ constexpr int64_t kMmaWorkgroups = 1024;
 
 int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, int io, bool backward, int64_t max_stride) {
   p = HeadsPlan{};
-  p.mma = io == MM_IO_BF16 && N <= kMmaMaxN && !backward && max_stride <= kMmaMaxStride &&
+  p.mma = io == MM_IO_BF16 && N <= kMmaMaxN && max_stride <= kMmaMaxStride &&
           static_cast<int64_t>(H) * P <= kMmaMaxStride;
   p.nrp = static_cast<int>(cdiv(P, kSeqRows));
   p.nrn = static_cast<int>(cdiv(N, kSeqRows));
@@ -68,6 +70,11 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
     if (want_m <= S || p.Ls >= T) p.Ls = (T / kMmaTok + 1) * kMmaTok;
   }
   p.whole = p.Ls > T;
+  p.npb = static_cast<int>(cdiv(P, 64));
+  p.nk = N <= 32 ? 1 : N <= 64 ? 2 : 4;
+  // two workgroups of the gradient kernel per CU, or one for each head
+  p.splits = H > 0 ? static_cast<int>(std::max<int64_t>(
+                 1, std::min<int64_t>(H / G, cdiv(2 * kCUs, std::max<int64_t>(segment_rows(S, T, kHeadsBlock) * G, 1))))) : 1;
   p.rows = segment_rows(S, T, p.Ls);
   p.rows64 = segment_rows(S, T, kHeadsBlock);
   const size_t set = static_cast<size_t>(H) * P * N * 4;
@@ -83,6 +90,16 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
       take(p.off_carry2, p.rows * set);
       take(p.off_decay2, static_cast<size_t>(p.rows) * H * 4);
     }
+  }
+  if (backward && p.mma) {
+    const size_t blocks = static_cast<size_t>(p.rows64) * H * p.npb * 64 * (32 * p.nk) * 4;
+    const size_t part = static_cast<size_t>(p.splits) * T * G * N * 4;
+    take(p.off_hb, blocks);
+    take(p.off_gs, blocks);
+    take(p.off_dB, part);
+    take(p.off_dC, part);
+    take(p.off_sums, static_cast<size_t>(p.rows64) * H * 3 * 4);
+  } else if (backward) {
     take(p.off_hb, p.rows64 * set);
     take(p.off_dots, static_cast<size_t>(p.rows64) * H * p.nrp * 4);
     take(p.off_dB, th * N * 4);
@@ -94,7 +111,9 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   }
   p.total = off;
   const int64_t most = std::max<int64_t>(p.rows * H * std::max(p.nrp, p.nrn), p.rows64 * H);
-  if (most * kSeqThreads > kMaxThreads || static_cast<int64_t>(th) * 16 > kMaxThreads) return MM_ERR_DIM;
+  if (most * kSeqThreads > kMaxThreads || static_cast<int64_t>(th) * 16 > kMaxThreads ||
+      T * G * N > kMaxThreads)
+    return MM_ERR_DIM;
   return MM_OK;
 }
 
@@ -160,24 +179,38 @@ int allow_lds(K kernel, size_t bytes) {
   return MM_OK;
 }
 
-template <int NK, bool LOCAL, bool VEC>
-int launch_mma_t(const MmaArgs& q, const HeadPar& hp, hipStream_t st) {
-  const int rc = allow_lds(&k_heads_mma<NK, LOCAL, VEC>, MmaGeo<NK>::bytes);
-  if (rc != MM_OK) return rc;
-  const dim3 grid(static_cast<unsigned>(q.rows * q.pairs));
-  if (grid.x > 0)
-    hipLaunchKernelGGL((k_heads_mma<NK, LOCAL, VEC>), grid, dim3(kMmaThreads), MmaGeo<NK>::bytes, st, q, hp);
-  return MM_OK;
-}
-template <bool LOCAL>
-int launch_mma(const MmaArgs& q, const HeadPar& hp, bool vec, hipStream_t st) {
-  const auto go = [&](auto nk) {
-    constexpr int NK = decltype(nk)::value;
-    return vec ? launch_mma_t<NK, LOCAL, true>(q, hp, st) : launch_mma_t<NK, LOCAL, false>(q, hp, st);
-  };
-  if (q.N <= 32) return go(std::integral_constant<int, 1>{});
-  if (q.N <= 64) return go(std::integral_constant<int, 2>{});
+template <typename F>
+int by_steps(int nk, bool vec, F f) {
+  const auto go = [&](auto k) { return vec ? f(k, std::true_type{}) : f(k, std::false_type{}); };
+  if (nk == 1) return go(std::integral_constant<int, 1>{});
+  if (nk == 2) return go(std::integral_constant<int, 2>{});
   return go(std::integral_constant<int, 4>{});
+}
+
+int launch_states(const StateArgs& q, const HeadPar& hp, int nk, int dirs, bool vec, hipStream_t st) {
+  return by_steps(nk, vec, [&](auto k, auto v) -> int {
+    constexpr int NK = decltype(k)::value;
+    constexpr bool VEC = decltype(v)::value;
+    const int rc = allow_lds(&k_heads_states<NK, VEC>, StateGeo<NK>::bytes);
+    if (rc != MM_OK) return rc;
+    const dim3 grid(static_cast<unsigned>(q.rows * q.pairs), static_cast<unsigned>(dirs));
+    if (grid.x > 0)
+      hipLaunchKernelGGL((k_heads_states<NK, VEC>), grid, dim3(kMmaThreads), StateGeo<NK>::bytes, st, q, hp);
+    return MM_OK;
+  });
+}
+
+int launch_mma(const MmaArgs& q, const HeadPar& hp, int nk, bool vec, hipStream_t st) {
+  return by_steps(nk, vec, [&](auto k, auto v) -> int {
+    constexpr int NK = decltype(k)::value;
+    constexpr bool VEC = decltype(v)::value;
+    const int rc = allow_lds(&k_heads_mma<NK, VEC>, MmaGeo<NK>::bytes);
+    if (rc != MM_OK) return rc;
+    const dim3 grid(static_cast<unsigned>(q.rows * q.pairs));
+    if (grid.x > 0)
+      hipLaunchKernelGGL((k_heads_mma<NK, VEC>), grid, dim3(kMmaThreads), MmaGeo<NK>::bytes, st, q, hp);
+    return MM_OK;
+  });
 }
 
 int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* state_in, float* state_out, void* y,
@@ -201,12 +234,25 @@ int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* stat
   const bool vec = heads_vec(a, {state_in, state_out, y});
   if (!p.whole) {
     q.carry = reinterpret_cast<float*>(ws + p.off_carry);
-    q.decay = reinterpret_cast<float*>(ws + p.off_decay);
-    const int rc = launch_mma<true>(q, a.hp, vec, st);
+    StateArgs s{};
+    s.u[0] = q.x;
+    s.v[0] = q.B;
+    s.P = q.P;
+    s.N = q.N;
+    s.npb = q.npb;
+    s.vper = q.vper;
+    s.ppg = q.ppg;
+    s.pairs = q.pairs;
+    s.rows = q.rows;
+    s.Ls = q.Ls;
+    s.carry[0] = q.carry;
+    s.decay[0] = reinterpret_cast<float*>(ws + p.off_decay);
+    s.local = 1;
+    const int rc = launch_states(s, a.hp, p.nk, 1, vec, st);
     if (rc != MM_OK) return rc;
-    launch_carry(q.carry, q.decay, state_in, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, false, st);
+    launch_carry(q.carry, s.decay[0], state_in, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, false, st);
   }
-  const int rc = launch_mma<false>(q, a.hp, vec, st);
+  const int rc = launch_mma(q, a.hp, p.nk, vec, st);
   return rc != MM_OK ? rc : launched();
 }
 
@@ -246,6 +292,67 @@ struct HeadsGrads {
   int64_t dx_ts, ddt_ts, db_ts, dc_ts;
   float *dA_log, *dD, *ddt_bias, *dstate_in;
 };
+
+int launch_backward_mma(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o, char* ws, hipStream_t st) {
+  const int H = a.hp.H, div = H / a.G;
+  const int64_t T = a.hp.T, PN = static_cast<int64_t>(a.P) * a.N;
+  const Tok<uint16_t> x = tok<uint16_t>(a.x, a.x_ts, a.P, 1);
+  const Tok<uint16_t> dy = tok<uint16_t>(o.dy, static_cast<int64_t>(H) * a.P, a.P, 1);
+  const Tok<uint16_t> B = tok<uint16_t>(a.B, a.b_ts, a.N, div), C = tok<uint16_t>(a.C, a.c_ts, a.N, div);
+  const bool vec = heads_vec(a, {o.dy, o.dx}) && o.dx_ts % 8 == 0;
+  const auto at = [ws](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  StateArgs s{};
+  s.u[0] = x;
+  s.v[0] = B;
+  s.u[1] = dy;
+  s.v[1] = C;
+  s.P = a.P;
+  s.N = a.N;
+  s.npb = p.npb;
+  s.vper = div * p.npb;
+  s.ppg = static_cast<int>(cdiv(s.vper, 2));
+  s.pairs = s.ppg * a.G;
+  s.rows = p.rows;
+  s.Ls = p.Ls;
+  s.init[0] = o.state_in;
+  s.init[1] = o.dstate_out;
+  if (!p.whole) {
+    s.carry[0] = at(p.off_carry);
+    s.decay[0] = at(p.off_decay);
+    s.carry[1] = at(p.off_carry2);
+    s.decay[1] = at(p.off_decay2);
+    s.local = 1;
+    const int rc = launch_states(s, a.hp, p.nk, 2, vec, st);
+    if (rc != MM_OK) return rc;
+    s.local = 0;
+    launch_carry(s.carry[0], s.decay[0], s.init[0], a.hp, PN, p.Ls, false, st);
+    launch_carry(s.carry[1], s.decay[1], s.init[1], a.hp, PN, p.Ls, true, st);
+  }
+  s.store[0] = at(p.off_hb);
+  s.store[1] = at(p.off_gs);
+  s.fin[1] = o.dstate_in;
+  int rc = launch_states(s, a.hp, p.nk, 2, vec, st);
+  if (rc != MM_OK) return rc;
+  if (T > 0) {
+    const GradArgs g{x, dy, B, C, a.P, a.N, p.npb, a.G, p.splits, s.store[0], s.store[1], static_cast<uint16_t*>(o.dx),
+                     o.dx_ts, at(p.off_dB), at(p.off_dC), static_cast<uint16_t*>(o.ddt), o.ddt_ts, at(p.off_sums)};
+    rc = by_steps(p.nk, vec, [&](auto k, auto v) -> int {
+      constexpr int NK = decltype(k)::value;
+      constexpr bool VEC = decltype(v)::value;
+      const int r = allow_lds(&k_heads_grads<NK, VEC>, GradGeo<NK>::bytes);
+      if (r != MM_OK) return r;
+      hipLaunchKernelGGL((k_heads_grads<NK, VEC>), dim3(static_cast<unsigned>(p.rows64 * a.G * p.splits)), dim3(kMmaThreads),
+                         GradGeo<NK>::bytes, st, g, a.hp);
+      return MM_OK;
+    });
+    if (rc != MM_OK) return rc;
+    hipLaunchKernelGGL(k_heads_shares, dim3(static_cast<unsigned>(cdiv(T * a.G * a.N, 256))), dim3(256), 0, st, g.pB, g.pC,
+                       static_cast<uint16_t*>(o.dB), static_cast<uint16_t*>(o.dC), o.db_ts, o.dc_ts, T, a.G * a.N, p.splits);
+  }
+  hipLaunchKernelGGL(k_heads_params, dim3(static_cast<unsigned>(H)), dim3(256), 0, st, at(p.off_sums), T > 0 ? p.rows64 : 0, H,
+                     o.dA_log, o.ddt_bias, o.dD);
+  return launched();
+}
 
 template <typename IO>
 int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o, char* ws, hipStream_t st) {
@@ -573,6 +680,7 @@ int mamba_mixer_heads_backward(const void* x, const void* dt, const void* B, con
                      dA_log, D != nullptr ? dD : nullptr, dt != nullptr ? ddt_bias : nullptr, dstate_in};
   char* ws = static_cast<char*>(workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (p.mma) return launch_backward_mma(p, a, o, ws, st);
   if (io_dtype == MM_IO_BF16) return launch_backward<uint16_t>(p, a, o, ws, st);
   return launch_backward<float>(p, a, o, ws, st);
 }

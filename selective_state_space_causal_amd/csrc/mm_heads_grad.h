@@ -1,0 +1,674 @@
+// The gradients of the head scan on the matrix cores (bfloat16 io), in two kernels.
+//
+// k_heads_states walks the states: h forward, and from the last token to the first their adjoint
+//   Gam <- e^{c_last} Gam + sum_i e^{c_i} dy_i C_i^T          (the gradient of the state before a block)
+// and stores h at the start and Gam at the end of every 64-token block.  The blocks are those of the packed
+// stream (segment rows of length 64), so that
+// k_heads_grads can take every block by itself: a workgroup takes a block and some heads of a group, one after
+// another.  With M_ij = (C_i . B_j) d_ij, W_ij = dy_i . x_j, d_ij = e^{c_i - c_j}, w_j = e^{c_last - c_j} delta_j:
+//   dx_j = delta_j sum_{i>=j} M_ij dy_i + w_j Gam B_j + D dy_j
+//   dB_j = sum_{i>=j} delta_j W_ij d_ij C_i + w_j Gam^T x_j              (summed over the heads in registers)
+//   dC_i = sum_{j<=i} delta_j W_ij d_ij B_j + e^{c_i} h^T dy_i           (likewise)
+//   r_j  = sum_{i>=j} M_ij W_ij + e^{c_last - c_j} x_j . (Gam B_j)       (= dL/d(delta_j x_j) . x_j)
+//   dl_t = sum_{i>=t>j} delta_j M_ij W_ij + sum_{i>=t} e^{c_i} dy_i . (h C_i) + sum_{j<t} w_j x_j . (Gam B_j)
+//          + e^{c_last} <Gam, h>                                         (l = log a)
+//   ddelta = r + A dl
+// Each term of dl joins something before t to something from t on, so nothing cancels but in the first sum, which
+// is taken as a sum of strict row sums minus strict column sums from the block's end.
+//
+// Precision: dx, dB and dC leave in bfloat16; their computed operands (M, W d, h, Gam) are rounded to bfloat16
+// once.  dl, r and what is summed from them (dA_log, ddt_bias: float32 results) use float32 products of the exact
+// scores, and h and Gam in three bfloat16 parts (24 bits).
+#pragma once
+
+#include "mm_heads_mma.h"
+
+namespace mm {
+
+struct StateArgs {
+  Tok<uint16_t> u[2], v[2];   // forward x, B; reverse dy, C
+  int P, N, npb, vper, ppg, pairs;
+  int64_t rows, Ls;
+  const float* init[2];       // [S] states, or NULL: zeros
+  float* carry[2];            // [rows] states: written by local runs, else read where a sequence has several segments
+  float* decay[2];            // [rows, H] log2 of a segment's decay, written by local runs
+  float* store[2];            // [rows64, H npb, 64, NP]: the states at the blocks' starts / ends, or NULL
+  float* fin[2];              // [S] final states, or NULL
+  int local;                  // from zero, over all segments but a sequence's last (reverse: first)
+};
+
+template <int NK>
+struct StateGeo {
+  static constexpr int NP = NK * 32, PC = NP / 8;
+  static constexpr int B = 0, X = kMmaTok * NP * 2, F = X + kMmaTok * kMmaCols * 2, bytes = F + 2 * (2 * kMmaTok + 4) * 4;
+};
+
+// grid: (row, pair of head blocks) x direction
+template <int NK, bool VEC>
+__global__ __launch_bounds__(kMmaThreads, 2) void k_heads_states(StateArgs q, HeadPar hp) {
+  typedef StateGeo<NK> G;
+  constexpr int NT = 2 * NK, PC = G::PC;
+  extern __shared__ __align__(16) char lds[];
+  char *const sB = lds + G::B, *const sX = lds + G::X;
+  float* const sF = reinterpret_cast<float*>(lds + G::F);  // two sets of [block][64] weights and [block] last decays
+
+  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int dir = blockIdx.y;
+  const int pair = blockIdx.x % q.pairs;
+  const int64_t rho = blockIdx.x / q.pairs;
+  const Segment sg = segment_of(hp.cu, hp.S, rho, q.Ls);
+  const bool many = sg.many(q.Ls);
+  if (sg.none(rho, q.Ls)) return;
+  if (q.local && (!many || (dir ? sg.first() : sg.last()))) return;
+  const Tok<uint16_t> tu = q.u[dir], tv = q.v[dir];
+
+  const int group = pair / q.ppg, blk = wave >> 1;
+  const int in_group = 2 * (pair % q.ppg);
+  const bool have = in_group + blk < q.vper;
+  const int vh = group * q.vper + in_group + (have ? blk : 0);
+  const int h = vh / q.npb, p0 = (vh % q.npb) * 64;
+  const int pw = q.P - p0 < 64 ? q.P - p0 : 64;
+  const int col0 = (wave & 1) * 32;
+  const int64_t PN = static_cast<int64_t>(q.P) * q.N, set = hp.H * PN;
+
+  hf4 st[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) st[nt][ct] = hf4{0, 0, 0, 0};
+  if (!q.local) {
+    const float* from = many ? q.carry[dir] + rho * set : (q.init[dir] ? q.init[dir] + sg.s * set : nullptr);
+    if (from != nullptr && have)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) {
+        const int p = col0 + 16 * ct + li;
+        if (p < pw)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int n = 16 * nt + 4 * g;
+            const float* a = from + h * PN + static_cast<int64_t>(p0 + p) * q.N + n;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (n + r < q.N) st[nt][ct][r] = a[r];
+          }
+      }
+  }
+
+  const int brow = tid / PC, bcol = (tid % PC) * 8;
+  constexpr int bstep = kMmaThreads / PC;
+  const int xrow = tid >> 4, xcol = (tid & 15) * 8, xv = group * q.vper + in_group + (xcol >> 6);
+  const int xin = (xv % q.npb) * 64 + (xcol & 63);
+  const int xn = in_group + (xcol >> 6) < q.vper ? q.P - xin : 0, bn = q.N - bcol;
+  const int dH = hp.H * q.P, gn = (hp.H / tv.div) * q.N;
+  const int b_off = (brow * static_cast<int>(tv.ts) + group * q.N + bcol) * 2;
+  const int x_off = (xrow * static_cast<int>(tu.ts) + (xv / q.npb) * q.P + xin) * 2;
+  hu4 rB[NK], rX[4];
+  const auto load = [&](int64_t tb, int cnt) {
+    const hbuf bB = token_rows(tv.p, tb, tv.ts, cnt, gn), bX = token_rows(tu.p, tb, tu.ts, cnt, dH);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) rB[i] = load8<VEC>(bB, b_off + i * bstep * static_cast<int>(tv.ts) * 2, bn);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rX[i] = load8<VEC>(bX, x_off + i * 16 * static_cast<int>(tu.ts) * 2, xn);
+  };
+  // wave 0: the weights of block 0, wave 1: of block 1, a chunk ahead
+  const bool dhave = in_group + wave < q.vper;
+  const int dh = (group * q.vper + in_group + (dhave ? wave & 1 : 0)) / q.npb;
+  const float A2 = head_A2(hp, dh), bias = hp.dt != nullptr ? hp.dt_bias[dh] : 0.0f;
+  uint32_t rdt = 0;
+  double dsum = 0.0;
+  const auto load_dt = [&](int64_t tb, int cnt) {
+    if (wave < 2 && hp.dt != nullptr && lane < cnt)
+      rdt = static_cast<const uint16_t*>(hp.dt)[(tb + lane) * hp.dt_ts + dh];
+  };
+  const auto factors = [&](int cnt, int fs) {
+    if (wave >= 2) return;
+    const float del = !dhave || lane >= cnt ? 0.0f : hp.dt == nullptr ? 1.0f : softplus(io_value<uint16_t>(rdt) + bias);
+    const double c = lane_scan(static_cast<double>(fmaxf(del * A2, -512.0f)));  // (2^-512 is 0 in float32)
+    const double last = last_lane(c);
+    float* f = sF + fs * (2 * kMmaTok + 4);
+    f[wave * kMmaTok + lane] = dir ? exp2_hw(static_cast<float>(c)) : exp2_hw(static_cast<float>(last - c)) * del;
+    if (lane == 0) f[2 * kMmaTok + wave] = exp2_hw(static_cast<float>(last));
+    dsum += last;
+  };
+  // the segment's blocks of the packed stream, in the direction's order
+  const int64_t b0 = sg.t0 / kMmaTok, nb = sg.t0 < sg.t1 ? (sg.t1 - 1) / kMmaTok - b0 + 1 : 0;
+  const auto block = [&](int64_t k, int64_t& tb, int& cnt) {
+    const int64_t b = b0 + (dir ? nb - 1 - k : k);
+    tb = b * kMmaTok > sg.t0 ? b * kMmaTok : sg.t0;
+    const int64_t te = (b + 1) * kMmaTok < sg.t1 ? (b + 1) * kMmaTok : sg.t1;
+    cnt = k < nb ? static_cast<int>(te - tb) : 0;
+    return b;
+  };
+  int64_t tb, tn;
+  int cnt, cn;
+  block(0, tb, cnt);
+  if (nb > 0) {
+    load_dt(tb, cnt);
+    if (VEC) load(tb, cnt);
+    factors(cnt, 0);
+    block(1, tn, cn);
+    load_dt(tn, cn);
+  }
+  int aT = tile_at<PC>(4 * g + (li >> 2), 4 * (li & 3));
+  int xT = tile_at<kMmaXP>(4 * g + (li >> 2), 8 * (8 * blk + (col0 >> 3)) + 4 * (li & 3));
+  constexpr int R16 = 16 * PC * 16, X16 = 16 * kMmaXP * 16;
+  for (int64_t k = 0; k < nb; ++k) {
+    const int64_t b = block(k, tb, cnt);
+    asm volatile("" : "+v"(aT), "+v"(xT));
+    if (!VEC) load(tb, cnt);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NK; ++i) *reinterpret_cast<hu4*>(sB + tile_at<PC>(brow + i * bstep, bcol)) = rB[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<hu4*>(sX + tile_at<kMmaXP>(xrow + 16 * i, xcol)) = rX[i];
+    __syncthreads();
+    const float* const fs = sF + (k & 1) * (2 * kMmaTok + 4);
+    const float* const f = fs + blk * kMmaTok;
+    const float el = fs[2 * kMmaTok + blk];
+    block(k + 1, tn, cn);
+    if (VEC && k + 1 < nb) load(tn, cn);
+    factors(cn, (k + 1) & 1);
+    {
+      int64_t t2;
+      int c2;
+      block(k + 2, t2, c2);
+      load_dt(t2, c2);
+    }
+    if (q.store[dir] != nullptr && have) {
+      float* o = q.store[dir] + (((sg.s + b) * hp.H + h) * q.npb + (vh % q.npb)) * (64 * G::NP);
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          *reinterpret_cast<hf4*>(o + (col0 + 16 * ct + li) * G::NP + 16 * nt + 4 * g) = st[nt][ct];
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) st[nt][ct] *= el;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const hf4 w0 = *reinterpret_cast<const hf4*>(f + 32 * ks + 4 * g);
+      const hf4 w1 = *reinterpret_cast<const hf4*>(f + 32 * ks + 16 + 4 * g);
+      hb8 part[2][3];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) {
+        const char* a = sX + 2 * ks * X16 + (xT ^ (ct << 5));
+        weighted_parts(join(tr_read(a), tr_read(a + X16)), w0, w1, part[ct]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const char* a = sB + 2 * ks * R16 + (aT ^ (nt << 5));
+        const hb8 bt = join(tr_read(a), tr_read(a + R16));
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          st[nt][0] = mfma(bt, part[0][u], st[nt][0]);
+          st[nt][1] = mfma(bt, part[1][u], st[nt][1]);
+        }
+      }
+    }
+  }
+  float* to = q.local ? q.carry[dir] + rho * set
+                      : ((dir ? sg.first() : sg.last()) && q.fin[dir] != nullptr ? q.fin[dir] + sg.s * set : nullptr);
+  if (to != nullptr && have)
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+      const int p = col0 + 16 * ct + li;
+      if (p < pw)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int n = 16 * nt + 4 * g;
+          float* a = to + h * PN + static_cast<int64_t>(p0 + p) * q.N + n;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (n + r < q.N) a[r] = st[nt][ct][r];
+        }
+    }
+  if (q.local && wave < 2 && lane == 0 && dhave) q.decay[dir][rho * hp.H + dh] = static_cast<float>(dsum);
+}
+
+struct GradArgs {
+  Tok<uint16_t> x, dy, B, C;
+  int P, N, npb, G, splits;
+  const float *hs, *gs;   // the states at the blocks' starts, their adjoints at the ends
+  uint16_t* dx;
+  int64_t dx_ts;
+  float *pB, *pC;         // [splits, T, G N] sums over a workgroup's heads
+  uint16_t* ddt;
+  int64_t ddt_ts;
+  float* sums;            // [rows64, H, 3]: the block's shares of dA_log, ddt_bias and dD
+};
+
+enum { kGci, kGcf, kGdel, kGe, kGew, kGv16, kGe16, kGn = kGe16 + 3 };
+template <int NK>
+struct GradGeo {
+  static constexpr int NP = NK * 32, PC = NP / 8, T2 = kMmaTok * kMmaTok * 2;
+  static constexpr int B = 0, C = B + kMmaTok * NP * 2, X = C + kMmaTok * NP * 2, Y = X + T2, S = Y + T2,
+                       M = S + 64 * NP * 2, F = M + T2, R = F + kGn * kMmaTok * 4, bytes = R + (18 * kMmaTok + 8) * 4;
+};
+
+// grid: (block, group, share of its heads)
+template <int NK, bool VEC>
+__global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, HeadPar hp) {
+  typedef GradGeo<NK> G;
+  constexpr int NT = 2 * NK, PC = G::PC, NTW = (NT + 3) / 4;  // column tiles of dB and dC per wave
+  extern __shared__ __align__(16) char lds[];
+  char *const sB = lds + G::B, *const sC = lds + G::C, *const sX = lds + G::X, *const sY = lds + G::Y;
+  char *const sS = lds + G::S, *const sM = lds + G::M;
+  float* const f = reinterpret_cast<float*>(lds + G::F);
+  float* const rq = reinterpret_cast<float*>(lds + G::R);  // strict row sums, by column tile [4][64]
+  float* const rp = rq + 4 * kMmaTok;                      // strict column sums, by row tile [4][64]
+  float* const ri = rp + 4 * kMmaTok;                      // dy . (h C), by channel tile [4][64]
+  float* const rj = ri + 4 * kMmaTok;                      // x . (Gam B), likewise
+  float* const rd = rj + 4 * kMmaTok;                      // M_tt W_tt, then W_tt [2][64]
+  float* const re = rd + 2 * kMmaTok;                      // <Gam, h> by channel tile [4], e^{c_last}
+
+  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = blockIdx.x % q.splits;
+  const int group = (blockIdx.x / q.splits) % q.G;
+  const int64_t rho = blockIdx.x / q.splits / q.G;
+  const Segment sg = segment_of(hp.cu, hp.S, rho, kMmaTok);
+  const int hg = hp.H / q.G;
+  const int h0 = group * hg + split * hg / q.splits, h1 = group * hg + (split + 1) * hg / q.splits;
+  if (sg.t0 >= sg.t1) {
+    for (int i = tid; i < (h1 - h0) * 3; i += kMmaThreads) q.sums[(rho * hp.H + h0) * 3 + i] = 0.0f;
+    return;
+  }
+  const int64_t tb = sg.t0;
+  const int cnt = static_cast<int>(sg.t1 - tb);
+
+  const int aN = tile_at<PC>(li, 8 * g), aK = tile_at<PC>(li, 4 * g), aT = tile_at<PC>(4 * g + (li >> 2), 4 * (li & 3));
+  const int mN = tile_at<kMmaMP>(li, 8 * g), mK = tile_at<kMmaMP>(li, 4 * g),
+            mT = tile_at<kMmaMP>(4 * g + (li >> 2), 4 * (li & 3));
+  constexpr int R16 = 16 * PC * 16, M16 = 16 * kMmaMP * 16;
+
+  // B and C of the block, for all heads
+  const int dH = hp.H * q.P, gn = q.G * q.N;
+  {
+    const int brow = tid / PC, bcol = (tid % PC) * 8;
+    constexpr int bstep = kMmaThreads / PC;
+    const hbuf bB = token_rows(q.B.p, tb, q.B.ts, cnt, gn), bC = token_rows(q.C.p, tb, q.C.ts, cnt, gn);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int row = brow + i * bstep, col = group * q.N + bcol;
+      *reinterpret_cast<hu4*>(sB + tile_at<PC>(row, bcol)) = load8<VEC>(bB, (row * static_cast<int>(q.B.ts) + col) * 2, q.N - bcol);
+      *reinterpret_cast<hu4*>(sC + tile_at<PC>(row, bcol)) = load8<VEC>(bC, (row * static_cast<int>(q.C.ts) + col) * 2, q.N - bcol);
+    }
+  }
+  const hbuf bX = token_rows(q.x.p, tb, q.x.ts, cnt, dH), bY = token_rows(q.dy.p, tb, q.dy.ts, cnt, dH);
+  const hbuf bO = token_rows(q.dx, tb, q.dx_ts, cnt, dH);
+  const int xrow = tid >> 3, xcol = (tid & 7) * 8;
+  hu4 rX[2], rY[2];
+  const auto load = [&](int h, int pb) {
+    const int n = q.P - 64 * pb - xcol, at = h * q.P + 64 * pb + xcol;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      rX[i] = load8<VEC>(bX, ((xrow + 32 * i) * static_cast<int>(q.x.ts) + at) * 2, n);
+      rY[i] = load8<VEC>(bY, ((xrow + 32 * i) * static_cast<int>(q.dy.ts) + at) * 2, n);
+    }
+  };
+  load(h0, 0);
+  __syncthreads();
+
+  // the wave's score tiles (it, jt <= it): C_i . B_j, rows j and columns i, the same for every head
+  const int its[3] = {wave < 2 ? 3 : wave == 2 ? 2 : 1, wave < 2 ? 3 : wave == 2 ? 2 : 1, wave == 2 ? 2 : 0};
+  const int jts[3] = {wave == 1 ? 2 : 0, wave == 1 ? 3 : 1, wave == 2 ? 2 : 0};
+  hf4 cb[3];
+#pragma unroll
+  for (int u = 0; u < 3; ++u) {
+    cb[u] = hf4{0, 0, 0, 0};
+    if (u == 2 && wave < 2) continue;
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+      cb[u] = mfma(lds8(sB + jts[u] * R16 + (aN ^ (k << 6))), lds8(sC + its[u] * R16 + (aN ^ (k << 6))), cb[u]);
+  }
+  hf4 dB[4][NTW], dC[4][NTW];  // [token 16 t + 4g + r][n = 16 nt + li]
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int n = 0; n < NTW; ++n) dB[t][n] = dC[t][n] = hf4{0, 0, 0, 0};
+
+  const hb4 none = to_bf4(hf4{0, 0, 0, 0});
+  // of wave 0: a token's sums over the channel blocks of a head
+  float qs = 0.0f, ps = 0.0f, dg = 0.0f, wd = 0.0f, qi = 0.0f, pi = 0.0f, e0 = 0.0f;
+  for (int h = h0; h < h1; ++h)
+    for (int pb = 0; pb < q.npb; ++pb) {
+      // the state and its adjoint: rows p = 16 wave + li, columns 32 k + 8 g ..
+      const int64_t srow = ((rho * hp.H + h) * q.npb + pb) * (64 * G::NP) + (16 * wave + li) * G::NP + 8 * g;
+      hf4 s[NK][2];
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        s[k][0] = *reinterpret_cast<const hf4*>(q.hs + srow + 32 * k);
+        s[k][1] = *reinterpret_cast<const hf4*>(q.hs + srow + 32 * k + 4);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<hu4*>(sX + tile_at<kMmaMP>(xrow + 32 * i, xcol)) = rX[i];
+        *reinterpret_cast<hu4*>(sY + tile_at<kMmaMP>(xrow + 32 * i, xcol)) = rY[i];
+      }
+      if (wave == 3 && pb == 0) {
+        float del = 0.0f;
+        if (lane < cnt) del = head_delta<uint16_t>(hp, tb + lane, h);
+        const double c = lane_scan(static_cast<double>(fmaxf(del * head_A2(hp, h), -512.0f)));  // (2^-512 is 0 in float32)
+        const double last = last_lane(c);
+        const double whole = floor(c);
+        const float ci = static_cast<float>(whole), cf = static_cast<float>(c - whole);
+        f[kGci * kMmaTok + lane] = ci;
+        f[kGcf * kMmaTok + lane] = cf;
+        f[kGdel * kMmaTok + lane] = del;
+        f[kGe * kMmaTok + lane] = exp2_hw(static_cast<float>(c));
+        f[kGew * kMmaTok + lane] = exp2_hw(static_cast<float>(last - c));
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          const float ti = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ci), 16 * t + 15));
+          const float tf = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cf), 16 * t + 15));
+          const float d = (ci - ti) + (cf - tf);
+          f[(kGe16 + t) * kMmaTok + lane] = exp2_hw(d);
+          if (lane >> 4 == t) f[kGv16 * kMmaTok + lane] = exp2_hw(-d);
+        }
+        if (lane == 0) re[4] = exp2_hw(static_cast<float>(last));
+      }
+      __syncthreads();
+      {
+        const int hn = pb + 1 < q.npb ? h : h + 1, pn = pb + 1 < q.npb ? pb + 1 : 0;
+        if (hn < h1) load(hn, pn);
+      }
+      // scores dy_i . x_j; the tiles of delta M (for dx) now, those of delta W d (for dB, dC) later
+      hb4 m2[3];
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        m2[u] = none;
+        if (u == 2 && wave < 2) continue;
+        const int it = its[u], jt = jts[u], i = 16 * it + li, j = 16 * jt + 4 * g;
+        hf4 w = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          w = mfma(lds8(sX + jt * M16 + (mN ^ (k << 6))), lds8(sY + it * M16 + (mN ^ (k << 6))), w);
+        const hf4 del = *reinterpret_cast<const hf4*>(f + kGdel * kMmaTok + j);
+        hf4 d;
+        if (it != jt) {
+          d = f[(kGe16 + jt) * kMmaTok + i] * *reinterpret_cast<const hf4*>(f + kGv16 * kMmaTok + j);
+        } else {
+          const float ci = f[kGci * kMmaTok + i], cf = f[kGcf * kMmaTok + i];
+          const hf4 cj = *reinterpret_cast<const hf4*>(f + kGci * kMmaTok + j), fj = *reinterpret_cast<const hf4*>(f + kGcf * kMmaTok + j);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float v = exp2_hw((ci - cj[r]) + (cf - fj[r]));
+            d[r] = 4 * g + r <= li ? v : 0.0f;
+          }
+        }
+        // a value that is not finite times a masked zero would be NaN: the mask selects
+        hf4 m1, w2, tt;
+        float row = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool on = it != jt || 4 * g + r <= li;
+          const float md = on ? cb[u][r] * d[r] : 0.0f;
+          m1[r] = md * del[r];
+          w2[r] = on ? w[r] * d[r] * del[r] : 0.0f;
+          tt[r] = on ? md * w[r] : 0.0f;
+        }
+        if (it == jt && li >> 2 == g) {
+          const int r = li & 3;
+          rd[i] = r == 0 ? tt[0] : r == 1 ? tt[1] : r == 2 ? tt[2] : tt[3];
+          rd[kMmaTok + i] = r == 0 ? w[0] : r == 1 ? w[1] : r == 2 ? w[2] : w[3];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (it == jt && 4 * g + r == li) tt[r] = 0.0f;
+          row = __builtin_fmaf(tt[r], del[r], row);
+          tt[r] = row_sum16(tt[r]);
+        }
+        row += __shfl_xor(row, 16);
+        row += __shfl_xor(row, 32);
+        if (g == 0) rq[jt * kMmaTok + i] = row;
+        if (li < 4) rp[it * kMmaTok + j + li] = li == 0 ? tt[0] : li == 1 ? tt[1] : li == 2 ? tt[2] : tt[3];
+        *reinterpret_cast<hb4*>(sM + it * M16 + (mK ^ (jt << 5))) = to_bf4(m1);
+        m2[u] = to_bf4(w2);
+      }
+      // h C for q, in three parts; h's first part to LDS for dC
+      hf4 acc[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = hf4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        hb8 part[3];
+        split3(s[k][0], s[k][1], part);
+        *reinterpret_cast<hb8*>(sS + wave * R16 + (aN ^ (k << 6))) = part[0];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const hb8 c = lds8(sC + t * R16 + (aN ^ (k << 6)));
+#pragma unroll
+          for (int u = 0; u < 3; ++u) acc[t] = mfma(part[u], c, acc[t]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const hf4 y = to_f4(lds4(sY + t * M16 + (mK ^ (wave << 5))));
+        float v = (acc[t][0] * y[0] + acc[t][1] * y[1]) + (acc[t][2] * y[2] + acc[t][3] * y[3]);
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+        if (g == 0) ri[wave * kMmaTok + 16 * t + li] = v;
+      }
+      __syncthreads();
+      // the adjoint's loads, in flight over the products of the state
+      hf4 a[NK][2];
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        a[k][0] = *reinterpret_cast<const hf4*>(q.gs + srow + 32 * k);
+        a[k][1] = *reinterpret_cast<const hf4*>(q.gs + srow + 32 * k + 4);
+      }
+      // dx within the block: rows p = 16 wave + 4g + r, columns j = 16 jt + li
+      hf4 dx[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) dx[t] = hf4{0, 0, 0, 0};
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const char* ya = sY + 2 * ks * M16 + (mT ^ (wave << 5));
+        const hb8 yt = join(tr_read(ya), tr_read(ya + M16));
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) {
+          if (ks == 0 && jt > 1) continue;
+          const char* ma = sM + 2 * ks * M16 + (mT ^ (jt << 5));
+          // tiles above the diagonal's were not written: zeros
+          const hb8 m = join((jt & 1) && jt / 2 == ks ? none : tr_read(ma), tr_read(ma + M16));
+          dx[jt] = mfma(yt, m, dx[jt]);
+        }
+      }
+      // dC from the state
+#pragma unroll
+      for (int n = 0; n < NTW; ++n) {
+        const int nt = wave * NTW + n;
+        if (nt >= NT) continue;
+        hb8 sT[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const char* sa = sS + 2 * ks * R16 + (aT ^ (nt << 5));
+          sT[ks] = join(tr_read(sa), tr_read(sa + R16));
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          hf4 v = {0, 0, 0, 0};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            v = mfma(join(lds4(sY + t * M16 + (mK ^ (ks << 6))), lds4(sY + t * M16 + (mK ^ (ks << 6) ^ 32))), sT[ks], v);
+          dC[t][n] += v * *reinterpret_cast<const hf4*>(f + kGe * kMmaTok + 16 * t + 4 * g);
+        }
+      }
+      __syncthreads();
+      // Gam B in three parts, <Gam, h>; the tiles of delta W d and Gam's first part to LDS
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        if (u == 2 && wave < 2) continue;
+        *reinterpret_cast<hb4*>(sM + its[u] * M16 + (mK ^ (jts[u] << 5))) = m2[u];
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = hf4{0, 0, 0, 0};
+      float dot = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          dot = __builtin_fmaf(s[k][0][r], a[k][0][r], dot);
+          dot = __builtin_fmaf(s[k][1][r], a[k][1][r], dot);
+        }
+        hb8 part[3];
+        split3(a[k][0], a[k][1], part);
+        *reinterpret_cast<hb8*>(sS + wave * R16 + (aN ^ (k << 6))) = part[0];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const hb8 b = lds8(sB + t * R16 + (aN ^ (k << 6)));
+#pragma unroll
+          for (int u = 0; u < 3; ++u) acc[t] = mfma(part[u], b, acc[t]);
+        }
+      }
+      dot = row_sum16(dot);
+      dot += __shfl_xor(dot, 16);
+      dot += __shfl_xor(dot, 32);
+      if (lane == 0) re[wave] = dot;
+      const float Dh = hp.D != nullptr ? hp.D[h] : 0.0f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int j = 16 * t + li, p = 16 * wave + 4 * g;
+        const hf4 x = to_f4(lds4(sX + t * M16 + (mK ^ (wave << 5))));
+        const hf4 y = to_f4(lds4(sY + t * M16 + (mK ^ (wave << 5))));
+        float v = (acc[t][0] * x[0] + acc[t][1] * x[1]) + (acc[t][2] * x[2] + acc[t][3] * x[3]);
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+        if (g == 0) rj[wave * kMmaTok + j] = v;
+        const hf4 o = dx[t] + acc[t] * (f[kGew * kMmaTok + j] * f[kGdel * kMmaTok + j]) + y * Dh;
+        const hu2 ob = __builtin_bit_cast(hu2, to_bf4(o));
+        const int off = (j * static_cast<int>(q.dx_ts) + h * q.P + 64 * pb + p) * 2, n = q.P - 64 * pb - p;
+        if (VEC) {
+          typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, ob), bO, n > 0 ? off : kMmaPastEnd, 0, 0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(ob[e / 2] >> (16 * (e % 2))), bO,
+                                                  e < n ? off + 2 * e : kMmaPastEnd, 0, 0);
+        }
+      }
+      __syncthreads();
+      // dB and dC: from the adjoint, and within the block
+#pragma unroll
+      for (int n = 0; n < NTW; ++n) {
+        const int nt = wave * NTW + n;
+        if (nt >= NT) continue;
+        hb8 gT[2], cT[2], bT[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const int o = 2 * ks * R16 + (aT ^ (nt << 5));
+          gT[ks] = join(tr_read(sS + o), tr_read(sS + o + R16));
+          cT[ks] = join(tr_read(sC + o), tr_read(sC + o + R16));
+          bT[ks] = join(tr_read(sB + o), tr_read(sB + o + R16));
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          hf4 v = {0, 0, 0, 0};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            v = mfma(join(lds4(sX + t * M16 + (mK ^ (ks << 6))), lds4(sX + t * M16 + (mK ^ (ks << 6) ^ 32))), gT[ks], v);
+          dB[t][n] += v * (*reinterpret_cast<const hf4*>(f + kGew * kMmaTok + 16 * t + 4 * g) *
+                           *reinterpret_cast<const hf4*>(f + kGdel * kMmaTok + 16 * t + 4 * g));
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            if (!(ks == 0 && t > 1)) {  // i >= j: rows j = 16 t ..
+              const char* ma = sM + 2 * ks * M16 + (mT ^ (t << 5));
+              dB[t][n] = mfma(join((t & 1) && t / 2 == ks ? none : tr_read(ma), tr_read(ma + M16)), cT[ks], dB[t][n]);
+            }
+            if (!(ks == 1 && t < 2)) {  // j <= i: rows i = 16 t ..
+              const char* ma = sM + t * M16;
+              dC[t][n] = mfma(join(lds4(ma + (mK ^ (ks << 6))), (t & 1) == 0 && t / 2 == ks ? none : lds4(ma + (mK ^ (ks << 6) ^ 32))),
+                              bT[ks], dC[t][n]);
+            }
+          }
+        }
+      }
+      if (wave == 0) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if (t <= g) qs += rq[t * kMmaTok + lane];
+          if (t >= g) ps += rp[t * kMmaTok + lane];
+          qi += ri[t * kMmaTok + lane];
+          pi += rj[t * kMmaTok + lane];
+          e0 += re[t];
+        }
+        dg += rd[lane];
+        wd += rd[kMmaTok + lane];
+        if (pb == q.npb - 1) {
+          const float del = f[kGdel * kMmaTok + lane];
+          qi *= f[kGe * kMmaTok + lane];
+          pi *= f[kGew * kMmaTok + lane];
+          const float r = ps + dg + pi;
+          float suf = qs - del * ps, sq = qi, pre = del * pi;
+          for (int k = 1; k < 64; k *= 2) {
+            const float o = __shfl_down(suf, k), oq = __shfl_down(sq, k), op = __shfl_up(pre, k);
+            if (lane + k < 64) suf += o, sq += oq;
+            if (lane >= k) pre += op;
+          }
+          const float dl = ((suf + sq) + (pre - del * pi)) + re[4] * e0;
+          const float A = -exp2_hw(hp.A_log[h] * kLog2e);
+          float dA = 0.0f, db = 0.0f;
+          if (lane < cnt) {
+            dA = del * dl * A;
+            if (hp.dt != nullptr) {
+              const float v = ld_io(static_cast<const uint16_t*>(hp.dt) + (tb + lane) * hp.dt_ts, h) + hp.dt_bias[h];
+              db = __builtin_fmaf(A, dl, r) * rcp_hw(1.0f + exp2_hw(-v * kLog2e));
+              st_io(q.ddt, (tb + lane) * q.ddt_ts + h, db);
+            }
+          }
+          for (int k = 32; k > 0; k /= 2) {
+            dA += __shfl_xor(dA, k);
+            db += __shfl_xor(db, k);
+            wd += __shfl_xor(wd, k);
+          }
+          if (lane == 0) {
+            float* o = q.sums + (rho * hp.H + h) * 3;
+            o[0] = dA;
+            o[1] = db;
+            o[2] = wd;
+          }
+          qs = ps = dg = wd = qi = pi = e0 = 0.0f;
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+  for (int n = 0; n < NTW; ++n) {
+    const int col = 16 * (wave * NTW + n) + li;
+    if (wave * NTW + n < NT && col < q.N)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * t + 4 * g + r;
+          if (row < cnt) {
+            const int64_t o = (static_cast<int64_t>(split) * hp.T + tb + row) * gn + group * q.N + col;
+            q.pB[o] = dB[t][n][r];
+            q.pC[o] = dC[t][n][r];
+          }
+        }
+  }
+}
+
+// dB and dC: the sums of the workgroups' shares, in order
+__global__ __launch_bounds__(256) void k_heads_shares(const float* __restrict__ pB, const float* __restrict__ pC,
+                                                      uint16_t* __restrict__ dB, uint16_t* __restrict__ dC, int64_t db_ts,
+                                                      int64_t dc_ts, int64_t T, int gn, int splits) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= T * gn) return;
+  float b = 0.0f, c = 0.0f;
+  for (int k = 0; k < splits; ++k) {
+    b += pB[k * T * gn + i];
+    c += pC[k * T * gn + i];
+  }
+  const int64_t t = i / gn;
+  const int n = static_cast<int>(i % gn);
+  st_io(dB, t * db_ts + n, b);
+  st_io(dC, t * dc_ts + n, c);
+}
+
+}  // namespace mm

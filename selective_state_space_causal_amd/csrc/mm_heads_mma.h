@@ -51,7 +51,6 @@ struct MmaArgs {
   const float* state_in;
   float* state_out;
   float* carry;
-  float* decay;
   uint16_t* y;
 };
 
@@ -122,6 +121,33 @@ __device__ __forceinline__ double last_lane(double v) {
   return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
 
+// eight float32 as three bfloat16 parts, whose sum has all 24 bits (of a value that is not finite the first part
+// says so and the others are NaN or zero)
+__device__ __forceinline__ void split3(hf4 a, hf4 b, hb8 (&part)[3]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float v[2] = {e < 4 ? a[e & 3] : b[e & 3], e < 4 ? a[(e + 1) & 3] : b[(e + 1) & 3]};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const hb2 o = to_bf2(v[0], v[1]);
+      part[k][e] = o[0];
+      part[k][e + 1] = o[1];
+      v[0] -= static_cast<float>(o[0]);
+      v[1] -= static_cast<float>(o[1]);
+    }
+  }
+}
+// the same of w x, the weights of the operand's K indices in w0 and w1
+__device__ __forceinline__ void weighted_parts(hb8 x, hf4 w0, hf4 w1, hb8 (&part)[3]) {
+  hf4 a, b;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    a[e] = w0[e] * static_cast<float>(x[e]);
+    b[e] = w1[e] * static_cast<float>(x[4 + e]);
+  }
+  split3(a, b, part);
+}
+
 // Rows of a token tensor from token tb on as a range-checked buffer: rows from `cnt` on read as zeros (and
 // stores to them are dropped), so nothing branches on a sequence's end.
 typedef __amdgpu_buffer_rsrc_t hbuf;
@@ -162,7 +188,7 @@ __device__ __forceinline__ uint32_t not_finite(hu4 v) {
   return f;
 }
 
-template <int NK, bool LOCAL, bool VEC>
+template <int NK, bool VEC>
 __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar hp) {
   typedef MmaGeo<NK> G;
   constexpr int NT = 2 * NK, PC = G::PC;
@@ -178,7 +204,6 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   const Segment sg = segment_of(hp.cu, hp.S, rho, q.Ls);
   const bool many = sg.many(q.Ls);
   if (sg.none(rho, q.Ls)) return;
-  if (LOCAL && (!many || sg.last())) return;
 
   // the wave's block of head channels, and where its columns lie
   const int group = pair / q.ppg, blk = wave >> 1;
@@ -197,7 +222,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) st[nt][ct] = hf4{0, 0, 0, 0};
-  if (!LOCAL) {
+  {
     const float* from = many ? q.carry + rho * set : (q.state_in ? q.state_in + sg.s * set : nullptr);
     if (from != nullptr && have)
 #pragma unroll
@@ -236,9 +261,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
     const hbuf bC = token_rows(q.C.p, tb, q.C.ts, cnt, gn);
 #pragma unroll
     for (int i = 0; i < NK; ++i) rB[i] = load8<VEC>(bB, b_off + i * bstep * static_cast<int>(q.B.ts) * 2, bn);
-    if (!LOCAL)
 #pragma unroll
-      for (int i = 0; i < NK; ++i) rC[i] = load8<VEC>(bC, c_off + i * bstep * static_cast<int>(q.C.ts) * 2, bn);
+    for (int i = 0; i < NK; ++i) rC[i] = load8<VEC>(bC, c_off + i * bstep * static_cast<int>(q.C.ts) * 2, bn);
 #pragma unroll
     for (int i = 0; i < 4; ++i) rX[i] = load8<VEC>(bX, x_off + i * 16 * static_cast<int>(q.x.ts) * 2, xn);
   };
@@ -261,7 +285,6 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   const int dh = (group * q.vper + in_group + (dhave ? wave & 1 : 0)) / q.npb;
   const float A2 = head_A2(hp, dh), bias = hp.dt != nullptr ? hp.dt_bias[dh] : 0.0f;
   uint32_t rdt = 0;  // as loaded: its use waits for it
-  double dsum = 0.0;
   const auto load_dt = [&](int64_t tb) {
     if (wave < 2 && hp.dt != nullptr && tb + lane < sg.t1)
       rdt = static_cast<const uint16_t*>(hp.dt)[(tb + lane) * hp.dt_ts + dh];
@@ -277,7 +300,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
     const float ci = static_cast<float>(whole), cf = static_cast<float>(c - whole);
     f[kFe * kMmaTok] = exp2_hw(static_cast<float>(c));
     f[kFw * kMmaTok] = exp2_hw(static_cast<float>(last - c)) * del;
-    if (!LOCAL) {
+    {
       f[kFci * kMmaTok] = ci;
       f[kFcf * kMmaTok] = cf;
       f[kFdel * kMmaTok] = del;
@@ -292,7 +315,6 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
       }
     }
     if (lane == 0) sF[set * kMmaFSet + 2 * kFn * kMmaTok + wave] = exp2_hw(static_cast<float>(last));
-    dsum += last;
   };
   int par = 0;  // two flags in turn: one is cleared while the other may still be read
   if (tid == 0) sFlag[0] = 0;
@@ -312,7 +334,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
     for (int i = 0; i < NK; ++i) {
       const int a = tile_at<PC>(brow + i * bstep, bcol);
       *reinterpret_cast<hu4*>(sB + a) = rB[i];
-      if (!LOCAL) *reinterpret_cast<hu4*>(sC + a) = rC[i];
+      *reinterpret_cast<hu4*>(sC + a) = rC[i];
     }
     uint32_t odd = 0;
 #pragma unroll
@@ -328,7 +350,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
     const float el = fs[2 * kFn * kMmaTok + blk];
     par ^= 1;
     hf4 acc[4][2];  // y transposed: [p = 16 ct + 4g + r][token 16 it + li]
-    if (!LOCAL) {
+    {
       // C . B for 16 x 16 tiles (it, jt <= it), M of both blocks from it.  Below the diagonal's tiles the decay is
       // split at the end of tile jt, both parts <= 1: one exponential for each token instead of one for each pair.
       const auto tile = [&](auto it_, auto jt_) {
@@ -399,10 +421,6 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (LOCAL) {
-      factors(tb + kMmaTok, par);
-      load_dt(tb + 2 * kMmaTok);
-    }
     // x transposed: the operand of the products over tokens
     hb8 xt[2][2];  // [32 tokens ks][ct]
 #pragma unroll
@@ -412,7 +430,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
         const char* a = sX + 2 * ks * X16 + (xT ^ (ct << 5));
         xt[ks][ct] = join(tr_read(a), tr_read(a + X16));
       }
-    if (!LOCAL) {
+    {
       __syncthreads();
       const hb4 none = to_bf4(hf4{0, 0, 0, 0});
       if (!flag) {
@@ -471,23 +489,9 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
     for (int ks = 0; ks < 2; ++ks) {
       const hf4 w0 = *reinterpret_cast<const hf4*>(f + kFw * kMmaTok + 32 * ks + 4 * g);
       const hf4 w1 = *reinterpret_cast<const hf4*>(f + kFw * kMmaTok + 32 * ks + 16 + 4 * g);
-      hb8 part[2][3];  // of a value that is not finite the first part says so and the others are NaN or zero
+      hb8 part[2][3];
 #pragma unroll
-      for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          float v[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) v[u] = (e < 4 ? w0[(e + u) & 3] : w1[(e + u) & 3]) * static_cast<float>(xt[ks][ct][e + u]);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const hb2 o = to_bf2(v[0], v[1]);
-            part[ct][k][e] = o[0];
-            part[ct][k][e + 1] = o[1];
-            v[0] -= static_cast<float>(o[0]);
-            v[1] -= static_cast<float>(o[1]);
-          }
-        }
+      for (int ct = 0; ct < 2; ++ct) weighted_parts(xt[ks][ct], w0, w1, part[ct]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const char* a = sB + 2 * ks * R16 + (aT ^ (nt << 5));
@@ -500,7 +504,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
       }
     }
   }
-  float* to = LOCAL ? q.carry + rho * set : (sg.last() ? q.state_out + sg.s * set : nullptr);
+  float* to = sg.last() ? q.state_out + sg.s * set : nullptr;
   if (to != nullptr && have)
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
@@ -519,7 +523,6 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
           }
         }
     }
-  if (LOCAL && wave < 2 && lane == 0 && dhave) q.decay[rho * hp.H + dh] = static_cast<float>(dsum);
 }
 
 }  // namespace mm
