@@ -264,8 +264,9 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
   float* const rd = rj + 4 * kMmaTok;                      // M_tt W_tt, then W_tt [2][64]
   float* const re = rd + 2 * kMmaTok;                      // <Gam, h> by channel tile [4], e^{c_last}
 
-  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x;
+  int lane = tid & 63, li = lane & 15, g = lane >> 4;
+  int wv = tid >> 6, wave = __builtin_amdgcn_readfirstlane(wv);
   const int split = blockIdx.x % q.splits;
   const int group = (blockIdx.x / q.splits) % q.G;
   const int64_t rho = blockIdx.x / q.splits / q.G;
@@ -279,9 +280,10 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
   const int64_t tb = sg.t0;
   const int cnt = static_cast<int>(sg.t1 - tb);
 
-  const int aN = tile_at<PC>(li, 8 * g), aK = tile_at<PC>(li, 4 * g), aT = tile_at<PC>(4 * g + (li >> 2), 4 * (li & 3));
-  const int mN = tile_at<kMmaMP>(li, 8 * g), mK = tile_at<kMmaMP>(li, 4 * g),
-            mT = tile_at<kMmaMP>(4 * g + (li >> 2), 4 * (li & 3));
+  // LDS offsets of a lane's operands (natural order, four columns, transposed) in tiles of PC and of 8 pieces;
+  // opaque for each head, since their sums with the tiles' constants would not fit the registers
+  int aN = tile_at<PC>(li, 8 * g), aT = tile_at<PC>(4 * g + (li >> 2), 4 * (li & 3));
+  int mN = tile_at<kMmaMP>(li, 8 * g), mK = tile_at<kMmaMP>(li, 4 * g), mT = tile_at<kMmaMP>(4 * g + (li >> 2), 4 * (li & 3));
   constexpr int R16 = 16 * PC * 16, M16 = 16 * kMmaMP * 16;
 
   // B and C of the block, for all heads
@@ -313,8 +315,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
   __syncthreads();
 
   // the wave's score tiles (it, jt <= it): C_i . B_j, rows j and columns i, the same for every head
-  const int its[3] = {wave < 2 ? 3 : wave == 2 ? 2 : 1, wave < 2 ? 3 : wave == 2 ? 2 : 1, wave == 2 ? 2 : 0};
-  const int jts[3] = {wave == 1 ? 2 : 0, wave == 1 ? 3 : 1, wave == 2 ? 2 : 0};
+  const auto tile_i = [&](int u) { return u < 2 ? (wave < 2 ? 3 : wave == 2 ? 2 : 1) : (wave == 2 ? 2 : 0); };
+  const auto tile_j = [&](int u) { return u < 2 ? (wave == 1 ? 2 + u : u) : (wave == 2 ? 2 : 0); };
   hf4 cb[3];
 #pragma unroll
   for (int u = 0; u < 3; ++u) {
@@ -322,7 +324,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
     if (u == 2 && wave < 2) continue;
 #pragma unroll
     for (int k = 0; k < NK; ++k)
-      cb[u] = mfma(lds8(sB + jts[u] * R16 + (aN ^ (k << 6))), lds8(sC + its[u] * R16 + (aN ^ (k << 6))), cb[u]);
+      cb[u] = mfma(lds8(sB + tile_j(u) * R16 + (aN ^ (k << 6))), lds8(sC + tile_i(u) * R16 + (aN ^ (k << 6))), cb[u]);
   }
   hf4 dB[4][NTW], dC[4][NTW];  // [token 16 t + 4g + r][n = 16 nt + li]
 #pragma unroll
@@ -335,6 +337,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
   float qs = 0.0f, ps = 0.0f, dg = 0.0f, wd = 0.0f, qi = 0.0f, pi = 0.0f, e0 = 0.0f;
   for (int h = h0; h < h1; ++h)
     for (int pb = 0; pb < q.npb; ++pb) {
+      asm volatile("" : "+v"(aN), "+v"(aT), "+v"(mN), "+v"(mK), "+v"(mT), "+v"(lane), "+v"(li), "+v"(g), "+v"(wv));
+      wave = __builtin_amdgcn_readfirstlane(wv);
       // the state and its adjoint: rows p = 16 wave + li, columns 32 k + 8 g ..
       const int64_t srow = ((rho * hp.H + h) * q.npb + pb) * (64 * G::NP) + (16 * wave + li) * G::NP + 8 * g;
       hf4 s[NK][2];
@@ -371,17 +375,13 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         if (lane == 0) re[4] = exp2_hw(static_cast<float>(last));
       }
       __syncthreads();
-      {
-        const int hn = pb + 1 < q.npb ? h : h + 1, pn = pb + 1 < q.npb ? pb + 1 : 0;
-        if (hn < h1) load(hn, pn);
-      }
       // scores dy_i . x_j; the tiles of delta M (for dx) now, those of delta W d (for dB, dC) later
       hb4 m2[3];
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
         m2[u] = none;
         if (u == 2 && wave < 2) continue;
-        const int it = its[u], jt = jts[u], i = 16 * it + li, j = 16 * jt + 4 * g;
+        const int it = tile_i(u), jt = tile_j(u), i = 16 * it + li, j = 16 * jt + 4 * g;
         hf4 w = {0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -428,6 +428,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         *reinterpret_cast<hb4*>(sM + it * M16 + (mK ^ (jt << 5))) = to_bf4(m1);
         m2[u] = to_bf4(w2);
       }
+      __builtin_amdgcn_sched_barrier(0);
       // h C for q, in three parts; h's first part to LDS for dC
       hf4 acc[4];
 #pragma unroll
@@ -460,6 +461,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         a[k][0] = *reinterpret_cast<const hf4*>(q.gs + srow + 32 * k);
         a[k][1] = *reinterpret_cast<const hf4*>(q.gs + srow + 32 * k + 4);
       }
+      __builtin_amdgcn_sched_barrier(0);
       // dx within the block: rows p = 16 wave + 4g + r, columns j = 16 jt + li
       hf4 dx[4];
 #pragma unroll
@@ -477,6 +479,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
           dx[jt] = mfma(yt, m, dx[jt]);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
       // dC from the state
 #pragma unroll
       for (int n = 0; n < NTW; ++n) {
@@ -502,7 +505,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
         if (u == 2 && wave < 2) continue;
-        *reinterpret_cast<hb4*>(sM + its[u] * M16 + (mK ^ (jts[u] << 5))) = m2[u];
+        *reinterpret_cast<hb4*>(sM + tile_i(u) * M16 + (mK ^ (tile_j(u) << 5))) = m2[u];
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[t] = hf4{0, 0, 0, 0};
@@ -528,6 +531,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       dot += __shfl_xor(dot, 16);
       dot += __shfl_xor(dot, 32);
       if (lane == 0) re[wave] = dot;
+      __builtin_amdgcn_sched_barrier(0);
       const float Dh = hp.D != nullptr ? hp.D[h] : 0.0f;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -552,6 +556,10 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         }
       }
       __syncthreads();
+      {  // the next tiles' loads, now that the adjoint has left its registers
+        const int hn = pb + 1 < q.npb ? h : h + 1, pn = pb + 1 < q.npb ? pb + 1 : 0;
+        if (hn < h1) load(hn, pn);
+      }
       // dB and dC: from the adjoint, and within the block
 #pragma unroll
       for (int n = 0; n < NTW; ++n) {
