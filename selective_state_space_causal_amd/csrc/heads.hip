@@ -193,7 +193,7 @@ int launch_states(const StateArgs& q, const HeadPar& hp, int nk, int dirs, bool 
     constexpr bool VEC = decltype(v)::value;
     const int rc = allow_lds(&k_heads_states<NK, VEC>, StateGeo<NK>::bytes);
     if (rc != MM_OK) return rc;
-    const dim3 grid(static_cast<unsigned>(q.rows * q.pairs), static_cast<unsigned>(dirs));
+    const dim3 grid(static_cast<unsigned>(q.rows * hp.H * q.npb), static_cast<unsigned>(dirs));
     if (grid.x > 0)
       hipLaunchKernelGGL((k_heads_states<NK, VEC>), grid, dim3(kMmaThreads), StateGeo<NK>::bytes, st, q, hp);
     return MM_OK;
@@ -239,10 +239,8 @@ int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* stat
     s.v[0] = q.B;
     s.P = q.P;
     s.N = q.N;
+    s.G = a.G;
     s.npb = q.npb;
-    s.vper = q.vper;
-    s.ppg = q.ppg;
-    s.pairs = q.pairs;
     s.rows = q.rows;
     s.Ls = q.Ls;
     s.carry[0] = q.carry;
@@ -308,10 +306,8 @@ int launch_backward_mma(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads
   s.v[1] = C;
   s.P = a.P;
   s.N = a.N;
+  s.G = a.G;
   s.npb = p.npb;
-  s.vper = div * p.npb;
-  s.ppg = static_cast<int>(cdiv(s.vper, 2));
-  s.pairs = s.ppg * a.G;
   s.rows = p.rows;
   s.Ls = p.Ls;
   s.init[0] = o.state_in;

@@ -27,12 +27,14 @@ namespace mm {
 
 struct StateArgs {
   Tok<uint16_t> u[2], v[2];   // forward x, B; reverse dy, C
-  int P, N, npb, vper, ppg, pairs;
+  int P, N, G, npb;
   int64_t rows, Ls;
   const float* init[2];       // [S] states, or NULL: zeros
   float* carry[2];            // [rows] states: written by local runs, else read where a sequence has several segments
   float* decay[2];            // [rows, H] log2 of a segment's decay, written by local runs
-  float* store[2];            // [rows64, H npb, 64, NP]: the states at the blocks' starts / ends, or NULL
+  // [rows64, H npb] states at the blocks' starts / ends, or NULL: element (p, n) of a 64-channel block at
+  // ((p / 16) NP + n / 4 * 4) 16 + (p % 16) 4 + n % 4, the order of the accumulators
+  float* store[2];
   float* fin[2];              // [S] final states, or NULL
   int local;                  // from zero, over all segments but a sequence's last (reverse: first)
 };
@@ -40,12 +42,12 @@ struct StateArgs {
 template <int NK>
 struct StateGeo {
   static constexpr int NP = NK * 32, PC = NP / 8;
-  static constexpr int B = 0, X = kMmaTok * NP * 2, F = X + kMmaTok * kMmaCols * 2, bytes = F + 2 * (2 * kMmaTok + 4) * 4;
+  static constexpr int B = 0, X = kMmaTok * NP * 2, F = X + kMmaTok * kMmaTok * 2, bytes = F + 2 * (kMmaTok + 4) * 4;
 };
 
-// grid: (row, pair of head blocks) x direction
+// grid: (row, 64-channel block) x direction; a wave takes 16 of the channels
 template <int NK, bool VEC>
-__global__ __launch_bounds__(kMmaThreads, 2) void k_heads_states(StateArgs q, HeadPar hp) {
+__global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, HeadPar hp) {
   typedef StateGeo<NK> G;
   constexpr int NT = 2 * NK, PC = G::PC;
   extern __shared__ __align__(16) char lds[];
@@ -55,80 +57,65 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_states(StateArgs q, He
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int dir = blockIdx.y;
-  const int pair = blockIdx.x % q.pairs;
-  const int64_t rho = blockIdx.x / q.pairs;
+  const int vh = blockIdx.x % (hp.H * q.npb);
+  const int64_t rho = blockIdx.x / (hp.H * q.npb);
   const Segment sg = segment_of(hp.cu, hp.S, rho, q.Ls);
   const bool many = sg.many(q.Ls);
   if (sg.none(rho, q.Ls)) return;
   if (q.local && (!many || (dir ? sg.first() : sg.last()))) return;
   const Tok<uint16_t> tu = q.u[dir], tv = q.v[dir];
 
-  const int group = pair / q.ppg, blk = wave >> 1;
-  const int in_group = 2 * (pair % q.ppg);
-  const bool have = in_group + blk < q.vper;
-  const int vh = group * q.vper + in_group + (have ? blk : 0);
-  const int h = vh / q.npb, p0 = (vh % q.npb) * 64;
+  const int h = vh / q.npb, p0 = (vh % q.npb) * 64, group = h / (hp.H / q.G);
   const int pw = q.P - p0 < 64 ? q.P - p0 : 64;
-  const int col0 = (wave & 1) * 32;
+  const int p = 16 * wave + li;  // the lane's channel in the block
   const int64_t PN = static_cast<int64_t>(q.P) * q.N, set = hp.H * PN;
 
-  hf4 st[NT][2];
+  hf4 st[NT];  // [n = 16 nt + 4g + r][channel p]
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int ct = 0; ct < 2; ++ct) st[nt][ct] = hf4{0, 0, 0, 0};
+  for (int nt = 0; nt < NT; ++nt) st[nt] = hf4{0, 0, 0, 0};
   if (!q.local) {
     const float* from = many ? q.carry[dir] + rho * set : (q.init[dir] ? q.init[dir] + sg.s * set : nullptr);
-    if (from != nullptr && have)
+    if (from != nullptr && p < pw)
 #pragma unroll
-      for (int ct = 0; ct < 2; ++ct) {
-        const int p = col0 + 16 * ct + li;
-        if (p < pw)
+      for (int nt = 0; nt < NT; ++nt) {
+        const int n = 16 * nt + 4 * g;
+        const float* a = from + h * PN + static_cast<int64_t>(p0 + p) * q.N + n;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int n = 16 * nt + 4 * g;
-            const float* a = from + h * PN + static_cast<int64_t>(p0 + p) * q.N + n;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (n + r < q.N) st[nt][ct][r] = a[r];
-          }
+        for (int r = 0; r < 4; ++r)
+          if (n + r < q.N) st[nt][r] = a[r];
       }
   }
 
   const int brow = tid / PC, bcol = (tid % PC) * 8;
   constexpr int bstep = kMmaThreads / PC;
-  const int xrow = tid >> 4, xcol = (tid & 15) * 8, xv = group * q.vper + in_group + (xcol >> 6);
-  const int xin = (xv % q.npb) * 64 + (xcol & 63);
-  const int xn = in_group + (xcol >> 6) < q.vper ? q.P - xin : 0, bn = q.N - bcol;
+  const int xrow = tid >> 3, xcol = (tid & 7) * 8, xn = pw - xcol, bn = q.N - bcol;
   const int dH = hp.H * q.P, gn = (hp.H / tv.div) * q.N;
   const int b_off = (brow * static_cast<int>(tv.ts) + group * q.N + bcol) * 2;
-  const int x_off = (xrow * static_cast<int>(tu.ts) + (xv / q.npb) * q.P + xin) * 2;
-  hu4 rB[NK], rX[4];
+  const int x_off = (xrow * static_cast<int>(tu.ts) + h * q.P + p0 + xcol) * 2;
+  hu4 rB[NK], rX[2];
   const auto load = [&](int64_t tb, int cnt) {
     const hbuf bB = token_rows(tv.p, tb, tv.ts, cnt, gn), bX = token_rows(tu.p, tb, tu.ts, cnt, dH);
 #pragma unroll
     for (int i = 0; i < NK; ++i) rB[i] = load8<VEC>(bB, b_off + i * bstep * static_cast<int>(tv.ts) * 2, bn);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rX[i] = load8<VEC>(bX, x_off + i * 16 * static_cast<int>(tu.ts) * 2, xn);
+    for (int i = 0; i < 2; ++i) rX[i] = load8<VEC>(bX, x_off + i * 32 * static_cast<int>(tu.ts) * 2, xn);
   };
-  // wave 0: the weights of block 0, wave 1: of block 1, a chunk ahead
-  const bool dhave = in_group + wave < q.vper;
-  const int dh = (group * q.vper + in_group + (dhave ? wave & 1 : 0)) / q.npb;
-  const float A2 = head_A2(hp, dh), bias = hp.dt != nullptr ? hp.dt_bias[dh] : 0.0f;
+  // wave 0 makes the tokens' weights, a chunk ahead
+  const float A2 = head_A2(hp, h), bias = hp.dt != nullptr ? hp.dt_bias[h] : 0.0f;
   uint32_t rdt = 0;
   double dsum = 0.0;
   const auto load_dt = [&](int64_t tb, int cnt) {
-    if (wave < 2 && hp.dt != nullptr && lane < cnt)
-      rdt = static_cast<const uint16_t*>(hp.dt)[(tb + lane) * hp.dt_ts + dh];
+    if (wave == 0 && hp.dt != nullptr && lane < cnt)
+      rdt = static_cast<const uint16_t*>(hp.dt)[(tb + lane) * hp.dt_ts + h];
   };
   const auto factors = [&](int cnt, int fs) {
-    if (wave >= 2) return;
-    const float del = !dhave || lane >= cnt ? 0.0f : hp.dt == nullptr ? 1.0f : softplus(io_value<uint16_t>(rdt) + bias);
+    if (wave != 0) return;
+    const float del = lane >= cnt ? 0.0f : hp.dt == nullptr ? 1.0f : softplus(io_value<uint16_t>(rdt) + bias);
     const double c = lane_scan(static_cast<double>(fmaxf(del * A2, -512.0f)));  // (2^-512 is 0 in float32)
     const double last = last_lane(c);
-    float* f = sF + fs * (2 * kMmaTok + 4);
-    f[wave * kMmaTok + lane] = dir ? exp2_hw(static_cast<float>(c)) : exp2_hw(static_cast<float>(last - c)) * del;
-    if (lane == 0) f[2 * kMmaTok + wave] = exp2_hw(static_cast<float>(last));
+    float* f = sF + fs * (kMmaTok + 4);
+    f[lane] = dir ? exp2_hw(static_cast<float>(c)) : exp2_hw(static_cast<float>(last - c)) * del;
+    if (lane == 0) f[kMmaTok] = exp2_hw(static_cast<float>(last));
     dsum += last;
   };
   // the segment's blocks of the packed stream, in the direction's order
@@ -151,8 +138,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_states(StateArgs q, He
     load_dt(tn, cn);
   }
   int aT = tile_at<PC>(4 * g + (li >> 2), 4 * (li & 3));
-  int xT = tile_at<kMmaXP>(4 * g + (li >> 2), 8 * (8 * blk + (col0 >> 3)) + 4 * (li & 3));
-  constexpr int R16 = 16 * PC * 16, X16 = 16 * kMmaXP * 16;
+  int xT = tile_at<kMmaMP>(4 * g + (li >> 2), 16 * wave + 4 * (li & 3));
+  constexpr int R16 = 16 * PC * 16, X16 = 16 * kMmaMP * 16;
   for (int64_t k = 0; k < nb; ++k) {
     const int64_t b = block(k, tb, cnt);
     asm volatile("" : "+v"(aT), "+v"(xT));
@@ -161,11 +148,10 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_states(StateArgs q, He
 #pragma unroll
     for (int i = 0; i < NK; ++i) *reinterpret_cast<hu4*>(sB + tile_at<PC>(brow + i * bstep, bcol)) = rB[i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<hu4*>(sX + tile_at<kMmaXP>(xrow + 16 * i, xcol)) = rX[i];
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<hu4*>(sX + tile_at<kMmaMP>(xrow + 32 * i, xcol)) = rX[i];
     __syncthreads();
-    const float* const fs = sF + (k & 1) * (2 * kMmaTok + 4);
-    const float* const f = fs + blk * kMmaTok;
-    const float el = fs[2 * kMmaTok + blk];
+    const float* const f = sF + (k & 1) * (kMmaTok + 4);
+    const float el = f[kMmaTok];
     block(k + 1, tn, cn);
     if (VEC && k + 1 < nb) load(tn, cn);
     factors(cn, (k + 1) & 1);
@@ -175,57 +161,41 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_states(StateArgs q, He
       block(k + 2, t2, c2);
       load_dt(t2, c2);
     }
-    if (q.store[dir] != nullptr && have) {
-      float* o = q.store[dir] + (((sg.s + b) * hp.H + h) * q.npb + (vh % q.npb)) * (64 * G::NP);
+    if (q.store[dir] != nullptr) {  // as it lies in the registers: 1024 contiguous bytes a tile
+      float* o = q.store[dir] + ((sg.s + b) * hp.H * q.npb + vh) * (64 * G::NP) + wave * (16 * G::NP) + lane * 4;
 #pragma unroll
-      for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          *reinterpret_cast<hf4*>(o + (col0 + 16 * ct + li) * G::NP + 16 * nt + 4 * g) = st[nt][ct];
+      for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<hf4*>(o + 256 * nt) = st[nt];
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct) st[nt][ct] *= el;
+    for (int nt = 0; nt < NT; ++nt) st[nt] *= el;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const hf4 w0 = *reinterpret_cast<const hf4*>(f + 32 * ks + 4 * g);
       const hf4 w1 = *reinterpret_cast<const hf4*>(f + 32 * ks + 16 + 4 * g);
-      hb8 part[2][3];
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct) {
-        const char* a = sX + 2 * ks * X16 + (xT ^ (ct << 5));
-        weighted_parts(join(tr_read(a), tr_read(a + X16)), w0, w1, part[ct]);
-      }
+      const char* a = sX + 2 * ks * X16 + xT;
+      hb8 part[3];
+      weighted_parts(join(tr_read(a), tr_read(a + X16)), w0, w1, part);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const char* a = sB + 2 * ks * R16 + (aT ^ (nt << 5));
         const hb8 bt = join(tr_read(a), tr_read(a + R16));
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          st[nt][0] = mfma(bt, part[0][u], st[nt][0]);
-          st[nt][1] = mfma(bt, part[1][u], st[nt][1]);
-        }
+        for (int u = 0; u < 3; ++u) st[nt] = mfma(bt, part[u], st[nt]);
       }
     }
   }
   float* to = q.local ? q.carry[dir] + rho * set
                       : ((dir ? sg.first() : sg.last()) && q.fin[dir] != nullptr ? q.fin[dir] + sg.s * set : nullptr);
-  if (to != nullptr && have)
+  if (to != nullptr && p < pw)
 #pragma unroll
-    for (int ct = 0; ct < 2; ++ct) {
-      const int p = col0 + 16 * ct + li;
-      if (p < pw)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = 16 * nt + 4 * g;
+      float* a = to + h * PN + static_cast<int64_t>(p0 + p) * q.N + n;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int n = 16 * nt + 4 * g;
-          float* a = to + h * PN + static_cast<int64_t>(p0 + p) * q.N + n;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < q.N) a[r] = st[nt][ct][r];
-        }
+      for (int r = 0; r < 4; ++r)
+        if (n + r < q.N) a[r] = st[nt][r];
     }
-  if (q.local && wave < 2 && lane == 0 && dhave) q.decay[dir][rho * hp.H + dh] = static_cast<float>(dsum);
+  if (q.local && wave == 0 && lane == 0 && p0 == 0) q.decay[dir][rho * hp.H + h] = static_cast<float>(dsum);
 }
 
 struct GradArgs {
@@ -340,12 +310,12 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       asm volatile("" : "+v"(aN), "+v"(aT), "+v"(mN), "+v"(mK), "+v"(mT), "+v"(lane), "+v"(li), "+v"(g), "+v"(wv));
       wave = __builtin_amdgcn_readfirstlane(wv);
       // the state and its adjoint: rows p = 16 wave + li, columns 32 k + 8 g ..
-      const int64_t srow = ((rho * hp.H + h) * q.npb + pb) * (64 * G::NP) + (16 * wave + li) * G::NP + 8 * g;
+      const int64_t srow = ((rho * hp.H + h) * q.npb + pb) * (64 * G::NP) + wave * (16 * G::NP) + (g >> 1) * 256 + (g & 1) * 128 + li * 4;
       hf4 s[NK][2];
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        s[k][0] = *reinterpret_cast<const hf4*>(q.hs + srow + 32 * k);
-        s[k][1] = *reinterpret_cast<const hf4*>(q.hs + srow + 32 * k + 4);
+        s[k][0] = *reinterpret_cast<const hf4*>(q.hs + srow + 512 * k);
+        s[k][1] = *reinterpret_cast<const hf4*>(q.hs + srow + 512 * k + 64);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -458,8 +428,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       hf4 a[NK][2];
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        a[k][0] = *reinterpret_cast<const hf4*>(q.gs + srow + 32 * k);
-        a[k][1] = *reinterpret_cast<const hf4*>(q.gs + srow + 32 * k + 4);
+        a[k][0] = *reinterpret_cast<const hf4*>(q.gs + srow + 512 * k);
+        a[k][1] = *reinterpret_cast<const hf4*>(q.gs + srow + 512 * k + 64);
       }
       __builtin_amdgcn_sched_barrier(0);
       // dx within the block: rows p = 16 wave + 4g + r, columns j = 16 jt + li
