@@ -187,15 +187,14 @@ int by_steps(int nk, bool vec, F f) {
   return go(std::integral_constant<int, 4>{});
 }
 
+template <bool LOCAL>
 int launch_states(const StateArgs& q, const HeadPar& hp, int nk, int dirs, bool vec, hipStream_t st) {
   return by_steps(nk, vec, [&](auto k, auto v) -> int {
     constexpr int NK = decltype(k)::value;
     constexpr bool VEC = decltype(v)::value;
-    const int rc = allow_lds(&k_heads_states<NK, VEC>, StateGeo<NK>::bytes);
-    if (rc != MM_OK) return rc;
     const dim3 grid(static_cast<unsigned>(q.rows * hp.H * q.npb), static_cast<unsigned>(dirs));
     if (grid.x > 0)
-      hipLaunchKernelGGL((k_heads_states<NK, VEC>), grid, dim3(kMmaThreads), StateGeo<NK>::bytes, st, q, hp);
+      hipLaunchKernelGGL((k_heads_states<NK, VEC, LOCAL>), grid, dim3(kMmaThreads), StateGeo<NK>::bytes, st, q, hp);
     return MM_OK;
   });
 }
@@ -245,8 +244,7 @@ int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* stat
     s.Ls = q.Ls;
     s.carry[0] = q.carry;
     s.decay[0] = reinterpret_cast<float*>(ws + p.off_decay);
-    s.local = 1;
-    const int rc = launch_states(s, a.hp, p.nk, 1, vec, st);
+    const int rc = launch_states<true>(s, a.hp, p.nk, 1, vec, st);
     if (rc != MM_OK) return rc;
     launch_carry(q.carry, s.decay[0], state_in, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, false, st);
   }
@@ -317,17 +315,15 @@ int launch_backward_mma(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads
     s.decay[0] = at(p.off_decay);
     s.carry[1] = at(p.off_carry2);
     s.decay[1] = at(p.off_decay2);
-    s.local = 1;
-    const int rc = launch_states(s, a.hp, p.nk, 2, vec, st);
+    const int rc = launch_states<true>(s, a.hp, p.nk, 2, vec, st);
     if (rc != MM_OK) return rc;
-    s.local = 0;
     launch_carry(s.carry[0], s.decay[0], s.init[0], a.hp, PN, p.Ls, false, st);
     launch_carry(s.carry[1], s.decay[1], s.init[1], a.hp, PN, p.Ls, true, st);
   }
   s.store[0] = at(p.off_hb);
   s.store[1] = at(p.off_gs);
   s.fin[1] = o.dstate_in;
-  int rc = launch_states(s, a.hp, p.nk, 2, vec, st);
+  int rc = launch_states<false>(s, a.hp, p.nk, 2, vec, st);
   if (rc != MM_OK) return rc;
   if (T > 0) {
     const GradArgs g{x, dy, B, C, a.P, a.N, p.npb, a.G, p.splits, s.store[0], s.store[1], static_cast<uint16_t*>(o.dx),

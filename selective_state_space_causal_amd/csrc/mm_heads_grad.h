@@ -32,11 +32,10 @@ struct StateArgs {
   const float* init[2];       // [S] states, or NULL: zeros
   float* carry[2];            // [rows] states: written by local runs, else read where a sequence has several segments
   float* decay[2];            // [rows, H] log2 of a segment's decay, written by local runs
-  // [rows64, H npb] states at the blocks' starts / ends, or NULL: element (p, n) of a 64-channel block at
+  // [rows64, H npb] states at the blocks' starts / ends (not by local runs): element (p, n) of a 64-channel block at
   // ((p / 16) NP + n / 4 * 4) 16 + (p % 16) 4 + n % 4, the order of the accumulators
   float* store[2];
   float* fin[2];              // [S] final states, or NULL
-  int local;                  // from zero, over all segments but a sequence's last (reverse: first)
 };
 
 template <int NK>
@@ -46,7 +45,10 @@ struct StateGeo {
 };
 
 // grid: (row, 64-channel block) x direction; a wave takes 16 of the channels
-template <int NK, bool VEC>
+// LOCAL: from zero, over all segments but a sequence's last (reverse: first); else the whole walk, which stores.
+// (The two are told apart at compile time so that the stores' place among the outstanding accesses is known: a wait
+// for the tile loads then leaves the stores in flight.)
+template <int NK, bool VEC, bool LOCAL>
 __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, HeadPar hp) {
   typedef StateGeo<NK> G;
   constexpr int NT = 2 * NK, PC = G::PC;
@@ -62,7 +64,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   const Segment sg = segment_of(hp.cu, hp.S, rho, q.Ls);
   const bool many = sg.many(q.Ls);
   if (sg.none(rho, q.Ls)) return;
-  if (q.local && (!many || (dir ? sg.first() : sg.last()))) return;
+  if (LOCAL && (!many || (dir ? sg.first() : sg.last()))) return;
   const Tok<uint16_t> tu = q.u[dir], tv = q.v[dir];
 
   const int h = vh / q.npb, p0 = (vh % q.npb) * 64, group = h / (hp.H / q.G);
@@ -73,7 +75,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   hf4 st[NT];  // [n = 16 nt + 4g + r][channel p]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) st[nt] = hf4{0, 0, 0, 0};
-  if (!q.local) {
+  if (!LOCAL) {
     const float* from = many ? q.carry[dir] + rho * set : (q.init[dir] ? q.init[dir] + sg.s * set : nullptr);
     if (from != nullptr && p < pw)
 #pragma unroll
@@ -161,7 +163,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
       block(k + 2, t2, c2);
       load_dt(t2, c2);
     }
-    if (q.store[dir] != nullptr) {  // as it lies in the registers: 1024 contiguous bytes a tile
+    if (!LOCAL) {  // as it lies in the registers: 1024 contiguous bytes a tile
       float* o = q.store[dir] + ((sg.s + b) * hp.H * q.npb + vh) * (64 * G::NP) + wave * (16 * G::NP) + lane * 4;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<hf4*>(o + 256 * nt) = st[nt];
@@ -184,7 +186,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
       }
     }
   }
-  float* to = q.local ? q.carry[dir] + rho * set
+  float* to = LOCAL ? q.carry[dir] + rho * set
                       : ((dir ? sg.first() : sg.last()) && q.fin[dir] != nullptr ? q.fin[dir] + sg.s * set : nullptr);
   if (to != nullptr && p < pw)
 #pragma unroll
@@ -195,7 +197,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
       for (int r = 0; r < 4; ++r)
         if (n + r < q.N) a[r] = st[nt][r];
     }
-  if (q.local && wave == 0 && lane == 0 && p0 == 0) q.decay[dir][rho * hp.H + h] = static_cast<float>(dsum);
+  if (LOCAL && wave == 0 && lane == 0 && p0 == 0) q.decay[dir][rho * hp.H + h] = static_cast<float>(dsum);
 }
 
 struct GradArgs {
