@@ -353,13 +353,22 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
     {
       // C . B for 16 x 16 tiles (it, jt <= it), M of both blocks from it.  Below the diagonal's tiles the decay is
       // split at the end of tile jt, both parts <= 1: one exponential for each token instead of one for each pair.
-      const auto tile = [&](auto it_, auto jt_) {
+      // All of a wave's products and factors come before its first write: a read from LDS is not moved over a write.
+      const auto product = [&](auto it_, auto jt_) {  // rows j, columns i
         constexpr int it = decltype(it_)::value, jt = decltype(jt_)::value;
         hf4 raw = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < NK; ++k)  // rows j, columns i
+        for (int k = 0; k < NK; ++k)
           raw = mfma(lds8(sB + jt * R16 + (aN ^ (k << 6))), lds8(sC + it * R16 + (aN ^ (k << 6))), raw);
+        return raw;
+      };
+      struct Pair {
+        hb4 b[2];
+      };
+      const auto decayed = [&](auto it_, auto jt_, hf4 raw) {
+        constexpr int it = decltype(it_)::value, jt = decltype(jt_)::value;
         const int i = 16 * it + li, j = 16 * jt + 4 * g;
+        Pair o;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const float* d = fs + b * (kFn * kMmaTok);
@@ -376,26 +385,41 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
               m[r] = 4 * g + r <= li ? v : 0.0f;
             }
           }
-          *reinterpret_cast<hb4*>(lds + G::M + b * (kMmaTok * kMmaTok * 2) + it * M16 + (mK ^ (jt << 5))) = to_bf4(m);
+          o.b[b] = to_bf4(m);
         }
+        return o;
+      };
+      const auto keep = [&](auto it_, auto jt_, Pair m) {
+        constexpr int it = decltype(it_)::value, jt = decltype(jt_)::value;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          *reinterpret_cast<hb4*>(lds + G::M + b * (kMmaTok * kMmaTok * 2) + it * M16 + (mK ^ (jt << 5))) = m.b[b];
       };
       constexpr auto n0 = std::integral_constant<int, 0>{};
       constexpr auto n1 = std::integral_constant<int, 1>{};
       constexpr auto n2 = std::integral_constant<int, 2>{};
       constexpr auto n3 = std::integral_constant<int, 3>{};
+      const auto two = [&](auto i0, auto j0, auto i1, auto j1) {
+        const hf4 r0 = product(i0, j0), r1 = product(i1, j1);
+        const Pair m0 = decayed(i0, j0, r0), m1 = decayed(i1, j1, r1);
+        keep(i0, j0, m0), keep(i1, j1, m1);
+      };
+      const auto three = [&](auto i0, auto j0, auto i1, auto j1, auto i2, auto j2) {
+        const hf4 r0 = product(i0, j0), r1 = product(i1, j1), r2 = product(i2, j2);
+        const Pair m0 = decayed(i0, j0, r0), m1 = decayed(i1, j1, r1), m2 = decayed(i2, j2, r2);
+        keep(i0, j0, m0), keep(i1, j1, m1), keep(i2, j2, m2);
+      };
       if (wave == 0) {
-        tile(n3, n0), tile(n3, n1);
-        factors(tb + kMmaTok, par);
-        load_dt(tb + 2 * kMmaTok);
+        two(n3, n0, n3, n1);
       } else if (wave == 1) {
-        tile(n3, n2), tile(n3, n3);
-        factors(tb + kMmaTok, par);
-        load_dt(tb + 2 * kMmaTok);
+        two(n3, n2, n3, n3);
       } else if (wave == 2) {
-        tile(n2, n0), tile(n2, n1), tile(n2, n2);
+        three(n2, n0, n2, n1, n2, n2);
       } else {
-        tile(n1, n0), tile(n1, n1), tile(n0, n0);
+        three(n1, n0, n1, n1, n0, n0);
       }
+      factors(tb + kMmaTok, par);
+      load_dt(tb + 2 * kMmaTok);
       __builtin_amdgcn_sched_barrier(0);
       // h0 C
 #pragma unroll
@@ -457,17 +481,16 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
           }
       }
       // + D x, to bfloat16 in the x tile's place (the wave's own columns), and out in rows
+      hb4 xv4[4][2];  // (read before the first write)
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-          char* a = sX + it * X16 + (xK ^ (ct << 5));
-          const hf4 xv4 = to_f4(lds4(a));
-          hf4 o;
+        for (int ct = 0; ct < 2; ++ct) xv4[it][ct] = lds4(sX + it * X16 + (xK ^ (ct << 5)));
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(Dh, xv4[r], acc[it][ct][r]);
-          *reinterpret_cast<hb4*>(a) = to_bf4(o);
-        }
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+          *reinterpret_cast<hb4*>(sX + it * X16 + (xK ^ (ct << 5))) = to_bf4(to_f4(xv4[it][ct]) * Dh + acc[it][ct]);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       const hbuf bY = token_rows(q.y, tb, dH, cnt, dH);
