@@ -33,6 +33,7 @@ struct HeadsPlan {
   bool mma;        // the matrix-core kernels
   bool whole;      // every sequence is one segment
   int64_t rows;    // segments at most
+  int64_t walks;   // matrix-core kernels: sequences, or stretches of Ls tokens
   int64_t rows64;  // 64-token blocks at most (backward)
   int nrp, nrn;    // 16-row blocks of P and N
   size_t off_carry, off_decay, off_carry2, off_decay2, off_hb, off_dots, off_dB, off_dC, off_q, off_r, off_delta,
@@ -61,13 +62,16 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   p.Ls = std::max<int64_t>(256, cdiv(cdiv(T, std::max<int64_t>(want, 1)), kHeadsBlock) * kHeadsBlock);
   if (want <= S || p.Ls >= T) p.Ls = (T / kHeadsBlock + 1) * kHeadsBlock;
   if (p.mma) {
-    // Few long sequences are cut until about kMmaWorkgroups workgroups walk at once; a segment's state
-    // costs as much traffic as 128 tokens of it, so none is shorter than 1024 tokens.  Measured at 16384
-    // packed tokens, d 4096: segments of 512 tokens 274 us, 1024 261, 2048 310, whole sequences 342.
+    // Whole sequences where they alone give the GPU its workgroups twice over (the backward, whose two walks store
+    // every block's state, is as fast with one per CU: 8 x 2048 tokens, 24 heads, 415 us whole, 490 cut); else
+    // stretches of equal length, as many as the GPU runs workgroups at once (two walks per CU, of two 64-channel blocks, or four state
+    // walks of one), so that all end together.  A stretch's state costs as much traffic as 128 tokens of it: none is
+    // shorter than 512 tokens.
     const int64_t pairs = H > 0 ? G * cdiv(H / G * cdiv(P, 64), 2) : 1;
-    const int64_t want_m = cdiv(kMmaWorkgroups, pairs);
-    p.Ls = std::max<int64_t>(1024, cdiv(cdiv(T, want_m), kMmaTok) * kMmaTok);
-    if (want_m <= S || p.Ls >= T) p.Ls = (T / kMmaTok + 1) * kMmaTok;
+    const int64_t walks = std::max<int64_t>(1, 2 * kCUs / pairs);
+    const bool whole = backward ? S * H * cdiv(P, 64) * 2 >= kCUs : S * pairs >= kMmaWorkgroups;
+    p.Ls = std::max<int64_t>(512, cdiv(cdiv(T, walks), kMmaTok) * kMmaTok);
+    if (whole || p.Ls >= T) p.Ls = (T / kMmaTok + 1) * kMmaTok;
   }
   p.whole = p.Ls > T;
   p.npb = static_cast<int>(cdiv(P, 64));
@@ -76,6 +80,7 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   p.splits = H > 0 ? static_cast<int>(std::max<int64_t>(
                  1, std::min<int64_t>(H / G, cdiv(2 * kCUs, std::max<int64_t>(segment_rows(S, T, kHeadsBlock) * G, 1))))) : 1;
   p.rows = segment_rows(S, T, p.Ls);
+  p.walks = p.whole ? S : cdiv(T, p.Ls);
   p.rows64 = segment_rows(S, T, kHeadsBlock);
   const size_t set = static_cast<size_t>(H) * P * N * 4;
   const size_t th = static_cast<size_t>(T) * H;
@@ -145,12 +150,12 @@ void launch_seq(const SeqRun<IO>& q, const HeadPar& hp, int64_t rows, hipStream_
   else hipLaunchKernelGGL((k_heads_seq<IO, 16, REV, LOCAL>), grid, block, 0, st, q, hp);
 }
 
-void launch_carry(float* carry, const float* decay, const float* init, const HeadPar& hp, int64_t PN, int64_t Ls,
-                  bool reverse, hipStream_t st) {
+void launch_carry(float* carry, const float* decay, const float* init, float* fin, const HeadPar& hp, int64_t PN,
+                  int64_t Ls, bool reverse, bool all, hipStream_t st) {
   for (int s0 = 0; s0 < hp.S; s0 += 65535)
     hipLaunchKernelGGL(k_heads_carry, dim3(static_cast<unsigned>(cdiv(hp.H * PN, 256)),
                                            static_cast<unsigned>(std::min(hp.S - s0, 65535))),
-                       dim3(256), 0, st, carry, decay, init, hp.cu, hp.H, PN, Ls, reverse ? 1 : 0, s0);
+                       dim3(256), 0, st, carry, decay, init, fin, hp.cu, hp.H, PN, Ls, reverse ? 1 : 0, all ? 1 : 0, s0);
 }
 
 struct HeadsArgs {
@@ -188,26 +193,27 @@ int by_steps(int nk, bool vec, F f) {
 }
 
 template <bool LOCAL>
-int launch_states(const StateArgs& q, const HeadPar& hp, int nk, int dirs, bool vec, hipStream_t st) {
+int launch_states(const StateArgs& q, const HeadPar& hp, int64_t rows, int nk, int dirs, bool vec, hipStream_t st) {
   return by_steps(nk, vec, [&](auto k, auto v) -> int {
     constexpr int NK = decltype(k)::value;
     constexpr bool VEC = decltype(v)::value;
-    const dim3 grid(static_cast<unsigned>(q.rows * hp.H * q.npb), static_cast<unsigned>(dirs));
+    const dim3 grid(static_cast<unsigned>(rows * hp.H * q.npb), static_cast<unsigned>(dirs));
     if (grid.x > 0)
       hipLaunchKernelGGL((k_heads_states<NK, VEC, LOCAL>), grid, dim3(kMmaThreads), StateGeo<NK>::bytes, st, q, hp);
     return MM_OK;
   });
 }
 
-int launch_mma(const MmaArgs& q, const HeadPar& hp, int nk, bool vec, hipStream_t st) {
+template <int PARTS>
+int launch_mma(const MmaArgs& q, const HeadPar& hp, int64_t rows, int nk, bool vec, hipStream_t st) {
   return by_steps(nk, vec, [&](auto k, auto v) -> int {
     constexpr int NK = decltype(k)::value;
     constexpr bool VEC = decltype(v)::value;
-    const int rc = allow_lds(&k_heads_mma<NK, VEC>, MmaGeo<NK>::bytes);
+    const int rc = allow_lds(&k_heads_mma<NK, PARTS, VEC>, MmaGeo<NK>::bytes);
     if (rc != MM_OK) return rc;
-    const dim3 grid(static_cast<unsigned>(q.rows * q.pairs));
+    const dim3 grid(static_cast<unsigned>(rows * q.pairs));
     if (grid.x > 0)
-      hipLaunchKernelGGL((k_heads_mma<NK, VEC>), grid, dim3(kMmaThreads), MmaGeo<NK>::bytes, st, q, hp);
+      hipLaunchKernelGGL((k_heads_mma<NK, PARTS, VEC>), grid, dim3(kMmaThreads), MmaGeo<NK>::bytes, st, q, hp);
     return MM_OK;
   });
 }
@@ -225,30 +231,31 @@ int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* stat
   q.vper = div * q.npb;
   q.ppg = static_cast<int>(cdiv(q.vper, 2));
   q.pairs = q.ppg * a.G;
-  q.rows = p.rows;
   q.Ls = p.Ls;
   q.state_in = state_in;
   q.state_out = state_out;
   q.y = static_cast<uint16_t*>(y);
   const bool vec = heads_vec(a, {state_in, state_out, y});
-  if (!p.whole) {
-    q.carry = reinterpret_cast<float*>(ws + p.off_carry);
-    StateArgs s{};
-    s.u[0] = q.x;
-    s.v[0] = q.B;
-    s.P = q.P;
-    s.N = q.N;
-    s.G = a.G;
-    s.npb = q.npb;
-    s.rows = q.rows;
-    s.Ls = q.Ls;
-    s.carry[0] = q.carry;
-    s.decay[0] = reinterpret_cast<float*>(ws + p.off_decay);
-    const int rc = launch_states<true>(s, a.hp, p.nk, 1, vec, st);
-    if (rc != MM_OK) return rc;
-    launch_carry(q.carry, s.decay[0], state_in, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, false, st);
+  if (p.whole) {
+    const int rc = launch_mma<3>(q, a.hp, p.walks, p.nk, vec, st);
+    return rc != MM_OK ? rc : launched();
   }
-  const int rc = launch_mma(q, a.hp, p.nk, vec, st);
+  StateArgs s{};
+  s.u[0] = q.x;
+  s.v[0] = q.B;
+  s.P = q.P;
+  s.N = q.N;
+  s.G = a.G;
+  s.npb = q.npb;
+  s.Ls = q.Ls;
+  s.carry[0] = reinterpret_cast<float*>(ws + p.off_carry);
+  s.decay[0] = reinterpret_cast<float*>(ws + p.off_decay);
+  s.all = 1;
+  q.carry = s.carry[0];
+  int rc = launch_states<true>(s, a.hp, p.walks, p.nk, 1, vec, st);
+  if (rc != MM_OK) return rc;
+  launch_carry(s.carry[0], s.decay[0], state_in, state_out, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, false, true, st);
+  rc = launch_mma<1>(q, a.hp, p.walks, p.nk, vec, st);
   return rc != MM_OK ? rc : launched();
 }
 
@@ -275,7 +282,7 @@ int launch_prefill(const HeadsPlan& p, const HeadsArgs& a, const float* state_in
     q.carry = reinterpret_cast<float*>(ws + p.off_carry);
     q.decay = reinterpret_cast<float*>(ws + p.off_decay);
     launch_seq<IO, false, true>(q, a.hp, p.rows, st);
-    launch_carry(q.carry, q.decay, state_in, a.hp, q.sh, p.Ls, false, st);
+    launch_carry(q.carry, q.decay, state_in, nullptr, a.hp, q.sh, p.Ls, false, false, st);
   }
   launch_seq<IO, false, false>(q, a.hp, p.rows, st);
   return launched();
@@ -306,8 +313,8 @@ int launch_backward_mma(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads
   s.N = a.N;
   s.G = a.G;
   s.npb = p.npb;
-  s.rows = p.rows;
   s.Ls = p.Ls;
+  s.whole = p.whole ? 1 : 0;
   s.init[0] = o.state_in;
   s.init[1] = o.dstate_out;
   if (!p.whole) {
@@ -315,15 +322,15 @@ int launch_backward_mma(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads
     s.decay[0] = at(p.off_decay);
     s.carry[1] = at(p.off_carry2);
     s.decay[1] = at(p.off_decay2);
-    const int rc = launch_states<true>(s, a.hp, p.nk, 2, vec, st);
+    const int rc = launch_states<true>(s, a.hp, p.walks, p.nk, 2, vec, st);
     if (rc != MM_OK) return rc;
-    launch_carry(s.carry[0], s.decay[0], s.init[0], a.hp, PN, p.Ls, false, st);
-    launch_carry(s.carry[1], s.decay[1], s.init[1], a.hp, PN, p.Ls, true, st);
+    launch_carry(s.carry[0], s.decay[0], s.init[0], nullptr, a.hp, PN, p.Ls, false, false, st);
+    launch_carry(s.carry[1], s.decay[1], s.init[1], o.dstate_in, a.hp, PN, p.Ls, true, false, st);
   }
   s.store[0] = at(p.off_hb);
   s.store[1] = at(p.off_gs);
   s.fin[1] = o.dstate_in;
-  int rc = launch_states<false>(s, a.hp, p.nk, 2, vec, st);
+  int rc = launch_states<false>(s, a.hp, p.walks, p.nk, 2, vec, st);
   if (rc != MM_OK) return rc;
   if (T > 0) {
     const GradArgs g{x, dy, B, C, a.P, a.N, p.npb, a.G, p.splits, s.store[0], s.store[1], static_cast<uint16_t*>(o.dx),
@@ -401,9 +408,9 @@ int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o,
     b.carry = d.carry = reinterpret_cast<float*>(ws + p.off_carry2);
     b.decay = d.decay = reinterpret_cast<float*>(ws + p.off_decay2);
     launch_seq<IO, false, true>(c, a.hp, p.rows, st);
-    launch_carry(c.carry, c.decay, o.state_in, a.hp, set, p.Ls, false, st);
+    launch_carry(c.carry, c.decay, o.state_in, nullptr, a.hp, set, p.Ls, false, false, st);
     launch_seq<IO, true, true>(d, a.hp, p.rows, st);
-    launch_carry(d.carry, d.decay, o.dstate_out, a.hp, set, p.Ls, true, st);
+    launch_carry(d.carry, d.decay, o.dstate_out, nullptr, a.hp, set, p.Ls, true, false, st);
   }
   launch_seq<IO, false, false>(c, a.hp, p.rows, st);
   launch_seq<IO, true, false>(d, a.hp, p.rows, st);

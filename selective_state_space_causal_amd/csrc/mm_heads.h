@@ -59,6 +59,33 @@ __device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ cu, in
   g.t1 = (b + 1) * L < g.seq1 ? (b + 1) * L : g.seq1;
   return g;
 }
+// The segments that a workgroup of the matrix-core kernels walks: with `whole`, sequence `row` (Ls > T); else all
+// segments of the packed stream's tokens [row Ls, (row + 1) Ls), whatever sequences they belong to, so that every
+// workgroup has the same number of tokens.
+struct SegmentWalk {
+  const int32_t* cu;
+  int S, s;
+  int64_t row, L;
+  bool whole;
+  __device__ SegmentWalk(const int32_t* cu_, int S_, int64_t row_, int64_t L_, bool whole_)
+      : cu(cu_), S(S_), s(whole_ ? static_cast<int>(row_) : seq_of(cu_, S_, row_ * L_)), row(row_), L(L_), whole(whole_) {}
+  // the next segment and its row of the per-segment arrays; false: none
+  __device__ bool next(Segment& g, int64_t& rho) {
+    const int64_t lo = whole ? 0 : row * L, hi = whole ? INT32_MAX : (row + 1) * L;
+    while (s < S) {
+      g.s = s;
+      g.seq0 = cu[s];
+      g.seq1 = cu[s + 1];
+      if (g.seq0 >= hi) return false;
+      s = whole ? S : s + 1;
+      g.t0 = g.seq0 > lo ? g.seq0 : lo;
+      g.t1 = g.seq1 < hi ? g.seq1 : hi;
+      rho = g.s + (whole ? 0 : row);
+      if (whole || g.t0 < g.t1) return true;
+    }
+    return false;
+  }
+};
 // rows of a per-segment array for S sequences and T tokens
 inline int64_t segment_rows(int64_t S, int64_t T, int64_t L) { return S + T / L; }
 
@@ -242,27 +269,44 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar
 }
 
 // The states that the segments of a sequence start from, in place of what they add: one thread per
-// state element of a sequence with several segments, segment after segment.  reverse: from the last.
+// state element of a sequence, segment after segment (four loads ahead).  reverse: from the last.
+// all == 0: the sequences with several segments, whose last segment added nothing, and fin (if not NULL) only of
+// empty sequences; else all sequences, all of whose segments added, and the final states of all.  fin may be init.
 __global__ __launch_bounds__(256) void k_heads_carry(float* __restrict__ carry, const float* __restrict__ decay,
-                                                     const float* __restrict__ init, const int32_t* __restrict__ cu,
-                                                     int H, int64_t PN, int64_t Ls, int reverse, int s0) {
+                                                     const float* init, float* fin, const int32_t* __restrict__ cu, int H,
+                                                     int64_t PN, int64_t Ls, int reverse, int all, int s0) {
   const int s = s0 + blockIdx.y;
-  const int64_t seq0 = cu[s], seq1 = cu[s + 1];
-  if (seq1 <= seq0 || (seq1 - 1) / Ls <= seq0 / Ls) return;
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t set = H * PN;
   if (e >= set) return;
+  const uint32_t L = static_cast<uint32_t>(Ls), seq0 = cu[s], seq1 = cu[s + 1];
+  const int n = seq1 > seq0 ? static_cast<int>((seq1 - 1) / L - seq0 / L) + 1 : 0;
+  if (!all && n == 0 && fin != nullptr) fin[s * set + e] = init != nullptr ? init[s * set + e] : 0.0f;
+  if (!all && n < 2) return;
   const int h = static_cast<int>(e / PN);
-  const int64_t r0 = s + seq0 / Ls, r1 = s + (seq1 - 1) / Ls;
+  const int64_t r0 = s + static_cast<int64_t>(seq0 / L), step = reverse ? -1 : 1;
+  int64_t rho = reverse ? r0 + n - 1 : r0;
   float cur = init != nullptr ? init[s * set + e] : 0.0f;
-  for (int64_t i = 0; i <= r1 - r0; ++i) {
-    const int64_t rho = reverse ? r1 - i : r0 + i;
-    float* slot = carry + rho * set + e;
-    float local = 0.0f;
-    if (i < r1 - r0) local = *slot;
-    *slot = cur;
-    if (i < r1 - r0) cur = __builtin_fmaf(exp2_hw(decay[rho * H + h]), cur, local);
+  const int added = all ? n : n - 1;  // segments whose shares are there
+  for (int i = 0; i < n; i += 4) {
+    float local[4], a[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      local[k] = a[k] = 0.0f;
+      if (i + k < added) {
+        local[k] = carry[(rho + k * step) * set + e];
+        a[k] = decay[(rho + k * step) * H + h];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < n) {
+        carry[rho * set + e] = cur;
+        rho += step;
+        cur = __builtin_fmaf(exp2_hw(a[k]), cur, local[k]);
+      }
   }
+  if (all) fin[s * set + e] = cur;
 }
 
 // ------------------------------------------------------------------------------------ decode

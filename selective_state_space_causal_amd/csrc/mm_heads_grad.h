@@ -28,7 +28,8 @@ namespace mm {
 struct StateArgs {
   Tok<uint16_t> u[2], v[2];   // forward x, B; reverse dy, C
   int P, N, G, npb;
-  int64_t rows, Ls;
+  int64_t Ls;
+  int whole;                  // Ls > T
   const float* init[2];       // [S] states, or NULL: zeros
   float* carry[2];            // [rows] states: written by local runs, else read where a sequence has several segments
   float* decay[2];            // [rows, H] log2 of a segment's decay, written by local runs
@@ -36,6 +37,7 @@ struct StateArgs {
   // ((p / 16) NP + n / 4 * 4) 16 + (p % 16) 4 + n % 4, the order of the accumulators
   float* store[2];
   float* fin[2];              // [S] final states, or NULL
+  int all;                    // local runs: every segment, not only those that another one follows
 };
 
 template <int NK>
@@ -45,7 +47,7 @@ struct StateGeo {
 };
 
 // grid: (row, 64-channel block) x direction; a wave takes 16 of the channels
-// LOCAL: from zero, over all segments but a sequence's last (reverse: first); else the whole walk, which stores.
+// LOCAL: what a segment adds to a zero state; else the whole walk, which stores.
 // (The two are told apart at compile time so that the stores' place among the outstanding accesses is known: a wait
 // for the tile loads then leaves the stores in flight.)
 template <int NK, bool VEC, bool LOCAL>
@@ -60,11 +62,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int dir = blockIdx.y;
   const int vh = blockIdx.x % (hp.H * q.npb);
-  const int64_t rho = blockIdx.x / (hp.H * q.npb);
-  const Segment sg = segment_of(hp.cu, hp.S, rho, q.Ls);
-  const bool many = sg.many(q.Ls);
-  if (sg.none(rho, q.Ls)) return;
-  if (LOCAL && (!many || (dir ? sg.first() : sg.last()))) return;
+  SegmentWalk walk(hp.cu, hp.S, blockIdx.x / (hp.H * q.npb), q.Ls, q.whole != 0);
   const Tok<uint16_t> tu = q.u[dir], tv = q.v[dir];
 
   const int h = vh / q.npb, p0 = (vh % q.npb) * 64, group = h / (hp.H / q.G);
@@ -72,6 +70,11 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   const int p = 16 * wave + li;  // the lane's channel in the block
   const int64_t PN = static_cast<int64_t>(q.P) * q.N, set = hp.H * PN;
 
+  Segment sg;
+  int64_t rho;
+  while (walk.next(sg, rho)) {
+  const bool many = sg.many(q.Ls);
+  if (LOCAL && !q.all && (!many || (dir ? sg.first() : sg.last()))) continue;
   hf4 st[NT];  // [n = 16 nt + 4g + r][channel p]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) st[nt] = hf4{0, 0, 0, 0};
@@ -198,6 +201,8 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
         if (n + r < q.N) a[r] = st[nt][r];
     }
   if (LOCAL && wave == 0 && lane == 0 && p0 == 0) q.decay[dir][rho * hp.H + h] = static_cast<float>(dsum);
+  __syncthreads();  // the last chunk's weights are read until here
+  }
 }
 
 struct GradArgs {
@@ -408,7 +413,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         hb8 part[3];
-        split3(s[k][0], s[k][1], part);
+        bf_parts(s[k][0], s[k][1], part);
         *reinterpret_cast<hb8*>(sS + wave * R16 + (aN ^ (k << 6))) = part[0];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -490,7 +495,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
           dot = __builtin_fmaf(s[k][1][r], a[k][1][r], dot);
         }
         hb8 part[3];
-        split3(a[k][0], a[k][1], part);
+        bf_parts(a[k][0], a[k][1], part);
         *reinterpret_cast<hb8*>(sS + wave * R16 + (aN ^ (k << 6))) = part[0];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {

@@ -15,8 +15,10 @@
 // 16 lanes) give from their natural layout.
 //
 // Precision: x, B and C are exact operands; M and h0 are rounded to bfloat16 for their products, whose
-// sums are float32 and leave in bfloat16.  The state itself is a float32 result: the products that
-// update it take e^{..} delta x in three bfloat16 parts (24 bits).
+// sums are float32 and leave in bfloat16.  Where the walk makes the final states, float32 results, the
+// products that update the state take e^{..} delta x in three bfloat16 parts (PARTS = 3: 24 bits).
+// Where sequences are cut into segments, the states between them and at the ends come from
+// k_heads_states with that precision, this walk's state serves y alone, and one part does.
 #pragma once
 
 #include <type_traits>
@@ -47,10 +49,10 @@ struct MmaArgs {
   int vper;    // such blocks per group
   int ppg;     // pairs of them per group
   int pairs;   // in all
-  int64_t rows, Ls;
+  int64_t Ls;
   const float* state_in;
   float* state_out;
-  float* carry;
+  const float* carry;  // [rows] the states of the segments' starts, or NULL: whole sequences from state_in
   uint16_t* y;
 };
 
@@ -121,14 +123,15 @@ __device__ __forceinline__ double last_lane(double v) {
   return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-// eight float32 as three bfloat16 parts, whose sum has all 24 bits (of a value that is not finite the first part
+// eight float32 as bfloat16 parts; the sum of three has all 24 bits (of a value that is not finite the first part
 // says so and the others are NaN or zero)
-__device__ __forceinline__ void split3(hf4 a, hf4 b, hb8 (&part)[3]) {
+template <int PARTS>
+__device__ __forceinline__ void bf_parts(hf4 a, hf4 b, hb8 (&part)[PARTS]) {
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
     float v[2] = {e < 4 ? a[e & 3] : b[e & 3], e < 4 ? a[(e + 1) & 3] : b[(e + 1) & 3]};
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < PARTS; ++k) {
       const hb2 o = to_bf2(v[0], v[1]);
       part[k][e] = o[0];
       part[k][e + 1] = o[1];
@@ -138,14 +141,15 @@ __device__ __forceinline__ void split3(hf4 a, hf4 b, hb8 (&part)[3]) {
   }
 }
 // the same of w x, the weights of the operand's K indices in w0 and w1
-__device__ __forceinline__ void weighted_parts(hb8 x, hf4 w0, hf4 w1, hb8 (&part)[3]) {
+template <int PARTS>
+__device__ __forceinline__ void weighted_parts(hb8 x, hf4 w0, hf4 w1, hb8 (&part)[PARTS]) {
   hf4 a, b;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     a[e] = w0[e] * static_cast<float>(x[e]);
     b[e] = w1[e] * static_cast<float>(x[4 + e]);
   }
-  split3(a, b, part);
+  bf_parts(a, b, part);
 }
 
 // Rows of a token tensor from token tb on as a range-checked buffer: rows from `cnt` on read as zeros (and
@@ -188,7 +192,7 @@ __device__ __forceinline__ uint32_t not_finite(hu4 v) {
   return f;
 }
 
-template <int NK, bool VEC>
+template <int NK, int PARTS, bool VEC>
 __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar hp) {
   typedef MmaGeo<NK> G;
   constexpr int NT = 2 * NK, PC = G::PC;
@@ -197,13 +201,11 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   float* const sF = reinterpret_cast<float*>(lds + G::F);  // two sets: this chunk's and the next one's
   int* const sFlag = reinterpret_cast<int*>(sF + 2 * kMmaFSet);
 
-  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x;
+  int lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pair = blockIdx.x % q.pairs;
-  const int64_t rho = blockIdx.x / q.pairs;
-  const Segment sg = segment_of(hp.cu, hp.S, rho, q.Ls);
-  const bool many = sg.many(q.Ls);
-  if (sg.none(rho, q.Ls)) return;
+  SegmentWalk walk(hp.cu, hp.S, blockIdx.x / q.pairs, q.Ls, PARTS == 3);
 
   // the wave's block of head channels, and where its columns lie
   const int group = pair / q.ppg, blk = wave >> 1;
@@ -217,13 +219,16 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   char* const sM = lds + G::M + blk * (kMmaTok * kMmaTok * 2);
   const float Dh = hp.D != nullptr ? hp.D[h] : 0.0f;
 
+  Segment sg;
+  int64_t rho;
+  while (walk.next(sg, rho)) {
   hf4 st[NT][2];  // the state: [n = 16 nt + 4g + r][column 16 ct + li]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) st[nt][ct] = hf4{0, 0, 0, 0};
   {
-    const float* from = many ? q.carry + rho * set : (q.state_in ? q.state_in + sg.s * set : nullptr);
+    const float* from = q.carry != nullptr ? q.carry + rho * set : (q.state_in ? q.state_in + sg.s * set : nullptr);
     if (from != nullptr && have)
 #pragma unroll
       for (int ct = 0; ct < 2; ++ct) {
@@ -327,7 +332,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   for (int64_t tb = sg.t0; tb < sg.t1; tb += kMmaTok) {
     const int cnt = static_cast<int>(sg.t1 - tb < kMmaTok ? sg.t1 - tb : kMmaTok);
     if (!VEC) load(tb);  // element by element: too many registers to hold ahead
-    asm volatile("" : "+v"(aN), "+v"(aK), "+v"(aT), "+v"(xT), "+v"(xK), "+v"(xN), "+v"(mK));
+    asm volatile("" : "+v"(aN), "+v"(aK), "+v"(aT), "+v"(xT), "+v"(xK), "+v"(xN), "+v"(mK), "+v"(lane), "+v"(li), "+v"(g));
     __syncthreads();
     if (tid == 0) sFlag[par ^ 1] = 0;
 #pragma unroll
@@ -512,7 +517,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
     for (int ks = 0; ks < 2; ++ks) {
       const hf4 w0 = *reinterpret_cast<const hf4*>(f + kFw * kMmaTok + 32 * ks + 4 * g);
       const hf4 w1 = *reinterpret_cast<const hf4*>(f + kFw * kMmaTok + 32 * ks + 16 + 4 * g);
-      hb8 part[2][3];
+      hb8 part[2][PARTS];
 #pragma unroll
       for (int ct = 0; ct < 2; ++ct) weighted_parts(xt[ks][ct], w0, w1, part[ct]);
 #pragma unroll
@@ -520,14 +525,14 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
         const char* a = sB + 2 * ks * R16 + (aT ^ (nt << 5));
         const hb8 bt = join(tr_read(a), tr_read(a + R16));
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
+        for (int k = 0; k < PARTS; ++k) {
           st[nt][0] = mfma(bt, part[0][k], st[nt][0]);
           st[nt][1] = mfma(bt, part[1][k], st[nt][1]);
         }
       }
     }
   }
-  float* to = sg.last() ? q.state_out + sg.s * set : nullptr;
+  float* to = PARTS == 3 && sg.last() ? q.state_out + sg.s * set : nullptr;
   if (to != nullptr && have)
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
@@ -546,6 +551,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
           }
         }
     }
+  if (PARTS != 3) __syncthreads();  // the last chunk's factors are read until here
+  }
 }
 
 }  // namespace mm
