@@ -41,9 +41,9 @@ struct HeadsPlan {
   int npb, nk, splits;  // matrix-core backward: 64-channel blocks per head, 32-column steps of N, shares of a group's heads
 };
 
-// A workgroup of the sequential kernels walks one segment, about 0.1 us a token, so few long
-// sequences are cut until some four workgroups are on every CU; segments shorter than 256 tokens
-// are not worth their states.
+// A workgroup of the sequential kernels walks one segment, about 0.13 us a token, so few long sequences are cut until
+// some four workgroups are on every CU, down to 64 tokens (777 tokens in 8 sequences, 6 heads: segments of 256 tokens
+// 87 us, of 64 30 us).
 constexpr int64_t kSeqWorkgroups = 1024;
 
 // The matrix-core kernels take bfloat16 io and N <= 128.  Their workgroups take two 64-channel blocks of
@@ -59,7 +59,7 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   p.nrn = static_cast<int>(cdiv(N, kSeqRows));
   const int64_t per = static_cast<int64_t>(H) * (backward ? std::min(p.nrp, p.nrn) : p.nrp);
   const int64_t want = cdiv(kSeqWorkgroups, std::max<int64_t>(per, 1));
-  p.Ls = std::max<int64_t>(256, cdiv(cdiv(T, std::max<int64_t>(want, 1)), kHeadsBlock) * kHeadsBlock);
+  p.Ls = std::max<int64_t>(kHeadsBlock, cdiv(cdiv(T, std::max<int64_t>(want, 1)), kHeadsBlock) * kHeadsBlock);
   if (want <= S || p.Ls >= T) p.Ls = (T / kHeadsBlock + 1) * kHeadsBlock;
   if (p.mma) {
     // Whole sequences where they alone give the GPU its workgroups twice over (the backward, whose two walks store

@@ -8,17 +8,56 @@ the elements of a row are contiguous.
 """
 from __future__ import annotations
 
-import ctypes
+from . import MM_OK, MambaMixError, _check, _io_code, check_cu_seqlens, load
 
-from . import MM_OK, MambaMixError, _check, _io_code, _ptr, _stream, check_cu_seqlens, load
+torch = _BF16 = _F32 = _raw_stream = None  # (the package can be imported without torch)
+
+
+def _lib():
+    """The library; torch and its types are at hand from then on: calls of a few microseconds have no time for more."""
+    global torch, _BF16, _F32, _raw_stream
+    if torch is None:
+        import torch as t
+
+        torch, _BF16, _F32 = t, t.bfloat16, t.float32
+        _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None)
+    return load()
+
+
+def _need(t, shape, dtype, name):
+    """``_check`` with the answer yes found quickly."""
+    if not (t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        _check(t, shape, dtype, name)
+
+
+def _code(t) -> int:
+    return 1 if t.dtype is _BF16 else 0 if t.dtype is _F32 else _io_code(t)
 
 
 def _opt(t):
-    return _ptr(t) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
+
+
+def _on(stream, t):
+    """The raw stream a call goes to: the given one, or the current one of the tensor's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _rows(t, shape, dtype, name) -> int:
     """Check a token tensor [T, ...] whose rows may be strided; returns the row stride in elements."""
+    if t.shape == shape and t.dtype is dtype and t.is_cuda:
+        stride, width = t.stride(), 1
+        for n, s in zip(shape[:0:-1], stride[:0:-1]):
+            if n != 1 and s != width:
+                break
+            width *= n
+        else:
+            if width > 0 and (shape[0] <= 1 or stride[0] >= width):
+                return stride[0] if shape[0] > 1 else width
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
@@ -32,36 +71,31 @@ def _rows(t, shape, dtype, name) -> int:
         width *= n
     if t.shape[0] <= 1 or t.numel() == 0:
         return max(width, 1)
-    if t.stride(0) < width:
-        raise ValueError(f"{name}: rows must not overlap (stride {t.stride(0)}, row length {width})")
-    return t.stride(0)
+    raise ValueError(f"{name}: rows must not overlap (stride {t.stride(0)}, row length {width})")
 
 
 def _head_inputs(x, dt, B, C, A_log, D, dt_bias):
     """Checks of the inputs all three head-scan calls share; returns (T, H, P, G, N, strides)."""
-    import torch
-
     if x.dim() != 3 or B.dim() != 3:
         raise ValueError("x must be [T, H, P] and B [T, G, N]")
     T, H, P = x.shape
     G, N = B.shape[1], B.shape[2]
     io = x.dtype
-    _io_code(x)
+    _lib()
+    _code(x)
     strides = [_rows(x, (T, H, P), io, "x"), 0, _rows(B, (T, G, N), io, "B"), _rows(C, (T, G, N), io, "C")]
-    _check(A_log, (H,), torch.float32, "A_log")
+    _need(A_log, (H,), _F32, "A_log")
     if dt is not None:
         strides[1] = _rows(dt, (T, H), io, "dt")
         if dt_bias is None:
             raise ValueError("dt_bias: required with dt")
-        _check(dt_bias, (H,), torch.float32, "dt_bias")
+        _need(dt_bias, (H,), _F32, "dt_bias")
     if D is not None:
-        _check(D, (H,), torch.float32, "D")
+        _need(D, (H,), _F32, "D")
     return T, H, P, G, N, strides
 
 
 def _workspace(given, need, device):
-    import torch
-
     if given is None:
         given = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
     return given, _opt(given), 0 if given is None else given.numel() * given.element_size()
@@ -69,8 +103,6 @@ def _workspace(given, need, device):
 
 def _out(t, shape, dtype, device, name):
     """An output tensor: the caller's (rows may be strided) or a new one; returns it and its row stride."""
-    import torch
-
     if t is None:
         t = torch.empty(shape, dtype=dtype, device=device)
     return t, _rows(t, shape, dtype, name)
@@ -90,29 +122,30 @@ def heads_prefill(x, dt, B, C, A_log, D, dt_bias, cu_seqlens, state_in=None, sta
     state_in [S, H, P, N] float32 (None: zeros).  Returns (y [T, H, P], state_out [S, H, P, N]);
     pass state_out=state_in to update a state in place.
     """
-    import torch
-
     from . import CHECK_CU
 
     T, H, P, G, N, strides = _head_inputs(x, dt, B, C, A_log, D, dt_bias)
     S = cu_seqlens.shape[0] - 1
-    _check(cu_seqlens, (S + 1,), torch.int32, "cu_seqlens")
+    _need(cu_seqlens, (S + 1,), torch.int32, "cu_seqlens")
     if CHECK_CU:
         check_cu_seqlens(cu_seqlens, T)
     if state_in is not None:
-        _check(state_in, (S, H, P, N), torch.float32, "state_in")
+        _need(state_in, (S, H, P, N), _F32, "state_in")
     if state_out is None:
-        state_out = torch.empty((S, H, P, N), dtype=torch.float32, device=x.device)
-    _check(state_out, (S, H, P, N), torch.float32, "state_out")
+        state_out = torch.empty((S, H, P, N), dtype=_F32, device=x.device)
+    else:
+        _need(state_out, (S, H, P, N), _F32, "state_out")
     if y is None:
         y = torch.empty((T, H, P), dtype=x.dtype, device=x.device)
-    _check(y, (T, H, P), x.dtype, "y")
-    io = _io_code(x)
-    need = load().mamba_mixer_heads_prefill_workspace_bytes(S, T, H, P, G, N, io) if workspace is None else 0
+    else:
+        _need(y, (T, H, P), x.dtype, "y")
+    io = _code(x)
+    need = _lib().mamba_mixer_heads_prefill_workspace_bytes(S, T, H, P, G, N, io) if workspace is None else 0
     workspace, wptr, wbytes = _workspace(workspace, need, x.device)
-    rc = load().mamba_mixer_heads_prefill(
-        _ptr(x), _opt(dt), _ptr(B), _ptr(C), _ptr(A_log), _opt(D), _opt(dt_bias), _ptr(cu_seqlens), _opt(state_in),
-        _ptr(state_out), _ptr(y), S, T, H, P, G, N, io, *strides, wptr, wbytes, _stream(stream))
+    rc = _lib().mamba_mixer_heads_prefill(
+        x.data_ptr(), _opt(dt), B.data_ptr(), C.data_ptr(), A_log.data_ptr(), _opt(D), _opt(dt_bias),
+        cu_seqlens.data_ptr(), _opt(state_in), state_out.data_ptr(), y.data_ptr(), S, T, H, P, G, N, io, *strides,
+        wptr, wbytes, _on(stream, x))
     _raise(rc, "mamba_mixer_heads_prefill")
     return y, state_out
 
@@ -121,20 +154,20 @@ def heads_decode(x, dt, B, C, A_log, D, dt_bias, state_in=None, state_out=None, 
     """One token of the head scan for each of Bs rows (see ``mamba_mixer_heads_decode``): x [Bs, H, P],
     dt [Bs, H] or None, B, C [Bs, G, N], state_in [Bs, H, P, N] float32 (None: zeros).  Returns
     (y [Bs, H, P], state_out); pass state_out=state_in to update the states in place."""
-    import torch
-
     Bs, H, P, G, N, strides = _head_inputs(x, dt, B, C, A_log, D, dt_bias)
     if state_in is not None:
-        _check(state_in, (Bs, H, P, N), torch.float32, "state_in")
+        _need(state_in, (Bs, H, P, N), _F32, "state_in")
     if state_out is None:
-        state_out = torch.empty((Bs, H, P, N), dtype=torch.float32, device=x.device)
-    _check(state_out, (Bs, H, P, N), torch.float32, "state_out")
+        state_out = torch.empty((Bs, H, P, N), dtype=_F32, device=x.device)
+    else:
+        _need(state_out, (Bs, H, P, N), _F32, "state_out")
     if y is None:
         y = torch.empty((Bs, H, P), dtype=x.dtype, device=x.device)
-    _check(y, (Bs, H, P), x.dtype, "y")
-    rc = load().mamba_mixer_heads_decode(
-        _ptr(x), _opt(dt), _ptr(B), _ptr(C), _ptr(A_log), _opt(D), _opt(dt_bias), _opt(state_in), _ptr(state_out),
-        _ptr(y), Bs, H, P, G, N, _io_code(x), *strides, _stream(stream))
+    else:
+        _need(y, (Bs, H, P), x.dtype, "y")
+    rc = _lib().mamba_mixer_heads_decode(
+        x.data_ptr(), _opt(dt), B.data_ptr(), C.data_ptr(), A_log.data_ptr(), _opt(D), _opt(dt_bias),
+        _opt(state_in), state_out.data_ptr(), y.data_ptr(), Bs, H, P, G, N, _code(x), *strides, _on(stream, x))
     _raise(rc, "mamba_mixer_heads_decode")
     return y, state_out
 
@@ -146,46 +179,44 @@ def heads_backward(x, dt, B, C, A_log, D, dt_bias, cu_seqlens, state_in, dy, dst
     given (column ranges of one gradient, for instance).  Returns a dict of dx, ddt, dB, dC (io), dA_log, dD,
     ddt_bias and dstate_in (float32); ddt and ddt_bias are None without dt, dD without D, dstate_in with
     need_dstate=False."""
-    import torch
-
     from . import CHECK_CU
 
     T, H, P, G, N, strides = _head_inputs(x, dt, B, C, A_log, D, dt_bias)
     S = cu_seqlens.shape[0] - 1
     io, dev = x.dtype, x.device
-    _check(cu_seqlens, (S + 1,), torch.int32, "cu_seqlens")
+    _need(cu_seqlens, (S + 1,), torch.int32, "cu_seqlens")
     if CHECK_CU:
         check_cu_seqlens(cu_seqlens, T)
     for t, n in ((state_in, "state_in"), (dstate_out, "dstate_out")):
         if t is not None:
-            _check(t, (S, H, P, N), torch.float32, n)
-    _check(dy, (T, H, P), io, "dy")
+            _need(t, (S, H, P, N), _F32, n)
+    _need(dy, (T, H, P), io, "dy")
     dx, sx = _out(dx, (T, H, P), io, dev, "dx")
     ddt, sd = _out(ddt, (T, H), io, dev, "ddt") if dt is not None else (None, 0)
     dB, sb = _out(dB, (T, G, N), io, dev, "dB")
     dC, sc = _out(dC, (T, G, N), io, dev, "dC")
-    new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+    new = lambda *s: torch.empty(s, dtype=_F32, device=dev)  # noqa: E731
     dA_log, dD, dbias = new(H), new(H) if D is not None else None, new(H) if dt is not None else None
     dstate_in = new(S, H, P, N) if need_dstate else None
-    code = _io_code(x)
-    need = load().mamba_mixer_heads_backward_workspace_bytes(S, T, H, P, G, N, code) if workspace is None else 0
+    code = _code(x)
+    need = _lib().mamba_mixer_heads_backward_workspace_bytes(S, T, H, P, G, N, code) if workspace is None else 0
     workspace, wptr, wbytes = _workspace(workspace, need, dev)
-    rc = load().mamba_mixer_heads_backward(
-        _ptr(x), _opt(dt), _ptr(B), _ptr(C), _ptr(A_log), _opt(D), _opt(dt_bias), _ptr(cu_seqlens), _opt(state_in),
-        _ptr(dy), _opt(dstate_out), _ptr(dx), _opt(ddt), _ptr(dB), _ptr(dC), _ptr(dA_log), _opt(dD), _opt(dbias),
-        _opt(dstate_in), S, T, H, P, G, N, code, *strides, sx, sd, sb, sc, wptr, wbytes, _stream(stream))
+    rc = _lib().mamba_mixer_heads_backward(
+        x.data_ptr(), _opt(dt), B.data_ptr(), C.data_ptr(), A_log.data_ptr(), _opt(D), _opt(dt_bias),
+        cu_seqlens.data_ptr(), _opt(state_in), dy.data_ptr(), _opt(dstate_out), dx.data_ptr(), _opt(ddt),
+        dB.data_ptr(), dC.data_ptr(), dA_log.data_ptr(), _opt(dD), _opt(dbias), _opt(dstate_in), S, T, H, P, G, N,
+        code, *strides, sx, sd, sb, sc, wptr, wbytes, _on(stream, x))
     _raise(rc, "mamba_mixer_heads_backward")
     return dict(dx=dx, ddt=ddt, dB=dB, dC=dC, dA_log=dA_log, dD=dD, ddt_bias=dbias, dstate_in=dstate_in)
 
 
 def _gate_inputs(y, z, weight, groups):
-    import torch
-
     if y.dim() != 2:
         raise ValueError("y must be [rows, d]")
     rows, d = y.shape
-    _io_code(y)
-    _check(weight, (d,), torch.float32, "weight")
+    _lib()
+    _code(y)
+    _need(weight, (d,), _F32, "weight")
     return rows, d, _rows(y, (rows, d), y.dtype, "y"), _rows(z, (rows, d), y.dtype, "z")
 
 
@@ -193,14 +224,14 @@ def gate_norm(y, z, weight, groups: int = 1, eps: float = 1e-5, gate_first: bool
     """The norm after a mixer block, fused with its gate (see ``mamba_mixer_gate_norm``): with s = SiLU(z),
     weight n(y s) (gate_first) or weight n(y) s, n the root-mean-square norm of each of `groups` column
     ranges.  y, z [rows, d] io, weight [d] float32.  Returns out [rows, d]."""
-    import torch
-
     rows, d, ys, zs = _gate_inputs(y, z, weight, groups)
     if out is None:
         out = torch.empty((rows, d), dtype=y.dtype, device=y.device)
-    _check(out, (rows, d), y.dtype, "out")
-    rc = load().mamba_mixer_gate_norm(_ptr(y), _ptr(z), _ptr(weight), _ptr(out), rows, d, int(groups), float(eps),
-                                      1 if gate_first else 0, _io_code(y), ys, zs, _stream(stream))
+    else:
+        _need(out, (rows, d), y.dtype, "out")
+    rc = _lib().mamba_mixer_gate_norm(
+        y.data_ptr(), z.data_ptr(), weight.data_ptr(), out.data_ptr(), rows, d, int(groups), float(eps),
+        1 if gate_first else 0, _code(y), ys, zs, _on(stream, y))
     _raise(rc, "mamba_mixer_gate_norm")
     return out
 
@@ -209,38 +240,36 @@ def gate_norm_backward(dout, y, z, weight, groups: int = 1, eps: float = 1e-5, g
                        dz=None, workspace=None, stream=None):
     """The gradients of ``gate_norm`` from dout [rows, d]: (dy, dz, dweight); dy and dz may be given (with
     strided rows)."""
-    import torch
-
     rows, d, ys, zs = _gate_inputs(y, z, weight, groups)
-    _check(dout, (rows, d), y.dtype, "dout")
+    _need(dout, (rows, d), y.dtype, "dout")
     dy, dys = _out(dy, (rows, d), y.dtype, y.device, "dy")
     dz, dzs = _out(dz, (rows, d), y.dtype, y.device, "dz")
-    dweight = torch.empty(d, dtype=torch.float32, device=y.device)
-    need = load().mamba_mixer_gate_norm_backward_workspace_bytes(rows, d, int(groups)) if workspace is None else 0
+    dweight = torch.empty(d, dtype=_F32, device=y.device)
+    need = _lib().mamba_mixer_gate_norm_backward_workspace_bytes(rows, d, int(groups)) if workspace is None else 0
     workspace, wptr, wbytes = _workspace(workspace, need, y.device)
-    rc = load().mamba_mixer_gate_norm_backward(
-        _ptr(dout), _ptr(y), _ptr(z), _ptr(weight), _ptr(dy), _ptr(dz), _ptr(dweight), rows, d, int(groups), float(eps),
-        1 if gate_first else 0, _io_code(y), ys, zs, dys, dzs, wptr, wbytes, _stream(stream))
+    rc = _lib().mamba_mixer_gate_norm_backward(
+        dout.data_ptr(), y.data_ptr(), z.data_ptr(), weight.data_ptr(), dy.data_ptr(), dz.data_ptr(),
+        dweight.data_ptr(), rows, d, int(groups), float(eps), 1 if gate_first else 0, _code(y), ys, zs, dys, dzs,
+        wptr, wbytes, _on(stream, y))
     _raise(rc, "mamba_mixer_gate_norm_backward")
     return dy, dz, dweight
 
 
 def _residual_inputs(h, residual, weight, post_weight, scale_vec):
-    import torch
-
     if h.dim() != 2:
         raise ValueError("h must be [rows, d]")
     rows, d = h.shape
-    _check(h, (rows, d), h.dtype, "h")
-    _io_code(h)
+    _lib()
+    _need(h, (rows, d), h.dtype, "h")
+    _code(h)
     for t, n in ((weight, "weight"), (post_weight, "post_weight"), (scale_vec, "scale_vec")):
         if t is not None:
-            _check(t, (d,), torch.float32, n)
+            _need(t, (d,), _F32, n)
     res = residual.dtype if residual is not None else h.dtype
     if residual is not None:
-        if res not in (torch.float32, h.dtype):
+        if res is not _F32 and res is not h.dtype:
             raise TypeError(f"residual: expected float32 or {h.dtype}, got {res}")
-        _check(residual, (rows, d), res, "residual")
+        _need(residual, (rows, d), res, "residual")
     return rows, d, res
 
 
@@ -250,20 +279,20 @@ def residual_norm(h, residual, weight, post_weight=None, scale: float = 1.0, sca
     r' = residual + scale scale_vec p; out = weight n(r').  h [rows, d] io; residual [rows, d] float32 or h's
     type (None: zeros, of h's type); weight, post_weight, scale_vec [d] float32.  Returns (out, residual_out);
     pass residual_out=residual to update the residual in place."""
-    import torch
-
     rows, d, res = _residual_inputs(h, residual, weight, post_weight, scale_vec)
     if residual_out is None:
-        residual_out = torch.empty((rows, d), dtype=res, device=h.device)
-    elif residual is None:
-        res = residual_out.dtype
+        residual_out = torch.empty_like(h, dtype=res)
+    else:
+        if residual is None:
+            res = residual_out.dtype
+        _need(residual_out, (rows, d), res, "residual_out")
     if out is None:
-        out = torch.empty((rows, d), dtype=h.dtype, device=h.device)
-    _check(residual_out, (rows, d), res, "residual_out")
-    _check(out, (rows, d), h.dtype, "out")
-    rc = load().mamba_mixer_residual_norm(
-        _ptr(h), _opt(residual), _ptr(weight), _opt(post_weight), _opt(scale_vec), float(scale), _ptr(residual_out),
-        _ptr(out), rows, d, float(eps), _io_code(h), _io_code(residual_out), _stream(stream))
+        out = torch.empty_like(h)
+    else:
+        _need(out, (rows, d), h.dtype, "out")
+    rc = _lib().mamba_mixer_residual_norm(
+        h.data_ptr(), _opt(residual), weight.data_ptr(), _opt(post_weight), _opt(scale_vec), float(scale),
+        residual_out.data_ptr(), out.data_ptr(), rows, d, float(eps), _code(h), _code(residual_out), _on(stream, h))
     _raise(rc, "mamba_mixer_residual_norm")
     return out, residual_out
 
@@ -274,30 +303,31 @@ def residual_norm_backward(dout, dresidual_out, h, residual_out, weight, post_we
     """The gradients of ``residual_norm`` from dout [rows, d] and dresidual_out [rows, d] (None: zeros);
     residual_out is the new residual that the forward call returned.  Returns a dict of dresidual, dh, dweight
     and, with post_weight and scale_vec, dpost_weight and dscale_vec."""
-    import torch
-
     rows, d, res = _residual_inputs(h, residual_out, weight, post_weight, scale_vec)
-    _check(dout, (rows, d), h.dtype, "dout")
+    _need(dout, (rows, d), h.dtype, "dout")
     if dresidual_out is not None:
-        _check(dresidual_out, (rows, d), res, "dresidual_out")
+        _need(dresidual_out, (rows, d), res, "dresidual_out")
     if dresidual is None:
-        dresidual = torch.empty((rows, d), dtype=res, device=h.device)
+        dresidual = torch.empty_like(h, dtype=res)
+    else:
+        _need(dresidual, (rows, d), res, "dresidual")
     if dh is None:
-        dh = torch.empty((rows, d), dtype=h.dtype, device=h.device)
-    _check(dresidual, (rows, d), res, "dresidual")
-    _check(dh, (rows, d), h.dtype, "dh")
-    new = lambda: torch.empty(d, dtype=torch.float32, device=h.device)  # noqa: E731
+        dh = torch.empty_like(h)
+    else:
+        _need(dh, (rows, d), h.dtype, "dh")
+    new = lambda: torch.empty(d, dtype=_F32, device=h.device)  # noqa: E731
     got = dict(dresidual=dresidual, dh=dh, dweight=new())
     if post_weight is not None:
         got["dpost_weight"] = new()
     if scale_vec is not None:
         got["dscale_vec"] = new()
-    need = load().mamba_mixer_residual_norm_backward_workspace_bytes(rows, d) if workspace is None else 0
+    need = _lib().mamba_mixer_residual_norm_backward_workspace_bytes(rows, d) if workspace is None else 0
     workspace, wptr, wbytes = _workspace(workspace, need, h.device)
-    rc = load().mamba_mixer_residual_norm_backward(
-        _ptr(dout), _opt(dresidual_out), _ptr(h), _ptr(residual_out), _ptr(weight), _opt(post_weight), _opt(scale_vec),
-        float(scale), _ptr(dresidual), _ptr(dh), _ptr(got["dweight"]), _opt(got.get("dpost_weight")),
-        _opt(got.get("dscale_vec")), rows, d, float(eps), _io_code(h), _io_code(residual_out), wptr, wbytes,
-        _stream(stream))
+    rc = _lib().mamba_mixer_residual_norm_backward(
+        dout.data_ptr(), _opt(dresidual_out), h.data_ptr(), residual_out.data_ptr(), weight.data_ptr(),
+        _opt(post_weight), _opt(scale_vec), float(scale), dresidual.data_ptr(), dh.data_ptr(), got["dweight"].data_ptr(),
+        _opt(got.get("dpost_weight")),
+        _opt(got.get("dscale_vec")), rows, d, float(eps), _code(h), _code(residual_out), wptr, wbytes,
+        _on(stream, h))
     _raise(rc, "mamba_mixer_residual_norm_backward")
     return got
