@@ -37,7 +37,7 @@ struct HeadsPlan {
   int64_t rows64;  // 64-token blocks at most (backward)
   int nrp, nrn;    // 16-row blocks of P and N
   size_t off_carry, off_decay, off_carry2, off_decay2, off_hb, off_dots, off_dB, off_dC, off_q, off_r, off_delta,
-      off_sums, off_gs, total;
+      off_sums, off_gs, off_w, total;
   int npb, nk, splits;  // matrix-core backward: 64-channel blocks per head, 32-column steps of N, shares of a group's heads
 };
 
@@ -112,6 +112,7 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
     take(p.off_q, th * 4);
     take(p.off_r, th * 4);
     take(p.off_delta, th * 4);
+    take(p.off_w, th * 4);
     take(p.off_sums, static_cast<size_t>(p.rows64) * H * 3 * 4);
   }
   p.total = off;
@@ -150,12 +151,24 @@ void launch_seq(const SeqRun<IO>& q, const HeadPar& hp, int64_t rows, hipStream_
   else hipLaunchKernelGGL((k_heads_seq<IO, 16, REV, LOCAL>), grid, block, 0, st, q, hp);
 }
 
-void launch_carry(float* carry, const float* decay, const float* init, float* fin, const HeadPar& hp, int64_t PN,
-                  int64_t Ls, bool reverse, bool all, hipStream_t st) {
+// a forward and a reverse run of the same sizes in one launch
+template <typename IO, bool LOCAL>
+void launch_seq_both(const SeqRun<IO>& f, const SeqRun<IO>& r, const HeadPar& hp, int64_t rows, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(rows * hp.H * cdiv(f.R, kSeqRows)), 2), block(kSeqThreads);
+  if (grid.x == 0) return;
+  if (f.K <= 16) hipLaunchKernelGGL((k_heads_seq_both<IO, 1, LOCAL>), grid, block, 0, st, f, r, hp);
+  else if (f.K <= 32) hipLaunchKernelGGL((k_heads_seq_both<IO, 2, LOCAL>), grid, block, 0, st, f, r, hp);
+  else if (f.K <= 64) hipLaunchKernelGGL((k_heads_seq_both<IO, 4, LOCAL>), grid, block, 0, st, f, r, hp);
+  else if (f.K <= 128) hipLaunchKernelGGL((k_heads_seq_both<IO, 8, LOCAL>), grid, block, 0, st, f, r, hp);
+  else hipLaunchKernelGGL((k_heads_seq_both<IO, 16, LOCAL>), grid, block, 0, st, f, r, hp);
+}
+
+// dirs: 1, the forward states, or 2, the adjoints too
+void launch_carry(const Carry& c, const HeadPar& hp, int64_t PN, int64_t Ls, int dirs, bool all, hipStream_t st) {
   for (int s0 = 0; s0 < hp.S; s0 += 65535)
     hipLaunchKernelGGL(k_heads_carry, dim3(static_cast<unsigned>(cdiv(hp.H * PN, 256)),
-                                           static_cast<unsigned>(std::min(hp.S - s0, 65535))),
-                       dim3(256), 0, st, carry, decay, init, fin, hp.cu, hp.H, PN, Ls, reverse ? 1 : 0, all ? 1 : 0, s0);
+                                           static_cast<unsigned>(std::min(hp.S - s0, 65535)), static_cast<unsigned>(dirs)),
+                       dim3(256), 0, st, c, hp.cu, hp.H, PN, Ls, all ? 1 : 0, s0);
 }
 
 struct HeadsArgs {
@@ -254,7 +267,7 @@ int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* stat
   q.carry = s.carry[0];
   int rc = launch_states<true>(s, a.hp, p.walks, p.nk, 1, vec, st);
   if (rc != MM_OK) return rc;
-  launch_carry(s.carry[0], s.decay[0], state_in, state_out, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, false, true, st);
+  launch_carry({{s.carry[0]}, {s.decay[0]}, {state_in}, {state_out}}, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, 1, true, st);
   rc = launch_mma<1>(q, a.hp, p.walks, p.nk, vec, st);
   return rc != MM_OK ? rc : launched();
 }
@@ -282,7 +295,7 @@ int launch_prefill(const HeadsPlan& p, const HeadsArgs& a, const float* state_in
     q.carry = reinterpret_cast<float*>(ws + p.off_carry);
     q.decay = reinterpret_cast<float*>(ws + p.off_decay);
     launch_seq<IO, false, true>(q, a.hp, p.rows, st);
-    launch_carry(q.carry, q.decay, state_in, nullptr, a.hp, q.sh, p.Ls, false, false, st);
+    launch_carry({{q.carry}, {q.decay}, {state_in}, {nullptr}}, a.hp, q.sh, p.Ls, 1, false, st);
   }
   launch_seq<IO, false, false>(q, a.hp, p.rows, st);
   return launched();
@@ -324,8 +337,8 @@ int launch_backward_mma(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads
     s.decay[1] = at(p.off_decay2);
     const int rc = launch_states<true>(s, a.hp, p.walks, p.nk, 2, vec, st);
     if (rc != MM_OK) return rc;
-    launch_carry(s.carry[0], s.decay[0], s.init[0], nullptr, a.hp, PN, p.Ls, false, false, st);
-    launch_carry(s.carry[1], s.decay[1], s.init[1], o.dstate_in, a.hp, PN, p.Ls, true, false, st);
+    launch_carry({{s.carry[0], s.carry[1]}, {s.decay[0], s.decay[1]}, {s.init[0], s.init[1]}, {nullptr, o.dstate_in}}, a.hp,
+                 PN, p.Ls, 2, false, st);
   }
   s.store[0] = at(p.off_hb);
   s.store[1] = at(p.off_gs);
@@ -359,10 +372,11 @@ int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o,
   const int64_t T = a.hp.T, set = static_cast<int64_t>(a.P) * a.N;
   const Tok<IO> x = tok<IO>(a.x, a.x_ts, a.P, 1), dy = tok<IO>(o.dy, static_cast<int64_t>(H) * a.P, a.P, 1);
   const Tok<IO> B = tok<IO>(a.B, a.b_ts, a.N, div), C = tok<IO>(a.C, a.c_ts, a.N, div);
-  float* f[] = {reinterpret_cast<float*>(ws + p.off_hb), reinterpret_cast<float*>(ws + p.off_dots),
+  float* f32[] = {reinterpret_cast<float*>(ws + p.off_hb), reinterpret_cast<float*>(ws + p.off_dots),
                 reinterpret_cast<float*>(ws + p.off_dB), reinterpret_cast<float*>(ws + p.off_dC),
                 reinterpret_cast<float*>(ws + p.off_q), reinterpret_cast<float*>(ws + p.off_r),
-                reinterpret_cast<float*>(ws + p.off_delta), reinterpret_cast<float*>(ws + p.off_sums)};
+                reinterpret_cast<float*>(ws + p.off_delta), reinterpret_cast<float*>(ws + p.off_sums),
+                  reinterpret_cast<float*>(ws + p.off_w)};
   // dC (and the states at the blocks' ends): forward, the state transposed (rows N)
   SeqRun<IO> c{};
   c.u = B;
@@ -375,15 +389,15 @@ int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o,
   c.sh = set;
   c.init = o.state_in;
   c.Ls = p.Ls;
-  c.out32 = f[3];
-  c.store = f[0];
+  c.out32 = f32[3];
+  c.store = f32[0];
   // dB: reverse, the state transposed
   SeqRun<IO> b = c;
   b.u = C;
   b.v = dy;
   b.s = x;
   b.init = o.dstate_out;
-  b.out32 = f[2];
+  b.out32 = f32[2];
   b.store = nullptr;
   // dx, dstate_in and the inner products at the blocks' ends: reverse (rows P)
   SeqRun<IO> d = b;
@@ -400,31 +414,35 @@ int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o,
   d.out_ts = o.dx_ts;
   d.out_delta = 1;
   d.add_D = 1;
-  d.dots_with = f[0];
-  d.dots = f[1];
+  d.dots_with = f32[0];
+  d.dots = f32[1];
   if (!p.whole) {
     c.carry = reinterpret_cast<float*>(ws + p.off_carry);
     c.decay = reinterpret_cast<float*>(ws + p.off_decay);
     b.carry = d.carry = reinterpret_cast<float*>(ws + p.off_carry2);
     b.decay = d.decay = reinterpret_cast<float*>(ws + p.off_decay2);
-    launch_seq<IO, false, true>(c, a.hp, p.rows, st);
-    launch_carry(c.carry, c.decay, o.state_in, nullptr, a.hp, set, p.Ls, false, false, st);
-    launch_seq<IO, true, true>(d, a.hp, p.rows, st);
-    launch_carry(d.carry, d.decay, o.dstate_out, nullptr, a.hp, set, p.Ls, true, false, st);
+    SeqRun<IO> f = d;  // the forward states' shares with the state as it is stored (rows P), as the adjoints'
+    f.u = x;
+    f.v = B;
+    f.carry = c.carry;
+    f.decay = c.decay;
+    launch_seq_both<IO, true>(f, d, a.hp, p.rows, st);
+    launch_carry({{c.carry, d.carry}, {c.decay, d.decay}, {o.state_in, o.dstate_out}, {nullptr, nullptr}}, a.hp, set, p.Ls, 2,
+                 false, st);
   }
-  launch_seq<IO, false, false>(c, a.hp, p.rows, st);
+  if (T > 0) launch_seq_both<IO, false>(c, b, a.hp, p.rows, st);
   launch_seq<IO, true, false>(d, a.hp, p.rows, st);
   if (T > 0) {
-    launch_seq<IO, true, false>(b, a.hp, p.rows, st);
     const unsigned nqr = static_cast<unsigned>(cdiv(T * H * 16, 256));
-    hipLaunchKernelGGL((k_heads_qr<IO>), dim3(nqr), dim3(256), 0, st, B, C, f[2], f[3], f[4], f[5], T, H, a.N);
-    hipLaunchKernelGGL((k_heads_ddt<IO>), dim3(static_cast<unsigned>(p.rows64 * H)), dim3(64), 0, st, a.hp, x, dy, f[4],
-                       f[5], f[1], p.nrp, f[6], static_cast<IO*>(o.ddt), o.ddt_ts, f[7], a.P);
+    hipLaunchKernelGGL((k_heads_qr<IO>), dim3(nqr), dim3(256), 0, st, B, C, x, dy, f32[2], f32[3], f32[4], f32[5], f32[8], T, H,
+                       a.N, a.P);
+    hipLaunchKernelGGL((k_heads_ddt<IO>), dim3(static_cast<unsigned>(p.rows64 * H)), dim3(64), 0, st, a.hp, f32[4],
+                       f32[5], f32[8], f32[1], p.nrp, f32[6], static_cast<IO*>(o.ddt), o.ddt_ts, f32[7]);
     hipLaunchKernelGGL((k_heads_group<IO>), dim3(static_cast<unsigned>(cdiv(T * a.G * a.N, 256))), dim3(256), 0, st,
-                       f[2], f[3], f[6], static_cast<IO*>(o.dB), static_cast<IO*>(o.dC), o.db_ts, o.dc_ts, T, H, a.G,
+                       f32[2], f32[3], f32[6], static_cast<IO*>(o.dB), static_cast<IO*>(o.dC), o.db_ts, o.dc_ts, T, H, a.G,
                        a.N);
   }
-  hipLaunchKernelGGL(k_heads_params, dim3(static_cast<unsigned>(H)), dim3(256), 0, st, f[7], T > 0 ? p.rows64 : 0, H,
+  hipLaunchKernelGGL(k_heads_params, dim3(static_cast<unsigned>(H)), dim3(256), 0, st, f32[7], T > 0 ? p.rows64 : 0, H,
                      o.dA_log, o.ddt_bias, o.dD);
   return launched();
 }

@@ -145,18 +145,27 @@ struct SeqRun {
   float* store;               // forward: those states, or NULL
 };
 
+// A workgroup walks its segment in groups of 16 tokens of the packed stream, the next one loaded while this one is
+// computed.  Places of a group that are not the segment's hold zeros and delta = 0, which leave the state as it is.
+// 16 lanes share a state row.  777 ragged float32 tokens, 6 heads: TUNED us.
+template <int KV>
+struct SeqLds {
+  float v[kSeqTok][16 * KV], s[kSeqTok][16 * KV], u[kSeqTok][kSeqRows], o[kSeqTok][kSeqRows + 1];
+  float del[kSeqTok], dec[kSeqTok], dot[kSeqThreads / kWave];
+};
 template <typename IO, int KV, bool REV, bool LOCAL>
-__global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar hp) {
+__device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp, int64_t item, SeqLds<KV>& lds) {
   constexpr int KP = 16 * KV;
-  __shared__ float sv[kSeqTok][KP], ss[kSeqTok][KP];
-  __shared__ float su[kSeqTok][kSeqRows], so[kSeqTok][kSeqRows + 1];
-  __shared__ float sdel[kSeqTok], sdec[kSeqTok];
-  __shared__ float sdot[kSeqThreads / kWave];
+  auto &sv = lds.v, &ss = lds.s;
+  auto& su = lds.u;
+  auto& so = lds.o;
+  auto &sdel = lds.del, &sdec = lds.dec;
+  auto& sdot = lds.dot;
   const int tid = threadIdx.x, lane = tid & 15, row = tid >> 4;
   const int nrb = (q.R + kSeqRows - 1) / kSeqRows;
-  const int rb = blockIdx.x % nrb;
-  const int h = (blockIdx.x / nrb) % hp.H;
-  const int64_t rho = blockIdx.x / nrb / hp.H;
+  const int rb = static_cast<int>(item % nrb);
+  const int h = static_cast<int>(item / nrb % hp.H);
+  const int64_t rho = item / nrb / hp.H;
   const Segment g = segment_of(hp.cu, hp.S, rho, q.Ls);
   const int r = rb * kSeqRows + row;
   const bool many = g.many(q.Ls);
@@ -165,6 +174,7 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar
   const int64_t soff = h * q.sh + static_cast<int64_t>(r) * q.sr;
   const int64_t sset = static_cast<int64_t>(hp.H) * q.sh;
   const float A2 = head_A2(hp, h);
+  const float bias = hp.dt != nullptr ? hp.dt_bias[h] : 0.0f;
   const float Dh = (q.add_D && hp.D != nullptr) ? hp.D[h] : 0.0f;
   float st[KV];
 #pragma unroll
@@ -179,53 +189,67 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar
       }
   }
   float dsum = 0.0f;
-  const int64_t n = g.t1 - g.t0;
-  // blocks of kSeqTok tokens from the segment's first token on, taken in reverse by a reverse run
-  const int64_t nb = n > 0 ? (n + kSeqTok - 1) / kSeqTok : 0;
-  for (int64_t ib = 0; ib < nb; ++ib) {
-    const int64_t tb = g.t0 + (REV ? nb - 1 - ib : ib) * kSeqTok;
-    const int cnt = static_cast<int>(g.t1 - tb < kSeqTok ? g.t1 - tb : kSeqTok);
-    __syncthreads();
-    for (int i = tid; i < kSeqTok * KP; i += kSeqThreads) {
-      const int t = i / KP, k = i % KP;
-      const bool in = t < cnt && k < q.K;
-      sv[t][k] = in ? ld_io(q.v.at(tb + t, h), k) : 0.0f;
-      if (!LOCAL) ss[t][k] = in ? ld_io(q.s.at(tb + t, h), k) : 0.0f;
+  const int64_t b0 = g.t0 / kSeqTok, nb = g.t0 < g.t1 ? (g.t1 - 1) / kSeqTok - b0 + 1 : 0;
+  uint32_t rv[KV], rs[KV], ru = 0, rdt = 0;  // as loaded
+  bool din = false;
+  const auto load = [&](int64_t ib) {
+    const int64_t tb = (b0 + (REV ? nb - 1 - ib : ib)) * kSeqTok;
+#pragma unroll
+    for (int i = 0; i < KV; ++i) {
+      const int e = tid + i * kSeqThreads, t = e / KP, k = e % KP;
+      const bool in = tb + t >= g.t0 && tb + t < g.t1 && k < q.K;
+      rv[i] = in ? ld_io_raw(q.v.at(tb + t, h), k) : 0u;
+      if (!LOCAL) rs[i] = in ? ld_io_raw(q.s.at(tb + t, h), k) : 0u;
     }
-    {
-      const int t = tid >> 4, rr = rb * kSeqRows + (tid & 15);
-      su[t][tid & 15] = (t < cnt && rr < q.R) ? ld_io(q.u.at(tb + t, h), rr) : 0.0f;
-    }
+    const int64_t tu = tb + (tid >> 4);
+    const int rr = rb * kSeqRows + (tid & 15);
+    ru = tu >= g.t0 && tu < g.t1 && rr < q.R ? ld_io_raw(q.u.at(tu, h), rr) : 0u;
     if (tid < kSeqTok) {
-      const float d = tid < cnt ? head_delta<IO>(hp, tb + tid, h) : 0.0f;
+      din = tb + tid >= g.t0 && tb + tid < g.t1;
+      if (din && hp.dt != nullptr) rdt = ld_io_raw(static_cast<const IO*>(hp.dt) + (tb + tid) * hp.dt_ts, h);
+    }
+  };
+  if (nb > 0) load(0);
+  for (int64_t ib = 0; ib < nb; ++ib) {
+    const int64_t b = b0 + (REV ? nb - 1 - ib : ib), tb = b * kSeqTok;
+    const int lo = g.t0 > tb ? static_cast<int>(g.t0 - tb) : 0;
+    const int hi = g.t1 - tb < kSeqTok ? static_cast<int>(g.t1 - tb) : kSeqTok;
+    const bool edge = (b + 1) % (kHeadsBlock / kSeqTok) == 0 || tb + hi == g.seq1;  // the end of a 64-token block
+    const int64_t at64 = (g.s + tb / kHeadsBlock) * sset + soff;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < KV; ++i) {
+      const int e = tid + i * kSeqThreads, t = e / KP, k = e % KP;
+      sv[t][k] = io_value<IO>(rv[i]);
+      if (!LOCAL) ss[t][k] = io_value<IO>(rs[i]);
+    }
+    su[tid >> 4][tid & 15] = io_value<IO>(ru);
+    if (tid < kSeqTok) {
+      const float d = !din ? 0.0f : hp.dt == nullptr ? 1.0f : softplus(io_value<IO>(rdt) + bias);
       sdel[tid] = d;
       sdec[tid] = d * A2;
     }
     __syncthreads();
-#pragma unroll 4
+    if (ib + 1 < nb) load(ib + 1);
+    if (REV && !LOCAL && q.dots_with != nullptr && edge) {
+      // before the block's last token enters: the adjoint of the state after it
+      float d = 0.0f;
+      if (r < q.R)
+#pragma unroll
+        for (int i = 0; i < KV; ++i) {
+          const int k = lane * KV + i;
+          if (k < q.K) d = __builtin_fmaf(st[i], q.dots_with[at64 + k * q.sk], d);
+        }
+      d = row_sum16(d);
+      d += __shfl_xor(d, 16);
+      d += __shfl_xor(d, 32);
+      if ((tid & 63) == 0) sdot[tid >> 6] = d;
+      __syncthreads();
+      if (tid == 0) q.dots[((g.s + tb / kHeadsBlock) * hp.H + h) * nrb + rb] = (sdot[0] + sdot[1]) + (sdot[2] + sdot[3]);
+    }
+#pragma unroll
     for (int j = 0; j < kSeqTok; ++j) {
       const int t = REV ? kSeqTok - 1 - j : j;
-      if (t >= cnt) continue;
-      const int64_t tok = tb + t;
-      if (REV && !LOCAL && q.dots_with != nullptr && ((tok + 1) % kHeadsBlock == 0 || tok + 1 == g.seq1)) {
-        // before token tok enters: h is the adjoint of the state after it
-        const float* with = q.dots_with + (g.s + tok / kHeadsBlock) * sset + soff;
-        float d = 0.0f;
-        if (r < q.R)
-#pragma unroll
-          for (int i = 0; i < KV; ++i) {
-            const int k = lane * KV + i;
-            if (k < q.K) d = __builtin_fmaf(st[i], with[k * q.sk], d);
-          }
-        d = row_sum16(d);
-        d += __shfl_xor(d, 16);
-        d += __shfl_xor(d, 32);
-        if ((tid & 63) == 0) sdot[tid >> 6] = d;
-        __syncthreads();
-        if (tid == 0)
-          q.dots[((g.s + tok / kHeadsBlock) * hp.H + h) * nrb + rb] = (sdot[0] + sdot[1]) + (sdot[2] + sdot[3]);
-        __syncthreads();
-      }
       const float a = exp2_hw(sdec[t]);
       dsum += sdec[t];
       const float uu = su[t][row] * (REV ? 1.0f : sdel[t]);
@@ -241,17 +265,17 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar
         o = row_sum16(o);
         if (lane == 0) so[t][row] = (q.out_delta ? sdel[t] * o : o) + Dh * su[t][row];
       }
-      if (!REV && !LOCAL && q.store != nullptr && ((tok + 1) % kHeadsBlock == 0 || tok + 1 == g.seq1) && r < q.R)
-#pragma unroll
-        for (int i = 0; i < KV; ++i) {
-          const int k = lane * KV + i;
-          if (k < q.K) q.store[(g.s + tok / kHeadsBlock) * sset + soff + k * q.sk] = st[i];
-        }
     }
+    if (!REV && !LOCAL && q.store != nullptr && edge && r < q.R)
+#pragma unroll
+      for (int i = 0; i < KV; ++i) {
+        const int k = lane * KV + i;
+        if (k < q.K) q.store[at64 + k * q.sk] = st[i];
+      }
     if (!LOCAL && (q.out != nullptr || q.out32 != nullptr)) {
       __syncthreads();
       const int t = tid >> 4, rr = rb * kSeqRows + (tid & 15);
-      if (t < cnt && rr < q.R) {
+      if (t >= lo && t < hi && rr < q.R) {
         const int64_t at = static_cast<int64_t>(h) * q.R + rr;
         if (q.out != nullptr) st_io(q.out, (tb + t) * q.out_ts + at, so[t][tid & 15]);
         if (q.out32 != nullptr) q.out32[(tb + t) * hp.H * q.R + at] = so[t][tid & 15];
@@ -267,14 +291,35 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar
     }
   if (LOCAL && rb == 0 && tid == 0) q.decay[rho * hp.H + h] = dsum;
 }
+template <typename IO, int KV, bool REV, bool LOCAL>
+__global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar hp) {
+  __shared__ SeqLds<KV> lds;
+  heads_seq<IO, KV, REV, LOCAL>(q, hp, blockIdx.x, lds);
+}
+// a forward and a reverse run that do not need one another
+template <typename IO, int KV, bool LOCAL>
+__global__ __launch_bounds__(kSeqThreads) void k_heads_seq_both(SeqRun<IO> fwd, SeqRun<IO> rev, HeadPar hp) {
+  __shared__ SeqLds<KV> lds;
+  if (blockIdx.y == 0) heads_seq<IO, KV, false, LOCAL>(fwd, hp, blockIdx.x, lds);
+  else heads_seq<IO, KV, true, LOCAL>(rev, hp, blockIdx.x, lds);
+}
 
 // The states that the segments of a sequence start from, in place of what they add: one thread per
 // state element of a sequence, segment after segment (four loads ahead).  reverse: from the last.
 // all == 0: the sequences with several segments, whose last segment added nothing, and fin (if not NULL) only of
 // empty sequences; else all sequences, all of whose segments added, and the final states of all.  fin may be init.
-__global__ __launch_bounds__(256) void k_heads_carry(float* __restrict__ carry, const float* __restrict__ decay,
-                                                     const float* init, float* fin, const int32_t* __restrict__ cu, int H,
-                                                     int64_t PN, int64_t Ls, int reverse, int all, int s0) {
+// blockIdx.z: the forward states and the adjoints.
+struct Carry {
+  float* carry[2];
+  const float *decay[2], *init[2];
+  float* fin[2];
+};
+__global__ __launch_bounds__(256) void k_heads_carry(Carry c, const int32_t* __restrict__ cu, int H, int64_t PN,
+                                                     int64_t Ls, int all, int s0) {
+  const int reverse = blockIdx.z;
+  float* const carry = c.carry[reverse];
+  const float *const decay = c.decay[reverse], *const init = c.init[reverse];
+  float* const fin = c.fin[reverse];
   const int s = s0 + blockIdx.y;
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t set = H * PN;
@@ -404,11 +449,13 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_decode(Tok<IO> x, Tok<IO>
 }
 
 // ------------------------------------------------------------------------------------ backward
-// q_t = C_t . dC_t and r_t = B_t . dB_t (head by head, dB before its factor delta): a 16-lane row per (t, h)
+// q_t = C_t . dC_t, r_t = B_t . dB_t (head by head, dB before its factor delta) and w_t = x_t . dy_t: a 16-lane row
+// per (t, h)
 template <typename IO>
-__global__ __launch_bounds__(256) void k_heads_qr(Tok<IO> B, Tok<IO> C, const float* __restrict__ dB,
+__global__ __launch_bounds__(256) void k_heads_qr(Tok<IO> B, Tok<IO> C, Tok<IO> x, Tok<IO> dy, const float* __restrict__ dB,
                                                   const float* __restrict__ dC, float* __restrict__ q,
-                                                  float* __restrict__ r, int64_t T, int H, int N) {
+                                                  float* __restrict__ r, float* __restrict__ w, int64_t T, int H, int N,
+                                                  int P) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
   const int lane = threadIdx.x & 15;
   if (i >= T * H) return;
@@ -420,11 +467,16 @@ __global__ __launch_bounds__(256) void k_heads_qr(Tok<IO> B, Tok<IO> C, const fl
     sq = __builtin_fmaf(ld_io(Cp, n), dC[i * N + n], sq);
     sr = __builtin_fmaf(ld_io(Bp, n), dB[i * N + n], sr);
   }
+  const IO *xp = x.at(t, h), *gp = dy.at(t, h);
+  float sw = 0.0f;
+  for (int p = lane; p < P; p += 16) sw = __builtin_fmaf(ld_io(xp, p), ld_io(gp, p), sw);
   sq = row_sum16(sq);
   sr = row_sum16(sr);
+  sw = row_sum16(sw);
   if (lane == 0) {
     q[i] = sq;
     r[i] = sr;
+    w[i] = sw;
   }
 }
 
@@ -433,10 +485,10 @@ __global__ __launch_bounds__(256) void k_heads_qr(Tok<IO> B, Tok<IO> C, const fl
 // of the adjoint and the state (dots): the sum restarts there and its rounding does not build up along the
 // sequence.  One wave per (block, head), one token per lane.
 template <typename IO>
-__global__ __launch_bounds__(64) void k_heads_ddt(HeadPar hp, Tok<IO> x, Tok<IO> dy, const float* __restrict__ q,
-                                                  const float* __restrict__ r, const float* __restrict__ dots, int ndots,
+__global__ __launch_bounds__(64) void k_heads_ddt(HeadPar hp, const float* __restrict__ q, const float* __restrict__ r,
+                                                  const float* __restrict__ w, const float* __restrict__ dots, int ndots,
                                                   float* __restrict__ delta, IO* __restrict__ ddt, int64_t ddt_ts,
-                                                  float* __restrict__ sums, int P) {
+                                                  float* __restrict__ sums) {
   const int lane = threadIdx.x;
   const int h = blockIdx.x % hp.H;
   const int64_t rho = blockIdx.x / hp.H;
@@ -471,8 +523,7 @@ __global__ __launch_bounds__(64) void k_heads_ddt(HeadPar hp, Tok<IO> x, Tok<IO>
       db = __builtin_fmaf(A, dl, rr) * rcp_hw(1.0f + exp2_hw(-v * kLog2e));
       st_io(ddt, t * ddt_ts + h, db);
     }
-    const IO *xp = x.at(t, h), *gp = dy.at(t, h);
-    for (int p = 0; p < P; ++p) dD = __builtin_fmaf(ld_io(xp, p), ld_io(gp, p), dD);
+    dD = w[t * hp.H + h];
   }
   for (int k = 32; k > 0; k /= 2) {
     dA += __shfl_xor(dA, k);
