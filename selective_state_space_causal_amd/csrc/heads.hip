@@ -526,29 +526,44 @@ int by_types(int32_t io, int32_t res, F f) {
   return f(uint16_t{}, uint16_t{});
 }
 
-// How a row (or its group) of n columns is spread: pieces of 8 columns, at most 512 threads and as few pieces per
-// thread as that allows.
+// How a row (or its group) of n columns is spread: NV pieces of E columns for each thread.  With float32 arrays E = 4
+// (16 bytes).  With bfloat16 alone 8 (gate_norm of 16384 x 4096: 75.5 us, with 4 78.0), or 4 where that leaves fewer
+// lanes idle (groups of 640 columns: 8 leaves 38% idle, 4 17%; the backward of 8192 x 5120 92.2 against 93.3 us).
 struct NormShape {
-  int threads, nv;
+  int e, threads, nv;
 };
-NormShape norm_shape(int n) {
-  const int pieces = static_cast<int>(cdiv(n, 8));
-  int nv = 1;
-  while (cdiv(pieces, nv) > kNormMaxThreads) nv *= 2;
-  return {static_cast<int>(cdiv(cdiv(pieces, nv), kWave) * kWave), nv};
+NormShape norm_shape(int n, bool f32) {
+  const auto of = [n](int e) {
+    const int pieces = static_cast<int>(cdiv(n, e)), nv = pieces > kNormMaxThreads ? 2 : 1;
+    return NormShape{e, static_cast<int>(cdiv(cdiv(pieces, nv), kWave) * kWave), nv};
+  };
+  const NormShape four = of(4), eight = of(8);
+  return f32 || (four.nv == 1 && four.threads * 4 < eight.threads * 8) ? four : eight;
 }
-// Workgroups of a backward call, for every group: rows beyond this many wait their turn.  Two workgroups (or 16
-// waves) per CU keep enough rows in flight; more would only add partial sums of the weights.
+// Workgroups for every group of columns; rows beyond this many wait their turn, the next one's loads ahead.
+// Backward: what is resident together (24 waves per CU), because each workgroup adds a row of partial sums: gate_norm
+// 8192 x 5120 in 8 groups 92.2 us, with 20 waves 97.4, with 28 (the last ones a round of their own) 120; residual_norm
+// 8191 x 2560 89.0 us, 10 waves 88.4.  Forward: several rounds even out the ends: gate_norm 16384 x 4096 75.0 us with
+// 16 workgroups per CU, with 4 to 8 77 to 79.
 int64_t norm_slots(int64_t rows, int n, int groups, bool backward) {
-  const int t = norm_shape(n).threads;
-  const int64_t wgs = kCUs * (backward ? std::max(2, 1024 / t) : std::max(4, 2048 / t));
+  const int t = norm_shape(n, true).threads;
+  const int64_t wgs = kCUs * (backward ? std::max(1, 24 * kWave / t) : std::max(16, 8192 / t));
   return std::max<int64_t>(1, std::min<int64_t>(rows, cdiv(wgs, groups)));
 }
-template <typename F>
-void by_pieces(int nv, F f) {
-  if (nv == 1) f(std::integral_constant<int, 1>{});
-  else f(std::integral_constant<int, 2>{});
+// f(E, NV) of a shape
+template <bool BF16, typename F>
+void by_pieces(const NormShape& sh, F f) {
+  constexpr auto one = std::integral_constant<int, 1>{};
+  constexpr auto four = std::integral_constant<int, 4>{};
+  if constexpr (BF16) {
+    if (sh.e == 8) f(std::integral_constant<int, 8>{}, one);
+    else f(four, one);
+  } else {
+    if (sh.nv == 1) f(four, one);
+    else f(four, std::integral_constant<int, 2>{});
+  }
 }
+
 // workspace of a backward call: partial sums of K weights, for wide rows behind the rows' factors
 size_t norm_workspace(int64_t rows, int d, int groups, int K) {
   if (d == 0) return 0;
@@ -727,10 +742,14 @@ int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, voi
                          static_cast<IO*>(out));
       return;
     }
-    const NormShape sh = norm_shape(d / groups);
+    const NormShape sh = norm_shape(d / groups, io_dtype == MM_IO_F32);
     const dim3 grid(static_cast<unsigned>(norm_slots(nrows, d / groups, groups, false) * groups));
-    by_pieces(sh.nv, [&](auto nv) {
-      hipLaunchKernelGGL((k_gate_norm<IO, decltype(nv)::value>), grid, dim3(sh.threads), 0, st, a, static_cast<IO*>(out));
+    by_pieces<sizeof(IO) == 2>(sh, [&](auto e, auto nv) {
+      constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
+      const dim3 block(sh.threads);
+      IO* o = static_cast<IO*>(out);
+      if (gate_first != 0) hipLaunchKernelGGL((k_gate_norm<IO, E, NV, true>), grid, block, 0, st, a, o);
+      else hipLaunchKernelGGL((k_gate_norm<IO, E, NV, false>), grid, block, 0, st, a, o);
     });
   };
   if (io_dtype == MM_IO_BF16) go(uint16_t{}); else go(float{});
@@ -780,10 +799,15 @@ int mamba_mixer_gate_norm_backward(const void* dout, const void* y, const void* 
       hipLaunchKernelGGL((k_wide_gate_norm_dw<IO>), cols, block, 0, st, a, stats, part, cdiv(nrows, slots));
       return;
     }
-    const NormShape sh = norm_shape(n);
-    by_pieces(sh.nv, [&](auto nv) {
-      hipLaunchKernelGGL((k_gate_norm_bwd<IO, decltype(nv)::value>), dim3(static_cast<unsigned>(slots * groups)),
-                         dim3(sh.threads), 0, st, a, static_cast<IO*>(dy), static_cast<IO*>(dz), dy_stride, dz_stride, part);
+    const NormShape sh = norm_shape(n, io_dtype == MM_IO_F32);
+    by_pieces<sizeof(IO) == 2>(sh, [&](auto e, auto nv) {
+      constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
+      const dim3 grid(static_cast<unsigned>(slots * groups)), block(sh.threads);
+      IO *oy = static_cast<IO*>(dy), *oz = static_cast<IO*>(dz);
+      if (gate_first != 0)
+        hipLaunchKernelGGL((k_gate_norm_bwd<IO, E, NV, true>), grid, block, 0, st, a, oy, oz, dy_stride, dz_stride, part);
+      else
+        hipLaunchKernelGGL((k_gate_norm_bwd<IO, E, NV, false>), grid, block, 0, st, a, oy, oz, dy_stride, dz_stride, part);
     });
   };
   if (nrows > 0) { if (io_dtype == MM_IO_BF16) go(uint16_t{}); else go(float{}); }
@@ -818,9 +842,9 @@ int mamba_mixer_residual_norm(const void* h, const void* residual, const float* 
                          static_cast<RES*>(residual_out), static_cast<IO*>(out));
       return launched();
     }
-    const NormShape sh = norm_shape(d);
-    by_pieces(sh.nv, [&](auto nv) {
-      hipLaunchKernelGGL((k_residual_norm<IO, RES, decltype(nv)::value>),
+    const NormShape sh = norm_shape(d, res_dtype == MM_IO_F32);
+    by_pieces<sizeof(RES) == 2>(sh, [&](auto e, auto nv) {
+      hipLaunchKernelGGL((k_residual_norm<IO, RES, decltype(e)::value, decltype(nv)::value>),
                          dim3(static_cast<unsigned>(norm_slots(nrows, d, 1, false))), dim3(sh.threads), 0, st, a,
                          static_cast<RES*>(residual_out), static_cast<IO*>(out));
     });
@@ -882,9 +906,9 @@ int mamba_mixer_residual_norm_backward(const void* dout, const void* dresidual_o
                            static_cast<RES*>(dresidual), static_cast<IO*>(dh), stats);
         return launched();
       }
-      const NormShape sh = norm_shape(d);
-      by_pieces(sh.nv, [&](auto nv) {
-        hipLaunchKernelGGL((k_residual_norm_bwd<IO, RES, decltype(nv)::value>), dim3(static_cast<unsigned>(slots)),
+      const NormShape sh = norm_shape(d, res_dtype == MM_IO_F32);
+      by_pieces<sizeof(RES) == 2>(sh, [&](auto e, auto nv) {
+        hipLaunchKernelGGL((k_residual_norm_bwd<IO, RES, decltype(e)::value, decltype(nv)::value>), dim3(static_cast<unsigned>(slots)),
                            dim3(sh.threads), 0, st, a, static_cast<const IO*>(dout), static_cast<const RES*>(dresidual_out),
                            static_cast<RES*>(dresidual), static_cast<IO*>(dh), part);
       });

@@ -4,12 +4,12 @@
 //   residual_norm   p = h or w_post n(h);  r' = r + scale scale_vec p;  out = w n(r')
 // and their gradients.  All arithmetic is float32; the outputs are rounded once.
 //
-// Bound by memory.  A workgroup takes a (row, group) at a time, eight neighbouring columns per thread
-// and NV such pieces, in registers from the load to the store: every array is read and written once.
+// Bound by memory.  A workgroup takes a (row, group) at a time, E neighbouring columns per thread and NV
+// such pieces, in registers from the load to the store: every array is read and written once.
 // The next row is loaded before this one's sums are taken.  In the backward a workgroup keeps to one
 // column range over all its rows, so the weights' gradients gather in registers too and leave as one
 // partial sum per workgroup, added in a fixed order by k_norm_parts.
-// Rows may start anywhere: 16-byte accesses need no alignment here, and a row's last piece is taken
+// Rows may start anywhere: wide accesses need no alignment here, and a row's last piece is taken
 // element by element.
 #pragma once
 
@@ -17,109 +17,109 @@
 
 namespace mm {
 
-constexpr int kNormMaxThreads = 512;
-constexpr int kNormMaxPieces = 2;  // per thread
-constexpr int kNormUnit = kNormMaxThreads * kNormMaxPieces * 8;  // columns that fit: 8192
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormUnit = kNormMaxThreads * 8;  // columns that fit: 8 for each thread
 
-typedef uint32_t nu4 __attribute__((ext_vector_type(4), aligned(2)));
-typedef float nf4 __attribute__((ext_vector_type(4), aligned(4)));
-
-// eight elements as loaded
-template <typename IO>
-struct Raw8;
-template <>
-struct Raw8<uint16_t> {
-  nu4 v;
-};
-template <>
-struct Raw8<float> {
-  nf4 a, b;
+// E (8 or 4) neighbouring elements as loaded
+template <typename IO, int E>
+struct Raw {
+  static constexpr int W = E * sizeof(IO) / 4;
+  typedef uint32_t vec __attribute__((ext_vector_type(W), aligned(sizeof(IO))));
+  vec v;
 };
 // n: how many exist (the others read as zeros)
-__device__ __forceinline__ Raw8<uint16_t> load_raw(const uint16_t* p, int n) {
-  Raw8<uint16_t> r;
-  r.v = nu4{0, 0, 0, 0};
-  if (n >= 8) {
-    r.v = *reinterpret_cast<const nu4*>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) r.v[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
+template <int E, typename IO>
+__device__ __forceinline__ Raw<IO, E> load_raw(const IO* p, int n) {
+  typedef Raw<IO, E> R;
+  R r;
+  if (n >= E) {
+    if constexpr (R::W > 4) {  // float32: two 16-byte loads
+      typedef uint32_t half __attribute__((ext_vector_type(4), aligned(4)));
+      const half a = *reinterpret_cast<const half*>(p), b = *reinterpret_cast<const half*>(p + E / 2);
+      r.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      r.v = *reinterpret_cast<const typename R::vec*>(p);
+    }
+    return r;
   }
+#pragma unroll
+  for (int i = 0; i < R::W; ++i) r.v[i] = 0;
+#pragma unroll
+  for (int i = 0; i < E - 1; ++i)
+    if (i < n) {
+      if constexpr (sizeof(IO) == 2) r.v[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
+      else r.v[i] = __float_as_uint(p[i]);
+    }
   return r;
 }
-__device__ __forceinline__ Raw8<float> load_raw(const float* p, int n) {
-  Raw8<float> r;
-  r.a = r.b = nf4{0, 0, 0, 0};
-  if (n >= 8) {
-    r.a = *reinterpret_cast<const nf4*>(p);
-    r.b = *reinterpret_cast<const nf4*>(p + 4);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) r.a[i] = p[i];
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (4 + i < n) r.b[i] = p[4 + i];
-  }
-  return r;
-}
-__device__ __forceinline__ float get(const Raw8<uint16_t>& r, int i) {
+template <int E>
+__device__ __forceinline__ float get(const Raw<uint16_t, E>& r, int i) {
   return __uint_as_float(i % 2 ? r.v[i / 2] & 0xFFFF0000u : r.v[i / 2] << 16);
 }
-__device__ __forceinline__ float get(const Raw8<float>& r, int i) { return i < 4 ? r.a[i & 3] : r.b[i & 3]; }
-__device__ __forceinline__ void store_8(uint16_t* p, int n, const float (&v)[8]) {
-  typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-  typedef float f8 __attribute__((ext_vector_type(8)));
-  f8 f;
+template <int E>
+__device__ __forceinline__ float get(const Raw<float, E>& r, int i) { return __uint_as_float(r.v[i]); }
+template <int E>
+__device__ __forceinline__ void set(Raw<float, E>& r, int i, float v) { r.v[i] = __float_as_uint(v); }
+template <int E>
+__device__ __forceinline__ void store_raw(uint16_t* p, int n, const float (&v)[E]) {
+  typedef __bf16 bE __attribute__((ext_vector_type(E)));
+  typedef float fE __attribute__((ext_vector_type(E)));
+  typedef typename Raw<uint16_t, E>::vec vec;
+  fE f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = v[i];
-  const b8 b = __builtin_convertvector(f, b8);  // round to nearest even
-  if (n >= 8) {
-    *reinterpret_cast<nu4*>(p) = __builtin_bit_cast(nu4, b);
+  for (int i = 0; i < E; ++i) f[i] = v[i];
+  const vec u = __builtin_bit_cast(vec, __builtin_convertvector(f, bE));  // round to nearest even
+  if (n >= E) {
+    *reinterpret_cast<vec*>(p) = u;
   } else {
-    const nu4 u = __builtin_bit_cast(nu4, b);
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < E - 1; ++i)
       if (i < n) p[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i % 2)));
   }
 }
-__device__ __forceinline__ void store_8(float* p, int n, const float (&v)[8]) {
-  if (n >= 8) {
-    *reinterpret_cast<nf4*>(p) = nf4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<nf4*>(p + 4) = nf4{v[4], v[5], v[6], v[7]};
+template <int E>
+__device__ __forceinline__ void store_raw(float* p, int n, const float (&v)[E]) {
+  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+  if (n >= E) {
+#pragma unroll
+    for (int i = 0; i < E; i += 4) *reinterpret_cast<f4*>(p + i) = f4{v[i], v[i + 1], v[i + 2], v[i + 3]};
   } else {
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < E - 1; ++i)
       if (i < n) p[i] = v[i];
   }
 }
 
 // Sums of K values over the workgroup, in every thread; LDS for two calls in turn, so that one barrier
-// serves each.
+// serves each.  Within a wave by DPP (a row of 16, then rows broadcast into the next ones: lane 63 has all);
+// each lane then reads one wave's sum, not every lane all of them: with ten waves and six sums those reads
+// alone took a third of the time.
 struct NormRed {
-  float s[2][3][kNormMaxThreads / kWave];
+  float s[2][6][kNormMaxThreads / kWave];
 };
 template <int K>
 __device__ __forceinline__ void group_sums(float (&v)[K], NormRed& red, int& turn) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     v[k] = row_sum16(v[k]);
-    v[k] += __shfl_xor(v[k], 16);
-    v[k] += __shfl_xor(v[k], 32);
+    v[k] += __builtin_amdgcn_update_dpp(0.0f, v[k], 0x142, 0xA, 0xF, false);  // row_bcast:15, rows 1 and 3
+    v[k] += __builtin_amdgcn_update_dpp(0.0f, v[k], 0x143, 0xC, 0xF, false);  // row_bcast:31, rows 2 and 3
   }
-  const int waves = blockDim.x / kWave;
-  if (waves == 1) return;
-  if ((threadIdx.x & 63) == 0)
+  const int waves = blockDim.x / kWave, lane = threadIdx.x & 63;
+  if (waves == 1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      v[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v[k]), 63));
+    return;
+  }
+  if (lane == 63)
 #pragma unroll
     for (int k = 0; k < K; ++k) red.s[turn][k][threadIdx.x >> 6] = v[k];
   __syncthreads();
+  const int w = lane & 15;
+  static_assert(kNormMaxThreads / kWave <= 16, "one lane of a row for each wave");
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    float t = 0.0f;
-    for (int w = 0; w < waves; ++w) t += red.s[turn][k][w];
-    v[k] = t;
-  }
+  for (int k = 0; k < K; ++k) v[k] = row_sum16(w < waves ? red.s[turn][k][w] : 0.0f);
   turn ^= 1;
 }
 __device__ __forceinline__ float sigmoid(float z) { return rcp_hw(1.0f + exp2_hw(-z * kLog2e)); }
@@ -136,39 +136,38 @@ struct GateArgs {
 };
 
 // Workgroups b, b + groups, ...: the rows b / groups, b / groups + slots, ... of group b % groups.
-template <typename IO, int NV>
+template <typename IO, int E, int NV, bool FIRST>
 __global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm(GateArgs<IO> a, IO* __restrict__ out) {
   __shared__ NormRed red;
   int turn = 0;
   const int n = a.d / a.groups, g = blockIdx.x % a.groups, T = blockDim.x;
   const int64_t slots = gridDim.x / a.groups;
-  const bool first = a.gate_first != 0;
-  Raw8<float> w[NV];
-  Raw8<IO> y[NV], z[NV];
+  Raw<float, E> w[NV];
+  Raw<IO, E> y[NV], z[NV];
   const auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + threadIdx.x) * 8;
-      y[i] = load_raw(a.y + row * a.y_ts + g * n + c, n - c);
-      z[i] = load_raw(a.z + row * a.z_ts + g * n + c, n - c);
+      const int c = (i * T + threadIdx.x) * E;
+      y[i] = load_raw<E>(a.y + row * a.y_ts + g * n + c, n - c);
+      z[i] = load_raw<E>(a.z + row * a.z_ts + g * n + c, n - c);
     }
   };
   int64_t row = blockIdx.x / a.groups;
   load(row);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * T + threadIdx.x) * 8;
-    w[i] = load_raw(a.w + g * n + c, n - c);
+    const int c = (i * T + threadIdx.x) * E;
+    w[i] = load_raw<E>(a.w + g * n + c, n - c);
   }
   for (; row < a.rows; row += slots) {
-    float v[NV][8], sum[1] = {0.0f};
+    float v[NV][E], sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < E; ++e) {
         const float yv = get(y[i], e), zv = get(z[i], e);
         v[i][e] = yv * (zv * sigmoid(zv));
-        const float u = first ? v[i][e] : yv;
+        const float u = FIRST ? v[i][e] : yv;
         sum[0] = __builtin_fmaf(u, u, sum[0]);
       }
     if (row + slots < a.rows) load(row + slots);
@@ -176,10 +175,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm(GateArgs<IO> a, I
     const float k = rsqrtf(sum[0] / n + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + threadIdx.x) * 8;
+      const int c = (i * T + threadIdx.x) * E;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] *= k * get(w[i], e);
-      if (c < n) store_8(out + row * a.d + g * n + c, n - c, v[i]);
+      for (int e = 0; e < E; ++e) v[i][e] *= k * get(w[i], e);
+      if (c < n) store_raw<E>(out + row * a.d + g * n + c, n - c, v[i]);
     }
   }
 }
@@ -187,7 +186,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm(GateArgs<IO> a, I
 // With u = y s (gate first) or y, n = u k, k = rsqrt(mean(u^2) + eps) and dn = dout w (times s, gate last):
 //   du = k (dn - n mean(dn n));  first: dy = du s, dz = du y s';  last: dy = du, dz = dout w n s'
 // part: [slots, d] partial sums of dw.
-template <typename IO, int NV>
+template <typename IO, int E, int NV, bool FIRST>
 __global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm_bwd(GateArgs<IO> a, IO* __restrict__ dy, IO* __restrict__ dz,
                                                                    int64_t dy_ts, int64_t dz_ts,
                                                                    float* __restrict__ part) {
@@ -195,30 +194,30 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm_bwd(GateArgs<IO> 
   int turn = 0;
   const int n = a.d / a.groups, g = blockIdx.x % a.groups, T = blockDim.x;
   const int64_t slots = gridDim.x / a.groups;
-  const bool first = a.gate_first != 0;
-  Raw8<float> w[NV];
-  Raw8<IO> y[NV], z[NV], go[NV];
-  float dw[NV][8];
+  Raw<float, E> w[NV];
+  Raw<IO, E> y[NV], z[NV], go[NV];
+  float dw[NV][E];
   const auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + threadIdx.x) * 8;
-      y[i] = load_raw(a.y + row * a.y_ts + g * n + c, n - c);
-      z[i] = load_raw(a.z + row * a.z_ts + g * n + c, n - c);
-      go[i] = load_raw(a.dout + row * a.d + g * n + c, n - c);
+      const int c = (i * T + threadIdx.x) * E;
+      y[i] = load_raw<E>(a.y + row * a.y_ts + g * n + c, n - c);
+      z[i] = load_raw<E>(a.z + row * a.z_ts + g * n + c, n - c);
+      go[i] = load_raw<E>(a.dout + row * a.d + g * n + c, n - c);
     }
   };
   int64_t row = blockIdx.x / a.groups;
   load(row);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * T + threadIdx.x) * 8;
-    w[i] = load_raw(a.w + g * n + c, n - c);
+    const int c = (i * T + threadIdx.x) * E;
+    w[i] = load_raw<E>(a.w + g * n + c, n - c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+    for (int e = 0; e < E; ++e) dw[i][e] = 0.0f;
   }
   for (; row < a.rows; row += slots) {
-    Raw8<IO> yr[NV], zr[NV], gr[NV];
+    Raw<IO, E> yr[NV], zr[NV], gr[NV];
+    float sg[NV][E];  // sigmoid(z): its exponential and reciprocal are the costly part, taken once
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -226,9 +225,11 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm_bwd(GateArgs<IO> 
       zr[i] = z[i];
       gr[i] = go[i];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float zv = get(zr[i], e), s = zv * sigmoid(zv), yv = get(yr[i], e);
-        const float u = first ? yv * s : yv, gw = get(gr[i], e) * get(w[i], e);
+      for (int e = 0; e < E; ++e) {
+        const float zv = get(zr[i], e), yv = get(yr[i], e);
+        sg[i][e] = sigmoid(zv);
+        const float s = zv * sg[i][e];
+        const float u = FIRST ? yv * s : yv, gw = get(gr[i], e) * get(w[i], e);
         sum[0] = __builtin_fmaf(u, u, sum[0]);
         sum[1] = __builtin_fmaf(gw * s, yv, sum[1]);  // dn u, either way
       }
@@ -239,13 +240,13 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm_bwd(GateArgs<IO> 
     const float km = k * k * (sum[1] / n);  // k mean(dn n): n mean(dn n) = u km
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + threadIdx.x) * 8;
-      float oy[8], oz[8];
+      const int c = (i * T + threadIdx.x) * E;
+      float oy[E], oz[E];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float zv = get(zr[i], e), sg = sigmoid(zv), s = zv * sg, ds = sg * (1.0f + zv * (1.0f - sg));
+      for (int e = 0; e < E; ++e) {
+        const float zv = get(zr[i], e), g1 = sg[i][e], s = zv * g1, ds = g1 * (1.0f + zv * (1.0f - g1));
         const float yv = get(yr[i], e), gv = get(gr[i], e), gw = gv * get(w[i], e);
-        if (first) {
+        if (FIRST) {
           const float du = k * (gw - yv * s * km);
           oy[e] = du * s;
           oz[e] = du * yv * ds;
@@ -256,15 +257,15 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_gate_norm_bwd(GateArgs<IO> 
         dw[i][e] = __builtin_fmaf(gv * k, yv * s, dw[i][e]);
       }
       if (c < n) {
-        store_8(dy + row * dy_ts + g * n + c, n - c, oy);
-        store_8(dz + row * dz_ts + g * n + c, n - c, oz);
+        store_raw<E>(dy + row * dy_ts + g * n + c, n - c, oy);
+        store_raw<E>(dz + row * dz_ts + g * n + c, n - c, oz);
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * T + threadIdx.x) * 8;
-    if (c < n) store_8(part + static_cast<int64_t>(blockIdx.x / a.groups) * a.d + g * n + c, n - c, dw[i]);
+    const int c = (i * T + threadIdx.x) * E;
+    if (c < n) store_raw<E>(part + static_cast<int64_t>(blockIdx.x / a.groups) * a.d + g * n + c, n - c, dw[i]);
   }
 }
 
@@ -308,41 +309,43 @@ struct ResArgs {
   int64_t rows;
   int d;
 };
-// eight of a per-column parameter; ones where there is none
-__device__ __forceinline__ Raw8<float> load_or_one(const float* p, int c, int n) {
-  if (p != nullptr) return load_raw(p + c, n);
-  Raw8<float> r;
-  r.a = r.b = nf4{1, 1, 1, 1};
+// E of a per-column parameter; ones where there is none
+template <int E>
+__device__ __forceinline__ Raw<float, E> load_or_one(const float* p, int c, int n) {
+  if (p != nullptr) return load_raw<E>(p + c, n);
+  Raw<float, E> r;
+#pragma unroll
+  for (int i = 0; i < E; ++i) set(r, i, 1.0f);
   return r;
 }
 
-template <typename IO, typename RES, int NV>
+template <typename IO, typename RES, int E, int NV>
 __global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm(ResArgs<IO, RES> a, RES* __restrict__ res_out,
                                                                    IO* __restrict__ out) {
   __shared__ NormRed red;
   int turn = 0;
   const int n = a.d, T = blockDim.x;
-  Raw8<float> w[NV], f[NV];  // f: everything that multiplies h's norm
-  Raw8<IO> h[NV];
-  Raw8<RES> res[NV];
+  Raw<float, E> w[NV], f[NV];  // f: everything that multiplies h's norm
+  Raw<IO, E> h[NV];
+  Raw<RES, E> res[NV];
   const auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + threadIdx.x) * 8;
-      h[i] = load_raw(a.h + row * n + c, n - c);
-      res[i] = load_raw(a.res + (a.res != nullptr ? row * n + c : 0), a.res != nullptr ? n - c : 0);
+      const int c = (i * T + threadIdx.x) * E;
+      h[i] = load_raw<E>(a.h + row * n + c, n - c);
+      res[i] = load_raw<E>(a.res + (a.res != nullptr ? row * n + c : 0), a.res != nullptr ? n - c : 0);
     }
   };
   int64_t row = blockIdx.x;
   load(row);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * T + threadIdx.x) * 8;
-    w[i] = load_raw(a.w + c, n - c);
-    f[i] = load_or_one(a.wp, c, n - c);
-    const Raw8<float> v = load_or_one(a.vec, c, n - c);
-    f[i].a *= a.scale * v.a;
-    f[i].b *= a.scale * v.b;
+    const int c = (i * T + threadIdx.x) * E;
+    w[i] = load_raw<E>(a.w + c, n - c);
+    f[i] = load_or_one<E>(a.wp, c, n - c);
+    const Raw<float, E> v = load_or_one<E>(a.vec, c, n - c);
+#pragma unroll
+    for (int e = 0; e < E; ++e) set(f[i], e, get(f[i], e) * (a.scale * get(v, e)));
   }
   for (; row < a.rows; row += gridDim.x) {
     float kp = 1.0f;
@@ -351,15 +354,15 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm(ResArgs<IO, R
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[0] = __builtin_fmaf(get(h[i], e), get(h[i], e), sum[0]);
+        for (int e = 0; e < E; ++e) sum[0] = __builtin_fmaf(get(h[i], e), get(h[i], e), sum[0]);
       group_sums(sum, red, turn);
       kp = rsqrtf(sum[0] / n + a.eps);
     }
-    float r[NV][8], sum[1] = {0.0f};
+    float r[NV][E], sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < E; ++e) {
         r[i][e] = __builtin_fmaf(get(h[i], e) * kp, get(f[i], e), get(res[i], e));
         sum[0] = __builtin_fmaf(r[i][e], r[i][e], sum[0]);
       }
@@ -368,11 +371,11 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm(ResArgs<IO, R
     const float k = rsqrtf(sum[0] / n + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + threadIdx.x) * 8;
-      if (c < n) store_8(res_out + row * n + c, n - c, r[i]);
+      const int c = (i * T + threadIdx.x) * E;
+      if (c < n) store_raw<E>(res_out + row * n + c, n - c, r[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[i][e] *= k * get(w[i], e);
-      if (c < n) store_8(out + row * n + c, n - c, r[i]);
+      for (int e = 0; e < E; ++e) r[i][e] *= k * get(w[i], e);
+      if (c < n) store_raw<E>(out + row * n + c, n - c, r[i]);
     }
   }
 }
@@ -381,7 +384,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm(ResArgs<IO, R
 //   dr = dr' + k (dn - n mean(dn n)),  dp = scale vec dr,  and through the norm of h, kp = rsqrt(mean(h^2) + eps):
 //   dh = kp (dp wp - h kp^2 mean(dp wp h))          (without wp: dh = dp)
 // part: per slot the partial sums of dw = dout n, dwp = dp h kp and dvec = scale dr p.
-template <typename IO, typename RES, int NV>
+template <typename IO, typename RES, int E, int NV>
 __global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm_bwd(ResArgs<IO, RES> a, const IO* __restrict__ dout,
                                                                        const RES* dres_out, RES* dres,
                                                                        IO* __restrict__ dh, float* __restrict__ part) {
@@ -389,88 +392,102 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm_bwd(ResArgs<I
   int turn = 0;
   const int n = a.d, T = blockDim.x;
   const bool post = a.wp != nullptr;
-  Raw8<float> w[NV], wp[NV], vec[NV];
-  Raw8<IO> h[NV], go[NV];
-  Raw8<RES> res[NV], up[NV];
-  float acc[3][NV][8];
+  Raw<float, E> w[NV], wp[NV], vec[NV];
+  Raw<IO, E> h[NV], go[NV];
+  Raw<RES, E> res[NV], up[NV];
+  float acc[3][NV][E];
   const auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + threadIdx.x) * 8;
-      h[i] = load_raw(a.h + row * n + c, n - c);
-      go[i] = load_raw(dout + row * n + c, n - c);
-      res[i] = load_raw(a.res + row * n + c, n - c);
-      up[i] = load_raw(dres_out + (dres_out != nullptr ? row * n + c : 0), dres_out != nullptr ? n - c : 0);
+      const int c = (i * T + threadIdx.x) * E;
+      h[i] = load_raw<E>(a.h + row * n + c, n - c);
+      go[i] = load_raw<E>(dout + row * n + c, n - c);
+      res[i] = load_raw<E>(a.res + row * n + c, n - c);
+      up[i] = load_raw<E>(dres_out + (dres_out != nullptr ? row * n + c : 0), dres_out != nullptr ? n - c : 0);
     }
   };
+  constexpr bool kAhead = NV == 1;  // the next row's loads wait in registers, where there are enough
   int64_t row = blockIdx.x;
-  load(row);
+  if (kAhead) load(row);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * T + threadIdx.x) * 8;
-    w[i] = load_raw(a.w + c, n - c);
-    wp[i] = load_or_one(a.wp, c, n - c);
-    vec[i] = load_or_one(a.vec, c, n - c);
-    vec[i].a *= a.scale;
-    vec[i].b *= a.scale;
+    const int c = (i * T + threadIdx.x) * E;
+    w[i] = load_raw<E>(a.w + c, n - c);
+    wp[i] = load_or_one<E>(a.wp, c, n - c);
+    vec[i] = load_or_one<E>(a.vec, c, n - c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[0][i][e] = acc[1][i][e] = acc[2][i][e] = 0.0f;
+    for (int e = 0; e < E; ++e) set(vec[i], e, get(vec[i], e) * a.scale);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[0][i][e] = acc[1][i][e] = acc[2][i][e] = 0.0f;
   }
   for (; row < a.rows; row += gridDim.x) {
-    float sum[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float rv = get(res[i], e), hv = get(h[i], e);
-        sum[0] = __builtin_fmaf(rv, rv, sum[0]);
-        sum[1] = __builtin_fmaf(get(go[i], e) * get(w[i], e), rv, sum[1]);
-        sum[2] = __builtin_fmaf(hv, hv, sum[2]);
-      }
-    group_sums(sum, red, turn);
-    const float k = rsqrtf(sum[0] / n + a.eps), km = k * k * (sum[1] / n);
-    const float kp = post ? rsqrtf(sum[2] / n + a.eps) : 1.0f;
-    float dr[NV][8], sh[1] = {0.0f};
-    Raw8<IO> hr[NV];
+    if (!kAhead) load(row);
+    // r^2, w g r, h^2 and the three parts of dr f h (f = vec w_p), so that one reduction serves both norms
+    float sum[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    Raw<IO, E> hr[NV], gr[NV];
+    Raw<RES, E> rr[NV], ur[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       hr[i] = h[i];
+      gr[i] = go[i];
+      rr[i] = res[i];
+      ur[i] = up[i];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float rv = get(res[i], e), gv = get(go[i], e), hv = get(h[i], e);
-        dr[i][e] = get(up[i], e) + k * (gv * get(w[i], e) - rv * km);
-        const float dp = dr[i][e] * get(vec[i], e);
-        sh[0] = __builtin_fmaf(dp * get(wp[i], e), hv, sh[0]);
-        acc[0][i][e] = __builtin_fmaf(gv, rv * k, acc[0][i][e]);
-        acc[1][i][e] = __builtin_fmaf(dp, hv * kp, acc[1][i][e]);
-        // scale dr p; the parameter may be zero, so not dp p / vec
-        acc[2][i][e] = __builtin_fmaf(a.scale * dr[i][e], hv * kp * get(wp[i], e), acc[2][i][e]);
+      for (int e = 0; e < E; ++e) {
+        const float rv = get(res[i], e), hv = get(h[i], e), gw = get(go[i], e) * get(w[i], e);
+        sum[0] = __builtin_fmaf(rv, rv, sum[0]);
+        sum[1] = __builtin_fmaf(gw, rv, sum[1]);
+        if (post) {
+          const float fh = get(vec[i], e) * get(wp[i], e) * hv;
+          sum[2] = __builtin_fmaf(hv, hv, sum[2]);
+          sum[3] = __builtin_fmaf(get(up[i], e), fh, sum[3]);
+          sum[4] = __builtin_fmaf(gw, fh, sum[4]);
+          sum[5] = __builtin_fmaf(rv, fh, sum[5]);
+        }
       }
     }
-    if (row + gridDim.x < a.rows) load(row + gridDim.x);
-    float m = 0.0f;
+    if (kAhead && row + gridDim.x < a.rows) load(row + gridDim.x);
+    float kp = 1.0f, m = 0.0f;
     if (post) {
-      group_sums(sh, red, turn);
-      m = kp * kp * (sh[0] / n);
+      group_sums(sum, red, turn);
+    } else {
+      float two[2] = {sum[0], sum[1]};
+      group_sums(two, red, turn);
+      sum[0] = two[0];
+      sum[1] = two[1];
+    }
+    const float k = rsqrtf(sum[0] / n + a.eps), km = k * k * (sum[1] / n);
+    if (post) {
+      kp = rsqrtf(sum[2] / n + a.eps);
+      m = kp * kp * ((sum[3] + k * (sum[4] - km * sum[5])) / n);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + threadIdx.x) * 8;
-      if (c < n) store_8(dres + row * n + c, n - c, dr[i]);
+      const int c = (i * T + threadIdx.x) * E;
+      float dr[E], gh[E];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float dp = dr[i][e] * get(vec[i], e);
-        dr[i][e] = post ? kp * (dp * get(wp[i], e) - get(hr[i], e) * m) : dp;
+      for (int e = 0; e < E; ++e) {
+        const float rv = get(rr[i], e), gv = get(gr[i], e), hv = get(hr[i], e);
+        dr[e] = get(ur[i], e) + k * (gv * get(w[i], e) - rv * km);
+        const float dp = dr[e] * get(vec[i], e), hk = hv * kp;
+        acc[0][i][e] = __builtin_fmaf(gv, rv * k, acc[0][i][e]);
+        acc[1][i][e] = __builtin_fmaf(dp, hk, acc[1][i][e]);
+        // scale dr p; the parameter may be zero, so not dp p / vec
+        acc[2][i][e] = __builtin_fmaf(a.scale * dr[e], hk * get(wp[i], e), acc[2][i][e]);
+        gh[e] = post ? kp * (dp * get(wp[i], e) - hv * m) : dp;
       }
-      if (c < n) store_8(dh + row * n + c, n - c, dr[i]);
+      if (c < n) {
+        store_raw<E>(dres + row * n + c, n - c, dr);
+        store_raw<E>(dh + row * n + c, n - c, gh);
+      }
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * T + threadIdx.x) * 8;
+    const int c = (i * T + threadIdx.x) * E;
     if (c < n)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) store_8(part + (static_cast<int64_t>(blockIdx.x) * 3 + k) * n + c, n - c, acc[k][i]);
+      for (int k = 0; k < 3; ++k) store_raw<E>(part + (static_cast<int64_t>(blockIdx.x) * 3 + k) * n + c, n - c, acc[k][i]);
   }
 }
 
