@@ -3,12 +3,12 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <type_traits>
 
 #include <stdint.h>
 
-#include <cmath>
 
 #include "mambamix.h"
 #include "mm_device.h"
@@ -64,13 +64,17 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   if (p.mma) {
     // Whole sequences where they alone give the GPU its workgroups twice over (the backward, whose two walks store
     // every block's state, is as fast with one per CU: 8 x 2048 tokens, 24 heads, 415 us whole, 490 cut); else
-    // stretches of equal length, as many as the GPU runs workgroups at once (two walks per CU, of two 64-channel blocks, or four state
-    // walks of one), so that all end together.  A stretch's state costs as much traffic as 128 tokens of it: none is
-    // shorter than 512 tokens.
+    // stretches of equal length, as many as the GPU runs workgroups at once (two walks per CU, of two 64-channel
+    // blocks, or four state walks of one), so that all end together.  Short calls have fewer: a walk's time grows with
+    // its length L, the carries' with the T / L states of every pair of blocks, and sqrt(T pairs / 2) is near the least sum
+    // (64 heads in 8 groups, N 128: 1024 tokens 67 us in stretches of 512, 47 of 256, 44 of 128; 2048 tokens 69, 60,
+    // 67; 4096 84, 87, 87).  The backward, with three times the carries, gains nothing below 512 (512 tokens 72 us,
+    // cut to 256 87; 4096 tokens 337 and 373).
     const int64_t pairs = H > 0 ? G * cdiv(H / G * cdiv(P, 64), 2) : 1;
     const int64_t walks = std::max<int64_t>(1, 2 * kCUs / pairs);
     const bool whole = backward ? S * H * cdiv(P, 64) * 2 >= kCUs : S * pairs >= kMmaWorkgroups;
-    p.Ls = std::max<int64_t>(512, cdiv(cdiv(T, walks), kMmaTok) * kMmaTok);
+    const int64_t least = backward ? 512 : static_cast<int64_t>(std::sqrt(0.5 * T * pairs));
+    p.Ls = std::max<int64_t>(1, cdiv(std::max(least, cdiv(T, walks)), kMmaTok)) * kMmaTok;
     if (whole || p.Ls >= T) p.Ls = (T / kMmaTok + 1) * kMmaTok;
   }
   p.whole = p.Ls > T;
