@@ -61,8 +61,9 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int dir = blockIdx.y;
-  const int vh = blockIdx.x % (hp.H * q.npb);
-  SegmentWalk walk(hp.cu, hp.S, blockIdx.x / (hp.H * q.npb), q.Ls, q.whole != 0);
+  const int wg = xcd_unit(blockIdx.x, gridDim.x, hp.H / q.G * q.npb);
+  const int vh = wg % (hp.H * q.npb);
+  SegmentWalk walk(hp.cu, hp.S, wg / (hp.H * q.npb), q.Ls, q.whole != 0);
   const Tok<uint16_t> tu = q.u[dir], tv = q.v[dir];
 
   const int h = vh / q.npb, p0 = (vh % q.npb) * 64, group = h / (hp.H / q.G);

@@ -192,6 +192,17 @@ __device__ __forceinline__ uint32_t not_finite(hu4 v) {
   return f;
 }
 
+// Workgroups are dealt to the eight XCDs in turn, each with an L2 of its own.  Those of one unit (`size` neighbours,
+// which read the same B and C) go to one XCD, so that its L2 serves all but the first; the units go in turn.  A number
+// of units that eight does not divide leaves the last ones as they come.
+__device__ __forceinline__ int xcd_unit(int b, int blocks, int size) {
+  constexpr int kXcds = 8;
+  const int even = blocks / size / kXcds * kXcds * size;
+  if (b >= even) return b;
+  const int i = b / kXcds;
+  return (i / size * kXcds + b % kXcds) * size + i % size;
+}
+
 template <int NK, int PARTS, bool VEC>
 __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar hp) {
   typedef MmaGeo<NK> G;
@@ -204,8 +215,9 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   const int tid = threadIdx.x;
   int lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pair = blockIdx.x % q.pairs;
-  SegmentWalk walk(hp.cu, hp.S, blockIdx.x / q.pairs, q.Ls, PARTS == 3);
+  const int wg = xcd_unit(blockIdx.x, gridDim.x, q.ppg);
+  const int pair = wg % q.pairs;
+  SegmentWalk walk(hp.cu, hp.S, wg / q.pairs, q.Ls, PARTS == 3);
 
   // the wave's block of head channels, and where its columns lie
   const int group = pair / q.ppg, blk = wave >> 1;
