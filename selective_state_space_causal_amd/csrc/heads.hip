@@ -1,5 +1,6 @@
 // The head scan and the norms around a mixer block: argument checks, plans and launches of the
-// entry points declared in include/mambamix.h.  The kernels are in mm_heads.h and mm_norm.h.
+// entry points declared in include/mambamix.h.  The kernels are in mm_heads.h
+// (token by token, decode), mm_heads_mma.h, mm_heads_grad.h (matrix cores) and mm_norm.h.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -41,9 +42,9 @@ struct HeadsPlan {
   int npb, nk, splits;  // matrix-core backward: 64-channel blocks per head, 32-column steps of N, shares of a group's heads
 };
 
-// A workgroup of the sequential kernels walks one segment, about 0.13 us a token, so few long sequences are cut until
-// some four workgroups are on every CU, down to 64 tokens (777 tokens in 8 sequences, 6 heads: segments of 256 tokens
-// 87 us, of 64 30 us).
+// A workgroup of the sequential kernels walks one segment token by token, so few long sequences are cut until some four
+// workgroups are on every CU, down to 64 tokens (777 tokens in 8 sequences, 6 heads: segments of 256 tokens took 87 us
+// where those of 64 took 30).
 constexpr int64_t kSeqWorkgroups = 1024;
 
 // The matrix-core kernels take bfloat16 io and N <= 128.  Their workgroups take two 64-channel blocks of
@@ -63,7 +64,7 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   if (want <= S || p.Ls >= T) p.Ls = (T / kHeadsBlock + 1) * kHeadsBlock;
   if (p.mma) {
     // Whole sequences where they alone give the GPU its workgroups twice over (the backward, whose two walks store
-    // every block's state, is as fast with one per CU: 8 x 2048 tokens, 24 heads, 415 us whole, 490 cut); else
+    // every block's state, is as fast with one per CU: 8 x 2048 tokens, 24 heads, 415 us whole where cut took 490); else
     // stretches of equal length, as many as the GPU runs workgroups at once (two walks per CU, of two 64-channel
     // blocks, or four state walks of one), so that all end together.  Short calls have fewer: a walk's time grows with
     // its length L, the carries' with the T / L states of every pair of blocks, and sqrt(T pairs / 2) is near the least sum

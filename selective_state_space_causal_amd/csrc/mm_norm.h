@@ -11,6 +11,10 @@
 // partial sum per workgroup, added in a fixed order by k_norm_parts.
 // Rows may start anywhere: wide accesses need no alignment here, and a row's last piece is taken
 // element by element.
+// Measured, as the fraction of a plain copy's 6.2 TB/s: gate_norm 16384 x 4096 75 us (0.88), residual_norm
+// 16384 x 2048 with a float32 residual 73 us (0.91); their backward 8192 x 5120 in 8 groups 88 us (0.78: VALU issue 70%,
+// two exponential-class operations an element and 17% idle lanes) and 8191 x 2560 89 us (0.70: a row is one barrier and
+// twelve loaded bytes a column, then its stores; 6 us of it add up the weights' partial sums).
 #pragma once
 
 #include "mm_device.h"
