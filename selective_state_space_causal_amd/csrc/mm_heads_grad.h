@@ -233,8 +233,8 @@ struct GradGeo {
 // grid: (block, group, share of its heads)
 // B, C and the scores C . B stay for all heads of the workgroup, x, dy and the two states of the next head are loaded
 // under this one's products.  8 x 2048 tokens, 24 heads: 240 us, of which its traffic (0.96 GB, the states mostly) would
-// be 156 at the copy's rate.  A head is a chain of products between barriers, and two workgroups (256 registers, 45 of
-// them spilled outside the products; 81 KB of LDS) cover it in part: waves wait 71% of their cycles, VALU issue 24%,
+// be 156 at the copy's rate.  A head is a chain of products between barriers, and two workgroups (256 registers, 45
+// more spilled; 81 KB of LDS) cover it in part: waves wait 71% of their cycles, VALU issue 24%,
 // MFMA 11%.
 template <int NK, bool VEC>
 __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, HeadPar hp) {
