@@ -211,11 +211,15 @@ int by_steps(int nk, bool vec, F f) {
 }
 
 template <bool LOCAL>
-int launch_states(const StateArgs& q, const HeadPar& hp, int64_t rows, int nk, int dirs, bool vec, hipStream_t st) {
-  return by_steps(nk, vec, [&](auto k, auto v) -> int {
+int launch_states(StateArgs q, const HeadPar& hp, int64_t rows, int nk, int dirs, bool vec, hipStream_t st) {
+  // Two slices of the columns where the walks alone are at most two per CU: a block's chain is then shorter and more
+  // chains overlap, but x is read and weighted twice.  Backward of 512 tokens of 64 heads 72 us whole, 64 in slices, of
+  // four sequences of 5100 474 and 449; with four walks per CU (4096 tokens) 327 and 330, with eight 613 and 629.
+  q.slices = nk == 4 && rows * hp.H * q.npb * dirs <= 2 * kCUs ? 2 : 1;
+  return by_steps(nk / q.slices, vec, [&](auto k, auto v) -> int {
     constexpr int NK = decltype(k)::value;
     constexpr bool VEC = decltype(v)::value;
-    const dim3 grid(static_cast<unsigned>(rows * hp.H * q.npb), static_cast<unsigned>(dirs));
+    const dim3 grid(static_cast<unsigned>(rows * hp.H * q.npb * q.slices), static_cast<unsigned>(dirs));
     if (grid.x > 0)
       hipLaunchKernelGGL((k_heads_states<NK, VEC, LOCAL>), grid, dim3(kMmaThreads), StateGeo<NK>::bytes, st, q, hp);
     return MM_OK;

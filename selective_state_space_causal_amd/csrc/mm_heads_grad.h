@@ -28,6 +28,7 @@ namespace mm {
 struct StateArgs {
   Tok<uint16_t> u[2], v[2];   // forward x, B; reverse dy, C
   int P, N, G, npb;
+  int slices;                 // of the state's columns, 32 NK each, a workgroup for each
   int64_t Ls;
   int whole;                  // Ls > T
   const float* init[2];       // [S] states, or NULL: zeros
@@ -46,7 +47,7 @@ struct StateGeo {
   static constexpr int B = 0, X = kMmaTok * NP * 2, F = X + kMmaTok * kMmaTok * 2, bytes = F + 2 * (kMmaTok + 4) * 4;
 };
 
-// grid: (row, 64-channel block) x direction; a wave takes 16 of the channels
+// grid: (row, 64-channel block, slice) x direction; a wave takes 16 of the channels
 // The storing walks of 8 x 2048 tokens, 24 heads 64 x 128, both directions, write 403 MB of states in 146 us (3.6 TB/s
 // of all traffic): 384 workgroups, one or two to a CU, each with a block's load, decay, product and store in one
 // chain.  The local walks of 16384 tokens, 64 heads, take 91 us: VALU issue 34%, MFMA 23%, the rest waits
@@ -65,9 +66,9 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int dir = blockIdx.y;
-  const int wg = xcd_unit(blockIdx.x, gridDim.x, hp.H / q.G * q.npb);
-  const int vh = wg % (hp.H * q.npb);
-  SegmentWalk walk(hp.cu, hp.S, wg / (hp.H * q.npb), q.Ls, q.whole != 0);
+  const int wg = xcd_unit(blockIdx.x, gridDim.x, hp.H / q.G * q.npb * q.slices);
+  const int n0 = wg % q.slices * G::NP, vh = wg / q.slices % (hp.H * q.npb);
+  SegmentWalk walk(hp.cu, hp.S, wg / q.slices / (hp.H * q.npb), q.Ls, q.whole != 0);
   const Tok<uint16_t> tu = q.u[dir], tv = q.v[dir];
 
   const int h = vh / q.npb, p0 = (vh % q.npb) * 64, group = h / (hp.H / q.G);
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
     if (from != nullptr && p < pw)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int n = 16 * nt + 4 * g;
+        const int n = n0 + 16 * nt + 4 * g;
         const float* a = from + h * PN + static_cast<int64_t>(p0 + p) * q.N + n;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -98,9 +99,9 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
 
   const int brow = tid / PC, bcol = (tid % PC) * 8;
   constexpr int bstep = kMmaThreads / PC;
-  const int xrow = tid >> 3, xcol = (tid & 7) * 8, xn = pw - xcol, bn = q.N - bcol;
+  const int xrow = tid >> 3, xcol = (tid & 7) * 8, xn = pw - xcol, bn = q.N - n0 - bcol;
   const int dH = hp.H * q.P, gn = (hp.H / tv.div) * q.N;
-  const int b_off = (brow * static_cast<int>(tv.ts) + group * q.N + bcol) * 2;
+  const int b_off = (brow * static_cast<int>(tv.ts) + group * q.N + n0 + bcol) * 2;
   const int x_off = (xrow * static_cast<int>(tu.ts) + h * q.P + p0 + xcol) * 2;
   hu4 rB[NK], rX[2];
   const auto load = [&](int64_t tb, int cnt) {
@@ -172,7 +173,8 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
       load_dt(t2, c2);
     }
     if (!LOCAL) {  // as it lies in the registers: 1024 contiguous bytes a tile
-      float* o = q.store[dir] + ((sg.s + b) * hp.H * q.npb + vh) * (64 * G::NP) + wave * (16 * G::NP) + lane * 4;
+      const int np16 = q.slices * (16 * G::NP);  // of 16 channels
+      float* o = q.store[dir] + ((sg.s + b) * hp.H * q.npb + vh) * (4 * np16) + wave * np16 + 16 * n0 + lane * 4;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<hf4*>(o + 256 * nt) = st[nt];
     }
@@ -199,13 +201,13 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   if (to != nullptr && p < pw)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int n = 16 * nt + 4 * g;
+      const int n = n0 + 16 * nt + 4 * g;
       float* a = to + h * PN + static_cast<int64_t>(p0 + p) * q.N + n;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (n + r < q.N) a[r] = st[nt][r];
     }
-  if (LOCAL && wave == 0 && lane == 0 && p0 == 0) q.decay[dir][rho * hp.H + h] = static_cast<float>(dsum);
+  if (LOCAL && wave == 0 && lane == 0 && p0 == 0 && n0 == 0) q.decay[dir][rho * hp.H + h] = static_cast<float>(dsum);
   __syncthreads();  // the last chunk's weights are read until here
   }
 }
