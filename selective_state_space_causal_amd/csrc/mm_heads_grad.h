@@ -48,10 +48,10 @@ struct StateGeo {
 };
 
 // grid: (row, 64-channel block, slice) x direction; a wave takes 16 of the channels
-// The storing walks of 8 x 2048 tokens, 24 heads 64 x 128, both directions, write 403 MB of states in 146 us (3.6 TB/s
-// of all traffic): 384 workgroups, one or two to a CU, each with a block's load, decay, product and store in one
-// chain.  The local walks of 16384 tokens, 64 heads, take 91 us: VALU issue 34%, MFMA 23%, the rest waits
-// in the chain of a block (load, LDS, weights, product); shorter stretches would add carries.
+// The storing walks are bound by their stores: 8 x 2048 tokens, 24 heads 64 x 128, both directions, write 403 MB of
+// states in 108 to 125 us.  States pass the caches by, on the way out and in: the whole backward 382 us where plain accesses
+// took 397 (4 x 2048 tokens 227 and 262).  The local walks of 16384 tokens, 64 heads, take 91 us: VALU issue 34%, MFMA
+// 23%, the rest waits in the chain of a block (load, LDS, weights, product); shorter stretches would add carries.
 // LOCAL: what a segment adds to a zero state; else the whole walk, which stores.
 // (The two are told apart at compile time so that the stores' place among the outstanding accesses is known: a wait
 // for the tile loads then leaves the stores in flight.)
@@ -172,11 +172,11 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
       block(k + 2, t2, c2);
       load_dt(t2, c2);
     }
-    if (!LOCAL) {  // as it lies in the registers: 1024 contiguous bytes a tile
+    if (!LOCAL) {  // as it lies in the registers, 1024 contiguous bytes a tile; read once, by the next kernel: past the caches
       const int np16 = q.slices * (16 * G::NP);  // of 16 channels
       float* o = q.store[dir] + ((sg.s + b) * hp.H * q.npb + vh) * (4 * np16) + wave * np16 + 16 * n0 + lane * 4;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<hf4*>(o + 256 * nt) = st[nt];
+      for (int nt = 0; nt < NT; ++nt) nt_store(st[nt], reinterpret_cast<hf4*>(o + 256 * nt));
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) st[nt] *= el;
@@ -234,10 +234,10 @@ struct GradGeo {
 
 // grid: (block, group, share of its heads)
 // B, C and the scores C . B stay for all heads of the workgroup, x, dy and the two states of the next head are loaded
-// under this one's products.  8 x 2048 tokens, 24 heads: 240 us, of which its traffic (0.96 GB, the states mostly) would
-// be 156 at the copy's rate.  A head is a chain of products between barriers, and two workgroups (256 registers, 45
-// more spilled; 81 KB of LDS) cover it in part: waves wait 71% of their cycles, VALU issue 24%,
-// MFMA 11%.
+// under this one's products.  8 x 2048 tokens, 24 heads: 220 to 245 us, of which its traffic (0.84 GB, the
+// states mostly) would be 136 at the copy's rate.  A head is a chain of products between barriers, and two workgroups
+// (256 registers, 45 more spilled; 81 KB of LDS) cover it in part: waves wait 66% of their cycles, VALU issue 27%, MFMA
+// 12%.
 template <int NK, bool VEC>
 __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, HeadPar hp) {
   typedef GradGeo<NK> G;
@@ -333,8 +333,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       hf4 s[NK][2];
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        s[k][0] = *reinterpret_cast<const hf4*>(q.hs + srow + 512 * k);
-        s[k][1] = *reinterpret_cast<const hf4*>(q.hs + srow + 512 * k + 64);
+        s[k][0] = nt_load(reinterpret_cast<const hf4*>(q.hs + srow + 512 * k));
+        s[k][1] = nt_load(reinterpret_cast<const hf4*>(q.hs + srow + 512 * k + 64));
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -447,8 +447,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       hf4 a[NK][2];
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        a[k][0] = *reinterpret_cast<const hf4*>(q.gs + srow + 512 * k);
-        a[k][1] = *reinterpret_cast<const hf4*>(q.gs + srow + 512 * k + 64);
+        a[k][0] = nt_load(reinterpret_cast<const hf4*>(q.gs + srow + 512 * k));
+        a[k][1] = nt_load(reinterpret_cast<const hf4*>(q.gs + srow + 512 * k + 64));
       }
       __builtin_amdgcn_sched_barrier(0);
       // dx within the block: rows p = 16 wave + 4g + r, columns j = 16 jt + li
