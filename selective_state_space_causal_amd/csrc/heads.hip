@@ -35,6 +35,7 @@ struct HeadsPlan {
   bool whole;      // every sequence is one segment
   int64_t rows;    // segments at most
   int64_t walks;   // matrix-core kernels: sequences, or stretches of Ls tokens
+  int64_t even;    // not 0: both ways are launched, and the whole sequences run if none is longer than this
   int64_t rows64;  // 64-token blocks at most (backward)
   int nrp, nrn;    // 16-row blocks of P and N
   size_t off_carry, off_decay, off_carry2, off_decay2, off_hb, off_dots, off_dB, off_dC, off_q, off_r, off_delta,
@@ -50,7 +51,9 @@ constexpr int64_t kSeqWorkgroups = 1024;
 // The matrix-core kernels take bfloat16 io and N <= 128.  Their workgroups take two 64-channel blocks of
 // a group; two workgroups fit on a CU.
 constexpr int kMmaMaxN = 128;
-constexpr int64_t kMmaWorkgroups = 1024;
+constexpr int64_t kMmaWorkgroups = 512;
+// Prefill: up to so many sequences the device chooses between whole sequences and stretches, by the longest one.
+constexpr int64_t kMmaMaxEven = 256;
 
 int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, int io, bool backward, int64_t max_stride) {
   p = HeadsPlan{};
@@ -63,8 +66,10 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   p.Ls = std::max<int64_t>(kHeadsBlock, cdiv(cdiv(T, std::max<int64_t>(want, 1)), kHeadsBlock) * kHeadsBlock);
   if (want <= S || p.Ls >= T) p.Ls = (T / kHeadsBlock + 1) * kHeadsBlock;
   if (p.mma) {
-    // Whole sequences where they alone give the GPU its workgroups twice over (the backward, whose two walks store
-    // every block's state, is as fast with one per CU: 8 x 2048 tokens, 24 heads, 415 us whole where cut took 490); else
+    // Prefill: whole sequences where they alone give the GPU its workgroups and none is longer than two stretches, which
+    // the kernels of both ways find out (16 x 1024 tokens, 64 heads in 8 groups: whole 158 us, cut 254; 24 x 100 54 and
+    // 167; but one long sequence among short ones would be one long chain).  The backward, whose two walks store every
+    // block's state, takes them with one workgroup per CU (8 x 2048 tokens, 24 heads, 415 us where cut took 490).  Else
     // stretches of equal length, as many as the GPU runs workgroups at once (two walks per CU, of two 64-channel
     // blocks, or four state walks of one), so that all end together.  Short calls have fewer: a walk's time grows with
     // its length L, the carries' with the T / L states of every pair of blocks, and sqrt(T pairs / 2) is near the least sum
@@ -73,10 +78,12 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
     // cut to 256 87; 4096 tokens 337 and 373).
     const int64_t pairs = H > 0 ? G * cdiv(H / G * cdiv(P, 64), 2) : 1;
     const int64_t walks = std::max<int64_t>(1, 2 * kCUs / pairs);
-    const bool whole = backward ? S * H * cdiv(P, 64) * 2 >= kCUs : S * pairs >= kMmaWorkgroups;
+    const bool enough = backward ? S * H * cdiv(P, 64) * 2 >= kCUs : S * pairs >= kMmaWorkgroups;
+    const bool whole = enough && (backward || S > kMmaMaxEven);
     const int64_t least = backward ? 512 : static_cast<int64_t>(std::sqrt(0.5 * T * pairs));
     p.Ls = std::max<int64_t>(1, cdiv(std::max(least, cdiv(T, walks)), kMmaTok)) * kMmaTok;
     if (whole || p.Ls >= T) p.Ls = (T / kMmaTok + 1) * kMmaTok;
+    else if (enough && !backward) p.even = 2 * p.Ls;
   }
   p.whole = p.Ls > T;
   p.npb = static_cast<int>(cdiv(P, 64));
@@ -170,10 +177,9 @@ void launch_seq_both(const SeqRun<IO>& f, const SeqRun<IO>& r, const HeadPar& hp
 
 // dirs: 1, the forward states, or 2, the adjoints too
 void launch_carry(const Carry& c, const HeadPar& hp, int64_t PN, int64_t Ls, int dirs, bool all, hipStream_t st) {
-  for (int s0 = 0; s0 < hp.S; s0 += 65535)
-    hipLaunchKernelGGL(k_heads_carry, dim3(static_cast<unsigned>(cdiv(hp.H * PN, 256)),
-                                           static_cast<unsigned>(std::min(hp.S - s0, 65535)), static_cast<unsigned>(dirs)),
-                       dim3(256), 0, st, c, hp.cu, hp.H, PN, Ls, all ? 1 : 0, s0);
+  hipLaunchKernelGGL(k_heads_carry, dim3(static_cast<unsigned>(cdiv(hp.H * PN, 256)),
+                                         static_cast<unsigned>(std::min(hp.S, 8)), static_cast<unsigned>(dirs)),
+                     dim3(256), 0, st, c, hp.cu, hp.H, PN, Ls, all ? 1 : 0, hp.S);
 }
 
 struct HeadsArgs {
@@ -262,7 +268,15 @@ int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* stat
     const int rc = launch_mma<3>(q, a.hp, p.walks, p.nk, vec, st);
     return rc != MM_OK ? rc : launched();
   }
+  q.even = p.even;
+  if (p.even > 0) {
+    MmaArgs w = q;
+    w.Ls = a.hp.T + 1;
+    const int rc = launch_mma<3>(w, a.hp, a.hp.S, p.nk, vec, st);
+    if (rc != MM_OK) return rc;
+  }
   StateArgs s{};
+  s.even = p.even;
   s.u[0] = q.x;
   s.v[0] = q.B;
   s.P = q.P;
@@ -276,7 +290,7 @@ int launch_prefill_mma(const HeadsPlan& p, const HeadsArgs& a, const float* stat
   q.carry = s.carry[0];
   int rc = launch_states<true>(s, a.hp, p.walks, p.nk, 1, vec, st);
   if (rc != MM_OK) return rc;
-  launch_carry({{s.carry[0]}, {s.decay[0]}, {state_in}, {state_out}}, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, 1, true, st);
+  launch_carry({{s.carry[0]}, {s.decay[0]}, {state_in}, {state_out}, p.even}, a.hp, static_cast<int64_t>(a.P) * a.N, p.Ls, 1, true, st);
   rc = launch_mma<1>(q, a.hp, p.walks, p.nk, vec, st);
   return rc != MM_OK ? rc : launched();
 }

@@ -86,6 +86,13 @@ struct SegmentWalk {
     return false;
   }
 };
+// whether a sequence has more than `limit` tokens: the choice between two ways that the host, which does not know the
+// lengths, leaves to the kernels of both; every wave finds it by itself
+__device__ __forceinline__ bool longer_than(const int32_t* __restrict__ cu, int S, int64_t limit) {
+  int any = 0;
+  for (int s = threadIdx.x & 63; s < S; s += kWave) any |= static_cast<int64_t>(cu[s + 1]) - cu[s] > limit;
+  return __any(any) != 0;
+}
 // rows of a per-segment array for S sequences and T tokens
 inline int64_t segment_rows(int64_t S, int64_t T, int64_t L) { return S + T / L; }
 
@@ -316,21 +323,23 @@ struct Carry {
   float* carry[2];
   const float *decay[2], *init[2];
   float* fin[2];
+  int64_t even;  // not 0: only if a sequence is longer
 };
 __global__ __launch_bounds__(256) void k_heads_carry(Carry c, const int32_t* __restrict__ cu, int H, int64_t PN,
-                                                     int64_t Ls, int all, int s0) {
+                                                     int64_t Ls, int all, int S) {
+  if (c.even > 0 && !longer_than(cu, S, c.even)) return;
   const int reverse = blockIdx.z;
   float* const carry = c.carry[reverse];
   const float *const decay = c.decay[reverse], *const init = c.init[reverse];
   float* const fin = c.fin[reverse];
-  const int s = s0 + blockIdx.y;
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t set = H * PN;
   if (e >= set) return;
+  for (int s = blockIdx.y; s < S; s += gridDim.y) {
   const uint32_t L = static_cast<uint32_t>(Ls), seq0 = cu[s], seq1 = cu[s + 1];
   const int n = seq1 > seq0 ? static_cast<int>((seq1 - 1) / L - seq0 / L) + 1 : 0;
   if (!all && n == 0 && fin != nullptr) fin[s * set + e] = init != nullptr ? init[s * set + e] : 0.0f;
-  if (!all && n < 2) return;
+  if (!all && n < 2) continue;
   const int h = static_cast<int>(e / PN);
   const int64_t r0 = s + static_cast<int64_t>(seq0 / L), step = reverse ? -1 : 1;
   int64_t rho = reverse ? r0 + n - 1 : r0;
@@ -355,6 +364,7 @@ __global__ __launch_bounds__(256) void k_heads_carry(Carry c, const int32_t* __r
       }
   }
   if (all) fin[s * set + e] = cur;
+  }
 }
 
 // ------------------------------------------------------------------------------------ decode

@@ -39,6 +39,7 @@ struct StateArgs {
   float* store[2];
   float* fin[2];              // [S] final states, or NULL
   int all;                    // local runs: every segment, not only those that another one follows
+  int64_t even;               // not 0: only if a sequence is longer
 };
 
 template <int NK>
@@ -63,6 +64,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   char *const sB = lds + G::B, *const sX = lds + G::X;
   float* const sF = reinterpret_cast<float*>(lds + G::F);  // two sets of [block][64] weights and [block] last decays
 
+  if (q.even > 0 && !longer_than(hp.cu, hp.S, q.even)) return;
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int dir = blockIdx.y;

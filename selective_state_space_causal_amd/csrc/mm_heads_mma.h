@@ -61,6 +61,7 @@ struct MmaArgs {
   float* state_out;
   const float* carry;  // [rows] the states of the segments' starts, or NULL: whole sequences from state_in
   uint16_t* y;
+  int64_t even;  // not 0: whole sequences (PARTS = 3) only if none is longer, stretches only if one is
 };
 
 // Tiles in LDS are rows of PC 16-byte pieces without padding.  Piece c of row r lies at c ^ swz(r): for any
@@ -219,6 +220,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   float* const sF = reinterpret_cast<float*>(lds + G::F);  // two sets: this chunk's and the next one's
   int* const sFlag = reinterpret_cast<int*>(sF + 2 * kMmaFSet);
 
+  if (q.even > 0 && longer_than(hp.cu, hp.S, q.even) == (PARTS == 3)) return;
   const int tid = threadIdx.x;
   int lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
