@@ -490,12 +490,16 @@ int check_arrays(const Array* a, int n) {
     if (!aligned(a[i].r.p, a[i].es)) return MM_ERR_ALIGN;
   return MM_OK;
 }
-// no output on an input or another output; same: an output may be this input itself
-int check_overlap(const Array* in, int ni, const Array* out, int no, const void* same = nullptr) {
+// an output that may be an input itself (in place), by their places in the call's lists
+struct InPlace {
+  int out, in;
+};
+// no output on an input or another output, but an output at the very address of the input it may replace
+int check_overlap(const Array* in, int ni, const Array* out, int no, InPlace same = {-1, -1}) {
   for (int i = 0; i < no; ++i) {
     if (out[i].r.p == nullptr) continue;
     for (int k = 0; k < ni; ++k) {
-      if (in[k].r.p == nullptr || (same != nullptr && out[i].r.p == same && in[k].r.p == same)) continue;
+      if (in[k].r.p == nullptr || (i == same.out && k == same.in && out[i].r.p == in[k].r.p)) continue;
       if (overlap(out[i].r, in[k].r)) return MM_ERR_ALIAS;
     }
     for (int k = i + 1; k < no; ++k)
@@ -625,7 +629,7 @@ int mamba_mixer_heads_prefill(const void* x, const void* dt, const void* B, cons
                       {flat(cu_seqlens, (static_cast<size_t>(S) + 1) * 4), 4, false}, {flat(state_in, ns), 4, true}};
   const Array out[] = {{flat(y, static_cast<size_t>(T) * d * es), es, false}, {flat(state_out, ns), 4, false}};
   if ((rc = check_arrays(in, 9)) != MM_OK || (rc = check_arrays(out, 2)) != MM_OK) return rc;
-  if ((rc = check_overlap(in, 9, out, 2, state_in)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 9, out, 2, {1, 8})) != MM_OK) return rc;
   HeadsPlan p;
   if ((rc = plan_heads(p, S, T, H, P, G, N, io_dtype, false, std::max({x_stride, b_stride, c_stride}))) != MM_OK) return rc;
   if (p.total > 0 && (workspace == nullptr || workspace_bytes < p.total)) return MM_ERR_WORKSPACE;
@@ -655,7 +659,7 @@ int mamba_mixer_heads_decode(const void* x, const void* dt, const void* B, const
                       {flat(dt_bias, dt != nullptr ? nh : 0), 4, false}, {flat(state_in, ns), 4, true}};
   const Array out[] = {{flat(y, static_cast<size_t>(Bs) * d * es), es, false}, {flat(state_out, ns), 4, false}};
   if ((rc = check_arrays(in, 8)) != MM_OK || (rc = check_arrays(out, 2)) != MM_OK) return rc;
-  if ((rc = check_overlap(in, 8, out, 2, state_in)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 8, out, 2, {1, 7})) != MM_OK) return rc;
   const HeadPar hp{dt, dt_stride, A_log, dt_bias, D, nullptr, Bs, H, Bs};
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool vec = N % 4 == 0 && aligned(state_in, 16) && aligned(state_out, 16);
@@ -754,7 +758,7 @@ int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, voi
                       {flat(weight, static_cast<size_t>(d) * 4), 4, false}};
   const Array o[] = {{flat(out, static_cast<size_t>(nrows) * d * es), es, false}};
   if ((rc = check_arrays(in, 3)) != MM_OK || (rc = check_arrays(o, 1)) != MM_OK) return rc;
-  if ((rc = check_overlap(in, 3, o, 1, y_stride == d ? y : nullptr)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 3, o, 1, y_stride == d ? InPlace{0, 0} : InPlace{-1, -1})) != MM_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const auto go = [&](auto io) {
     using IO = decltype(io);
@@ -851,7 +855,7 @@ int mamba_mixer_residual_norm(const void* h, const void* residual, const float* 
                       {flat(post_weight, nd), 4, true}, {flat(scale_vec, nd), 4, true}};
   const Array o[] = {{flat(residual_out, n * rs), rs, false}, {flat(out, n * es), es, false}};
   if ((rc = check_arrays(in, 5)) != MM_OK || (rc = check_arrays(o, 2)) != MM_OK) return rc;
-  if ((rc = check_overlap(in, 5, o, 2, residual != out ? residual : nullptr)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 5, o, 2, {0, 1})) != MM_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return by_types(io_dtype, res_dtype, [&](auto io, auto rt) {
     using IO = decltype(io);
@@ -897,7 +901,7 @@ int mamba_mixer_residual_norm_backward(const void* dout, const void* dresidual_o
                      {flat(dpost_weight, post_weight != nullptr ? nd : 0), 4, false},
                      {flat(dscale_vec, scale_vec != nullptr ? nd : 0), 4, false}};
   if ((rc = check_arrays(in, 7)) != MM_OK || (rc = check_arrays(o, 5)) != MM_OK) return rc;
-  if ((rc = check_overlap(in, 7, o, 5, dresidual == dresidual_out ? dresidual_out : nullptr)) != MM_OK) return rc;
+  if ((rc = check_overlap(in, 7, o, 5, {0, 1})) != MM_OK) return rc;
   const size_t need = mamba_mixer_residual_norm_backward_workspace_bytes(nrows, d);
   if (workspace == nullptr || workspace_bytes < need) return MM_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MM_ERR_ALIGN;
