@@ -195,6 +195,23 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def new_on(stream, shape, dtype, device, returned: bool = True):
+    """An uninitialised tensor for a call that runs on ``stream`` (None: the current one).  The allocator hands memory
+    on in the order of the stream it was allocated on: memory of another stream could go to that one's next user
+    while the call still runs, or still be read there when the call writes it.  So it is allocated on the
+    call's stream, and what the caller gets (``returned``) is kept, once dropped, until the current stream has done
+    with it too."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _check(t, shape, dtype, name):
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")

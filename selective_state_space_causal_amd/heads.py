@@ -5,10 +5,15 @@ passes pointers; the computation is in the library's kernels.
 
 Token tensors may be column ranges of a wider one (a projection's output): their rows may be strided,
 the elements of a row are contiguous.
+
+With ``stream`` given the kernels run on that stream, and what a call allocates belongs to it: the workspace
+goes back to that stream's memory, and outputs may be used and dropped on the stream that was current at the call,
+once it has waited for the given one.  Ordering the inputs before the call, and keeping them until the stream has
+read them, is the caller's part, as with any work on a second stream.
 """
 from __future__ import annotations
 
-from . import MM_OK, MambaMixError, _check, _io_code, check_cu_seqlens, load
+from . import MM_OK, MambaMixError, _check, _io_code, check_cu_seqlens, load, new_on
 
 torch = _BF16 = _F32 = _raw_stream = None  # (the package can be imported without torch)
 
@@ -95,16 +100,23 @@ def _head_inputs(x, dt, B, C, A_log, D, dt_bias):
     return T, H, P, G, N, strides
 
 
-def _workspace(given, need, device):
-    if given is None:
-        given = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+def _new(shape, dtype, device, stream):
+    return torch.empty(shape, dtype=dtype, device=device) if stream is None else new_on(stream, shape, dtype, device)
+
+
+def _workspace(given, need, device, stream):
+    if given is None and need > 0:
+        if stream is None:
+            given = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            given = new_on(stream, need, torch.uint8, device, returned=False)
     return given, _opt(given), 0 if given is None else given.numel() * given.element_size()
 
 
-def _out(t, shape, dtype, device, name):
+def _out(t, shape, dtype, device, name, stream):
     """An output tensor: the caller's (rows may be strided) or a new one; returns it and its row stride."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = _new(shape, dtype, device, stream)
     return t, _rows(t, shape, dtype, name)
 
 
@@ -132,16 +144,16 @@ def heads_prefill(x, dt, B, C, A_log, D, dt_bias, cu_seqlens, state_in=None, sta
     if state_in is not None:
         _need(state_in, (S, H, P, N), _F32, "state_in")
     if state_out is None:
-        state_out = torch.empty((S, H, P, N), dtype=_F32, device=x.device)
+        state_out = _new((S, H, P, N), _F32, x.device, stream)
     else:
         _need(state_out, (S, H, P, N), _F32, "state_out")
     if y is None:
-        y = torch.empty((T, H, P), dtype=x.dtype, device=x.device)
+        y = _new((T, H, P), x.dtype, x.device, stream)
     else:
         _need(y, (T, H, P), x.dtype, "y")
     io = _code(x)
     need = _lib().mamba_mixer_heads_prefill_workspace_bytes(S, T, H, P, G, N, io) if workspace is None else 0
-    workspace, wptr, wbytes = _workspace(workspace, need, x.device)
+    workspace, wptr, wbytes = _workspace(workspace, need, x.device, stream)
     rc = _lib().mamba_mixer_heads_prefill(
         x.data_ptr(), _opt(dt), B.data_ptr(), C.data_ptr(), A_log.data_ptr(), _opt(D), _opt(dt_bias),
         cu_seqlens.data_ptr(), _opt(state_in), state_out.data_ptr(), y.data_ptr(), S, T, H, P, G, N, io, *strides,
@@ -158,11 +170,11 @@ def heads_decode(x, dt, B, C, A_log, D, dt_bias, state_in=None, state_out=None, 
     if state_in is not None:
         _need(state_in, (Bs, H, P, N), _F32, "state_in")
     if state_out is None:
-        state_out = torch.empty((Bs, H, P, N), dtype=_F32, device=x.device)
+        state_out = _new((Bs, H, P, N), _F32, x.device, stream)
     else:
         _need(state_out, (Bs, H, P, N), _F32, "state_out")
     if y is None:
-        y = torch.empty((Bs, H, P), dtype=x.dtype, device=x.device)
+        y = _new((Bs, H, P), x.dtype, x.device, stream)
     else:
         _need(y, (Bs, H, P), x.dtype, "y")
     rc = _lib().mamba_mixer_heads_decode(
@@ -191,16 +203,16 @@ def heads_backward(x, dt, B, C, A_log, D, dt_bias, cu_seqlens, state_in, dy, dst
         if t is not None:
             _need(t, (S, H, P, N), _F32, n)
     _need(dy, (T, H, P), io, "dy")
-    dx, sx = _out(dx, (T, H, P), io, dev, "dx")
-    ddt, sd = _out(ddt, (T, H), io, dev, "ddt") if dt is not None else (None, 0)
-    dB, sb = _out(dB, (T, G, N), io, dev, "dB")
-    dC, sc = _out(dC, (T, G, N), io, dev, "dC")
-    new = lambda *s: torch.empty(s, dtype=_F32, device=dev)  # noqa: E731
+    dx, sx = _out(dx, (T, H, P), io, dev, "dx", stream)
+    ddt, sd = _out(ddt, (T, H), io, dev, "ddt", stream) if dt is not None else (None, 0)
+    dB, sb = _out(dB, (T, G, N), io, dev, "dB", stream)
+    dC, sc = _out(dC, (T, G, N), io, dev, "dC", stream)
+    new = lambda *s: _new(s, _F32, dev, stream)  # noqa: E731
     dA_log, dD, dbias = new(H), new(H) if D is not None else None, new(H) if dt is not None else None
     dstate_in = new(S, H, P, N) if need_dstate else None
     code = _code(x)
     need = _lib().mamba_mixer_heads_backward_workspace_bytes(S, T, H, P, G, N, code) if workspace is None else 0
-    workspace, wptr, wbytes = _workspace(workspace, need, dev)
+    workspace, wptr, wbytes = _workspace(workspace, need, dev, stream)
     rc = _lib().mamba_mixer_heads_backward(
         x.data_ptr(), _opt(dt), B.data_ptr(), C.data_ptr(), A_log.data_ptr(), _opt(D), _opt(dt_bias),
         cu_seqlens.data_ptr(), _opt(state_in), dy.data_ptr(), _opt(dstate_out), dx.data_ptr(), _opt(ddt),
@@ -226,7 +238,7 @@ def gate_norm(y, z, weight, groups: int = 1, eps: float = 1e-5, gate_first: bool
     ranges.  y, z [rows, d] io, weight [d] float32.  Returns out [rows, d]."""
     rows, d, ys, zs = _gate_inputs(y, z, weight, groups)
     if out is None:
-        out = torch.empty((rows, d), dtype=y.dtype, device=y.device)
+        out = _new((rows, d), y.dtype, y.device, stream)
     else:
         _need(out, (rows, d), y.dtype, "out")
     rc = _lib().mamba_mixer_gate_norm(
@@ -242,11 +254,11 @@ def gate_norm_backward(dout, y, z, weight, groups: int = 1, eps: float = 1e-5, g
     strided rows)."""
     rows, d, ys, zs = _gate_inputs(y, z, weight, groups)
     _need(dout, (rows, d), y.dtype, "dout")
-    dy, dys = _out(dy, (rows, d), y.dtype, y.device, "dy")
-    dz, dzs = _out(dz, (rows, d), y.dtype, y.device, "dz")
-    dweight = torch.empty(d, dtype=_F32, device=y.device)
+    dy, dys = _out(dy, (rows, d), y.dtype, y.device, "dy", stream)
+    dz, dzs = _out(dz, (rows, d), y.dtype, y.device, "dz", stream)
+    dweight = _new((d,), _F32, y.device, stream)
     need = _lib().mamba_mixer_gate_norm_backward_workspace_bytes(rows, d, int(groups)) if workspace is None else 0
-    workspace, wptr, wbytes = _workspace(workspace, need, y.device)
+    workspace, wptr, wbytes = _workspace(workspace, need, y.device, stream)
     rc = _lib().mamba_mixer_gate_norm_backward(
         dout.data_ptr(), y.data_ptr(), z.data_ptr(), weight.data_ptr(), dy.data_ptr(), dz.data_ptr(),
         dweight.data_ptr(), rows, d, int(groups), float(eps), 1 if gate_first else 0, _code(y), ys, zs, dys, dzs,
@@ -281,13 +293,13 @@ def residual_norm(h, residual, weight, post_weight=None, scale: float = 1.0, sca
     pass residual_out=residual to update the residual in place."""
     rows, d, res = _residual_inputs(h, residual, weight, post_weight, scale_vec)
     if residual_out is None:
-        residual_out = torch.empty_like(h, dtype=res)
+        residual_out = _new((rows, d), res, h.device, stream)
     else:
         if residual is None:
             res = residual_out.dtype
         _need(residual_out, (rows, d), res, "residual_out")
     if out is None:
-        out = torch.empty_like(h)
+        out = _new((rows, d), h.dtype, h.device, stream)
     else:
         _need(out, (rows, d), h.dtype, "out")
     rc = _lib().mamba_mixer_residual_norm(
@@ -308,21 +320,21 @@ def residual_norm_backward(dout, dresidual_out, h, residual_out, weight, post_we
     if dresidual_out is not None:
         _need(dresidual_out, (rows, d), res, "dresidual_out")
     if dresidual is None:
-        dresidual = torch.empty_like(h, dtype=res)
+        dresidual = _new((rows, d), res, h.device, stream)
     else:
         _need(dresidual, (rows, d), res, "dresidual")
     if dh is None:
-        dh = torch.empty_like(h)
+        dh = _new((rows, d), h.dtype, h.device, stream)
     else:
         _need(dh, (rows, d), h.dtype, "dh")
-    new = lambda: torch.empty(d, dtype=_F32, device=h.device)  # noqa: E731
+    new = lambda: _new((d,), _F32, h.device, stream)  # noqa: E731
     got = dict(dresidual=dresidual, dh=dh, dweight=new())
     if post_weight is not None:
         got["dpost_weight"] = new()
     if scale_vec is not None:
         got["dscale_vec"] = new()
     need = _lib().mamba_mixer_residual_norm_backward_workspace_bytes(rows, d) if workspace is None else 0
-    workspace, wptr, wbytes = _workspace(workspace, need, h.device)
+    workspace, wptr, wbytes = _workspace(workspace, need, h.device, stream)
     rc = _lib().mamba_mixer_residual_norm_backward(
         dout.data_ptr(), _opt(dresidual_out), h.data_ptr(), residual_out.data_ptr(), weight.data_ptr(),
         _opt(post_weight), _opt(scale_vec), float(scale), dresidual.data_ptr(), dh.data_ptr(), got["dweight"].data_ptr(),
