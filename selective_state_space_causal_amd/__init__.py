@@ -195,7 +195,7 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def new_on(stream, shape, dtype, device, returned: bool = True):
+def _new_on(stream, shape, dtype, device, returned: bool = True):
     """An uninitialised tensor for a call that runs on ``stream`` (None: the current one).  The allocator hands memory
     on in the order of the stream it was allocated on: memory of another stream could go to that one's next user
     while the call still runs, or still be read there when the call writes it.  So it is allocated on the
@@ -251,12 +251,12 @@ def prefill(x, z, dt, B, C, A_log, D, dt_bias, conv_w, conv_b, cu_seqlens, conv_
     _check(conv_state, (S, d, CONV_K - 1), torch.float32, "conv_state")
     _check(ssm_state, (S, d, N), torch.float32, "ssm_state")
     if y is None:
-        y = torch.empty((T, d), dtype=io, device=x.device)
+        y = _new_on(stream, (T, d), io, x.device)
     _check(y, (T, d), io, "y")
     if workspace is None:  # (a caller-provided workspace is size-checked by the library)
         need = workspace_bytes(S, T, d, N, CONV_K, chunk_len, engine) if T > 0 and d > 0 and S > 0 else 0
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = _new_on(stream, need, torch.uint8, x.device, returned=False)
     wptr = _ptr(workspace) if workspace is not None else ctypes.c_void_p(0)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if events is None:
@@ -302,7 +302,7 @@ def prefill_noalloc(x, z, dt, B, C, A_log, D, dt_bias, conv_w, conv_b, cu_seqlen
     _check(conv_state, (S, d, CONV_K - 1), torch.float32, "conv_state")
     _check(ssm_state, (S, d, N), torch.float32, "ssm_state")
     if y is None:
-        y = torch.empty((T, d), dtype=io, device=x.device)
+        y = _new_on(stream, (T, d), io, x.device)
     _check(y, (T, d), io, "y")
     rc = load().mamba_mixer_prefill_noalloc(
         _ptr(x), _ptr(z), _ptr(dt), _ptr(B), _ptr(C), _ptr(A_log), _ptr(D), _ptr(dt_bias), _ptr(conv_w),
@@ -356,16 +356,16 @@ def prefill_train(x, z, dt, B, C, A_log, D, dt_bias, conv_w, conv_b, cu_seqlens,
     _check(conv_state, (S, d, CONV_K - 1), torch.float32, "conv_state")
     _check(ssm_state, (S, d, N), torch.float32, "ssm_state")
     if y is None:
-        y = torch.empty((T, d), dtype=io, device=x.device)
+        y = _new_on(stream, (T, d), io, x.device)
     _check(y, (T, d), io, "y")
     rows = (T + 15) // 16 + S
     if ckpt is None:
-        ckpt = torch.empty((rows, d, 16), dtype=torch.float32, device=x.device)
+        ckpt = _new_on(stream, (rows, d, 16), torch.float32, x.device)
     _check(ckpt, (rows, d, 16), torch.float32, "ckpt")
     if workspace is None:  # (a caller-provided workspace is size-checked by the library)
         need = workspace_bytes(S, T, d, N, CONV_K, chunk_len, ENGINE_ROW) if T > 0 and d > 0 and S > 0 else 0
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = _new_on(stream, need, torch.uint8, x.device, returned=False)
     wptr = _ptr(workspace) if workspace is not None else ctypes.c_void_p(0)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     ev, nev = (None, 0) if events is None else ((ctypes.c_void_p * len(events))(*events), len(events))
@@ -419,12 +419,12 @@ def prefill_backward(x, z, dt, B, C, A_log, D, dt_bias, conv_w, conv_b, cu_seqle
     g = dict(out) if out is not None else {}
     for k, (shape, dt_) in shapes.items():
         if k not in g:
-            g[k] = torch.empty(shape, dtype=dt_, device=x.device)
+            g[k] = _new_on(stream, shape, dt_, x.device)
         _check(g[k], shape, dt_, k)
     if workspace is None:  # (a caller-provided workspace is size-checked by the library)
         need = backward_plan(S, T, d, N, has_ckpt=ckpt is not None)["workspace"] if d > 0 else 0
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = _new_on(stream, need, torch.uint8, x.device, returned=False)
     wptr = _ptr(workspace) if workspace is not None else ctypes.c_void_p(0)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if events is None:
@@ -468,17 +468,17 @@ def project(x, conv_w, conv_b, cu_seqlens, conv_state, w_x, w_dt, dt=None, B=Non
     _check(w_x, (d, P), torch.bfloat16, "w_x")
     _check(w_dt, (R, d), torch.bfloat16, "w_dt")
     if dt is None:
-        dt = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+        dt = _new_on(stream, (T, d), torch.bfloat16, x.device)
     if B is None:
-        B = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        B = _new_on(stream, (T, N), torch.bfloat16, x.device)
     if C is None:
-        C = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        C = _new_on(stream, (T, N), torch.bfloat16, x.device)
     _check(dt, (T, d), torch.bfloat16, "dt")
     _check(B, (T, N), torch.bfloat16, "B")
     _check(C, (T, N), torch.bfloat16, "C")
     if workspace is None:  # (a caller-provided workspace is size-checked by the library)
         need = int(load().mamba_mixer_project_workspace_bytes(T, d, N, R))
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        workspace = _new_on(stream, max(need, 1), torch.uint8, x.device, returned=False)
     rc = load().mamba_mixer_project(
         _ptr(x), _ptr(conv_w), _ptr(conv_b), _ptr(cu_seqlens), _ptr(conv_state), _ptr(w_x), _ptr(w_dt), _ptr(dt),
         _ptr(B), _ptr(C), S, T, d, N, R, CONV_K, MM_IO_BF16, _ptr(workspace),
@@ -508,7 +508,7 @@ def decode(x, z, dt, B, C, A_log, D, dt_bias, conv_w, conv_b, conv_state, ssm_st
     _check(conv_state, (Bs, d, CONV_K - 1), torch.float32, "conv_state")
     _check(ssm_state, (Bs, d, N), torch.float32, "ssm_state")
     if y is None:
-        y = torch.empty((Bs, d), dtype=io, device=x.device)
+        y = _new_on(stream, (Bs, d), io, x.device)
     _check(y, (Bs, d), io, "y")
     rc = load().mamba_mixer_decode(
         _ptr(x), _ptr(z), _ptr(dt), _ptr(B), _ptr(C), _ptr(A_log), _ptr(D), _ptr(dt_bias), _ptr(conv_w),
@@ -545,7 +545,7 @@ def decode_replay(x_ring, dt_ring, B_ring, z, C, A_log, D, dt_bias, conv_w, conv
     _check(conv_state, (Bs, d, CONV_K - 1), torch.float32, "conv_state")
     _check(ssm_state, (Bs, d, N), torch.float32, "ssm_state")
     if y is None:
-        y = torch.empty((Bs, d), dtype=io, device=x_ring.device)
+        y = _new_on(stream, (Bs, d), io, x_ring.device)
     _check(y, (Bs, d), io, "y")
     rc = load().mamba_mixer_decode_replay(
         _ptr(x_ring), _ptr(dt_ring), _ptr(B_ring), _ptr(z), _ptr(C), _ptr(A_log), _ptr(D), _ptr(dt_bias),
@@ -565,9 +565,9 @@ def replay_checkpoint_lo(conv_state, ssm_state, conv_lo=None, ssm_lo=None, strea
     _check(conv_state, (Bs, d, CONV_K - 1), torch.float32, "conv_state")
     _check(ssm_state, (Bs, d, N), torch.float32, "ssm_state")
     if conv_lo is None:
-        conv_lo = torch.empty((Bs, d, 4), dtype=torch.bfloat16, device=ssm_state.device)
+        conv_lo = _new_on(stream, (Bs, d, 4), torch.bfloat16, ssm_state.device)
     if ssm_lo is None:
-        ssm_lo = torch.empty((Bs, d, N), dtype=torch.bfloat16, device=ssm_state.device)
+        ssm_lo = _new_on(stream, (Bs, d, N), torch.bfloat16, ssm_state.device)
     _check(conv_lo, (Bs, d, 4), torch.bfloat16, "conv_lo")
     _check(ssm_lo, (Bs, d, N), torch.bfloat16, "ssm_lo")
     rc = load().mamba_mixer_replay_checkpoint_lo(_ptr(conv_state), _ptr(ssm_state), _ptr(conv_lo), _ptr(ssm_lo),
@@ -602,7 +602,7 @@ def decode_replay_dual(x_ring, dt_ring, B_ring, z, C, A_log, D, dt_bias, conv_w,
     _check(conv_lo, (Bs, d, 4), torch.bfloat16, "conv_lo")
     _check(ssm_lo, (Bs, d, N), torch.bfloat16, "ssm_lo")
     if y is None:
-        y = torch.empty((Bs, d), dtype=io, device=x_ring.device)
+        y = _new_on(stream, (Bs, d), io, x_ring.device)
     _check(y, (Bs, d), io, "y")
     rc = load().mamba_mixer_decode_replay_dual(
         _ptr(x_ring), _ptr(dt_ring), _ptr(B_ring), _ptr(z), _ptr(C), _ptr(A_log), _ptr(D), _ptr(dt_bias),
@@ -633,7 +633,7 @@ def decode_replay_multi(x_ring, dt_ring, B_ring, z_ring, C_ring, A_log, D, dt_bi
     _check(conv_state, (Bs, d, CONV_K - 1), torch.float32, "conv_state")
     _check(ssm_state, (Bs, d, N), torch.float32, "ssm_state")
     if y_ring is None:
-        y_ring = torch.empty((W, Bs, d), dtype=io, device=x_ring.device)
+        y_ring = _new_on(stream, (W, Bs, d), io, x_ring.device)
     _check(y_ring, (W, Bs, d), io, "y_ring")
     rc = load().mamba_mixer_decode_replay_multi(
         _ptr(x_ring), _ptr(dt_ring), _ptr(B_ring), _ptr(z_ring), _ptr(C_ring), _ptr(A_log), _ptr(D), _ptr(dt_bias),

@@ -13,7 +13,7 @@ read them, is the caller's part, as with any work on a second stream.
 """
 from __future__ import annotations
 
-from . import MM_OK, MambaMixError, _check, _io_code, check_cu_seqlens, load, new_on
+from . import MM_OK, MambaMixError, _check, _io_code, check_cu_seqlens, load, _new_on
 
 torch = _BF16 = _F32 = _raw_stream = None  # (the package can be imported without torch)
 
@@ -101,7 +101,7 @@ def _head_inputs(x, dt, B, C, A_log, D, dt_bias):
 
 
 def _new(shape, dtype, device, stream):
-    return torch.empty(shape, dtype=dtype, device=device) if stream is None else new_on(stream, shape, dtype, device)
+    return torch.empty(shape, dtype=dtype, device=device) if stream is None else _new_on(stream, shape, dtype, device)
 
 
 def _workspace(given, need, device, stream):
@@ -109,7 +109,7 @@ def _workspace(given, need, device, stream):
         if stream is None:
             given = torch.empty(need, dtype=torch.uint8, device=device)
         else:
-            given = new_on(stream, need, torch.uint8, device, returned=False)
+            given = _new_on(stream, need, torch.uint8, device, returned=False)
     return given, _opt(given), 0 if given is None else given.numel() * given.element_size()
 
 

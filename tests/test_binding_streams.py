@@ -5,6 +5,7 @@ stand-ins that record what is allocated where."""
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import pytest
 import torch
@@ -22,7 +23,8 @@ class OnDevice(torch.Tensor):
 
 
 class Stream:
-    cuda_stream = 0x1234
+    def __init__(self, handle):
+        self.cuda_stream = handle
 
 
 class Log:
@@ -31,7 +33,7 @@ class Log:
 
 
 LOG = Log()
-CURRENT, SIDE = Stream(), Stream()
+CURRENT, SIDE = Stream(0x123456789), Stream(0x987654321)
 
 
 class Library:
@@ -43,7 +45,7 @@ class Library:
     def __getattr__(self, name):
         if "workspace" in name or "plan" in name or "name" in name or "bytes" in name:
             return getattr(self.real, name)
-        return lambda *a: LOG.launched.append((name, a[-1])) or 0
+        return lambda *a: LOG.launched.append({getattr(v, "value", v) for v in a if not isinstance(v, ctypes.Array)}) or 0
 
 
 def dev(*shape, dtype=BF16):
@@ -112,14 +114,73 @@ def residual_norm_backward(**kw):
     return list(mm.residual_norm_backward(dev(3, 64), None, dev(3, 64), dev(3, 64), w, w, scale_vec=w, **kw).values())
 
 
-CALLS = [heads_prefill, heads_decode, heads_backward, gate_norm, gate_norm_backward, residual_norm, residual_norm_backward]
-WITH_WORKSPACE = (heads_prefill, heads_backward, gate_norm_backward, residual_norm_backward)
+def mixer(T=600, S=2, d=64, N=16, states=True):
+    """x, z, dt, B, C, the parameters, cu_seqlens and the states of the selective scan's calls."""
+    return [dev(T, d), dev(T, d), dev(T, d), dev(T, N), dev(T, N), dev(d, N, dtype=F32), dev(d, dtype=F32), dev(d, dtype=F32),
+            dev(d, 4, dtype=F32), dev(d, dtype=F32), cu(T, S), dev(S, d, 3, dtype=F32), dev(S, d, N, dtype=F32)]
+
+
+def ring(W, Bs, d=64, N=16):
+    p = mixer(Bs, Bs)
+    return [dev(W, Bs, d), dev(W, Bs, d), dev(W, Bs, N)], [dev(Bs, d), dev(Bs, N)], p[5:10], p[11:]
+
+
+def prefill(**kw):
+    return [mm.prefill(*mixer(), chunk_len=64, **kw)]
+
+
+def prefill_noalloc(**kw):
+    return [mm.prefill_noalloc(*mixer(), **kw)]
+
+
+def prefill_train(**kw):
+    return mm.prefill_train(*mixer(), chunk_len=64, **kw)
+
+
+def prefill_backward(**kw):
+    return list(mm.prefill_backward(*mixer(), dev(600, 64), **kw).values())
+
+
+def project(**kw):
+    p = mixer()
+    return mm.project(p[0], p[8], p[9], p[10], p[11], dev(64, 8 + 32), dev(8, 64), **kw)
+
+
+def decode(**kw):
+    p = mixer(3, 3)
+    return [mm.decode(*p[:10], *p[11:], **kw)]
+
+
+def decode_replay(**kw):
+    rings, now, params, states = ring(4, 3)
+    return [mm.decode_replay(*rings, *now, *params, *states, 1, **kw)]
+
+
+def replay_checkpoint_lo(**kw):
+    return mm.replay_checkpoint_lo(*ring(4, 3)[3], **kw)
+
+
+def decode_replay_dual(**kw):
+    rings, now, params, states = ring(4, 3)
+    return [mm.decode_replay_dual(*rings, *now, *params, *states, dev(3, 64, 4), dev(3, 64, 16), 1, **kw)]
+
+
+def decode_replay_multi(**kw):
+    rings, _, params, states = ring(4, 3)
+    return [mm.decode_replay_multi(*rings, dev(4, 3, 64), dev(4, 3, 16), *params, *states, 0, 1, **kw)]
+
+
+CALLS = [heads_prefill, heads_decode, heads_backward, gate_norm, gate_norm_backward, residual_norm, residual_norm_backward,
+         prefill, prefill_noalloc, prefill_train, prefill_backward, project, decode, decode_replay, replay_checkpoint_lo,
+         decode_replay_dual, decode_replay_multi]
+WITH_WORKSPACE = (heads_prefill, heads_backward, gate_norm_backward, residual_norm_backward, prefill, prefill_train,
+                  prefill_backward, project)
 
 
 @pytest.mark.parametrize("call", CALLS, ids=[c.__name__ for c in CALLS])
 def test_allocations_belong_to_the_given_stream(call):
     outputs = [t for t in call(stream=SIDE) if t is not None]
-    assert LOG.launched and all(s in (SIDE.cuda_stream, None) or s.value == SIDE.cuda_stream for _, s in LOG.launched)
+    assert len(LOG.launched) == 1 and SIDE.cuda_stream in LOG.launched[0]
     assert LOG.made and all(stream is SIDE for _, stream in LOG.made)
     assert len(LOG.made) == len(outputs) + (call in WITH_WORKSPACE)
     used = {p for p, stream in LOG.used if stream is CURRENT}
