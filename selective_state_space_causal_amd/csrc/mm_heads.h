@@ -115,10 +115,12 @@ struct HeadPar {
   int S, H;
   int64_t T;
 };
+// softplus's hardware minimum and maximum pass a NaN over; here it stays one
+__device__ __forceinline__ float head_softplus(float v) { return v != v ? v : softplus(v); }
 template <typename IO>
 __device__ __forceinline__ float head_delta(const HeadPar& hp, int64_t t, int h) {
   if (hp.dt == nullptr) return 1.0f;
-  return softplus(ld_io(static_cast<const IO*>(hp.dt) + t * hp.dt_ts, h) + hp.dt_bias[h]);
+  return head_softplus(ld_io(static_cast<const IO*>(hp.dt) + t * hp.dt_ts, h) + hp.dt_bias[h]);
 }
 __device__ __forceinline__ float head_A2(const HeadPar& hp, int h) {  // A log2(e)
   return -exp2_hw(hp.A_log[h] * kLog2e) * kLog2e;
@@ -234,7 +236,7 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
     }
     su[tid >> 4][tid & 15] = io_value<IO>(ru);
     if (tid < kSeqTok) {
-      const float d = !din ? 0.0f : hp.dt == nullptr ? 1.0f : softplus(io_value<IO>(rdt) + bias);
+      const float d = !din ? 0.0f : hp.dt == nullptr ? 1.0f : head_softplus(io_value<IO>(rdt) + bias);
       sdel[tid] = d;
       sdec[tid] = d * A2;
     }

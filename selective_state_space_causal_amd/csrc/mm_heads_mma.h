@@ -131,6 +131,13 @@ __device__ __forceinline__ double last_lane(double v) {
   return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
 
+// A token's exponent (log2 of its decay) for the sums.  Below 2^-512 a decay is 0 in float32 whatever it multiplies,
+// and the sums stay finite; a NaN stays one.
+__device__ __forceinline__ double exponent(float del, float A2) {
+  const float e = del * A2;
+  return static_cast<double>(e < -512.0f ? -512.0f : e);
+}
+
 // eight float32 as bfloat16 parts; the sum of three has all 24 bits (of a value that is not finite the first part
 // says so and the others are NaN or zero)
 template <int PARTS>
@@ -318,9 +325,9 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
   const auto factors = [&](int64_t tb, int set) {
     if (wave >= 2) return;
     float* f = sF + set * kMmaFSet + wave * (kFn * kMmaTok) + lane;
-    const float del = !dhave || tb + lane >= sg.t1 ? 0.0f : hp.dt == nullptr ? 1.0f : softplus(io_value<uint16_t>(rdt) + bias);
-    // a decay below 2^-512 is 0 in float32 whatever it multiplies
-    const double c = lane_scan(static_cast<double>(fmaxf(del * A2, -512.0f)));
+    const bool token = dhave && tb + lane < sg.t1;
+    const float del = !token ? 0.0f : hp.dt == nullptr ? 1.0f : head_softplus(io_value<uint16_t>(rdt) + bias);
+    const double c = lane_scan(exponent(del, A2));
     const double last = last_lane(c);
     const double whole = floor(c);
     const float ci = static_cast<float>(whole), cf = static_cast<float>(c - whole);
