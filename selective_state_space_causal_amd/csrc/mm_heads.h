@@ -238,7 +238,7 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
     if (tid < kSeqTok) {
       const float d = !din ? 0.0f : hp.dt == nullptr ? 1.0f : head_softplus(io_value<IO>(rdt) + bias);
       sdel[tid] = d;
-      sdec[tid] = d * A2;
+      sdec[tid] = din ? d * A2 : 0.0f;  // (A2 may be infinite)
     }
     __syncthreads();
     if (ib + 1 < nb) load(ib + 1);

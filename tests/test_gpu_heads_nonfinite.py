@@ -1,5 +1,5 @@
 """NaN in what makes the decays (dt, dt_bias, A_log) shows in the results: by the formulas a NaN step or decay makes the
-state NaN from its token on, in its head and sequence alone.  Needs an MI355X."""
+state NaN from its token on, in its head and sequence alone.  And decays that vanish altogether.  Needs an MI355X."""
 from __future__ import annotations
 
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 import selective_state_space_causal_amd as mm
 from tests import heads_ref as ref
-from tests.test_gpu_heads import run_backward, run_prefill, to_gpu, tokens
+from tests.test_gpu_heads import check_prefill, run_backward, run_prefill, to_gpu, tokens
 from tests.test_gpu_heads_paths import prefill_stretch
 
 pytestmark = pytest.mark.gpu
@@ -124,3 +124,11 @@ def test_backward_nan_decay(shape):
         assert torch.equal(got[k][rest], clean[k][rest]), k
     for k in ("dx", "ddt"):
         assert torch.equal(got[k][:, rest], clean[k][:, rest]), k
+
+
+@pytest.mark.parametrize("name", SHAPES)
+def test_decays_that_vanish(name):
+    """exp(A_log) past float32: every decay is 0, and places without a token still leave the state as it is."""
+    c = inputs(name)
+    c["A_log"][1] = 100.0
+    check_prefill(c, *run_prefill(c))
