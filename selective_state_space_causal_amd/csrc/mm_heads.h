@@ -122,8 +122,10 @@ __device__ __forceinline__ float head_delta(const HeadPar& hp, int64_t t, int h)
   if (hp.dt == nullptr) return 1.0f;
   return head_softplus(ld_io(static_cast<const IO*>(hp.dt) + t * hp.dt_ts, h) + hp.dt_bias[h]);
 }
-__device__ __forceinline__ float head_A2(const HeadPar& hp, int h) {  // A log2(e)
-  return -exp2_hw(hp.A_log[h] * kLog2e) * kLog2e;
+// A log2(e), finite (or NaN): a place without a token has delta = 0, and must have the exponent 0
+__device__ __forceinline__ float head_A2(const HeadPar& hp, int h) {
+  const float A2 = -exp2_hw(hp.A_log[h] * kLog2e) * kLog2e;
+  return A2 < -3e38f ? -3e38f : A2;
 }
 
 // One run of the recurrence on a state of R rows and K columns (element (r, k) of a stored state at
@@ -238,7 +240,7 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
     if (tid < kSeqTok) {
       const float d = !din ? 0.0f : hp.dt == nullptr ? 1.0f : head_softplus(io_value<IO>(rdt) + bias);
       sdel[tid] = d;
-      sdec[tid] = din ? d * A2 : 0.0f;  // (A2 may be infinite)
+      sdec[tid] = d * A2;
     }
     __syncthreads();
     if (ib + 1 < nb) load(ib + 1);

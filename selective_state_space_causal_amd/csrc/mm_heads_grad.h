@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   const auto factors = [&](int cnt, int fs) {
     if (wave != 0) return;
     const float del = lane >= cnt ? 0.0f : hp.dt == nullptr ? 1.0f : head_softplus(io_value<uint16_t>(rdt) + bias);
-    const double c = lane_scan(exponent(lane < cnt, del, A2));
+    const double c = lane_scan(exponent(del, A2));
     const double last = last_lane(c);
     float* f = sF + fs * (kMmaTok + 4);
     f[lane] = dir ? exp2_hw(static_cast<float>(c)) : exp2_hw(static_cast<float>(last - c)) * del;
@@ -346,7 +346,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       if (wave == 3 && pb == 0) {
         float del = 0.0f;
         if (lane < cnt) del = head_delta<uint16_t>(hp, tb + lane, h);
-        const double c = lane_scan(exponent(lane < cnt, del, head_A2(hp, h)));
+        const double c = lane_scan(exponent(del, head_A2(hp, h)));
         const double last = last_lane(c);
         const double whole = floor(c);
         const float ci = static_cast<float>(whole), cf = static_cast<float>(c - whole);

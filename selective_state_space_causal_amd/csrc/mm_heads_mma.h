@@ -131,11 +131,11 @@ __device__ __forceinline__ double last_lane(double v) {
   return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-// A token's exponent (log2 of its decay) for the sums; 0 where there is no token.  Below 2^-512 a decay is 0 in float32
-// whatever it multiplies, and the sums stay finite; a NaN stays one.
-__device__ __forceinline__ double exponent(bool token, float del, float A2) {
+// A token's exponent (log2 of its decay) for the sums.  Below 2^-512 a decay is 0 in float32 whatever it multiplies,
+// and the sums stay finite; a NaN stays one.
+__device__ __forceinline__ double exponent(float del, float A2) {
   const float e = del * A2;
-  return static_cast<double>(!token ? 0.0f : e < -512.0f ? -512.0f : e);
+  return static_cast<double>(e < -512.0f ? -512.0f : e);
 }
 
 // eight float32 as bfloat16 parts; the sum of three has all 24 bits (of a value that is not finite the first part
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_mma(MmaArgs q, HeadPar
     float* f = sF + set * kMmaFSet + wave * (kFn * kMmaTok) + lane;
     const bool token = dhave && tb + lane < sg.t1;
     const float del = !token ? 0.0f : hp.dt == nullptr ? 1.0f : head_softplus(io_value<uint16_t>(rdt) + bias);
-    const double c = lane_scan(exponent(token, del, A2));
+    const double c = lane_scan(exponent(del, A2));
     const double last = last_lane(c);
     const double whole = floor(c);
     const float ci = static_cast<float>(whole), cf = static_cast<float>(c - whole);
