@@ -231,7 +231,7 @@ template <int NK>
 struct GradGeo {
   static constexpr int NP = NK * 32, PC = NP / 8, T2 = kMmaTok * kMmaTok * 2;
   static constexpr int B = 0, C = B + kMmaTok * NP * 2, X = C + kMmaTok * NP * 2, Y = X + T2, S = Y + T2,
-                       M = S + 64 * NP * 2, F = M + T2, R = F + kGn * kMmaTok * 4, bytes = R + (18 * kMmaTok + 8) * 4;
+                       M = S + 64 * NP * 2, F = M + T2, R = F + kGn * kMmaTok * 4, bytes = R + (18 * kMmaTok + 16) * 4;
 };
 
 // grid: (block, group, share of its heads)
@@ -254,6 +254,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
   float* const rj = ri + 4 * kMmaTok;                      // x . (Gam B), likewise
   float* const rd = rj + 4 * kMmaTok;                      // M_tt W_tt, then W_tt [2][64]
   float* const re = rd + 2 * kMmaTok;                      // <Gam, h> by channel tile [4], e^{c_last}
+  int* const odd = reinterpret_cast<int*>(re + 8);         // by wave: not all finite in its pieces of dy [4], of B and C [4]
 
   const int tid = threadIdx.x;
   int lane = tid & 63, li = lane & 15, g = lane >> 4;
@@ -283,12 +284,18 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
     const int brow = tid / PC, bcol = (tid % PC) * 8;
     constexpr int bstep = kMmaThreads / PC;
     const hbuf bB = token_rows(q.B.p, tb, q.B.ts, cnt, gn), bC = token_rows(q.C.p, tb, q.C.ts, cnt, gn);
+    uint32_t bad = 0;
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
       const int row = brow + i * bstep, col = group * q.N + bcol;
-      *reinterpret_cast<hu4*>(sB + tile_at<PC>(row, bcol)) = load8<VEC>(bB, (row * static_cast<int>(q.B.ts) + col) * 2, q.N - bcol);
-      *reinterpret_cast<hu4*>(sC + tile_at<PC>(row, bcol)) = load8<VEC>(bC, (row * static_cast<int>(q.C.ts) + col) * 2, q.N - bcol);
+      const hu4 b = load8<VEC>(bB, (row * static_cast<int>(q.B.ts) + col) * 2, q.N - bcol);
+      const hu4 c = load8<VEC>(bC, (row * static_cast<int>(q.C.ts) + col) * 2, q.N - bcol);
+      *reinterpret_cast<hu4*>(sB + tile_at<PC>(row, bcol)) = b;
+      *reinterpret_cast<hu4*>(sC + tile_at<PC>(row, bcol)) = c;
+      bad |= not_finite(b) | not_finite(c);
     }
+    const int any = __any(bad != 0);
+    if (lane == 0) odd[4 + wave] = any;
   }
   const hbuf bX = token_rows(q.x.p, tb, q.x.ts, cnt, dH), bY = token_rows(q.dy.p, tb, q.dy.ts, cnt, dH);
   const hbuf bO = token_rows(q.dx, tb, q.dx_ts, cnt, dH);
@@ -304,6 +311,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
   };
   load(h0, 0);
   __syncthreads();
+  const bool odd_bc = __builtin_amdgcn_readfirstlane(odd[4] | odd[5] | odd[6] | odd[7]) != 0;
 
   // the wave's score tiles (it, jt <= it): C_i . B_j, rows j and columns i, the same for every head
   const auto tile_i = [&](int u) { return u < 2 ? (wave < 2 ? 3 : wave == 2 ? 2 : 1) : (wave == 2 ? 2 : 0); };
@@ -343,6 +351,8 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         *reinterpret_cast<hu4*>(sX + tile_at<kMmaMP>(xrow + 32 * i, xcol)) = rX[i];
         *reinterpret_cast<hu4*>(sY + tile_at<kMmaMP>(xrow + 32 * i, xcol)) = rY[i];
       }
+      const int any = __any((not_finite(rY[0]) | not_finite(rY[1])) != 0);
+      if (lane == 0) odd[wave] = any;
       if (wave == 3 && pb == 0) {
         float del = 0.0f;
         if (lane < cnt) del = head_delta<uint16_t>(hp, tb + lane, h);
@@ -457,6 +467,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       hf4 dx[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) dx[t] = hf4{0, 0, 0, 0};
+      if (__builtin_amdgcn_readfirstlane(odd[0] | odd[1] | odd[2] | odd[3]) == 0) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const char* ya = sY + 2 * ks * M16 + (mT ^ (wave << 5));
@@ -468,6 +479,16 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
           // tiles above the diagonal's were not written: zeros
           const hb8 m = join((jt & 1) && jt / 2 == ks ? none : tr_read(ma), tr_read(ma + M16));
           dx[jt] = mfma(yt, m, dx[jt]);
+        }
+      }
+      } else {  // a value that is not finite must not meet the zeros of later tokens: token by token
+#pragma unroll 1
+        for (int i = 0; i < cnt; ++i) {
+          const hf4 y = to_f4(lds4(sY + tile_at<kMmaMP>(i, 16 * wave + 4 * g)));
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (16 * t + li <= i)
+              dx[t] += y * io_value<uint16_t>(*reinterpret_cast<const uint16_t*>(sM + tile_at<kMmaMP>(i, 16 * t + li)));
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -572,6 +593,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
             v = mfma(join(lds4(sX + t * M16 + (mK ^ (ks << 6))), lds4(sX + t * M16 + (mK ^ (ks << 6) ^ 32))), gT[ks], v);
           dB[t][n] += v * (*reinterpret_cast<const hf4*>(f + kGew * kMmaTok + 16 * t + 4 * g) *
                            *reinterpret_cast<const hf4*>(f + kGdel * kMmaTok + 16 * t + 4 * g));
+          if (odd_bc) continue;
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
             if (!(ks == 0 && t > 1)) {  // i >= j: rows j = 16 t ..
@@ -582,6 +604,26 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
               const char* ma = sM + t * M16;
               dC[t][n] = mfma(join(lds4(ma + (mK ^ (ks << 6))), (t & 1) == 0 && t / 2 == ks ? none : lds4(ma + (mK ^ (ks << 6) ^ 32))),
                               bT[ks], dC[t][n]);
+            }
+          }
+        }
+        if (odd_bc) {  // as for dx: C of earlier and B of later tokens have no part in a sum
+          const int col = 16 * nt + li;
+#pragma unroll 1
+          for (int u = 0; u < cnt; ++u) {
+            const float c = io_value<uint16_t>(*reinterpret_cast<const uint16_t*>(sC + tile_at<PC>(u, col)));
+            const float b = io_value<uint16_t>(*reinterpret_cast<const uint16_t*>(sB + tile_at<PC>(u, col)));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const hf4 m = to_f4(lds4(sM + tile_at<kMmaMP>(u, 16 * t + 4 * g)));
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int row = 16 * t + 4 * g + r;
+                if (row <= u) dB[t][n][r] = __builtin_fmaf(m[r], c, dB[t][n][r]);
+                if (row >= u)
+                  dC[t][n][r] = __builtin_fmaf(
+                      io_value<uint16_t>(*reinterpret_cast<const uint16_t*>(sM + tile_at<kMmaMP>(row, u))), b, dC[t][n][r]);
+              }
             }
           }
         }
