@@ -115,8 +115,13 @@ struct HeadPar {
   int S, H;
   int64_t T;
 };
-// softplus's hardware minimum and maximum pass a NaN over; here it stays one
-__device__ __forceinline__ float head_softplus(float v) { return v != v ? v : softplus(v); }
+// softplus with a minimum and a maximum that keep a NaN
+__device__ __forceinline__ float head_softplus(float v) {
+  const float e = exp2_hw(__builtin_elementwise_minimum(v, 20.0f) * kLog2e);
+  const float u = 1.0f + e;
+  const float d = e - (u - 1.0f);
+  return __builtin_elementwise_maximum(v, __builtin_fmaf(log2_hw(u), kLn2, d));
+}
 template <typename IO>
 __device__ __forceinline__ float head_delta(const HeadPar& hp, int64_t t, int h) {
   if (hp.dt == nullptr) return 1.0f;
@@ -124,8 +129,7 @@ __device__ __forceinline__ float head_delta(const HeadPar& hp, int64_t t, int h)
 }
 // A log2(e), finite (or NaN): a place without a token has delta = 0, and must have the exponent 0
 __device__ __forceinline__ float head_A2(const HeadPar& hp, int h) {
-  const float A2 = -exp2_hw(hp.A_log[h] * kLog2e) * kLog2e;
-  return A2 < -3e38f ? -3e38f : A2;
+  return __builtin_elementwise_maximum(-exp2_hw(hp.A_log[h] * kLog2e) * kLog2e, -3e38f);
 }
 
 // One run of the recurrence on a state of R rows and K columns (element (r, k) of a stored state at

@@ -134,8 +134,7 @@ __device__ __forceinline__ double last_lane(double v) {
 // A token's exponent (log2 of its decay) for the sums.  Below 2^-512 a decay is 0 in float32 whatever it multiplies,
 // and the sums stay finite; a NaN stays one.
 __device__ __forceinline__ double exponent(float del, float A2) {
-  const float e = del * A2;
-  return static_cast<double>(e < -512.0f ? -512.0f : e);
+  return static_cast<double>(__builtin_elementwise_maximum(del * A2, -512.0f));
 }
 
 // eight float32 as bfloat16 parts; the sum of three has all 24 bits (of a value that is not finite the first part
