@@ -128,11 +128,17 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
     take(p.off_sums, static_cast<size_t>(p.rows64) * H * 3 * 4);
   }
   p.total = off;
-  const int64_t most = std::max<int64_t>(p.rows * H * std::max(p.nrp, p.nrn), p.rows64 * H);
-  if (most * kSeqThreads > kMaxThreads || static_cast<int64_t>(th) * 16 > kMaxThreads ||
-      T * G * N > kMaxThreads)
-    return MM_ERR_DIM;
-  return MM_OK;
+  // the threads of each launch of the path taken (whole sequences run beside stretches: S of them)
+  const int64_t tgn = T * G * N, seq = p.rows * H * (backward ? std::max(p.nrp, p.nrn) : p.nrp) * kSeqThreads;
+  int64_t most = static_cast<int64_t>(H) * std::max(P * N, kSeqThreads);
+  if (p.mma) {
+    most = std::max(most, std::max(p.walks, S) * H * p.npb * kMmaThreads);
+    if (backward) most = std::max({most, p.rows64 * G * p.splits * kMmaThreads, tgn});
+  } else {
+    most = std::max(most, seq);
+    if (backward) most = std::max({most, static_cast<int64_t>(th) * 16, p.rows64 * H * 64, tgn});
+  }
+  return most > kMaxThreads ? MM_ERR_DIM : MM_OK;
 }
 
 int check_heads_sizes(int64_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N, int32_t io) {
@@ -514,8 +520,7 @@ size_t heads_workspace(int64_t S, int64_t T, int32_t H, int32_t P, int32_t G, in
   size_t most = 0;
   for (int64_t stride : {int64_t{0}, int64_t{INT32_MAX}}) {
     HeadsPlan p;
-    if (H == 0 || plan_heads(p, S, T, H, P, G, N, io, backward, stride) != MM_OK) return 0;
-    most = std::max(most, p.total);
+    if (H > 0 && plan_heads(p, S, T, H, P, G, N, io, backward, stride) == MM_OK) most = std::max(most, p.total);
   }
   return most;
 }
