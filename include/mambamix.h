@@ -501,7 +501,9 @@ size_t mamba_mixer_heads_backward_workspace_bytes(int32_t S, int64_t T, int32_t 
  *   y [rows, d], z [rows, d] io, rows y_stride and z_stride apart; weight [d] f32;
  *   out [rows, d] io, contiguous; may be y itself when y is contiguous (in place), and may overlap
  *   no other input (MM_ERR_ALIAS)
- * d is a multiple of groups (MM_ERR_DIM), eps >= 0.  rows == 0 or d == 0 is a no-op.
+ * d is a multiple of groups, eps >= 0, and a launch has less than 2^32 threads: at least 64 for each group, 256 for
+ * each (row, group) of more than 8192 columns, 16 for each column in the backward (else MM_ERR_DIM).
+ * rows == 0 or d == 0 is a no-op.
  */
 int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, void* out, int64_t rows, int32_t d,
                           int32_t groups, float eps, int32_t gate_first, int32_t io_dtype, int64_t y_stride,

@@ -582,6 +582,13 @@ int64_t norm_slots(int64_t rows, int n, int groups, bool backward) {
   const int64_t wgs = kCUs * (backward ? std::max(1, 24 * kWave / t) : std::max(16, 8192 / t));
   return std::max<int64_t>(1, std::min<int64_t>(rows, cdiv(wgs, groups)));
 }
+// gate_norm's other launches: a workgroup for each group at least, and 16 threads for each column of the weights' sums
+int check_gate_launch(int64_t rows, int d, int groups, bool backward) {
+  const int n = d / groups;
+  if (n <= kNormUnit && norm_slots(rows, n, groups, backward) * groups * norm_shape(n, true).threads > kMaxThreads)
+    return MM_ERR_DIM;
+  return backward && int64_t{d} * 16 > kMaxThreads ? MM_ERR_DIM : MM_OK;
+}
 // f(E, NV) of a shape
 template <bool BF16, typename F>
 void by_pieces(const NormShape& sh, F f) {
@@ -757,6 +764,7 @@ int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, voi
   int rc = check_gate_sizes(nrows, d, groups, eps, io_dtype);
   if (rc != MM_OK) return rc;
   if (nrows == 0 || d == 0) return MM_OK;
+  if ((rc = check_gate_launch(nrows, d, groups, false)) != MM_OK) return rc;
   if (y_stride < d || z_stride < d) return MM_ERR_DIM;
   const size_t es = esize(io_dtype);
   const Array in[] = {{rows(y, nrows, d, y_stride, es), es, false}, {rows(z, nrows, d, z_stride, es), es, false},
@@ -789,8 +797,8 @@ int mamba_mixer_gate_norm(const void* y, const void* z, const float* weight, voi
 }
 
 size_t mamba_mixer_gate_norm_backward_workspace_bytes(int64_t nrows, int32_t d, int32_t groups) {
-  if (check_gate_sizes(nrows, d, groups, 0.0f, MM_IO_F32) != MM_OK) return 0;
-  return norm_workspace(nrows, d, groups, 1);
+  if (check_gate_sizes(nrows, d, groups, 0.0f, MM_IO_F32) != MM_OK || d == 0) return 0;
+  return check_gate_launch(nrows, d, groups, true) == MM_OK ? norm_workspace(nrows, d, groups, 1) : 0;
 }
 
 int mamba_mixer_gate_norm_backward(const void* dout, const void* y, const void* z, const float* weight, void* dy,
@@ -801,6 +809,7 @@ int mamba_mixer_gate_norm_backward(const void* dout, const void* y, const void* 
   int rc = check_gate_sizes(nrows, d, groups, eps, io_dtype);
   if (rc != MM_OK) return rc;
   if (d == 0) return MM_OK;
+  if ((rc = check_gate_launch(nrows, d, groups, true)) != MM_OK) return rc;
   if (y_stride < d || z_stride < d || dy_stride < d || dz_stride < d) return MM_ERR_DIM;
   const size_t es = esize(io_dtype), nd = static_cast<size_t>(d) * 4;
   const Array in[] = {{flat(dout, static_cast<size_t>(nrows) * d * es), es, false},

@@ -4,7 +4,7 @@ from __future__ import annotations
 
 import ctypes
 
-from tests.test_heads_host import DIM, WORKSPACE, backward, lib, prefill  # noqa: F401
+from tests.test_heads_host import ALIAS, DIM, WORKSPACE, backward, gate, gate_backward, lib, prefill  # noqa: F401
 
 FAR = 1 << 40  # no two arrays overlap
 
@@ -40,3 +40,19 @@ def test_a_backward_on_the_matrix_cores_has_none_either(lib):  # noqa: F811
 def test_the_float32_backward_has(lib):  # noqa: F811
     assert backward(lib, far(19), **grads((1 << 28) // 64 - 1, N=16, io=0)) == WORKSPACE
     assert backward(lib, far(19), **grads((1 << 28) // 64 + 1, N=16, io=0)) == DIM
+
+
+def test_gate_norm_of_more_groups_than_a_launch_has_workgroups(lib):  # noqa: F811
+    """Refused on the host as sizes, not by the launch."""
+    d = 1 << 26
+    wide = dict(rows=2, d=d, ys=d, zs=d)
+    assert gate(lib, far(4), g=d, **wide) == DIM
+    p = far(4)
+    p[3] = p[1]
+    assert gate(lib, p, g=d // 2, **wide) == ALIAS  # half as many are accepted: past the sizes
+    grads = dict(wide, gy=d, gz=d, wsb=0)
+    assert gate_backward(lib, far(7), g=d, **grads) == DIM
+    assert gate_backward(lib, far(7), g=d // 2, **grads) == WORKSPACE
+    d = 1 << 28  # the weights' sums: 16 threads a column
+    assert gate_backward(lib, far(7), rows=2, d=d, g=8, ys=d, zs=d, gy=d, gz=d, wsb=0) == DIM
+    assert lib.mamba_mixer_gate_norm_backward_workspace_bytes(2, d, 8) == 0
