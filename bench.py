@@ -108,16 +108,32 @@ class HipEvents:
 KERNEL_DIR = os.path.join(ROOT, "selective_state_space_causal_amd", "csrc")
 
 
-def kernel_source_sha256():
-    """sha256 over the HIP sources (every file of csrc/, in name order), to tie a counter summary to them."""
+def kernel_sources(unit="mambamix.hip", folder=KERNEL_DIR):
+    """The files of a compilation unit of the library: its .hip file and what it includes of csrc/, in name order."""
+    import re
+
+    seen, todo = set(), [unit]
+    while todo:
+        name = todo.pop()
+        if name in seen or not os.path.exists(os.path.join(folder, name)):
+            continue
+        seen.add(name)
+        with open(os.path.join(folder, name)) as f:
+            todo += re.findall(r'^\s*#\s*include\s+"([^"]+)"', f.read(), re.M)
+    return sorted(seen)
+
+
+def kernel_source_sha256(unit="mambamix.hip", folder=KERNEL_DIR):
+    """sha256 over the HIP sources of one compilation unit (the selective scan's, or heads.hip), to tie a counter summary
+    to the sources of the kernel it describes and to no others."""
     import hashlib
 
     h = hashlib.sha256()
-    for name in sorted(os.listdir(KERNEL_DIR)):
-        if name.endswith((".hip", ".h")):
-            with open(os.path.join(KERNEL_DIR, name), "rb") as f:
-                h.update(name.encode() + b"\0" + f.read())
+    for name in kernel_sources(unit, folder):
+        with open(os.path.join(folder, name), "rb") as f:
+            h.update(name.encode() + b"\0" + f.read())
     return h.hexdigest()
+
 
 PROFILE_DECODE = os.path.join(ROOT, "profiles", "k_decode_vec__m7b_decode_b256_d8192_N16_bf16.txt")
 PROFILE_REPLAY = os.path.join(ROOT, "profiles", "k_decode_replay__m7b_decode_b256_d8192_N16_W4_bf16.txt")
@@ -1006,7 +1022,8 @@ def main():
     ap.add_argument("--summarize-rocprof", metavar="CSV",
                     help="print a per-kernel table of a rocprofv3 kernel_stats.csv or counter_collection.csv "
                          "and exit")
-    ap.add_argument("--source-sha", action="store_true", help="print the HIP source hash and exit")
+    ap.add_argument("--source-sha", nargs="?", const="mambamix.hip", metavar="UNIT",
+                    help="print the source hash of a compilation unit of csrc/ (mambamix.hip or heads.hip) and exit")
     ap.add_argument("--copy-calibration", action="store_true",
                     help="run only a plain 1 GiB device-to-device copy three times (to scale HBM byte counters)")
     ap.add_argument("--hbm-probe", action="store_true",
@@ -1018,7 +1035,7 @@ def main():
         summarize_rocprof(args.summarize_rocprof)
         return
     if args.source_sha:
-        print(kernel_source_sha256())
+        print(kernel_source_sha256(args.source_sha))
         return
     if args.gpus != 1:
         print(f"bench.py measures one GPU only; --gpus {args.gpus} is not supported "
