@@ -52,7 +52,10 @@ constexpr int64_t kSeqWorkgroups = 1024;
 // a group; two workgroups fit on a CU.
 constexpr int kMmaMaxN = 128;
 constexpr int64_t kMmaWorkgroups = 512;
-// Prefill: up to so many sequences the device chooses between whole sequences and stretches, by the longest one.
+// Prefill: up to so many sequences the device chooses between whole sequences and stretches, by the longest one.  Beyond,
+// whole sequences run unasked: with 24 heads 1000 sequences of 16 tokens take 360 us (494 when both ways are launched),
+// 300 of 90 180 (201), with 64 heads in 8 groups 913 (1294) and 418 (459).  One long sequence among many pays for it where
+// the heads are few: 299 of 50 tokens and one of 12000, 24 heads 1075 us, in stretches 678; 64 heads 1247 and 1532.
 constexpr int64_t kMmaMaxEven = 256;
 
 int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, int io, bool backward, int64_t max_stride) {
@@ -69,7 +72,10 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
     // Prefill: whole sequences where they alone give the GPU its workgroups and none is longer than two stretches, which
     // the kernels of both ways find out (16 x 1024 tokens, 64 heads in 8 groups: whole 158 us, cut 254; 24 x 100 54 and
     // 167; but one long sequence among short ones would be one long chain).  The backward, whose two walks store every
-    // block's state, takes them with one workgroup per CU (8 x 2048 tokens, 24 heads, 415 us where cut took 490).  Else
+    // block's state, takes them with one workgroup per CU, whatever their lengths: its stretches walk everything twice.
+    // 8 x 2044 tokens, 24 heads, whole 474 us, cut 608; seven of 425 to 4011 tokens, 24 heads 536 and 596, 64 heads 1307
+    // and 1484; 2 x 8192, 64 heads, 963 and 1075.  One long sequence alone among short ones loses: 16000 and 384 tokens, 64
+    // heads, 1237 and 1178; 16000 and seven of 50, 24 heads, 898 and 659.  Else
     // stretches of equal length, as many as the GPU runs workgroups at once (two walks per CU, of two 64-channel
     // blocks, or four state walks of one), so that all end together.  Short calls have fewer: a walk's time grows with
     // its length L, the carries' with the T / L states of every pair of blocks, and sqrt(T pairs / 2) is near the least sum
@@ -88,7 +94,8 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   p.whole = p.Ls > T;
   p.npb = static_cast<int>(cdiv(P, 64));
   p.nk = N <= 32 ? 1 : N <= 64 ? 2 : 4;
-  // two workgroups of the gradient kernel per CU, or one for each head
+  // Two workgroups of the gradient kernel per CU, or one for each head.  (The count is that of full blocks; a few more
+  // than fit at once make a round of their own: 8 x 2048 tokens, 24 heads, 377 us, 8 x 2044 474.)
   p.splits = H > 0 ? static_cast<int>(std::max<int64_t>(
                  1, std::min<int64_t>(H / G, cdiv(2 * kCUs, std::max<int64_t>(segment_rows(S, T, kHeadsBlock) * G, 1))))) : 1;
   p.rows = segment_rows(S, T, p.Ls);
@@ -195,7 +202,8 @@ struct HeadsArgs {
   HeadPar hp;
 };
 
-// 16-byte pieces of rows and states: every row starts on one
+// 16-byte pieces of rows and states: every row starts on one.  Where one does not, all tiles are loaded element by
+// element: the prefill of 16384 packed tokens of 10 heads takes 187 us with rows of 1546 columns, 81 with 1552.
 bool heads_vec(const HeadsArgs& a, std::initializer_list<const void*> more) {
   if (a.P % 8 != 0 || a.N % 8 != 0 || a.x_ts % 8 != 0 || a.b_ts % 8 != 0 || a.c_ts % 8 != 0) return false;
   for (const void* p : {a.x, a.B, a.C})

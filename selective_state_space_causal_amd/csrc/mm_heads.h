@@ -410,8 +410,9 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_decode_any(Tok<IO> x, Tok
 
 // The same for N a multiple of 4 with every row on 16 bytes: RL lanes take a state row, 4 entries each, and a
 // thread two rows, so that a workgroup's accesses are contiguous.  Bound by the states' traffic, 8 P N bytes a
-// head, which passes the caches by (nontemporal).  256 rows, d 8192, state 64 x 128 (2.15 GB): 363 us, 5.9 TB/s
-// (a plain copy reaches 6.2); one row per thread 481 us, four 364, eight 611 (204 registers); plain accesses 392.
+// head, which passes the caches by (nontemporal).  256 rows, d 8192, state 64 x 128 (2.15 GB): 353 us, 6.2 TB/s
+// (traced mean; a plain copy reaches 6.2); when it was 363, one row per thread took 481, four 364, eight 611 (204
+// registers), plain accesses 392.
 constexpr int kDecodeRows = 2;
 template <typename IO, int RL>
 __global__ __launch_bounds__(kSeqThreads) void k_heads_decode(Tok<IO> x, Tok<IO> B, Tok<IO> C, HeadPar hp,
@@ -504,7 +505,8 @@ __global__ __launch_bounds__(256) void k_heads_qr(Tok<IO> B, Tok<IO> C, Tok<IO> 
 // The gradients of delta.  With l = log a, dl_t = <G_t, a_t h_{t-1}> satisfies dl_t = dl_{t+1} + q_t - p_t
 // (p = delta r), so inside a 64-token block it is a sum from the block's end, where it is the inner product
 // of the adjoint and the state (dots): the sum restarts there and its rounding does not build up along the
-// sequence.  One wave per (block, head), one token per lane.
+// sequence.  (So a value of x or B that is not finite reaches ddt of the block's earlier tokens too.)  One wave per
+// (block, head), one token per lane.
 template <typename IO>
 __global__ __launch_bounds__(64) void k_heads_ddt(HeadPar hp, const float* __restrict__ q, const float* __restrict__ r,
                                                   const float* __restrict__ w, const float* __restrict__ dots, int ndots,

@@ -50,9 +50,10 @@ struct StateGeo {
 
 // grid: (row, 64-channel block, slice) x direction; a wave takes 16 of the channels
 // The storing walks are bound by their stores: 8 x 2048 tokens, 24 heads 64 x 128, both directions, write 403 MB of
-// states in 108 to 125 us.  States pass the caches by, on the way out and in: the whole backward 382 us where plain accesses
-// took 397 (4 x 2048 tokens 227 and 262).  The local walks of 16384 tokens, 64 heads, take 91 us: VALU issue 34%, MFMA
-// 23%, the rest waits in the chain of a block (load, LDS, weights, product); shorter stretches would add carries.
+// states in 152 us (traced mean, inputs of successive calls in different memory; 536 MB in all, 3.5 TB/s).  States pass the
+// caches by, on the way out and in: the whole backward 382 us where plain accesses took 397 (4 x 2048 tokens 227 and
+// 262).  The local walks of 16384 tokens, 64 heads, take 96 us: VALU issue 32%, MFMA 22%, the rest waits in the chain of a
+// block (load, LDS, weights, product); shorter stretches would add carries.
 // LOCAL: what a segment adds to a zero state; else the whole walk, which stores.
 // (The two are told apart at compile time so that the stores' place among the outstanding accesses is known: a wait
 // for the tile loads then leaves the stores in flight.)
@@ -236,10 +237,13 @@ struct GradGeo {
 
 // grid: (block, group, share of its heads)
 // B, C and the scores C . B stay for all heads of the workgroup, x, dy and the two states of the next head are loaded
-// under this one's products.  8 x 2048 tokens, 24 heads: 220 to 245 us, of which its traffic (0.84 GB, the
-// states mostly) would be 136 at the copy's rate.  A head is a chain of products between barriers, and two workgroups
-// (256 registers, 45 more spilled; 81 KB of LDS) cover it in part: waves wait 66% of their cycles, VALU issue 27%, MFMA
+// under this one's products.  8 x 2048 tokens, 24 heads: 217 us (traced mean), of which its traffic (0.78 GB, the
+// states mostly) would be 127 at the copy's rate.  A head is a chain of products between barriers, and two workgroups
+// (256 registers, 37 more spilled; 81 KB of LDS) cover it in part: waves wait 66% of their cycles, VALU issue 28%, MFMA
 // 12%.
+// Values that are not finite: masked zeros of M and of delta W d must not meet them in dy, C or B, so blocks that hold one
+// take those products token by token.  (x needs no such care: its products are masked before they are used.)  The sum of
+// row sums minus column sums remains: x or B that is not finite reaches ddt of the block's earlier tokens too.
 template <int NK, bool VEC>
 __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, HeadPar hp) {
   typedef GradGeo<NK> G;
