@@ -13,8 +13,10 @@
 //   dl_t = sum_{i>=t>j} delta_j M_ij W_ij + sum_{i>=t} e^{c_i} dy_i . (h C_i) + sum_{j<t} w_j x_j . (Gam B_j)
 //          + e^{c_last} <Gam, h>                                         (l = log a)
 //   ddelta = r + A dl
-// Each term of dl joins something before t to something from t on, so nothing cancels but in the first sum, which
-// is taken as a sum of strict row sums minus strict column sums from the block's end.
+// Each term of dl joins something before t to something from t on, and the first sum is put together from those of whole
+// 16 x 16 tiles, parts of tiles' row and column sums and the diagonal's tile, all of pairs that belong to it: nothing cancels.
+// (As row sums minus column sums from the block's end, which is one scan, dA_log and ddt_bias were off by 1.2e-6 where float32
+// arithmetic throughout gives 2e-7.)
 //
 // Precision: dx, dB and dC leave in bfloat16; their computed operands (M, W d, h, Gam) are rounded to bfloat16
 // once.  dl, r and what is summed from them (dA_log, ddt_bias: float32 results) use float32 products of the exact
@@ -215,6 +217,26 @@ __global__ __launch_bounds__(kMmaThreads, 4) void k_heads_states(StateArgs q, He
   }
 }
 
+// Sums within the lane's row of 16: of the lanes from it on, and of those before it; and lane `l`'s value, to all
+__device__ __forceinline__ float row_from(float v) {
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x101, 0xF, 0xF, true);  // row_shl:1
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x102, 0xF, 0xF, true);  // row_shl:2
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x104, 0xF, 0xF, true);  // row_shl:4
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x108, 0xF, 0xF, true);  // row_shl:8
+  return v;
+}
+__device__ __forceinline__ float row_before(float v) {
+  v = __builtin_amdgcn_update_dpp(0.0f, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x111, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x112, 0xF, 0xF, true);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x114, 0xF, 0xF, true);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0.0f, v, 0x118, 0xF, 0xF, true);  // row_shr:8
+  return v;
+}
+__device__ __forceinline__ float lane_of(float v, int l) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l));
+}
+
 struct GradArgs {
   Tok<uint16_t> x, dy, B, C;
   int P, N, npb, G, splits;
@@ -237,13 +259,12 @@ struct GradGeo {
 
 // grid: (block, group, share of its heads)
 // B, C and the scores C . B stay for all heads of the workgroup, x, dy and the two states of the next head are loaded
-// under this one's products.  8 x 2048 tokens, 24 heads: 217 us (traced mean), of which its traffic (0.78 GB, the
-// states mostly) would be 127 at the copy's rate.  A head is a chain of products between barriers, and two workgroups
-// (256 registers, 37 more spilled; 81 KB of LDS) cover it in part: waves wait 66% of their cycles, VALU issue 28%, MFMA
+// under this one's products.  8 x 2048 tokens, 24 heads: 213 us (traced mean), of which its traffic (0.74 GB, the
+// states mostly) would be 120 at the copy's rate.  A head is a chain of products between barriers, and two workgroups
+// (256 registers, 27 more spilled; 81 KB of LDS) cover it in part: waves wait 66% of their cycles, VALU issue 28%, MFMA
 // 12%.
 // Values that are not finite: masked zeros of M and of delta W d must not meet them in dy, C or B, so blocks that hold one
-// take those products token by token.  (x needs no such care: its products are masked before they are used.)  The sum of
-// row sums minus column sums remains: x or B that is not finite reaches ddt of the block's earlier tokens too.
+// take those products token by token.  (x needs no such care: its products are masked before they are used.)
 template <int NK, bool VEC>
 __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, HeadPar hp) {
   typedef GradGeo<NK> G;
@@ -252,8 +273,9 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
   char *const sB = lds + G::B, *const sC = lds + G::C, *const sX = lds + G::X, *const sY = lds + G::Y;
   char *const sS = lds + G::S, *const sM = lds + G::M;
   float* const f = reinterpret_cast<float*>(lds + G::F);
-  float* const rq = reinterpret_cast<float*>(lds + G::R);  // strict row sums, by column tile [4][64]
-  float* const rp = rq + 4 * kMmaTok;                      // strict column sums, by row tile [4][64]
+  float* const rq = reinterpret_cast<float*>(lds + G::R);  // row sums of delta M W, by column tile left of the diagonal's [3][64]
+  float* const rt = rq + 3 * kMmaTok;                      // its sums over i >= t > j in the diagonal's tiles [64]
+  float* const rp = rt + kMmaTok;                          // column sums of M W without the diagonal, by row tile [4][64]
   float* const ri = rp + 4 * kMmaTok;                      // dy . (h C), by channel tile [4][64]
   float* const rj = ri + 4 * kMmaTok;                      // x . (Gam B), likewise
   float* const rd = rj + 4 * kMmaTok;                      // M_tt W_tt, then W_tt [2][64]
@@ -336,10 +358,10 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
     for (int n = 0; n < NTW; ++n) dB[t][n] = dC[t][n] = hf4{0, 0, 0, 0};
 
   const hb4 none = to_bf4(hf4{0, 0, 0, 0});
-  // of wave 0: a token's sums over the channel blocks of a head
-  float qs = 0.0f, ps = 0.0f, dg = 0.0f, wd = 0.0f, qi = 0.0f, pi = 0.0f, e0 = 0.0f;
   for (int h = h0; h < h1; ++h)
     for (int pb = 0; pb < q.npb; ++pb) {
+      // a token's sums over the channel blocks of a head gather where they lie: the same lane adds to a place each time
+      const auto add = [&](float* at, float v) { *at = pb > 0 ? *at + v : v; };
       asm volatile("" : "+v"(aN), "+v"(aT), "+v"(mN), "+v"(mK), "+v"(mT), "+v"(lane), "+v"(li), "+v"(g), "+v"(wv));
       wave = __builtin_amdgcn_readfirstlane(wv);
       // the state and its adjoint: rows p = 16 wave + li, columns 32 k + 8 g ..
@@ -405,8 +427,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
           }
         }
         // a value that is not finite times a masked zero would be NaN: the mask selects
-        hf4 m1, w2, tt;
-        float row = 0.0f;
+        hf4 m1, w2, tt, z;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const bool on = it != jt || 4 * g + r <= li;
@@ -417,19 +438,30 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         }
         if (it == jt && li >> 2 == g) {
           const int r = li & 3;
-          rd[i] = r == 0 ? tt[0] : r == 1 ? tt[1] : r == 2 ? tt[2] : tt[3];
-          rd[kMmaTok + i] = r == 0 ? w[0] : r == 1 ? w[1] : r == 2 ? w[2] : w[3];
+          add(rd + i, r == 0 ? tt[0] : r == 1 ? tt[1] : r == 2 ? tt[2] : tt[3]);
+          add(rd + kMmaTok + i, r == 0 ? w[0] : r == 1 ? w[1] : r == 2 ? w[2] : w[3]);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           if (it == jt && 4 * g + r == li) tt[r] = 0.0f;
-          row = __builtin_fmaf(tt[r], del[r], row);
+          z[r] = tt[r] * del[r];
           tt[r] = row_sum16(tt[r]);
         }
-        row += __shfl_xor(row, 16);
-        row += __shfl_xor(row, 32);
-        if (g == 0) rq[jt * kMmaTok + i] = row;
-        if (li < 4) rp[it * kMmaTok + j + li] = li == 0 ? tt[0] : li == 1 ? tt[1] : li == 2 ? tt[2] : tt[3];
+        if (li < 4) add(rp + it * kMmaTok + j + li, li == 0 ? tt[0] : li == 1 ? tt[1] : li == 2 ? tt[2] : tt[3]);
+        // sums over j up to each of the lane's: within the lane, then those of the lanes before it
+        z[1] += z[0];
+        z[2] += z[1];
+        z[3] += z[2];
+        const float o16 = __shfl_xor(z[3], 16), two = z[3] + o16, o32 = __shfl_xor(two, 32);
+        if (it != jt) {
+          if (g == 0) add(rq + jt * kMmaTok + i, two + o32);
+        } else {
+          const float before = (g & 1 ? o16 : 0.0f) + (g & 2 ? o32 : 0.0f);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) z[r] = row_sum16(li > 4 * g + r ? before + z[r] : 0.0f);  // of the rows below: t = j + 1
+          if (li < 4 && 4 * g + li < 15) add(rt + j + li + 1, li == 0 ? z[0] : li == 1 ? z[1] : li == 2 ? z[2] : z[3]);
+          if (lane == 0) rt[j] = 0.0f;
+        }
         *reinterpret_cast<hb4*>(sM + it * M16 + (mK ^ (jt << 5))) = to_bf4(m1);
         m2[u] = to_bf4(w2);
       }
@@ -456,7 +488,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         float v = (acc[t][0] * y[0] + acc[t][1] * y[1]) + (acc[t][2] * y[2] + acc[t][3] * y[3]);
         v += __shfl_xor(v, 16);
         v += __shfl_xor(v, 32);
-        if (g == 0) ri[wave * kMmaTok + 16 * t + li] = v;
+        if (g == 0) add(ri + wave * kMmaTok + 16 * t + li, v);
       }
       __syncthreads();
       // the adjoint's loads, in flight over the products of the state
@@ -546,7 +578,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       dot = row_sum16(dot);
       dot += __shfl_xor(dot, 16);
       dot += __shfl_xor(dot, 32);
-      if (lane == 0) re[wave] = dot;
+      if (lane == 0) add(re + wave, dot);
       __builtin_amdgcn_sched_barrier(0);
       const float Dh = hp.D != nullptr ? hp.D[h] : 0.0f;
 #pragma unroll
@@ -557,7 +589,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         float v = (acc[t][0] * x[0] + acc[t][1] * x[1]) + (acc[t][2] * x[2] + acc[t][3] * x[3]);
         v += __shfl_xor(v, 16);
         v += __shfl_xor(v, 32);
-        if (g == 0) rj[wave * kMmaTok + j] = v;
+        if (g == 0) add(rj + wave * kMmaTok + j, v);
         const hf4 o = dx[t] + acc[t] * (f[kGew * kMmaTok + j] * f[kGdel * kMmaTok + j]) + y * Dh;
         const hu2 ob = __builtin_bit_cast(hu2, to_bf4(o));
         const int off = (j * static_cast<int>(q.dx_ts) + h * q.P + 64 * pb + p) * 2, n = q.P - 64 * pb - p;
@@ -632,29 +664,32 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
           }
         }
       }
-      if (wave == 0) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (t <= g) qs += rq[t * kMmaTok + lane];
-          if (t >= g) ps += rp[t * kMmaTok + lane];
-          qi += ri[t * kMmaTok + lane];
-          pi += rj[t * kMmaTok + lane];
-          e0 += re[t];
-        }
-        dg += rd[lane];
-        wd += rd[kMmaTok + lane];
-        if (pb == q.npb - 1) {
+      if (wave == 0 && pb == q.npb - 1) {
           const float del = f[kGdel * kMmaTok + lane];
+          float qi = 0.0f, pi = 0.0f, below = 0.0f;  // below: column sums of the row tiles below the token's own
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if (t > g) below += rp[t * kMmaTok + lane];
+            qi += ri[t * kMmaTok + lane];
+            pi += rj[t * kMmaTok + lane];
+          }
+          const float q0 = g > 0 ? rq[lane] : 0.0f, q1 = g > 1 ? rq[kMmaTok + lane] : 0.0f;
+          const float q2 = g > 2 ? rq[2 * kMmaTok + lane] : 0.0f;
           qi *= f[kGe * kMmaTok + lane];
           pi *= f[kGew * kMmaTok + lane];
-          const float r = ps + dg + pi;
-          float suf = qs - del * ps, sq = qi, pre = del * pi;
-          for (int k = 1; k < 64; k *= 2) {
-            const float o = __shfl_down(suf, k), oq = __shfl_down(sq, k), op = __shfl_up(pre, k);
-            if (lane + k < 64) suf += o, sq += oq;
-            if (lane >= k) pre += op;
-          }
-          const float dl = ((suf + sq) + (pre - del * pi)) + re[4] * e0;
+          const float r = below + rp[g * kMmaTok + lane] + rd[lane] + pi;
+          // sum over i >= t > j of delta M W, with t in tile g: whole tiles below and left of it, columns j < t of the
+          // tiles below it, rows i >= t of the tiles left of it, and the diagonal's tile
+          const float t0 = row_sum16(q0), t1 = row_sum16(q1);
+          const float far1 = lane_of(t0, 32) + lane_of(t0, 48), far2 = lane_of(t0, 48) + lane_of(t1, 48);
+          const float in = ((g == 1 ? far1 : g == 2 ? far2 : 0.0f) + row_before(below * del)) + (row_from(q0 + q1 + q2) + rt[lane]);
+          // dy . (h C) of i >= t, delta x . (Gam B) of j < t
+          const float qs = row_from(qi), qt1 = lane_of(qs, 16), qt2 = lane_of(qs, 32), qt3 = lane_of(qs, 48);
+          const float pd = del * pi, ps = row_sum16(pd), pt0 = lane_of(ps, 0), pt1 = lane_of(ps, 16), pt2 = lane_of(ps, 32);
+          const float from = qs + (g == 0 ? qt1 + qt2 + qt3 : g == 1 ? qt2 + qt3 : g == 2 ? qt3 : 0.0f);
+          const float before = row_before(pd) + (g == 3 ? pt0 + pt1 + pt2 : g == 2 ? pt0 + pt1 : g == 1 ? pt0 : 0.0f);
+          const float dl = ((in + from) + before) + re[4] * ((re[0] + re[1]) + (re[2] + re[3]));
+          float wd = rd[kMmaTok + lane];
           const float A = -exp2_hw(hp.A_log[h] * kLog2e);
           float dA = 0.0f, db = 0.0f;
           if (lane < cnt) {
@@ -676,8 +711,6 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
             o[1] = db;
             o[2] = wd;
           }
-          qs = ps = dg = wd = qi = pi = e0 = 0.0f;
-        }
       }
       __syncthreads();
     }

@@ -1,6 +1,7 @@
 """NaN and infinities in dy, x, B and C reach the gradients that depend on them and no others: those of the later (or
-earlier) tokens that the causal mask leaves out keep their values.  Of ddt, whose sums run over 64-token blocks, the
-tokens just before a spoiled x or B in its block may be lost too.  Needs an MI355X."""
+earlier) tokens that the causal mask leaves out keep their values.  Of the
+token-by-token path's ddt, whose sums run over 64-token blocks, the tokens just before a spoiled x or B in its block may be
+lost too.  Needs an MI355X."""
 from __future__ import annotations
 
 import pytest
@@ -45,7 +46,7 @@ def test_backward(shape, key, value):
         bad = torch.zeros(T, dtype=torch.bool)
         bad[list(tokens)] = True
         assert not torch.isfinite(got[k][bad.cuda()]).any(), f"{k}: tokens that depend on it"
-        if k == "ddt" and key in "xB":
+        if k == "ddt" and key in "xB" and (io == "f32" or N > 128):
             bad[BLOCK:AT] = True
         good = ~bad
         ref.check(got[k][good.cuda()], *(t[good] for t in want[k]), T, k)

@@ -1,0 +1,50 @@
+"""The parameters' gradients of the matrix-core backward are float32 results: they are held to the error that the same
+recurrence and its adjoint have in float32 arithmetic throughout.  The kernels make no more roundings per term than that, so
+over several inputs their errors are of its size; three times allows for chance.  Needs an MI355X."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import heads_ref as ref
+from tests.gpu_util import log
+from tests.test_gpu_heads import run_backward
+
+pytestmark = pytest.mark.gpu
+
+NAMES = dict(A_log="dA_log", dt_bias="ddt_bias", D="dD", state="dstate_in")
+
+
+def gradients(c, dtype):
+    """Through torch's differentiation of the recurrence, token by token, in one type."""
+    H, G = c["H"], c["G"]
+    t = {k: c[k].to(dtype) for k in ("x", "dt", "B", "C", "dy", "dstate")}
+    p = {k: c[k].to(dtype).clone().requires_grad_() for k in NAMES}
+    B, C = (t[k].repeat_interleave(H // G, 1) for k in "BC")
+    delta = torch.nn.functional.softplus(t["dt"] + p["dt_bias"], threshold=700)
+    a = torch.exp(-torch.exp(p["A_log"]) * delta)
+    loss, at = 0, 0
+    for s, n in enumerate(c["lens"]):
+        h = p["state"][s]
+        for i in range(at, at + n):
+            h = a[i][:, None, None] * h + (delta[i][:, None] * t["x"][i])[:, :, None] * B[i][:, None, :]
+            y = (h * C[i][:, None, :]).sum(-1) + p["D"][:, None] * t["x"][i]
+            loss = loss + (y * t["dy"][i]).sum()
+        loss = loss + (h * t["dstate"][s]).sum()
+        at += n
+    return dict(zip(NAMES.values(), torch.autograd.grad(loss, list(p.values()))))
+
+
+@pytest.mark.parametrize("lens,H,P,G,N", [([320], 8, 16, 1, 32), ([100, 7, 200], 8, 20, 2, 24), ([256], 4, 80, 1, 16)])
+def test_float32_gradients_have_float32_errors(lens, H, P, G, N):
+    mine, plain, size = ({k: 0.0 for k in NAMES.values()} for _ in range(3))
+    for seed in range(70, 74):
+        c = ref.heads_inputs(seed, lens, H, P, G, N, "bf16")
+        exact, f32, got = gradients(c, torch.float64), gradients(c, torch.float32), run_backward(c)
+        for k in NAMES.values():
+            mine[k] += float((got[k].cpu().double() - exact[k]).square().sum())
+            plain[k] += float((f32[k].double() - exact[k]).square().sum())
+            size[k] += float(exact[k].square().sum())
+    for k in NAMES.values():
+        log(f"  {k}: {(mine[k] / size[k]) ** 0.5:.2e}, float32 throughout {(plain[k] / size[k]) ** 0.5:.2e}")
+        assert mine[k] <= 9 * plain[k], k
