@@ -443,8 +443,8 @@ size_t mamba_mixer_project_workspace_bytes(int64_t T, int32_t d, int32_t N, int3
  * row's length (MM_ERR_DIM).  y and state_out may overlap no input but state_out == state_in.
  * Limits: 1 <= P <= MM_HEADS_MAX_P, 1 <= N <= MM_HEADS_MAX_N (else MM_ERR_UNSUPPORTED).
  * One launch has less than 2^32 threads (else MM_ERR_DIM), which bounds the tokens of a call: on the matrix
- * cores (bfloat16, N <= 128) T G N < 2^32 in the backward; else T H P < 2^34 or so, and in the
- * backward T H < 2^28 and T G N < 2^32.
+ * cores (bfloat16, N <= 128) T G N < 2^32 in the backward; else (S + T / 64) H < 2^24 and T G N < 2^32 in the
+ * backward.
  * T == 0 copies the states and is otherwise a no-op; H == 0 is a no-op.
  */
 #define MM_HEADS_MAX_P 256

@@ -38,8 +38,7 @@ struct HeadsPlan {
   int64_t even;    // not 0: both ways are launched, and the whole sequences run if none is longer than this
   int64_t rows64;  // 64-token blocks at most (backward)
   int nrp, nrn;    // 16-row blocks of P and N
-  size_t off_carry, off_decay, off_carry2, off_decay2, off_hb, off_dots, off_dB, off_dC, off_q, off_r, off_delta,
-      off_sums, off_gs, off_w, total;
+  size_t off_carry, off_decay, off_carry2, off_decay2, off_hb, off_gs, off_dB, off_dC, off_delta, off_sums, total;
   int npb, nk, splits;  // matrix-core backward: 64-channel blocks per head, 32-column steps of N, shares of a group's heads
 };
 
@@ -125,13 +124,10 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
     take(p.off_sums, static_cast<size_t>(p.rows64) * H * 3 * 4);
   } else if (backward) {
     take(p.off_hb, p.rows64 * set);
-    take(p.off_dots, static_cast<size_t>(p.rows64) * H * p.nrp * 4);
+    take(p.off_gs, p.rows64 * set);
     take(p.off_dB, th * N * 4);
     take(p.off_dC, th * N * 4);
-    take(p.off_q, th * 4);
-    take(p.off_r, th * 4);
     take(p.off_delta, th * 4);
-    take(p.off_w, th * 4);
     take(p.off_sums, static_cast<size_t>(p.rows64) * H * 3 * 4);
   }
   p.total = off;
@@ -143,7 +139,7 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
     if (backward) most = std::max({most, p.rows64 * G * p.splits * kMmaThreads, tgn});
   } else {
     most = std::max(most, seq);
-    if (backward) most = std::max({most, static_cast<int64_t>(th) * 16, p.rows64 * H * 64, tgn});
+    if (backward) most = std::max({most, p.rows64 * H * kMmaThreads, tgn});
   }
   return most > kMaxThreads ? MM_ERR_DIM : MM_OK;
 }
@@ -409,12 +405,8 @@ int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o,
   const int64_t T = a.hp.T, set = static_cast<int64_t>(a.P) * a.N;
   const Tok<IO> x = tok<IO>(a.x, a.x_ts, a.P, 1), dy = tok<IO>(o.dy, static_cast<int64_t>(H) * a.P, a.P, 1);
   const Tok<IO> B = tok<IO>(a.B, a.b_ts, a.N, div), C = tok<IO>(a.C, a.c_ts, a.N, div);
-  float* f32[] = {reinterpret_cast<float*>(ws + p.off_hb), reinterpret_cast<float*>(ws + p.off_dots),
-                reinterpret_cast<float*>(ws + p.off_dB), reinterpret_cast<float*>(ws + p.off_dC),
-                reinterpret_cast<float*>(ws + p.off_q), reinterpret_cast<float*>(ws + p.off_r),
-                reinterpret_cast<float*>(ws + p.off_delta), reinterpret_cast<float*>(ws + p.off_sums),
-                  reinterpret_cast<float*>(ws + p.off_w)};
-  // dC (and the states at the blocks' ends): forward, the state transposed (rows N)
+  const auto at = [ws](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  // dC and the states at the blocks' starts: forward, the state transposed (rows N)
   SeqRun<IO> c{};
   c.u = B;
   c.v = x;
@@ -426,17 +418,17 @@ int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o,
   c.sh = set;
   c.init = o.state_in;
   c.Ls = p.Ls;
-  c.out32 = f32[3];
-  c.store = f32[0];
+  c.out32 = at(p.off_dC);
+  c.store = at(p.off_hb);
   // dB: reverse, the state transposed
   SeqRun<IO> b = c;
   b.u = C;
   b.v = dy;
   b.s = x;
   b.init = o.dstate_out;
-  b.out32 = f32[2];
+  b.out32 = at(p.off_dB);
   b.store = nullptr;
-  // dx, dstate_in and the inner products at the blocks' ends: reverse (rows P)
+  // dx, dstate_in and the adjoints at the blocks' ends: reverse (rows P)
   SeqRun<IO> d = b;
   d.u = dy;
   d.v = C;
@@ -451,8 +443,7 @@ int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o,
   d.out_ts = o.dx_ts;
   d.out_delta = 1;
   d.add_D = 1;
-  d.dots_with = f32[0];
-  d.dots = f32[1];
+  d.store = at(p.off_gs);
   if (!p.whole) {
     c.carry = reinterpret_cast<float*>(ws + p.off_carry);
     c.decay = reinterpret_cast<float*>(ws + p.off_decay);
@@ -470,16 +461,17 @@ int launch_backward(const HeadsPlan& p, const HeadsArgs& a, const HeadsGrads& o,
   if (T > 0) launch_seq_both<IO, false>(c, b, a.hp, p.rows, st);
   launch_seq<IO, true, false>(d, a.hp, p.rows, st);
   if (T > 0) {
-    const unsigned nqr = static_cast<unsigned>(cdiv(T * H * 16, 256));
-    hipLaunchKernelGGL((k_heads_qr<IO>), dim3(nqr), dim3(256), 0, st, B, C, x, dy, f32[2], f32[3], f32[4], f32[5], f32[8], T, H,
-                       a.N, a.P);
-    hipLaunchKernelGGL((k_heads_ddt<IO>), dim3(static_cast<unsigned>(p.rows64 * H)), dim3(64), 0, st, a.hp, f32[4],
-                       f32[5], f32[8], f32[1], p.nrp, f32[6], static_cast<IO*>(o.ddt), o.ddt_ts, f32[7]);
+    const auto steps = [&](auto wide) {
+      hipLaunchKernelGGL((k_heads_ddt<IO, decltype(wide)::value>), dim3(static_cast<unsigned>(p.rows64 * H)), dim3(kMmaThreads), 0,
+                         st, x, dy, B, C, a.hp, at(p.off_hb), at(p.off_gs), a.P, a.N, at(p.off_delta), static_cast<IO*>(o.ddt),
+                         o.ddt_ts, at(p.off_sums));
+    };
+    if (a.P >= 4 && a.N >= 4) steps(std::true_type{}); else steps(std::false_type{});
     hipLaunchKernelGGL((k_heads_group<IO>), dim3(static_cast<unsigned>(cdiv(T * a.G * a.N, 256))), dim3(256), 0, st,
-                       f32[2], f32[3], f32[6], static_cast<IO*>(o.dB), static_cast<IO*>(o.dC), o.db_ts, o.dc_ts, T, H, a.G,
-                       a.N);
+                       at(p.off_dB), at(p.off_dC), at(p.off_delta), static_cast<IO*>(o.dB), static_cast<IO*>(o.dC), o.db_ts,
+                       o.dc_ts, T, H, a.G, a.N);
   }
-  hipLaunchKernelGGL(k_heads_params, dim3(static_cast<unsigned>(H)), dim3(256), 0, st, f32[7], T > 0 ? p.rows64 : 0, H,
+  hipLaunchKernelGGL(k_heads_params, dim3(static_cast<unsigned>(H)), dim3(256), 0, st, at(p.off_sums), T > 0 ? p.rows64 : 0, H,
                      o.dA_log, o.ddt_bias, o.dD);
   return launched();
 }

@@ -12,7 +12,7 @@
 // (LOCAL), the states the segments start from (k_heads_carry), and the outputs.
 //
 // The kernels here take the recurrence token by token in float32 and serve every type, size and
-// stride.
+// stride.  (The gradients of their decays come from k_heads_ddt, by blocks of 64 tokens.)
 #pragma once
 
 #include "mm_device.h"
@@ -155,9 +155,7 @@ struct SeqRun {
   float* out32;               // [T, H, R] contiguous in float32, or NULL
   int out_delta;              // multiply the output by delta
   int add_D;                  // add D u
-  const float* dots_with;     // reverse: the forward states at the ends of 64-token blocks, [rows64] states, or NULL
-  float* dots;                // and the inner products with them, [rows64, H, row blocks]
-  float* store;               // forward: those states, or NULL
+  float* store;               // [rows64] the states at the starts of 64-token blocks, reverse at their ends, or NULL
 };
 
 // A workgroup walks its segment in groups of 16 tokens of the packed stream, the next one loaded while this one is
@@ -168,7 +166,7 @@ struct SeqRun {
 template <int KV>
 struct SeqLds {
   float v[kSeqTok][16 * KV], s[kSeqTok][16 * KV], u[kSeqTok][kSeqRows], o[kSeqTok][kSeqRows + 1];
-  float del[kSeqTok], dec[kSeqTok], dot[kSeqThreads / kWave];
+  float del[kSeqTok], dec[kSeqTok];
 };
 template <typename IO, int KV, bool REV, bool LOCAL>
 __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp, int64_t item, SeqLds<KV>& lds) {
@@ -177,7 +175,6 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
   auto& su = lds.u;
   auto& so = lds.o;
   auto &sdel = lds.del, &sdec = lds.dec;
-  auto& sdot = lds.dot;
   const int tid = threadIdx.x, lane = tid & 15, row = tid >> 4;
   const int nrb = (q.R + kSeqRows - 1) / kSeqRows;
   const int rb = static_cast<int>(item % nrb);
@@ -231,7 +228,9 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
     const int64_t b = b0 + (REV ? nb - 1 - ib : ib), tb = b * kSeqTok;
     const int lo = g.t0 > tb ? static_cast<int>(g.t0 - tb) : 0;
     const int hi = g.t1 - tb < kSeqTok ? static_cast<int>(g.t1 - tb) : kSeqTok;
-    const bool edge = (b + 1) % (kHeadsBlock / kSeqTok) == 0 || tb + hi == g.seq1;  // the end of a 64-token block
+    // where the walk enters a 64-token block: from its start, or from its end
+    const bool edge = REV ? (b + 1) % (kHeadsBlock / kSeqTok) == 0 || tb + hi == g.seq1
+                          : b % (kHeadsBlock / kSeqTok) == 0 || tb + lo == g.seq0;
     const int64_t at64 = (g.s + tb / kHeadsBlock) * sset + soff;
     __syncthreads();
 #pragma unroll
@@ -248,22 +247,12 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
     }
     __syncthreads();
     if (ib + 1 < nb) load(ib + 1);
-    if (REV && !LOCAL && q.dots_with != nullptr && edge) {
-      // before the block's last token enters: the adjoint of the state after it
-      float d = 0.0f;
-      if (r < q.R)
+    if (!LOCAL && q.store != nullptr && edge && r < q.R)
 #pragma unroll
-        for (int i = 0; i < KV; ++i) {
-          const int k = lane * KV + i;
-          if (k < q.K) d = __builtin_fmaf(st[i], q.dots_with[at64 + k * q.sk], d);
-        }
-      d = row_sum16(d);
-      d += __shfl_xor(d, 16);
-      d += __shfl_xor(d, 32);
-      if ((tid & 63) == 0) sdot[tid >> 6] = d;
-      __syncthreads();
-      if (tid == 0) q.dots[((g.s + tb / kHeadsBlock) * hp.H + h) * nrb + rb] = (sdot[0] + sdot[1]) + (sdot[2] + sdot[3]);
-    }
+      for (int i = 0; i < KV; ++i) {
+        const int k = lane * KV + i;
+        if (k < q.K) q.store[at64 + k * q.sk] = st[i];
+      }
 #pragma unroll
     for (int j = 0; j < kSeqTok; ++j) {
       const int t = REV ? kSeqTok - 1 - j : j;
@@ -283,12 +272,6 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
         if (lane == 0) so[t][row] = (q.out_delta ? sdel[t] * o : o) + Dh * su[t][row];
       }
     }
-    if (!REV && !LOCAL && q.store != nullptr && edge && r < q.R)
-#pragma unroll
-      for (int i = 0; i < KV; ++i) {
-        const int k = lane * KV + i;
-        if (k < q.K) q.store[at64 + k * q.sk] = st[i];
-      }
     if (!LOCAL && (q.out != nullptr || q.out32 != nullptr)) {
       __syncthreads();
       const int t = tid >> 4, rr = rb * kSeqRows + (tid & 15);
@@ -471,95 +454,6 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_decode(Tok<IO> x, Tok<IO>
 }
 
 // ------------------------------------------------------------------------------------ backward
-// q_t = C_t . dC_t, r_t = B_t . dB_t (head by head, dB before its factor delta) and w_t = x_t . dy_t: a 16-lane row
-// per (t, h)
-template <typename IO>
-__global__ __launch_bounds__(256) void k_heads_qr(Tok<IO> B, Tok<IO> C, Tok<IO> x, Tok<IO> dy, const float* __restrict__ dB,
-                                                  const float* __restrict__ dC, float* __restrict__ q,
-                                                  float* __restrict__ r, float* __restrict__ w, int64_t T, int H, int N,
-                                                  int P) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
-  const int lane = threadIdx.x & 15;
-  if (i >= T * H) return;
-  const int64_t t = i / H;
-  const int h = static_cast<int>(i % H);
-  const IO *Bp = B.at(t, h), *Cp = C.at(t, h);
-  float sq = 0.0f, sr = 0.0f;
-  for (int n = lane; n < N; n += 16) {
-    sq = __builtin_fmaf(ld_io(Cp, n), dC[i * N + n], sq);
-    sr = __builtin_fmaf(ld_io(Bp, n), dB[i * N + n], sr);
-  }
-  const IO *xp = x.at(t, h), *gp = dy.at(t, h);
-  float sw = 0.0f;
-  for (int p = lane; p < P; p += 16) sw = __builtin_fmaf(ld_io(xp, p), ld_io(gp, p), sw);
-  sq = row_sum16(sq);
-  sr = row_sum16(sr);
-  sw = row_sum16(sw);
-  if (lane == 0) {
-    q[i] = sq;
-    r[i] = sr;
-    w[i] = sw;
-  }
-}
-
-// The gradients of delta.  With l = log a, dl_t = <G_t, a_t h_{t-1}> satisfies dl_t = dl_{t+1} + q_t - p_t
-// (p = delta r), so inside a 64-token block it is a sum from the block's end, where it is the inner product
-// of the adjoint and the state (dots): the sum restarts there and its rounding does not build up along the
-// sequence.  (So a value of x or B that is not finite reaches ddt of the block's earlier tokens too.)  One wave per
-// (block, head), one token per lane.
-template <typename IO>
-__global__ __launch_bounds__(64) void k_heads_ddt(HeadPar hp, const float* __restrict__ q, const float* __restrict__ r,
-                                                  const float* __restrict__ w, const float* __restrict__ dots, int ndots,
-                                                  float* __restrict__ delta, IO* __restrict__ ddt, int64_t ddt_ts,
-                                                  float* __restrict__ sums) {
-  const int lane = threadIdx.x;
-  const int h = blockIdx.x % hp.H;
-  const int64_t rho = blockIdx.x / hp.H;
-  const Segment g = segment_of(hp.cu, hp.S, rho, kHeadsBlock);
-  float* part = sums + (rho * hp.H + h) * 3;
-  if (g.t0 >= g.t1) {
-    if (lane < 3) part[lane] = 0.0f;
-    return;
-  }
-  const int64_t t = g.t0 + lane;
-  const bool in = t < g.t1;
-  float del = 0.0f, rr = 0.0f, diff = 0.0f;
-  if (in) {
-    del = head_delta<IO>(hp, t, h);
-    delta[t * hp.H + h] = del;
-    rr = r[t * hp.H + h];
-    diff = q[t * hp.H + h] - del * rr;
-  }
-  float e = 0.0f;
-  for (int i = 0; i < ndots; ++i) e += dots[(rho * hp.H + h) * ndots + i];
-  for (int k = 1; k < 64; k *= 2) {  // sums over the lanes from this one on
-    const float o = __shfl_down(diff, k);
-    if (lane + k < 64) diff += o;
-  }
-  const float dl = e + diff;
-  const float A = -exp2_hw(hp.A_log[h] * kLog2e);
-  float dA = 0.0f, db = 0.0f, dD = 0.0f;
-  if (in) {
-    dA = del * dl * A;
-    if (hp.dt != nullptr) {
-      const float v = ld_io(static_cast<const IO*>(hp.dt) + t * hp.dt_ts, h) + hp.dt_bias[h];
-      db = __builtin_fmaf(A, dl, rr) * rcp_hw(1.0f + exp2_hw(-v * kLog2e));
-      st_io(ddt, t * ddt_ts + h, db);
-    }
-    dD = w[t * hp.H + h];
-  }
-  for (int k = 32; k > 0; k /= 2) {
-    dA += __shfl_xor(dA, k);
-    db += __shfl_xor(db, k);
-    dD += __shfl_xor(dD, k);
-  }
-  if (lane == 0) {
-    part[0] = dA;
-    part[1] = db;
-    part[2] = dD;
-  }
-}
-
 // dB and dC of a group: the sums of its heads' shares (dB's times delta)
 template <typename IO>
 __global__ __launch_bounds__(256) void k_heads_group(const float* __restrict__ dBh, const float* __restrict__ dCh,

@@ -1,4 +1,4 @@
-"""The parameters' gradients of the matrix-core backward are float32 results: they are held to the error that the same
+"""The parameters' gradients of the head scan are float32 results: they are held to the error that the same
 recurrence and its adjoint have in float32 arithmetic throughout.  The kernels make no more roundings per term than that, so
 over several inputs their errors are of its size; three times allows for chance.  Needs an MI355X."""
 from __future__ import annotations
@@ -35,11 +35,13 @@ def gradients(c, dtype):
     return dict(zip(NAMES.values(), torch.autograd.grad(loss, list(p.values()))))
 
 
-@pytest.mark.parametrize("lens,H,P,G,N", [([320], 8, 16, 1, 32), ([100, 7, 200], 8, 20, 2, 24), ([256], 4, 80, 1, 16)])
-def test_float32_gradients_have_float32_errors(lens, H, P, G, N):
+@pytest.mark.parametrize("lens,H,P,G,N,io", [([320], 8, 16, 1, 32, "bf16"), ([100, 7, 200], 8, 20, 2, 24, "bf16"),
+                                             ([256], 4, 80, 1, 16, "bf16"), ([320], 8, 16, 1, 32, "f32"),
+                                             ([100, 7, 200], 8, 22, 2, 25, "f32"), ([200], 4, 16, 1, 150, "bf16")])
+def test_float32_gradients_have_float32_errors(lens, H, P, G, N, io):
     mine, plain, size = ({k: 0.0 for k in NAMES.values()} for _ in range(3))
     for seed in range(70, 74):
-        c = ref.heads_inputs(seed, lens, H, P, G, N, "bf16")
+        c = ref.heads_inputs(seed, lens, H, P, G, N, io)
         exact, f32, got = gradients(c, torch.float64), gradients(c, torch.float32), run_backward(c)
         for k in NAMES.values():
             mine[k] += float((got[k].cpu().double() - exact[k]).square().sum())

@@ -38,8 +38,11 @@ def test_a_backward_on_the_matrix_cores_has_none_either(lib):  # noqa: F811
 
 
 def test_the_float32_backward_has(lib):  # noqa: F811
-    assert backward(lib, far(19), **grads((1 << 28) // 64 - 1, N=16, io=0)) == WORKSPACE
-    assert backward(lib, far(19), **grads((1 << 28) // 64 + 1, N=16, io=0)) == DIM
+    """A workgroup for each (64-token block, head)."""
+    fits = 64 * ((1 << 18) - 3) - 1
+    assert backward(lib, far(19), **grads(fits, N=16, io=0)) == WORKSPACE
+    assert lib.mamba_mixer_heads_backward_workspace_bytes(3, fits, 64, 64, 1, 16, 0) > 0
+    assert backward(lib, far(19), **grads(fits + 65, N=16, io=0)) == DIM
 
 
 def test_gate_norm_of_more_groups_than_a_launch_has_workgroups(lib):  # noqa: F811
