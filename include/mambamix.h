@@ -451,7 +451,10 @@ size_t mamba_mixer_project_workspace_bytes(int64_t T, int32_t d, int32_t N, int3
 #define MM_HEADS_MAX_N 256
 
 /* The head scan over S packed sequences.  workspace: mamba_mixer_heads_prefill_workspace_bytes
- * bytes (0 for short calls), 256-byte aligned, contents on entry do not matter. */
+ * bytes (0 for short calls), 256-byte aligned, contents on entry do not matter.  The size queries are for
+ * rows of x, B, C (and dx) up to MM_HEADS_MAX_STRIDE elements apart; wider rows are taken token by token,
+ * whatever their type, and need what the query gives for MM_IO_F32. */
+#define MM_HEADS_MAX_STRIDE 4194304
 int mamba_mixer_heads_prefill(const void* x, const void* dt, const void* B, const void* C, const float* A_log,
                               const float* D, const float* dt_bias, const int32_t* cu_seqlens, const float* state_in,
                               float* state_out, void* y, int32_t S, int64_t T, int32_t H, int32_t P, int32_t G,
@@ -477,7 +480,7 @@ int mamba_mixer_heads_decode(const void* x, const void* dt, const void* B, const
  *   dA_log, dD, ddt_bias [H]     f32; dD is NULL when D is, ddt_bias when dt is
  *   dstate_in [S, H, P, N]       f32, or NULL: not wanted
  * All outputs are overwritten, and summed in a fixed order: the results do not vary from run to run.
- * workspace: mamba_mixer_heads_backward_workspace_bytes bytes, 256-byte aligned.
+ * workspace: mamba_mixer_heads_backward_workspace_bytes bytes, 256-byte aligned (MM_HEADS_MAX_STRIDE as above).
  * No output may overlap an input or another output (column ranges of one array with the same row
  * stride are taken apart).  With T == 0 the parameters' gradients are zeros and dstate_in is a copy of
  * dstate_out.

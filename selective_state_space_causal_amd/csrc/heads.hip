@@ -514,15 +514,11 @@ int check_overlap(const Array* in, int ni, const Array* out, int no, InPlace sam
   return MM_OK;
 }
 
-// the largest workspace of a call of these sizes, whatever its strides are
+// the workspace of a call of these sizes, of rows up to kMmaMaxStride elements apart
 size_t heads_workspace(int64_t S, int64_t T, int32_t H, int32_t P, int32_t G, int32_t N, int32_t io, bool backward) {
-  if (check_heads_sizes(S, T, H, P, G, N, io) != MM_OK) return 0;
-  size_t most = 0;
-  for (int64_t stride : {int64_t{0}, int64_t{INT32_MAX}}) {
-    HeadsPlan p;
-    if (H > 0 && plan_heads(p, S, T, H, P, G, N, io, backward, stride) == MM_OK) most = std::max(most, p.total);
-  }
-  return most;
+  HeadsPlan p;
+  if (check_heads_sizes(S, T, H, P, G, N, io) != MM_OK || H == 0) return 0;
+  return plan_heads(p, S, T, H, P, G, N, io, backward, 0) == MM_OK ? p.total : 0;
 }
 
 size_t esize(int32_t io) { return io == MM_IO_BF16 ? 2 : 4; }

@@ -46,7 +46,7 @@ typedef uint32_t hu2 __attribute__((ext_vector_type(2)));
 constexpr int kMmaTok = 64;      // tokens per chunk
 constexpr int kMmaThreads = 256;
 constexpr int kMmaCols = 128;    // head channels per workgroup: two blocks of 64
-constexpr int kMmaMaxStride = 1 << 22;  // elements between rows: a chunk's offsets stay far below 2^31
+constexpr int kMmaMaxStride = MM_HEADS_MAX_STRIDE;  // elements between rows: a chunk's offsets stay far below 2^31
 constexpr int kMmaPastEnd = 0x40000000;  // a buffer offset past every range
 
 struct MmaArgs {

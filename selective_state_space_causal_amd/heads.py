@@ -39,6 +39,14 @@ def _code(t) -> int:
     return 1 if t.dtype is _BF16 else 0 if t.dtype is _F32 else _io_code(t)
 
 
+_MAX_STRIDE = 4194304  # MM_HEADS_MAX_STRIDE
+
+
+def _plan_code(code, *strides) -> int:
+    """The io type whose workspace a head scan of these row strides needs: wider rows take float32's path."""
+    return code if max(strides) <= _MAX_STRIDE else 0
+
+
 def _opt(t):
     return t.data_ptr() if t is not None else None
 
@@ -152,7 +160,9 @@ def heads_prefill(x, dt, B, C, A_log, D, dt_bias, cu_seqlens, state_in=None, sta
     else:
         _need(y, (T, H, P), x.dtype, "y")
     io = _code(x)
-    need = _lib().mamba_mixer_heads_prefill_workspace_bytes(S, T, H, P, G, N, io) if workspace is None else 0
+    need = 0
+    if workspace is None:
+        need = _lib().mamba_mixer_heads_prefill_workspace_bytes(S, T, H, P, G, N, _plan_code(io, *strides))
     workspace, wptr, wbytes = _workspace(workspace, need, x.device, stream)
     rc = _lib().mamba_mixer_heads_prefill(
         x.data_ptr(), _opt(dt), B.data_ptr(), C.data_ptr(), A_log.data_ptr(), _opt(D), _opt(dt_bias),
@@ -211,7 +221,9 @@ def heads_backward(x, dt, B, C, A_log, D, dt_bias, cu_seqlens, state_in, dy, dst
     dA_log, dD, dbias = new(H), new(H) if D is not None else None, new(H) if dt is not None else None
     dstate_in = new(S, H, P, N) if need_dstate else None
     code = _code(x)
-    need = _lib().mamba_mixer_heads_backward_workspace_bytes(S, T, H, P, G, N, code) if workspace is None else 0
+    need = 0
+    if workspace is None:
+        need = _lib().mamba_mixer_heads_backward_workspace_bytes(S, T, H, P, G, N, _plan_code(code, *strides, sx))
     workspace, wptr, wbytes = _workspace(workspace, need, dev, stream)
     rc = _lib().mamba_mixer_heads_backward(
         x.data_ptr(), _opt(dt), B.data_ptr(), C.data_ptr(), A_log.data_ptr(), _opt(D), _opt(dt_bias),

@@ -9,8 +9,9 @@ import math
 import pytest
 import torch
 
+import selective_state_space_causal_amd as mm
 from tests import heads_ref as ref
-from tests.test_gpu_heads import check_backward, check_prefill, run_backward, run_prefill
+from tests.test_gpu_heads import check_backward, check_prefill, run_backward, run_prefill, to_gpu, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +114,17 @@ def test_backward_of_several_heads_a_workgroup_without(no):
     assert head_shares(lens, H, G) < H
     c = ref.heads_inputs(36, lens, H, P, G, N, "bf16", no != "dt", no != "D")
     check_backward(c, run_backward(c))
+
+
+@pytest.mark.parametrize("lens", [[40, 3], [300]])
+def test_rows_too_far_apart_for_the_matrix_cores(lens):
+    """x in rows of more than 2^22 elements: token by token, in the workspace that the binding asks for then."""
+    T, far = sum(lens), 4194304 + 8
+    c = ref.heads_inputs(37, lens, 2, 16, 1, 32, "bf16")
+    g = to_gpu(c)
+    wide = torch.empty(T * far, dtype=torch.bfloat16, device="cuda").as_strided((T, 2, 16), (far, 16, 1))
+    wide.copy_(g["x"])
+    args = [wide] + tokens(g)[1:]
+    y, s = mm.heads_prefill(*args, g["cu"], g["state"])
+    check_prefill(c, y, s)
+    check_backward(c, mm.heads_backward(*args, g["cu"], g["state"], g["dy"], g["dstate"]))
