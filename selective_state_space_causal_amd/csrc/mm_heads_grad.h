@@ -18,8 +18,10 @@
 // (As row sums minus column sums from the block's end, which is one scan, dA_log and ddt_bias were off by 1.2e-6 where float32
 // arithmetic throughout gives 2e-7.)
 //
-// Precision: dx, dB and dC leave in bfloat16; their computed operands (M, W d, h, Gam) are rounded to bfloat16
-// once.  dl, r and what is summed from them (dA_log, ddt_bias: float32 results) use float32 products of the exact
+// Precision: dx, dB and dC leave in bfloat16, and their computed operands are rounded to bfloat16 once: delta M (dx), delta W d
+// and h and Gam (dB, dC).  A result is then off by its own rounding, 1.66e-3 of its norm, and dB and dC by an operand's, as large
+// again: 2.3e-3.  (delta W d in two parts takes dB to 1.7e-3, at one more barrier a head: 371 -> 383 us; h and Gam in two would
+// be two more each.)  dl, r and what is summed from them (dA_log, ddt_bias: float32 results) use float32 products of the exact
 // scores, and h and Gam in three bfloat16 parts (24 bits).
 #pragma once
 
