@@ -168,7 +168,8 @@ struct SeqLds {
   float v[kSeqTok][16 * KV], s[kSeqTok][16 * KV], u[kSeqTok][kSeqRows], o[kSeqTok][kSeqRows + 1];
   float del[kSeqTok], dec[kSeqTok];
 };
-template <typename IO, int KV, bool REV, bool LOCAL>
+// STORE: the blocks' states may be wanted (the backward's runs)
+template <typename IO, int KV, bool REV, bool LOCAL, bool STORE>
 __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp, int64_t item, SeqLds<KV>& lds) {
   constexpr int KP = 16 * KV;
   auto &sv = lds.v, &ss = lds.s;
@@ -247,7 +248,7 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
     }
     __syncthreads();
     if (ib + 1 < nb) load(ib + 1);
-    if (!LOCAL && q.store != nullptr && edge && r < q.R)
+    if (STORE && !LOCAL && q.store != nullptr && edge && r < q.R)
 #pragma unroll
       for (int i = 0; i < KV; ++i) {
         const int k = lane * KV + i;
@@ -294,14 +295,14 @@ __device__ __forceinline__ void heads_seq(const SeqRun<IO>& q, const HeadPar& hp
 template <typename IO, int KV, bool REV, bool LOCAL>
 __global__ __launch_bounds__(kSeqThreads) void k_heads_seq(SeqRun<IO> q, HeadPar hp) {
   __shared__ SeqLds<KV> lds;
-  heads_seq<IO, KV, REV, LOCAL>(q, hp, blockIdx.x, lds);
+  heads_seq<IO, KV, REV, LOCAL, REV>(q, hp, blockIdx.x, lds);
 }
 // a forward and a reverse run that do not need one another
 template <typename IO, int KV, bool LOCAL>
 __global__ __launch_bounds__(kSeqThreads) void k_heads_seq_both(SeqRun<IO> fwd, SeqRun<IO> rev, HeadPar hp) {
   __shared__ SeqLds<KV> lds;
-  if (blockIdx.y == 0) heads_seq<IO, KV, false, LOCAL>(fwd, hp, blockIdx.x, lds);
-  else heads_seq<IO, KV, true, LOCAL>(rev, hp, blockIdx.x, lds);
+  if (blockIdx.y == 0) heads_seq<IO, KV, false, LOCAL, true>(fwd, hp, blockIdx.x, lds);
+  else heads_seq<IO, KV, true, LOCAL, false>(rev, hp, blockIdx.x, lds);
 }
 
 // The states that the segments of a sequence start from, in place of what they add: one thread per
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(kSeqThreads) void k_heads_decode_any(Tok<IO> x, Tok
 
 // The same for N a multiple of 4 with every row on 16 bytes: RL lanes take a state row, 4 entries each, and a
 // thread two rows, so that a workgroup's accesses are contiguous.  Bound by the states' traffic, 8 P N bytes a
-// head, which passes the caches by (nontemporal).  256 rows, d 8192, state 64 x 128 (2.15 GB): 353 us, 6.2 TB/s
+// head, which passes the caches by (nontemporal).  256 rows, d 8192, state 64 x 128 (2.15 GB): 351 us, 6.2 TB/s
 // (traced mean; a plain copy reaches 6.2); when it was 363, one row per thread took 481, four 364, eight 611 (204
 // registers), plain accesses 392.
 constexpr int kDecodeRows = 2;

@@ -1,4 +1,5 @@
-// The gradients of the head scan on the matrix cores (bfloat16 io), in two kernels.
+// The gradients of the head scan on the matrix cores (bfloat16 io), in two kernels; at the end of the file the decays'
+// gradients of the token-by-token backward, from the same sums.
 //
 // k_heads_states walks the states: h forward, and from the last token to the first their adjoint
 //   Gam <- e^{c_last} Gam + sum_i e^{c_i} dy_i C_i^T          (the gradient of the state before a block)
@@ -18,10 +19,11 @@
 // (As row sums minus column sums from the block's end, which is one scan, dA_log and ddt_bias were off by 1.2e-6 where float32
 // arithmetic throughout gives 2e-7.)
 //
-// Precision: dx, dB and dC leave in bfloat16, and their computed operands are rounded to bfloat16 once: delta M (dx), delta W d
-// and h and Gam (dB, dC).  A result is then off by its own rounding, 1.66e-3 of its norm, and dB and dC by an operand's, as large
-// again: 2.3e-3.  (delta W d in two parts takes dB to 1.7e-3, at one more barrier a head: 371 -> 383 us; h and Gam in two would
-// be two more each.)  dl, r and what is summed from them (dA_log, ddt_bias: float32 results) use float32 products of the exact
+// Precision: dx, dB and dC leave in bfloat16.  Of their computed operands delta M (dx, whose own rounding hides it) and the
+// states h and Gam (dC, dB) are rounded to bfloat16 once; delta W d, the better part of dB, is taken in two parts.  dx and dB are
+// then off by their own rounding, 1.66e-3 to 1.7e-3 of their norm, dC, where the states weigh, by up to 2.3e-3 (the states in two
+// parts would be three more barriers a head; delta W d in one left dB at 2.3e-3 too, the call at 371 instead of 383 us).
+// dl, r and what is summed from them (dA_log, ddt_bias: float32 results) use float32 products of the exact
 // scores, and h and Gam in three bfloat16 parts (24 bits).
 #pragma once
 
@@ -54,9 +56,9 @@ struct StateGeo {
 
 // grid: (row, 64-channel block, slice) x direction; a wave takes 16 of the channels
 // The storing walks are bound by their stores: 8 x 2048 tokens, 24 heads 64 x 128, both directions, write 403 MB of
-// states in 152 us (traced mean, inputs of successive calls in different memory; 536 MB in all, 3.5 TB/s).  States pass the
+// states in 157 us (traced mean, inputs of successive calls in different memory; 536 MB in all, 3.4 TB/s).  States pass the
 // caches by, on the way out and in: the whole backward 382 us where plain accesses took 397 (4 x 2048 tokens 227 and
-// 262).  The local walks of 16384 tokens, 64 heads, take 96 us: VALU issue 32%, MFMA 22%, the rest waits in the chain of a
+// 262).  The local walks of 16384 tokens, 64 heads, take 95 us: VALU issue 32%, MFMA 22%, the rest waits in the chain of a
 // block (load, LDS, weights, product); shorter stretches would add carries.
 // LOCAL: what a segment adds to a zero state; else the whole walk, which stores.
 // (The two are told apart at compile time so that the stores' place among the outstanding accesses is known: a wait
@@ -362,9 +364,9 @@ struct GradGeo {
 
 // grid: (block, group, share of its heads)
 // B, C and the scores C . B stay for all heads of the workgroup, x, dy and the two states of the next head are loaded
-// under this one's products.  8 x 2048 tokens, 24 heads: 213 us (traced mean), of which its traffic (0.74 GB, the
+// under this one's products.  8 x 2048 tokens, 24 heads: 210 us (traced mean), of which its traffic (0.74 GB, the
 // states mostly) would be 120 at the copy's rate.  A head is a chain of products between barriers, and two workgroups
-// (256 registers, 27 more spilled; 81 KB of LDS) cover it in part: waves wait 66% of their cycles, VALU issue 28%, MFMA
+// (256 registers, 28 more spilled; 81 KB of LDS) cover it in part: waves wait 63% of their cycles, VALU issue 30%, MFMA
 // 12%.
 // Values that are not finite: masked zeros of M and of delta W d must not meet them in dy, C or B, so blocks that hold one
 // take those products token by token.  (x needs no such care: its products are masked before they are used.)
@@ -500,10 +502,10 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
       }
       __syncthreads();
       // scores dy_i . x_j; the tiles of delta M (for dx) now, those of delta W d (for dB, dC) later
-      hb4 m2[3];
+      hb4 m2[3], m2l[3];
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
-        m2[u] = none;
+        m2[u] = m2l[u] = none;
         if (u == 2 && wave < 2) continue;
         const int it = tile_i(u), jt = tile_j(u), i = 16 * it + li, j = 16 * jt + 4 * g;
         hf4 w = {0, 0, 0, 0};
@@ -536,6 +538,7 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         ds.tile(it, jt, tt, w, del, lane, li, g, add);
         *reinterpret_cast<hb4*>(sM + it * M16 + (mK ^ (jt << 5))) = to_bf4(m1);
         m2[u] = to_bf4(w2);
+        m2l[u] = to_bf4(w2 - to_f4(m2[u]));
       }
       __builtin_amdgcn_sched_barrier(0);
       // h C for q, in three parts; h's first part to LDS for dC
@@ -676,22 +679,26 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
         }
       }
       __syncthreads();
+      // delta W d's second part in dy's place, which is not needed any more
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        if (u == 2 && wave < 2) continue;
+        *reinterpret_cast<hb4*>(sY + tile_i(u) * M16 + (mK ^ (tile_j(u) << 5))) = m2l[u];
+      }
       {  // the next tiles' loads, now that the adjoint has left its registers
         const int hn = pb + 1 < q.npb ? h : h + 1, pn = pb + 1 < q.npb ? pb + 1 : 0;
         if (hn < h1) load(hn, pn);
       }
-      // dB and dC: from the adjoint, and within the block
+      // dB from the adjoint
 #pragma unroll
       for (int n = 0; n < NTW; ++n) {
         const int nt = wave * NTW + n;
         if (nt >= NT) continue;
-        hb8 gT[2], cT[2], bT[2];
+        hb8 gT[2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           const int o = 2 * ks * R16 + (aT ^ (nt << 5));
           gT[ks] = join(tr_read(sS + o), tr_read(sS + o + R16));
-          cT[ks] = join(tr_read(sC + o), tr_read(sC + o + R16));
-          bT[ks] = join(tr_read(sB + o), tr_read(sB + o + R16));
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -701,18 +708,39 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
             v = mfma(join(lds4(sX + t * M16 + (mK ^ (ks << 6))), lds4(sX + t * M16 + (mK ^ (ks << 6) ^ 32))), gT[ks], v);
           dB[t][n] += v * (*reinterpret_cast<const hf4*>(f + kGew * kMmaTok + 16 * t + 4 * g) *
                            *reinterpret_cast<const hf4*>(f + kGdel * kMmaTok + 16 * t + 4 * g));
-          if (odd_bc) continue;
+        }
+      }
+      __syncthreads();
+      // dB and dC within the block
+#pragma unroll
+      for (int n = 0; n < NTW; ++n) {
+        const int nt = wave * NTW + n;
+        if (nt >= NT) continue;
+        if (!odd_bc) {
+          hb8 cT[2], bT[2];
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
-            if (!(ks == 0 && t > 1)) {  // i >= j: rows j = 16 t ..
-              const char* ma = sM + 2 * ks * M16 + (mT ^ (t << 5));
-              dB[t][n] = mfma(join((t & 1) && t / 2 == ks ? none : tr_read(ma), tr_read(ma + M16)), cT[ks], dB[t][n]);
-            }
-            if (!(ks == 1 && t < 2)) {  // j <= i: rows i = 16 t ..
-              const char* ma = sM + t * M16;
-              dC[t][n] = mfma(join(lds4(ma + (mK ^ (ks << 6))), (t & 1) == 0 && t / 2 == ks ? none : lds4(ma + (mK ^ (ks << 6) ^ 32))),
-                              bT[ks], dC[t][n]);
-            }
+            const int o = 2 * ks * R16 + (aT ^ (nt << 5));
+            cT[ks] = join(tr_read(sC + o), tr_read(sC + o + R16));
+            bT[ks] = join(tr_read(sB + o), tr_read(sB + o + R16));
+          }
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const char* const sm = part ? sY : sM;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int ks = 0; ks < 2; ++ks) {
+                if (!(ks == 0 && t > 1)) {  // i >= j: rows j = 16 t ..
+                  const char* ma = sm + 2 * ks * M16 + (mT ^ (t << 5));
+                  dB[t][n] = mfma(join((t & 1) && t / 2 == ks ? none : tr_read(ma), tr_read(ma + M16)), cT[ks], dB[t][n]);
+                }
+                if (!(ks == 1 && t < 2)) {  // j <= i: rows i = 16 t ..
+                  const char* ma = sm + t * M16;
+                  dC[t][n] = mfma(join(lds4(ma + (mK ^ (ks << 6))), (t & 1) == 0 && t / 2 == ks ? none : lds4(ma + (mK ^ (ks << 6) ^ 32))),
+                                  bT[ks], dC[t][n]);
+                }
+              }
           }
         }
         if (odd_bc) {  // as for dx: C of earlier and B of later tokens have no part in a sum
@@ -723,14 +751,18 @@ __global__ __launch_bounds__(kMmaThreads, 2) void k_heads_grads(GradArgs q, Head
             const float b = io_value<uint16_t>(*reinterpret_cast<const uint16_t*>(sB + tile_at<PC>(u, col)));
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const hf4 m = to_f4(lds4(sM + tile_at<kMmaMP>(u, 16 * t + 4 * g)));
+              const int at = tile_at<kMmaMP>(u, 16 * t + 4 * g);
+              const hf4 m = to_f4(lds4(sM + at)) + to_f4(lds4(sY + at));
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int row = 16 * t + 4 * g + r;
                 if (row <= u) dB[t][n][r] = __builtin_fmaf(m[r], c, dB[t][n][r]);
-                if (row >= u)
-                  dC[t][n][r] = __builtin_fmaf(
-                      io_value<uint16_t>(*reinterpret_cast<const uint16_t*>(sM + tile_at<kMmaMP>(row, u))), b, dC[t][n][r]);
+                if (row >= u) {
+                  const int one = tile_at<kMmaMP>(row, u);
+                  dC[t][n][r] = __builtin_fmaf(io_value<uint16_t>(*reinterpret_cast<const uint16_t*>(sM + one)) +
+                                                   io_value<uint16_t>(*reinterpret_cast<const uint16_t*>(sY + one)),
+                                               b, dC[t][n][r]);
+                }
               }
             }
           }

@@ -24,8 +24,8 @@
 // workgroups to a CU, ran out of registers and took 590 us where two took 260.  A chunk is a chain of two barriers,
 // the products C . B, their decay, and two more products, and two workgroups (2 waves per SIMD: 245 registers, 75 KB
 // of LDS) overlap only in part: VALU issue 34%, MFMA 16% of the cycles, waves waiting 38%, LDS bank conflicts 15%.
-// Traced means, inputs of successive calls in different memory: 16384 packed tokens of 64 heads 64 x 128, one group, 123 us
-// (325 MB, 2.7 TB/s; the call 228); 32768 tokens of 80 heads, 8 groups, 286 us (3.5 TB/s; the call 453).
+// Traced means, inputs of successive calls in different memory: 16384 packed tokens of 64 heads 64 x 128, one group, 120 us
+// (325 MB, 2.7 TB/s; the call 228); 32768 tokens of 80 heads, 8 groups, 281 us (3.5 TB/s; the call 450).
 #pragma once
 
 #include <type_traits>

@@ -50,3 +50,22 @@ def test_float32_gradients_have_float32_errors(lens, H, P, G, N, io):
     for k in NAMES.values():
         log(f"  {k}: {(mine[k] / size[k]) ** 0.5:.2e}, float32 throughout {(plain[k] / size[k]) ** 0.5:.2e}")
         assert mine[k] <= 9 * plain[k], k
+
+
+def relative(got, want):
+    return float((got.double().cpu() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("lens,H,P,G,N", [([300], 8, 16, 1, 32), ([5, 74, 37, 100], 8, 64, 2, 100), ([3] * 150 + [70], 7, 64, 1, 64)])
+def test_bfloat16_gradients(lens, H, P, G, N):
+    """dx and dB without initial states and final gradients, where nothing rounded but M meets them: their errors are those of
+    one rounding of the result (at most 1.15 times, as the other operand's second part leaves 2^-17)."""
+    c = ref.heads_inputs(75, lens, H, P, G, N, "bf16", state=False)
+    c["dstate"].zero_()
+    want, got = ref.backward(c), run_backward(c)
+    for k in ("dx", "dB"):
+        exact = want[k][0]
+        once = relative(exact.to(torch.bfloat16), exact)
+        mine = relative(got[k], exact)
+        log(f"  {k}: {mine:.2e}, rounded once {once:.2e}")
+        assert mine <= 1.15 * once, k
