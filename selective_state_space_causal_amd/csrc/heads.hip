@@ -94,7 +94,7 @@ int plan_heads(HeadsPlan& p, int64_t S, int64_t T, int H, int P, int G, int N, i
   p.npb = static_cast<int>(cdiv(P, 64));
   p.nk = N <= 32 ? 1 : N <= 64 ? 2 : 4;
   // Two workgroups of the gradient kernel per CU, or one for each head.  (The count is that of full blocks; a few more
-  // than fit at once make a round of their own: 8 x 2048 tokens, 24 heads, 371 us, 8 x 2044 about 470.)
+  // than fit at once make a round of their own: 8 x 2048 tokens, 24 heads, 384 us, 8 x 2044 about 480.)
   p.splits = H > 0 ? static_cast<int>(std::max<int64_t>(
                  1, std::min<int64_t>(H / G, cdiv(2 * kCUs, std::max<int64_t>(segment_rows(S, T, kHeadsBlock) * G, 1))))) : 1;
   p.rows = segment_rows(S, T, p.Ls);

@@ -364,10 +364,10 @@ struct GradGeo {
 
 // grid: (block, group, share of its heads)
 // B, C and the scores C . B stay for all heads of the workgroup, x, dy and the two states of the next head are loaded
-// under this one's products.  8 x 2048 tokens, 24 heads: 210 us (traced mean), of which its traffic (0.74 GB, the
+// under this one's products.  8 x 2048 tokens, 24 heads: 228 us (traced mean), of which its traffic (0.73 GB, the
 // states mostly) would be 120 at the copy's rate.  A head is a chain of products between barriers, and two workgroups
-// (256 registers, 28 more spilled; 81 KB of LDS) cover it in part: waves wait 63% of their cycles, VALU issue 30%, MFMA
-// 12%.
+// (256 registers, 28 more spilled; 81 KB of LDS) cover it in part: waves wait 62% of their cycles, VALU issue 32%, MFMA
+// 14%.
 // Values that are not finite: masked zeros of M and of delta W d must not meet them in dy, C or B, so blocks that hold one
 // take those products token by token.  (x needs no such care: its products are masked before they are used.)
 template <int NK, bool VEC>
@@ -813,7 +813,7 @@ __global__ __launch_bounds__(256) void k_heads_shares(const float* __restrict__ 
 // workgroup per (block, head).  It stages 64 columns at a time of B and C, then of x and dy, the next ones loaded under
 // this one's products; for each 64 channels the states' columns go from memory to the wave that takes their 16 channels.
 // Lane l supplies row (or column) l % 16, and of 16 K indices 4g .. 4g+3, one to each of four products.
-// 8 x 2048 float32 tokens, 24 heads 64 x 128: 303 us of the call's 5090 (0.4 GB of states read, 19 GFLOP; 212 registers,
+// 8 x 2048 float32 tokens, 24 heads 64 x 128: 303 us of the call's 5080 (0.4 GB of states read, 19 GFLOP; 212 registers,
 // two workgroups a CU); 389 ragged tokens, 6 heads 40 x 24: 11 us of 58.  The sums of C . dC - B . dB from the block's end,
 // which need no scores, took 150 and 9 with errors of 1e-6 where these have 2e-7.
 // Four elements of a row, of which n exist (the others read as zeros); rows may start anywhere.  WIDE: rows have four at
