@@ -1,12 +1,16 @@
 """The committed rocprofv3 summaries are tied to the sources of the kernel they describe, and to those alone."""
 from __future__ import annotations
 
+import glob
 import os
+import re
 import shutil
 
 import pytest
 
 import bench
+
+PROFILES = sorted(glob.glob(os.path.join(bench.ROOT, "profiles", "*.txt")))
 
 
 def test_the_units_sources():
@@ -28,3 +32,9 @@ def test_a_change_makes_the_summaries_of_its_own_units_stale(tmp_path, changed):
         f.write("\n// changed\n")
     after = [bench.kernel_source_sha256(u, folder) for u in units]
     assert [a != b for a, b in zip(after, before)] == [changed in bench.kernel_sources(u, folder) for u in units]
+
+
+@pytest.mark.parametrize("path", PROFILES, ids=[os.path.basename(p) for p in PROFILES])
+def test_every_summary_names_its_sources(path):
+    text = open(path).read()
+    assert len(re.findall(r"^kernel source sha256: [0-9a-f]{64}$", text, re.M)) == 1
