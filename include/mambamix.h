@@ -547,6 +547,133 @@ int mamba_mixer_residual_norm_backward(const void* dout, const void* dresidual_o
                                        void* stream);
 size_t mamba_mixer_residual_norm_backward_workspace_bytes(int64_t rows, int32_t d);
 
+/*
+ * ------------------------------------------------------------------------------------------
+ * The causal depthwise convolution by itself, for layers that need it ahead of something else than the
+ * selective scan (the gates of a gated recurrence; x, B and C of a head scan).  For sequence s, place p and
+ * channel c, with X(q) = x for q >= 0 and X(q) = state_in[s, c, W - 1 + q] for q < 0:
+ *
+ *   u[p, c] = bias[c] + sum_k weight[c, k] X(p - W + 1 + k)        y = u, or SiLU(u) when silu != 0
+ *
+ *   x          [T, d]       io    rows x_stride elements apart
+ *   weight     [d, W] f32;  bias [d] f32 or NULL (zeros)
+ *   state_in   [S, d, W-1]  f32   the raw inputs before each sequence, oldest first, or NULL: zeros
+ *   state_out  [S, d, W-1]  f32   the newest W - 1 raw inputs after it; may be state_in itself (in place).
+ *                                 A sequence shorter than W - 1 keeps the end of its initial state.
+ *   y          [T, d]       io    contiguous
+ * y and state_out may overlap no input but state_out == state_in.  Limits: 2 <= W <= MM_CONV_MAX_W (else
+ * MM_ERR_UNSUPPORTED); a launch has less than 2^32 threads (else MM_ERR_DIM): ceil(T / 16) d < 2^31 and S d < 2^31.
+ * T == 0 copies the states; d == 0 is a no-op.
+ */
+#define MM_CONV_MAX_W 4
+int mamba_mixer_conv_prefill(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
+                             const float* state_in, float* state_out, void* y, int32_t S, int64_t T, int32_t d,
+                             int32_t W, int32_t silu, int32_t io_dtype, int64_t x_stride, void* stream);
+/* One token for each of Bs rows; row r is state slot r. */
+int mamba_mixer_conv_decode(const void* x, const float* weight, const float* bias, const float* state_in,
+                            float* state_out, void* y, int32_t Bs, int32_t d, int32_t W, int32_t silu,
+                            int32_t io_dtype, int64_t x_stride, void* stream);
+/* Its gradients, from dy [T, d] (io, contiguous) and dstate_out [S, d, W-1] (f32, or NULL: the loss does not depend
+ * on the final states): dx [T, d] (io, rows dx_stride apart), dweight [d, W], dbias [d] (NULL when bias is),
+ * dstate_in [S, d, W-1] (or NULL: not wanted), all overwritten, summed in a fixed order.  Outputs overlap no input
+ * and no other output.  workspace: mamba_mixer_conv_backward_workspace_bytes bytes, 256-byte aligned. */
+int mamba_mixer_conv_backward(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
+                              const float* state_in, const void* dy, const float* dstate_out, void* dx,
+                              float* dweight, float* dbias, float* dstate_in, int32_t S, int64_t T, int32_t d,
+                              int32_t W, int32_t silu, int32_t io_dtype, int64_t x_stride, int64_t dx_stride,
+                              void* workspace, size_t workspace_bytes, void* stream);
+size_t mamba_mixer_conv_backward_workspace_bytes(int64_t T, int32_t d, int32_t W);
+
+/*
+ * ------------------------------------------------------------------------------------------
+ * The gated recurrence: one decay and one state per channel, both gates from the token.
+ *
+ *   rho = sigmoid(r)      iota = sigmoid(g)  (g == NULL: 1)
+ *   with lam:             a = exp(-c softplus(lam) rho),  m = sqrt(1 - a^2)
+ *   lam == NULL:          a = rho,                        m = 1 - rho
+ *   h_t = a h_{t-1} + m iota x_t
+ *   y_t = h_t act(z_t)    act = SiLU (MM_GATE_SILU) or GELU in its tanh form (MM_GATE_GELU); z == NULL: 1
+ *
+ *   x, r, g, z [T, d]  io    rows x_stride, r_stride, g_stride, z_stride elements apart
+ *   lam        [d]     f32   c >= 0 a finite number
+ *   state_in   [S, d]  f32   initial states, or NULL: zeros
+ *   state_out  [S, d]  f32   final states; may be state_in itself (in place).  An empty sequence keeps its own.
+ *   y          [T, d]  io    contiguous
+ *   ckpt       NULL, or [ceil(T / MM_GATED_BLOCK), d] f32, out: the state before token MM_GATED_BLOCK b of the packed
+ *              stream, in that token's sequence (mamba_mixer_gated_checkpoint_bytes), for the backward
+ * The sequence boundaries and the io types are those of mamba_mixer_prefill.  y, state_out and ckpt may overlap no
+ * input but state_out == state_in.  workspace: mamba_mixer_gated_prefill_workspace_bytes bytes (0 for short calls),
+ * 256-byte aligned, contents on entry do not matter; it is one call's until that call has run.
+ * A launch has less than 2^32 threads (else MM_ERR_DIM): ceil(T / MM_GATED_BLOCK) ceil(d / 32) < 2^23 and S d < 2^31.
+ * T == 0 copies the states; d == 0 is a no-op.
+ */
+#define MM_GATE_SILU 0
+#define MM_GATE_GELU 1
+#define MM_GATED_BLOCK 256
+int mamba_mixer_gated_prefill(const void* x, const void* r, const void* g, const void* z, const float* lam,
+                              const int32_t* cu_seqlens, const float* state_in, float* state_out, void* y, float* ckpt,
+                              int32_t S, int64_t T, int32_t d, float c, int32_t gate, int32_t io_dtype,
+                              int64_t x_stride, int64_t r_stride, int64_t g_stride, int64_t z_stride, void* workspace,
+                              size_t workspace_bytes, void* stream);
+size_t mamba_mixer_gated_prefill_workspace_bytes(int64_t T, int32_t d);
+size_t mamba_mixer_gated_checkpoint_bytes(int64_t T, int32_t d);
+/* One token for each of Bs rows; row r is state slot r. */
+int mamba_mixer_gated_decode(const void* x, const void* r, const void* g, const void* z, const float* lam,
+                             const float* state_in, float* state_out, void* y, int32_t Bs, int32_t d, float c,
+                             int32_t gate, int32_t io_dtype, int64_t x_stride, int64_t r_stride, int64_t g_stride,
+                             int64_t z_stride, void* stream);
+/* Its gradients, from dy [T, d] (io, contiguous) and dstate_out [S, d] (f32, or NULL: the loss does not depend on the
+ * final states).  ckpt: what the forward call stored for these inputs, or NULL: the states are made again.
+ *   dx, dr, dg, dz [T, d] io, rows dx_stride ... dz_stride apart; dg is NULL when g is, dz when z is
+ *   dlam [d] f32, NULL when lam is;  dstate_in [S, d] f32, or NULL: not wanted
+ * All outputs are overwritten, summed in a fixed order, and overlap no input and no other output (column ranges of one
+ * array with the same row stride are taken apart).  workspace: mamba_mixer_gated_backward_workspace_bytes bytes,
+ * 256-byte aligned, one call's until that call has run. */
+int mamba_mixer_gated_backward(const void* x, const void* r, const void* g, const void* z, const float* lam,
+                               const int32_t* cu_seqlens, const float* state_in, const void* dy,
+                               const float* dstate_out, const float* ckpt, void* dx, void* dr, void* dg, void* dz,
+                               float* dlam, float* dstate_in, int32_t S, int64_t T, int32_t d, float c, int32_t gate,
+                               int32_t io_dtype, int64_t x_stride, int64_t r_stride, int64_t g_stride,
+                               int64_t z_stride, int64_t dx_stride, int64_t dr_stride, int64_t dg_stride,
+                               int64_t dz_stride, void* workspace, size_t workspace_bytes, void* stream);
+size_t mamba_mixer_gated_backward_workspace_bytes(int64_t T, int32_t d, int32_t has_ckpt);
+
+/*
+ * ------------------------------------------------------------------------------------------
+ * The norms of queries and keys, head by head, with the rotation by position in the same pass (C and B of a head
+ * scan are its queries and keys).  For every token and head, with n(v) = v / sqrt(mean(v^2) + eps) over D columns:
+ *
+ *   u = weight n(v)
+ *   the pair (u_i, u_j) of number k < R / 2 turns by the angle f = positions[t] inv_freq[k]:
+ *     (u_i cos f - u_j sin f,  u_j cos f + u_i sin f)
+ *   pairs: (k, k + R / 2), or (2 k, 2 k + 1) when interleaved != 0; columns R .. D - 1 are not turned
+ *
+ *   q, q_out [T, Hq, D], k, k_out [T, Hk, D] io   rows (one token's heads) q_stride, qo_stride, k_stride, ko_stride
+ *                                                 elements apart; q_out may be q and k_out k (the same strides)
+ *   q_weight, k_weight [D] f32
+ *   positions [T] int32, inv_freq [R / 2] f32     not read with R == 0 (no rotation)
+ * The angles are taken in 64 bits: far positions lose nothing.  Limits: 1 <= D <= MM_QK_MAX_D (else
+ * MM_ERR_UNSUPPORTED), R even and 0 <= R <= D, Hq, Hk >= 1, T (Hq + Hk) < 2^31 (else MM_ERR_DIM).
+ * T == 0 is a no-op.
+ */
+#define MM_QK_MAX_D 256
+int mamba_mixer_qk_norm(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                        const int32_t* positions, const float* inv_freq, void* q_out, void* k_out, int64_t T,
+                        int32_t Hq, int32_t Hk, int32_t D, int32_t R, float eps, int32_t interleaved, int32_t io_dtype,
+                        int64_t q_stride, int64_t k_stride, int64_t qo_stride, int64_t ko_stride, void* stream);
+/* Its gradients, from dq_out [T, Hq, D] and dk_out [T, Hk, D] (io, contiguous) and the call's inputs: dq, dk (io, rows
+ * dq_stride, dk_stride apart), dq_weight, dk_weight [D] f32, summed over tokens and heads in a fixed order.  Outputs
+ * overlap no input and no other output.  With T == 0 the weights' gradients are zeros.  workspace:
+ * mamba_mixer_qk_norm_backward_workspace_bytes bytes, 256-byte aligned. */
+int mamba_mixer_qk_norm_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                 const float* q_weight, const float* k_weight, const int32_t* positions,
+                                 const float* inv_freq, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                 int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R, float eps,
+                                 int32_t interleaved, int32_t io_dtype, int64_t q_stride, int64_t k_stride,
+                                 int64_t dq_stride, int64_t dk_stride, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+size_t mamba_mixer_qk_norm_backward_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D);
+
 /* Static text for a status code (never NULL).  Host only. */
 const char* mamba_mixer_status_string(int status);
 

@@ -108,6 +108,26 @@ def load() -> ctypes.CDLL:
     lib.mamba_mixer_residual_norm_backward.restype = ctypes.c_int
     lib.mamba_mixer_residual_norm_backward_workspace_bytes.argtypes = [i64, i32]
     lib.mamba_mixer_residual_norm_backward_workspace_bytes.restype = sz
+    lib.mamba_mixer_conv_prefill.argtypes = [P] * 7 + [i32, i64, i32, i32, i32, i32, i64, P]
+    lib.mamba_mixer_conv_decode.argtypes = [P] * 6 + [i32] * 5 + [i64, P]
+    lib.mamba_mixer_conv_backward.argtypes = [P] * 11 + [i32, i64, i32, i32, i32, i32, i64, i64, P, sz, P]
+    lib.mamba_mixer_conv_backward_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.mamba_mixer_gated_prefill.argtypes = [P] * 10 + [i32, i64, i32, f32, i32, i32] + [i64] * 4 + [P, sz, P]
+    lib.mamba_mixer_gated_prefill_workspace_bytes.argtypes = [i64, i32]
+    lib.mamba_mixer_gated_checkpoint_bytes.argtypes = [i64, i32]
+    lib.mamba_mixer_gated_decode.argtypes = [P] * 8 + [i32, i32, f32, i32, i32] + [i64] * 4 + [P]
+    lib.mamba_mixer_gated_backward.argtypes = [P] * 16 + [i32, i64, i32, f32, i32, i32] + [i64] * 8 + [P, sz, P]
+    lib.mamba_mixer_gated_backward_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.mamba_mixer_qk_norm.argtypes = [P] * 8 + [i64, i32, i32, i32, i32, f32, i32, i32] + [i64] * 4 + [P]
+    lib.mamba_mixer_qk_norm_backward.argtypes = ([P] * 12 + [i64, i32, i32, i32, i32, f32, i32, i32] + [i64] * 4
+                                                 + [P, sz, P])
+    lib.mamba_mixer_qk_norm_backward_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    for name in ("conv_prefill", "conv_decode", "conv_backward", "gated_prefill", "gated_decode", "gated_backward",
+                 "qk_norm", "qk_norm_backward"):
+        getattr(lib, "mamba_mixer_" + name).restype = ctypes.c_int
+    for name in ("conv_backward_workspace_bytes", "gated_prefill_workspace_bytes", "gated_checkpoint_bytes",
+                 "gated_backward_workspace_bytes", "qk_norm_backward_workspace_bytes"):
+        getattr(lib, "mamba_mixer_" + name).restype = sz
     lib.mamba_mixer_status_string.argtypes = [ctypes.c_int]
     lib.mamba_mixer_status_string.restype = ctypes.c_char_p
     lib.mamba_mixer_version.argtypes = []
@@ -647,3 +667,7 @@ def decode_replay_multi(x_ring, dt_ring, B_ring, z_ring, C_ring, A_log, D, dt_bi
 # the head scan and the norms around a mixer block
 from .heads import (gate_norm, gate_norm_backward, heads_backward, heads_decode,  # noqa: E402,F401
                     heads_prefill, residual_norm, residual_norm_backward)
+
+# the causal convolution, the gated recurrence and the norms of queries and keys
+from .layer import (conv_backward, conv_decode, conv_prefill, gated_backward, gated_decode,  # noqa: E402,F401
+                    gated_prefill, gated_prefill_train, qk_norm, qk_norm_backward)

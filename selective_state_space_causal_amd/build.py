@@ -7,7 +7,8 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = [os.path.join(HERE, "csrc", f) for f in ("mambamix.hip", "heads.hip")]
+CSRC = os.path.join(HERE, "csrc")
+SRC = [os.path.join(CSRC, f) for f in ("mambamix.hip", "heads.hip", "layer/conv.hip", "layer/gated.hip", "layer/qk_norm.hip")]
 LIB = os.path.join(HERE, "libmambamix.so")
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -29,7 +30,7 @@ def build(verbose: bool = False) -> str:
     objs, running = [], []
     for src in SRC:
         objs.append(f"{LIB}.{os.path.basename(src)}.o")
-        cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f != "-shared"], "-I", INCLUDE, "-c", "-o", objs[-1], src]
+        cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f != "-shared"], "-I", INCLUDE, "-I", CSRC, "-c", "-o", objs[-1], src]
         running.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
     said = "".join(p.communicate()[0] for p in running)
     tmp = LIB + ".tmp"
@@ -56,7 +57,7 @@ def asm(out: str) -> None:
     """Write the gfx950 device assembly of the library to ``out`` (for inspection), one source after another."""
     text = ""
     for src in SRC:
-        cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")], "-I", INCLUDE,
+        cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")], "-I", INCLUDE, "-I", CSRC,
                "--cuda-device-only", "-S", "-o", out, src]
         subprocess.run(cmd, check=True, capture_output=True)
         with open(out) as f:

@@ -1,0 +1,98 @@
+// What the units of the convolution, the gated recurrence and the head norm share: argument checks, and on the device
+// the sigmoid's pieces and the sums of partial results.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <initializer_list>
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "mambamix.h"
+#include "mm_device.h"
+#include "mm_host.h"
+
+namespace mm {
+namespace {
+
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;  // of one launch
+
+int launched() { return hipGetLastError() == hipSuccess ? MM_OK : MM_ERR_HIP; }
+size_t esize(int32_t io) { return io == MM_IO_BF16 ? 2 : 4; }
+
+// An array of a call: rows of `width` elements `stride` apart.  Arrays of zero bytes, and optional ones, may be NULL.
+struct Arg {
+  Rows r;
+  size_t es;
+  bool optional;
+};
+Arg strided(const void* p, int64_t rows, int64_t width, int64_t stride, size_t es, bool optional = false) {
+  return Arg{Rows{p, rows, static_cast<size_t>(width) * es, static_cast<size_t>(stride) * es}, es, optional};
+}
+Arg flat(const void* p, int64_t elements, size_t es, bool optional = false) {
+  const size_t n = static_cast<size_t>(elements) * es;
+  return Arg{Rows{p, 1, n, n}, es, optional};
+}
+struct Pair {
+  int out, in;
+};
+
+// NULL where an array is needed, addresses that are not of whole elements, outputs on an input or on another output;
+// `same`: the outputs that may be written over an input, at that very address.
+int check_args(std::initializer_list<Arg> ins, std::initializer_list<Arg> outs, std::initializer_list<Pair> same = {}) {
+  for (const auto& list : {ins, outs})
+    for (const Arg& a : list)
+      if (a.r.p == nullptr && !a.optional && a.r.extent() > 0) return MM_ERR_NULL;
+  for (const auto& list : {ins, outs})
+    for (const Arg& a : list)
+      if (!aligned(a.r.p, a.es)) return MM_ERR_ALIGN;
+  int o = 0;
+  for (const Arg* out = outs.begin(); out != outs.end(); ++out, ++o) {
+    if (out->r.p == nullptr) continue;
+    int i = 0;
+    for (const Arg* in = ins.begin(); in != ins.end(); ++in, ++i) {
+      bool in_place = false;
+      for (const Pair& s : same) in_place |= s.out == o && s.in == i && out->r.p == in->r.p && out->r.stride == in->r.stride;
+      if (in->r.p != nullptr && !in_place && overlap(out->r, in->r)) return MM_ERR_ALIAS;
+    }
+    for (const Arg* next = out + 1; next != outs.end(); ++next)
+      if (next->r.p != nullptr && overlap(out->r, next->r)) return MM_ERR_ALIAS;
+  }
+  return MM_OK;
+}
+
+// sizes of a call over T tokens in S sequences with d channels
+int check_tokens(int64_t S, int64_t T, int32_t d, int32_t io) {
+  if (S < 0 || T < 0 || d < 0 || T > INT32_MAX) return MM_ERR_DIM;
+  if (io != MM_IO_F32 && io != MM_IO_BF16) return MM_ERR_UNSUPPORTED;
+  if (S == 0 && T > 0) return MM_ERR_DIM;
+  const uint64_t n = static_cast<uint64_t>(d);
+  if (n > 0 && (static_cast<uint64_t>(T) > MM_MAX_ROWS_X_D / n || S * d >= (int64_t{1} << 31))) return MM_ERR_DIM;
+  return MM_OK;
+}
+int check_workspace(const void* p, size_t bytes, size_t need) {
+  if (need > 0 && (p == nullptr || bytes < need)) return MM_ERR_WORKSPACE;
+  return aligned(p, 256) ? MM_OK : MM_ERR_ALIGN;
+}
+
+// f(IO{}) for the io type
+template <typename F>
+int by_io(int32_t io, F f) {
+  return io == MM_IO_BF16 ? f(uint16_t{}) : f(float{});
+}
+
+}  // namespace
+
+// sigmoid(v), and both it and sigmoid(-v), the latter without the cancellation of 1 - sigmoid(v).  An infinite or NaN v is
+// taken as the formula has it.
+__device__ __forceinline__ float sigmoid(float v) { return rcp_hw(1.0f + exp2_hw(-v * kLog2e)); }
+struct Sigmoids {
+  float s, s1;
+};
+__device__ __forceinline__ Sigmoids sigmoids(float v) {
+  const float e = exp2_hw(-v * kLog2e), s = rcp_hw(1.0f + e);
+  return {s, v < 0.0f ? 1.0f - s : e * s};
+}
+
+}  // namespace mm
