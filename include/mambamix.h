@@ -604,12 +604,13 @@ size_t mamba_mixer_conv_backward_workspace_bytes(int64_t T, int32_t d, int32_t W
  * The sequence boundaries and the io types are those of mamba_mixer_prefill.  y, state_out and ckpt may overlap no
  * input but state_out == state_in.  workspace: mamba_mixer_gated_prefill_workspace_bytes bytes (0 for short calls),
  * 256-byte aligned, contents on entry do not matter; it is one call's until that call has run.
- * A launch has less than 2^32 threads (else MM_ERR_DIM): ceil(T / MM_GATED_BLOCK) ceil(d / 32) < 2^23 and S d < 2^31.
- * T == 0 copies the states; d == 0 is a no-op.
+ * Rows are at most MM_LAYER_MAX_STRIDE elements apart (else MM_ERR_UNSUPPORTED).  S < 2^29, and a launch has less than
+ * 2^32 threads: ceil(T / MM_GATED_BLOCK) ceil(d / 64) < 2^24 and S d < 2^31 (else MM_ERR_DIM).  T == 0 copies the states; d == 0 is a no-op.
  */
+#define MM_LAYER_MAX_STRIDE (1 << 22)
 #define MM_GATE_SILU 0
 #define MM_GATE_GELU 1
-#define MM_GATED_BLOCK 256
+#define MM_GATED_BLOCK 64
 int mamba_mixer_gated_prefill(const void* x, const void* r, const void* g, const void* z, const float* lam,
                               const int32_t* cu_seqlens, const float* state_in, float* state_out, void* y, float* ckpt,
                               int32_t S, int64_t T, int32_t d, float c, int32_t gate, int32_t io_dtype,

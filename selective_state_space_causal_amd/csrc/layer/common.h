@@ -95,4 +95,51 @@ __device__ __forceinline__ Sigmoids sigmoids(float v) {
   return {s, v < 0.0f ? 1.0f - s : e * s};
 }
 
+// V neighbouring channels of one token as loaded.  Rows may start at any element: accesses need no more alignment.
+template <typename IO, int V>
+struct Chans {
+  static constexpr int W = (V * static_cast<int>(sizeof(IO)) + 3) / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+};
+// `off` bytes behind a base that is the same in the whole wave
+template <typename IO, int V>
+__device__ __forceinline__ Chans<IO, V> load_chans(gmem<const IO>* p, uint32_t off) {
+  constexpr int W = Chans<IO, V>::W;
+  Chans<IO, V> r;
+  gmem<const char>* q = reinterpret_cast<gmem<const char>*>(p) + off;
+  if constexpr (V * sizeof(IO) == 2) {
+    r.w[0] = __builtin_nontemporal_load(reinterpret_cast<gmem<const uint16_t>*>(q));
+  } else if constexpr (W == 1) {
+    typedef uint32_t word __attribute__((aligned(2)));
+    r.w[0] = __builtin_nontemporal_load(reinterpret_cast<gmem<const word>*>(q));
+  } else {
+    typedef uint32_t vec __attribute__((ext_vector_type(W), aligned(sizeof(IO))));
+    const vec v = __builtin_nontemporal_load(reinterpret_cast<gmem<const vec>*>(q));
+#pragma unroll
+    for (int i = 0; i < W; ++i) r.w[i] = v[i];
+  }
+  return r;
+}
+template <typename IO, int V>
+__device__ __forceinline__ void store_chans(gmem<IO>* p, uint32_t off, const float (&f)[V]) {
+  gmem<char>* q = reinterpret_cast<gmem<char>*>(p) + off;
+  typedef float fv __attribute__((ext_vector_type(V), aligned(4)));
+  fv t;
+#pragma unroll
+  for (int i = 0; i < V; ++i) t[i] = f[i];
+  if constexpr (sizeof(IO) == 2) {
+    typedef __bf16 bv __attribute__((ext_vector_type(V)));
+    typedef uint16_t hv __attribute__((ext_vector_type(V), aligned(2)));
+    __builtin_nontemporal_store(__builtin_bit_cast(hv, __builtin_convertvector(t, bv)), reinterpret_cast<gmem<hv>*>(q));  // round to nearest even
+  } else {
+    __builtin_nontemporal_store(t, reinterpret_cast<gmem<fv>*>(q));
+  }
+}
+template <typename IO>
+__device__ __forceinline__ gmem<IO>* global(IO* p) { return reinterpret_cast<gmem<IO>*>(reinterpret_cast<uint64_t>(p)); }
+
 }  // namespace mm

@@ -1,5 +1,7 @@
 // The gated recurrence: kernels, argument checks and entry points.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "layer/common.h"
 
@@ -13,25 +15,406 @@ struct GatedArgs {
   const float* state_in;
   int64_t x_ts, r_ts, g_ts, z_ts, T;
   int S, d;
-  float c, c0, c1;  // the output gate: z sigmoid(z (c0 + c1 z^2))
+  float c;
+  bool gelu;
 };
 
 // c softplus(lam) log2(e), so that a = exp2(-kap rho); NaN stays NaN
-__device__ __forceinline__ float gated_kap(const GatedArgs& a, int c) {
-  if (a.lam == nullptr) return 0.0f;
-  const float v = a.lam[c];
-  return (v != v ? v : softplus(v)) * a.c * kLog2e;
+__device__ __forceinline__ float gated_kap(float lam, float c) { return (lam != lam ? lam : softplus(lam)) * c * kLog2e; }
+
+// The decay a and the input's factor m of one element.  With l = log2 a = -kap rho, 1 - a^2 = -expm1(2 ln2 l): five terms of its
+// series near 0 (4e-8 of it at a^2 = e^-1/8), 1 - a a beyond (there a's last unit is 5e-7 of m).
+struct Decay {
+  float a, m;
+};
+__device__ __forceinline__ float gated_m2(float l, float a) {
+  constexpr float b = 2.0f * kLn2;
+  float s = __builtin_fmaf(l, -b * b * b * b * b / 120, -b * b * b * b / 24);
+  s = __builtin_fmaf(s, l, -b * b * b / 6);
+  s = __builtin_fmaf(s, l, -b * b / 2);
+  s = __builtin_fmaf(s, l, -b);
+  return l > -0.125f / b ? s * l : __builtin_fmaf(-a, a, 1.0f);
+}
+template <bool LAM>
+__device__ __forceinline__ Decay gated_decay(float r, float kap) {
+  if constexpr (!LAM) {
+    const Sigmoids s = sigmoids(r);
+    return {s.s, s.s1};
+  } else {
+    const float l = -kap * sigmoid(r), a = exp2_hw(l);
+    return {a, __builtin_amdgcn_sqrtf(gated_m2(l, a))};
+  }
+}
+// The output gate z sigmoid(k): k = z, or for GELU's tanh form k = 2 sqrt(2 / pi) (z + 0.044715 z^3).
+constexpr float kGelu0 = 1.5957691216057308f, kGelu1 = 1.5957691216057308f * 0.044715f;
+__device__ __forceinline__ float gated_act(bool gelu, float z) {
+  return gelu ? z * rcp_hw(1.0f + exp2_hw(z * __builtin_fmaf(-kGelu1 * kLog2e, z * z, -kGelu0 * kLog2e))) : z * sigmoid(z);
 }
 
-// The decay and the input's factor of one element, and what their gradients need.
-//   1 - a^2 = -expm1(t), t = 2 log a: a series near 0 (six terms, 5e-8 of it at t = -1/4), 1 - a a beyond.
-struct Decay {
+// One pass over the tokens.  A workgroup takes a tile: kGatedTile tokens of the packed stream by 256 bytes of channels.  A thread
+// has V neighbouring channels and a run of K tokens: every (a, b = m iota x) of them is in registers from the load to the
+// store, so each array is read and written once.  Runs compose as pairs (A, h): h_out = A h_in + h; the first threads put
+// a tile's runs together, one for each channel, and the tiles of a channel are a chain in memory:
+//   - a tile publishes its own pair as soon as it has it;
+//   - every kGatedGroup-th tile also publishes its final state;
+//   - a tile's initial state is that of the last whole group of tiles before it, taken through the pairs of the tiles since.
+// The order of these products does not depend on timing: results repeat bit for bit.  The links that wait for one another are
+// one in kGatedGroup tiles.  Tiles are numbered by tickets, not by the workgroup's index, so a tile waits only for tiles
+// whose workgroups run already or are done, and every wait ends.
+// Where a sequence starts, A is set to -1: what comes before has no part in what follows, whatever it is (0 times an infinity
+// would have).
+constexpr int kGatedTile = 2 * MM_GATED_BLOCK, kGatedThreads = 512, kGatedGroup = 8;
+constexpr uint32_t kGatedQueues = 4, kGatedQueueStep = 64;  // tickets: counters, and elements between them
+template <typename IO, int V, int TILE>
+struct GatedShape {
+  static constexpr int C = V == 1 ? 64 : 256 / sizeof(IO);  // channels of a tile
+  static constexpr int lanes = C / V;                     // of a token
+  static constexpr int runs = kGatedThreads / lanes;
+  static constexpr int K = TILE / runs;                     // tokens of a run
+};
+
+// ---------------------------------------------------------------- the chain of a channel's tiles
+typedef unsigned long long u64;
+constexpr u64 kUnset = ~0ull;  // no pair: a NaN is published as 0x7FC00000 in its place
+
+struct GatedChain {
+  u64* pairs;        // [tiles, d]: A in the upper half, h in the lower
+  u64* states;       // [tiles / kGatedGroup, d]: h
+  uint32_t* tickets;  // a counter for each queue, apart
+};
+__device__ __forceinline__ u64 gated_pair(float A, float h) {
+  return static_cast<u64>(A != A ? 0x7FC00000u : __float_as_uint(A)) << 32 | __float_as_uint(h);
+}
+// Written through to where all XCDs see it; the value itself says that it is there, so nothing else has to be ordered.
+__device__ __forceinline__ void gated_publish(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ u64 gated_read(const u64* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// What comes into tile `n` (in the chain's order) of a run that goes back to tile `first`: the last whole group's state, and
+// the pairs of the tiles since.
+struct Incoming {
+  u64 state, pairs[kGatedGroup - 1];
+  int64_t from;
+  int count;
+  bool older;
+};
+__device__ __forceinline__ Incoming gated_from(int64_t n, int64_t first) {
+  const int64_t group = n / kGatedGroup * kGatedGroup;
+  Incoming in;
+  in.older = first < group;
+  in.from = in.older ? group : first;
+  in.count = static_cast<int>(n - in.from);
+  in.state = in.older ? kUnset : 0;
+#pragma unroll
+  for (int i = 0; i < kGatedGroup - 1; ++i) in.pairs[i] = kUnset;
+  return in;
+}
+// One look at channel c0 + c of d; whether all of it is there.
+__device__ __forceinline__ bool gated_look(Incoming& in, const GatedChain& ch, int64_t d, int64_t c0, uint32_t c) {
+  if (in.older) in.state = gated_read(ch.states + (in.from / kGatedGroup - 1) * d + c0 + c);
+#pragma unroll
+  for (int i = 0; i < kGatedGroup - 1; ++i)
+    if (i < in.count) in.pairs[i] = gated_read(ch.pairs + (in.from + i) * d + c0 + c);
+  bool there = in.state != kUnset;
+#pragma unroll
+  for (int i = 0; i < kGatedGroup - 1; ++i) there &= i >= in.count || in.pairs[i] != kUnset;
+  return there;
+}
+__device__ __forceinline__ float gated_state(const Incoming& in) {
+  float h = __uint_as_float(static_cast<uint32_t>(in.state));
+#pragma unroll
+  for (int i = 0; i < kGatedGroup - 1; ++i)
+    if (i < in.count) {
+      const float A = __uint_as_float(static_cast<uint32_t>(in.pairs[i] >> 32)), l = __uint_as_float(static_cast<uint32_t>(in.pairs[i]));
+      h = A < 0.0f ? l : __builtin_fmaf(A, h, l);
+    }
+  return h;
+}
+// Every wait ends: the tiles before have their tickets, and what waits for them never holds them up.  A workspace that another
+// call overwrites meanwhile would break that: after so many looks (seconds) the tile goes on with what it has, kUnset being a NaN.
+constexpr int kGatedLooks = 1 << 21;
+
+__global__ __launch_bounds__(256) void k_gated_clear(u64* p, int64_t n, uint32_t* tickets) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) p[i] = kUnset;
+  if (i < kGatedQueues) tickets[i * kGatedQueueStep] = 0;
+}
+
+// A token's place: its sequence and whether it is the first or the last of it.  Behind the last token: neither.
+struct Place {
+  int v;
+  __device__ bool starts() const { return v & 1; }
+  __device__ bool ends() const { return v & 2; }
+  __device__ int seq() const { return v >> 2; }
+};
+__device__ __forceinline__ void gated_places(const int32_t* __restrict__ cu, int S, int64_t T, int64_t t0, Place* place) {
+  for (int i = threadIdx.x; i < kGatedTile; i += kGatedThreads) {
+    const int64_t t = t0 + i;
+    int v = 0;
+    if (t < T) {
+      const int s = seq_of(cu, S, t);
+      v = s << 2 | (cu[s] == t ? 1 : 0) | (cu[s + 1] == t + 1 ? 2 : 0);
+    }
+    place[i].v = v;
+  }
+}
+// Final states of empty sequences, channels c0 .. c0 + width: wave `part` of `parts` looks through its share of the sequences.
+__device__ __forceinline__ void gated_empty(const int32_t* __restrict__ cu, int S, const float* in, float* out, int64_t d, int64_t c0,
+                                            int width, int64_t part, int64_t parts) {
+  if (out == in) return;
+  const int lane = threadIdx.x & 63;
+  for (int64_t s0 = part * 64; s0 < S; s0 += parts * 64) {
+    const int64_t s = s0 + lane;
+    u64 empty = __ballot(s < S && cu[s < S ? s : 0] == cu[s < S ? s + 1 : 0]);
+    for (; empty != 0; empty &= empty - 1) {
+      const int64_t e = (s0 + __builtin_ctzll(empty)) * d;
+      for (int64_t c = c0 + lane; c < c0 + width && c < d; c += 64) out[e + c] = in != nullptr ? in[e + c] : 0.0f;
+    }
+  }
+}
+
+// LDS is written, a wave's loads from memory may stay in flight
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The ticket's tile: queue q has the slices q, q + kGatedQueues, ..., tile by tile (one counter for all is at its limit, 10 ns a
+// ticket).  As many workgroups as tiles: a queue that is through hands its workgroups on to the next one.
+__device__ __forceinline__ uint32_t gated_take(uint32_t* tickets, uint32_t tiles, uint32_t slices) {
+  for (uint32_t q = blockIdx.x % kGatedQueues;; q = (q + 1) % kGatedQueues) {
+    const uint32_t w = (slices + kGatedQueues - 1 - q) / kGatedQueues;
+    const uint32_t t = atomicAdd(tickets + q * kGatedQueueStep, 1u);
+    if (t < w * tiles) return t / w * slices + t % w * kGatedQueues + q;
+  }
+}
+
+// OUT: y and the final states; else only the checkpoints (for a backward without the forward's)
+template <typename IO, int V, bool LAM, bool OUT>
+__global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedChain ch, float* state_out, IO* y, float* ckpt) {
+  typedef GatedShape<IO, V, kGatedTile> Shape;
+  constexpr int K = Shape::K, C = Shape::C, NG = Shape::runs;
+  __shared__ float sA[NG][C], sH[NG][C], sC[C];
+  __shared__ Place place[kGatedTile];
+  __shared__ uint32_t turn;
+  const int64_t d = a.d;
+  const uint32_t slices = static_cast<uint32_t>((d + C - 1) / C), tiles = gridDim.x / slices;
+  uint32_t id = blockIdx.x;
+  if (tiles > 1) {
+    if (threadIdx.x == 0) turn = gated_take(ch.tickets, tiles, slices);
+    lds_barrier();
+    id = __builtin_amdgcn_readfirstlane(turn);
+  }
+  const uint32_t tile = id / slices;
+  const int64_t c0 = static_cast<int64_t>(id % slices) * C, t0 = static_cast<int64_t>(tile) * kGatedTile;
+  const int lane = threadIdx.x % Shape::lanes, run = threadIdx.x / Shape::lanes;
+  const int64_t c = c0 + lane * V;
+  const bool on = c < d, whole = t0 + kGatedTile <= a.T;
+  const int64_t left = a.T - t0 - run * K;  // tokens of this run, if under K
+
+  Chans<IO, V> rx[K], rr[K], rg[K], rz[K];
+  const auto load = [&](const void* p, int64_t ts, Chans<IO, V>(&v)[K]) {
+    gmem<const IO>* base = sbase(static_cast<const IO*>(p) + t0 * ts + c0);
+    const uint32_t step = static_cast<uint32_t>(ts * static_cast<int64_t>(sizeof(IO)));
+    uint32_t off = run * K * step + lane * V * static_cast<uint32_t>(sizeof(IO));
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        v[k] = load_chans<IO, V>(base, off);
+        off += step;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        v[k] = Chans<IO, V>{};
+        if (k < left) v[k] = load_chans<IO, V>(base, off);
+        off += step;
+      }
+    }
+  };
+  float kap[V];
+  if (on) {
+    load(a.r, a.r_ts, rr);
+    load(a.x, a.x_ts, rx);
+    if (a.g != nullptr) load(a.g, a.g_ts, rg);
+#pragma unroll
+    for (int i = 0; i < V; ++i) kap[i] = LAM ? gated_kap(a.lam[c + i], a.c) : 0.0f;
+  }
+  const int seq = seq_of(a.cu, a.S, t0);
+  const int64_t lo = a.cu[seq], hi = a.cu[seq + 1];
+  const bool cut = lo == t0 || hi <= t0 + kGatedTile;  // sequences start or end in the tile
+  if (cut) {
+    gated_places(a.cu, a.S, a.T, t0, place);
+    lds_barrier();
+  }
+
+  float da[K][V], db[K][V], A[V], h[V];
+  uint32_t starts = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    A[i] = 1.0f;
+    h[i] = 0.0f;
+  }
+  if (on) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const Decay v = gated_decay<LAM>(rr[k][i], kap[i]);
+        da[k][i] = v.a;
+        db[k][i] = v.m * rx[k][i];
+      }
+      if (a.g != nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) db[k][i] *= sigmoid(rg[k][i]);
+      }
+      if (cut) {
+        const Place p = place[run * K + k];
+        if (p.starts()) {  // the run so far has no part in it; its initial state becomes part of its input
+          starts |= 1u << k;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (a.state_in != nullptr) db[k][i] = __builtin_fmaf(da[k][i], a.state_in[p.seq() * d + c + i], db[k][i]);
+            h[i] = 0.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        A[i] *= da[k][i];
+        h[i] = __builtin_fmaf(da[k][i], h[i], db[k][i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one token after the other: fewer registers
+    }
+    if (OUT && a.z != nullptr) load(a.z, a.z_ts, rz);  // on its way while the tile waits for the one before
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    sA[run][lane * V + i] = starts != 0 ? -1.0f : A[i];
+    sH[run][lane * V + i] = h[i];
+  }
+  const int64_t cc = c0 + threadIdx.x;
+  const bool chain = threadIdx.x < C && cc < d, waits = lo != t0;
+  Incoming in = gated_from(tile, lo / kGatedTile);
+  bool there = !(chain && waits) || gated_look(in, ch, d, c0, threadIdx.x);  // the first look is under way while the runs are put together
+  lds_barrier();
+  if (chain) {
+    const int j = threadIdx.x;
+    float At = 1.0f, ht = 0.0f, from = 0.0f, Am = 0.0f, hm = 0.0f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float Ag = sA[g][j], hg = sH[g][j];
+      if (g == NG / 2) {
+        Am = At;
+        hm = ht;
+      }
+      sA[g][j] = At;
+      sH[g][j] = ht;
+      ht = Ag < 0.0f ? hg : __builtin_fmaf(Ag, ht, hg);
+      At = Ag < 0.0f || At < 0.0f ? -1.0f : At * Ag;
+    }
+    if (tile + 1 < tiles) gated_publish(ch.pairs + tile * d + cc, gated_pair(At, ht));
+    if (waits) {
+      for (int look = 0; !there && look < kGatedLooks; ++look) {
+        __builtin_amdgcn_s_sleep(1);
+        there = gated_look(in, ch, d, c0, threadIdx.x);
+      }
+      from = gated_state(in);
+    } else if (a.T > 0 && a.state_in != nullptr) {
+      from = a.state_in[seq * d + cc];
+    }
+    if (tile + 1 < tiles && tile % kGatedGroup == kGatedGroup - 1)
+      gated_publish(ch.states + tile / kGatedGroup * d + cc, __float_as_uint(At < 0.0f ? ht : __builtin_fmaf(At, from, ht)));
+    if (ckpt != nullptr && a.T > 0) {
+      static_assert(kGatedTile == 2 * MM_GATED_BLOCK, "a checkpoint before the tile and one in its middle");
+      ckpt[static_cast<int64_t>(2) * tile * d + cc] = from;
+      if (t0 + MM_GATED_BLOCK < a.T) {
+        float middle = Am < 0.0f ? hm : __builtin_fmaf(Am, from, hm);
+        const Place p = place[MM_GATED_BLOCK];
+        if (cut && p.starts()) middle = a.state_in != nullptr ? a.state_in[p.seq() * d + cc] : 0.0f;
+        ckpt[(static_cast<int64_t>(2) * tile + 1) * d + cc] = middle;
+      }
+    }
+    sC[j] = from;
+  }
+  if (!OUT) return;
+  lds_barrier();
+  gated_empty(a.cu, a.S, a.state_in, state_out, d, c0, C, tile * (kGatedThreads / 64) + threadIdx.x / 64, tiles * (kGatedThreads / 64));
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float Ap = sA[run][lane * V + i], hp = sH[run][lane * V + i];
+    h[i] = Ap < 0.0f ? hp : __builtin_fmaf(Ap, sC[lane * V + i], hp);
+  }
+  gmem<IO>* base = sbase(y + t0 * d + c0);
+  const uint32_t step = static_cast<uint32_t>(d * static_cast<int64_t>(sizeof(IO)));
+  uint32_t off = run * K * step + lane * V * static_cast<uint32_t>(sizeof(IO));
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (cut && (starts >> k & 1)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) db[k][i] = h[i] = __builtin_fmaf(da[k][i], h[i], db[k][i]);
+    if (cut) {
+      const Place p = place[run * K + k];
+      if (p.ends()) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) state_out[p.seq() * d + c + i] = h[i];
+      }
+    }
+    if (a.z != nullptr) {
+      if (a.gelu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) db[k][i] *= gated_act(true, rz[k][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) db[k][i] *= gated_act(false, rz[k][i]);
+      }
+    }
+    if (whole || k < left) store_chans<IO, V>(base, off, db[k]);
+    off += step;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// One token a row: V channels a thread.
+template <typename IO, int V, bool LAM>
+__global__ __launch_bounds__(256) void k_gated_decode(GatedArgs a, float* state_out, IO* y) {
+  const int64_t n = static_cast<int64_t>(a.S) * a.d;
+  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
+  if (i0 >= n) return;
+  const int64_t row = i0 / a.d;
+  const int c = static_cast<int>(i0 - row * a.d);
+  const auto load = [&](const void* p, int64_t ts) {
+    return load_chans<IO, V>(global(static_cast<const IO*>(p) + row * ts + c), 0);
+  };
+  const Chans<IO, V> r = load(a.r, a.r_ts), x = load(a.x, a.x_ts);
+  Chans<IO, V> g{}, z{};
+  if (a.g != nullptr) g = load(a.g, a.g_ts);
+  if (a.z != nullptr) z = load(a.z, a.z_ts);
+  float h[V], o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float h0 = a.state_in != nullptr ? a.state_in[i0 + i] : 0.0f;
+    const Decay v = gated_decay<LAM>(r[i], LAM ? gated_kap(a.lam[c + i], a.c) : 0.0f);
+    const float u = a.g != nullptr ? x[i] * sigmoid(g[i]) : x[i];
+    h[i] = __builtin_fmaf(v.a, h0, v.m * u);
+    o[i] = a.z != nullptr ? h[i] * gated_act(a.gelu, z[i]) : h[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) state_out[i0 + i] = h[i];
+  store_chans<IO, V>(global(y + i0), 0, o);
+}
+
+struct DecayS {
   float a, m;      // decay, input factor
   float rho, rho1; // sigmoid(r), sigmoid(-r)
   float L, q;      // log a, log a / m (lam given)
 };
-__device__ __forceinline__ Decay gated_decay(float r, float kap, bool lam) {
-  Decay v;
+__device__ __forceinline__ DecayS gated_decay_s(float r, float kap, bool lam) {
+  DecayS v;
   const Sigmoids s0 = sigmoids(r);
   v.rho = s0.s;
   v.rho1 = s0.s1;
@@ -57,34 +440,34 @@ __device__ __forceinline__ Decay gated_decay(float r, float kap, bool lam) {
   v.q = v.L * rm;
   return v;
 }
-__device__ __forceinline__ float gated_act(const GatedArgs& a, float z, float& slope) {
+__device__ __forceinline__ float gated_act_s(const GatedArgs& a, float z, float& slope) {
   const float z2 = fminf(z * z, 1e8f);  // far beyond where the sigmoid is 0 or 1; c1 may be 0
-  const Sigmoids v = sigmoids(z * __builtin_fmaf(a.c1, z2, a.c0));
-  slope = __builtin_fmaf(z * v.s * v.s1, __builtin_fmaf(3.0f * a.c1, z2, a.c0), v.s);
+  const Sigmoids v = sigmoids(z * __builtin_fmaf((a.gelu ? kGelu1 : 0.0f), z2, (a.gelu ? kGelu0 : 1.0f)));
+  slope = __builtin_fmaf(z * v.s * v.s1, __builtin_fmaf(3.0f * (a.gelu ? kGelu1 : 0.0f), z2, (a.gelu ? kGelu0 : 1.0f)), v.s);
   return z * v.s;
 }
 
 template <typename IO>
-__device__ float at(const void* p, int64_t ts, int64_t t, int c) { return ld_io(static_cast<const IO*>(p), t * ts + c); }
+__device__ float at_(const void* p, int64_t ts, int64_t t, int c) { return ld_io(static_cast<const IO*>(p), t * ts + c); }
 
 // a thread for each (sequence, channel); before: NULL or [T, d], the state before each token
 template <typename IO>
-__global__ __launch_bounds__(256) void k_gated(GatedArgs a, float* state_out, IO* __restrict__ y, float* __restrict__ ckpt,
+__global__ __launch_bounds__(256) void k_gated_seq(GatedArgs a, float* state_out, IO* __restrict__ y, float* __restrict__ ckpt,
                                                float* __restrict__ before) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(a.S) * a.d) return;
   const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
   const int64_t t0 = a.cu != nullptr ? a.cu[s] : s, t1 = a.cu != nullptr ? a.cu[s + 1] : s + 1;
-  const float kap = gated_kap(a, c);
+  const float kap = a.lam != nullptr ? gated_kap(a.lam[c], a.c) : 0.0f;
   float h = a.state_in != nullptr ? a.state_in[i] : 0.0f, slope;
   for (int64_t t = t0; t < t1; ++t) {
     if (ckpt != nullptr && t % MM_GATED_BLOCK == 0) ckpt[t / MM_GATED_BLOCK * a.d + c] = h;
     if (before != nullptr) before[t * a.d + c] = h;
-    const Decay v = gated_decay(at<IO>(a.r, a.r_ts, t, c), kap, a.lam != nullptr);
-    float u = at<IO>(a.x, a.x_ts, t, c);
-    if (a.g != nullptr) u *= sigmoid(at<IO>(a.g, a.g_ts, t, c));
+    const DecayS v = gated_decay_s(at_<IO>(a.r, a.r_ts, t, c), kap, a.lam != nullptr);
+    float u = at_<IO>(a.x, a.x_ts, t, c);
+    if (a.g != nullptr) u *= sigmoid(at_<IO>(a.g, a.g_ts, t, c));
     h = __builtin_fmaf(v.a, h, v.m * u);
-    if (y != nullptr) st_io(y, t * a.d + c, a.z != nullptr ? h * gated_act(a, at<IO>(a.z, a.z_ts, t, c), slope) : h);
+    if (y != nullptr) st_io(y, t * a.d + c, a.z != nullptr ? h * gated_act_s(a, at_<IO>(a.z, a.z_ts, t, c), slope) : h);
   }
   if (state_out != nullptr) state_out[i] = h;
 }
@@ -106,14 +489,14 @@ __global__ __launch_bounds__(256) void k_gated_bwd(GatedArgs a, GatedGrads o) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(a.S) * a.d) return;
   const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
-  const float kap = gated_kap(a, c);
+  const float kap = a.lam != nullptr ? gated_kap(a.lam[c], a.c) : 0.0f;
   float G = o.dstate_out != nullptr ? o.dstate_out[i] : 0.0f;
   for (int64_t t = a.cu[s + 1] - int64_t{1}; t >= a.cu[s]; --t) {
-    const Decay v = gated_decay(at<IO>(a.r, a.r_ts, t, c), kap, a.lam != nullptr);
-    const float x = at<IO>(a.x, a.x_ts, t, c), h0 = o.before[t * a.d + c];
+    const DecayS v = gated_decay_s(at_<IO>(a.r, a.r_ts, t, c), kap, a.lam != nullptr);
+    const float x = at_<IO>(a.x, a.x_ts, t, c), h0 = o.before[t * a.d + c];
     float iota = 1.0f, iota1 = 0.0f;
     if (a.g != nullptr) {
-      const Sigmoids v = sigmoids(at<IO>(a.g, a.g_ts, t, c));
+      const Sigmoids v = sigmoids(at_<IO>(a.g, a.g_ts, t, c));
       iota = v.s;
       iota1 = v.s1;
     }
@@ -121,7 +504,7 @@ __global__ __launch_bounds__(256) void k_gated_bwd(GatedArgs a, GatedGrads o) {
     float dh = ld_io(static_cast<const IO*>(o.dy), t * a.d + c);
     if (a.z != nullptr) {
       float slope;
-      const float act = gated_act(a, at<IO>(a.z, a.z_ts, t, c), slope);
+      const float act = gated_act_s(a, at_<IO>(a.z, a.z_ts, t, c), slope);
       st_io(static_cast<IO*>(o.dz), t * o.dz_ts + c, dh * __builtin_fmaf(v.a, h0, v.m * u) * slope);
       dh *= act;
     }
@@ -153,26 +536,57 @@ __global__ __launch_bounds__(256) void k_gated_dlam(const float* __restrict__ pa
   dlam[c] = v * (l < -20.0f ? 1.0f : sigmoid(l) / (l != l ? l : softplus(l)));
 }
 
-int64_t gated_blocks(int64_t T) { return cdiv(T, MM_GATED_BLOCK); }
+int64_t gated_blocks(int64_t T) { return cdiv(T, MM_GATED_BLOCK); }  // checkpoints
+int64_t gated_tiles(int64_t T) { return cdiv(T, kGatedTile); }
 
 int check_gated(int64_t S, int64_t T, int32_t d, float c, int32_t gate, int32_t io) {
   const int rc = check_tokens(S, T, d, io);
   if (rc != MM_OK) return rc;
   if (gate != MM_GATE_SILU && gate != MM_GATE_GELU) return MM_ERR_UNSUPPORTED;
   if (!(c >= 0.0f) || std::isinf(c)) return MM_ERR_DIM;
-  if (gated_blocks(T) * cdiv(d, 32) >= (int64_t{1} << 23)) return MM_ERR_DIM;
+  if (S >= (int64_t{1} << 29)) return MM_ERR_DIM;  // a token's place holds its sequence and two bits
+  if (gated_blocks(T) * cdiv(d, 64) >= (int64_t{1} << 24)) return MM_ERR_DIM;
   return MM_OK;
 }
-bool strides(const GatedArgs& a) {
-  return a.x_ts >= a.d && a.r_ts >= a.d && (a.g == nullptr || a.g_ts >= a.d) && (a.z == nullptr || a.z_ts >= a.d);
+// the chain in the workspace: the ticket, the tiles' pairs, their groups' states
+constexpr size_t kTicketBytes = kGatedQueues * kGatedQueueStep * 4;
+struct ChainLayout {
+  int64_t pairs, states;  // elements
+  size_t total;
+};
+ChainLayout chain_layout(int64_t tiles, int32_t d) {
+  if (tiles <= 1) return {0, 0, 0};
+  const int64_t pairs = tiles * d, states = tiles / kGatedGroup * d;
+  return {pairs, states, align256(kTicketBytes + static_cast<size_t>(pairs + states) * 8)};
+}
+GatedChain start_chain(int64_t tiles, int32_t d, void* ws, hipStream_t st) {
+  const ChainLayout l = chain_layout(tiles, d);
+  if (l.total == 0) return GatedChain{};
+  u64* p = reinterpret_cast<u64*>(static_cast<char*>(ws) + kTicketBytes);
+  const int64_t n = l.pairs + l.states;
+  hipLaunchKernelGGL(k_gated_clear, dim3(static_cast<unsigned>(cdiv(n, 256))), dim3(256), 0, st, p, n, static_cast<uint32_t*>(ws));
+  return GatedChain{p, p + l.pairs, static_cast<uint32_t*>(ws)};
+}
+// f(V as a type) for d channels: pairs of them where every thread's are all there or all missing
+template <typename IO, typename F>
+int by_channels(int32_t d, F f) {
+  if (d % 4 == 0) return f(std::integral_constant<int, 4>{});
+  if constexpr (sizeof(IO) == 2)
+    if (d % 2 == 0) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 1>{});
+}
+// rows at least d apart, and near enough for the offsets within a tile to have 32 bits
+int check_strides(int32_t d, std::initializer_list<int64_t> ts) {
+  for (int64_t s : ts)
+    if (s < d) return MM_ERR_DIM;
+  for (int64_t s : ts)
+    if (s > MM_LAYER_MAX_STRIDE) return MM_ERR_UNSUPPORTED;
+  return MM_OK;
 }
 GatedArgs gated_args(const void* x, const void* r, const void* g, const void* z, const float* lam, const int32_t* cu,
                      const float* state_in, int64_t x_ts, int64_t r_ts, int64_t g_ts, int64_t z_ts, int64_t T, int S, int d,
                      float c, int gate) {
-  // GELU's tanh form is z sigmoid(2 sqrt(2 / pi) (z + 0.044715 z^3))
-  const float k = 1.5957691216057308f;
-  return GatedArgs{x, r, g, z, lam, cu, state_in, x_ts, r_ts, g_ts, z_ts, T, S, d, c,
-                   gate == MM_GATE_GELU ? k : 1.0f, gate == MM_GATE_GELU ? k * 0.044715f : 0.0f};
+  return GatedArgs{x, r, g, z, lam, cu, state_in, x_ts, r_ts, g_ts, z_ts, T, S, d, c, gate == MM_GATE_GELU};
 }
 }  // namespace
 }  // namespace mm
@@ -181,7 +595,10 @@ using namespace mm;
 
 extern "C" {
 
-size_t mamba_mixer_gated_prefill_workspace_bytes(int64_t T, int32_t d) { return 0; }
+size_t mamba_mixer_gated_prefill_workspace_bytes(int64_t T, int32_t d) {
+  if (check_gated(1, T, d, 0.0f, MM_GATE_SILU, MM_IO_F32) != MM_OK) return 0;
+  return chain_layout(gated_tiles(T), d).total;
+}
 
 size_t mamba_mixer_gated_checkpoint_bytes(int64_t T, int32_t d) {
   if (check_gated(1, T, d, 0.0f, MM_GATE_SILU, MM_IO_F32) != MM_OK) return 0;
@@ -196,7 +613,7 @@ int mamba_mixer_gated_prefill(const void* x, const void* r, const void* g, const
   int rc = check_gated(S, T, d, c, gate, io_dtype);
   if (rc != MM_OK) return rc;
   const GatedArgs a = gated_args(x, r, g, z, lam, cu_seqlens, state_in, x_stride, r_stride, g_stride, z_stride, T, S, d, c, gate);
-  if (!strides(a)) return MM_ERR_DIM;
+  if ((rc = check_strides(d, {x_stride, r_stride, g != nullptr ? g_stride : d, z != nullptr ? z_stride : d})) != MM_OK) return rc;
   if (d == 0) return MM_OK;
   const size_t es = esize(io_dtype);
   const int64_t ns = static_cast<int64_t>(S) * d;
@@ -207,11 +624,17 @@ int mamba_mixer_gated_prefill(const void* x, const void* r, const void* g, const
   if (rc != MM_OK) return rc;
   rc = check_workspace(workspace, workspace_bytes, mamba_mixer_gated_prefill_workspace_bytes(T, d));
   if (rc != MM_OK || S == 0) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
   return by_io(io_dtype, [&](auto io) {
     using IO = decltype(io);
-    hipLaunchKernelGGL((k_gated<IO>), dim3(static_cast<unsigned>(cdiv(ns, 256))), dim3(256), 0, static_cast<hipStream_t>(stream),
-                       a, state_out, static_cast<IO*>(y), ckpt, static_cast<float*>(nullptr));
-    return launched();
+    return by_channels<IO>(d, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      const GatedChain ch = start_chain(gated_tiles(T), d, workspace, st);
+      const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, gated_tiles(T)) * cdiv(d, GatedShape<IO, V, kGatedTile>::C)));
+      if (lam != nullptr) hipLaunchKernelGGL((k_gated<IO, V, true, true>), grid, dim3(kGatedThreads), 0, st, a, ch, state_out, static_cast<IO*>(y), ckpt);
+      else hipLaunchKernelGGL((k_gated<IO, V, false, true>), grid, dim3(kGatedThreads), 0, st, a, ch, state_out, static_cast<IO*>(y), ckpt);
+      return launched();
+    });
   });
 }
 
@@ -222,7 +645,7 @@ int mamba_mixer_gated_decode(const void* x, const void* r, const void* g, const 
   int rc = check_gated(Bs, Bs, d, c, gate, io_dtype);
   if (rc != MM_OK) return rc;
   const GatedArgs a = gated_args(x, r, g, z, lam, nullptr, state_in, x_stride, r_stride, g_stride, z_stride, Bs, Bs, d, c, gate);
-  if (!strides(a)) return MM_ERR_DIM;
+  if ((rc = check_strides(d, {x_stride, r_stride, g != nullptr ? g_stride : d, z != nullptr ? z_stride : d})) != MM_OK) return rc;
   const int64_t n = static_cast<int64_t>(Bs) * d;
   if (n == 0) return MM_OK;
   const size_t es = esize(io_dtype);
@@ -230,11 +653,16 @@ int mamba_mixer_gated_decode(const void* x, const void* r, const void* g, const 
                    strided(z, Bs, d, z_stride, es, true), flat(lam, d, 4, true), flat(state_in, n, 4, true)},
                   {flat(state_out, n, 4), flat(y, n, es)}, {{0, 5}});
   if (rc != MM_OK) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
   return by_io(io_dtype, [&](auto io) {
     using IO = decltype(io);
-    hipLaunchKernelGGL((k_gated<IO>), dim3(static_cast<unsigned>(cdiv(n, 256))), dim3(256), 0, static_cast<hipStream_t>(stream),
-                       a, state_out, static_cast<IO*>(y), static_cast<float*>(nullptr), static_cast<float*>(nullptr));
-    return launched();
+    return by_channels<IO>(d, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      const dim3 grid(static_cast<unsigned>(cdiv(n, 256 * V)));
+      if (lam != nullptr) hipLaunchKernelGGL((k_gated_decode<IO, V, true>), grid, dim3(256), 0, st, a, state_out, static_cast<IO*>(y));
+      else hipLaunchKernelGGL((k_gated_decode<IO, V, false>), grid, dim3(256), 0, st, a, state_out, static_cast<IO*>(y));
+      return launched();
+    });
   });
 }
 
@@ -253,8 +681,9 @@ int mamba_mixer_gated_backward(const void* x, const void* r, const void* g, cons
   int rc = check_gated(S, T, d, c, gate, io_dtype);
   if (rc != MM_OK) return rc;
   const GatedArgs a = gated_args(x, r, g, z, lam, cu_seqlens, state_in, x_stride, r_stride, g_stride, z_stride, T, S, d, c, gate);
-  if (!strides(a) || dx_stride < d || dr_stride < d || (g != nullptr && dg_stride < d) || (z != nullptr && dz_stride < d))
-    return MM_ERR_DIM;
+  rc = check_strides(d, {x_stride, r_stride, g != nullptr ? g_stride : d, z != nullptr ? z_stride : d, dx_stride, dr_stride,
+                         g != nullptr ? dg_stride : d, z != nullptr ? dz_stride : d});
+  if (rc != MM_OK) return rc;
   if (d == 0) return MM_OK;
   const size_t es = esize(io_dtype);
   const int64_t ns = static_cast<int64_t>(S) * d;
@@ -275,7 +704,7 @@ int mamba_mixer_gated_backward(const void* x, const void* r, const void* g, cons
     using IO = decltype(io);
     const dim3 grid(static_cast<unsigned>(cdiv(ns, 256)));
     if (S > 0) {
-      hipLaunchKernelGGL((k_gated<IO>), grid, dim3(256), 0, st, a, static_cast<float*>(nullptr), static_cast<IO*>(nullptr),
+      hipLaunchKernelGGL((k_gated_seq<IO>), grid, dim3(256), 0, st, a, static_cast<float*>(nullptr), static_cast<IO*>(nullptr),
                          static_cast<float*>(nullptr), before);
       hipLaunchKernelGGL((k_gated_bwd<IO>), grid, dim3(256), 0, st, a, o);
     }

@@ -10,7 +10,7 @@ from . import check_cu_seqlens
 from .heads import _code, _need, _new, _on, _opt, _out, _raise, _rows, _workspace
 
 GATES = {"silu": 0, "gelu": 1}
-GATED_BLOCK = 256  # MM_GATED_BLOCK: tokens between two checkpoints
+GATED_BLOCK = 64  # MM_GATED_BLOCK: tokens between two checkpoints
 
 _current_device = None
 

@@ -157,19 +157,19 @@ def test_sizes_at_the_launches_limits(lib):
     assert conv_backward(lib, far(11), T=2 ** 31 - 1, d=15, xs=15, gx=15, wsb=0) == WORKSPACE
     assert conv_backward(lib, far(11), T=2 ** 31 - 1, d=16, xs=16, gx=16, wsb=0) == DIM
     rows = lambda d: {k: d for k in ("d", "xs", "rs", "gs", "zs", "dxs", "drs", "dgs", "dzs")}  # noqa: E731
-    assert gated_backward(lib, far(16), T=2 ** 31 - 512, wsb=0, **rows(32)) == WORKSPACE
-    assert gated_backward(lib, far(16), T=2 ** 31 - 1, wsb=0, **rows(32)) == DIM
+    assert gated_backward(lib, far(16), T=2 ** 30 - 256, wsb=0, **rows(32)) == WORKSPACE
+    assert gated_backward(lib, far(16), T=2 ** 30, wsb=0, **rows(32)) == DIM
     assert qk_backward(lib, far(12), T=(2 ** 31 - 1) // 6, wsb=0) == WORKSPACE
 
 
 def test_size_queries(lib):
     assert lib.mamba_mixer_conv_backward_workspace_bytes(4000, 64, 4) > lib.mamba_mixer_conv_backward_workspace_bytes(40, 64, 4) > 0
     assert lib.mamba_mixer_conv_backward_workspace_bytes(40, 64, 5) == 0 == lib.mamba_mixer_conv_backward_workspace_bytes(-1, 64, 4)
-    assert lib.mamba_mixer_gated_checkpoint_bytes(257, 10) == 80 and lib.mamba_mixer_gated_checkpoint_bytes(-1, 10) == 0
+    assert lib.mamba_mixer_gated_checkpoint_bytes(65, 10) == 80 and lib.mamba_mixer_gated_checkpoint_bytes(-1, 10) == 0
     assert lib.mamba_mixer_gated_backward_workspace_bytes(1 << 20, 64, 0) >= lib.mamba_mixer_gated_backward_workspace_bytes(1 << 20, 64, 1) > 0
     assert lib.mamba_mixer_gated_prefill_workspace_bytes(1, 64) == 0
     assert lib.mamba_mixer_qk_norm_backward_workspace_bytes(10, 2, 2, 64) > 0 == lib.mamba_mixer_qk_norm_backward_workspace_bytes(10, 2, 2, 300)
-    assert mm.layer.GATED_BLOCK == 256
+    assert mm.layer.GATED_BLOCK == 64
 
 
 def test_binding_checks():
