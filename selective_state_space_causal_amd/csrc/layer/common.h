@@ -92,7 +92,7 @@ struct Sigmoids {
 };
 __device__ __forceinline__ Sigmoids sigmoids(float v) {
   const float e = exp2_hw(-v * kLog2e), s = rcp_hw(1.0f + e);
-  return {s, v < 0.0f ? 1.0f - s : e * s};
+  return {s, fminf(e * s, 1.0f)};  // an e that is infinite meets s = 0, and their product's NaN is 1 here; v = NaN shows in s
 }
 
 // V neighbouring channels of one token as loaded.  Rows may start at any element: accesses need no more alignment.
@@ -141,5 +141,32 @@ __device__ __forceinline__ void store_chans(gmem<IO>* p, uint32_t off, const flo
 }
 template <typename IO>
 __device__ __forceinline__ gmem<IO>* global(IO* p) { return reinterpret_cast<gmem<IO>*>(reinterpret_cast<uint64_t>(p)); }
+
+// The sum of `parts` rows' column c (d columns), in the first kPartColumns threads of a workgroup of 256: kPartColumns columns, eight
+// threads each, in a fixed order.
+constexpr int kPartColumns = 32;
+__device__ __forceinline__ float sum_parts(const float* __restrict__ part, int64_t parts, int64_t d, int64_t c) {
+  __shared__ float s[256 / kPartColumns][kPartColumns];
+  const int row = threadIdx.x / kPartColumns, col = threadIdx.x % kPartColumns;
+  constexpr int rows = 256 / kPartColumns;
+  float v = 0.0f;
+  if (c < d) {
+    int64_t i = row;
+    for (; i + 7 * rows < parts; i += 8 * rows) {
+      float t[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[k] = part[(i + k * rows) * d + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += t[k];
+    }
+    for (; i < parts; i += rows) v += part[i * d + c];
+  }
+  s[row][col] = v;
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (int k = 0; k < rows; ++k) t += s[k][col];
+  return t;
+}
 
 }  // namespace mm

@@ -63,7 +63,7 @@ __device__ __forceinline__ float gated_act(bool gelu, float z) {
 // whose workgroups run already or are done, and every wait ends.
 // Where a sequence starts, A is set to -1: what comes before has no part in what follows, whatever it is (0 times an infinity
 // would have).
-constexpr int kGatedTile = 2 * MM_GATED_BLOCK, kGatedThreads = 512, kGatedGroup = 8;
+constexpr int kGatedTile = 2 * MM_GATED_BLOCK, kGatedThreads = 512, kGatedGroup = 6;
 constexpr uint32_t kGatedQueues = 4, kGatedQueueStep = 64;  // tickets: counters, and elements between them
 template <typename IO, int V, int TILE>
 struct GatedShape {
@@ -87,7 +87,7 @@ __device__ __forceinline__ u64 gated_pair(float A, float h) {
 }
 // Written through to where all XCDs see it; the value itself says that it is there, so nothing else has to be ordered.
 __device__ __forceinline__ void gated_publish(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ __forceinline__ u64 gated_read(const u64* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ u64 gated_read(gmem<const u64>* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 // What comes into tile `n` (in the chain's order) of a run that goes back to tile `first`: the last whole group's state, and
 // the pairs of the tiles since.
@@ -110,10 +110,11 @@ __device__ __forceinline__ Incoming gated_from(int64_t n, int64_t first) {
 }
 // One look at channel c0 + c of d; whether all of it is there.
 __device__ __forceinline__ bool gated_look(Incoming& in, const GatedChain& ch, int64_t d, int64_t c0, uint32_t c) {
-  if (in.older) in.state = gated_read(ch.states + (in.from / kGatedGroup - 1) * d + c0 + c);
+  // scalar bases: the looks run where every thread's tile is in registers
+  if (in.older) in.state = gated_read(sbase(static_cast<const u64*>(ch.states) + (in.from / kGatedGroup - 1) * d + c0) + c);
 #pragma unroll
   for (int i = 0; i < kGatedGroup - 1; ++i)
-    if (i < in.count) in.pairs[i] = gated_read(ch.pairs + (in.from + i) * d + c0 + c);
+    if (i < in.count) in.pairs[i] = gated_read(sbase(static_cast<const u64*>(ch.pairs) + (in.from + i) * d + c0) + c);
   bool there = in.state != kUnset;
 #pragma unroll
   for (int i = 0; i < kGatedGroup - 1; ++i) there &= i >= in.count || in.pairs[i] != kUnset;
@@ -146,8 +147,9 @@ struct Place {
   __device__ bool ends() const { return v & 2; }
   __device__ int seq() const { return v >> 2; }
 };
+template <int TILE>
 __device__ __forceinline__ void gated_places(const int32_t* __restrict__ cu, int S, int64_t T, int64_t t0, Place* place) {
-  for (int i = threadIdx.x; i < kGatedTile; i += kGatedThreads) {
+  for (int i = threadIdx.x; i < TILE; i += kGatedThreads) {
     const int64_t t = t0 + i;
     int v = 0;
     if (t < T) {
@@ -244,7 +246,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
   const int64_t lo = a.cu[seq], hi = a.cu[seq + 1];
   const bool cut = lo == t0 || hi <= t0 + kGatedTile;  // sequences start or end in the tile
   if (cut) {
-    gated_places(a.cu, a.S, a.T, t0, place);
+    gated_places<kGatedTile>(a.cu, a.S, a.T, t0, place);
     lds_barrier();
   }
 
@@ -408,130 +410,355 @@ __global__ __launch_bounds__(256) void k_gated_decode(GatedArgs a, float* state_
   store_chans<IO, V>(global(y + i0), 0, o);
 }
 
-struct DecayS {
-  float a, m;      // decay, input factor
-  float rho, rho1; // sigmoid(r), sigmoid(-r)
-  float L, q;      // log a, log a / m (lam given)
-};
-__device__ __forceinline__ DecayS gated_decay_s(float r, float kap, bool lam) {
-  DecayS v;
-  const Sigmoids s0 = sigmoids(r);
-  v.rho = s0.s;
-  v.rho1 = s0.s1;
-  if (!lam) {
-    v.a = v.rho;
-    v.m = v.rho1;
-    v.L = v.q = 0.0f;
-    return v;
-  }
-  const float la = -kap * v.rho;
-  v.a = exp2_hw(la);
-  v.L = la * kLn2;
-  const float t = 2.0f * v.L;
-  float s = __builtin_fmaf(t, 1.0f / 6, 1.0f);
-  s = __builtin_fmaf(s * t, 1.0f / 5, 1.0f);
-  s = __builtin_fmaf(s * t, 1.0f / 4, 1.0f);
-  s = __builtin_fmaf(s * t, 1.0f / 3, 1.0f);
-  s = __builtin_fmaf(s * t, 1.0f / 2, 1.0f);
-  const float m2 = t > -0.25f ? -t * s : __builtin_fmaf(-v.a, v.a, 1.0f);
-  // a decay of 1 has m = 0, and log a / m tends to 0 with it
-  const float rm = __builtin_amdgcn_rsqf(__builtin_elementwise_maximum(m2, 1.2e-38f));
-  v.m = m2 * rm;
-  v.q = v.L * rm;
-  return v;
-}
-__device__ __forceinline__ float gated_act_s(const GatedArgs& a, float z, float& slope) {
-  const float z2 = fminf(z * z, 1e8f);  // far beyond where the sigmoid is 0 or 1; c1 may be 0
-  const Sigmoids v = sigmoids(z * __builtin_fmaf((a.gelu ? kGelu1 : 0.0f), z2, (a.gelu ? kGelu0 : 1.0f)));
-  slope = __builtin_fmaf(z * v.s * v.s1, __builtin_fmaf(3.0f * (a.gelu ? kGelu1 : 0.0f), z2, (a.gelu ? kGelu0 : 1.0f)), v.s);
-  return z * v.s;
-}
-
-template <typename IO>
-__device__ float at_(const void* p, int64_t ts, int64_t t, int c) { return ld_io(static_cast<const IO*>(p), t * ts + c); }
-
-// a thread for each (sequence, channel); before: NULL or [T, d], the state before each token
-template <typename IO>
-__global__ __launch_bounds__(256) void k_gated_seq(GatedArgs a, float* state_out, IO* __restrict__ y, float* __restrict__ ckpt,
-                                               float* __restrict__ before) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.S) * a.d) return;
-  const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
-  const int64_t t0 = a.cu != nullptr ? a.cu[s] : s, t1 = a.cu != nullptr ? a.cu[s + 1] : s + 1;
-  const float kap = a.lam != nullptr ? gated_kap(a.lam[c], a.c) : 0.0f;
-  float h = a.state_in != nullptr ? a.state_in[i] : 0.0f, slope;
-  for (int64_t t = t0; t < t1; ++t) {
-    if (ckpt != nullptr && t % MM_GATED_BLOCK == 0) ckpt[t / MM_GATED_BLOCK * a.d + c] = h;
-    if (before != nullptr) before[t * a.d + c] = h;
-    const DecayS v = gated_decay_s(at_<IO>(a.r, a.r_ts, t, c), kap, a.lam != nullptr);
-    float u = at_<IO>(a.x, a.x_ts, t, c);
-    if (a.g != nullptr) u *= sigmoid(at_<IO>(a.g, a.g_ts, t, c));
-    h = __builtin_fmaf(v.a, h, v.m * u);
-    if (y != nullptr) st_io(y, t * a.d + c, a.z != nullptr ? h * gated_act_s(a, at_<IO>(a.z, a.z_ts, t, c), slope) : h);
-  }
-  if (state_out != nullptr) state_out[i] = h;
-}
-
-// With G the adjoint of h:  dx = G m iota,  dg = G m x iota (1 - iota),  dz = dy h act'(z), and
-//   lam given: log a's gradient times log a is  e = G (a h' L - u a^2 L / m),  dr = e (1 - rho),
+// ---------------------------------------------------------------- backward
+// With G the adjoint of h, h' the state before the token and u = iota x:
+//   G_t = dy act(z) + a_{t+1} G_{t+1};   dx = G m iota,  dg = G m u (1 - iota),  dz = dy h act'(z)
+//   lam given: log a's gradient times log a is  e = G (a h' L - u a^2 L / m),  L = log a:  dr = e (1 - rho),
 //              dlam = sum e sigmoid(lam) / softplus(lam)
-//   else:      dr = G (h' - u) rho (1 - rho)                    (h' the state before, u = iota x)
+//   else:      dr = G (h' - u) rho (1 - rho)
+// m tends to 0 with L, and L / m with it.
+// One pass from the last tile to the first, in the forward's manner: R = a G is what a token hands to the one before it, so a
+// run is a pair (A, R) and the tiles are a chain.  The states before each token come from the checkpoint before the tile.
+// What a thread keeps of a token from the first look to the gradients are a and h', and the inputs as they were loaded: the
+// rest is computed twice, which costs less than the registers.
 struct GatedGrads {
   const void* dy;
-  const float* dstate_out;
-  float* before;  // the states before each token; then log a's gradients times log a
+  const float *dstate_out, *ckpt;
   void *dx, *dr, *dg, *dz;
   int64_t dx_ts, dr_ts, dg_ts, dz_ts;
-  float* dstate_in;
+  float *dstate_in, *part;  // part: [tiles, d], sums of e over a tile's tokens
 };
-template <typename IO>
-__global__ __launch_bounds__(256) void k_gated_bwd(GatedArgs a, GatedGrads o) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.S) * a.d) return;
-  const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
-  const float kap = a.lam != nullptr ? gated_kap(a.lam[c], a.c) : 0.0f;
-  float G = o.dstate_out != nullptr ? o.dstate_out[i] : 0.0f;
-  for (int64_t t = a.cu[s + 1] - int64_t{1}; t >= a.cu[s]; --t) {
-    const DecayS v = gated_decay_s(at_<IO>(a.r, a.r_ts, t, c), kap, a.lam != nullptr);
-    const float x = at_<IO>(a.x, a.x_ts, t, c), h0 = o.before[t * a.d + c];
-    float iota = 1.0f, iota1 = 0.0f;
-    if (a.g != nullptr) {
-      const Sigmoids v = sigmoids(at_<IO>(a.g, a.g_ts, t, c));
-      iota = v.s;
-      iota1 = v.s1;
-    }
-    const float u = iota * x;
-    float dh = ld_io(static_cast<const IO*>(o.dy), t * a.d + c);
-    if (a.z != nullptr) {
-      float slope;
-      const float act = gated_act_s(a, at_<IO>(a.z, a.z_ts, t, c), slope);
-      st_io(static_cast<IO*>(o.dz), t * o.dz_ts + c, dh * __builtin_fmaf(v.a, h0, v.m * u) * slope);
-      dh *= act;
-    }
-    G += dh;
-    st_io(static_cast<IO*>(o.dx), t * o.dx_ts + c, G * v.m * iota);
-    if (a.g != nullptr) st_io(static_cast<IO*>(o.dg), t * o.dg_ts + c, G * v.m * u * iota1);
-    float dr;
-    if (a.lam != nullptr) {
-      const float e = G * v.a * (h0 * v.L - u * v.a * v.q);
-      o.before[t * a.d + c] = e;
-      dr = e * v.rho1;
-    } else {
-      dr = G * (h0 - u) * v.rho * v.rho1;
-    }
-    st_io(static_cast<IO*>(o.dr), t * o.dr_ts + c, dr);
-    G *= v.a;
-  }
-  if (o.dstate_in != nullptr) o.dstate_in[i] = G;
+// the slope of the output gate
+__device__ __forceinline__ float gated_slope(bool gelu, float z) {
+  const float z2 = z * z;
+  const Sigmoids s = sigmoids(gelu ? z * __builtin_fmaf(kGelu1, z2, kGelu0) : z);
+  // an infinite slope of the argument meets a sigmoid that is 0 or 1
+  return __builtin_fmaf(z * s.s * s.s1, gelu ? fminf(__builtin_fmaf(3.0f * kGelu1, z2, kGelu0), 1e30f) : 1.0f, s.s);
+}
+template <typename IO, int V>
+__device__ __forceinline__ void again(Chans<IO, V>& v) {  // a value that the compiler does not know to be the same
+#pragma unroll
+  for (int i = 0; i < Chans<IO, V>::W; ++i) asm volatile("" : "+v"(v.w[i]));
 }
 
-// dlam from `parts` rows of partial sums, in their order.  sigmoid / softplus tends to 1 for lam -> -infinity.
+constexpr int kGatedBwdTile = MM_GATED_BLOCK;
+template <typename IO, int V, bool LAM>
+__global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, GatedChain ch, GatedGrads o) {
+  typedef GatedShape<IO, V, kGatedBwdTile> Shape;
+  constexpr int K = Shape::K, C = Shape::C, NG = Shape::runs;
+  __shared__ float sA[NG][C], sH[NG][C], sR[NG][C];
+  __shared__ Place place[kGatedBwdTile];
+  __shared__ int cuts[NG];  // of a run: 1 a sequence starts in it, 2 one ends
+  __shared__ uint32_t turn;
+  const int64_t d = a.d;
+  const uint32_t slices = static_cast<uint32_t>((d + C - 1) / C), tiles = gridDim.x / slices;
+  uint32_t id = blockIdx.x;
+  if (tiles > 1) {
+    if (threadIdx.x == 0) turn = gated_take(ch.tickets, tiles, slices);
+    lds_barrier();
+    id = __builtin_amdgcn_readfirstlane(turn);
+  }
+  const uint32_t n = id / slices, tile = tiles - 1 - n;
+  const int64_t c0 = static_cast<int64_t>(id % slices) * C, t0 = static_cast<int64_t>(tile) * kGatedBwdTile;
+  const int lane = threadIdx.x % Shape::lanes, run = threadIdx.x / Shape::lanes;
+  const int64_t c = c0 + lane * V;
+  const bool on = c < d, whole = t0 + kGatedBwdTile <= a.T;
+  const int64_t left = a.T - t0 - run * K;  // tokens of this run, if under K
+
+  const auto offset = [&](int64_t ts, uint32_t& step) {
+    step = static_cast<uint32_t>(ts * static_cast<int64_t>(sizeof(IO)));
+    return run * K * step + lane * V * static_cast<uint32_t>(sizeof(IO));
+  };
+  Chans<IO, V> rx[K], rr[K], rg[K], rz[K], ry[K];
+  const auto load = [&](const void* p, int64_t ts, Chans<IO, V>(&v)[K]) {
+    gmem<const IO>* base = sbase(static_cast<const IO*>(p) + t0 * ts + c0);
+    uint32_t step, off = offset(ts, step);
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        v[k] = load_chans<IO, V>(base, off);
+        off += step;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        v[k] = Chans<IO, V>{};
+        if (k < left) v[k] = load_chans<IO, V>(base, off);
+        off += step;
+      }
+    }
+  };
+  float kap[V];
+  if (on) {
+    load(a.r, a.r_ts, rr);
+    load(a.x, a.x_ts, rx);
+    if (a.g != nullptr) load(a.g, a.g_ts, rg);
+    load(o.dy, d, ry);
+    if (a.z != nullptr) load(a.z, a.z_ts, rz);
+#pragma unroll
+    for (int i = 0; i < V; ++i) kap[i] = LAM ? gated_kap(a.lam[c + i], a.c) : 0.0f;
+  }
+  const int seq = seq_of(a.cu, a.S, t0);
+  const int64_t lo = a.cu[seq];
+  int64_t hi = a.cu[seq + 1];
+  const bool cut = lo == t0 || hi <= t0 + kGatedBwdTile;  // sequences start or end in the tile
+  if (cut) {
+    gated_places<kGatedBwdTile>(a.cu, a.S, a.T, t0, place);
+    const int64_t last = whole ? t0 + kGatedBwdTile - 1 : a.T - 1;
+    hi = a.cu[seq_of(a.cu, a.S, last > 0 ? last : 0) + 1];  // the end of the tile's last sequence
+    lds_barrier();
+  }
+
+  // a, b and the runs; b makes room for the state before the token afterwards
+  float da[K][V], db[K][V], A[V], h[V], R[V];
+  int marks = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    A[i] = 1.0f;
+    h[i] = R[i] = 0.0f;
+  }
+  // dy act(z), and what the final state asks for
+  const auto adjoint = [&](int k, float(&dh)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) dh[i] = ry[k][i];
+    if (a.z != nullptr) {
+      if (a.gelu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) dh[i] *= gated_act(true, rz[k][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) dh[i] *= gated_act(false, rz[k][i]);
+      }
+    }
+    if (cut && o.dstate_out != nullptr) {
+      const Place p = place[run * K + k];
+      if (p.ends()) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) dh[i] += o.dstate_out[p.seq() * d + c + i];
+      }
+    }
+  };
+  if (on) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const Decay v = gated_decay<LAM>(rr[k][i], kap[i]);
+        da[k][i] = v.a;
+        db[k][i] = v.m * rx[k][i];
+      }
+      if (a.g != nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) db[k][i] *= sigmoid(rg[k][i]);
+      }
+      if (cut) {
+        const Place p = place[run * K + k];
+        if (p.starts()) {
+          marks |= 1;
+#pragma unroll
+          for (int i = 0; i < V; ++i) h[i] = a.state_in != nullptr ? a.state_in[p.seq() * d + c + i] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        A[i] *= da[k][i];
+        h[i] = __builtin_fmaf(da[k][i], h[i], db[k][i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      float dh[V];
+      adjoint(k, dh);
+      if (cut && place[run * K + k].ends()) {
+        marks |= 2;
+#pragma unroll
+        for (int i = 0; i < V; ++i) R[i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) R[i] = da[k][i] * (dh[i] + R[i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    sA[run][lane * V + i] = A[i];
+    sH[run][lane * V + i] = h[i];
+    sR[run][lane * V + i] = R[i];
+  }
+  if (lane == 0) cuts[run] = marks;  // the first channels of a slice are there
+  const int64_t cc = c0 + threadIdx.x;
+  const bool chain = threadIdx.x < C && cc < d, waits = hi > t0 + kGatedBwdTile;
+  Incoming in = gated_from(n, tiles - 1 - static_cast<int64_t>((hi > 0 ? hi - 1 : 0) / kGatedBwdTile));
+  bool there = !(chain && waits) || gated_look(in, ch, d, c0, threadIdx.x);
+  lds_barrier();
+  if (chain) {
+    const int j = threadIdx.x;
+    float At = 1.0f, Rt = 0.0f, from = 0.0f, state = a.T > 0 ? o.ckpt[tile * d + cc] : 0.0f;
+#pragma unroll
+    for (int g = NG - 1; g >= 0; --g) {
+      const float Ag = sA[g][j], Rg = sR[g][j];
+      const bool ends = cuts[g] & 2;
+      Rt = ends ? Rg : __builtin_fmaf(Ag, Rt, Rg);
+      At = ends || At < 0.0f ? -1.0f : At * Ag;
+    }
+    if (n + 1 < tiles) gated_publish(ch.pairs + n * d + cc, gated_pair(At, Rt));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {  // the state that each run starts from
+      const float hg = sH[g][j];
+      sH[g][j] = state;
+      state = cuts[g] & 1 ? hg : __builtin_fmaf(sA[g][j], state, hg);
+    }
+    if (waits) {
+      for (int look = 0; !there && look < kGatedLooks; ++look) {
+        __builtin_amdgcn_s_sleep(1);
+        there = gated_look(in, ch, d, c0, threadIdx.x);
+      }
+      from = gated_state(in);
+    }
+    if (n + 1 < tiles && n % kGatedGroup == kGatedGroup - 1)
+      gated_publish(ch.states + n / kGatedGroup * d + cc, __float_as_uint(At < 0.0f ? Rt : __builtin_fmaf(At, from, Rt)));
+#pragma unroll
+    for (int g = NG - 1; g >= 0; --g) {  // what each run's last token is handed
+      const float Rg = sR[g][j];
+      sR[g][j] = from;
+      from = cuts[g] & 2 ? Rg : __builtin_fmaf(sA[g][j], from, Rg);
+    }
+  }
+  lds_barrier();
+  if (o.dstate_in != nullptr)
+    gated_empty(a.cu, a.S, o.dstate_out, o.dstate_in, d, c0, C, tile * (kGatedThreads / 64) + threadIdx.x / 64,
+                tiles * (kGatedThreads / 64));
+  float sum[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    h[i] = sH[run][lane * V + i];
+    R[i] = sR[run][lane * V + i];
+    sum[i] = 0.0f;
+  }
+  if (on) {
+    uint32_t step, off = offset(o.dz_ts, step);
+    gmem<IO>* base = sbase(static_cast<IO*>(o.dz) + t0 * o.dz_ts + c0);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      again(rr[k]);
+      again(rz[k]);
+      again(rg[k]);
+      again(ry[k]);
+      if (cut) {
+        const Place p = place[run * K + k];
+        if (p.starts()) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) h[i] = a.state_in != nullptr ? a.state_in[p.seq() * d + c + i] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float before = h[i];
+        h[i] = __builtin_fmaf(da[k][i], h[i], db[k][i]);
+        db[k][i] = before;
+      }
+      if (a.z != nullptr) {
+        float dz[V];
+        if (a.gelu) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) dz[i] = gated_slope(true, rz[k][i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) dz[i] = gated_slope(false, rz[k][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) dz[i] *= ry[k][i] * h[i];
+        if (whole || k < left) store_chans<IO, V>(base, off, dz);
+        off += step;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    uint32_t sx, sr, sg;
+    uint32_t ox = offset(o.dx_ts, sx) + K * sx, og = offset(o.dg_ts, sg) + K * sg, orr = offset(o.dr_ts, sr) + K * sr;
+    gmem<IO>* const bx = sbase(static_cast<IO*>(o.dx) + t0 * o.dx_ts + c0);
+    gmem<IO>* const br = sbase(static_cast<IO*>(o.dr) + t0 * o.dr_ts + c0);
+    gmem<IO>* const bg = sbase(static_cast<IO*>(o.dg) + t0 * o.dg_ts + c0);
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      again(rz[k]);
+      const Place p = cut ? place[run * K + k] : Place{0};
+      if (p.ends()) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) R[i] = 0.0f;
+      }
+      ox -= sx;
+      orr -= sr;
+      og -= sg;
+      const bool here = whole || k < left;
+      float G[V], u[V], dr[V], dx[V], dg[V];
+      adjoint(k, G);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        G[i] += R[i];
+        R[i] = da[k][i] * G[i];
+        u[i] = rx[k][i];
+        dx[i] = G[i];
+      }
+      if (a.g != nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const Sigmoids s = sigmoids(rg[k][i]);
+          u[i] *= s.s;
+          dx[i] *= s.s;
+          dg[i] = s.s1 * u[i] * G[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const Sigmoids s = sigmoids(rr[k][i]);
+        const float av = da[k][i], before = db[k][i];
+        float m;
+        if constexpr (LAM) {
+          const float l = -kap[i] * s.s, m2 = gated_m2(l, av);
+          const float rm = __builtin_amdgcn_rsqf(__builtin_elementwise_maximum(m2, 1.2e-38f)), L = l * kLn2;
+          m = m2 * rm;
+          const float e = R[i] * L * __builtin_fmaf(-u[i] * av, rm, before);
+          sum[i] += e;
+          dr[i] = e * s.s1;
+        } else {
+          m = s.s1;
+          dr[i] = G[i] * (before - u[i]) * s.s * s.s1;
+        }
+        dx[i] *= m;
+        dg[i] *= m;
+      }
+      if (here) {
+        store_chans<IO, V>(br, orr, dr);
+        store_chans<IO, V>(bx, ox, dx);
+        if (a.g != nullptr) store_chans<IO, V>(bg, og, dg);
+      }
+      if (p.starts() && o.dstate_in != nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o.dstate_in[p.seq() * d + c + i] = R[i];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if constexpr (LAM) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sA[run][lane * V + i] = sum[i];
+    lds_barrier();
+    if (chain && a.T > 0) {
+      float t = 0.0f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) t += sA[g][threadIdx.x];
+      o.part[tile * d + cc] = t;
+    }
+  }
+}
+
+// dlam from the tiles' sums.  sigmoid / softplus tends to 1 for lam -> -infinity.
 __global__ __launch_bounds__(256) void k_gated_dlam(const float* __restrict__ part, int64_t parts, int d,
                                                     const float* __restrict__ lam, float* __restrict__ dlam) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= d) return;
-  float v = 0.0f;
-  for (int64_t k = 0; k < parts; ++k) v += part[k * d + c];
+  const int c = blockIdx.x * kPartColumns + threadIdx.x % kPartColumns;
+  const float v = sum_parts(part, parts, d, c);
+  if (c >= d || threadIdx.x >= kPartColumns) return;
   const float l = lam[c];
   dlam[c] = v * (l < -20.0f ? 1.0f : sigmoid(l) / (l != l ? l : softplus(l)));
 }
@@ -566,6 +793,18 @@ GatedChain start_chain(int64_t tiles, int32_t d, void* ws, hipStream_t st) {
   const int64_t n = l.pairs + l.states;
   hipLaunchKernelGGL(k_gated_clear, dim3(static_cast<unsigned>(cdiv(n, 256))), dim3(256), 0, st, p, n, static_cast<uint32_t*>(ws));
   return GatedChain{p, p + l.pairs, static_cast<uint32_t*>(ws)};
+}
+// the backward's workspace: a chain (the forward's first, where the states are made again), the tiles' sums, those states
+struct BackwardLayout {
+  size_t part, ckpt, total;
+};
+BackwardLayout backward_layout(int64_t T, int32_t d, bool has_ckpt) {
+  const int64_t n = gated_blocks(T) * d;
+  BackwardLayout l;
+  l.part = std::max(chain_layout(gated_blocks(T), d).total, chain_layout(gated_tiles(T), d).total);
+  l.ckpt = l.part + align256(static_cast<size_t>(n) * 4);
+  l.total = l.ckpt + (has_ckpt ? 0 : align256(static_cast<size_t>(n) * 4));
+  return l;
 }
 // f(V as a type) for d channels: pairs of them where every thread's are all there or all missing
 template <typename IO, typename F>
@@ -668,7 +907,7 @@ int mamba_mixer_gated_decode(const void* x, const void* r, const void* g, const 
 
 size_t mamba_mixer_gated_backward_workspace_bytes(int64_t T, int32_t d, int32_t has_ckpt) {
   if (check_gated(1, T, d, 0.0f, MM_GATE_SILU, MM_IO_F32) != MM_OK) return 0;
-  return align256(static_cast<size_t>(T) * d * 4);
+  return backward_layout(T, d, has_ckpt != 0).total;
 }
 
 int mamba_mixer_gated_backward(const void* x, const void* r, const void* g, const void* z, const float* lam,
@@ -698,20 +937,35 @@ int mamba_mixer_gated_backward(const void* x, const void* r, const void* g, cons
   rc = check_workspace(workspace, workspace_bytes, mamba_mixer_gated_backward_workspace_bytes(T, d, ckpt != nullptr));
   if (rc != MM_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  float* before = static_cast<float*>(workspace);
-  const GatedGrads o{dy, dstate_out, before, dx, dr, dg, dz, dx_stride, dr_stride, dg_stride, dz_stride, dstate_in};
+  const BackwardLayout l = backward_layout(T, d, ckpt != nullptr);
+  char* ws = static_cast<char*>(workspace);
+  float* part = reinterpret_cast<float*>(ws + l.part);
+  float* states = reinterpret_cast<float*>(ws + l.ckpt);
+  const GatedGrads o{dy, dstate_out, ckpt != nullptr ? ckpt : states, dx, dr, dg, dz, dx_stride, dr_stride, dg_stride, dz_stride,
+                     dstate_in, part};
   return by_io(io_dtype, [&](auto io) {
     using IO = decltype(io);
-    const dim3 grid(static_cast<unsigned>(cdiv(ns, 256)));
-    if (S > 0) {
-      hipLaunchKernelGGL((k_gated_seq<IO>), grid, dim3(256), 0, st, a, static_cast<float*>(nullptr), static_cast<IO*>(nullptr),
-                         static_cast<float*>(nullptr), before);
-      hipLaunchKernelGGL((k_gated_bwd<IO>), grid, dim3(256), 0, st, a, o);
-    }
-    if (lam != nullptr)
-      hipLaunchKernelGGL(k_gated_dlam, dim3(static_cast<unsigned>(cdiv(d, 256))), dim3(256), 0, st, before, T, d, lam,
-                         dlam);
-    return launched();
+    return by_channels<IO>(d, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      const int64_t tiles = gated_blocks(T);
+      const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, tiles) * cdiv(d, GatedShape<IO, V, kGatedBwdTile>::C)));
+      if (S > 0 && ckpt == nullptr && T > 0) {
+        const dim3 forward(static_cast<unsigned>(gated_tiles(T) * cdiv(d, GatedShape<IO, V, kGatedTile>::C)));
+        const GatedChain ch = start_chain(gated_tiles(T), d, workspace, st);
+        if (lam != nullptr)
+          hipLaunchKernelGGL((k_gated<IO, V, true, false>), forward, dim3(kGatedThreads), 0, st, a, ch, nullptr, static_cast<IO*>(nullptr), states);
+        else
+          hipLaunchKernelGGL((k_gated<IO, V, false, false>), forward, dim3(kGatedThreads), 0, st, a, ch, nullptr, static_cast<IO*>(nullptr), states);
+      }
+      if (S > 0) {
+        const GatedChain ch = start_chain(tiles, d, workspace, st);
+        if (lam != nullptr) hipLaunchKernelGGL((k_gated_bwd<IO, V, true>), grid, dim3(kGatedThreads), 0, st, a, ch, o);
+        else hipLaunchKernelGGL((k_gated_bwd<IO, V, false>), grid, dim3(kGatedThreads), 0, st, a, ch, o);
+      }
+      if (lam != nullptr)
+        hipLaunchKernelGGL(k_gated_dlam, dim3(static_cast<unsigned>(cdiv(d, kPartColumns))), dim3(256), 0, st, part, tiles, d, lam, dlam);
+      return launched();
+    });
   });
 }
 
