@@ -428,12 +428,16 @@ struct GatedGrads {
   int64_t dx_ts, dr_ts, dg_ts, dz_ts;
   float *dstate_in, *part;  // part: [tiles, d], sums of e over a tile's tokens
 };
-// the slope of the output gate
-__device__ __forceinline__ float gated_slope(bool gelu, float z) {
+// the output gate and its slope
+struct Act {
+  float act, slope;
+};
+__device__ __forceinline__ Act gated_act_slope(bool gelu, float z) {
   const float z2 = z * z;
   const Sigmoids s = sigmoids(gelu ? z * __builtin_fmaf(kGelu1, z2, kGelu0) : z);
+  const float act = z * s.s;
   // an infinite slope of the argument meets a sigmoid that is 0 or 1
-  return __builtin_fmaf(z * s.s * s.s1, gelu ? fminf(__builtin_fmaf(3.0f * kGelu1, z2, kGelu0), 1e30f) : 1.0f, s.s);
+  return {act, __builtin_fmaf(act * s.s1, gelu ? fminf(__builtin_fmaf(3.0f * kGelu1, z2, kGelu0), 1e30f) : 1.0f, s.s)};
 }
 template <typename IO, int V>
 __device__ __forceinline__ void again(Chans<IO, V>& v) {  // a value that the compiler does not know to be the same
@@ -517,19 +521,8 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
     A[i] = 1.0f;
     h[i] = R[i] = 0.0f;
   }
-  // dy act(z), and what the final state asks for
-  const auto adjoint = [&](int k, float(&dh)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) dh[i] = ry[k][i];
-    if (a.z != nullptr) {
-      if (a.gelu) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) dh[i] *= gated_act(true, rz[k][i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) dh[i] *= gated_act(false, rz[k][i]);
-      }
-    }
+  // what the final state of a sequence that ends at token k asks for
+  const auto final_adjoint = [&](int k, float(&dh)[V]) {
     if (cut && o.dstate_out != nullptr) {
       const Place p = place[run * K + k];
       if (p.ends()) {
@@ -569,7 +562,18 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
       float dh[V];
-      adjoint(k, dh);
+#pragma unroll
+      for (int i = 0; i < V; ++i) dh[i] = ry[k][i];
+      if (a.z != nullptr) {
+        if (a.gelu) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) dh[i] *= gated_act(true, rz[k][i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) dh[i] *= gated_act(false, rz[k][i]);
+        }
+      }
+      final_adjoint(k, dh);
       if (cut && place[run * K + k].ends()) {
         marks |= 2;
 #pragma unroll
@@ -636,6 +640,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
     R[i] = sR[run][lane * V + i];
     sum[i] = 0.0f;
   }
+  float dh[K][V];  // in the place of dy and z
   if (on) {
     uint32_t step, off = offset(o.dz_ts, step);
     gmem<IO>* base = sbase(static_cast<IO*>(o.dz) + t0 * o.dz_ts + c0);
@@ -658,20 +663,24 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
         h[i] = __builtin_fmaf(da[k][i], h[i], db[k][i]);
         db[k][i] = before;
       }
+#pragma unroll
+      for (int i = 0; i < V; ++i) dh[k][i] = ry[k][i];
       if (a.z != nullptr) {
         float dz[V];
-        if (a.gelu) {
+        const auto gate = [&](bool gelu) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) dz[i] = gated_slope(true, rz[k][i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) dz[i] = gated_slope(false, rz[k][i]);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) dz[i] *= ry[k][i] * h[i];
+          for (int i = 0; i < V; ++i) {
+            const Act v = gated_act_slope(gelu, rz[k][i]);
+            dz[i] = v.slope * ry[k][i] * h[i];
+            dh[k][i] *= v.act;
+          }
+        };
+        if (a.gelu) gate(true);
+        else gate(false);
         if (whole || k < left) store_chans<IO, V>(base, off, dz);
         off += step;
       }
+      final_adjoint(k, dh[k]);
       __builtin_amdgcn_sched_barrier(0);
     }
     uint32_t sx, sr, sg;
@@ -681,7 +690,6 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
     gmem<IO>* const bg = sbase(static_cast<IO*>(o.dg) + t0 * o.dg_ts + c0);
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
-      again(rz[k]);
       const Place p = cut ? place[run * K + k] : Place{0};
       if (p.ends()) {
 #pragma unroll
@@ -692,10 +700,9 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
       og -= sg;
       const bool here = whole || k < left;
       float G[V], u[V], dr[V], dx[V], dg[V];
-      adjoint(k, G);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        G[i] += R[i];
+        G[i] = dh[k][i] + R[i];
         R[i] = da[k][i] * G[i];
         u[i] = rx[k][i];
         dx[i] = G[i];
