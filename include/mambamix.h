@@ -562,8 +562,8 @@ size_t mamba_mixer_residual_norm_backward_workspace_bytes(int64_t rows, int32_t 
  *                                 A sequence shorter than W - 1 keeps the end of its initial state.
  *   y          [T, d]       io    contiguous
  * y and state_out may overlap no input but state_out == state_in.  Limits: 2 <= W <= MM_CONV_MAX_W (else
- * MM_ERR_UNSUPPORTED); a launch has less than 2^32 threads (else MM_ERR_DIM): ceil(T / 16) d < 2^31 and S d < 2^31.
- * T == 0 copies the states; d == 0 is a no-op.
+ * MM_ERR_UNSUPPORTED); S d < 2^31, and a launch has less than 2^24 workgroups (else MM_ERR_DIM): about T d / 65536 of
+ * 256 tokens by up to 256 channels, and S d / 256.  T == 0 copies the states; d == 0 is a no-op.
  */
 #define MM_CONV_MAX_W 4
 int mamba_mixer_conv_prefill(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,

@@ -1,8 +1,20 @@
 // The causal depthwise convolution by itself: kernels, argument checks and entry points.
+//   u[p] = bias + sum_k w_k X(p - W + 1 + k),  y = u sigmoid(u) or u;  X(q < 0): the state's inputs
+//   dX(q) = sum_k w_k du(q + W - 1 - k) + what the final state asks for,  dw_k = sum_p du(p) X(p - W + 1 + k)
+// Bound by memory.  A wave walks L tokens of 64 V channels (512 bytes of bfloat16 a row: narrower rows cost a fifth of the
+// bandwidth), its window, weights and the weights' gradients in registers: an input is read once, but for the W - 1 tokens
+// around a walk.  kStep tokens are loaded at a time, the next ones while these are used; a step in which sequences start or
+// end goes token by token and reads its rows again.
+#include <algorithm>
+#include <type_traits>
+
 #include "layer/common.h"
 
 namespace mm {
 namespace {
+
+constexpr int kConvWaves = 4, kConvThreads = kConvWaves * 64, kStep = 8;
+constexpr int64_t kConvWalks = 4096;  // waves that are wanted: L is at most 64 tokens, less where there would be fewer
 
 struct ConvArgs {
   const void* x;
@@ -10,137 +22,408 @@ struct ConvArgs {
   const int32_t* cu;
   const float* state_in;
   int64_t x_ts, T;
-  int S, d, W, silu;
+  int S, d, L, silu;
 };
 
-// X(q) of sequence s (its first token g0, channel c): a token's raw input or the state's
+// ---------------------------------------------------------------- a thread's channel, one by one: states
 template <typename IO>
-__device__ float conv_raw(const ConvArgs& a, int s, int64_t g0, int64_t q, int c) {
+__device__ __forceinline__ float conv_raw(const ConvArgs& a, int W, int s, int64_t g0, int64_t q, int c) {
   if (q >= 0) return ld_io(static_cast<const IO*>(a.x), (g0 + q) * a.x_ts + c);
-  return a.state_in != nullptr ? a.state_in[(static_cast<int64_t>(s) * a.d + c) * (a.W - 1) + a.W - 1 + q] : 0.0f;
+  return a.state_in != nullptr ? a.state_in[(static_cast<int64_t>(s) * a.d + c) * (W - 1) + W - 1 + q] : 0.0f;
 }
-template <typename IO>
-__device__ float conv_u(const ConvArgs& a, int s, int64_t g0, int64_t p, int c) {
-  float u = a.bias != nullptr ? a.bias[c] : 0.0f;
-  for (int k = 0; k < a.W; ++k) u = __builtin_fmaf(a.w[c * a.W + k], conv_raw<IO>(a, s, g0, p - a.W + 1 + k, c), u);
-  return u;
-}
-
-template <typename IO>
-__global__ __launch_bounds__(256) void k_conv(ConvArgs a, IO* __restrict__ y) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t t0 = i / a.d * 16;
-  const int c = static_cast<int>(i % a.d);
-  for (int64_t t = t0; t < t0 + 16 && t < a.T; ++t) {
-    const int s = seq_of(a.cu, a.S, t);
-    const int64_t g0 = a.cu[s];
-    const float u = conv_u<IO>(a, s, g0, t - g0, c);
-    st_io(y, t * a.d + c, a.silu ? u * sigmoid(u) : u);
-  }
-}
-
-// final states, a thread for each (sequence, channel); state_out may be state_in
-template <typename IO>
-__global__ __launch_bounds__(256) void k_conv_state(ConvArgs a, float* state_out) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.S) * a.d) return;
-  const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
-  const int64_t g0 = a.cu[s], n = a.cu[s + 1] - g0;
-  float v[MM_CONV_MAX_W - 1];
-  for (int k = 0; k < a.W - 1; ++k) v[k] = conv_raw<IO>(a, s, g0, n - a.W + 1 + k, c);
-  for (int k = 0; k < a.W - 1; ++k) state_out[i * (a.W - 1) + k] = v[k];
-}
-
-template <typename IO>
-__global__ __launch_bounds__(256) void k_conv_decode(ConvArgs a, float* state_out, IO* __restrict__ y) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.S) * a.d) return;
-  const int64_t s = i / a.d;
-  const int c = static_cast<int>(i % a.d);
-  float u = a.bias != nullptr ? a.bias[c] : 0.0f, v[MM_CONV_MAX_W];
-  for (int k = 0; k < a.W - 1; ++k) v[k] = a.state_in != nullptr ? a.state_in[i * (a.W - 1) + k] : 0.0f;
-  v[a.W - 1] = ld_io(static_cast<const IO*>(a.x), s * a.x_ts + c);
-  for (int k = 0; k < a.W; ++k) u = __builtin_fmaf(a.w[c * a.W + k], v[k], u);
-  for (int k = 0; k < a.W - 1; ++k) state_out[i * (a.W - 1) + k] = v[k + 1];
-  st_io(y, i, a.silu ? u * sigmoid(u) : u);
-}
-
-// dL/du at place p of sequence s
-template <typename IO>
-__device__ float conv_du(const ConvArgs& a, const IO* dy, int s, int64_t g0, int64_t p, int c) {
-  const float g = ld_io(dy, (g0 + p) * a.d + c);
-  if (!a.silu) return g;
-  const float u = conv_u<IO>(a, s, g0, p, c);
+__device__ __forceinline__ float conv_slope(float u, float g, bool silu) {
+  if (!silu) return g;
   const Sigmoids v = sigmoids(u);
   return g * v.s * __builtin_fmaf(u, v.s1, 1.0f);
 }
-
-// dX(q) = sum_k w_k du(q + W - 1 - k), and what the final state asks for
-template <typename IO>
-__device__ float conv_dx(const ConvArgs& a, const IO* dy, const float* dstate_out, int s, int64_t g0, int64_t n, int64_t q, int c) {
-  float v = 0.0f;
-  for (int k = 0; k < a.W; ++k) {
-    const int64_t p = q + a.W - 1 - k;
-    if (p >= 0 && p < n) v = __builtin_fmaf(a.w[c * a.W + k], conv_du(a, dy, s, g0, p, c), v);
-  }
-  const int64_t j = q - (n - a.W + 1);
-  if (dstate_out != nullptr && j >= 0) v += dstate_out[(static_cast<int64_t>(s) * a.d + c) * (a.W - 1) + j];
-  return v;
-}
-
-template <typename IO>
-__global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, const IO* __restrict__ dy, const float* __restrict__ dstate_out,
-                                                  IO* __restrict__ dx, int64_t dx_ts, float* __restrict__ part) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t t0 = i / a.d * 16;
-  const int c = static_cast<int>(i % a.d);
-  if (t0 >= a.T) return;
-  float dw[MM_CONV_MAX_W] = {}, db = 0.0f;
-  for (int64_t t = t0; t < t0 + 16 && t < a.T; ++t) {
-    const int s = seq_of(a.cu, a.S, t);
-    const int64_t g0 = a.cu[s], n = a.cu[s + 1] - g0;
-    st_io(dx, t * dx_ts + c, conv_dx(a, dy, dstate_out, s, g0, n, t - g0, c));
-    const float g = conv_du(a, dy, s, g0, t - g0, c);
-    db += g;
-    for (int k = 0; k < a.W; ++k) dw[k] = __builtin_fmaf(g, conv_raw<IO>(a, s, g0, t - g0 - a.W + 1 + k, c), dw[k]);
-  }
-  float* p = part + t0 / 16 * a.d * (a.W + 1) + c;
-  for (int k = 0; k < a.W; ++k) p[static_cast<int64_t>(k) * a.d] = dw[k];
-  p[static_cast<int64_t>(a.W) * a.d] = db;
-}
-
-template <typename IO>
-__global__ __launch_bounds__(256) void k_conv_dstate(ConvArgs a, const IO* __restrict__ dy, const float* __restrict__ dstate_out,
-                                                     float* __restrict__ dstate_in) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+// the final state of (sequence, channel) i; state_out may be state_in
+template <typename IO, int W>
+__device__ __forceinline__ void conv_state(const ConvArgs& a, float* state_out, int64_t i) {
   if (i >= static_cast<int64_t>(a.S) * a.d) return;
   const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
   const int64_t g0 = a.cu[s], n = a.cu[s + 1] - g0;
-  for (int k = 0; k < a.W - 1; ++k)
-    dstate_in[i * (a.W - 1) + k] = conv_dx(a, dy, dstate_out, s, g0, n, k - a.W + 1, c);
+  float v[W - 1];
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) v[k] = conv_raw<IO>(a, W, s, g0, n - W + 1 + k, c);
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) state_out[i * (W - 1) + k] = v[k];
+}
+// the gradient of the initial state of (sequence, channel) i, from its first W - 1 tokens
+template <typename IO, int W>
+__device__ __forceinline__ void conv_dstate(const ConvArgs& a, const IO* dy, const float* dstate_out, float* dstate_in, int64_t i) {
+  if (i >= static_cast<int64_t>(a.S) * a.d) return;
+  const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
+  const int64_t g0 = a.cu[s], n = a.cu[s + 1] - g0;
+  const float b = a.bias != nullptr ? a.bias[c] : 0.0f;
+  float w[W], du[W - 1];
+#pragma unroll
+  for (int k = 0; k < W; ++k) w[k] = a.w[static_cast<int64_t>(c) * W + k];
+#pragma unroll
+  for (int p = 0; p < W - 1; ++p) {
+    du[p] = 0.0f;
+    if (p < n) {
+      float u = b;
+#pragma unroll
+      for (int k = 0; k < W; ++k) u = __builtin_fmaf(w[k], conv_raw<IO>(a, W, s, g0, p - W + 1 + k, c), u);
+      du[p] = conv_slope(u, ld_io(dy, (g0 + p) * a.d + c), a.silu);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {  // X(q), q = j - W + 1; a sequence shorter than that leaves it in its final state
+    const int64_t f = j - n;
+    float v = dstate_out != nullptr && f >= 0 ? dstate_out[i * (W - 1) + f] : 0.0f;
+#pragma unroll
+    for (int p = 0; p <= j; ++p) v = __builtin_fmaf(w[j - p], du[p], v);
+    dstate_in[i * (W - 1) + j] = v;
+  }
 }
 
-// the weights' gradients from `parts` rows of [W + 1, d] partial sums, in their order
+// ---------------------------------------------------------------- walks
+// what a wave's walk knows of its tokens and channels
+template <typename IO, int V, int W>
+struct ConvWalk {
+  const ConvArgs& a;
+  int64_t c, c0, t0, t1;
+  uint32_t off;      // of this lane's channels in a row
+  int s;             // the sequence of the present token,
+  int64_t lo, hi;    // its first token and the one behind its last
+  float w[W][V], b[V], win[W - 1][V];
+
+  __device__ __forceinline__ ConvWalk(const ConvArgs& a, int64_t slice, int64_t walk) : a(a) {
+    const int lane = threadIdx.x & 63;
+    c0 = slice * 64 * V;
+    c = c0 + lane * V;
+    const bool on = c < a.d;
+    off = on ? lane * V * static_cast<uint32_t>(sizeof(IO)) : 0;  // lanes without channels read the first ones
+    t0 = walk * a.L;
+    t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
+    s = seq_of(a.cu, a.S, t0);
+    lo = a.cu[s];
+    hi = a.cu[s + 1];
+    const int64_t cw = on ? c : c0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      b[i] = a.bias != nullptr ? a.bias[cw + i] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k][i] = a.w[(cw + i) * W + k];
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int64_t q = t0 - W + 1 + j;
+      if (q >= lo) set(j, row(q));
+      else from_state(j, static_cast<int>(q - lo + W - 1));
+    }
+  }
+  __device__ __forceinline__ gmem<const IO>* base(int64_t t) const { return sbase(static_cast<const IO*>(a.x) + t * a.x_ts + c0); }
+  __device__ __forceinline__ Chans<IO, V> row(int64_t t) const { return load_chans<IO, V>(base(t), off); }
+  __device__ __forceinline__ void set(int j, const Chans<IO, V>& r) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) win[j][i] = r[i];
+  }
+  __device__ __forceinline__ void from_state(int j, int k) {
+    const int64_t cs = c < a.d ? c : c0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) win[j][i] = a.state_in != nullptr ? a.state_in[(s * static_cast<int64_t>(a.d) + cs + i) * (W - 1) + k] : 0.0f;
+  }
+  // token t, which may be the first of another sequence
+  __device__ __forceinline__ void enter(int64_t t) {
+    if (t < hi) return;
+    while (t >= hi) {
+      ++s;
+      lo = hi;
+      hi = a.cu[s + 1];
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) from_state(j, j);
+  }
+  __device__ __forceinline__ void pre(const Chans<IO, V>& r, float (&u)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      u[i] = b[i];
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) u[i] = __builtin_fmaf(w[k][i], win[k][i], u[i]);
+      u[i] = __builtin_fmaf(w[W - 1][i], r[i], u[i]);
+    }
+  }
+  __device__ __forceinline__ void shift(const Chans<IO, V>& r) {
+#pragma unroll
+    for (int j = 0; j < W - 2; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
+    set(W - 2, r);
+  }
+};
+
+// blocks of `walks` (kConvWaves to a block, slice by slice), then those of the states where state_out is given
+template <typename IO, int V, int W>
+__global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, int64_t blocks, uint32_t slices, IO* __restrict__ y, float* state_out) {
+  if (blockIdx.x >= blocks) {
+    conv_state<IO, W>(a, state_out, (blockIdx.x - blocks) * kConvThreads + threadIdx.x);
+    return;
+  }
+  const int64_t walk = static_cast<int64_t>(blockIdx.x / slices) * kConvWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  if (walk * a.L >= a.T) return;
+  ConvWalk<IO, V, W> x(a, blockIdx.x % slices, walk);
+  const bool on = x.c < a.d;
+  const auto out = [&](int64_t t, const Chans<IO, V>& r) {
+    float u[V];
+    x.pre(r, u);
+    if (a.silu) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[i] *= sigmoid(u[i]);
+    }
+    if (on) store_chans<IO, V>(sbase(y + t * a.d + x.c0), x.off, u);
+    x.shift(r);
+  };
+  Chans<IO, V> r[kStep];
+  const auto load = [&](int64_t t) {
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) r[k] = x.row(t + k);
+  };
+  int64_t t = x.t0;
+  if (t + kStep <= x.t1) load(t);
+  for (; t + kStep <= x.t1; t += kStep) {
+    if (t + kStep <= x.hi) {
+      Chans<IO, V> now[kStep];
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) now[k] = r[k];
+      // the last step reads its own rows again, which nothing uses
+      load(t + 2 * kStep <= x.t1 ? t + kStep : t);
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) out(t + k, now[k]);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kStep; ++k) {
+        x.enter(t + k);
+        out(t + k, x.row(t + k));
+      }
+      load(t + 2 * kStep <= x.t1 ? t + kStep : t);
+    }
+  }
+#pragma unroll 1
+  for (; t < x.t1; ++t) {
+    x.enter(t);
+    out(t, x.row(t));
+  }
+}
+
+// One token a row, a thread for V channels of it.
+template <typename IO, int V, int W>
+__global__ __launch_bounds__(256) void k_conv_decode(ConvArgs a, float* state_out, IO* __restrict__ y) {
+  const int64_t n = static_cast<int64_t>(a.S) * a.d, i0 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
+  if (i0 >= n) return;
+  const int64_t s = i0 / a.d, c = i0 - s * a.d;
+  const Chans<IO, V> r = load_chans<IO, V>(global(static_cast<const IO*>(a.x) + s * a.x_ts + c), 0);
+  float v[V][W - 1], w[V][W], u[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    u[i] = a.bias != nullptr ? a.bias[c + i] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) v[i][k] = a.state_in != nullptr ? a.state_in[(i0 + i) * (W - 1) + k] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[i][k] = a.w[(c + i) * W + k];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) u[i] = __builtin_fmaf(w[i][k], v[i][k], u[i]);
+    u[i] = __builtin_fmaf(w[i][W - 1], r[i], u[i]);
+    if (a.silu) u[i] *= sigmoid(u[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) state_out[(i0 + i) * (W - 1) + k] = k < W - 2 ? v[i][k + 1] : r[i];
+  store_chans<IO, V>(global(y + i0), 0, u);
+}
+
+// A walk computes du for its own tokens and the W - 1 behind them; pend holds the gradients of the last W tokens as they gather.
+// part: [blocks / slices][W + 1][d], a block's sums of dw and dbias.
+template <typename IO, int V, int W>
+__global__ __launch_bounds__(kConvThreads) void k_conv_bwd(ConvArgs a, int64_t blocks, uint32_t slices, const IO* __restrict__ dy,
+                                                           const float* __restrict__ dstate_out, IO* __restrict__ dx, int64_t dx_ts,
+                                                           float* __restrict__ part, float* __restrict__ dstate_in) {
+  if (blockIdx.x >= blocks) {
+    conv_dstate<IO, W>(a, dy, dstate_out, dstate_in, (blockIdx.x - blocks) * kConvThreads + threadIdx.x);
+    return;
+  }
+  __shared__ float sums[kConvWaves][W + 1][64 * V];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
+  const int64_t slice = blockIdx.x % slices, group = blockIdx.x / slices, walk = group * kConvWaves + wave;
+  float dw[W][V], db[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    db[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) dw[k][i] = 0.0f;
+  }
+  if (walk * a.L < a.T) {
+    ConvWalk<IO, V, W> x(a, slice, walk);
+    const bool on = x.c < a.d;
+    float pend[W][V];  // tokens p - W + 1 .. p
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) pend[j][i] = 0.0f;
+    const auto slope = [&](const Chans<IO, V>& r, const Chans<IO, V>& g, float(&du)[V]) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) du[i] = g[i];
+      if (a.silu) {
+        float u[V];
+        x.pre(r, u);
+#pragma unroll
+        for (int i = 0; i < V; ++i) du[i] = conv_slope(u[i], du[i], true);
+      }
+    };
+    const auto weights = [&](const Chans<IO, V>& r, const float(&du)[V]) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        db[i] += du[i];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) dw[k][i] = __builtin_fmaf(du[i], x.win[k][i], dw[k][i]);
+        dw[W - 1][i] = __builtin_fmaf(du[i], r[i], dw[W - 1][i]);
+      }
+    };
+    // token q = p - W + 1 is through
+    const auto leave = [&](int64_t p) {
+      const int64_t q = p - W + 1;
+      if (q >= x.t0 && on) store_chans<IO, V>(sbase(dx + q * dx_ts + x.c0), x.off, pend[0]);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) pend[j][i] = pend[j + 1][i];
+#pragma unroll
+      for (int i = 0; i < V; ++i) pend[W - 1][i] = 0.0f;
+    };
+    const auto grads = [&](int64_t t) { return load_chans<IO, V>(sbase(dy + t * a.d + x.c0), x.off); };
+    // token p, wherever sequences start and end; behind the last token the others leave
+    const auto slow = [&](int64_t p) {
+      if (p < a.T) {
+        x.enter(p);
+        const Chans<IO, V> r = x.row(p);
+        float du[V];
+        slope(r, grads(p), du);
+        if (p < x.t1) weights(r, du);
+        const int64_t f = p - (x.hi - W + 1);  // its place in the final state
+        if (dstate_out != nullptr && f >= 0) {
+          const int64_t cs = on ? x.c : x.c0;
+#pragma unroll
+          for (int i = 0; i < V; ++i) pend[W - 1][i] += dstate_out[(x.s * static_cast<int64_t>(a.d) + cs + i) * (W - 1) + f];
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          if (p - j >= x.lo) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) pend[W - 1 - j][i] = __builtin_fmaf(x.w[W - 1 - j][i], du[i], pend[W - 1 - j][i]);
+          }
+        x.shift(r);
+      }
+      leave(p);
+    };
+    Chans<IO, V> r[kStep], g[kStep];
+    const auto load = [&](int64_t t) {
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        r[k] = x.row(t + k);
+        g[k] = grads(t + k);
+      }
+    };
+    int64_t t = x.t0;
+    if (t + kStep <= x.t1) load(t);
+    for (; t + kStep <= x.t1; t += kStep) {
+      const int64_t next = t + 2 * kStep <= x.t1 ? t + kStep : t;
+      if (t - W + 1 >= x.lo && t + kStep + W - 1 <= x.hi) {
+        Chans<IO, V> now[kStep], gn[kStep];
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          now[k] = r[k];
+          gn[k] = g[k];
+        }
+        load(next);
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          float du[V];
+          slope(now[k], gn[k], du);
+          weights(now[k], du);
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) pend[j][i] = __builtin_fmaf(x.w[j][i], du[i], pend[j][i]);
+          x.shift(now[k]);
+          leave(t + k);
+        }
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < kStep; ++k) slow(t + k);
+        load(next);
+      }
+    }
+#pragma unroll 1
+    for (; t < x.t1 + W - 1; ++t) slow(t);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) sums[wave][k][lane * V + i] = dw[k][i];
+    sums[wave][W][lane * V + i] = db[i];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < (W + 1) * 64 * V; i += kConvThreads) {
+    const int k = i / (64 * V), j = i % (64 * V);
+    const int64_t c = slice * 64 * V + j;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kConvWaves; ++q) v += sums[q][k][j];
+    if (c < a.d) part[(group * (W + 1) + k) * a.d + c] = v;
+  }
+}
+
+// the weights' gradients from `parts` rows of [W + 1, d] partial sums
 __global__ __launch_bounds__(256) void k_conv_parts(const float* __restrict__ part, int64_t parts, int d, int W,
                                                     float* __restrict__ dw, float* __restrict__ db) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t n = static_cast<int64_t>(W + 1) * d;
-  if (i >= n) return;
-  float v = 0.0f;
-  for (int64_t k = 0; k < parts; ++k) v += part[k * n + i];
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kPartColumns + threadIdx.x % kPartColumns, n = static_cast<int64_t>(W + 1) * d;
+  const float v = sum_parts(part, parts, n, i);
+  if (i >= n || threadIdx.x >= kPartColumns) return;
   const int64_t k = i / d, c = i % d;
   if (k < W) dw[c * W + k] = v;
   else if (db != nullptr) db[c] = v;
 }
 
+// ---------------------------------------------------------------- host
+int conv_channels(int32_t d) { return d % 4 == 0 ? 4 : d % 2 == 0 ? 2 : 1; }  // of a lane: all there or none
+int64_t conv_slices(int32_t d) { return cdiv(d, 64 * conv_channels(d)); }
+// tokens of a walk: kConvWalks of them where there are enough, in steps of kStep
+int64_t conv_tokens(int64_t T, int32_t d) {
+  const int64_t L = T * conv_slices(d) / kConvWalks / kStep * kStep;
+  return std::min<int64_t>(64, std::max<int64_t>(kStep, L));
+}
+int64_t conv_groups(int64_t T, int32_t d) { return cdiv(T, conv_tokens(T, d) * kConvWaves); }
+
 int check_conv(int64_t S, int64_t T, int32_t d, int32_t W, int32_t io, int64_t x_ts) {
   const int rc = check_tokens(S, T, d, io);
   if (rc != MM_OK) return rc;
   if (W < 2 || W > MM_CONV_MAX_W) return MM_ERR_UNSUPPORTED;
-  if (cdiv(T, 16) * d >= (int64_t{1} << 31)) return MM_ERR_DIM;
-  return x_ts < d ? MM_ERR_DIM : MM_OK;
+  if (x_ts < d) return MM_ERR_DIM;
+  if (d == 0) return MM_OK;
+  const int64_t blocks = conv_groups(T, d) * conv_slices(d) + cdiv(S * d, kConvThreads);
+  return blocks * kConvThreads > kMaxThreads || cdiv(int64_t{W + 1} * d, kPartColumns) * 256 > kMaxThreads ? MM_ERR_DIM : MM_OK;
 }
-unsigned blocks(int64_t threads) { return static_cast<unsigned>(cdiv(threads, 256)); }
+// f(IO, channels of a lane, taps)
+template <typename F>
+int by_conv(int32_t io, int32_t d, int32_t W, F f) {
+  return by_io(io, [&](auto t) {
+    const auto taps = [&](auto v) {
+      if (W == 2) return f(t, v, std::integral_constant<int, 2>{});
+      if (W == 3) return f(t, v, std::integral_constant<int, 3>{});
+      return f(t, v, std::integral_constant<int, 4>{});
+    };
+    switch (conv_channels(d)) {
+      case 4: return taps(std::integral_constant<int, 4>{});
+      case 2: return taps(std::integral_constant<int, 2>{});
+      default: return taps(std::integral_constant<int, 1>{});
+    }
+  });
+}
 }  // namespace
 }  // namespace mm
 
@@ -161,13 +444,23 @@ int mamba_mixer_conv_prefill(const void* x, const float* weight, const float* bi
                   {flat(state_out, ns, 4), flat(y, T * d, es)}, {{0, 4}});
   if (rc != MM_OK) return rc;
   if (S == 0) return MM_OK;
-  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, W, silu};
+  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d)), silu != 0};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return by_io(io_dtype, [&](auto io) {
+  return by_conv(io_dtype, d, W, [&](auto io, auto v, auto taps) {
     using IO = decltype(io);
-    if (T > 0)
-      hipLaunchKernelGGL((k_conv<IO>), dim3(blocks(cdiv(T, 16) * d)), dim3(256), 0, st, a, static_cast<IO*>(y));
-    hipLaunchKernelGGL((k_conv_state<IO>), dim3(blocks(static_cast<int64_t>(S) * d)), dim3(256), 0, st, a, state_out);
+    constexpr int V = decltype(v)::value, K = decltype(taps)::value;
+    const uint32_t slices = static_cast<uint32_t>(conv_slices(d));
+    const int64_t blocks = T > 0 ? conv_groups(T, d) * slices : 0, states = cdiv(static_cast<int64_t>(S) * d, kConvThreads);
+    const auto launch = [&](int64_t walks, int64_t rest) {
+      hipLaunchKernelGGL((k_conv<IO, V, K>), dim3(static_cast<unsigned>(walks + rest)), dim3(kConvThreads), 0, st, a, walks, slices,
+                         static_cast<IO*>(y), state_out);
+    };
+    if (state_out == state_in && blocks > 0) {  // in place: the initial states are read until the walks are through
+      launch(blocks, 0);
+      launch(0, states);
+    } else {
+      launch(blocks, states);
+    }
     return launched();
   });
 }
@@ -184,18 +477,19 @@ int mamba_mixer_conv_decode(const void* x, const float* weight, const float* bia
                    flat(state_in, n * (W - 1), 4, true)},
                   {flat(state_out, n * (W - 1), 4), flat(y, n, es)}, {{0, 3}});
   if (rc != MM_OK) return rc;
-  const ConvArgs a{x, weight, bias, nullptr, state_in, x_stride, Bs, Bs, d, W, silu};
-  return by_io(io_dtype, [&](auto io) {
+  const ConvArgs a{x, weight, bias, nullptr, state_in, x_stride, Bs, Bs, d, 1, silu != 0};
+  return by_conv(io_dtype, d, W, [&](auto io, auto v, auto taps) {
     using IO = decltype(io);
-    hipLaunchKernelGGL((k_conv_decode<IO>), dim3(blocks(n)), dim3(256), 0, static_cast<hipStream_t>(stream), a, state_out,
-                       static_cast<IO*>(y));
+    constexpr int V = decltype(v)::value;
+    hipLaunchKernelGGL((k_conv_decode<IO, V, decltype(taps)::value>), dim3(static_cast<unsigned>(cdiv(n, 256 * V))), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), a, state_out, static_cast<IO*>(y));
     return launched();
   });
 }
 
 size_t mamba_mixer_conv_backward_workspace_bytes(int64_t T, int32_t d, int32_t W) {
   if (check_conv(1, T, d, W, MM_IO_F32, d) != MM_OK || d == 0) return 0;
-  return align256(static_cast<size_t>(cdiv(T, 16)) * d * (W + 1) * 4);
+  return align256(static_cast<size_t>(conv_groups(T, d)) * d * (W + 1) * 4);
 }
 
 int mamba_mixer_conv_backward(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
@@ -217,21 +511,20 @@ int mamba_mixer_conv_backward(const void* x, const float* weight, const float* b
   if (rc != MM_OK) return rc;
   rc = check_workspace(workspace, workspace_bytes, mamba_mixer_conv_backward_workspace_bytes(T, d, W));
   if (rc != MM_OK) return rc;
-  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, W, silu};
+  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d)), silu != 0};
   hipStream_t st = static_cast<hipStream_t>(stream);
   float* part = static_cast<float*>(workspace);
-  const int64_t parts = cdiv(T, 16);
-  return by_io(io_dtype, [&](auto io) {
+  return by_conv(io_dtype, d, W, [&](auto io, auto v, auto taps) {
     using IO = decltype(io);
-    const IO* g = static_cast<const IO*>(dy);
-    if (T > 0)
-      hipLaunchKernelGGL((k_conv_bwd<IO>), dim3(blocks(parts * d)), dim3(256), 0, st, a, g, dstate_out,
-                         static_cast<IO*>(dx), dx_stride, part);
-    if (dstate_in != nullptr && S > 0)
-      hipLaunchKernelGGL((k_conv_dstate<IO>), dim3(blocks(static_cast<int64_t>(S) * d)), dim3(256), 0, st, a, g, dstate_out,
-                         dstate_in);
-    hipLaunchKernelGGL(k_conv_parts, dim3(blocks(nw + d)), dim3(256), 0, st, part, parts, d, W, dweight,
-                       bias != nullptr ? dbias : nullptr);
+    constexpr int V = decltype(v)::value, K = decltype(taps)::value;
+    const uint32_t slices = static_cast<uint32_t>(conv_slices(d));
+    const int64_t groups = T > 0 ? conv_groups(T, d) : 0, blocks = groups * slices;
+    const int64_t states = dstate_in != nullptr ? cdiv(static_cast<int64_t>(S) * d, kConvThreads) : 0;
+    if (blocks + states > 0)
+      hipLaunchKernelGGL((k_conv_bwd<IO, V, K>), dim3(static_cast<unsigned>(blocks + states)), dim3(kConvThreads), 0, st, a, blocks,
+                         slices, static_cast<const IO*>(dy), dstate_out, static_cast<IO*>(dx), dx_stride, part, dstate_in);
+    hipLaunchKernelGGL(k_conv_parts, dim3(static_cast<unsigned>(cdiv(nw + d, kPartColumns))), dim3(256), 0, st, part, groups, d, W,
+                       dweight, bias != nullptr ? dbias : nullptr);
     return launched();
   });
 }

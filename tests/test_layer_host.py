@@ -155,7 +155,7 @@ def test_calls_of_no_size(lib):
 def test_sizes_at_the_launches_limits(lib):
     far = lambda n: ptrs(n, 1 << 42)  # noqa: E731
     assert conv_backward(lib, far(11), T=2 ** 31 - 1, d=15, xs=15, gx=15, wsb=0) == WORKSPACE
-    assert conv_backward(lib, far(11), T=2 ** 31 - 1, d=16, xs=16, gx=16, wsb=0) == DIM
+    assert conv_backward(lib, far(11), T=2 ** 31 - 1, d=512, xs=512, gx=512, wsb=0) == DIM
     rows = lambda d: {k: d for k in ("d", "xs", "rs", "gs", "zs", "dxs", "drs", "dgs", "dzs")}  # noqa: E731
     assert gated_backward(lib, far(16), T=2 ** 30 - 256, wsb=0, **rows(32)) == WORKSPACE
     assert gated_backward(lib, far(16), T=2 ** 30, wsb=0, **rows(32)) == DIM
