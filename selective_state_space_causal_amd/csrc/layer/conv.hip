@@ -13,8 +13,9 @@
 namespace mm {
 namespace {
 
-constexpr int kConvWaves = 4, kConvThreads = kConvWaves * 64, kStep = 8;
-constexpr int64_t kConvWalks = 4096;  // waves that are wanted: L is at most 64 tokens, less where there would be fewer
+constexpr int kConvWaves = 4, kConvThreads = kConvWaves * 64, kStep = 4;
+// A walk has at most 64 tokens (backward 128), fewer where there would be fewer walks than these.
+constexpr int64_t kConvWalks = 4096, kConvBackWalks = 2048;
 
 struct ConvArgs {
   const void* x;
@@ -392,12 +393,12 @@ __global__ __launch_bounds__(256) void k_conv_parts(const float* __restrict__ pa
 // ---------------------------------------------------------------- host
 int conv_channels(int32_t d) { return d % 4 == 0 ? 4 : d % 2 == 0 ? 2 : 1; }  // of a lane: all there or none
 int64_t conv_slices(int32_t d) { return cdiv(d, 64 * conv_channels(d)); }
-// tokens of a walk: kConvWalks of them where there are enough, in steps of kStep
-int64_t conv_tokens(int64_t T, int32_t d) {
-  const int64_t L = T * conv_slices(d) / kConvWalks / kStep * kStep;
-  return std::min<int64_t>(64, std::max<int64_t>(kStep, L));
+// tokens of a walk, in steps of kStep
+int64_t conv_tokens(int64_t T, int32_t d, bool back) {
+  const int64_t L = T * conv_slices(d) / (back ? kConvBackWalks : kConvWalks) / kStep * kStep;
+  return std::min<int64_t>(back ? 128 : 64, std::max<int64_t>(kStep, L));
 }
-int64_t conv_groups(int64_t T, int32_t d) { return cdiv(T, conv_tokens(T, d) * kConvWaves); }
+int64_t conv_groups(int64_t T, int32_t d, bool back) { return cdiv(T, conv_tokens(T, d, back) * kConvWaves); }
 
 int check_conv(int64_t S, int64_t T, int32_t d, int32_t W, int32_t io, int64_t x_ts) {
   const int rc = check_tokens(S, T, d, io);
@@ -405,7 +406,7 @@ int check_conv(int64_t S, int64_t T, int32_t d, int32_t W, int32_t io, int64_t x
   if (W < 2 || W > MM_CONV_MAX_W) return MM_ERR_UNSUPPORTED;
   if (x_ts < d) return MM_ERR_DIM;
   if (d == 0) return MM_OK;
-  const int64_t blocks = conv_groups(T, d) * conv_slices(d) + cdiv(S * d, kConvThreads);
+  const int64_t blocks = std::max(conv_groups(T, d, false), conv_groups(T, d, true)) * conv_slices(d) + cdiv(S * d, kConvThreads);
   return blocks * kConvThreads > kMaxThreads || cdiv(int64_t{W + 1} * d, kPartColumns) * 256 > kMaxThreads ? MM_ERR_DIM : MM_OK;
 }
 // f(IO, channels of a lane, taps)
@@ -444,13 +445,13 @@ int mamba_mixer_conv_prefill(const void* x, const float* weight, const float* bi
                   {flat(state_out, ns, 4), flat(y, T * d, es)}, {{0, 4}});
   if (rc != MM_OK) return rc;
   if (S == 0) return MM_OK;
-  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d)), silu != 0};
+  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d, false)), silu != 0};
   hipStream_t st = static_cast<hipStream_t>(stream);
   return by_conv(io_dtype, d, W, [&](auto io, auto v, auto taps) {
     using IO = decltype(io);
     constexpr int V = decltype(v)::value, K = decltype(taps)::value;
     const uint32_t slices = static_cast<uint32_t>(conv_slices(d));
-    const int64_t blocks = T > 0 ? conv_groups(T, d) * slices : 0, states = cdiv(static_cast<int64_t>(S) * d, kConvThreads);
+    const int64_t blocks = T > 0 ? conv_groups(T, d, false) * slices : 0, states = cdiv(static_cast<int64_t>(S) * d, kConvThreads);
     const auto launch = [&](int64_t walks, int64_t rest) {
       hipLaunchKernelGGL((k_conv<IO, V, K>), dim3(static_cast<unsigned>(walks + rest)), dim3(kConvThreads), 0, st, a, walks, slices,
                          static_cast<IO*>(y), state_out);
@@ -489,7 +490,7 @@ int mamba_mixer_conv_decode(const void* x, const float* weight, const float* bia
 
 size_t mamba_mixer_conv_backward_workspace_bytes(int64_t T, int32_t d, int32_t W) {
   if (check_conv(1, T, d, W, MM_IO_F32, d) != MM_OK || d == 0) return 0;
-  return align256(static_cast<size_t>(conv_groups(T, d)) * d * (W + 1) * 4);
+  return align256(static_cast<size_t>(conv_groups(T, d, true)) * d * (W + 1) * 4);
 }
 
 int mamba_mixer_conv_backward(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
@@ -511,14 +512,14 @@ int mamba_mixer_conv_backward(const void* x, const float* weight, const float* b
   if (rc != MM_OK) return rc;
   rc = check_workspace(workspace, workspace_bytes, mamba_mixer_conv_backward_workspace_bytes(T, d, W));
   if (rc != MM_OK) return rc;
-  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d)), silu != 0};
+  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d, true)), silu != 0};
   hipStream_t st = static_cast<hipStream_t>(stream);
   float* part = static_cast<float*>(workspace);
   return by_conv(io_dtype, d, W, [&](auto io, auto v, auto taps) {
     using IO = decltype(io);
     constexpr int V = decltype(v)::value, K = decltype(taps)::value;
     const uint32_t slices = static_cast<uint32_t>(conv_slices(d));
-    const int64_t groups = T > 0 ? conv_groups(T, d) : 0, blocks = groups * slices;
+    const int64_t groups = T > 0 ? conv_groups(T, d, true) : 0, blocks = groups * slices;
     const int64_t states = dstate_in != nullptr ? cdiv(static_cast<int64_t>(S) * d, kConvThreads) : 0;
     if (blocks + states > 0)
       hipLaunchKernelGGL((k_conv_bwd<IO, V, K>), dim3(static_cast<unsigned>(blocks + states)), dim3(kConvThreads), 0, st, a, blocks,
