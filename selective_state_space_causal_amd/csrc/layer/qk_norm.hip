@@ -1,4 +1,7 @@
 // The norms of queries and keys with their rotation: kernels, argument checks and entry points.
+#include <algorithm>
+#include <type_traits>
+
 #include "layer/common.h"
 
 namespace mm {
@@ -19,18 +22,258 @@ __device__ __forceinline__ void qk_angle(int32_t pos, float freq, float& c, floa
   const double turns = static_cast<double>(pos) * (static_cast<double>(freq) * 0.15915494309189535);
   sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
 }
-// the other column of column i's pair, and whether i is its first
-__device__ __forceinline__ int qk_mate(const QkArgs& a, int i, bool& first) {
+// ---------------------------------------------------------------- rows of 8 GP' columns
+// A group of GP lanes takes a row (one token's head) at a time, a lane eight columns: two pieces of four that hold whole pairs.
+// The angles of a block of tokens are computed once for all of its heads and lie in LDS.  A group stays with its heads and
+// walks over the block's tokens, kQkRows of them at a time so that loads are in flight.  Bound by memory.
+constexpr int kQkThreads = 256, kQkTokens = 16, kQkRows = 4;
+
+struct QkAngles {
+  float c[kQkTokens][MM_QK_MAX_D / 2], s[kQkTokens][MM_QK_MAX_D / 2];
+};
+__device__ __forceinline__ void qk_angles(const QkArgs& a, int64_t t0, int tokens, QkAngles& ang) {
+  const int P = a.R / 2;
+  for (int i = threadIdx.x; i < tokens * P; i += kQkThreads) {
+    const int t = i / P, p = i - t * P;
+    qk_angle(a.pos[t0 + t], a.freq[p], ang.c[t][p], ang.s[t][p]);
+  }
+}
+// The places of a lane's columns: where its two pieces start, and its first pair.
+struct QkPlace {
+  int c0, c1, pair;
+  bool on, turns;
+};
+__device__ __forceinline__ QkPlace qk_place(const QkArgs& a, int lane) {
+  QkPlace p;
+  p.pair = 4 * lane;
+  p.on = 8 * lane < a.D;
+  p.turns = p.pair < a.R / 2;
+  const int rest = (a.D - a.R) / 2;
+  p.c0 = a.inter ? 8 * lane : p.turns ? p.pair : a.R + p.pair - a.R / 2;
+  p.c1 = a.inter ? p.c0 + 4 : p.c0 + (p.turns ? a.R / 2 : rest);
+  return p;
+}
+// v[0..3], v[4..7]: the lane's pieces; sign -1 turns back
+__device__ __forceinline__ void qk_turn(const QkArgs& a, const QkPlace& p, const QkAngles& ang, int t, float sign, float (&v)[8]) {
+  if (!p.turns) return;
+  float c[4], s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = ang.c[t][p.pair + i];
+    s[i] = sign * ang.s[t][p.pair + i];
+  }
+  if (a.inter) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[2 * i], y = v[2 * i + 1];
+      v[2 * i] = __builtin_fmaf(x, c[i], -y * s[i]);
+      v[2 * i + 1] = __builtin_fmaf(y, c[i], x * s[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[i], y = v[i + 4];
+      v[i] = __builtin_fmaf(x, c[i], -y * s[i]);
+      v[i + 4] = __builtin_fmaf(y, c[i], x * s[i]);
+    }
+  }
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) { return v + __builtin_amdgcn_update_dpp(0.0f, v, CTRL, 0xF, 0xF, true); }
+// the sum over a group's lanes, in all of them
+template <int GP>
+__device__ __forceinline__ float group_sum(float v) {
+  if constexpr (GP >= 2) v = dpp_add<0xB1>(v);   // quad_perm 1 0 3 2
+  if constexpr (GP >= 4) v = dpp_add<0x4E>(v);   // quad_perm 2 3 0 1
+  if constexpr (GP >= 8) v = dpp_add<0x141>(v);  // row_half_mirror: the other four of eight
+  if constexpr (GP >= 16) v = dpp_add<0x140>(v); // row_mirror: the other eight of sixteen
+  if constexpr (GP >= 32) v += __shfl_xor(v, 16);
+  return v;
+}
+// a piece of four, in the place of its row
+template <typename IO>
+__device__ __forceinline__ Chans<IO, 4> qk_load(const IO* row, int c) { return load_chans<IO, 4>(global(row + c), 0); }
+
+// Heads of one kind: how a workgroup's groups share them and the tokens.
+struct QkShare {
+  int head, heads, token, tokens;  // first head and token of this group, and their steps
+};
+template <int GP>
+__device__ __forceinline__ QkShare qk_share(int H) {
+  constexpr int groups = kQkThreads / GP;
+  const int g = threadIdx.x / GP;
+  int n = 1;
+  while (n < H && n < groups) n *= 2;
+  return {g % n, n, g / n, groups / n};
+}
+
+template <typename IO, int GP>
+__global__ __launch_bounds__(kQkThreads) void k_qk_rows(QkArgs a, int block, IO* q_out, IO* k_out, int64_t qo_ts, int64_t ko_ts) {
+  __shared__ QkAngles ang;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * block;
+  const int tokens = static_cast<int>(a.T - t0 < block ? a.T - t0 : block);
+  qk_angles(a, t0, tokens, ang);
+  __syncthreads();
+  const QkPlace p = qk_place(a, threadIdx.x % GP);
+  const float mean = 1.0f / a.D;
+  const auto kind = [&](const IO* in, int64_t ts, IO* out, int64_t o_ts, const float* weight, int H) {
+    const QkShare sh = qk_share<GP>(H);
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = p.on ? weight[p.c0 + i] : 0.0f;
+      w[i + 4] = p.on ? weight[p.c1 + i] : 0.0f;
+    }
+    for (int h = sh.head; h < H; h += sh.heads) {
+      const IO* src = in + t0 * ts + static_cast<int64_t>(h) * a.D;
+      IO* dst = out + t0 * o_ts + static_cast<int64_t>(h) * a.D;
+      for (int t = sh.token; t < tokens; t += sh.tokens * kQkRows) {
+        Chans<IO, 4> r0[kQkRows], r1[kQkRows];
+#pragma unroll
+        for (int j = 0; j < kQkRows; ++j) {
+          const int tj = t + j * sh.tokens;
+          r0[j] = r1[j] = Chans<IO, 4>{};
+          if (p.on && tj < tokens) {
+            r0[j] = qk_load(src + tj * ts, p.c0);
+            r1[j] = qk_load(src + tj * ts, p.c1);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kQkRows; ++j) {
+          const int tj = t + j * sh.tokens;
+          float v[8], s = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = r0[j][i];
+            v[i + 4] = r1[j][i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s = __builtin_fmaf(v[i], v[i], s);
+          const float k = rsqrtf(__builtin_fmaf(group_sum<GP>(s), mean, a.eps));
+          if (!p.on || tj >= tokens) continue;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= k * w[i];
+          qk_turn(a, p, ang, tj, 1.0f, v);
+          const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+          store_chans<IO, 4>(global(dst + tj * o_ts + p.c0), 0, lo);
+          store_chans<IO, 4>(global(dst + tj * o_ts + p.c1), 0, hi);
+        }
+      }
+    }
+  };
+  kind(static_cast<const IO*>(a.q), a.q_ts, q_out, qo_ts, a.wq, a.Hq);
+  kind(static_cast<const IO*>(a.k), a.k_ts, k_out, ko_ts, a.wk, a.Hk);
+}
+
+// With g the output's gradient turned back, n = v k and dn = g w:  dv = k (dn - n mean(dn n)),  dw = sum g n.
+// A workgroup takes blocks of tokens and leaves its sums of dw: part [2][parts][D], queries' and keys'.
+constexpr int kQkParts = 512;
+template <typename IO, int GP>
+__global__ __launch_bounds__(kQkThreads) void k_qk_rows_bwd(QkArgs a, int block, const IO* dqo, const IO* dko, IO* dq, IO* dk,
+                                                            int64_t dq_ts, int64_t dk_ts, float* part) {
+  __shared__ QkAngles ang;
+  __shared__ float sums[kQkThreads / GP][8 * GP];
+  const QkPlace p = qk_place(a, threadIdx.x % GP);
+  const float mean = 1.0f / a.D;
+  float dw[2][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.0f;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * block; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * block) {
+    const int tokens = static_cast<int>(a.T - t0 < block ? a.T - t0 : block);
+    __syncthreads();
+    qk_angles(a, t0, tokens, ang);
+    __syncthreads();
+    const auto kind = [&](const IO* in, int64_t ts, const IO* dout, IO* out, int64_t o_ts, const float* weight, int H, float(&sum)[8]) {
+      const QkShare sh = qk_share<GP>(H);
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = p.on ? weight[p.c0 + i] : 0.0f;
+        w[i + 4] = p.on ? weight[p.c1 + i] : 0.0f;
+      }
+      const int64_t g_ts = static_cast<int64_t>(H) * a.D;
+      for (int h = sh.head; h < H; h += sh.heads) {
+        const IO* src = in + t0 * ts + static_cast<int64_t>(h) * a.D;
+        const IO* grad = dout + t0 * g_ts + static_cast<int64_t>(h) * a.D;
+        IO* dst = out + t0 * o_ts + static_cast<int64_t>(h) * a.D;
+        for (int t = sh.token; t < tokens; t += sh.tokens * kQkRows) {
+          Chans<IO, 4> r0[kQkRows], r1[kQkRows], g0[kQkRows], g1[kQkRows];
+#pragma unroll
+          for (int j = 0; j < kQkRows; ++j) {
+            const int tj = t + j * sh.tokens;
+            r0[j] = r1[j] = g0[j] = g1[j] = Chans<IO, 4>{};
+            if (p.on && tj < tokens) {
+              r0[j] = qk_load(src + tj * ts, p.c0);
+              r1[j] = qk_load(src + tj * ts, p.c1);
+              g0[j] = qk_load(grad + tj * g_ts, p.c0);
+              g1[j] = qk_load(grad + tj * g_ts, p.c1);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kQkRows; ++j) {
+            const int tj = t + j * sh.tokens;
+            float v[8], g[8], s = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i] = r0[j][i];
+              v[i + 4] = r1[j][i];
+              g[i] = g0[j][i];
+              g[i + 4] = g1[j][i];
+            }
+            if (tj < tokens) qk_turn(a, p, ang, tj, -1.0f, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              s = __builtin_fmaf(v[i], v[i], s);
+              dot = __builtin_fmaf(g[i] * w[i], v[i], dot);
+            }
+            const float k = rsqrtf(__builtin_fmaf(group_sum<GP>(s), mean, a.eps)), m = group_sum<GP>(dot) * mean * k;
+            if (!p.on || tj >= tokens) continue;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float n = v[i] * k;
+              sum[i] = __builtin_fmaf(g[i], n, sum[i]);
+              o[i] = k * __builtin_fmaf(g[i], w[i], -n * m);
+            }
+            const float lo[4] = {o[0], o[1], o[2], o[3]}, hi[4] = {o[4], o[5], o[6], o[7]};
+            store_chans<IO, 4>(global(dst + tj * o_ts + p.c0), 0, lo);
+            store_chans<IO, 4>(global(dst + tj * o_ts + p.c1), 0, hi);
+          }
+        }
+      }
+    };
+    kind(static_cast<const IO*>(a.q), a.q_ts, dqo, dq, dq_ts, a.wq, a.Hq, dw[0]);
+    kind(static_cast<const IO*>(a.k), a.k_ts, dko, dk, dk_ts, a.wk, a.Hk, dw[1]);
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    __syncthreads();
+    if (p.on) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sums[threadIdx.x / GP][p.c0 + i] = dw[n][i];
+        sums[threadIdx.x / GP][p.c1 + i] = dw[n][i + 4];
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.D; i += kQkThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int g = 0; g < kQkThreads / GP; ++g) v += sums[g][i];
+      part[(static_cast<int64_t>(n) * gridDim.x + blockIdx.x) * a.D + i] = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- rows of any width
+// A wave takes a row, with its values in LDS: pairs may lie anywhere.
+__device__ __forceinline__ int qk_mate(const QkArgs& a, int i, bool& first) {  // the other column of i's pair, and whether i is its first
   first = a.inter ? i % 2 == 0 : i < a.R / 2;
   return a.inter ? i ^ 1 : first ? i + a.R / 2 : i - a.R / 2;
 }
 __device__ __forceinline__ int qk_pair(const QkArgs& a, int i) { return a.inter ? i / 2 : i % (a.R / 2); }
-__device__ __forceinline__ float wave_sum(float v) {
-  for (int k = 32; k > 0; k >>= 1) v += __shfl_xor(v, k);
-  return v;
-}
+__device__ __forceinline__ float wave_sum(float v) { return group_sum<32>(v) + __shfl_xor(group_sum<32>(v), 32); }
 
-// a wave for each (token, head); with `dout` the gradients, else the outputs
 template <typename IO>
 __global__ __launch_bounds__(64) void k_qk(QkArgs a, IO* q_out, IO* k_out, int64_t qo_ts, int64_t ko_ts) {
   __shared__ float u[MM_QK_MAX_D];
@@ -63,9 +306,7 @@ __global__ __launch_bounds__(64) void k_qk(QkArgs a, IO* q_out, IO* k_out, int64
   }
 }
 
-// With g the output's gradient turned back, n = v r and dn = g w:  dv = r (dn - n mean(dn n)),  dw = sum g n.
-// A workgroup takes rows of one kind (queries or keys) and keeps the weight's gradient.
-constexpr int kQkParts = 512;
+// a workgroup takes rows of one kind (blockIdx.y: queries, keys)
 template <typename IO>
 __global__ __launch_bounds__(64) void k_qk_bwd(QkArgs a, const IO* dqo, const IO* dko, IO* dq, IO* dk, int64_t dq_ts, int64_t dk_ts,
                                                float* part) {
@@ -106,12 +347,31 @@ __global__ __launch_bounds__(64) void k_qk_bwd(QkArgs a, const IO* dqo, const IO
   }
   for (int i = threadIdx.x, e = 0; i < a.D; i += 64, ++e) part[(blockIdx.y * kQkParts + blockIdx.x) * a.D + i] = dw[e];
 }
-__global__ __launch_bounds__(256) void k_qk_parts(const float* part, int parts, int D, float* dwq, float* dwk) {
-  const int i = threadIdx.x;
-  if (i >= D) return;
-  float v = 0.0f;
-  for (int p = 0; p < parts; ++p) v += part[(blockIdx.x * kQkParts + p) * D + i];
-  (blockIdx.x == 0 ? dwq : dwk)[i] = v;
+// dwq, dwk from `parts` rows each
+__global__ __launch_bounds__(256) void k_qk_parts(const float* __restrict__ part, int64_t parts, int D, float* __restrict__ dwq,
+                                                  float* __restrict__ dwk) {
+  const int i = blockIdx.x * kPartColumns + threadIdx.x % kPartColumns;
+  const float v = sum_parts(part + blockIdx.y * parts * D, parts, D, i);
+  if (i < D && threadIdx.x < kPartColumns) (blockIdx.y == 0 ? dwq : dwk)[i] = v;
+}
+
+// Whole pairs lie in pieces of four columns where D and R are multiples of eight; the rest goes row by row, each through LDS.
+bool qk_by_groups(int D, int R) { return D % 8 == 0 && R % 8 == 0; }
+// tokens of a block: fewer where the blocks would not fill the GPU
+int qk_block(int64_t T) { return static_cast<int>(std::min<int64_t>(kQkTokens, std::max<int64_t>(1, T / 1024))); }
+int64_t qk_parts(int64_t T, int D, int R) {
+  return qk_by_groups(D, R) ? std::min<int64_t>(kQkParts, cdiv(T, qk_block(T))) : T > 0 ? kQkParts : 0;
+}
+// f(lanes of a group)
+template <typename F>
+void by_group(int D, F f) {
+  const int n = D / 8;
+  if (n <= 1) f(std::integral_constant<int, 1>{});
+  else if (n <= 2) f(std::integral_constant<int, 2>{});
+  else if (n <= 4) f(std::integral_constant<int, 4>{});
+  else if (n <= 8) f(std::integral_constant<int, 8>{});
+  else if (n <= 16) f(std::integral_constant<int, 16>{});
+  else f(std::integral_constant<int, 32>{});
 }
 
 int check_qk(int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R, float eps, int32_t io) {
@@ -144,8 +404,17 @@ int mamba_mixer_qk_norm(const void* q, const void* k, const float* q_weight, con
   const QkArgs a{q, k, q_weight, k_weight, positions, inv_freq, q_stride, k_stride, T, Hq, Hk, D, R, interleaved != 0, eps};
   return by_io(io_dtype, [&](auto io) {
     using IO = decltype(io);
-    hipLaunchKernelGGL((k_qk<IO>), dim3(static_cast<unsigned>(T * (Hq + Hk))), dim3(64), 0, static_cast<hipStream_t>(stream), a,
-                       static_cast<IO*>(q_out), static_cast<IO*>(k_out), qo_stride, ko_stride);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (qk_by_groups(D, R)) {
+      const int block = qk_block(T);
+      by_group(D, [&](auto n) {
+        hipLaunchKernelGGL((k_qk_rows<IO, decltype(n)::value>), dim3(static_cast<unsigned>(cdiv(T, block))), dim3(kQkThreads), 0, st, a,
+                           block, static_cast<IO*>(q_out), static_cast<IO*>(k_out), qo_stride, ko_stride);
+      });
+    } else {
+      hipLaunchKernelGGL((k_qk<IO>), dim3(static_cast<unsigned>(T * (Hq + Hk))), dim3(64), 0, st, a, static_cast<IO*>(q_out),
+                         static_cast<IO*>(k_out), qo_stride, ko_stride);
+    }
     return launched();
   });
 }
@@ -180,10 +449,19 @@ int mamba_mixer_qk_norm_backward(const void* dq_out, const void* dk_out, const v
   float* part = static_cast<float*>(workspace);
   return by_io(io_dtype, [&](auto io) {
     using IO = decltype(io);
-    if (T > 0)
+    const int64_t parts = qk_parts(T, D, R);
+    if (T > 0 && qk_by_groups(D, R)) {
+      by_group(D, [&](auto n) {
+        hipLaunchKernelGGL((k_qk_rows_bwd<IO, decltype(n)::value>), dim3(static_cast<unsigned>(parts)), dim3(kQkThreads), 0, st, a,
+                           qk_block(T), static_cast<const IO*>(dq_out), static_cast<const IO*>(dk_out), static_cast<IO*>(dq),
+                           static_cast<IO*>(dk), dq_stride, dk_stride, part);
+      });
+    } else if (T > 0) {
       hipLaunchKernelGGL((k_qk_bwd<IO>), dim3(kQkParts, 2), dim3(64), 0, st, a, static_cast<const IO*>(dq_out),
                          static_cast<const IO*>(dk_out), static_cast<IO*>(dq), static_cast<IO*>(dk), dq_stride, dk_stride, part);
-    hipLaunchKernelGGL(k_qk_parts, dim3(2), dim3(256), 0, st, part, T > 0 ? kQkParts : 0, D, dq_weight, dk_weight);
+    }
+    hipLaunchKernelGGL(k_qk_parts, dim3(static_cast<unsigned>(cdiv(D, kPartColumns)), 2), dim3(256), 0, st, part, parts, D, dq_weight,
+                       dk_weight);
     return launched();
   });
 }
