@@ -116,6 +116,14 @@ __device__ __forceinline__ Chans<IO, V> load_chans(gmem<const IO>* p, uint32_t o
   } else if constexpr (W == 1) {
     typedef uint32_t word __attribute__((aligned(2)));
     r.w[0] = __builtin_nontemporal_load(reinterpret_cast<gmem<const word>*>(q));
+  } else if constexpr (W > 4) {
+    typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+    for (int j = 0; j < W; j += 4) {
+      const vec v = __builtin_nontemporal_load(reinterpret_cast<gmem<const vec>*>(q + 4 * j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[j + i] = v[i];
+    }
   } else {
     typedef uint32_t vec __attribute__((ext_vector_type(W), aligned(sizeof(IO))));
     const vec v = __builtin_nontemporal_load(reinterpret_cast<gmem<const vec>*>(q));

@@ -43,18 +43,20 @@ struct QkPlace {
   int c0, c1, pair;
   bool on, turns;
 };
+template <bool INTER>
 __device__ __forceinline__ QkPlace qk_place(const QkArgs& a, int lane) {
   QkPlace p;
   p.pair = 4 * lane;
   p.on = 8 * lane < a.D;
   p.turns = p.pair < a.R / 2;
   const int rest = (a.D - a.R) / 2;
-  p.c0 = a.inter ? 8 * lane : p.turns ? p.pair : a.R + p.pair - a.R / 2;
-  p.c1 = a.inter ? p.c0 + 4 : p.c0 + (p.turns ? a.R / 2 : rest);
+  p.c0 = INTER ? 8 * lane : p.turns ? p.pair : a.R + p.pair - a.R / 2;
+  p.c1 = INTER ? p.c0 + 4 : p.c0 + (p.turns ? a.R / 2 : rest);
   return p;
 }
 // v[0..3], v[4..7]: the lane's pieces; sign -1 turns back
-__device__ __forceinline__ void qk_turn(const QkArgs& a, const QkPlace& p, const QkAngles& ang, int t, float sign, float (&v)[8]) {
+template <bool INTER>
+__device__ __forceinline__ void qk_turn(const QkPlace& p, const QkAngles& ang, int t, float sign, float (&v)[8]) {
   if (!p.turns) return;
   float c[4], s[4];
 #pragma unroll
@@ -62,7 +64,7 @@ __device__ __forceinline__ void qk_turn(const QkArgs& a, const QkPlace& p, const
     c[i] = ang.c[t][p.pair + i];
     s[i] = sign * ang.s[t][p.pair + i];
   }
-  if (a.inter) {
+  if constexpr (INTER) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x = v[2 * i], y = v[2 * i + 1];
@@ -90,9 +92,31 @@ __device__ __forceinline__ float group_sum(float v) {
   if constexpr (GP >= 32) v += __shfl_xor(v, 16);
   return v;
 }
-// a piece of four, in the place of its row
-template <typename IO>
-__device__ __forceinline__ Chans<IO, 4> qk_load(const IO* row, int c) { return load_chans<IO, 4>(global(row + c), 0); }
+// a lane's columns of a row: neighbours when interleaved, else two pieces
+template <bool INTER, typename IO>
+__device__ __forceinline__ void qk_load(const IO* row, const QkPlace& p, Chans<IO, 4>& lo, Chans<IO, 4>& hi) {
+  if constexpr (INTER) {
+    const Chans<IO, 8> v = load_chans<IO, 8>(global(row + p.c0), 0);
+#pragma unroll
+    for (int i = 0; i < Chans<IO, 4>::W; ++i) {
+      lo.w[i] = v.w[i];
+      hi.w[i] = v.w[Chans<IO, 4>::W + i];
+    }
+  } else {
+    lo = load_chans<IO, 4>(global(row + p.c0), 0);
+    hi = load_chans<IO, 4>(global(row + p.c1), 0);
+  }
+}
+template <bool INTER, typename IO>
+__device__ __forceinline__ void qk_store(IO* row, const QkPlace& p, const float (&v)[8]) {
+  if constexpr (INTER) {
+    store_chans<IO, 8>(global(row + p.c0), 0, v);
+  } else {
+    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+    store_chans<IO, 4>(global(row + p.c0), 0, lo);
+    store_chans<IO, 4>(global(row + p.c1), 0, hi);
+  }
+}
 
 // Heads of one kind: how a workgroup's groups share them and the tokens.
 struct QkShare {
@@ -107,14 +131,14 @@ __device__ __forceinline__ QkShare qk_share(int H) {
   return {g % n, n, g / n, groups / n};
 }
 
-template <typename IO, int GP>
+template <typename IO, int GP, bool INTER>
 __global__ __launch_bounds__(kQkThreads) void k_qk_rows(QkArgs a, int block, IO* q_out, IO* k_out, int64_t qo_ts, int64_t ko_ts) {
   __shared__ QkAngles ang;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * block;
   const int tokens = static_cast<int>(a.T - t0 < block ? a.T - t0 : block);
   qk_angles(a, t0, tokens, ang);
   __syncthreads();
-  const QkPlace p = qk_place(a, threadIdx.x % GP);
+  const QkPlace p = qk_place<INTER>(a, threadIdx.x % GP);
   const float mean = 1.0f / a.D;
   const auto kind = [&](const IO* in, int64_t ts, IO* out, int64_t o_ts, const float* weight, int H) {
     const QkShare sh = qk_share<GP>(H);
@@ -134,8 +158,7 @@ __global__ __launch_bounds__(kQkThreads) void k_qk_rows(QkArgs a, int block, IO*
           const int tj = t + j * sh.tokens;
           r0[j] = r1[j] = Chans<IO, 4>{};
           if (p.on && tj < tokens) {
-            r0[j] = qk_load(src + tj * ts, p.c0);
-            r1[j] = qk_load(src + tj * ts, p.c1);
+            qk_load<INTER>(src + tj * ts, p, r0[j], r1[j]);
           }
         }
 #pragma unroll
@@ -153,10 +176,8 @@ __global__ __launch_bounds__(kQkThreads) void k_qk_rows(QkArgs a, int block, IO*
           if (!p.on || tj >= tokens) continue;
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] *= k * w[i];
-          qk_turn(a, p, ang, tj, 1.0f, v);
-          const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-          store_chans<IO, 4>(global(dst + tj * o_ts + p.c0), 0, lo);
-          store_chans<IO, 4>(global(dst + tj * o_ts + p.c1), 0, hi);
+          qk_turn<INTER>(p, ang, tj, 1.0f, v);
+          qk_store<INTER>(dst + tj * o_ts, p, v);
         }
       }
     }
@@ -168,12 +189,12 @@ __global__ __launch_bounds__(kQkThreads) void k_qk_rows(QkArgs a, int block, IO*
 // With g the output's gradient turned back, n = v k and dn = g w:  dv = k (dn - n mean(dn n)),  dw = sum g n.
 // A workgroup takes blocks of tokens and leaves its sums of dw: part [2][parts][D], queries' and keys'.
 constexpr int kQkParts = 512;
-template <typename IO, int GP>
+template <typename IO, int GP, bool INTER>
 __global__ __launch_bounds__(kQkThreads) void k_qk_rows_bwd(QkArgs a, int block, const IO* dqo, const IO* dko, IO* dq, IO* dk,
                                                             int64_t dq_ts, int64_t dk_ts, float* part) {
   __shared__ QkAngles ang;
   __shared__ float sums[kQkThreads / GP][8 * GP];
-  const QkPlace p = qk_place(a, threadIdx.x % GP);
+  const QkPlace p = qk_place<INTER>(a, threadIdx.x % GP);
   const float mean = 1.0f / a.D;
   float dw[2][8];
 #pragma unroll
@@ -203,10 +224,8 @@ __global__ __launch_bounds__(kQkThreads) void k_qk_rows_bwd(QkArgs a, int block,
             const int tj = t + j * sh.tokens;
             r0[j] = r1[j] = g0[j] = g1[j] = Chans<IO, 4>{};
             if (p.on && tj < tokens) {
-              r0[j] = qk_load(src + tj * ts, p.c0);
-              r1[j] = qk_load(src + tj * ts, p.c1);
-              g0[j] = qk_load(grad + tj * g_ts, p.c0);
-              g1[j] = qk_load(grad + tj * g_ts, p.c1);
+              qk_load<INTER>(src + tj * ts, p, r0[j], r1[j]);
+              qk_load<INTER>(grad + tj * g_ts, p, g0[j], g1[j]);
             }
           }
 #pragma unroll
@@ -220,7 +239,7 @@ __global__ __launch_bounds__(kQkThreads) void k_qk_rows_bwd(QkArgs a, int block,
               g[i] = g0[j][i];
               g[i + 4] = g1[j][i];
             }
-            if (tj < tokens) qk_turn(a, p, ang, tj, -1.0f, g);
+            if (tj < tokens) qk_turn<INTER>(p, ang, tj, -1.0f, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               s = __builtin_fmaf(v[i], v[i], s);
@@ -235,9 +254,7 @@ __global__ __launch_bounds__(kQkThreads) void k_qk_rows_bwd(QkArgs a, int block,
               sum[i] = __builtin_fmaf(g[i], n, sum[i]);
               o[i] = k * __builtin_fmaf(g[i], w[i], -n * m);
             }
-            const float lo[4] = {o[0], o[1], o[2], o[3]}, hi[4] = {o[4], o[5], o[6], o[7]};
-            store_chans<IO, 4>(global(dst + tj * o_ts + p.c0), 0, lo);
-            store_chans<IO, 4>(global(dst + tj * o_ts + p.c1), 0, hi);
+            qk_store<INTER>(dst + tj * o_ts, p, o);
           }
         }
       }
@@ -362,16 +379,20 @@ int qk_block(int64_t T) { return static_cast<int>(std::min<int64_t>(kQkTokens, s
 int64_t qk_parts(int64_t T, int D, int R) {
   return qk_by_groups(D, R) ? std::min<int64_t>(kQkParts, cdiv(T, qk_block(T))) : T > 0 ? kQkParts : 0;
 }
-// f(lanes of a group)
+// f(lanes of a group, interleaved)
 template <typename F>
-void by_group(int D, F f) {
+void by_group(int D, bool inter, F f) {
   const int n = D / 8;
-  if (n <= 1) f(std::integral_constant<int, 1>{});
-  else if (n <= 2) f(std::integral_constant<int, 2>{});
-  else if (n <= 4) f(std::integral_constant<int, 4>{});
-  else if (n <= 8) f(std::integral_constant<int, 8>{});
-  else if (n <= 16) f(std::integral_constant<int, 16>{});
-  else f(std::integral_constant<int, 32>{});
+  const auto go = [&](auto lanes) {
+    if (inter) f(lanes, std::true_type{});
+    else f(lanes, std::false_type{});
+  };
+  if (n <= 1) go(std::integral_constant<int, 1>{});
+  else if (n <= 2) go(std::integral_constant<int, 2>{});
+  else if (n <= 4) go(std::integral_constant<int, 4>{});
+  else if (n <= 8) go(std::integral_constant<int, 8>{});
+  else if (n <= 16) go(std::integral_constant<int, 16>{});
+  else go(std::integral_constant<int, 32>{});
 }
 
 int check_qk(int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R, float eps, int32_t io) {
@@ -407,8 +428,8 @@ int mamba_mixer_qk_norm(const void* q, const void* k, const float* q_weight, con
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (qk_by_groups(D, R)) {
       const int block = qk_block(T);
-      by_group(D, [&](auto n) {
-        hipLaunchKernelGGL((k_qk_rows<IO, decltype(n)::value>), dim3(static_cast<unsigned>(cdiv(T, block))), dim3(kQkThreads), 0, st, a,
+      by_group(D, interleaved != 0, [&](auto n, auto inter) {
+        hipLaunchKernelGGL((k_qk_rows<IO, decltype(n)::value, decltype(inter)::value>), dim3(static_cast<unsigned>(cdiv(T, block))), dim3(kQkThreads), 0, st, a,
                            block, static_cast<IO*>(q_out), static_cast<IO*>(k_out), qo_stride, ko_stride);
       });
     } else {
@@ -451,8 +472,8 @@ int mamba_mixer_qk_norm_backward(const void* dq_out, const void* dk_out, const v
     using IO = decltype(io);
     const int64_t parts = qk_parts(T, D, R);
     if (T > 0 && qk_by_groups(D, R)) {
-      by_group(D, [&](auto n) {
-        hipLaunchKernelGGL((k_qk_rows_bwd<IO, decltype(n)::value>), dim3(static_cast<unsigned>(parts)), dim3(kQkThreads), 0, st, a,
+      by_group(D, interleaved != 0, [&](auto n, auto inter) {
+        hipLaunchKernelGGL((k_qk_rows_bwd<IO, decltype(n)::value, decltype(inter)::value>), dim3(static_cast<unsigned>(parts)), dim3(kQkThreads), 0, st, a,
                            qk_block(T), static_cast<const IO*>(dq_out), static_cast<const IO*>(dk_out), static_cast<IO*>(dq),
                            static_cast<IO*>(dk), dq_stride, dk_stride, part);
       });
