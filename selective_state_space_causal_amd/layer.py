@@ -25,17 +25,18 @@ def _lib():
 
 def _run(name, x, tensors, *args):
     """The library's call, on x's device, which all its tensors have to be on."""
-    device = x.device
+    index = x.get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: tensors on {device} and {t.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name}: tensors on {x.device} and {t.device}")
     call = getattr(_lib(), name)
-    if device.index is None or device.index == _current_device():
+    if index < 0 or index == _current_device():
         rc = call(*args)
     else:
-        with _h.torch.cuda.device(device):
+        with _h.torch.cuda.device(index):
             rc = call(*args)
-    _raise(rc, name)
+    if rc:
+        _raise(rc, name)
 
 
 def _sequences(cu_seqlens, T):
@@ -54,6 +55,11 @@ def _given(t, shape, dtype, name, device, stream):
         return _new(shape, dtype, device, stream)
     _need(t, shape, dtype, name)
     return t
+
+
+def _rows_out(t, shape, dtype, name, device, stream, width):
+    """An output whose rows (of `width` elements) may be strided, and their stride: the caller's or a new one."""
+    return (_new(shape, dtype, device, stream), width) if t is None else _out(t, shape, dtype, device, name, stream)
 
 
 def _conv_inputs(x, weight, bias):
@@ -113,7 +119,7 @@ def conv_backward(x, weight, bias, cu_seqlens, state_in, dy, dstate_out=None, si
         if t is not None:
             _need(t, shape, _h._F32, n)
     _need(dy, (T, d), x.dtype, "dy")
-    dx, dxs = _out(dx, (T, d), x.dtype, dev, "dx", stream)
+    dx, dxs = _rows_out(dx, (T, d), x.dtype, "dx", dev, stream, d)
     dweight = _new((d, W), _h._F32, dev, stream)
     dbias = _new((d,), _h._F32, dev, stream) if bias is not None else None
     dstate_in = _new(shape, _h._F32, dev, stream) if need_dstate else None
@@ -209,7 +215,7 @@ def gated_backward(x, r, g, z, lam, cu_seqlens, state_in, dy, dstate_out=None, c
     if ckpt is not None:
         _need(ckpt, (-(-T // GATED_BLOCK), d), _h._F32, "ckpt")
     _need(dy, (T, d), x.dtype, "dy")
-    one = lambda t, n: _out(t, (T, d), x.dtype, dev, n, stream)  # noqa: E731
+    one = lambda t, n: _rows_out(t, (T, d), x.dtype, n, dev, stream, d)  # noqa: E731
     (dx, xs), (dr, rs) = one(dx, "dx"), one(dr, "dr")
     dg, gs = one(dg, "dg") if g is not None else (None, 0)
     dz, zs = one(dz, "dz") if z is not None else (None, 0)
@@ -252,8 +258,9 @@ def qk_norm(q, k, q_weight, k_weight, positions=None, inv_freq=None, eps: float 
     [R / 2] float32: the first R columns turn, in pairs (k, k + R / 2), or (2 k, 2 k + 1) when interleaved; neither given:
     the norms alone.  Returns (q_out, k_out), which may be given (with strided rows) and may be q and k themselves."""
     _, T, Hq, Hk, D, R, io, qs, ks = _qk_inputs(q, k, q_weight, k_weight, positions, inv_freq)
-    q_out, qos = _out(q_out, (T, Hq, D), q.dtype, q.device, "q_out", stream)
-    k_out, kos = _out(k_out, (T, Hk, D), q.dtype, q.device, "k_out", stream)
+    dev = q.device
+    q_out, qos = _rows_out(q_out, (T, Hq, D), q.dtype, "q_out", dev, stream, Hq * D)
+    k_out, kos = _rows_out(k_out, (T, Hk, D), q.dtype, "k_out", dev, stream, Hk * D)
     _run("mamba_mixer_qk_norm", q, (k, q_weight, k_weight, positions, inv_freq, q_out, k_out), q.data_ptr(), k.data_ptr(),
          q_weight.data_ptr(), k_weight.data_ptr(), _opt(positions), _opt(inv_freq), q_out.data_ptr(), k_out.data_ptr(), T,
          Hq, Hk, D, R, eps, 1 if interleaved else 0, io, qs, ks, qos, kos, _on(stream, q))
@@ -268,8 +275,8 @@ def qk_norm_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions=None, i
     _need(dq_out, (T, Hq, D), q.dtype, "dq_out")
     _need(dk_out, (T, Hk, D), q.dtype, "dk_out")
     dev = q.device
-    dq, dqs = _out(dq, (T, Hq, D), q.dtype, dev, "dq", stream)
-    dk, dks = _out(dk, (T, Hk, D), q.dtype, dev, "dk", stream)
+    dq, dqs = _rows_out(dq, (T, Hq, D), q.dtype, "dq", dev, stream, Hq * D)
+    dk, dks = _rows_out(dk, (T, Hk, D), q.dtype, "dk", dev, stream, Hk * D)
     dwq, dwk = (_new((D,), _h._F32, dev, stream) for _ in range(2))
     need = lib.mamba_mixer_qk_norm_backward_workspace_bytes(T, Hq, Hk, D) if workspace is None else 0
     workspace, wptr, wbytes = _workspace(workspace, need, dev, stream)

@@ -197,6 +197,9 @@ def test_tensors_of_another_device_are_refused():
     class Elsewhere(streams.OnDevice):
         device = torch.device("cuda", 7)
 
+        def get_device(self):
+            return 7
+
     other = torch.zeros(3, 64, dtype=streams.BF16).as_subclass(Elsewhere)
     with pytest.raises(ValueError, match="cuda:7"):
         mm.gated_decode(dev(3, 64), other, None, None, None, stream=CURRENT)
