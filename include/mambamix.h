@@ -605,7 +605,7 @@ size_t mamba_mixer_conv_backward_workspace_bytes(int64_t T, int32_t d, int32_t W
  * input but state_out == state_in.  workspace: mamba_mixer_gated_prefill_workspace_bytes bytes (0 for short calls),
  * 256-byte aligned, contents on entry do not matter; it is one call's until that call has run.
  * Rows are at most MM_LAYER_MAX_STRIDE elements apart (else MM_ERR_UNSUPPORTED).  S < 2^29, and a launch has less than
- * 2^32 threads: ceil(T / MM_GATED_BLOCK) ceil(d / 64) < 2^24 and S d < 2^31 (else MM_ERR_DIM).  T == 0 copies the states; d == 0 is a no-op.
+ * 2^32 threads: ceil(T / MM_GATED_BLOCK) ceil(d / 64) < 2^23 and S d < 2^31 (else MM_ERR_DIM).  T == 0 copies the states; d == 0 is a no-op.
  */
 #define MM_LAYER_MAX_STRIDE (1 << 22)
 #define MM_GATE_SILU 0

@@ -182,13 +182,16 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // The ticket's tile: queue q has the slices q, q + kGatedQueues, ..., tile by tile (one counter for all is at its limit, 10 ns a
-// ticket).  As many workgroups as tiles: a queue that is through hands its workgroups on to the next one.
+// ticket).  There are as many workgroups as tiles, and a queue that is through hands its workgroups on to the next one, so each
+// has found its tile when it has asked every queue once; kGatedNone would mean that another call has the workspace too.
+constexpr uint32_t kGatedNone = ~0u;
 __device__ __forceinline__ uint32_t gated_take(uint32_t* tickets, uint32_t tiles, uint32_t slices) {
-  for (uint32_t q = blockIdx.x % kGatedQueues;; q = (q + 1) % kGatedQueues) {
-    const uint32_t w = (slices + kGatedQueues - 1 - q) / kGatedQueues;
+  for (uint32_t i = 0; i < kGatedQueues; ++i) {
+    const uint32_t q = (blockIdx.x + i) % kGatedQueues, w = (slices + kGatedQueues - 1 - q) / kGatedQueues;
     const uint32_t t = atomicAdd(tickets + q * kGatedQueueStep, 1u);
     if (t < w * tiles) return t / w * slices + t % w * kGatedQueues + q;
   }
+  return kGatedNone;
 }
 
 // OUT: y and the final states; else only the checkpoints (for a backward without the forward's)
@@ -206,6 +209,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
     if (threadIdx.x == 0) turn = gated_take(ch.tickets, tiles, slices);
     lds_barrier();
     id = __builtin_amdgcn_readfirstlane(turn);
+    if (id == kGatedNone) return;
   }
   const uint32_t tile = id / slices;
   const int64_t c0 = static_cast<int64_t>(id % slices) * C, t0 = static_cast<int64_t>(tile) * kGatedTile;
@@ -461,6 +465,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
     if (threadIdx.x == 0) turn = gated_take(ch.tickets, tiles, slices);
     lds_barrier();
     id = __builtin_amdgcn_readfirstlane(turn);
+    if (id == kGatedNone) return;
   }
   const uint32_t n = id / slices, tile = tiles - 1 - n;
   const int64_t c0 = static_cast<int64_t>(id % slices) * C, t0 = static_cast<int64_t>(tile) * kGatedBwdTile;
@@ -779,7 +784,7 @@ int check_gated(int64_t S, int64_t T, int32_t d, float c, int32_t gate, int32_t 
   if (gate != MM_GATE_SILU && gate != MM_GATE_GELU) return MM_ERR_UNSUPPORTED;
   if (!(c >= 0.0f) || std::isinf(c)) return MM_ERR_DIM;
   if (S >= (int64_t{1} << 29)) return MM_ERR_DIM;  // a token's place holds its sequence and two bits
-  if (gated_blocks(T) * cdiv(d, 64) >= (int64_t{1} << 24)) return MM_ERR_DIM;
+  if (gated_blocks(T) * cdiv(d, 64) >= (int64_t{1} << 23)) return MM_ERR_DIM;  // workgroups of 512 threads
   return MM_OK;
 }
 // the chain in the workspace: the ticket, the tiles' pairs, their groups' states

@@ -295,31 +295,34 @@ template <typename IO>
 __global__ __launch_bounds__(64) void k_qk(QkArgs a, IO* q_out, IO* k_out, int64_t qo_ts, int64_t ko_ts) {
   __shared__ float u[MM_QK_MAX_D];
   const int H = a.Hq + a.Hk;
-  const int64_t t = blockIdx.x / H;
-  int h = blockIdx.x % H;
-  const bool key = h >= a.Hq;
-  if (key) h -= a.Hq;
-  const IO* v = static_cast<const IO*>(key ? a.k : a.q) + t * (key ? a.k_ts : a.q_ts) + h * a.D;
-  const float* w = key ? a.wk : a.wq;
-  float s = 0.0f;
-  for (int i = threadIdx.x; i < a.D; i += 64) {
-    u[i] = ld_io(v, i);
-    s = __builtin_fmaf(u[i], u[i], s);
-  }
-  const float r = rsqrtf(wave_sum(s) / a.D + a.eps);
-  __syncthreads();
-  IO* out = (key ? k_out : q_out) + t * (key ? ko_ts : qo_ts) + h * a.D;
-  for (int i = threadIdx.x; i < a.D; i += 64) {
-    float o = u[i] * r * w[i];
-    if (i < a.R) {
-      bool first;
-      const int j = qk_mate(a, i, first);
-      float c, sn;
-      qk_angle(a.pos[t], a.freq[qk_pair(a, i)], c, sn);
-      const float m = u[j] * r * w[j];
-      o = first ? o * c - m * sn : o * c + m * sn;
+  for (int64_t row = blockIdx.x; row < a.T * H; row += gridDim.x) {
+    const int64_t t = row / H;
+    int h = static_cast<int>(row % H);
+    const bool key = h >= a.Hq;
+    if (key) h -= a.Hq;
+    const IO* v = static_cast<const IO*>(key ? a.k : a.q) + t * (key ? a.k_ts : a.q_ts) + static_cast<int64_t>(h) * a.D;
+    const float* w = key ? a.wk : a.wq;
+    float s = 0.0f;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.D; i += 64) {
+      u[i] = ld_io(v, i);
+      s = __builtin_fmaf(u[i], u[i], s);
     }
-    st_io(out, i, o);
+    const float r = rsqrtf(wave_sum(s) / a.D + a.eps);
+    __syncthreads();
+    IO* out = (key ? k_out : q_out) + t * (key ? ko_ts : qo_ts) + static_cast<int64_t>(h) * a.D;
+    for (int i = threadIdx.x; i < a.D; i += 64) {
+      float o = u[i] * r * w[i];
+      if (i < a.R) {
+        bool first;
+        const int j = qk_mate(a, i, first);
+        float c, sn;
+        qk_angle(a.pos[t], a.freq[qk_pair(a, i)], c, sn);
+        const float m = u[j] * r * w[j];
+        o = first ? o * c - m * sn : o * c + m * sn;
+      }
+      st_io(out, i, o);
+    }
   }
 }
 
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(64) void k_qk_bwd(QkArgs a, const IO* dqo, const IO
   for (int64_t row = blockIdx.x; row < a.T * H; row += kQkParts) {
     const int64_t t = row / H;
     const int h = row % H;
-    const IO* v = static_cast<const IO*>(key ? a.k : a.q) + t * (key ? a.k_ts : a.q_ts) + h * a.D;
+    const IO* v = static_cast<const IO*>(key ? a.k : a.q) + t * (key ? a.k_ts : a.q_ts) + static_cast<int64_t>(h) * a.D;
     const IO* go = (key ? dko : dqo) + row * a.D;
     __syncthreads();
     for (int i = threadIdx.x; i < a.D; i += 64) u[i] = ld_io(go, i);
@@ -355,7 +358,7 @@ __global__ __launch_bounds__(64) void k_qk_bwd(QkArgs a, const IO* dqo, const IO
       dot = __builtin_fmaf(g[e] * w[i], x[e], dot);
     }
     const float r = rsqrtf(wave_sum(s) / a.D + a.eps), m = wave_sum(dot) * r / a.D;
-    IO* out = (key ? dk : dq) + t * (key ? dk_ts : dq_ts) + h * a.D;
+    IO* out = (key ? dk : dq) + t * (key ? dk_ts : dq_ts) + static_cast<int64_t>(h) * a.D;
     for (int i = threadIdx.x, e = 0; i < a.D; i += 64, ++e) {
       const float n = x[e] * r;
       dw[e] = __builtin_fmaf(g[e], n, dw[e]);
@@ -433,8 +436,8 @@ int mamba_mixer_qk_norm(const void* q, const void* k, const float* q_weight, con
                            block, static_cast<IO*>(q_out), static_cast<IO*>(k_out), qo_stride, ko_stride);
       });
     } else {
-      hipLaunchKernelGGL((k_qk<IO>), dim3(static_cast<unsigned>(T * (Hq + Hk))), dim3(64), 0, st, a, static_cast<IO*>(q_out),
-                         static_cast<IO*>(k_out), qo_stride, ko_stride);
+      hipLaunchKernelGGL((k_qk<IO>), dim3(static_cast<unsigned>(std::min<int64_t>(T * (Hq + Hk), 1 << 20))), dim3(64), 0, st, a,
+                         static_cast<IO*>(q_out), static_cast<IO*>(k_out), qo_stride, ko_stride);
     }
     return launched();
   });

@@ -157,8 +157,13 @@ def test_sizes_at_the_launches_limits(lib):
     assert conv_backward(lib, far(11), T=2 ** 31 - 1, d=15, xs=15, gx=15, wsb=0) == WORKSPACE
     assert conv_backward(lib, far(11), T=2 ** 31 - 1, d=512, xs=512, gx=512, wsb=0) == DIM
     rows = lambda d: {k: d for k in ("d", "xs", "rs", "gs", "zs", "dxs", "drs", "dgs", "dzs")}  # noqa: E731
-    assert gated_backward(lib, far(16), T=2 ** 30 - 256, wsb=0, **rows(32)) == WORKSPACE
-    assert gated_backward(lib, far(16), T=2 ** 30, wsb=0, **rows(32)) == DIM
+    assert gated_backward(lib, far(16), T=2 ** 29 - 128, wsb=0, **rows(32)) == WORKSPACE
+    assert gated_backward(lib, far(16), T=2 ** 29, wsb=0, **rows(32)) == DIM
+    wide = {k: 2 ** 22 + 1 for k in ("xs", "rs", "gs", "zs", "dxs", "drs", "dgs", "dzs")}
+    for k, v in wide.items():
+        assert gated_backward(lib, far(16), **{k: v}, wsb=0) == UNSUPPORTED, k
+    assert gated(lib, far(10), zs=2 ** 22 + 1) == UNSUPPORTED and gated_decode(lib, far(8), rs=2 ** 22 + 1) == UNSUPPORTED
+    assert gated(lib, far(10), zs=2 ** 22, wsb=0) == WORKSPACE
     assert qk_backward(lib, far(12), T=(2 ** 31 - 1) // 6, wsb=0) == WORKSPACE
 
 
