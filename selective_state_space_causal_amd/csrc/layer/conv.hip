@@ -84,58 +84,85 @@ __device__ __forceinline__ void conv_dstate(const ConvArgs& a, const IO* dy, con
 template <typename IO, int V, int W>
 struct ConvWalk {
   const ConvArgs& a;
-  int64_t c, c0, t0, t1;
-  uint32_t off;      // of this lane's channels in a row
+  int64_t c0, c, t0, t1;
+  uint32_t off;      // of this lane's channels in a row; lanes without channels do the first ones' work again
   int s;             // the sequence of the present token,
   int64_t lo, hi;    // its first token and the one behind its last
   float w[W][V], b[V], win[W - 1][V];
+  Chans<IO, V> before[W - 1];
 
+  // asks for what the walk begins with, begin() waits for it
   __device__ __forceinline__ ConvWalk(const ConvArgs& a, int64_t slice, int64_t walk) : a(a) {
     const int lane = threadIdx.x & 63;
     c0 = slice * 64 * V;
-    c = c0 + lane * V;
-    const bool on = c < a.d;
-    off = on ? lane * V * static_cast<uint32_t>(sizeof(IO)) : 0;  // lanes without channels read the first ones
+    c = c0 + lane * V < a.d ? c0 + lane * V : c0;
+    off = static_cast<uint32_t>(c - c0) * static_cast<uint32_t>(sizeof(IO));
     t0 = walk * a.L;
-    t1 = t0 + a.L < a.T ? t0 + a.L : a.T;
+    t1 = std::min(t0 + a.L, a.T);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) before[j] = row(std::max<int64_t>(t0 - W + 1 + j, 0));
+  }
+  __device__ __forceinline__ void begin() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      b[i] = a.bias != nullptr ? a.bias[c + i] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k][i] = a.w[(c + i) * W + k];
+    }
     s = seq_of(a.cu, a.S, t0);
     lo = a.cu[s];
     hi = a.cu[s + 1];
-    const int64_t cw = on ? c : c0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      b[i] = a.bias != nullptr ? a.bias[cw + i] : 0.0f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) w[k][i] = a.w[(cw + i) * W + k];
-    }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-      const int64_t q = t0 - W + 1 + j;
-      if (q >= lo) set(j, row(q));
-      else from_state(j, static_cast<int>(q - lo + W - 1));
+#pragma unroll
+      for (int i = 0; i < V; ++i) win[j][i] = before[j][i];
     }
+    if (t0 - W + 1 < lo) from_state(t0);
   }
-  __device__ __forceinline__ gmem<const IO>* base(int64_t t) const { return sbase(static_cast<const IO*>(a.x) + t * a.x_ts + c0); }
-  __device__ __forceinline__ Chans<IO, V> row(int64_t t) const { return load_chans<IO, V>(base(t), off); }
-  __device__ __forceinline__ void set(int j, const Chans<IO, V>& r) {
+  // the base in scalar registers, and an offset that the compiler cannot make part of a 64-bit address ahead of its use
+  __device__ __forceinline__ Chans<IO, V> row(int64_t t) {
+    asm volatile("" : "+v"(off));
+    return load_chans<IO, V>(sbase(static_cast<const IO*>(a.x) + t * a.x_ts + c0), off);
+  }
+  __device__ __forceinline__ Chans<IO, V> grads(const IO* dy, int64_t t) {
+    asm volatile("" : "+v"(off));
+    return load_chans<IO, V>(sbase(dy + t * a.d + c0), off);
+  }
+  __device__ __forceinline__ void store(IO* p, int64_t t, int64_t ts, const float (&v)[V]) {
+    asm volatile("" : "+v"(off));
+    store_chans<IO, V>(sbase(p + t * ts + c0), off, v);
+  }
+  // those of the inputs before token t that its sequence has from its state.  The wait stands here, so
+  // that the way around it needs none.
+  __device__ __forceinline__ void from_state(int64_t t) {
+    const int64_t n = lo + W - 1 - t;  // of them (t - lo of the state's have left the window), if not all
+    if (a.state_in != nullptr) {
+      const float* p = a.state_in + (s * static_cast<int64_t>(a.d) + c) * (W - 1) + (t - lo);
 #pragma unroll
-    for (int i = 0; i < V; ++i) win[j][i] = r[i];
-  }
-  __device__ __forceinline__ void from_state(int j, int k) {
-    const int64_t cs = c < a.d ? c : c0;
+      for (int j = 0; j < W - 1; ++j)
+        if (j < n) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) win[j][i] = a.state_in != nullptr ? a.state_in[(s * static_cast<int64_t>(a.d) + cs + i) * (W - 1) + k] : 0.0f;
+          for (int i = 0; i < V; ++i) win[j][i] = p[i * (W - 1) + j];
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) win[j][i] = j < n ? 0.0f : win[j][i];
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) asm volatile("" : "+v"(win[j][i]));
   }
-  // token t, which may be the first of another sequence
+  // token t >= hi is the first of another sequence
   __device__ __forceinline__ void enter(int64_t t) {
-    if (t < hi) return;
     while (t >= hi) {
       ++s;
       lo = hi;
       hi = a.cu[s + 1];
     }
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) from_state(j, j);
+    from_state(t);
   }
   __device__ __forceinline__ void pre(const Chans<IO, V>& r, float (&u)[V]) const {
 #pragma unroll
@@ -148,12 +175,36 @@ struct ConvWalk {
   }
   __device__ __forceinline__ void shift(const Chans<IO, V>& r) {
 #pragma unroll
-    for (int j = 0; j < W - 2; ++j)
+    for (int i = 0; i < V; ++i) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
-    set(W - 2, r);
+      for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
+      win[W - 2][i] = r[i];
+    }
   }
 };
+// The walk's steps of kStep tokens: load(rows, t) asks for a step's rows, use(t + k, rows, k) is called for each token in turn.
+// Two sets of rows take turns: while one is used the other is on its way.  The first step stands before the loop, so that each
+// pass begins with the same accesses under way (a step's loads, then its stores) and waits for the loads alone.
+template <typename Rows, typename Load, typename Use>
+__device__ __forceinline__ int64_t conv_steps(int64_t t, int64_t t1, Rows& r0, Load load, Use use) {
+  const int64_t te = t + (t1 - t) / kStep * kStep;
+  const auto step = [&](const Rows& now, Rows& next) {
+    load(next, t + kStep < te ? t + kStep : t);  // the last step asks for its own rows again, which nothing uses
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) use(t + k, now, k);
+    t += kStep;
+  };
+  Rows r1;
+  if (t < te) {
+    step(r0, r1);
+    while (t < te) {
+      step(r1, r0);
+      if (t < te) step(r0, r1);
+      else break;
+    }
+  }
+  return t;
+}
 
 // blocks of `walks` (kConvWaves to a block, slice by slice), then those of the states where state_out is given
 template <typename IO, int V, int W>
@@ -164,48 +215,29 @@ __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, int64_t block
   }
   const int64_t walk = static_cast<int64_t>(blockIdx.x / slices) * kConvWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   if (walk * a.L >= a.T) return;
+  struct Rows {
+    Chans<IO, V> x[kStep];
+  };
   ConvWalk<IO, V, W> x(a, blockIdx.x % slices, walk);
-  const bool on = x.c < a.d;
+  const auto load = [&](Rows& r, int64_t t) {
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) r.x[k] = x.row(t + k);
+  };
   const auto out = [&](int64_t t, const Chans<IO, V>& r) {
+    if (t >= x.hi) x.enter(t);
     float u[V];
     x.pre(r, u);
-    if (a.silu) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) u[i] *= sigmoid(u[i]);
-    }
-    if (on) store_chans<IO, V>(sbase(y + t * a.d + x.c0), x.off, u);
+    for (int i = 0; i < V; ++i) u[i] *= a.silu ? sigmoid(u[i]) : 1.0f;
+    x.store(y, t, a.d, u);
     x.shift(r);
   };
-  Chans<IO, V> r[kStep];
-  const auto load = [&](int64_t t) {
-#pragma unroll
-    for (int k = 0; k < kStep; ++k) r[k] = x.row(t + k);
-  };
-  int64_t t = x.t0;
-  if (t + kStep <= x.t1) load(t);
-  for (; t + kStep <= x.t1; t += kStep) {
-    if (t + kStep <= x.hi) {
-      Chans<IO, V> now[kStep];
-#pragma unroll
-      for (int k = 0; k < kStep; ++k) now[k] = r[k];
-      // the last step reads its own rows again, which nothing uses
-      load(t + 2 * kStep <= x.t1 ? t + kStep : t);
-#pragma unroll
-      for (int k = 0; k < kStep; ++k) out(t + k, now[k]);
-    } else {
+  Rows r0;
+  if (x.t0 + kStep <= x.t1) load(r0, x.t0);
+  x.begin();
+  int64_t t = conv_steps(x.t0, x.t1, r0, load, [&](int64_t t, const Rows& r, int k) { out(t, r.x[k]); });
 #pragma unroll 1
-      for (int k = 0; k < kStep; ++k) {
-        x.enter(t + k);
-        out(t + k, x.row(t + k));
-      }
-      load(t + 2 * kStep <= x.t1 ? t + kStep : t);
-    }
-  }
-#pragma unroll 1
-  for (; t < x.t1; ++t) {
-    x.enter(t);
-    out(t, x.row(t));
-  }
+  for (; t < x.t1; ++t) out(t, x.row(t));
 }
 
 // One token a row, a thread for V channels of it.
@@ -238,7 +270,7 @@ __global__ __launch_bounds__(256) void k_conv_decode(ConvArgs a, float* state_ou
   store_chans<IO, V>(global(y + i0), 0, u);
 }
 
-// A walk computes du for its own tokens and the W - 1 behind them; pend holds the gradients of the last W tokens as they gather.
+// A walk computes du for its own tokens and up to W - 1 behind them; pend holds the gradients of the last W tokens as they gather.
 // part: [blocks / slices][W + 1][d], a block's sums of dw and dbias.
 template <typename IO, int V, int W>
 __global__ __launch_bounds__(kConvThreads) void k_conv_bwd(ConvArgs a, int64_t blocks, uint32_t slices, const IO* __restrict__ dy,
@@ -259,24 +291,83 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_bwd(ConvArgs a, int64_t b
     for (int k = 0; k < W; ++k) dw[k][i] = 0.0f;
   }
   if (walk * a.L < a.T) {
+    struct Rows {
+      Chans<IO, V> x[kStep], g[kStep];
+    };
     ConvWalk<IO, V, W> x(a, slice, walk);
-    const bool on = x.c < a.d;
-    float pend[W][V];  // tokens p - W + 1 .. p
+    const auto load = [&](Rows& r, int64_t t) {
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        r.x[k] = x.row(t + k);
+        r.g[k] = x.grads(dy, t + k);
+      }
+    };
+    Rows r0;
+    if (x.t0 + kStep <= x.t1) load(r0, x.t0);
+    x.begin();
+    float pend[W][V];  // of tokens p - W + 1 .. p
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) pend[j][i] = 0.0f;
-    const auto slope = [&](const Chans<IO, V>& r, const Chans<IO, V>& g, float(&du)[V]) {
+    int64_t first = std::max(x.t0, x.lo);  // of the tokens whose gradients this walk gathers now
+    // the first token that asks for more than its taps: of the final state or of another sequence
+    const auto more = [&] { return dstate_out != nullptr ? x.hi - W + 1 : x.hi; };
+    int64_t event = more();
+    // no token from p on adds to those before it
+    const auto flush = [&](int64_t p) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) du[i] = g[i];
-      if (a.silu) {
-        float u[V];
-        x.pre(r, u);
-#pragma unroll
-        for (int i = 0; i < V; ++i) du[i] = conv_slope(u[i], du[i], true);
+      for (int j = 0; j < W - 1; ++j) {
+        const int64_t q = p - W + 1 + j;
+        if (q >= first && q < x.t1) x.store(dx, q, dx_ts, pend[j]);
       }
     };
-    const auto weights = [&](const Chans<IO, V>& r, const float(&du)[V]) {
+    // du of token p, and what it adds to tokens p - W + 1 .. p
+    const auto taps = [&](const Chans<IO, V>& r, const Chans<IO, V>& g, float(&du)[V]) {
+      float u[V];
+      x.pre(r, u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float v = conv_slope(u[i], g[i], true);
+        du[i] = a.silu ? v : g[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) pend[j][i] = __builtin_fmaf(x.w[j][i], du[i], pend[j][i]);
+      }
+    };
+    // behind token p: token q is through.  What stands before `first` goes to its row, which gets its own value after it.
+    const auto leave = [&](int64_t p, const Chans<IO, V>& r) {
+      x.shift(r);
+      x.store(dx, std::max(p - W + 1, first), dx_ts, pend[0]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) pend[j][i] = pend[j + 1][i];
+        pend[W - 1][i] = 0.0f;
+      }
+    };
+    const auto back = [&](int64_t p, const Chans<IO, V>& r, const Chans<IO, V>& g) {
+      if (p >= event) {
+        if (p >= x.hi) {
+          flush(p);
+          x.enter(p);
+          first = p;
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) pend[j][i] = 0.0f;
+          event = more();
+        }
+        if (p >= event) {
+          const int64_t f = p - event;  // its place in the final state
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            pend[W - 1][i] = dstate_out[(x.s * static_cast<int64_t>(a.d) + x.c + i) * (W - 1) + f];
+#pragma unroll
+          for (int i = 0; i < V; ++i) asm volatile("" : "+v"(pend[W - 1][i]));  // waited for here
+        }
+      }
+      float du[V];
+      taps(r, g, du);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         db[i] += du[i];
@@ -284,83 +375,19 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_bwd(ConvArgs a, int64_t b
         for (int k = 0; k < W - 1; ++k) dw[k][i] = __builtin_fmaf(du[i], x.win[k][i], dw[k][i]);
         dw[W - 1][i] = __builtin_fmaf(du[i], r[i], dw[W - 1][i]);
       }
+      leave(p, r);
     };
-    // token q = p - W + 1 is through
-    const auto leave = [&](int64_t p) {
-      const int64_t q = p - W + 1;
-      if (q >= x.t0 && on) store_chans<IO, V>(sbase(dx + q * dx_ts + x.c0), x.off, pend[0]);
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) pend[j][i] = pend[j + 1][i];
-#pragma unroll
-      for (int i = 0; i < V; ++i) pend[W - 1][i] = 0.0f;
-    };
-    const auto grads = [&](int64_t t) { return load_chans<IO, V>(sbase(dy + t * a.d + x.c0), x.off); };
-    // token p, wherever sequences start and end; behind the last token the others leave
-    const auto slow = [&](int64_t p) {
-      if (p < a.T) {
-        x.enter(p);
-        const Chans<IO, V> r = x.row(p);
-        float du[V];
-        slope(r, grads(p), du);
-        if (p < x.t1) weights(r, du);
-        const int64_t f = p - (x.hi - W + 1);  // its place in the final state
-        if (dstate_out != nullptr && f >= 0) {
-          const int64_t cs = on ? x.c : x.c0;
-#pragma unroll
-          for (int i = 0; i < V; ++i) pend[W - 1][i] += dstate_out[(x.s * static_cast<int64_t>(a.d) + cs + i) * (W - 1) + f];
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-          if (p - j >= x.lo) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) pend[W - 1 - j][i] = __builtin_fmaf(x.w[W - 1 - j][i], du[i], pend[W - 1 - j][i]);
-          }
-        x.shift(r);
-      }
-      leave(p);
-    };
-    Chans<IO, V> r[kStep], g[kStep];
-    const auto load = [&](int64_t t) {
-#pragma unroll
-      for (int k = 0; k < kStep; ++k) {
-        r[k] = x.row(t + k);
-        g[k] = grads(t + k);
-      }
-    };
-    int64_t t = x.t0;
-    if (t + kStep <= x.t1) load(t);
-    for (; t + kStep <= x.t1; t += kStep) {
-      const int64_t next = t + 2 * kStep <= x.t1 ? t + kStep : t;
-      if (t - W + 1 >= x.lo && t + kStep + W - 1 <= x.hi) {
-        Chans<IO, V> now[kStep], gn[kStep];
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          now[k] = r[k];
-          gn[k] = g[k];
-        }
-        load(next);
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          float du[V];
-          slope(now[k], gn[k], du);
-          weights(now[k], du);
-#pragma unroll
-          for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) pend[j][i] = __builtin_fmaf(x.w[j][i], du[i], pend[j][i]);
-          x.shift(now[k]);
-          leave(t + k);
-        }
-      } else {
+    int64_t t = conv_steps(x.t0, x.t1, r0, load, [&](int64_t p, const Rows& r, int k) { back(p, r.x[k], r.g[k]); });
 #pragma unroll 1
-        for (int k = 0; k < kStep; ++k) slow(t + k);
-        load(next);
-      }
+    for (; t < x.t1; ++t) back(t, x.row(t), x.grads(dy, t));
+#pragma unroll 1
+    for (; t < x.t1 + W - 1 && t < x.hi; ++t) {
+      const Chans<IO, V> r = x.row(t);
+      float du[V];
+      taps(r, x.grads(dy, t), du);
+      leave(t, r);
     }
-#pragma unroll 1
-    for (; t < x.t1 + W - 1; ++t) slow(t);
+    flush(t);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
