@@ -3,8 +3,7 @@
 //   dX(q) = sum_k w_k du(q + W - 1 - k) + what the final state asks for,  dw_k = sum_p du(p) X(p - W + 1 + k)
 // Bound by memory.  A wave walks L tokens of 64 V channels (512 bytes of bfloat16 a row: narrower rows cost a fifth of the
 // bandwidth), its window, weights and the weights' gradients in registers: an input is read once, but for the W - 1 tokens
-// around a walk.  kStep tokens are loaded at a time, the next ones while these are used; a step in which sequences start or
-// end goes token by token and reads its rows again.
+// around a walk.  kStep tokens are loaded at a time, the next ones while these are used.
 #include <algorithm>
 #include <type_traits>
 
@@ -14,8 +13,10 @@ namespace mm {
 namespace {
 
 constexpr int kConvWaves = 4, kConvThreads = kConvWaves * 64, kStep = 4;
-// A walk has at most 64 tokens (backward 128), fewer where there would be fewer walks than these.
-constexpr int64_t kConvWalks = 4096, kConvBackWalks = 2048;
+// A walk has at most kConvTokens tokens, fewer where there would be fewer than kConvWalks of them (one for each SIMD).  More and
+// shorter walks read more rows twice: 8192 x 2048 f32 4096 walks 28.9 us, 2048 27.4, 1024 25.9; backward 46.7 with 2048, 44.1
+// with 1024.  Longer ones leave fewer: backward 8 x 2048 x 1792 bf16 with 128 tokens 63 us, with 64 47.5.
+constexpr int64_t kConvTokens = 64, kConvWalks = 1024;
 
 struct ConvArgs {
   const void* x;
@@ -41,7 +42,7 @@ __device__ __forceinline__ float conv_slope(float u, float g, bool silu) {
 template <typename IO, int W>
 __device__ __forceinline__ void conv_state(const ConvArgs& a, float* state_out, int64_t i) {
   if (i >= static_cast<int64_t>(a.S) * a.d) return;
-  const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
+  const int s = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.d)), c = static_cast<int>(i - static_cast<int64_t>(s) * a.d);  // S d < 2^31
   const int64_t g0 = a.cu[s], n = a.cu[s + 1] - g0;
   float v[W - 1];
 #pragma unroll
@@ -53,7 +54,7 @@ __device__ __forceinline__ void conv_state(const ConvArgs& a, float* state_out, 
 template <typename IO, int W>
 __device__ __forceinline__ void conv_dstate(const ConvArgs& a, const IO* dy, const float* dstate_out, float* dstate_in, int64_t i) {
   if (i >= static_cast<int64_t>(a.S) * a.d) return;
-  const int s = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
+  const int s = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.d)), c = static_cast<int>(i - static_cast<int64_t>(s) * a.d);  // S d < 2^31
   const int64_t g0 = a.cu[s], n = a.cu[s + 1] - g0;
   const float b = a.bias != nullptr ? a.bias[c] : 0.0f;
   float w[W], du[W - 1];
@@ -421,11 +422,10 @@ __global__ __launch_bounds__(256) void k_conv_parts(const float* __restrict__ pa
 int conv_channels(int32_t d) { return d % 4 == 0 ? 4 : d % 2 == 0 ? 2 : 1; }  // of a lane: all there or none
 int64_t conv_slices(int32_t d) { return cdiv(d, 64 * conv_channels(d)); }
 // tokens of a walk, in steps of kStep
-int64_t conv_tokens(int64_t T, int32_t d, bool back) {
-  const int64_t L = T * conv_slices(d) / (back ? kConvBackWalks : kConvWalks) / kStep * kStep;
-  return std::min<int64_t>(back ? 128 : 64, std::max<int64_t>(kStep, L));
+int64_t conv_tokens(int64_t T, int32_t d) {
+  return std::min(kConvTokens, std::max<int64_t>(kStep, T * conv_slices(d) / kConvWalks / kStep * kStep));
 }
-int64_t conv_groups(int64_t T, int32_t d, bool back) { return cdiv(T, conv_tokens(T, d, back) * kConvWaves); }
+int64_t conv_groups(int64_t T, int32_t d) { return cdiv(T, conv_tokens(T, d) * kConvWaves); }
 
 int check_conv(int64_t S, int64_t T, int32_t d, int32_t W, int32_t io, int64_t x_ts) {
   const int rc = check_tokens(S, T, d, io);
@@ -433,7 +433,7 @@ int check_conv(int64_t S, int64_t T, int32_t d, int32_t W, int32_t io, int64_t x
   if (W < 2 || W > MM_CONV_MAX_W) return MM_ERR_UNSUPPORTED;
   if (x_ts < d) return MM_ERR_DIM;
   if (d == 0) return MM_OK;
-  const int64_t blocks = std::max(conv_groups(T, d, false), conv_groups(T, d, true)) * conv_slices(d) + cdiv(S * d, kConvThreads);
+  const int64_t blocks = conv_groups(T, d) * conv_slices(d) + cdiv(S * d, kConvThreads);
   return blocks * kConvThreads > kMaxThreads || cdiv(int64_t{W + 1} * d, kPartColumns) * 256 > kMaxThreads ? MM_ERR_DIM : MM_OK;
 }
 // f(IO, channels of a lane, taps)
@@ -472,13 +472,13 @@ int mamba_mixer_conv_prefill(const void* x, const float* weight, const float* bi
                   {flat(state_out, ns, 4), flat(y, T * d, es)}, {{0, 4}});
   if (rc != MM_OK) return rc;
   if (S == 0) return MM_OK;
-  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d, false)), silu != 0};
+  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d)), silu != 0};
   hipStream_t st = static_cast<hipStream_t>(stream);
   return by_conv(io_dtype, d, W, [&](auto io, auto v, auto taps) {
     using IO = decltype(io);
     constexpr int V = decltype(v)::value, K = decltype(taps)::value;
     const uint32_t slices = static_cast<uint32_t>(conv_slices(d));
-    const int64_t blocks = T > 0 ? conv_groups(T, d, false) * slices : 0, states = cdiv(static_cast<int64_t>(S) * d, kConvThreads);
+    const int64_t blocks = T > 0 ? conv_groups(T, d) * slices : 0, states = cdiv(static_cast<int64_t>(S) * d, kConvThreads);
     const auto launch = [&](int64_t walks, int64_t rest) {
       hipLaunchKernelGGL((k_conv<IO, V, K>), dim3(static_cast<unsigned>(walks + rest)), dim3(kConvThreads), 0, st, a, walks, slices,
                          static_cast<IO*>(y), state_out);
@@ -517,7 +517,7 @@ int mamba_mixer_conv_decode(const void* x, const float* weight, const float* bia
 
 size_t mamba_mixer_conv_backward_workspace_bytes(int64_t T, int32_t d, int32_t W) {
   if (check_conv(1, T, d, W, MM_IO_F32, d) != MM_OK || d == 0) return 0;
-  return align256(static_cast<size_t>(conv_groups(T, d, true)) * d * (W + 1) * 4);
+  return align256(static_cast<size_t>(conv_groups(T, d)) * d * (W + 1) * 4);
 }
 
 int mamba_mixer_conv_backward(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
@@ -539,14 +539,14 @@ int mamba_mixer_conv_backward(const void* x, const float* weight, const float* b
   if (rc != MM_OK) return rc;
   rc = check_workspace(workspace, workspace_bytes, mamba_mixer_conv_backward_workspace_bytes(T, d, W));
   if (rc != MM_OK) return rc;
-  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d, true)), silu != 0};
+  const ConvArgs a{x, weight, bias, cu_seqlens, state_in, x_stride, T, S, d, static_cast<int>(conv_tokens(T, d)), silu != 0};
   hipStream_t st = static_cast<hipStream_t>(stream);
   float* part = static_cast<float*>(workspace);
   return by_conv(io_dtype, d, W, [&](auto io, auto v, auto taps) {
     using IO = decltype(io);
     constexpr int V = decltype(v)::value, K = decltype(taps)::value;
     const uint32_t slices = static_cast<uint32_t>(conv_slices(d));
-    const int64_t groups = T > 0 ? conv_groups(T, d, true) : 0, blocks = groups * slices;
+    const int64_t groups = T > 0 ? conv_groups(T, d) : 0, blocks = groups * slices;
     const int64_t states = dstate_in != nullptr ? cdiv(static_cast<int64_t>(S) * d, kConvThreads) : 0;
     if (blocks + states > 0)
       hipLaunchKernelGGL((k_conv_bwd<IO, V, K>), dim3(static_cast<unsigned>(blocks + states)), dim3(kConvThreads), 0, st, a, blocks,
