@@ -423,8 +423,8 @@ __global__ __launch_bounds__(256) void k_gated_decode(GatedArgs a, float* state_
 // m tends to 0 with L, and L / m with it.
 // One pass from the last tile to the first, in the forward's manner: R = a G is what a token hands to the one before it, so a
 // run is a pair (A, R) and the tiles are a chain.  The states before each token come from the checkpoint before the tile.
-// What a thread keeps of a token from the first look to the gradients are a and h', and the inputs as they were loaded: the
-// rest is computed twice, which costs less than the registers.
+// What a thread keeps of a token from the first look to the gradients are a, h' and dy act'(z) in registers, dy act(z) in shared
+// memory, and the other inputs as they were loaded: the rest is computed twice, which costs less than the registers.
 struct GatedGrads {
   const void* dy;
   const float *dstate_out, *ckpt;
@@ -455,6 +455,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
   typedef GatedShape<IO, V, kGatedBwdTile> Shape;
   constexpr int K = Shape::K, C = Shape::C, NG = Shape::runs;
   __shared__ float sA[NG][C], sH[NG][C], sR[NG][C];
+  __shared__ __align__(16) float sD[K][kGatedThreads][V];  // each thread's own
   __shared__ Place place[kGatedBwdTile];
   __shared__ int cuts[NG];  // of a run: 1 a sequence starts in it, 2 one ends
   __shared__ uint32_t turn;
@@ -519,7 +520,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
   }
 
   // a, b and the runs; b makes room for the state before the token afterwards
-  float da[K][V], db[K][V], A[V], h[V], R[V];
+  float da[K][V], db[K][V], dz[K][V], A[V], h[V], R[V];
   int marks = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -567,18 +568,24 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
       float dh[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) dh[i] = ry[k][i];
       if (a.z != nullptr) {
-        if (a.gelu) {
+        const auto gate = [&](bool gelu) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) dh[i] *= gated_act(true, rz[k][i]);
-        } else {
+          for (int i = 0; i < V; ++i) {
+            const Act v = gated_act_slope(gelu, rz[k][i]);
+            dz[k][i] = v.slope * ry[k][i];
+            dh[i] = ry[k][i] * v.act;
+          }
+        };
+        if (a.gelu) gate(true);
+        else gate(false);
+      } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) dh[i] *= gated_act(false, rz[k][i]);
-        }
+        for (int i = 0; i < V; ++i) dh[i] = ry[k][i];
       }
       final_adjoint(k, dh);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sD[k][threadIdx.x][i] = dh[i];
       if (cut && place[run * K + k].ends()) {
         marks |= 2;
 #pragma unroll
@@ -645,16 +652,13 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
     R[i] = sR[run][lane * V + i];
     sum[i] = 0.0f;
   }
-  float dh[K][V];  // in the place of dy and z
   if (on) {
     uint32_t step, off = offset(o.dz_ts, step);
     gmem<IO>* base = sbase(static_cast<IO*>(o.dz) + t0 * o.dz_ts + c0);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       again(rr[k]);
-      again(rz[k]);
       again(rg[k]);
-      again(ry[k]);
       if (cut) {
         const Place p = place[run * K + k];
         if (p.starts()) {
@@ -668,24 +672,12 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
         h[i] = __builtin_fmaf(da[k][i], h[i], db[k][i]);
         db[k][i] = before;
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) dh[k][i] = ry[k][i];
       if (a.z != nullptr) {
-        float dz[V];
-        const auto gate = [&](bool gelu) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const Act v = gated_act_slope(gelu, rz[k][i]);
-            dz[i] = v.slope * ry[k][i] * h[i];
-            dh[k][i] *= v.act;
-          }
-        };
-        if (a.gelu) gate(true);
-        else gate(false);
-        if (whole || k < left) store_chans<IO, V>(base, off, dz);
+        for (int i = 0; i < V; ++i) dz[k][i] *= h[i];
+        if (whole || k < left) store_chans<IO, V>(base, off, dz[k]);
         off += step;
       }
-      final_adjoint(k, dh[k]);
       __builtin_amdgcn_sched_barrier(0);
     }
     uint32_t sx, sr, sg;
@@ -707,7 +699,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
       float G[V], u[V], dr[V], dx[V], dg[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        G[i] = dh[k][i] + R[i];
+        G[i] = sD[k][threadIdx.x][i] + R[i];
         R[i] = da[k][i] * G[i];
         u[i] = rx[k][i];
         dx[i] = G[i];
