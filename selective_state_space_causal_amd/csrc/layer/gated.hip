@@ -319,6 +319,16 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
       ht = Ag < 0.0f ? hg : __builtin_fmaf(Ag, ht, hg);
       At = Ag < 0.0f || At < 0.0f ? -1.0f : At * Ag;
     }
+    static_assert(kGatedTile == 2 * MM_GATED_BLOCK, "a checkpoint before the tile and one in its middle");
+    float* const cp = ckpt + static_cast<int64_t>(2) * tile * d + cc;
+    const bool halfway = t0 + MM_GATED_BLOCK < a.T, restarts = cut && halfway && place[MM_GATED_BLOCK].starts();
+    if (ckpt != nullptr && a.T > 0) {
+      // Sequences that start at a checkpoint.  Their initial states are read before the pair is out: where state_out is
+      // state_in, the tile in which such a sequence ends may then write over them.
+      if (!waits) cp[0] = a.state_in != nullptr ? a.state_in[seq * d + cc] : 0.0f;
+      if (restarts) cp[d] = a.state_in != nullptr ? a.state_in[place[MM_GATED_BLOCK].seq() * d + cc] : 0.0f;
+      asm volatile("" : : : "memory");
+    }
     if (tile + 1 < tiles) gated_publish(ch.pairs + tile * d + cc, gated_pair(At, ht));
     if (waits) {
       for (int look = 0; !there && look < kGatedLooks; ++look) {
@@ -326,20 +336,12 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
         there = gated_look(in, ch, d, c0, threadIdx.x);
       }
       from = gated_state(in);
-    } else if (a.T > 0 && a.state_in != nullptr) {
-      from = a.state_in[seq * d + cc];
     }
     if (tile + 1 < tiles && tile % kGatedGroup == kGatedGroup - 1)
       gated_publish(ch.states + tile / kGatedGroup * d + cc, __float_as_uint(At < 0.0f ? ht : __builtin_fmaf(At, from, ht)));
-    if (ckpt != nullptr && a.T > 0) {
-      static_assert(kGatedTile == 2 * MM_GATED_BLOCK, "a checkpoint before the tile and one in its middle");
-      ckpt[static_cast<int64_t>(2) * tile * d + cc] = from;
-      if (t0 + MM_GATED_BLOCK < a.T) {
-        float middle = Am < 0.0f ? hm : __builtin_fmaf(Am, from, hm);
-        const Place p = place[MM_GATED_BLOCK];
-        if (cut && p.starts()) middle = a.state_in != nullptr ? a.state_in[p.seq() * d + cc] : 0.0f;
-        ckpt[(static_cast<int64_t>(2) * tile + 1) * d + cc] = middle;
-      }
+    if (ckpt != nullptr) {
+      if (waits) cp[0] = from;
+      if (halfway && !restarts) cp[d] = Am < 0.0f ? hm : __builtin_fmaf(Am, from, hm);
     }
     sC[j] = from;
   }

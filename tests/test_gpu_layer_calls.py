@@ -172,3 +172,20 @@ def test_long_sequences_repeat_bit_for_bit():
         for _ in range(3):
             for a, t in zip(call(), first):
                 assert torch.equal(a, t)
+
+
+def test_checkpoints_of_states_in_place():
+    """Sequences that start at a checkpoint, in the middle of a tile or at its start, and end many tiles later or in the next one:
+    the checkpoints hold their initial states, which the same call writes over."""
+    lens = [64, 128, 64, 2000, 48, 128, 0, 64, 192, 5000, 120, 65, 63, 128]
+    c = cuda(ref.gated_inputs(11, lens, 520, "bf16"))
+    ins = [c[k] for k in ("x", "r", "g", "z", "lam", "cu")]
+    y, last, ckpt = mm.gated_prefill_train(*ins, c["state"])
+    starts = c["cu"][:-1].long().tolist()
+    for s, t in enumerate(starts):
+        if t % mm.layer.GATED_BLOCK == 0 and lens[s] > 0:
+            assert torch.equal(ckpt[t // mm.layer.GATED_BLOCK], c["state"][s])
+    for _ in range(5):
+        st = c["state"].clone()
+        got = mm.gated_prefill_train(*ins, st, st)
+        assert torch.equal(got[0], y) and torch.equal(st, last) and torch.equal(got[2], ckpt)
