@@ -431,9 +431,18 @@ int mamba_mixer_qk_norm(const void* q, const void* k, const float* q_weight, con
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (qk_by_groups(D, R)) {
       const int block = qk_block(T);
+      const int64_t most = (kMaxThreads / kQkThreads) * block;  // tokens of a launch
       by_group(D, interleaved != 0, [&](auto n, auto inter) {
-        hipLaunchKernelGGL((k_qk_rows<IO, decltype(n)::value, decltype(inter)::value>), dim3(static_cast<unsigned>(cdiv(T, block))), dim3(kQkThreads), 0, st, a,
-                           block, static_cast<IO*>(q_out), static_cast<IO*>(k_out), qo_stride, ko_stride);
+        for (int64_t t0 = 0; t0 < T; t0 += most) {
+          QkArgs b = a;
+          b.q = static_cast<const IO*>(q) + t0 * q_stride;
+          b.k = static_cast<const IO*>(k) + t0 * k_stride;
+          b.pos = R > 0 ? positions + t0 : nullptr;
+          b.T = std::min(most, T - t0);
+          hipLaunchKernelGGL((k_qk_rows<IO, decltype(n)::value, decltype(inter)::value>), dim3(static_cast<unsigned>(cdiv(b.T, block))),
+                             dim3(kQkThreads), 0, st, b, block, static_cast<IO*>(q_out) + t0 * qo_stride,
+                             static_cast<IO*>(k_out) + t0 * ko_stride, qo_stride, ko_stride);
+        }
       });
     } else {
       hipLaunchKernelGGL((k_qk<IO>), dim3(static_cast<unsigned>(std::min<int64_t>(T * (Hq + Hk), 1 << 20))), dim3(64), 0, st, a,

@@ -189,3 +189,17 @@ def test_checkpoints_of_states_in_place():
         st = c["state"].clone()
         got = mm.gated_prefill_train(*ins, st, st)
         assert torch.equal(got[0], y) and torch.equal(st, last) and torch.equal(got[2], ckpt)
+
+
+def test_more_tokens_than_a_launch_has_threads_for():
+    """2^28 + 600 tokens of one head of eight columns, in place: 256 threads to 16 tokens, and at most 2^32 - 1 threads to a launch."""
+    T, n = 2 ** 28 + 600, 1000
+    g = torch.Generator().manual_seed(5)
+    rows = torch.randn(2, n, 1, 8, generator=g, dtype=torch.float32).bfloat16().cuda()
+    wq, wk = (torch.rand(8, generator=g).add(0.5).cuda() for _ in range(2))
+    q, k = (torch.zeros(T, 1, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    want = mm.qk_norm(rows[0], rows[1], wq, wk)
+    for t0 in (0, T // 2, 2 ** 28 - n, 2 ** 28 - 16 - n // 2, T - n):
+        q[t0:t0 + n], k[t0:t0 + n] = rows[0], rows[1]
+        mm.qk_norm(q, k, wq, wk, q_out=q, k_out=k)
+        assert torch.equal(q[t0:t0 + n], want[0]) and torch.equal(k[t0:t0 + n], want[1])
