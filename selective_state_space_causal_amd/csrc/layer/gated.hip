@@ -56,15 +56,15 @@ __device__ __forceinline__ float gated_act(bool gelu, float z) {
 // store, so each array is read and written once.  Runs compose as pairs (A, h): h_out = A h_in + h; the first threads put
 // a tile's runs together, one for each channel, and the tiles of a channel are a chain in memory:
 //   - a tile publishes its own pair as soon as it has it;
-//   - every kGatedGroup-th tile also publishes its final state;
+//   - the last of each group of tiles also publishes its final state;
 //   - a tile's initial state is that of the last whole group of tiles before it, taken through the pairs of the tiles since.
 // The order of these products does not depend on timing: results repeat bit for bit.  The links that wait for one another are
-// one in kGatedGroup tiles.  Tiles are numbered by tickets, not by the workgroup's index, so a tile waits only for tiles
+// one in a group.  Tiles are numbered by tickets, not by the workgroup's index, so a tile waits only for tiles
 // whose workgroups run already or are done, and every wait ends.
 // Where a sequence starts, A is set to -1: what comes before has no part in what follows, whatever it is (0 times an infinity
 // would have).
-constexpr int kGatedTile = 2 * MM_GATED_BLOCK, kGatedThreads = 512, kGatedGroup = 6;
-constexpr uint32_t kGatedQueues = 4, kGatedQueueStep = 64;  // tickets: counters, and elements between them
+constexpr int kGatedTile = 2 * MM_GATED_BLOCK, kGatedThreads = 512;
+constexpr uint32_t kGatedQueues = 2, kGatedQueueStep = 64;  // tickets: counters, and elements between them
 template <typename IO, int V, int TILE>
 struct GatedShape {
   static constexpr int C = V == 1 ? 64 : 256 / sizeof(IO);  // channels of a tile
@@ -78,61 +78,83 @@ typedef unsigned long long u64;
 constexpr u64 kUnset = ~0ull;  // no pair: a NaN is published as 0x7FC00000 in its place
 
 struct GatedChain {
-  u64* pairs;        // [tiles, d]: A in the upper half, h in the lower
-  u64* states;       // [tiles / kGatedGroup, d]: h
+  u64* pairs;         // [tiles, d]: A in the upper half, h in the lower
+  u64* states;        // [tiles >> group, d]: h
   uint32_t* tickets;  // a counter for each queue, apart
+  int group;          // log2 of a group's tiles
 };
 __device__ __forceinline__ u64 gated_pair(float A, float h) {
   return static_cast<u64>(A != A ? 0x7FC00000u : __float_as_uint(A)) << 32 | __float_as_uint(h);
 }
 // Written through to where all XCDs see it; the value itself says that it is there, so nothing else has to be ordered.
 __device__ __forceinline__ void gated_publish(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ __forceinline__ u64 gated_read(gmem<const u64>* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 // What comes into tile `n` (in the chain's order) of a run that goes back to tile `first`: the last whole group's state, and
-// the pairs of the tiles since.
+// the pairs of the tiles since, kGatedLook of them at a time.
+constexpr int kGatedLook = 4;
 struct Incoming {
-  u64 state, pairs[kGatedGroup - 1];
-  int64_t from;
+  u64 state, pairs[kGatedLook];
+  int64_t from;  // the first of the tiles since
   int count;
-  bool older;
+  bool older;    // a state comes in
 };
-__device__ __forceinline__ Incoming gated_from(int64_t n, int64_t first) {
-  const int64_t group = n / kGatedGroup * kGatedGroup;
+__device__ __forceinline__ Incoming gated_from(const GatedChain& ch, int64_t n, int64_t first) {
+  const int64_t group = n >> ch.group << ch.group;
   Incoming in;
   in.older = first < group;
   in.from = in.older ? group : first;
   in.count = static_cast<int>(n - in.from);
   in.state = in.older ? kUnset : 0;
 #pragma unroll
-  for (int i = 0; i < kGatedGroup - 1; ++i) in.pairs[i] = kUnset;
+  for (int i = 0; i < kGatedLook; ++i) in.pairs[i] = kUnset;
   return in;
 }
-// One look at channel c0 + c of d; whether all of it is there.
-__device__ __forceinline__ bool gated_look(Incoming& in, const GatedChain& ch, int64_t d, int64_t c0, uint32_t c) {
-  // scalar bases: the looks run where every thread's tile is in registers
-  if (in.older) in.state = gated_read(sbase(static_cast<const u64*>(ch.states) + (in.from / kGatedGroup - 1) * d + c0) + c);
-#pragma unroll
-  for (int i = 0; i < kGatedGroup - 1; ++i)
-    if (i < in.count) in.pairs[i] = gated_read(sbase(static_cast<const u64*>(ch.pairs) + (in.from + i) * d + c0) + c);
-  bool there = in.state != kUnset;
-#pragma unroll
-  for (int i = 0; i < kGatedGroup - 1; ++i) there &= i >= in.count || in.pairs[i] != kUnset;
-  return there;
+// A look at channel c0 + c of d: the state, and the pairs from number `first` on.  It runs where every thread's tile is in
+// registers: bases in scalar ones, and offsets that do not become 64-bit addresses ahead of their use.
+__device__ __forceinline__ u64 gated_read(const u64* p, int64_t row, int64_t d, int64_t c0, uint32_t c) {
+  uint32_t off = c * static_cast<uint32_t>(sizeof(u64));
+  asm volatile("" : "+v"(off));
+  gmem<const char>* base = reinterpret_cast<gmem<const char>*>(sbase(p + row * d + c0));
+  return __hip_atomic_load(reinterpret_cast<gmem<const u64>*>(base + off), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ float gated_state(const Incoming& in) {
-  float h = __uint_as_float(static_cast<uint32_t>(in.state));
+__device__ __forceinline__ void gated_look(Incoming& in, int first, const GatedChain& ch, int64_t d, int64_t c0, uint32_t c) {
+  if (in.older) in.state = gated_read(ch.states, (in.from >> ch.group) - 1, d, c0, c);
 #pragma unroll
-  for (int i = 0; i < kGatedGroup - 1; ++i)
-    if (i < in.count) {
-      const float A = __uint_as_float(static_cast<uint32_t>(in.pairs[i] >> 32)), l = __uint_as_float(static_cast<uint32_t>(in.pairs[i]));
-      h = A < 0.0f ? l : __builtin_fmaf(A, h, l);
-    }
-  return h;
+  for (int i = 0; i < kGatedLook; ++i)
+    if (first + i < in.count) in.pairs[i] = gated_read(ch.pairs, in.from + first + i, d, c0, c);
 }
 // Every wait ends: the tiles before have their tickets, and what waits for them never holds them up.  A workspace that another
 // call overwrites meanwhile would break that: after so many looks (seconds) the tile goes on with what it has, kUnset being a NaN.
 constexpr int kGatedLooks = 1 << 21;
+// The state that comes in, from the first look on: the pairs put together, then the state taken through them.
+__device__ __forceinline__ float gated_state(Incoming& in, const GatedChain& ch, int64_t d, int64_t c0, uint32_t c) {
+  float A = 1.0f, h = 0.0f;
+  int looks = 0;
+  for (int at = 0; at < in.count;) {
+    bool there = true;
+#pragma unroll
+    for (int i = 0; i < kGatedLook; ++i) there &= at + i >= in.count || in.pairs[i] != kUnset;
+    if (__all(there) || looks >= kGatedLooks) {  // the wave goes on together: its bases stay scalar
+#pragma unroll
+      for (int i = 0; i < kGatedLook; ++i)
+        if (at + i < in.count) {
+          const float Ai = __uint_as_float(static_cast<uint32_t>(in.pairs[i] >> 32)), hi = __uint_as_float(static_cast<uint32_t>(in.pairs[i]));
+          h = Ai < 0.0f ? hi : __builtin_fmaf(Ai, h, hi);
+          A = Ai < 0.0f || A < 0.0f ? -1.0f : A * Ai;
+        }
+      at += kGatedLook;
+    } else {
+      __builtin_amdgcn_s_sleep(1);
+    }
+    ++looks;
+    if (at < in.count) gated_look(in, at, ch, d, c0, c);
+  }
+  for (; !__all(in.state != kUnset) && looks < kGatedLooks; ++looks) {
+    __builtin_amdgcn_s_sleep(1);
+    gated_look(in, in.count, ch, d, c0, c);
+  }
+  return A < 0.0f ? h : __builtin_fmaf(A, __uint_as_float(static_cast<uint32_t>(in.state)), h);
+}
 
 __global__ __launch_bounds__(256) void k_gated_clear(u64* p, int64_t n, uint32_t* tickets) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -181,9 +203,9 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// The ticket's tile: queue q has the slices q, q + kGatedQueues, ..., tile by tile (one counter for all is at its limit, 10 ns a
-// ticket).  There are as many workgroups as tiles, and a queue that is through hands its workgroups on to the next one, so each
-// has found its tile when it has asked every queue once; kGatedNone would mean that another call has the workspace too.
+// The ticket's tile: queue q has the slices q, q + kGatedQueues, ..., tile by tile (one counter gives a ticket in 10 ns).  There
+// are as many workgroups as tiles, and a queue that is through hands its workgroups on to the next one, so each has found its
+// tile when it has asked every queue once; kGatedNone would mean that another call has the workspace too.
 constexpr uint32_t kGatedNone = ~0u;
 __device__ __forceinline__ uint32_t gated_take(uint32_t* tickets, uint32_t tiles, uint32_t slices) {
   for (uint32_t i = 0; i < kGatedQueues; ++i) {
@@ -301,8 +323,8 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
   }
   const int64_t cc = c0 + threadIdx.x;
   const bool chain = threadIdx.x < C && cc < d, waits = lo != t0;
-  Incoming in = gated_from(tile, lo / kGatedTile);
-  bool there = !(chain && waits) || gated_look(in, ch, d, c0, threadIdx.x);  // the first look is under way while the runs are put together
+  Incoming in = gated_from(ch, tile, lo / kGatedTile);
+  if (chain && waits) gated_look(in, 0, ch, d, c0, threadIdx.x);  // under way while the runs are put together
   lds_barrier();
   if (chain) {
     const int j = threadIdx.x;
@@ -330,15 +352,9 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
       asm volatile("" : : : "memory");
     }
     if (tile + 1 < tiles) gated_publish(ch.pairs + tile * d + cc, gated_pair(At, ht));
-    if (waits) {
-      for (int look = 0; !there && look < kGatedLooks; ++look) {
-        __builtin_amdgcn_s_sleep(1);
-        there = gated_look(in, ch, d, c0, threadIdx.x);
-      }
-      from = gated_state(in);
-    }
-    if (tile + 1 < tiles && tile % kGatedGroup == kGatedGroup - 1)
-      gated_publish(ch.states + tile / kGatedGroup * d + cc, __float_as_uint(At < 0.0f ? ht : __builtin_fmaf(At, from, ht)));
+    if (waits) from = gated_state(in, ch, d, c0, threadIdx.x);
+    if (tile + 1 < tiles && (tile + 1) >> ch.group << ch.group == tile + 1)
+      gated_publish(ch.states + (tile >> ch.group) * d + cc, __float_as_uint(At < 0.0f ? ht : __builtin_fmaf(At, from, ht)));
     if (ckpt != nullptr) {
       if (waits) cp[0] = from;
       if (halfway && !restarts) cp[d] = Am < 0.0f ? hm : __builtin_fmaf(Am, from, hm);
@@ -607,8 +623,8 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
   if (lane == 0) cuts[run] = marks;  // the first channels of a slice are there
   const int64_t cc = c0 + threadIdx.x;
   const bool chain = threadIdx.x < C && cc < d, waits = hi > t0 + kGatedBwdTile;
-  Incoming in = gated_from(n, tiles - 1 - static_cast<int64_t>((hi > 0 ? hi - 1 : 0) / kGatedBwdTile));
-  bool there = !(chain && waits) || gated_look(in, ch, d, c0, threadIdx.x);
+  Incoming in = gated_from(ch, n, tiles - 1 - static_cast<int64_t>((hi > 0 ? hi - 1 : 0) / kGatedBwdTile));
+  if (chain && waits) gated_look(in, 0, ch, d, c0, threadIdx.x);
   lds_barrier();
   if (chain) {
     const int j = threadIdx.x;
@@ -627,15 +643,9 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
       sH[g][j] = state;
       state = cuts[g] & 1 ? hg : __builtin_fmaf(sA[g][j], state, hg);
     }
-    if (waits) {
-      for (int look = 0; !there && look < kGatedLooks; ++look) {
-        __builtin_amdgcn_s_sleep(1);
-        there = gated_look(in, ch, d, c0, threadIdx.x);
-      }
-      from = gated_state(in);
-    }
-    if (n + 1 < tiles && n % kGatedGroup == kGatedGroup - 1)
-      gated_publish(ch.states + n / kGatedGroup * d + cc, __float_as_uint(At < 0.0f ? Rt : __builtin_fmaf(At, from, Rt)));
+    if (waits) from = gated_state(in, ch, d, c0, threadIdx.x);
+    if (n + 1 < tiles && (n + 1) >> ch.group << ch.group == n + 1)
+      gated_publish(ch.states + (n >> ch.group) * d + cc, __float_as_uint(At < 0.0f ? Rt : __builtin_fmaf(At, from, Rt)));
 #pragma unroll
     for (int g = NG - 1; g >= 0; --g) {  // what each run's last token is handed
       const float Rg = sR[g][j];
@@ -783,13 +793,19 @@ int check_gated(int64_t S, int64_t T, int32_t d, float c, int32_t gate, int32_t 
 }
 // the chain in the workspace: the ticket, the tiles' pairs, their groups' states
 constexpr size_t kTicketBytes = kGatedQueues * kGatedQueueStep * 4;
+// log2 of a group's tiles: 4, more (up to 32) where a chain would have more than 128 links
+int gated_group(int64_t tiles) {
+  int g = 2;
+  while (g < 5 && tiles >> g > 128) ++g;
+  return g;
+}
 struct ChainLayout {
   int64_t pairs, states;  // elements
   size_t total;
 };
 ChainLayout chain_layout(int64_t tiles, int32_t d) {
   if (tiles <= 1) return {0, 0, 0};
-  const int64_t pairs = tiles * d, states = tiles / kGatedGroup * d;
+  const int64_t pairs = tiles * d, states = (tiles >> gated_group(tiles)) * d;
   return {pairs, states, align256(kTicketBytes + static_cast<size_t>(pairs + states) * 8)};
 }
 GatedChain start_chain(int64_t tiles, int32_t d, void* ws, hipStream_t st) {
@@ -798,7 +814,7 @@ GatedChain start_chain(int64_t tiles, int32_t d, void* ws, hipStream_t st) {
   u64* p = reinterpret_cast<u64*>(static_cast<char*>(ws) + kTicketBytes);
   const int64_t n = l.pairs + l.states;
   hipLaunchKernelGGL(k_gated_clear, dim3(static_cast<unsigned>(cdiv(n, 256))), dim3(256), 0, st, p, n, static_cast<uint32_t*>(ws));
-  return GatedChain{p, p + l.pairs, static_cast<uint32_t*>(ws)};
+  return GatedChain{p, p + l.pairs, static_cast<uint32_t*>(ws), gated_group(tiles)};
 }
 // the backward's workspace: a chain (the forward's first, where the states are made again), the tiles' sums, those states
 struct BackwardLayout {
