@@ -203,3 +203,48 @@ def test_more_tokens_than_a_launch_has_threads_for():
         q[t0:t0 + n], k[t0:t0 + n] = rows[0], rows[1]
         mm.qk_norm(q, k, wq, wk, q_out=q, k_out=k)
         assert torch.equal(q[t0:t0 + n], want[0]) and torch.equal(k[t0:t0 + n], want[1])
+
+
+def scan(a, b, h):
+    """h_t = a_t h_{t-1} + b_t over the rows of a, b [T, d] from h [d]: blocks of rows side by side, then from block to block."""
+    T, n = len(a), 512
+    pad = -T % n
+    a = torch.cat([a, a.new_ones(pad, a.shape[1])]).unflatten(0, (-1, n))
+    b = torch.cat([b, b.new_zeros(pad, b.shape[1])]).unflatten(0, (-1, n))
+    A, H = torch.ones_like(a), torch.zeros_like(b)
+    A[:, 0], H[:, 0] = a[:, 0], b[:, 0]
+    for t in range(1, n):
+        A[:, t], H[:, t] = A[:, t - 1] * a[:, t], a[:, t] * H[:, t - 1] + b[:, t]
+    for k in range(len(H)):
+        H[k] += A[k] * h
+        h = H[k, -1]
+    return H.flatten(0, 1)[:T]
+
+
+@pytest.mark.parametrize("lens", [[150000], [90000, 60011]], ids=str)
+def test_long_chains(lens):
+    """Chains of more than a thousand tiles, with decays that carry a state over several thousand tokens."""
+    d = 40
+    c = cuda(ref.gated_inputs(9, lens, d, "f32"))
+    far = 1.0 - 10.0 ** -torch.linspace(3, 4.5, d, device="cuda", dtype=torch.float64)
+    c["lam"] = torch.log(torch.expm1(-torch.log(far) / 8)).float()
+    ins = [c[k] for k in ("x", "r", "g", "z", "lam", "cu", "state")]
+    y, last, ckpt = mm.gated_prefill_train(*ins)
+    got = mm.gated_backward(*ins, c["dy"], c["dstate"], ckpt)
+    again = mm.gated_backward(*ins, c["dy"], c["dstate"])
+    for s, lo, hi in ref.ranges(lens):
+        x, r, g, z, dy = (c[k][lo:hi].double() for k in ("x", "r", "g", "z", "dy"))
+        a, m, u = ref._gates(x, r, g, c["lam"].double())
+        o, n = ref.act(z, "silu"), hi - lo
+        h, mag = scan(a, m * u, c["state"][s].double()), scan(a, (m * u).abs(), c["state"][s].double().abs())
+        ref.check(y[lo:hi], (h * o).cpu(), (mag * o.abs() * (1 + z.abs())).cpu(), n, "y")
+        ref.check(last[s], h[-1].cpu(), mag[-1].cpu(), n, "state")
+        # R_t = a_t G_t, from the last token to the first: R_t = a_t R_{t+1} + a_t dy act
+        back, ask = a.flip(0), (dy * o).flip(0)
+        R = [scan(back, back * v, w) for v, w in ((ask, c["dstate"][s].double()),
+                                                  ((dy * o).abs().mul(1 + z.abs()).flip(0), c["dstate"][s].double().abs()))]
+        G, Gm = ((v / back).flip(0) for v in R)
+        iota = torch.sigmoid(g)
+        for grads in (got, again):
+            ref.check(grads["dx"][lo:hi], (G * m * iota).cpu(), (Gm * m * iota).cpu(), n, "dx")
+            ref.check(grads["dstate_in"][s], R[0][-1].cpu(), R[1][-1].cpu(), n, "dstate_in")
