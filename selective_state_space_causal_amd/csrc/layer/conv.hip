@@ -3,7 +3,10 @@
 //   dX(q) = sum_k w_k du(q + W - 1 - k) + what the final state asks for,  dw_k = sum_p du(p) X(p - W + 1 + k)
 // Bound by memory.  A wave walks L tokens of 64 V channels (512 bytes of bfloat16 a row: narrower rows cost a fifth of the
 // bandwidth), its window, weights and the weights' gradients in registers: an input is read once, but for the W - 1 tokens
-// around a walk.  kStep tokens are loaded at a time, the next ones while these are used.
+// around a walk.  kStep tokens are loaded at a time, the next ones while these are used (8 at a time: backward 53 us for
+// 48.7, and fewer walks fit; 2: 65.3 forward for 63.9).  16384 x 4352 of bfloat16: 285 MB in 63.5 us, 4.5 TB/s; backward
+// 8 x 2048 x 1792: 176 MB in 47 us with the sum of the partial gradients (4 us), half of the time vector instructions.
+// Longer: 65536 x 2048 5.1 TB/s forward, 4.9 backward.
 #include <algorithm>
 #include <type_traits>
 
@@ -13,9 +16,9 @@ namespace mm {
 namespace {
 
 constexpr int kConvWaves = 4, kConvThreads = kConvWaves * 64, kStep = 4;
-// A walk has at most kConvTokens tokens, fewer where there would be fewer than kConvWalks of them (one for each SIMD).  More and
-// shorter walks read more rows twice: 8192 x 2048 f32 4096 walks 28.9 us, 2048 27.4, 1024 25.9; backward 46.7 with 2048, 44.1
-// with 1024.  Longer ones leave fewer: backward 8 x 2048 x 1792 bf16 with 128 tokens 63 us, with 64 47.5.
+// A walk has at most kConvTokens tokens, fewer where there would be fewer than kConvWalks of them (one for each SIMD).
+// More and shorter walks read more rows twice: 8192 x 2048 f32 4096 walks 28.9 us, 2048 27.4, 1024 25.9; backward 46.7 with
+// 2048, 44.1 with 1024.  Longer ones leave fewer: backward 8 x 2048 x 1792 bf16 with 128 tokens 63 us, with 64 47.5.
 constexpr int64_t kConvTokens = 64, kConvWalks = 1024;
 
 struct ConvArgs {
@@ -38,11 +41,16 @@ __device__ __forceinline__ float conv_slope(float u, float g, bool silu) {
   const Sigmoids v = sigmoids(u);
   return g * v.s * __builtin_fmaf(u, v.s1, 1.0f);
 }
+__device__ __forceinline__ void conv_place(int64_t i, int d, int& s, int& c) {
+  s = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(d));  // S d < 2^31
+  c = static_cast<int>(i - static_cast<int64_t>(s) * d);
+}
 // the final state of (sequence, channel) i; state_out may be state_in
 template <typename IO, int W>
 __device__ __forceinline__ void conv_state(const ConvArgs& a, float* state_out, int64_t i) {
   if (i >= static_cast<int64_t>(a.S) * a.d) return;
-  const int s = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.d)), c = static_cast<int>(i - static_cast<int64_t>(s) * a.d);  // S d < 2^31
+  int s, c;
+  conv_place(i, a.d, s, c);
   const int64_t g0 = a.cu[s], n = a.cu[s + 1] - g0;
   float v[W - 1];
 #pragma unroll
@@ -54,7 +62,8 @@ __device__ __forceinline__ void conv_state(const ConvArgs& a, float* state_out, 
 template <typename IO, int W>
 __device__ __forceinline__ void conv_dstate(const ConvArgs& a, const IO* dy, const float* dstate_out, float* dstate_in, int64_t i) {
   if (i >= static_cast<int64_t>(a.S) * a.d) return;
-  const int s = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.d)), c = static_cast<int>(i - static_cast<int64_t>(s) * a.d);  // S d < 2^31
+  int s, c;
+  conv_place(i, a.d, s, c);
   const int64_t g0 = a.cu[s], n = a.cu[s + 1] - g0;
   const float b = a.bias != nullptr ? a.bias[c] : 0.0f;
   float w[W], du[W - 1];
@@ -183,9 +192,9 @@ struct ConvWalk {
     }
   }
 };
-// The walk's steps of kStep tokens: load(rows, t) asks for a step's rows, use(t + k, rows, k) is called for each token in turn.
-// Two sets of rows take turns: while one is used the other is on its way.  The first step stands before the loop, so that each
-// pass begins with the same accesses under way (a step's loads, then its stores) and waits for the loads alone.
+// The walk's steps of kStep tokens: load(rows, t) asks for a step's rows, use(t + k, rows, k) is called for each token in
+// turn.  Two sets of rows take turns: while one is used the other is on its way.  The first step stands before the loop, so
+// that each pass begins with the same accesses under way (a step's loads, then its stores) and waits for the loads alone.
 template <typename Rows, typename Load, typename Use>
 __device__ __forceinline__ int64_t conv_steps(int64_t t, int64_t t1, Rows& r0, Load load, Use use) {
   const int64_t te = t + (t1 - t) / kStep * kStep;
@@ -271,8 +280,10 @@ __global__ __launch_bounds__(256) void k_conv_decode(ConvArgs a, float* state_ou
   store_chans<IO, V>(global(y + i0), 0, u);
 }
 
-// A walk computes du for its own tokens and up to W - 1 behind them; pend holds the gradients of the last W tokens as they gather.
-// part: [blocks / slices][W + 1][d], a block's sums of dw and dbias.
+// A walk computes du for its own tokens and up to W - 1 behind them; pend holds the gradients of the last W tokens as they
+// gather.
+// part: [blocks / slices][W + 1][d], a block's sums of dw and dbias.  Registers allow three waves of a SIMD; asking for
+// four spills (121 us).
 template <typename IO, int V, int W>
 __global__ __launch_bounds__(kConvThreads) void k_conv_bwd(ConvArgs a, int64_t blocks, uint32_t slices, const IO* __restrict__ dy,
                                                            const float* __restrict__ dstate_out, IO* __restrict__ dx, int64_t dx_ts,
@@ -419,7 +430,9 @@ __global__ __launch_bounds__(256) void k_conv_parts(const float* __restrict__ pa
 }
 
 // ---------------------------------------------------------------- host
-int conv_channels(int32_t d) { return d % 4 == 0 ? 4 : d % 2 == 0 ? 2 : 1; }  // of a lane: all there or none
+// Channels of a lane: all there or none.  Two in place of four: 16384 x 4352 68 us for 65.8, backward 8 x 2048 x 1792 67
+// for 56.5.
+int conv_channels(int32_t d) { return d % 4 == 0 ? 4 : d % 2 == 0 ? 2 : 1; }
 int64_t conv_slices(int32_t d) { return cdiv(d, 64 * conv_channels(d)); }
 // tokens of a walk, in steps of kStep
 int64_t conv_tokens(int64_t T, int32_t d) {

@@ -22,8 +22,8 @@ struct GatedArgs {
 // c softplus(lam) log2(e), so that a = exp2(-kap rho); NaN stays NaN
 __device__ __forceinline__ float gated_kap(float lam, float c) { return (lam != lam ? lam : softplus(lam)) * c * kLog2e; }
 
-// The decay a and the input's factor m of one element.  With l = log2 a = -kap rho, 1 - a^2 = -expm1(2 ln2 l): five terms of its
-// series near 0 (4e-8 of it at a^2 = e^-1/8), 1 - a a beyond (there a's last unit is 5e-7 of m).
+// The decay a and the input's factor m of one element.  With l = log2 a = -kap rho, 1 - a^2 = -expm1(2 ln2 l): five terms
+// of its series near 0 (4e-8 of it at a^2 = e^-1/8), 1 - a a beyond (there a's last unit is 5e-7 of m).
 struct Decay {
   float a, m;
 };
@@ -51,18 +51,23 @@ __device__ __forceinline__ float gated_act(bool gelu, float z) {
   return gelu ? z * rcp_hw(1.0f + exp2_hw(z * __builtin_fmaf(-kGelu1 * kLog2e, z * z, -kGelu0 * kLog2e))) : z * sigmoid(z);
 }
 
-// One pass over the tokens.  A workgroup takes a tile: kGatedTile tokens of the packed stream by 256 bytes of channels.  A thread
-// has V neighbouring channels and a run of K tokens: every (a, b = m iota x) of them is in registers from the load to the
-// store, so each array is read and written once.  Runs compose as pairs (A, h): h_out = A h_in + h; the first threads put
-// a tile's runs together, one for each channel, and the tiles of a channel are a chain in memory:
+// One pass over the tokens.  A workgroup takes a tile: kGatedTile tokens of the packed stream by 256 bytes of channels.  A
+// thread has V neighbouring channels and a run of K tokens: every (a, b = m iota x) of them is in registers from the load
+// to the store, so each array is read and written once.  Runs compose as pairs (A, h): h_out = A h_in + h; the first
+// threads put a tile's runs together, one for each channel, and the tiles of a channel are a chain in memory:
 //   - a tile publishes its own pair as soon as it has it;
 //   - the last of each group of tiles also publishes its final state;
 //   - a tile's initial state is that of the last whole group of tiles before it, taken through the pairs of the tiles since.
-// The order of these products does not depend on timing: results repeat bit for bit.  The links that wait for one another are
-// one in a group.  Tiles are numbered by tickets, not by the workgroup's index, so a tile waits only for tiles
-// whose workgroups run already or are done, and every wait ends.
-// Where a sequence starts, A is set to -1: what comes before has no part in what follows, whatever it is (0 times an infinity
-// would have).
+// The order of these products does not depend on timing: results repeat bit for bit.  The links that wait for one another,
+// a microsecond each, are one in a group.  Tiles are numbered by tickets, not by the workgroup's index, so a tile waits
+// only for tiles whose workgroups run already or are done, and every wait ends.
+// 16384 x 4096 of bfloat16 with all gates: 671 MB in 173 us, 3.9 TB/s (a copy of its size would take 109), vector
+// instructions half of the time.  Two workgroups of a CU hold 128 registers a thread, and a tile's loads, its arithmetic
+// and its wait follow each other: what the other workgroup does meanwhile is all the overlap.  The wait itself is 5 us of
+// it.  Rows of 128 bytes of channels: 193 us; tiles of 64 tokens: 180; workgroups that stay and load the next tile ahead:
+// 214 and more, their registers left room for smaller tiles only.
+// Where a sequence starts, A is set to -1: what comes before has no part in what follows, whatever it is (0 times an
+// infinity would have).
 constexpr int kGatedTile = 2 * MM_GATED_BLOCK, kGatedThreads = 512;
 constexpr uint32_t kGatedQueues = 2, kGatedQueueStep = 64;  // tickets: counters, and elements between them
 template <typename IO, int V, int TILE>
@@ -89,8 +94,8 @@ __device__ __forceinline__ u64 gated_pair(float A, float h) {
 // Written through to where all XCDs see it; the value itself says that it is there, so nothing else has to be ordered.
 __device__ __forceinline__ void gated_publish(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
-// What comes into tile `n` (in the chain's order) of a run that goes back to tile `first`: the last whole group's state, and
-// the pairs of the tiles since, kGatedLook of them at a time.
+// What comes into tile `n` (in the chain's order) of a run that goes back to tile `first`: the last whole group's state,
+// and the pairs of the tiles since, kGatedLook of them at a time.
 constexpr int kGatedLook = 4;
 struct Incoming {
   u64 state, pairs[kGatedLook];
@@ -123,8 +128,9 @@ __device__ __forceinline__ void gated_look(Incoming& in, int first, const GatedC
   for (int i = 0; i < kGatedLook; ++i)
     if (first + i < in.count) in.pairs[i] = gated_read(ch.pairs, in.from + first + i, d, c0, c);
 }
-// Every wait ends: the tiles before have their tickets, and what waits for them never holds them up.  A workspace that another
-// call overwrites meanwhile would break that: after so many looks (seconds) the tile goes on with what it has, kUnset being a NaN.
+// Every wait ends: the tiles before have their tickets, and what waits for them never holds them up.  A workspace that
+// another call overwrites meanwhile would break that: after so many looks (seconds) the tile goes on with what it has,
+// kUnset being a NaN.
 constexpr int kGatedLooks = 1 << 21;
 // The state that comes in, from the first look on: the pairs put together, then the state taken through them.
 __device__ __forceinline__ float gated_state(Incoming& in, const GatedChain& ch, int64_t d, int64_t c0, uint32_t c) {
@@ -181,7 +187,8 @@ __device__ __forceinline__ void gated_places(const int32_t* __restrict__ cu, int
     place[i].v = v;
   }
 }
-// Final states of empty sequences, channels c0 .. c0 + width: wave `part` of `parts` looks through its share of the sequences.
+// Final states of empty sequences, channels c0 .. c0 + width: wave `part` of `parts` looks through its share of the
+// sequences.
 __device__ __forceinline__ void gated_empty(const int32_t* __restrict__ cu, int S, const float* in, float* out, int64_t d, int64_t c0,
                                             int width, int64_t part, int64_t parts) {
   if (out == in) return;
@@ -203,9 +210,10 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// The ticket's tile: queue q has the slices q, q + kGatedQueues, ..., tile by tile (one counter gives a ticket in 10 ns).  There
-// are as many workgroups as tiles, and a queue that is through hands its workgroups on to the next one, so each has found its
-// tile when it has asked every queue once; kGatedNone would mean that another call has the workspace too.
+// The ticket's tile: queue q has the slices q, q + kGatedQueues, ..., tile by tile (one counter gives a ticket in 10 ns:
+// 4 x 2048 x 768 31.1 us with one, 29.5 with two; with four the slices drift apart, 262144 x 256 191 -> 219).  There are as
+// many workgroups as tiles, and a queue that is through hands its workgroups on to the next one, so each has found its tile
+// when it has asked every queue once; kGatedNone would mean that another call has the workspace too.
 constexpr uint32_t kGatedNone = ~0u;
 __device__ __forceinline__ uint32_t gated_take(uint32_t* tickets, uint32_t tiles, uint32_t slices) {
   for (uint32_t i = 0; i < kGatedQueues; ++i) {
@@ -439,10 +447,12 @@ __global__ __launch_bounds__(256) void k_gated_decode(GatedArgs a, float* state_
 //              dlam = sum e sigmoid(lam) / softplus(lam)
 //   else:      dr = G (h' - u) rho (1 - rho)
 // m tends to 0 with L, and L / m with it.
-// One pass from the last tile to the first, in the forward's manner: R = a G is what a token hands to the one before it, so a
-// run is a pair (A, R) and the tiles are a chain.  The states before each token come from the checkpoint before the tile.
-// What a thread keeps of a token from the first look to the gradients are a, h' and dy act'(z) in registers, dy act(z) in shared
-// memory, and the other inputs as they were loaded: the rest is computed twice, which costs less than the registers.
+// One pass from the last tile to the first, in the forward's manner: R = a G is what a token hands to the one before it, so
+// a run is a pair (A, R) and the tiles are a chain.  The states before each token come from the checkpoint before the tile.
+// What a thread keeps of a token from the first look to the gradients are a, h' and dy act'(z) in registers, dy act(z) in
+// shared memory, and the other inputs as they were loaded: the rest is computed twice, which costs less than the registers.
+// 8 x 2048 x 1536 of bfloat16 with all gates: 453 MB in 145 us, 3.1 TB/s; vector instructions take 60% of the time (fifteen
+// exponentials, reciprocals and roots an element), and as in the forward little of it overlaps the loads.
 struct GatedGrads {
   const void* dy;
   const float *dstate_out, *ckpt;
@@ -793,7 +803,9 @@ int check_gated(int64_t S, int64_t T, int32_t d, float c, int32_t gate, int32_t 
 }
 // the chain in the workspace: the ticket, the tiles' pairs, their groups' states
 constexpr size_t kTicketBytes = kGatedQueues * kGatedQueueStep * 4;
-// log2 of a group's tiles: 4, more (up to 32) where a chain would have more than 128 links
+// log2 of a group's tiles: 4, more (up to 32) where a chain would have more than 128 links.  A tile's looks grow with its
+// group, a chain's links shrink: 65536 x 8192 with groups of 4 1147 us, of 8 1160; 262144 x 256 with groups of 4 406, of 16
+// 191.
 int gated_group(int64_t tiles) {
   int g = 2;
   while (g < 5 && tiles >> g > 128) ++g;
@@ -828,7 +840,8 @@ BackwardLayout backward_layout(int64_t T, int32_t d, bool has_ckpt) {
   l.total = l.ckpt + (has_ckpt ? 0 : align256(static_cast<size_t>(n) * 4));
   return l;
 }
-// f(V as a type) for d channels: pairs of them where every thread's are all there or all missing
+// f(V as a type) for d channels: as many of them, up to 4, as let every thread's be all there or all missing.  16384 x 4096
+// of bfloat16 with 4: 173 us, with 2: 175; single ones make rows of 128 bytes (193).
 template <typename IO, typename F>
 int by_channels(int32_t d, F f) {
   if (d % 4 == 0) return f(std::integral_constant<int, 4>{});
@@ -892,8 +905,9 @@ int mamba_mixer_gated_prefill(const void* x, const void* r, const void* g, const
       constexpr int V = decltype(v)::value;
       const GatedChain ch = start_chain(gated_tiles(T), d, workspace, st);
       const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, gated_tiles(T)) * cdiv(d, GatedShape<IO, V, kGatedTile>::C)));
-      if (lam != nullptr) hipLaunchKernelGGL((k_gated<IO, V, true, true>), grid, dim3(kGatedThreads), 0, st, a, ch, state_out, static_cast<IO*>(y), ckpt);
-      else hipLaunchKernelGGL((k_gated<IO, V, false, true>), grid, dim3(kGatedThreads), 0, st, a, ch, state_out, static_cast<IO*>(y), ckpt);
+      IO* const out = static_cast<IO*>(y);
+      if (lam != nullptr) hipLaunchKernelGGL((k_gated<IO, V, true, true>), grid, dim3(kGatedThreads), 0, st, a, ch, state_out, out, ckpt);
+      else hipLaunchKernelGGL((k_gated<IO, V, false, true>), grid, dim3(kGatedThreads), 0, st, a, ch, state_out, out, ckpt);
       return launched();
     });
   });
@@ -974,10 +988,9 @@ int mamba_mixer_gated_backward(const void* x, const void* r, const void* g, cons
       if (S > 0 && ckpt == nullptr && T > 0) {
         const dim3 forward(static_cast<unsigned>(gated_tiles(T) * cdiv(d, GatedShape<IO, V, kGatedTile>::C)));
         const GatedChain ch = start_chain(gated_tiles(T), d, workspace, st);
-        if (lam != nullptr)
-          hipLaunchKernelGGL((k_gated<IO, V, true, false>), forward, dim3(kGatedThreads), 0, st, a, ch, nullptr, static_cast<IO*>(nullptr), states);
-        else
-          hipLaunchKernelGGL((k_gated<IO, V, false, false>), forward, dim3(kGatedThreads), 0, st, a, ch, nullptr, static_cast<IO*>(nullptr), states);
+        IO* const none = nullptr;
+        if (lam != nullptr) hipLaunchKernelGGL((k_gated<IO, V, true, false>), forward, dim3(kGatedThreads), 0, st, a, ch, nullptr, none, states);
+        else hipLaunchKernelGGL((k_gated<IO, V, false, false>), forward, dim3(kGatedThreads), 0, st, a, ch, nullptr, none, states);
       }
       if (S > 0) {
         const GatedChain ch = start_chain(tiles, d, workspace, st);
