@@ -287,89 +287,125 @@ __global__ __launch_bounds__(kQkThreads) void k_qk_rows_bwd(QkArgs a, int block,
 }
 
 // ---------------------------------------------------------------- rows of any width
-// A wave takes a row, with its values in LDS: pairs may lie anywhere.
-__device__ __forceinline__ int qk_mate(const QkArgs& a, int i, bool& first) {  // the other column of i's pair, and whether i is its first
-  first = a.inter ? i % 2 == 0 : i < a.R / 2;
-  return a.inter ? i ^ 1 : first ? i + a.R / 2 : i - a.R / 2;
+// A workgroup takes a token, its angles in LDS, a wave one head after another, its row in LDS: pairs may lie anywhere.  Bound
+// by a row's chain of loads, sums and LDS; the backward's 512 workgroups take 591 us where 1024 take 341.
+constexpr int kQkWaves = kQkThreads / 64, kQkCols = MM_QK_MAX_D / 64, kQkTokenParts = 1024;
+struct QkToken {
+  float c[MM_QK_MAX_D / 2], s[MM_QK_MAX_D / 2], row[kQkWaves][MM_QK_MAX_D];
+};
+__device__ __forceinline__ void qk_token_angles(const QkArgs& a, int64_t t, QkToken& tok) {
+  __syncthreads();
+  for (int p = threadIdx.x; p < a.R / 2; p += kQkThreads) qk_angle(a.pos[t], a.freq[p], tok.c[p], tok.s[p]);
+  __syncthreads();
 }
-__device__ __forceinline__ int qk_pair(const QkArgs& a, int i) { return a.inter ? i / 2 : i % (a.R / 2); }
+// Column i of the row u, turned: (first, second) by (cos, sin); sign -1 turns back.
+__device__ __forceinline__ float qk_turned(const QkArgs& a, const QkToken& tok, const float* u, int i, float sign) {
+  if (i >= a.R) return u[i];
+  const bool first = a.inter ? i % 2 == 0 : i < a.R / 2;
+  const int mate = a.inter ? i ^ 1 : first ? i + a.R / 2 : i - a.R / 2, pair = a.inter ? i / 2 : first ? i : mate;
+  const float s = sign * tok.s[pair];
+  return __builtin_fmaf(u[i], tok.c[pair], first ? -u[mate] * s : u[mate] * s);
+}
 __device__ __forceinline__ float wave_sum(float v) { return group_sum<32>(v) + __shfl_xor(group_sum<32>(v), 32); }
 
 template <typename IO>
-__global__ __launch_bounds__(64) void k_qk(QkArgs a, IO* q_out, IO* k_out, int64_t qo_ts, int64_t ko_ts) {
-  __shared__ float u[MM_QK_MAX_D];
-  const int H = a.Hq + a.Hk;
-  for (int64_t row = blockIdx.x; row < a.T * H; row += gridDim.x) {
-    const int64_t t = row / H;
-    int h = static_cast<int>(row % H);
-    const bool key = h >= a.Hq;
-    if (key) h -= a.Hq;
-    const IO* v = static_cast<const IO*>(key ? a.k : a.q) + t * (key ? a.k_ts : a.q_ts) + static_cast<int64_t>(h) * a.D;
-    const float* w = key ? a.wk : a.wq;
-    float s = 0.0f;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.D; i += 64) {
-      u[i] = ld_io(v, i);
-      s = __builtin_fmaf(u[i], u[i], s);
-    }
-    const float r = rsqrtf(wave_sum(s) / a.D + a.eps);
-    __syncthreads();
-    IO* out = (key ? k_out : q_out) + t * (key ? ko_ts : qo_ts) + static_cast<int64_t>(h) * a.D;
-    for (int i = threadIdx.x; i < a.D; i += 64) {
-      float o = u[i] * r * w[i];
-      if (i < a.R) {
-        bool first;
-        const int j = qk_mate(a, i, first);
-        float c, sn;
-        qk_angle(a.pos[t], a.freq[qk_pair(a, i)], c, sn);
-        const float m = u[j] * r * w[j];
-        o = first ? o * c - m * sn : o * c + m * sn;
+__global__ __launch_bounds__(kQkThreads) void k_qk(QkArgs a, IO* q_out, IO* k_out, int64_t qo_ts, int64_t ko_ts) {
+  __shared__ QkToken tok;
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  float* const u = tok.row[wave];
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    qk_token_angles(a, t, tok);
+    for (int h = wave; h < a.Hq + a.Hk; h += kQkWaves) {
+      const bool key = h >= a.Hq;
+      const int64_t at = static_cast<int64_t>(key ? h - a.Hq : h) * a.D;
+      const IO* v = static_cast<const IO*>(key ? a.k : a.q) + t * (key ? a.k_ts : a.q_ts) + at;
+      IO* out = (key ? k_out : q_out) + t * (key ? ko_ts : qo_ts) + at;
+      const float* w = key ? a.wk : a.wq;
+      float x[kQkCols], s = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kQkCols; ++e) {
+        const int i = lane + 64 * e;
+        x[e] = i < a.D ? ld_io(v, i) : 0.0f;
+        s = __builtin_fmaf(x[e], x[e], s);
       }
-      st_io(out, i, o);
+      const float r = rsqrtf(wave_sum(s) / a.D + a.eps);
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int e = 0; e < kQkCols; ++e) {
+        const int i = lane + 64 * e;
+        if (i < a.D) u[i] = x[e] * r * w[i];
+      }
+      __builtin_amdgcn_wave_barrier();  // a wave's accesses to LDS are in order
+#pragma unroll
+      for (int e = 0; e < kQkCols; ++e) {
+        const int i = lane + 64 * e;
+        if (i < a.D) st_io(out, i, qk_turned(a, tok, u, i, 1.0f));
+      }
     }
   }
 }
 
-// a workgroup takes rows of one kind (blockIdx.y: queries, keys)
 template <typename IO>
-__global__ __launch_bounds__(64) void k_qk_bwd(QkArgs a, const IO* dqo, const IO* dko, IO* dq, IO* dk, int64_t dq_ts, int64_t dk_ts,
-                                               float* part) {
-  __shared__ float u[MM_QK_MAX_D];
-  const bool key = blockIdx.y != 0;
-  const int H = key ? a.Hk : a.Hq;
-  const float* w = key ? a.wk : a.wq;
-  float dw[MM_QK_MAX_D / 64] = {};
-  for (int64_t row = blockIdx.x; row < a.T * H; row += kQkParts) {
-    const int64_t t = row / H;
-    const int h = row % H;
-    const IO* v = static_cast<const IO*>(key ? a.k : a.q) + t * (key ? a.k_ts : a.q_ts) + static_cast<int64_t>(h) * a.D;
-    const IO* go = (key ? dko : dqo) + row * a.D;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.D; i += 64) u[i] = ld_io(go, i);
-    __syncthreads();
-    float s = 0.0f, dot = 0.0f, g[MM_QK_MAX_D / 64], x[MM_QK_MAX_D / 64];
-    for (int i = threadIdx.x, e = 0; i < a.D; i += 64, ++e) {
-      x[e] = ld_io(v, i);
-      g[e] = u[i];
-      if (i < a.R) {
-        bool first;
-        const int j = qk_mate(a, i, first);
-        float c, sn;
-        qk_angle(a.pos[t], a.freq[qk_pair(a, i)], c, sn);
-        g[e] = first ? u[i] * c + u[j] * sn : u[i] * c - u[j] * sn;
+__global__ __launch_bounds__(kQkThreads) void k_qk_bwd(QkArgs a, const IO* dqo, const IO* dko, IO* dq, IO* dk, int64_t dq_ts,
+                                                       int64_t dk_ts, float* part) {
+  __shared__ QkToken tok;
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  float* const u = tok.row[wave];
+  float dw[2][kQkCols] = {};
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    qk_token_angles(a, t, tok);
+    const auto kind = [&](const IO* in, int64_t ts, const IO* dout, IO* out, int64_t o_ts, const float* w, int H, float(&sum)[kQkCols]) {
+      for (int h = wave; h < H; h += kQkWaves) {
+        const IO* v = in + t * ts + static_cast<int64_t>(h) * a.D;
+        const IO* go = dout + (t * H + h) * a.D;
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int e = 0; e < kQkCols; ++e) {
+          const int i = lane + 64 * e;
+          if (i < a.D) u[i] = ld_io(go, i);
+        }
+        __builtin_amdgcn_wave_barrier();
+        float s = 0.0f, dot = 0.0f, g[kQkCols], x[kQkCols];
+#pragma unroll
+        for (int e = 0; e < kQkCols; ++e) {
+          const int i = lane + 64 * e;
+          x[e] = g[e] = 0.0f;
+          if (i < a.D) {
+            x[e] = ld_io(v, i);
+            g[e] = qk_turned(a, tok, u, i, -1.0f);
+            s = __builtin_fmaf(x[e], x[e], s);
+            dot = __builtin_fmaf(g[e] * w[i], x[e], dot);
+          }
+        }
+        const float r = rsqrtf(wave_sum(s) / a.D + a.eps), m = wave_sum(dot) * r / a.D;
+        IO* o = out + t * o_ts + static_cast<int64_t>(h) * a.D;
+#pragma unroll
+        for (int e = 0; e < kQkCols; ++e) {
+          const int i = lane + 64 * e;
+          if (i < a.D) {
+            const float n = x[e] * r;
+            sum[e] = __builtin_fmaf(g[e], n, sum[e]);
+            st_io(o, i, r * (g[e] * w[i] - n * m));
+          }
+        }
       }
-      s = __builtin_fmaf(x[e], x[e], s);
-      dot = __builtin_fmaf(g[e] * w[i], x[e], dot);
-    }
-    const float r = rsqrtf(wave_sum(s) / a.D + a.eps), m = wave_sum(dot) * r / a.D;
-    IO* out = (key ? dk : dq) + t * (key ? dk_ts : dq_ts) + static_cast<int64_t>(h) * a.D;
-    for (int i = threadIdx.x, e = 0; i < a.D; i += 64, ++e) {
-      const float n = x[e] * r;
-      dw[e] = __builtin_fmaf(g[e], n, dw[e]);
-      st_io(out, i, r * (g[e] * w[i] - n * m));
+    };
+    kind(static_cast<const IO*>(a.q), a.q_ts, dqo, dq, dq_ts, a.wq, a.Hq, dw[0]);
+    kind(static_cast<const IO*>(a.k), a.k_ts, dko, dk, dk_ts, a.wk, a.Hk, dw[1]);
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kQkCols; ++e) u[lane + 64 * e] = dw[n][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.D; i += kQkThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kQkWaves; ++k) v += tok.row[k][i];
+      part[(static_cast<int64_t>(n) * gridDim.x + blockIdx.x) * a.D + i] = v;
     }
   }
-  for (int i = threadIdx.x, e = 0; i < a.D; i += 64, ++e) part[(blockIdx.y * kQkParts + blockIdx.x) * a.D + i] = dw[e];
 }
 // dwq, dwk from `parts` rows each
 __global__ __launch_bounds__(256) void k_qk_parts(const float* __restrict__ part, int64_t parts, int D, float* __restrict__ dwq,
@@ -379,14 +415,13 @@ __global__ __launch_bounds__(256) void k_qk_parts(const float* __restrict__ part
   if (i < D && threadIdx.x < kPartColumns) (blockIdx.y == 0 ? dwq : dwk)[i] = v;
 }
 
-// Whole pairs lie in pieces of four columns where D and R are multiples of eight; the rest goes row by row, each through
-// LDS and with its angles computed again (16384 x (8 + 8) x 128 147 us for 28.8, backward 8 x 2048 x (24 + 24) x 64 1220
-// for 64.5).
+// Whole pairs lie in pieces of four columns where D and R are multiples of eight; the rest goes row by row through LDS
+// (16384 x (8 + 8) x 128 102 us for 28.8, backward 8 x 2048 x (24 + 24) x 64 341 for 64.5).
 bool qk_by_groups(int D, int R) { return D % 8 == 0 && R % 8 == 0; }
 // tokens of a block: fewer where the blocks would not fill the GPU
 int qk_block(int64_t T) { return static_cast<int>(std::min<int64_t>(kQkTokens, std::max<int64_t>(1, T / 1024))); }
 int64_t qk_parts(int64_t T, int D, int R) {
-  return qk_by_groups(D, R) ? std::min<int64_t>(kQkParts, cdiv(T, qk_block(T))) : T > 0 ? kQkParts : 0;
+  return qk_by_groups(D, R) ? std::min<int64_t>(kQkParts, cdiv(T, qk_block(T))) : std::min<int64_t>(kQkTokenParts, T);
 }
 // f(lanes of a group, interleaved)
 template <typename F>
@@ -451,7 +486,7 @@ int mamba_mixer_qk_norm(const void* q, const void* k, const float* q_weight, con
         }
       });
     } else {
-      hipLaunchKernelGGL((k_qk<IO>), dim3(static_cast<unsigned>(std::min<int64_t>(T * (Hq + Hk), 1 << 20))), dim3(64), 0, st, a,
+      hipLaunchKernelGGL((k_qk<IO>), dim3(static_cast<unsigned>(std::min<int64_t>(T, 1 << 16))), dim3(kQkThreads), 0, st, a,
                          static_cast<IO*>(q_out), static_cast<IO*>(k_out), qo_stride, ko_stride);
     }
     return launched();
@@ -460,7 +495,7 @@ int mamba_mixer_qk_norm(const void* q, const void* k, const float* q_weight, con
 
 size_t mamba_mixer_qk_norm_backward_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D) {
   if (check_qk(T, Hq, Hk, D, 0, 0.0f, MM_IO_F32) != MM_OK) return 0;
-  return align256(static_cast<size_t>(2) * kQkParts * D * 4);
+  return align256(static_cast<size_t>(2) * std::max(kQkParts, kQkTokenParts) * D * 4);
 }
 
 int mamba_mixer_qk_norm_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
@@ -497,7 +532,7 @@ int mamba_mixer_qk_norm_backward(const void* dq_out, const void* dk_out, const v
                            static_cast<IO*>(dk), dq_stride, dk_stride, part);
       });
     } else if (T > 0) {
-      hipLaunchKernelGGL((k_qk_bwd<IO>), dim3(kQkParts, 2), dim3(64), 0, st, a, static_cast<const IO*>(dq_out),
+      hipLaunchKernelGGL((k_qk_bwd<IO>), dim3(static_cast<unsigned>(parts)), dim3(kQkThreads), 0, st, a, static_cast<const IO*>(dq_out),
                          static_cast<const IO*>(dk_out), static_cast<IO*>(dq), static_cast<IO*>(dk), dq_stride, dk_stride, part);
     }
     hipLaunchKernelGGL(k_qk_parts, dim3(static_cast<unsigned>(cdiv(D, kPartColumns)), 2), dim3(256), 0, st, part, parts, D, dq_weight,
