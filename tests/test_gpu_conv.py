@@ -108,3 +108,18 @@ def test_empty_calls():
     assert y.shape == (0, 8) and torch.equal(last, s)
     g = mm.conv_backward(x, w, w[:, 0].contiguous(), cu, s, x, s)
     assert torch.equal(g["dstate_in"], s) and not g["dweight"].any() and not g["dbias"].any()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_long_walks(io):
+    """Enough tokens for walks of 64: sequences that start and end at every place of them, and sequences of many walks."""
+    lens = [61, 3, 64, 1, 127, 2, 0, 66, 4000, 62, 65, 130, 1, 1, 1, 7000] + [37] * 70
+    c = ref.conv_inputs(5, lens, 1028, 4, io)
+    x, w, b, cu, s0 = wide(c["x"]), c["weight"].cuda(), c["bias"].cuda(), c["cu"].cuda(), c["state"].cuda()
+    y, last = mm.conv_prefill(x, w, b, cu, s0)
+    want, wl, mag = ref.conv(c, True)
+    ref.check(y, want, mag, 4, "y")
+    assert torch.equal(last.cpu().double(), wl)
+    got = mm.conv_backward(x, w, b, cu, s0, c["dy"].cuda(), c["dstate"].cuda())
+    for k, (v, m) in ref.conv_backward(c, True).items():
+        ref.check(got[k], v, m, 4 if k in ("dx", "dstate_in") else sum(lens), k)
