@@ -100,3 +100,16 @@ def test_empty_calls():
     assert [t.shape[0] for t in mm.qk_norm(q, q, w, w)] == [0, 0]
     got = mm.qk_norm_backward(q, q, q, q, w, w)
     assert not got[2].any() and not got[3].any()
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,R,io", [(9001, 2, 1, 32, 16, "bf16"), (70001, 1, 2, 6, 4, "f32"), (2501, 5, 3, 36, 20, "bf16")])
+def test_more_tokens_than_workgroups(T, Hq, Hk, D, R, io):
+    c = ref.qk_inputs(5, T, Hq, Hk, D, R, io)
+    q, k = strided(c)
+    for g, (w, mag), n in zip(call(c, q, k, False), ref.qk(c, False), "qk"):
+        ref.check(g, w, mag, D, n)
+    got = mm.qk_norm_backward(c["dq"].cuda(), c["dk"].cuda(), q, k, c["wq"].cuda(), c["wk"].cuda(), gpu(c["pos"]), gpu(c["freq"]))
+    want = ref.qk_backward(c, False)
+    for g, n in zip(got, ("dq", "dk", "dwq", "dwk")):
+        v, mag = want[n]
+        ref.check(g, v, mag, T * max(Hq, Hk) if n[1] == "w" else D, n)
