@@ -451,7 +451,7 @@ __global__ __launch_bounds__(256) void k_gated_decode(GatedArgs a, float* state_
 // a run is a pair (A, R) and the tiles are a chain.  The states before each token come from the checkpoint before the tile.
 // What a thread keeps of a token from the first look to the gradients are a, h' and dy act'(z) in registers, dy act(z) in
 // shared memory, and the other inputs as they were loaded: the rest is computed twice, which costs less than the registers.
-// 8 x 2048 x 1536 of bfloat16 with all gates: 453 MB in 145 us, 3.1 TB/s; vector instructions take 60% of the time (fifteen
+// 8 x 2048 x 1536 of bfloat16 with all gates: 453 MB in 140 us, 3.2 TB/s; vector instructions take 60% of the time (fifteen
 // exponentials, reciprocals and roots an element), and as in the forward little of it overlaps the loads.
 struct GatedGrads {
   const void* dy;
