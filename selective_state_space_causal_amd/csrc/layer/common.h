@@ -84,15 +84,16 @@ int by_io(int32_t io, F f) {
 
 }  // namespace
 
-// sigmoid(v), and both it and sigmoid(-v), the latter without the cancellation of 1 - sigmoid(v).  An infinite or NaN v is
-// taken as the formula has it.
+// sigmoid(v), and both it and sigmoid(-v), the latter without the cancellation of 1 - sigmoid(v): e s with e = exp(-v).  The
+// hardware's reciprocal has no denormal results: past e = 2^126 (v < -87.34) s is 0, and sigmoid(-v) is 1 (it is from 2^24 on).
+// An infinite or NaN v is taken as the formula has it.
 __device__ __forceinline__ float sigmoid(float v) { return rcp_hw(1.0f + exp2_hw(-v * kLog2e)); }
 struct Sigmoids {
   float s, s1;
 };
 __device__ __forceinline__ Sigmoids sigmoids(float v) {
   const float e = exp2_hw(-v * kLog2e), s = rcp_hw(1.0f + e);
-  return {s, fminf(e * s, 1.0f)};  // an e that is infinite meets s = 0, and their product's NaN is 1 here; v = NaN shows in s
+  return {s, e < 0x1p126f ? fminf(e * s, 1.0f) : 1.0f};  // v = NaN shows in s
 }
 
 // V neighbouring channels of one token as loaded.  Rows may start at any element: accesses need no more alignment.
