@@ -93,7 +93,7 @@ struct Sigmoids {
 };
 __device__ __forceinline__ Sigmoids sigmoids(float v) {
   const float e = exp2_hw(-v * kLog2e), s = rcp_hw(1.0f + e);
-  return {s, e < 0x1p126f ? fminf(e * s, 1.0f) : 1.0f};  // v = NaN shows in s
+  return {s, e >= 0x1p126f ? 1.0f : e * s};  // v = NaN in both
 }
 
 // V neighbouring channels of one token as loaded.  Rows may start at any element: accesses need no more alignment.
