@@ -306,6 +306,13 @@ __device__ __forceinline__ float qk_turned(const QkArgs& a, const QkToken& tok, 
   const float s = sign * tok.s[pair];
   return __builtin_fmaf(u[i], tok.c[pair], first ? -u[mate] * s : u[mate] * s);
 }
+// Between a row's stores to LDS and its loads by other lanes of the wave, and before the next row's stores: the fences keep the
+// accesses in the program's order.  They cost no instruction, as a wave's accesses to LDS run in order.
+__device__ __forceinline__ void qk_row_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
 __device__ __forceinline__ float wave_sum(float v) { return group_sum<32>(v) + __shfl_xor(group_sum<32>(v), 32); }
 
 template <typename IO>
@@ -329,13 +336,13 @@ __global__ __launch_bounds__(kQkThreads) void k_qk(QkArgs a, IO* q_out, IO* k_ou
         s = __builtin_fmaf(x[e], x[e], s);
       }
       const float r = rsqrtf(wave_sum(s) / a.D + a.eps);
-      __builtin_amdgcn_wave_barrier();
+      qk_row_order();
 #pragma unroll
       for (int e = 0; e < kQkCols; ++e) {
         const int i = lane + 64 * e;
         if (i < a.D) u[i] = x[e] * r * w[i];
       }
-      __builtin_amdgcn_wave_barrier();  // a wave's accesses to LDS are in order
+      qk_row_order();
 #pragma unroll
       for (int e = 0; e < kQkCols; ++e) {
         const int i = lane + 64 * e;
@@ -358,13 +365,13 @@ __global__ __launch_bounds__(kQkThreads) void k_qk_bwd(QkArgs a, const IO* dqo, 
       for (int h = wave; h < H; h += kQkWaves) {
         const IO* v = in + t * ts + static_cast<int64_t>(h) * a.D;
         const IO* go = dout + (t * H + h) * a.D;
-        __builtin_amdgcn_wave_barrier();
+        qk_row_order();
 #pragma unroll
         for (int e = 0; e < kQkCols; ++e) {
           const int i = lane + 64 * e;
           if (i < a.D) u[i] = ld_io(go, i);
         }
-        __builtin_amdgcn_wave_barrier();
+        qk_row_order();
         float s = 0.0f, dot = 0.0f, g[kQkCols], x[kQkCols];
 #pragma unroll
         for (int e = 0; e < kQkCols; ++e) {
