@@ -162,10 +162,62 @@ __device__ __forceinline__ float gated_state(Incoming& in, const GatedChain& ch,
   return A < 0.0f ? h : __builtin_fmaf(A, __uint_as_float(static_cast<uint32_t>(in.state)), h);
 }
 
-__global__ __launch_bounds__(256) void k_gated_clear(u64* p, int64_t n, uint32_t* tickets) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i < n) p[i] = kUnset;
-  if (i < kGatedQueues) tickets[i * kGatedQueueStep] = 0;
+// Final states of empty sequences, `in` (NULL: zeros) to `out`.  The tiles see to kTileSlots sequences each (gated_empty) where
+// that is all of them, as it is where there are no more sequences than tokens.  Otherwise they are taken ahead of the tiles, in
+// the kernel that clears the chain: a workgroup looks through 64 of them for kEmptyChannels channels, its waves take turns, a
+// wave's loads are on their way together.  Taken by the tiles however many there are, 40000 empty ones beside 16 tokens x 256
+// took 3.2 ms for 32 us, 5000 beside 16 x 2048 412 us for 38; taken ahead however few, 512 sequences of 16 tokens x 2048 take
+// 54.5 us for 53.2, two of 4 tokens x 4096 18.4 for 16.0; in workgroups of the tiles' kernels, 8192 x 2048 58 us for 52.
+constexpr int kEmptySlots = 64, kEmptyChannels = 128, kTileSlots = 128;
+struct EmptySlots {
+  const int32_t* cu;
+  const float* in;
+  float* out;
+  int64_t d;
+  int S;
+};
+__global__ __launch_bounds__(256) void k_gated_begin(u64* p, int64_t n, uint32_t* tickets, EmptySlots e) {
+  const int64_t blocks = (n + 255) / 256;
+  if (blockIdx.x < blocks) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) p[i] = kUnset;
+    if (i < kGatedQueues) tickets[i * kGatedQueueStep] = 0;
+    return;
+  }
+  constexpr int waves = 4, N = kEmptySlots / waves, W = kEmptyChannels / 64;
+  const uint32_t block = static_cast<uint32_t>(blockIdx.x - blocks), slices = static_cast<uint32_t>((e.d + kEmptyChannels - 1) / kEmptyChannels);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+  const int64_t s0 = static_cast<int64_t>(block / slices) * kEmptySlots, c = static_cast<int64_t>(block % slices) * kEmptyChannels + lane;
+  const int64_t s = s0 + lane < e.S ? s0 + lane : e.S - 1;
+  const u64 empty = __ballot(s0 + lane < e.S && e.cu[s] == e.cu[s + 1]);
+  const auto here = [&](int j, int k) { return (empty >> (wave + j * waves) & 1) && c + 64 * k < e.d; };
+  const auto at = [&](int j, int k) { return (s0 + wave + j * waves) * e.d + c + 64 * k; };
+  float v[N][W];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[j][k] = e.in != nullptr && here(j, k) ? e.in[at(j, k)] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      if (here(j, k)) e.out[at(j, k)] = v[j][k];
+}
+
+// A tile's share of them, channels c0 .. c0 + width: its waves take turns.
+__device__ __forceinline__ void gated_empty(const int32_t* __restrict__ cu, int S, uint32_t tile, uint32_t tiles, const float* in, float* out,
+                                            int64_t d, int64_t c0, int width) {
+  const int64_t first = static_cast<int64_t>(tile) * kTileSlots;
+  if (first >= S || S > static_cast<int64_t>(tiles) * kTileSlots) return;
+  const int lane = threadIdx.x & 63;
+  for (int64_t s0 = first; s0 < first + kTileSlots && s0 < S; s0 += 64) {
+    const int64_t s = s0 + lane < S ? s0 + lane : S - 1;
+    u64 empty = __ballot(s0 + lane < S && cu[s] == cu[s + 1]) & (0x0101010101010101ull << threadIdx.x / 64);
+    for (; empty != 0; empty &= empty - 1) {
+      const int64_t e = (s0 + __builtin_ctzll(empty)) * d;
+      for (int64_t c = c0 + lane; c < c0 + width && c < d; c += 64) out[e + c] = in != nullptr ? in[e + c] : 0.0f;
+    }
+  }
 }
 
 // A token's place: its sequence and whether it is the first or the last of it.  Behind the last token: neither.
@@ -187,22 +239,6 @@ __device__ __forceinline__ void gated_places(const int32_t* __restrict__ cu, int
     place[i].v = v;
   }
 }
-// Final states of empty sequences, channels c0 .. c0 + width: wave `part` of `parts` looks through its share of the
-// sequences.
-__device__ __forceinline__ void gated_empty(const int32_t* __restrict__ cu, int S, const float* in, float* out, int64_t d, int64_t c0,
-                                            int width, int64_t part, int64_t parts) {
-  if (out == in) return;
-  const int lane = threadIdx.x & 63;
-  for (int64_t s0 = part * 64; s0 < S; s0 += parts * 64) {
-    const int64_t s = s0 + lane;
-    u64 empty = __ballot(s < S && cu[s < S ? s : 0] == cu[s < S ? s + 1 : 0]);
-    for (; empty != 0; empty &= empty - 1) {
-      const int64_t e = (s0 + __builtin_ctzll(empty)) * d;
-      for (int64_t c = c0 + lane; c < c0 + width && c < d; c += 64) out[e + c] = in != nullptr ? in[e + c] : 0.0f;
-    }
-  }
-}
-
 // LDS is written, a wave's loads from memory may stay in flight
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -352,7 +388,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
     static_assert(kGatedTile == 2 * MM_GATED_BLOCK, "a checkpoint before the tile and one in its middle");
     float* const cp = ckpt + static_cast<int64_t>(2) * tile * d + cc;
     const bool halfway = t0 + MM_GATED_BLOCK < a.T, restarts = cut && halfway && place[MM_GATED_BLOCK].starts();
-    if (ckpt != nullptr && a.T > 0) {
+    if (ckpt != nullptr) {
       // Sequences that start at a checkpoint.  Their initial states are read before the pair is out: where state_out is
       // state_in, the tile in which such a sequence ends may then write over them.
       if (!waits) cp[0] = a.state_in != nullptr ? a.state_in[seq * d + cc] : 0.0f;
@@ -371,7 +407,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
   }
   if (!OUT) return;
   lds_barrier();
-  gated_empty(a.cu, a.S, a.state_in, state_out, d, c0, C, tile * (kGatedThreads / 64) + threadIdx.x / 64, tiles * (kGatedThreads / 64));
+  if (state_out != a.state_in) gated_empty(a.cu, a.S, tile, tiles, a.state_in, state_out, d, c0, C);
   if (!on) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -543,7 +579,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
   if (cut) {
     gated_places<kGatedBwdTile>(a.cu, a.S, a.T, t0, place);
     const int64_t last = whole ? t0 + kGatedBwdTile - 1 : a.T - 1;
-    hi = a.cu[seq_of(a.cu, a.S, last > 0 ? last : 0) + 1];  // the end of the tile's last sequence
+    hi = a.cu[seq_of(a.cu, a.S, last) + 1];  // the end of the tile's last sequence
     lds_barrier();
   }
 
@@ -633,12 +669,12 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
   if (lane == 0) cuts[run] = marks;  // the first channels of a slice are there
   const int64_t cc = c0 + threadIdx.x;
   const bool chain = threadIdx.x < C && cc < d, waits = hi > t0 + kGatedBwdTile;
-  Incoming in = gated_from(ch, n, tiles - 1 - static_cast<int64_t>((hi > 0 ? hi - 1 : 0) / kGatedBwdTile));
+  Incoming in = gated_from(ch, n, tiles - 1 - (hi - 1) / kGatedBwdTile);
   if (chain && waits) gated_look(in, 0, ch, d, c0, threadIdx.x);
   lds_barrier();
   if (chain) {
     const int j = threadIdx.x;
-    float At = 1.0f, Rt = 0.0f, from = 0.0f, state = a.T > 0 ? o.ckpt[tile * d + cc] : 0.0f;
+    float At = 1.0f, Rt = 0.0f, from = 0.0f, state = o.ckpt[tile * d + cc];
 #pragma unroll
     for (int g = NG - 1; g >= 0; --g) {
       const float Ag = sA[g][j], Rg = sR[g][j];
@@ -664,9 +700,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
     }
   }
   lds_barrier();
-  if (o.dstate_in != nullptr)
-    gated_empty(a.cu, a.S, o.dstate_out, o.dstate_in, d, c0, C, tile * (kGatedThreads / 64) + threadIdx.x / 64,
-                tiles * (kGatedThreads / 64));
+  if (o.dstate_in != nullptr) gated_empty(a.cu, a.S, tile, tiles, o.dstate_out, o.dstate_in, d, c0, C);
   float sum[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -770,7 +804,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated_bwd(GatedArgs a, Gat
 #pragma unroll
     for (int i = 0; i < V; ++i) sA[run][lane * V + i] = sum[i];
     lds_barrier();
-    if (chain && a.T > 0) {
+    if (chain) {
       float t = 0.0f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) t += sA[g][threadIdx.x];
@@ -820,13 +854,15 @@ ChainLayout chain_layout(int64_t tiles, int32_t d) {
   const int64_t pairs = tiles * d, states = (tiles >> gated_group(tiles)) * d;
   return {pairs, states, align256(kTicketBytes + static_cast<size_t>(pairs + states) * 8)};
 }
-GatedChain start_chain(int64_t tiles, int32_t d, void* ws, hipStream_t st) {
+// Clears the chain of a call's tiles, and sees to its empty sequences where the tiles do not (e.out == NULL: nobody does).
+GatedChain start_chain(int64_t tiles, int32_t d, void* ws, hipStream_t st, EmptySlots e) {
   const ChainLayout l = chain_layout(tiles, d);
-  if (l.total == 0) return GatedChain{};
-  u64* p = reinterpret_cast<u64*>(static_cast<char*>(ws) + kTicketBytes);
-  const int64_t n = l.pairs + l.states;
-  hipLaunchKernelGGL(k_gated_clear, dim3(static_cast<unsigned>(cdiv(n, 256))), dim3(256), 0, st, p, n, static_cast<uint32_t*>(ws));
-  return GatedChain{p, p + l.pairs, static_cast<uint32_t*>(ws), gated_group(tiles)};
+  const bool chain = l.total > 0, slots = e.out != nullptr && e.S > tiles * kTileSlots;
+  u64* p = chain ? reinterpret_cast<u64*>(static_cast<char*>(ws) + kTicketBytes) : nullptr;
+  const int64_t n = l.pairs + l.states, rest = slots ? cdiv(e.S, kEmptySlots) * cdiv(d, kEmptyChannels) : 0;
+  if (chain || slots)
+    hipLaunchKernelGGL(k_gated_begin, dim3(static_cast<unsigned>(cdiv(n, 256) + rest)), dim3(256), 0, st, p, n, static_cast<uint32_t*>(ws), e);
+  return chain ? GatedChain{p, p + l.pairs, static_cast<uint32_t*>(ws), gated_group(tiles)} : GatedChain{};
 }
 // the backward's workspace: a chain (the forward's first, where the states are made again), the tiles' sums, those states
 struct BackwardLayout {
@@ -903,8 +939,10 @@ int mamba_mixer_gated_prefill(const void* x, const void* r, const void* g, const
     using IO = decltype(io);
     return by_channels<IO>(d, [&](auto v) {
       constexpr int V = decltype(v)::value;
-      const GatedChain ch = start_chain(gated_tiles(T), d, workspace, st);
-      const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, gated_tiles(T)) * cdiv(d, GatedShape<IO, V, kGatedTile>::C)));
+      const EmptySlots e{cu_seqlens, state_in, state_out != state_in ? state_out : nullptr, d, S};
+      const GatedChain ch = start_chain(gated_tiles(T), d, workspace, st, e);
+      if (T == 0) return launched();
+      const dim3 grid(static_cast<unsigned>(gated_tiles(T) * cdiv(d, GatedShape<IO, V, kGatedTile>::C)));
       IO* const out = static_cast<IO*>(y);
       if (lam != nullptr) hipLaunchKernelGGL((k_gated<IO, V, true, true>), grid, dim3(kGatedThreads), 0, st, a, ch, state_out, out, ckpt);
       else hipLaunchKernelGGL((k_gated<IO, V, false, true>), grid, dim3(kGatedThreads), 0, st, a, ch, state_out, out, ckpt);
@@ -984,16 +1022,16 @@ int mamba_mixer_gated_backward(const void* x, const void* r, const void* g, cons
     return by_channels<IO>(d, [&](auto v) {
       constexpr int V = decltype(v)::value;
       const int64_t tiles = gated_blocks(T);
-      const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, tiles) * cdiv(d, GatedShape<IO, V, kGatedBwdTile>::C)));
-      if (S > 0 && ckpt == nullptr && T > 0) {
+      if (ckpt == nullptr && T > 0) {
         const dim3 forward(static_cast<unsigned>(gated_tiles(T) * cdiv(d, GatedShape<IO, V, kGatedTile>::C)));
-        const GatedChain ch = start_chain(gated_tiles(T), d, workspace, st);
+        const GatedChain ch = start_chain(gated_tiles(T), d, workspace, st, EmptySlots{});
         IO* const none = nullptr;
         if (lam != nullptr) hipLaunchKernelGGL((k_gated<IO, V, true, false>), forward, dim3(kGatedThreads), 0, st, a, ch, nullptr, none, states);
         else hipLaunchKernelGGL((k_gated<IO, V, false, false>), forward, dim3(kGatedThreads), 0, st, a, ch, nullptr, none, states);
       }
-      if (S > 0) {
-        const GatedChain ch = start_chain(tiles, d, workspace, st);
+      const GatedChain ch = start_chain(tiles, d, workspace, st, EmptySlots{cu_seqlens, dstate_out, S > 0 ? dstate_in : nullptr, d, S});
+      if (T > 0) {
+        const dim3 grid(static_cast<unsigned>(tiles * cdiv(d, GatedShape<IO, V, kGatedBwdTile>::C)));
         if (lam != nullptr) hipLaunchKernelGGL((k_gated_bwd<IO, V, true>), grid, dim3(kGatedThreads), 0, st, a, ch, o);
         else hipLaunchKernelGGL((k_gated_bwd<IO, V, false>), grid, dim3(kGatedThreads), 0, st, a, ch, o);
       }
