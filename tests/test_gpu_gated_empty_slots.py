@@ -45,6 +45,37 @@ def test_values(lens, d, io):
     assert not got["dstate_in"][empty.cuda()].any(), "nothing asked of the final states"
 
 
+def test_captured_and_on_another_stream():
+    """More slots than tokens, forward and backward in one graph, replayed between eager calls; then behind the current stream."""
+    from tests.test_gpu_streams import check
+
+    lens, d = [0] * 900 + [70] + [0] * 500 + [3] + [0] * 60, 132
+    c = ref.gated_inputs(9, lens, d, "bf16")
+    ins = [c[k].cuda() for k in ("x", "r", "g", "z", "lam", "cu", "state")]
+    dy, dstate = c["dy"].cuda(), c["dstate"].cuda()
+
+    def both(**kw):
+        return [*mm.gated_prefill(*ins, **kw), *mm.gated_backward(*ins, dy, dstate, **kw).values()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for i in range(4):
+        ins[6].add_(0.25)
+        dstate.add_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        for j, (a, b) in enumerate(zip(held, both())):
+            assert torch.equal(a, b), (i, j)
+    check(lambda **kw: list(mm.gated_prefill(*ins, **kw)))
+    check(lambda **kw: list(mm.gated_backward(*ins, dy, dstate, **kw).values()))
+
+
 def test_time():
     """40000 slots, 16 tokens: about as long as the convolution takes, whose threads copy a slot and channel each."""
     S, T, d = 40000, 16, 256
