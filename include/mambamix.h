@@ -601,6 +601,8 @@ size_t mamba_mixer_conv_backward_workspace_bytes(int64_t T, int32_t d, int32_t W
  *   y          [T, d]  io    contiguous
  *   ckpt       NULL, or [ceil(T / MM_GATED_BLOCK), d] f32, out: the state before token MM_GATED_BLOCK b of the packed
  *              stream, in that token's sequence (mamba_mixer_gated_checkpoint_bytes), for the backward
+ * Float32 has no full precision below 2^-126: a sigmoid there (r or g below -87.3) counts as 0, and with lam m may where
+ * 1 - a^2 is.
  * The sequence boundaries and the io types are those of mamba_mixer_prefill.  y, state_out and ckpt may overlap no
  * input but state_out == state_in.  workspace: mamba_mixer_gated_prefill_workspace_bytes bytes (0 for short calls),
  * 256-byte aligned, contents on entry do not matter; it is one call's until that call has run.

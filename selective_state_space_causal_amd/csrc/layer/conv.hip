@@ -4,8 +4,8 @@
 // Bound by memory.  A wave walks L tokens of 64 V channels (512 bytes of bfloat16 a row: narrower rows cost a fifth of the
 // bandwidth), its window, weights and the weights' gradients in registers: an input is read once, but for the W - 1 tokens
 // around a walk.  kStep tokens are loaded at a time, the next ones while these are used (8 at a time: backward 53 us for
-// 48.7, and fewer walks fit; 2: 65.3 forward for 63.9).  16384 x 4352 of bfloat16: 285 MB in 63.5 us, 4.5 TB/s; backward
-// 8 x 2048 x 1792: 176 MB in 47 us with the sum of the partial gradients (4 us), half of the time vector instructions.
+// 48.7, and fewer walks fit; 2: 65.3 forward for 63.9).  16384 x 4352 of bfloat16: 286 MB in 61 us, 4.7 TB/s; backward
+// 8 x 2048 x 1792: 177 MB in 48 us with the sum of the partial gradients (4 us), half of the time vector instructions.
 // Longer: 65536 x 2048 5.1 TB/s forward, 4.9 backward.
 #include <algorithm>
 #include <type_traits>

@@ -62,10 +62,10 @@ __device__ __forceinline__ float gated_act(bool gelu, float z) {
 // a microsecond each, are one in a group.  Tiles are numbered by tickets, not by the workgroup's index, so a tile waits
 // only for tiles whose workgroups run already or are done, and every wait ends.
 // 16384 x 4096 of bfloat16 with all gates: 671 MB in 173 us, 3.9 TB/s (a copy of its size would take 109), vector
-// instructions half of the time.  Two workgroups of a CU hold 128 registers a thread, and a tile's loads, its arithmetic
-// and its wait follow each other: what the other workgroup does meanwhile is all the overlap.  The wait itself is 5 us of
-// it.  Rows of 128 bytes of channels: 193 us; tiles of 64 tokens: 180; workgroups that stay and load the next tile ahead:
-// 214 and more, their registers left room for smaller tiles only.
+// instructions half of the time.  Two workgroups of a CU hold 128 registers a thread (four channels of bfloat16 spill four
+// more, 20 bytes a thread), and a tile's loads, its arithmetic and its wait follow each other: what the other workgroup does
+// meanwhile is all the overlap.  The wait itself is 5 us of it.  Rows of 128 bytes of channels: 193 us; tiles of 64 tokens:
+// 180; workgroups that stay and load the next tile ahead: 214 and more, their registers left room for smaller tiles only.
 // Where a sequence starts, A is set to -1: what comes before has no part in what follows, whatever it is (0 times an
 // infinity would have).
 constexpr int kGatedTile = 2 * MM_GATED_BLOCK, kGatedThreads = 512;
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(kGatedThreads, 4) void k_gated(GatedArgs a, GatedCh
   }
 }
 
-// One token a row: V channels a thread.
+// One token a row: V channels a thread.  256 x 8192 of bfloat16 with all gates: 38 MB in 11 us, 3.4 TB/s.
 template <typename IO, int V, bool LAM>
 __global__ __launch_bounds__(256) void k_gated_decode(GatedArgs a, float* state_out, IO* y) {
   const int64_t n = static_cast<int64_t>(a.S) * a.d;
@@ -877,7 +877,7 @@ BackwardLayout backward_layout(int64_t T, int32_t d, bool has_ckpt) {
   return l;
 }
 // f(V as a type) for d channels: as many of them, up to 4, as let every thread's be all there or all missing.  16384 x 4096
-// of bfloat16 with 4: 173 us, with 2: 175; single ones make rows of 128 bytes (193).
+// of bfloat16 with 4: 173 us, with 2: 175 (both spill, see k_gated); single ones make rows of 128 bytes (193).
 template <typename IO, typename F>
 int by_channels(int32_t d, F f) {
   if (d % 4 == 0) return f(std::integral_constant<int, 4>{});
