@@ -166,7 +166,7 @@ __device__ __forceinline__ float gated_state(Incoming& in, const GatedChain& ch,
 // that is all of them, as it is where there are no more sequences than tokens.  Otherwise they are taken ahead of the tiles, in
 // the kernel that clears the chain: a workgroup looks through 64 of them for kEmptyChannels channels, its waves take turns, a
 // wave's loads are on their way together.  Taken by the tiles however many there are, 40000 empty ones beside 16 tokens x 256
-// took 3.2 ms for 32 us, 5000 beside 16 x 2048 412 us for 38; taken ahead however few, 512 sequences of 16 tokens x 2048 take
+// took 3.2 ms for 30 us, 5000 beside 16 x 2048 411 us for 31; taken ahead however few, 512 sequences of 16 tokens x 2048 take
 // 54.5 us for 53.2, two of 4 tokens x 4096 18.4 for 16.0; in workgroups of the tiles' kernels, 8192 x 2048 58 us for 52.
 constexpr int kEmptySlots = 64, kEmptyChannels = 128, kTileSlots = 128;
 struct EmptySlots {
